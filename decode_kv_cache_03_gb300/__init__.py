@@ -27,6 +27,10 @@ _LAZY = {
     "kara_get_error": ("kara", "kara_get_error"),
     "kara_decode_attention": ("kara", "kara_decode_attention"),
     "kara_decode_workspace_size": ("kara", "kara_decode_workspace_size"),
+    "kara_extend_tables": ("kara", "kara_extend_tables"),
+    "kara_append_kv": ("kara", "kara_append_kv"),
+    "kara_chunk_attention": ("kara", "kara_chunk_attention"),
+    "kara_chunk_workspace_size": ("kara", "kara_chunk_workspace_size"),
 }
 
 __all__ = sorted(_LAZY)

@@ -21,6 +21,7 @@ class Compressor:
         self.err = torch.zeros(1, dtype=torch.int32, device=k.device)
         self._ws = torch.empty(0, dtype=torch.uint8, device=k.device)
         self._dws = torch.empty(0, dtype=torch.uint8, device=k.device)
+        self._cws = torch.empty(0, dtype=torch.uint8, device=k.device)
 
     def workspace(self, n: int) -> torch.Tensor:
         need = kara.kara_workspace_size(self.cache, self.params, n)
@@ -48,6 +49,25 @@ class Compressor:
         if self._dws.numel() < need:
             self._dws = torch.empty(need, dtype=torch.uint8, device=self.k.device)
         kara.kara_decode_attention(self.cache, layer, lengths, block_table, q, out, self._dws, self.err, stream)
+
+    def extend(self, lengths, n_new, block_table, fresh, t, n_used, stream=None):
+        """Enqueue opening blocks for n_new[s] tokens per sequence: block_table gets ids from
+        `fresh` and the descriptor t (kara.tokens) is filled for append() and chunk()."""
+        kara.kara_extend_tables(self.cache.num_blocks, self.cache.block_size, lengths, n_new, block_table, fresh, t,
+                                n_used, self.err, stream)
+
+    def append(self, layer: int, t, rope, q, k, v, q_out, ring=None, stream=None):
+        """Enqueue norms, rotation and the cache write of the new tokens for one layer;
+        with `ring` (the q that compress() takes) the window queries are kept too."""
+        kara.kara_append_kv(self.cache, layer, t, rope, q, k, v, q_out, self.err, ring, stream)
+
+    def chunk(self, layer: int, t, block_table, q, out, stream=None):
+        """Enqueue causal attention of the new tokens for one layer over the paged cache,
+        after append() wrote their K and V."""
+        need = kara.kara_chunk_workspace_size(self.cache, t.n, t.rows)
+        if self._cws.numel() < need:
+            self._cws = torch.empty(need, dtype=torch.uint8, device=self.k.device)
+        kara.kara_chunk_attention(self.cache, layer, t, block_table, q, out, self._cws, self.err, stream)
 
     def error(self, stream=None) -> int:
         return kara.kara_get_error(self.err, stream)

@@ -1,0 +1,292 @@
+// Extending the block tables by new tokens: the tables' new entries, and the
+// indices (first row, slot, sequence, position) that the append and the
+// attention of those tokens read.
+//
+// For each sequence s with a cached length len and m new tokens:
+//     need   = ceil((len + m) / bs) - ceil(len / bs) blocks, taken from `fresh`
+//              in sequence order (exclusive prefix sums of need),
+//     q_start[s] = sum of m over the earlier sequences,
+//     token q_start[s] + i: position len + i, slot = its block * bs + its row.
+//
+// The work is a few KB to a few MB and is bound by latency, so everything runs
+// in one launch: one cluster of up to 8 CTAs.  Every CTA repeats the prefix sums
+// over the lengths (n values, from L2), which costs less than handing them
+// round; the checks, the table entries and the token rows are dealt out to the
+// CTAs, and two cluster barriers make the call all-or-nothing: nothing is
+// written before every check of every CTA has passed.  The check that no
+// consumed id is used twice or still listed by a table keeps a bitmap of the
+// consumed ids in shared memory (one bit per block of the pool, in windows of
+// 2^20 blocks), so it reads each table entry once.
+#include <cooperative_groups.h>
+
+#include "kara_common.cuh"
+#include "kara_sm100.cuh"
+
+namespace cg = cooperative_groups;
+
+namespace kara {
+namespace {
+
+constexpr int kExtThreads = 1024;
+constexpr int kExtCtas = 8;             // portable cluster size
+constexpr int kBitWindow = 1 << 20;     // ids per bitmap window: 128 KB of shared memory
+constexpr int kStartCap = 16384;        // sequences whose q_start fits beside it (64 KB)
+constexpr int kScanItem = 256;          // table entries a warp checks per turn
+// Up to this many entries to check and rows to write, one CTA does it all: the
+// cluster's barriers then cost more than its width saves.
+constexpr int64_t kOneCta = 4096;
+
+struct ExtArgs {
+    int32_t n, rows, num_blocks, bs, bt_stride, window;
+    int64_t n_fresh;
+    const int32_t *len, *n_new, *fresh;
+    int32_t *bt;
+    int32_t *q_start, *new_len, *seq, *pos, *used, *err;
+    int64_t *slot;
+    int32_t start_in_smem;
+};
+
+enum : int { kBad = 1, kDup = 2, kEarlier = 4 };
+
+// Inclusive scan of two 64-bit values over the block; tot gets the sums.
+__device__ longlong2 block_scan2(longlong2 v, longlong2 *scratch /* 33 */, longlong2 &tot)
+{
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long x = __shfl_up_sync(0xffffffffu, v.x, o), y = __shfl_up_sync(0xffffffffu, v.y, o);
+        if (lane >= o) v.x += x, v.y += y;
+    }
+    if (lane == 31) scratch[warp] = v;
+    __syncthreads();
+    if (warp == 0) {
+        longlong2 w = scratch[lane];
+        const longlong2 own = w;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long x = __shfl_up_sync(0xffffffffu, w.x, o), y = __shfl_up_sync(0xffffffffu, w.y, o);
+            if (lane >= o) w.x += x, w.y += y;
+        }
+        scratch[lane] = make_longlong2(w.x - own.x, w.y - own.y);
+        if (lane == 31) scratch[32] = w;
+    }
+    __syncthreads();
+    const longlong2 b = scratch[warp];
+    tot = scratch[32];
+    __syncthreads();
+    return make_longlong2(b.x + v.x, b.y + v.y);
+}
+
+__device__ __forceinline__ int32_t blocks_of(const ExtArgs &a, int64_t x) { return (int32_t)((x + a.bs - 1) / a.bs); }
+
+__device__ __forceinline__ bool seq_ok(const ExtArgs &a, int32_t len, int32_t m)
+{
+    return len >= 0 && m >= 0 && ((int64_t)len + m + a.bs - 1) / a.bs <= a.bt_stride;
+}
+
+__global__ void __launch_bounds__(kExtThreads, 1) extend_kernel(const ExtArgs a)
+{
+    extern __shared__ uint32_t ext_smem[];
+    uint32_t *bits = ext_smem;                                               // window / 32 words
+    int32_t *start = reinterpret_cast<int32_t *>(ext_smem + a.window / 32);  // [n + 1] when it fits
+    __shared__ longlong2 scratch[33];
+    __shared__ int flags;   // of the whole cluster, in CTA 0
+    __shared__ int wrong;   // this CTA saw a bad length
+    cg::cluster_group cluster = cg::this_cluster();
+    const int rank = (int)cluster.block_rank(), nc = (int)cluster.num_blocks();
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int gw = warp * nc + rank, nw = nc * (kExtThreads / 32);  // warps of the cluster, dealt across CTAs
+
+    if (tid == 0) {
+        flags = rank == 0 && *(volatile int32_t *)a.err != 0 ? kEarlier : 0;
+        wrong = 0;
+    }
+    __syncthreads();
+    ptx::cluster_arrive();  // CTA 0's flags are set up (waited for before the first CTA adds to them)
+
+    // ---- totals: tokens and blocks (every CTA, from the lengths)
+    longlong2 carry = make_longlong2(0, 0);
+    for (int base = 0; base < a.n; base += kExtThreads) {
+        const int s = base + tid;
+        longlong2 v = make_longlong2(0, 0);
+        if (s < a.n) {
+            const int32_t len = a.len[s], m = a.n_new[s];
+            if (seq_ok(a, len, m)) {
+                v = make_longlong2(m, blocks_of(a, (int64_t)len + m) - blocks_of(a, len));
+            } else {
+                wrong = 1;
+            }
+        }
+        longlong2 tot;
+        const longlong2 in = block_scan2(v, scratch, tot);
+        if (a.start_in_smem && s < a.n) start[s] = (int32_t)(carry.x + in.x - v.x);
+        carry.x += tot.x, carry.y += tot.y;
+    }
+    if (a.start_in_smem && tid == 0) start[a.n] = (int32_t)carry.x;
+    const int64_t total = carry.x, F = carry.y;
+    const int plan = wrong || total > a.rows ? KARA_EINVAL : F > a.n_fresh ? KARA_ENOBLOCKS : KARA_OK;
+
+    // ---- checks, dealt over the cluster
+    int found = 0;
+    if (plan == KARA_OK) {
+        // the open block of each growing sequence is read for its slots
+        for (int s = gw * 32 + lane; s < a.n; s += nw * 32) {
+            const int32_t len = a.len[s];
+            if (a.n_new[s] > 0 && len % a.bs) {
+                const int32_t b = a.bt[(int64_t)s * a.bt_stride + len / a.bs];
+                if (b < 0 || b >= a.num_blocks) found |= kBad;
+            }
+        }
+        const int per_row = (a.bt_stride + kScanItem - 1) / kScanItem;
+        for (int w0 = 0; F > 0 && w0 < a.num_blocks; w0 += a.window) {
+            __syncthreads();
+            for (int i = tid; i < a.window / 32; i += kExtThreads) bits[i] = 0;
+            __syncthreads();
+            for (int64_t i = tid; i < F; i += kExtThreads) {
+                const int32_t f = a.fresh[i];
+                if (f < 0 || f >= a.num_blocks) found |= kBad;
+                const uint32_t o = (uint32_t)f - (uint32_t)w0;
+                if (o < (uint32_t)a.window && (atomicOr(&bits[o >> 5], 1u << (o & 31)) >> (o & 31) & 1u)) found |= kDup;
+            }
+            __syncthreads();
+            for (int64_t it = gw; it < (int64_t)a.n * per_row; it += nw) {
+                const int s = (int)(it / per_row), c0 = (int)(it % per_row) * kScanItem;
+                const int32_t have = blocks_of(a, a.len[s]);
+                const int32_t *row = a.bt + (int64_t)s * a.bt_stride;
+                int32_t id[kScanItem / 32];
+#pragma unroll
+                for (int k = 0; k < kScanItem / 32; ++k) {
+                    const int c = c0 + k * 32 + lane;
+                    id[k] = c < have ? row[c] : -1;
+                }
+#pragma unroll
+                for (int k = 0; k < kScanItem / 32; ++k) {
+                    const uint32_t o = (uint32_t)id[k] - (uint32_t)w0;
+                    if (id[k] >= 0 && o < (uint32_t)a.window && (bits[o >> 5] >> (o & 31) & 1u)) found |= kDup;
+                }
+            }
+        }
+    }
+    found = __reduce_or_sync(0xffffffffu, found);
+    __syncwarp();
+    ptx::cluster_wait();
+    if (lane == 0 && found) atomicOr(cluster.map_shared_rank(&flags, 0), found);
+    cluster.sync();
+    const int all = *cluster.map_shared_rank(&flags, 0);
+    const bool ok = plan == KARA_OK && all == 0;
+
+    // ---- commit: table entries, first rows, lengths (or the state of a call that did nothing)
+    if (rank == 0 && tid == 0) {
+        if (plan != KARA_OK) set_err(a.err, plan);
+        else if (all & kDup) set_err(a.err, KARA_EDUPBLOCK);
+        else if (all & kBad) set_err(a.err, KARA_EBADBLOCK);
+        *a.used = ok ? (int32_t)F : 0;
+        a.q_start[a.n] = ok ? (int32_t)total : 0;
+    }
+    const bool in_place = a.new_len == a.len;
+    carry = make_longlong2(0, 0);
+    for (int base = 0; base < a.n; base += kExtThreads) {
+        const int s = base + tid;
+        int32_t len = 0, m = 0, need = 0;
+        if (s < a.n) {
+            len = a.len[s];
+            m = ok ? a.n_new[s] : 0;
+            need = blocks_of(a, (int64_t)len + m) - blocks_of(a, len);
+        }
+        longlong2 tot = make_longlong2(0, 0), in = tot;
+        if (ok) in = block_scan2(make_longlong2(m, need), scratch, tot);
+        if (warp % nc == rank && s < a.n) {
+            a.q_start[s] = ok ? (int32_t)(carry.x + in.x - m) : 0;
+            if (!in_place) a.new_len[s] = len + m;
+        }
+        if (warp % nc == rank) {
+            // a warp fills the entries of its sequences one after another
+            const int64_t off = carry.y + in.y - need;
+            for (unsigned todo = __ballot_sync(0xffffffffu, need > 0); todo; todo &= todo - 1) {
+                const int src = __ffs(todo) - 1;
+                const int64_t o = __shfl_sync(0xffffffffu, off, src);
+                const int cnt = __shfl_sync(0xffffffffu, need, src);
+                const int at = __shfl_sync(0xffffffffu, blocks_of(a, len), src);
+                int32_t *row = a.bt + (int64_t)(base + warp * 32 + src) * a.bt_stride + at;
+                for (int i = lane; i < cnt; i += 32) row[i] = a.fresh[o + i];
+            }
+        }
+        carry.x += tot.x, carry.y += tot.y;
+    }
+    cluster.sync();  // the new entries (and q_start, where it is searched in global memory) are visible
+
+    // ---- token rows: 32 per warp, each row's sequence by bisection of the first rows
+    const int32_t *first = a.start_in_smem ? start : a.q_start;
+    for (int64_t t0 = (int64_t)gw * 32; t0 < a.rows; t0 += (int64_t)nw * 32) {
+        const int64_t t = t0 + lane;
+        if (t >= a.rows) break;
+        int64_t slot = -1;
+        int32_t s = -1, x = -1;
+        if (ok && t < total) {
+            int lo = 0, hi = a.n;  // last sequence whose first row is <= t
+            while (hi - lo > 1) {
+                const int mid = (lo + hi) >> 1;
+                if (first[mid] <= t) lo = mid; else hi = mid;
+            }
+            s = lo;
+            x = a.len[s] + (int32_t)(t - first[s]);
+            slot = (int64_t)__ldcg(a.bt + (int64_t)s * a.bt_stride + x / a.bs) * a.bs + x % a.bs;
+        }
+        a.slot[t] = slot;
+        a.seq[t] = s;
+        a.pos[t] = x;
+    }
+    if (in_place && ok) {
+        cluster.sync();  // every CTA has read the old lengths
+        for (int s = gw * 32 + lane; s < a.n; s += nw * 32) a.new_len[s] += a.n_new[s];
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_extend(int32_t num_blocks, int32_t block_size, const int32_t *len, const int32_t *n_new,
+                          int32_t *bt, int32_t bt_stride, const int32_t *fresh, int64_t n_fresh, const kara_tokens *t,
+                          int32_t *used, int32_t *err, cudaStream_t st)
+{
+    ExtArgs a;
+    a.n = t->n;
+    a.rows = t->rows;
+    a.num_blocks = num_blocks;
+    a.bs = block_size;
+    a.bt_stride = bt_stride;
+    a.window = num_blocks < kBitWindow ? (num_blocks + 31) / 32 * 32 : kBitWindow;
+    a.n_fresh = n_fresh;
+    a.len = len;
+    a.n_new = n_new;
+    a.fresh = fresh;
+    a.bt = bt;
+    a.q_start = t->q_start;
+    a.new_len = t->len;
+    a.seq = t->seq;
+    a.pos = t->pos;
+    a.slot = t->slot;
+    a.used = used;
+    a.err = err;
+    a.start_in_smem = t->n <= kStartCap;
+    const size_t smem = (size_t)a.window / 8 + (a.start_in_smem ? sizeof(int32_t) * ((size_t)t->n + 1) : 0);
+    if (smem > 40 * 1024) {
+        const cudaError_t e =
+            cudaFuncSetAttribute(extend_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (e != cudaSuccess) return e;
+    }
+    const int nc = (int64_t)t->n * bt_stride + t->rows <= kOneCta ? 1 : kExtCtas;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)nc);
+    cfg.blockDim = dim3(kExtThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = (unsigned)nc;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, extend_kernel, a);
+}
+
+}  // namespace kara

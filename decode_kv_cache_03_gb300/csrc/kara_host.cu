@@ -14,6 +14,7 @@ namespace {
 
 constexpr int kMaxK = 1024;
 constexpr int kMaxG = 8;
+constexpr int kMaxSeqs = 65535;
 constexpr int kMaxGW = 8192;  // query rows per window the scoring kernel keeps statistics for
 
 bool aligned16(const void *p) { return ((uintptr_t)p & 15u) == 0; }
@@ -331,6 +332,69 @@ kara_status kara_decode_attention(const kara_cache *c, int32_t layer, int32_t n,
     if (!ws || ws_bytes < decode_workspace_bytes(c, n, bt_stride)) return KARA_EWORKSPACE;
     return cuda_status(launch_decode(c, layer, n, len, block_table, bt_stride, q, out, ws, err,
                                      (cudaStream_t)stream));
+}
+
+kara_status kara_extend_tables(int32_t num_blocks, int32_t block_size, const int32_t *len, const int32_t *n_new,
+                               int32_t *block_table, int32_t bt_stride, const int32_t *fresh, int64_t n_fresh,
+                               const kara_tokens *out, int32_t *n_used, int32_t *err, kara_stream_t stream)
+{
+    const Range range("kara_extend_tables");
+    if (block_size != 16) return KARA_EUNSUPPORTED;
+    if (!out || out->n < 0 || out->rows < 0 || num_blocks < 1 || bt_stride < 1 || n_fresh < 0) return KARA_EINVAL;
+    if (out->n == 0 && out->rows == 0) return KARA_OK;
+    if (out->n > kMaxSeqs || (int64_t)bt_stride * block_size > 0x7fffffffLL) return KARA_EUNSUPPORTED;
+    if (out->n > 0 && (!len || !n_new || !block_table || !out->len)) return KARA_EINVAL;
+    if ((n_fresh > 0 && !fresh) || !n_used || !err) return KARA_EINVAL;
+    if (!out->q_start || (out->rows > 0 && (!out->slot || !out->seq || !out->pos))) return KARA_EINVAL;
+    return cuda_status(launch_extend(num_blocks, block_size, len, n_new, block_table, bt_stride, fresh, n_fresh, out,
+                                     n_used, err, (cudaStream_t)stream));
+}
+
+kara_status kara_append_kv(const kara_cache *c, int32_t layer, const kara_tokens *t, const kara_rope *r, const void *q,
+                           int64_t q_stride, const void *k, int64_t k_stride, const void *v, int64_t v_stride,
+                           void *q_out, void *ring, int32_t W, int32_t *err, kara_stream_t stream)
+{
+    const Range range("kara_append_kv");
+    const kara_status st = check_cache(c);
+    if (st != KARA_OK) return st;
+    if (layer < 0 || layer >= c->num_layers || !t || t->n < 0 || t->rows < 0 || !r) return KARA_EINVAL;
+    if (r->rot_dim < 0 || r->rot_dim > c->head_dim || r->rot_dim % 16 || !(r->eps >= 0.f)) return KARA_EINVAL;
+    if (r->interleaved != 0 && r->interleaved != 1) return KARA_EINVAL;
+    if (r->rot_dim > 0 && (!r->cos_sin || !aligned16(r->cos_sin) || r->n_pos < 1)) return KARA_EINVAL;
+    if (!aligned16(r->q_weight) || !aligned16(r->k_weight)) return KARA_EINVAL;
+    if (ring && (W < 1 || !aligned16(ring))) return KARA_EINVAL;
+    if (t->rows == 0) return KARA_OK;
+    if (!t->slot || !t->seq || !t->pos || (ring && t->n > 0 && !t->len)) return KARA_EINVAL;
+    if (!q || !k || !v || !q_out || !err) return KARA_EINVAL;
+    if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(q_out)) return KARA_EINVAL;
+    const int64_t qd = (int64_t)c->num_q_heads * c->head_dim, kd = (int64_t)c->num_kv_heads * c->head_dim;
+    if (q_stride < qd || k_stride < kd || v_stride < kd || q_stride % 8 || k_stride % 8 || v_stride % 8)
+        return KARA_EINVAL;
+    if (q_out == q && q_stride != qd) return KARA_EINVAL;
+    return cuda_status(launch_append(c, layer, t, r, q, q_stride, k, k_stride, v, v_stride, q_out, ring, W, err,
+                                     (cudaStream_t)stream));
+}
+
+size_t kara_chunk_workspace_size(const kara_cache *c, int32_t n, int32_t rows)
+{
+    if (check_cache(c) != KARA_OK || n < 0 || rows < 0) return 0;
+    return chunk_workspace_bytes(c, n, rows);
+}
+
+kara_status kara_chunk_attention(const kara_cache *c, int32_t layer, const kara_tokens *t, const int32_t *block_table,
+                                 int32_t bt_stride, const void *q, void *out, void *ws, size_t ws_bytes, int32_t *err,
+                                 kara_stream_t stream)
+{
+    const Range range("kara_chunk_attention");
+    const kara_status st = check_cache(c);
+    if (st != KARA_OK) return st;
+    if (layer < 0 || layer >= c->num_layers || !t || t->n < 0 || t->rows < 0 || bt_stride < 1) return KARA_EINVAL;
+    if (t->n == 0 || t->rows == 0) return KARA_OK;
+    if (t->n > kMaxSeqs || (int64_t)bt_stride * c->block_size > 0x7fffffffLL) return KARA_EUNSUPPORTED;
+    if (!t->q_start || !t->len || !block_table || !q || !out || !err) return KARA_EINVAL;
+    if (!aligned16(q) || !aligned16(out)) return KARA_EINVAL;
+    if (!ws || ws_bytes < chunk_workspace_bytes(c, t->n, t->rows)) return KARA_EWORKSPACE;
+    return cuda_status(launch_chunk(c, layer, t, block_table, bt_stride, q, out, ws, err, (cudaStream_t)stream));
 }
 
 kara_status kara_select(const kara_params *p, int64_t n_windows, const float *scores, int32_t *cand,

@@ -50,12 +50,25 @@ class Batch(ctypes.Structure):
                 ("bt_stride", ctypes.c_int32), ("q", ctypes.c_void_p)]
 
 
+class Tokens(ctypes.Structure):
+    _fields_ = [("n", ctypes.c_int32), ("rows", ctypes.c_int32), ("q_start", ctypes.c_void_p),
+                ("len", ctypes.c_void_p), ("slot", ctypes.c_void_p), ("seq", ctypes.c_void_p),
+                ("pos", ctypes.c_void_p)]
+
+
+class Rope(ctypes.Structure):
+    _fields_ = [("q_weight", ctypes.c_void_p), ("k_weight", ctypes.c_void_p), ("eps", ctypes.c_float),
+                ("cos_sin", ctypes.c_void_p), ("n_pos", ctypes.c_int32), ("rot_dim", ctypes.c_int32),
+                ("interleaved", ctypes.c_int32), ("pos_offset", ctypes.c_void_p)]
+
+
 def _load():
     if not os.path.exists(LIB_PATH):
         raise ImportError(f"libkara.so is not built ({LIB_PATH}); run decode_kv_cache_03_gb300.build.build()")
     lib = ctypes.CDLL(LIB_PATH)
     P = ctypes.c_void_p
     PP, PC, PB = ctypes.POINTER(Params), ctypes.POINTER(Cache), ctypes.POINTER(Batch)
+    PT, PR = ctypes.POINTER(Tokens), ctypes.POINTER(Rope)
     I32, I64, SZ = ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
     sig = {
         "kara_status_string": ([ctypes.c_int], ctypes.c_char_p),
@@ -73,6 +86,10 @@ def _load():
         "kara_compact_queries": ([PC, PP, PB, P, P, P], ctypes.c_int),
         "kara_append_queries": ([PC, PP, PB, P, P], ctypes.c_int),
         "kara_decode_attention": ([PC, I32, I32, P, P, I32, P, P, P, SZ, P, P], ctypes.c_int),
+        "kara_extend_tables": ([I32, I32, P, P, P, I32, P, I64, PT, P, P, P], ctypes.c_int),
+        "kara_append_kv": ([PC, I32, PT, PR, P, I64, P, I64, P, I64, P, P, I32, P, P], ctypes.c_int),
+        "kara_chunk_workspace_size": ([PC, I32, I32], SZ),
+        "kara_chunk_attention": ([PC, I32, PT, P, I32, P, P, P, SZ, P, P], ctypes.c_int),
     }
     for name, (args, res) in sig.items():
         f = getattr(lib, name)
@@ -85,7 +102,8 @@ _lib = _load()
 EXPORTED = ("kara_status_string", "kara_version", "kara_plan", "kara_workspace_size", "kara_score",
             "kara_select", "kara_compact", "kara_compress_batch", "kara_get_error", "kara_compact_static",
             "kara_decode_workspace_size", "kara_decode_attention", "kara_compact_queries", "kara_append_queries",
-            "kara_batch_groups")
+            "kara_batch_groups", "kara_extend_tables", "kara_append_kv", "kara_chunk_workspace_size",
+            "kara_chunk_attention")
 STATIC_MAX_SEQS = 8192     # KARA_STATIC_MAX_SEQS
 
 
@@ -121,8 +139,10 @@ def cache(k: torch.Tensor, v: torch.Tensor, num_q_heads: int) -> Cache:
     assert k.dtype == torch.bfloat16 and v.shape == k.shape and v.stride() == k.stride()
     Lyr, nb, hkv, bs, d = k.shape
     assert k.stride(4) == 1 and k.stride(3) == d
-    return Cache(k.data_ptr(), v.data_ptr(), k.stride(0), k.stride(1), k.stride(2), Lyr, nb, hkv,
-                 int(num_q_heads), d, bs)
+    c = Cache(k.data_ptr(), v.data_ptr(), k.stride(0), k.stride(1), k.stride(2), Lyr, nb, hkv,
+              int(num_q_heads), d, bs)
+    c.device = k.device
+    return c
 
 
 def batch(lengths: torch.Tensor, block_table: torch.Tensor, q: torch.Tensor) -> Batch:
@@ -182,6 +202,110 @@ def kara_decode_attention(c: Cache, layer: int, lengths: torch.Tensor, block_tab
                                       int(bt_stride), _ptr(q), _ptr(out), _ptr(ws),
                                       ws.numel() * ws.element_size(), _ptr(err), _stream(stream)),
            "kara_decode_attention")
+
+
+def _same_device(err: torch.Tensor, where: str, *tensors):
+    """Refuses tensors that are not on the current CUDA device: the launch goes there."""
+    d = err.device
+    if d.type != "cuda" or d.index != torch.cuda.current_device():
+        raise KaraError(EINVAL, f"{where}: tensors on {d}, not on the current CUDA device")
+    for t in tensors:
+        if t is not None and t.device != d:
+            raise KaraError(EINVAL, f"{where}: tensors on {t.device} and on {d}")
+
+
+def tokens(q_start: torch.Tensor, length: torch.Tensor, slot: torch.Tensor, seq: torch.Tensor,
+           pos: torch.Tensor) -> Tokens:
+    """Describe the new tokens of a step: q_start [n + 1], length [n] (int32), slot (int64), seq, pos
+    (int32) [rows].  kara_extend_tables fills the arrays; the descriptor keeps them alive."""
+    n, rows = int(length.shape[0]), int(slot.shape[0])
+    assert q_start.shape == (n + 1,) and seq.shape == pos.shape == (rows,) and slot.dtype == torch.int64
+    for t in (q_start, length, seq, pos):
+        assert t.dtype == torch.int32 and t.device == slot.device
+    for t in (q_start, length, slot, seq, pos):
+        assert t.is_contiguous()
+    t = Tokens(n, rows, q_start.data_ptr(), length.data_ptr(), slot.data_ptr(), seq.data_ptr(), pos.data_ptr())
+    t.device = slot.device
+    t.keep = (q_start, length, slot, seq, pos)
+    return t
+
+
+def rope(cos_sin, q_weight=None, k_weight=None, eps: float = 1e-6, interleaved: bool = False,
+         pos_offset=None) -> Rope:
+    """Describe norms and rotation: cos_sin float [n_pos][rot_dim] (None: no rotation), weights bf16
+    [head_dim] or None, pos_offset int32 [n] or None.  The descriptor keeps the tensors alive."""
+    n_pos = rot = 0
+    if cos_sin is not None:
+        assert cos_sin.dtype == torch.float32 and cos_sin.is_contiguous()
+        n_pos, rot = cos_sin.shape
+    for w in (q_weight, k_weight):
+        assert w is None or (w.dtype == torch.bfloat16 and w.is_contiguous() and w.dim() == 1)
+    assert pos_offset is None or (pos_offset.dtype == torch.int32 and pos_offset.is_contiguous())
+    p = [None if t is None else t.data_ptr() for t in (q_weight, k_weight, cos_sin, pos_offset)]
+    r = Rope(p[0], p[1], float(eps), p[2], int(n_pos), int(rot), int(bool(interleaved)), p[3])
+    r.head_dim = {int(w.shape[0]) for w in (q_weight, k_weight) if w is not None}
+    r.n = None if pos_offset is None else int(pos_offset.shape[0])
+    r.keep = [t for t in (q_weight, k_weight, cos_sin, pos_offset) if t is not None]
+    r.on = r.keep[:1]
+    assert all(t.device == r.on[0].device for t in r.keep)
+    return r
+
+
+def kara_extend_tables(num_blocks: int, block_size: int, lengths: torch.Tensor, n_new: torch.Tensor,
+                       block_table: torch.Tensor, fresh: torch.Tensor, t: Tokens, n_used: torch.Tensor,
+                       err: torch.Tensor, stream=None):
+    """Open blocks for n_new[s] tokens after lengths[s] cached ones (ids from `fresh`, table rewritten
+    in place) and fill the descriptor t; t's lengths may be `lengths` itself."""
+    _same_device(err, "kara_extend_tables", lengths, n_new, block_table, fresh, n_used, t)
+    assert lengths.dtype == n_new.dtype == block_table.dtype == fresh.dtype == n_used.dtype == torch.int32
+    assert lengths.shape == n_new.shape == (t.n,) and block_table.shape[0] == t.n and n_used.numel() == 1
+    assert (lengths.is_contiguous() and n_new.is_contiguous() and block_table.is_contiguous()
+            and fresh.is_contiguous())
+    _check(_lib.kara_extend_tables(num_blocks, block_size, lengths.data_ptr(), n_new.data_ptr(),
+                                   block_table.data_ptr(), block_table.shape[1], fresh.data_ptr(), fresh.numel(),
+                                   t, n_used.data_ptr(), err.data_ptr(), _stream(stream)), "kara_extend_tables")
+
+
+def _token_stride(x: torch.Tensor, rows: int, heads: int, d: int) -> int:
+    assert x.dtype == torch.bfloat16 and x.shape == (rows, heads, d)
+    assert x.stride(2) == 1 and (heads == 1 or x.stride(1) == d)
+    return x.stride(0) if rows > 1 else heads * d
+
+
+def kara_append_kv(c: Cache, layer: int, t: Tokens, r: Rope, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
+                   q_out: torch.Tensor, err: torch.Tensor, ring=None, stream=None):
+    """Norm and rotate q [rows][num_q_heads][D] and k [rows][num_kv_heads][D] and write k, v into layer
+    `layer` of the cache at t's slots, queries to q_out (and to ring [n][layers][num_q_heads][W][D])."""
+    _same_device(err, "kara_append_kv", q, k, v, q_out, ring, c, t, *r.on)
+    d, W = c.head_dim, 0
+    qs, ks, vs = (_token_stride(x, t.rows, h, d) for x, h in
+                  ((q, c.num_q_heads), (k, c.num_kv_heads), (v, c.num_kv_heads)))
+    assert q_out.dtype == torch.bfloat16 and q_out.shape == q.shape and q_out.is_contiguous()
+    assert r.head_dim <= {d} and (r.n is None or r.n == t.n)
+    if ring is not None:
+        W = ring.shape[3]
+        assert ring.dtype == torch.bfloat16 and ring.is_contiguous()
+        assert ring.shape == (t.n, c.num_layers, c.num_q_heads, W, d)
+    _check(_lib.kara_append_kv(c, layer, t, r, q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs,
+                               q_out.data_ptr(), None if ring is None else ring.data_ptr(), W, err.data_ptr(),
+                               _stream(stream)), "kara_append_kv")
+
+
+def kara_chunk_workspace_size(c: Cache, n: int, rows: int) -> int:
+    return int(_lib.kara_chunk_workspace_size(ctypes.byref(c), int(n), int(rows)))
+
+
+def kara_chunk_attention(c: Cache, layer: int, t: Tokens, block_table: torch.Tensor, q: torch.Tensor,
+                         out: torch.Tensor, ws: torch.Tensor, err: torch.Tensor, stream=None):
+    """Causal attention of the new tokens q [rows][num_q_heads][head_dim] (bf16) over layer `layer` of
+    the paged cache, read through block_table [n][bt_stride]; out like q, padding rows untouched."""
+    _same_device(err, "kara_chunk_attention", block_table, q, out, ws, c, t)
+    assert block_table.dtype == torch.int32 and block_table.is_contiguous() and block_table.shape[0] == t.n
+    assert q.dtype == out.dtype == torch.bfloat16 and q.is_contiguous() and out.is_contiguous()
+    assert q.shape == out.shape == (t.rows, c.num_q_heads, c.head_dim)
+    _check(_lib.kara_chunk_attention(c, layer, t, block_table.data_ptr(), block_table.shape[1], q.data_ptr(),
+                                     out.data_ptr(), ws.data_ptr(), ws.numel() * ws.element_size(), err.data_ptr(),
+                                     _stream(stream)), "kara_chunk_attention")
 
 
 def kara_select(p: Params, n_windows: int, scores: torch.Tensor, cand, kept: torch.Tensor, stream=None):

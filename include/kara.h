@@ -225,6 +225,114 @@ kara_status kara_decode_attention(const kara_cache *c, int32_t layer, int32_t n,
                                   void *ws, size_t ws_bytes, int32_t *err, kara_stream_t stream);
 
 /*
+ * ---- New tokens -------------------------------------------------------------
+ * The step that puts tokens into the cache which the compression shortens and
+ * decode attention reads (the pages leave it to the engine around them,
+ * summary section 3).  One descriptor, filled by kara_extend_tables and read by
+ * the calls after it on the same stream with no host step between, describes
+ * the new tokens of n sequences: sequence s has the rows
+ * q_start[s] .. q_start[s+1]-1 of every per-token buffer, in position order; the
+ * rows from q_start[n] on are padding.  All arrays are device memory.
+ */
+typedef struct {
+    int32_t n;         /* sequences */
+    int32_t rows;      /* rows of the per-token buffers, padding included */
+    int32_t *q_start;  /* [n + 1] */
+    int32_t *len;      /* [n] cached length of each sequence, its new tokens included */
+    int64_t *slot;     /* [rows] block id * block_size + row in the block; -1: padding */
+    int32_t *seq;      /* [rows] sequence; -1: padding */
+    int32_t *pos;      /* [rows] logical position in the sequence; -1: padding */
+} kara_tokens;
+
+/*
+ * Block tables and slot maps from request lengths.  Sequence s, with len[s]
+ * cached tokens, gets n_new[s] >= 0 new ones: its table entries from
+ * ceil(len/bs) to ceil((len + n_new)/bs) - 1 become the next ids of `fresh` (in
+ * sequence order; total *n_used), and out is filled: out->len[s] =
+ * len[s] + n_new[s], q_start the running sum of n_new, slot, seq and pos of each
+ * token, -1 in the padding rows.
+ * len, n_new [n]; block_table [n][bt_stride]; fresh [n_fresh]; n_used [1]: device
+ * int32.  out->len may be len itself (lengths advance in place); no other
+ * arrays may overlap.
+ * Checked on the device before anything is written:
+ *   KARA_EINVAL     a negative length or count, len + n_new above
+ *                   bt_stride * bs, or more new tokens than out->rows;
+ *   KARA_ENOBLOCKS  fewer than the needed ids in `fresh`;
+ *   KARA_EDUPBLOCK  a consumed id repeats among the consumed ones, or is an
+ *                   entry below ceil(len/bs) of any table of the batch;
+ *   KARA_EBADBLOCK  a consumed id, or the entry of a block that new tokens
+ *                   continue, outside [0, num_blocks).
+ * With any of these, or an error already in *err, nothing is committed: tables
+ * are unchanged, out->len[s] = len[s], q_start and *n_used are 0 and every row
+ * is padding, so that the calls that follow do nothing.
+ * One launch; the call may be captured into a CUDA graph.
+ * Supported: block_size 16; n <= 65535; bt_stride * block_size < 2^31.
+ */
+kara_status kara_extend_tables(int32_t num_blocks, int32_t block_size, const int32_t *len, const int32_t *n_new,
+                               int32_t *block_table, int32_t bt_stride, const int32_t *fresh, int64_t n_fresh,
+                               const kara_tokens *out, int32_t *n_used, int32_t *err, kara_stream_t stream);
+
+/* Norms and rotation of new queries and keys. */
+typedef struct {
+    const void *q_weight, *k_weight;  /* bf16 [head_dim], 16-byte aligned; NULL: that side is not normalised */
+    float eps;                        /* added to the mean square, >= 0 */
+    const float *cos_sin;             /* [n_pos][rot_dim], 16-byte aligned: rot_dim/2 cosines, then the sines */
+    int32_t n_pos;                    /* rows of the table */
+    int32_t rot_dim;                  /* dims that turn: a multiple of 16 up to head_dim; 0: none (no table) */
+    int32_t interleaved;              /* 0: dim i turns with i + rot_dim/2; 1: dim 2i with 2i + 1 */
+    const int32_t *pos_offset;        /* device [n], or NULL: rotary position = pos + pos_offset[seq].  A
+                                         compression shortens a sequence, its later tokens keep their places:
+                                         the offset grows by the C - R tokens that it dropped */
+} kara_rope;
+
+/*
+ * New tokens into layer `layer` of the cache, in one pass.  For each row t with
+ * slot[t] >= 0 and each head:
+ *     y = x / sqrt(mean(x^2) + eps) * weight       (y = x without a weight)
+ *     z_a = y_a cos - y_b sin,  z_b = y_b cos + y_a sin   for each rotated pair
+ * in fp32 with one rounding to bf16; queries to q_out [rows][num_q_heads][D],
+ * keys and (unchanged) values to the pool rows of slot[t].  With `ring` (the
+ * window-query ring, bf16 [n][num_layers][num_q_heads][W][D]) the queries of the
+ * last W positions of each sequence also go to ring row pos mod W.
+ * q [rows][num_q_heads][D], k, v [rows][num_kv_heads][D]: bf16, heads of a row
+ * contiguous, rows q_stride / k_stride / v_stride elements apart (multiples of
+ * 8; views of one fused projection will do), 16-byte aligned.  q_out may be q
+ * when q_stride is num_q_heads * D; no other arrays may overlap.
+ * Rows with slot -1 are skipped: nothing of theirs is read or written.
+ * Recorded, the row then being skipped too: KARA_EBADBLOCK for a slot outside
+ * the pool, KARA_EINVAL for seq outside [0, n), a negative pos or a rotary
+ * position outside [0, n_pos).  Two rows with one slot race.
+ * One launch; the call may be captured into a CUDA graph.
+ */
+kara_status kara_append_kv(const kara_cache *c, int32_t layer, const kara_tokens *t, const kara_rope *r,
+                           const void *q, int64_t q_stride, const void *k, int64_t k_stride, const void *v,
+                           int64_t v_stride, void *q_out, void *ring, int32_t W, int32_t *err,
+                           kara_stream_t stream);
+
+/*
+ * Causal attention of the new tokens over the paged cache, their own K and V
+ * already in it (kara_append_kv).  For row t, the token at position p =
+ * len[s] - (q_start[s+1] - t) of sequence s, and query head h (KV head g = h / G):
+ *     out[t][h] = sum_{x <= p} softmax_x(<q[t][h], k_x> / sqrt(D)) v_x
+ * with k_x and v_x of layer `layer` read through block_table [n][bt_stride].
+ * Only n, rows, q_start and len of the descriptor are read.  q, out: bf16
+ * [rows][num_q_heads][D], 16-byte aligned, not overlapping; rows of padding are
+ * left as they were.
+ * Recorded: KARA_EINVAL for a sequence whose rows do not lie in order within
+ * [0, rows], or with fewer cached than new tokens, or a length above
+ * bt_stride * bs (its rows inside [0, rows] become 0); KARA_EBADBLOCK for a
+ * block id outside the pool (its keys and values count as zeros).
+ * ws/ws_bytes: at least kara_chunk_workspace_size(c, n, rows) bytes, used by
+ * this call alone until it has run.  The call may be captured into a CUDA graph.
+ * Supported: the kara_cache shapes above, n <= 65535,
+ * bt_stride * block_size < 2^31.
+ */
+size_t kara_chunk_workspace_size(const kara_cache *c, int32_t n, int32_t rows);
+kara_status kara_chunk_attention(const kara_cache *c, int32_t layer, const kara_tokens *t, const int32_t *block_table,
+                                 int32_t bt_stride, const void *q, void *out, void *ws, size_t ws_bytes, int32_t *err,
+                                 kara_stream_t stream);
+
+/*
  * Top-K and Token2Chunk (summary section 1 "Selection"; section 2 "Process").
  * (select_mode KARA_SELECT_TOP_R and KARA_SELECT_FIXED_CHUNK replace the
  * chunk step, keeping cand as below: kept is the R first positions in the
