@@ -5,118 +5,1033 @@
 //     out[t][h] = sum_{x <= p} softmax_x(<q[t][h], k_x> / sqrt(D)) v_x
 // over the keys of the sequence, read through its block table.
 //
-// One warp per (row, query head): lanes take one key each for the logits, and
-// D/32 dims each for the weighted sum, with the running maximum and sum of the
-// softmax in fp32.
+// Both contractions run on the 5th-generation tensor cores.  The G query heads
+// of a KV head read the same keys, so a query tile is 128 rows of (token, head):
+// TQ = 128 / G tokens.  A work item is up to two query tiles of one sequence and
+// KV head and the keys that they see, in tiles of 128:
+//     S[128 rows][128 keys] = Q . K^T       (both operands in shared memory)
+//     O[128 rows][D]       += P . V         (P in TMEM over its S, V in shared memory)
+// with the running maximum and sum of each row's softmax in the registers of
+// the thread that owns it (warps 0-3: tile 0, warps 4-7: tile 1).  While one
+// tile's logits are exponentiated the tensor cores work on the other's.  An item
+// of at most TQ tokens (a decode or a short draft) has one query tile; its two
+// halves then take the even and the odd key tiles and are joined at the end.
+//
+//   * The reference of a row's exponentials moves only when the row's maximum
+//     has grown by more than 2^8 (kLazy): the weights stay below 2^8, where bf16
+//     holds them as well as below 1, and O is rescaled in TMEM a few times per
+//     row and not per tile.  The weights are rounded to bf16 for the second
+//     product (2^-8 of each at most; the output's own rounding is as large);
+//     logits, maxima, sums and O are fp32.
+//   * K and V come by TMA, one (block, KV head) slice of 16 rows at a time,
+//     128-byte swizzled, as 128-row tiles in a ring of 5 stages (160 KB in
+//     flight per SM).  Blocks past a sequence's end, and ids outside the pool,
+//     are copied from past the pool's end: the copy fills zeros.
+//   * A weight of 0 times NaN or infinity is NaN, so what a row must not see is
+//     cleared from V and not only masked in the logits: a warp zeroes the rows of
+//     the last block past the sequence's end, whatever they hold, and the values
+//     of the chunk's own tokens that are not finite (earlier tokens share their
+//     tile).  The rows that do see such a value get it added at the end.
+//   * Every CTA gets the same number of key tiles (to within one), whatever the
+//     lengths: all items' key tiles are laid end to end and cut evenly.  A cut
+//     inside an item leaves partial (O, max, sum) in the workspace, joined by
+//     the merge kernel in CTA order, so results do not depend on timing.
+//
+// Three launches: the plan (one CTA: checks, items and cuts), the attention
+// (persistent, one CTA per SM) and the merge, programmatic dependents of each
+// other.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
 #include "kara_common.cuh"
+#include "kara_sm100.cuh"
 
 namespace kara {
+
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();  // defined beside the scoring kernel
+cudaError_t pool_map(CUtensorMap *m, const void *pool, const kara_cache *c);  // defined beside decode attention
+
 namespace {
 
-constexpr int kWarps = 4;
+using namespace ptx;
+
+constexpr int kTile = 128;       // rows of a query tile, keys of a key tile
+constexpr int kBlk = 16;         // tokens per cache block (the supported block size)
+constexpr int kBlkPerTile = kTile / kBlk;
+constexpr int kStages = 5;       // K and V tiles in flight
+static_assert((kStages + 1) / 2 < 4, "V tiles in the ring: Shared::edge and odd_values tell four apart");
+constexpr int kMaxCtas = 160;    // CTAs of the attention kernel, at most (workspace slots)
+constexpr int kThreads = 384;    // two softmax warpgroups, one control warpgroup
+constexpr int kWarpKv = 8, kWarpMma = 9, kWarpQ = 10, kWarpFix = 11;
+// Registers per thread: at launch (65536 / 384, rounded down to 8), then after the
+// warpgroups trade: 256 * kRegsSoft + 128 * kRegsCtl == 384 * kRegsLaunch.
+constexpr int kRegsLaunch = 168;
+constexpr uint32_t kRegsSoft = 208, kRegsCtl = 88;
+static_assert(256 * kRegsSoft + 128 * kRegsCtl == kThreads * kRegsLaunch, "register trade must add up");
+constexpr uint32_t kTmemCols = 512;  // S0 S1 (128 columns each), O0 O1 (128 each)
+constexpr float kLazy = 8.f;         // see above: rescale when the maximum grew by more than 2^8
+constexpr uint64_t kTimeoutNs = 1000000000ull;
+constexpr int kPlanThreads = 1024;
+constexpr int kPlanCap = 4096;       // sequences / items whose prefix sums the plan keeps in shared memory
+
+// One or two query tiles of a sequence (all KV heads have the same items).
+struct __align__(16) Item {
+    int32_t row0;   // first row of q
+    int32_t ntok;   // tokens, <= 2 TQ
+    int32_t pos0;   // position of the first token
+    int32_t nt;     // key tiles that its last token sees
+    int32_t seq;
+    int32_t len;    // cached length of the sequence
+    int32_t before; // key tiles of the items before this one
+    int32_t pad;
+};
+
+// Where a CTA starts: key tile `off` of item `item` for KV head `head`.
+struct __align__(16) Start {
+    int32_t head, item, off, pad;
+};
+
+struct PlanHead {
+    int64_t tiles;    // key tiles of all items of one KV head
+    int32_t items;
+    int32_t ctas;     // CTAs that get work
+};
 
 struct ChunkArgs {
-    const uint16_t *q;
-    uint16_t *out;
-    const uint16_t *k, *v;  // pools at the call's layer
-    int64_t block_stride, head_stride;
     const int32_t *q_start, *len, *bt;
     int32_t *err;
-    int32_t n, rows, bt_stride, num_blocks, bs, hq, G;
-    float scale2;
+    int32_t n, rows, bt_stride, num_blocks, layer, hq, hkv, D, G, TQ, ctas, cap_items;
+    float scale2;     // log2(e) / sqrt(D)
+    uint16_t *out;
+    PlanHead *head;
+    Start *start;     // [ctas]
+    Item *items;      // [cap_items]
+    int32_t *seq_items;  // [n + 1]: items before each sequence
+    float *part;      // [2 * ctas][256][D]
+    float2 *stat;     // [2 * ctas][256]: (max, sum) in the log2 domain
+    const uint16_t *v;   // V pool at the call's layer
+    int64_t block_stride, head_stride;
+    int32_t stall;
+    uint64_t wait_ns;
+};
+
+__device__ __forceinline__ bool chunk_ok(const ChunkArgs &a, int32_t r0, int32_t r1, int32_t L)
+{
+    return r0 >= 0 && r1 >= r0 && r1 <= a.rows && L >= r1 - r0 && ((int64_t)L + kBlk - 1) / kBlk <= a.bt_stride;
+}
+
+// First unit of CTA c: the key tiles of all heads cut into equal ranges.
+__device__ __forceinline__ int64_t cut(int64_t units, int ctas, int c) { return units * c / ctas; }
+
+// ---- plan --------------------------------------------------------------------
+__device__ int64_t plan_scan(int64_t v, int64_t *scratch /* 33 */, int64_t *tot)
+{
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int64_t in = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t x = __shfl_up_sync(0xffffffffu, in, o);
+        if (lane >= o) in += x;
+    }
+    if (lane == 31) scratch[warp] = in;
+    __syncthreads();
+    if (warp == 0) {
+        const int64_t own = scratch[lane];
+        int64_t w = own;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t x = __shfl_up_sync(0xffffffffu, w, o);
+            if (lane >= o) w += x;
+        }
+        scratch[lane] = w - own;
+        if (lane == 31) scratch[32] = w;
+    }
+    __syncthreads();
+    const int64_t r = scratch[warp] + in - v;
+    *tot = scratch[32];
+    __syncthreads();
+    return r;
+}
+
+// Last index i in [0, n) with f(i) <= x, for f increasing and f(0) <= x.
+template <class F>
+__device__ __forceinline__ int last_at_most(int n, int64_t x, F f)
+{
+    int lo = 0, hi = n;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (f(mid) <= x) lo = mid; else hi = mid;
+    }
+    return lo;
+}
+
+__global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const ChunkArgs a)
+{
+    __shared__ int64_t scratch[33];
+    __shared__ int32_t seq_s[kPlanCap];  // items before each sequence
+    __shared__ int32_t item_s[kPlanCap]; // key tiles before each item
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int tid = threadIdx.x;
+    const int per = 2 * a.TQ;  // tokens of an item
+    int64_t items = 0;
+    for (int base = 0; base < a.n; base += kPlanThreads) {
+        const int s = base + tid;
+        int64_t v = 0;
+        if (s < a.n) {
+            const int32_t r0 = a.q_start[s], r1 = a.q_start[s + 1], L = a.len[s];
+            if (chunk_ok(a, r0, r1, L)) {
+                v = (r1 - r0 + per - 1) / per;
+            } else {
+                set_err(a.err, KARA_EINVAL);
+                const int64_t lo = max(r0, 0), hi = min(r1, a.rows);
+                uint32_t *o = reinterpret_cast<uint32_t *>(a.out);
+                const int64_t words = (int64_t)a.hq * a.D / 2;
+                for (int64_t i = lo * words; i < hi * words; ++i) o[i] = 0u;
+            }
+        }
+        int64_t tot;
+        const int64_t ex = items + plan_scan(v, scratch, &tot);
+        if (s < a.n) {
+            if (s < kPlanCap) seq_s[s] = (int32_t)min(ex, (int64_t)a.cap_items);
+            a.seq_items[s] = (int32_t)min(ex, (int64_t)a.cap_items);
+        }
+        items += tot;
+    }
+    // overlapping rows of a broken q_start could ask for more items than rows allow
+    items = min(items, (int64_t)a.cap_items);
+    __syncthreads();
+    int64_t tiles = 0;
+    for (int64_t base = 0; base < items; base += kPlanThreads) {
+        const int64_t i = base + tid;
+        Item it;
+        it.nt = 0;
+        if (i < items) {
+            const int s = a.n <= kPlanCap ? last_at_most(a.n, i, [&](int x) { return (int64_t)seq_s[x]; })
+                                          : last_at_most(a.n, i, [&](int x) { return (int64_t)a.seq_items[x]; });
+            const int32_t r0 = a.q_start[s], m = a.q_start[s + 1] - r0;
+            const int32_t t0 = (int32_t)(i - (a.n <= kPlanCap ? seq_s[s] : a.seq_items[s])) * per;
+            it.seq = s;
+            it.len = a.len[s];
+            it.row0 = r0 + t0;
+            it.ntok = min(per, m - t0);
+            it.pos0 = it.len - m + t0;
+            it.nt = (it.pos0 + it.ntok - 1) / kTile + 1;
+            it.pad = 0;
+        }
+        int64_t tot;
+        const int64_t ex = tiles + plan_scan(it.nt, scratch, &tot);
+        if (i < items) {
+            it.before = (int32_t)ex;
+            if (i < kPlanCap) item_s[i] = it.before;
+            a.items[i] = it;
+        }
+        tiles += tot;
+    }
+    __syncthreads();
+    const int64_t units = tiles * a.hkv;
+    const int ctas = (int)min((int64_t)a.ctas, units);
+    for (int c = tid; c < ctas; c += kPlanThreads) {
+        const int64_t u = cut(units, ctas, c), r = u % tiles;
+        const int i = items <= kPlanCap
+                          ? last_at_most((int)items, r, [&](int x) { return (int64_t)item_s[x]; })
+                          : last_at_most((int)items, r, [&](int x) { return (int64_t)a.items[x].before; });
+        Start st;
+        st.head = (int32_t)(u / tiles);
+        st.item = i;
+        st.off = (int32_t)(r - (items <= kPlanCap ? item_s[i] : a.items[i].before));
+        st.pad = 0;
+        a.start[c] = st;
+    }
+    if (tid == 0) {
+        a.head->tiles = tiles;
+        a.head->items = (int32_t)items;
+        a.head->ctas = ctas;
+    }
+}
+
+// ---- attention ------------------------------------------------------------------
+struct Shared {
+    uint64_t full[kStages], empty[kStages];  // K / V tiles
+    uint64_t q_full, q_empty;
+    uint64_t s_full[2];   // logits of a query tile are in TMEM (and its earlier products are done)
+    uint64_t p_full[2];   // its weights are in TMEM
+    uint64_t o_full[2];   // its last product is done
+    uint64_t x_full, x_free;  // a single query tile's odd half is ready to be joined; is joined
+    uint64_t edge[4];     // an edge tile of V has landed (by their number mod 4: the ring holds at most three);
+                          // `full` then says that it is clean
+    uint64_t done;
+    uint32_t tmem;
+    int32_t abort;
+    int32_t odd_values[4];  // 1 + the last piece (by its number mod 4) whose V had values that are not finite
+    float2 stat[kTile];   // (max, sum) of the odd key tiles, for joining a single query tile
 };
 
 template <int D>
-__global__ void __launch_bounds__(kWarps * 32) chunk_kernel(const ChunkArgs a)
+struct Cfg {
+    static constexpr int kHalves = D / 64;
+    static constexpr int kHalfBytes = kTile * 128;            // 128 rows of 64 dims
+    static constexpr int kTileBytes = kHalves * kHalfBytes;
+    static constexpr size_t kSmem = 1024 + (size_t)(2 + kStages) * kTileBytes + sizeof(Shared);
+};
+
+// Bounded wait on phase `parity` of `bar`: gives up after limit_ns, or once another
+// warp of the CTA gave up, recording KARA_ETIMEOUT.
+__device__ __forceinline__ bool cwait(uint32_t bar, uint32_t parity, Shared *sh, const ChunkArgs &a)
 {
-    __shared__ float qs[kWarps][D];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int64_t unit = (int64_t)blockIdx.x * kWarps + warp;
-    const int64_t t = unit / a.hq;
-    const int h = (int)(unit % a.hq);
-    if (blockIdx.x == 0)
-        for (int s = threadIdx.x; s < a.n; s += kWarps * 32) {
-            const int32_t r0 = a.q_start[s], r1 = a.q_start[s + 1];
-            if (r0 < 0 || r1 < r0 || r1 > a.rows) set_err(a.err, KARA_EINVAL);
-        }
-    if (t >= a.rows || t >= a.q_start[a.n]) return;
-    int lo = 0, hi = a.n;
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (a.q_start[mid] <= t) lo = mid; else hi = mid;
-    }
-    const int s = lo;
-    const int32_t m = a.q_start[s + 1] - a.q_start[s], L = a.len[s];
-    uint16_t *o = a.out + (t * a.hq + h) * D;
-    if (m < 1 || L < m || t < a.q_start[s] || t >= a.q_start[s + 1] || ((int64_t)L + a.bs - 1) / a.bs > a.bt_stride) {
-        if (lane == 0) set_err(a.err, KARA_EINVAL);
-        for (int d = lane; d < D; d += 32) o[d] = 0;
-        return;
-    }
-    const int32_t last = L - m + (int32_t)(t - a.q_start[s]);
-    const uint16_t *qr = a.q + (t * a.hq + h) * D;
-    for (int d = lane; d < D; d += 32) qs[warp][d] = __uint_as_float((uint32_t)qr[d] << 16) * a.scale2;
-    __syncwarp();
-    float mx = -INFINITY, z = 0.f, acc[D / 32];
-#pragma unroll
-    for (int i = 0; i < D / 32; ++i) acc[i] = 0.f;
-    for (int32_t x0 = 0; x0 <= last; x0 += 32) {
-        const int32_t x = x0 + lane;
-        float l = -INFINITY;
-        int64_t off = -1;
-        if (x <= last) {
-            const int32_t b = a.bt[(int64_t)s * a.bt_stride + x / a.bs];
-            l = 0.f;
-            if (b < 0 || b >= a.num_blocks) {
-                set_err(a.err, KARA_EBADBLOCK);
-            } else {
-                off = b * a.block_stride + (int64_t)(h / a.G) * a.head_stride + (int64_t)(x % a.bs) * D;
-                for (int d = 0; d < D; ++d) l = fmaf(qs[warp][d], __uint_as_float((uint32_t)a.k[off + d] << 16), l);
+    if (mbar_try_wait(bar, parity)) return true;
+    uint64_t t0 = 0;
+    for (uint32_t it = 1;; ++it) {
+        if (mbar_try_wait(bar, parity)) return true;
+        if ((it & 63u) == 0) {
+            if (*(volatile int32_t *)&sh->abort) return false;
+            const uint64_t now = globaltimer();
+            if (t0 == 0) {
+                t0 = now;
+            } else if (now - t0 > a.wait_ns) {
+                set_err(a.err, KARA_ETIMEOUT);
+                *(volatile int32_t *)&sh->abort = 1;
+                return false;
             }
         }
-        float nm = l;
-#pragma unroll
-        for (int i = 16; i > 0; i >>= 1) nm = fmaxf(nm, __shfl_xor_sync(0xffffffffu, nm, i));
-        nm = fmaxf(nm, mx);
-        const float c = exp2f(mx - nm), p = x <= last ? exp2f(l - nm) : 0.f;
-        mx = nm;
-        z = z * c + p;
-#pragma unroll
-        for (int i = 0; i < D / 32; ++i) acc[i] *= c;
-        for (int j = 0; j < 32 && x0 + j <= last; ++j) {
-            const float pj = __shfl_sync(0xffffffffu, p, j);
-            const int64_t oj = __shfl_sync(0xffffffffu, off, j);
-            if (oj >= 0)
-#pragma unroll
-                for (int i = 0; i < D / 32; ++i)
-                    acc[i] = fmaf(pj, __uint_as_float((uint32_t)a.v[oj + i * 32 + lane] << 16), acc[i]);
+    }
+}
+
+// Wait for work in flight that has to land whatever happened: by time alone.
+__device__ __forceinline__ void drain(uint32_t bar, uint32_t parity)
+{
+    const uint64_t t0 = globaltimer();
+    while (!mbar_try_wait(bar, parity))
+        if (globaltimer() - t0 > kTimeoutNs) return;
+}
+
+// D[tmem] (+)= A[tmem, bf16] * B[smem], fp32 accumulate; one thread issues.
+__device__ __forceinline__ void mma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
+                                            uint32_t accumulate)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\ttcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::
+            "r"(d_tmem),
+        "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+// Descriptor of an operand whose rows (128 bytes, 128-byte swizzle) run along K:
+// its M/N dim is contiguous in 64-element pieces `piece` bytes apart, K in groups
+// of 8 rows 1024 bytes apart.
+__device__ __forceinline__ uint64_t sdesc_sw128_mn(uint32_t saddr, uint32_t piece)
+{
+    uint64_t d = 0;
+    d |= (uint64_t)((saddr & 0x3FFFFu) >> 4);
+    d |= (uint64_t)(piece >> 4) << 16;
+    d |= (uint64_t)(1024 >> 4) << 32;
+    d |= (uint64_t)1 << 46;
+    d |= (uint64_t)2 << 61;
+    return d;
+}
+
+// 32 lanes x 32 consecutive 32-bit columns into v[o..o+31].
+template <int N>
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&v)[N], const int o)
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
+        "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(v[o + 0]), "=r"(v[o + 1]), "=r"(v[o + 2]), "=r"(v[o + 3]), "=r"(v[o + 4]), "=r"(v[o + 5]),
+          "=r"(v[o + 6]), "=r"(v[o + 7]), "=r"(v[o + 8]), "=r"(v[o + 9]), "=r"(v[o + 10]), "=r"(v[o + 11]),
+          "=r"(v[o + 12]), "=r"(v[o + 13]), "=r"(v[o + 14]), "=r"(v[o + 15]), "=r"(v[o + 16]), "=r"(v[o + 17]),
+          "=r"(v[o + 18]), "=r"(v[o + 19]), "=r"(v[o + 20]), "=r"(v[o + 21]), "=r"(v[o + 22]), "=r"(v[o + 23]),
+          "=r"(v[o + 24]), "=r"(v[o + 25]), "=r"(v[o + 26]), "=r"(v[o + 27]), "=r"(v[o + 28]), "=r"(v[o + 29]),
+          "=r"(v[o + 30]), "=r"(v[o + 31])
+        : "r"(taddr));
+}
+
+template <int N>
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&v)[N], const int o)
+{
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,"
+        "%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+        "r"(v[o + 0]), "r"(v[o + 1]), "r"(v[o + 2]), "r"(v[o + 3]), "r"(v[o + 4]), "r"(v[o + 5]), "r"(v[o + 6]),
+        "r"(v[o + 7]), "r"(v[o + 8]), "r"(v[o + 9]), "r"(v[o + 10]), "r"(v[o + 11]), "r"(v[o + 12]), "r"(v[o + 13]),
+        "r"(v[o + 14]), "r"(v[o + 15]), "r"(v[o + 16]), "r"(v[o + 17]), "r"(v[o + 18]), "r"(v[o + 19]),
+        "r"(v[o + 20]), "r"(v[o + 21]), "r"(v[o + 22]), "r"(v[o + 23]), "r"(v[o + 24]), "r"(v[o + 25]),
+        "r"(v[o + 26]), "r"(v[o + 27]), "r"(v[o + 28]), "r"(v[o + 29]), "r"(v[o + 30]), "r"(v[o + 31])
+        : "memory");
+}
+
+// Waits for this thread's tcgen05.ld; ties the 32 registers so no use moves above it.
+template <int N>
+__device__ __forceinline__ void tmem_wait_ld32(uint32_t (&v)[N], const int o)
+{
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(v[o + 0]), "+r"(v[o + 1]), "+r"(v[o + 2]), "+r"(v[o + 3]), "+r"(v[o + 4]), "+r"(v[o + 5]),
+                   "+r"(v[o + 6]), "+r"(v[o + 7]), "+r"(v[o + 8]), "+r"(v[o + 9]), "+r"(v[o + 10]), "+r"(v[o + 11]),
+                   "+r"(v[o + 12]), "+r"(v[o + 13]), "+r"(v[o + 14]), "+r"(v[o + 15]), "+r"(v[o + 16]),
+                   "+r"(v[o + 17]), "+r"(v[o + 18]), "+r"(v[o + 19]), "+r"(v[o + 20]), "+r"(v[o + 21]),
+                   "+r"(v[o + 22]), "+r"(v[o + 23]), "+r"(v[o + 24]), "+r"(v[o + 25]), "+r"(v[o + 26]),
+                   "+r"(v[o + 27]), "+r"(v[o + 28]), "+r"(v[o + 29])
+                 :
+                 : "memory");
+    asm volatile("" : "+r"(v[o + 30]), "+r"(v[o + 31]) : : "memory");
+}
+
+// (lo, hi) rounded to nearest-even bf16, lo in the low half.
+__device__ __forceinline__ uint32_t bf16x2(float lo, float hi)
+{
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+// A CTA's walk over its range of key tiles: piece by piece, the same in every warp.
+struct Piece {
+    Item it;
+    int32_t head, j0, j1;  // key tiles [j0, j1)
+    bool whole;            // covers the item: the output is written, not a partial
+    int32_t slot;          // workspace slot of a partial
+};
+
+struct Walk {
+    const ChunkArgs &a;
+    int64_t left;
+    int32_t items, head, item, off, cta;
+    bool first;
+    Item next;
+    __device__ Walk(const ChunkArgs &args) : a(args)
+    {
+        cta = blockIdx.x;
+        const PlanHead h = *a.head;
+        items = h.items;
+        left = 0;
+        first = true;
+        if (cta < h.ctas) {
+            const int64_t units = h.tiles * a.hkv;
+            left = cut(units, h.ctas, cta + 1) - cut(units, h.ctas, cta);
+            const Start s = a.start[cta];
+            head = s.head, item = s.item, off = s.off;
+            next = a.items[item];
         }
     }
-#pragma unroll
-    for (int i = 16; i > 0; i >>= 1) z += __shfl_xor_sync(0xffffffffu, z, i);
-#pragma unroll
-    for (int i = 0; i < D / 32; ++i) {
-        const float r = acc[i] / z;
-        uint16_t b;
-        asm("cvt.rn.bf16.f32 %0, %1;" : "=h"(b) : "f"(r));
-        o[i * 32 + lane] = b;
+    __device__ bool step(Piece &p)
+    {
+        if (left <= 0) return false;
+        p.it = next;
+        p.head = head;
+        p.j0 = off;
+        p.j1 = (int32_t)min((int64_t)p.it.nt, off + left);
+        p.whole = off == 0 && p.j1 == p.it.nt;
+        p.slot = 2 * cta + (first ? 0 : 1);
+        first = false;
+        left -= p.j1 - p.j0;
+        off = 0;
+        if (++item == items) item = 0, ++head;
+        if (left > 0) next = a.items[item];
+        return true;
     }
+};
+
+// Key tiles of query tile x in a piece: `cnt` of them, from j, `by` apart.
+struct Part {
+    int32_t j, by, cnt;
+};
+
+__device__ __forceinline__ Part part_of(const Piece &p, int x, int TQ)
+{
+    Part r;
+    if (p.it.ntok > TQ) {  // two query tiles: both take every key tile they see
+        const int32_t seen = (p.it.pos0 + min(p.it.ntok, (x + 1) * TQ) - 1) / kTile + 1;
+        r.j = p.j0, r.by = 1, r.cnt = max(0, min(p.j1, seen) - p.j0);
+    } else {               // one query tile: the even and the odd key tiles of the piece
+        r.j = p.j0 + x, r.by = 2, r.cnt = (p.j1 - p.j0 + 1 - x) / 2;
+    }
+    return r;
+}
+
+// Key tile j holds rows that not every row of the item sees: new tokens after the
+// item's first, or the rest of the sequence's last block.
+__device__ __forceinline__ bool edge_tile(const Item &it, int j)
+{
+    const int32_t end = it.len - j * kTile;
+    return min(end, kTile) > it.pos0 + 1 - j * kTile || (end < kTile && end % kBlk != 0);
+}
+
+// A bf16 pair with its infinities and NaNs cleared.
+__device__ __forceinline__ uint32_t finite_pair(uint32_t w)
+{
+    if ((w & 0x7f80u) == 0x7f80u) w &= 0xffff0000u;
+    if ((w & 0x7f800000u) == 0x7f800000u) w &= 0x0000ffffu;
+    return w;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
+                 const __grid_constant__ CUtensorMap qmap, const ChunkArgs a)
+{
+    using C = Cfg<D>;
+    extern __shared__ uint8_t csm_raw[];
+    uint8_t *qbuf = csm_raw + ((1024u - (smem_u32(csm_raw) & 1023u)) & 1023u);  // two query tiles
+    uint8_t *ring = qbuf + 2 * C::kTileBytes;
+    Shared *sh = reinterpret_cast<Shared *>(ring + kStages * C::kTileBytes);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+    if (tid == 0) {
+        for (int i = 0; i < kStages; ++i) {
+            mbar_init(smem_u32(&sh->full[i]), 1);
+            mbar_init(smem_u32(&sh->empty[i]), 1);
+        }
+        mbar_init(smem_u32(&sh->q_full), 1);
+        mbar_init(smem_u32(&sh->q_empty), 1);
+        for (int x = 0; x < 2; ++x) {
+            mbar_init(smem_u32(&sh->s_full[x]), 1);
+            mbar_init(smem_u32(&sh->p_full[x]), 4);
+            mbar_init(smem_u32(&sh->o_full[x]), 1);
+        }
+        mbar_init(smem_u32(&sh->x_full), 4);
+        mbar_init(smem_u32(&sh->x_free), 4);
+        for (int i = 0; i < 4; ++i) mbar_init(smem_u32(&sh->edge[i]), 1);
+        mbar_init(smem_u32(&sh->done), 1);
+        sh->abort = 0;
+        for (int i = 0; i < 4; ++i) sh->odd_values[i] = 0;
+        fence_mbarrier_init();
+    }
+    // rows of the query tiles past G * TQ are never filled: zeros
+    const int qrows = a.G * a.TQ;
+    for (int i = tid; i < (kTile - qrows) * 8 * 2 * C::kHalves; i += kThreads) {
+        const int b = i / ((kTile - qrows) * 8), r = i % ((kTile - qrows) * 8);
+        reinterpret_cast<uint4 *>(qbuf + b * C::kHalfBytes + qrows * 128)[r] = make_uint4(0, 0, 0, 0);
+    }
+    fence_proxy_async_smem();
+    if (warp == kWarpMma) {
+        tmem_alloc(smem_u32(&sh->tmem), kTmemCols);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = sh->tmem;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+
+    if (warp >= 8) {
+        reg_dealloc<kRegsCtl>();
+        if (warp == kWarpKv) {
+            // ---------------- K and V tiles: 8 blocks x (D/64) halves per tile, a lane per copy
+            Walk w(a);
+            Piece p;
+            uint32_t k = 0;  // tiles issued
+            uint32_t ne = 0, were_edges = 0;  // edge tiles issued; which of the last tiles were (bit 0: the last)
+            const int b = lane % kBlkPerTile, h = lane / kBlkPerTile;
+            const bool mine = h < C::kHalves;
+            bool ok = !a.stall;
+            while (ok && w.step(p)) {
+                const int32_t *row = a.bt + (int64_t)p.it.seq * a.bt_stride;
+                const int32_t nblk = (p.it.len + kBlk - 1) / kBlk;
+                auto block_id = [&](int j) -> int32_t {
+                    const int i = j * kBlkPerTile + b;
+                    int32_t id = a.num_blocks;  // past the pool: zeros
+                    if (i < nblk) {
+                        id = row[i];
+                        if (id < 0 || id >= a.num_blocks) {
+                            set_err(a.err, KARA_EBADBLOCK);
+                            id = a.num_blocks;
+                        }
+                    }
+                    return id;
+                };
+                int32_t id = block_id(p.j0);
+                for (int j = p.j0; ok && j < p.j1; ++j) {
+                    const int32_t cur = id;
+                    if (j + 1 < p.j1) id = block_id(j + 1);
+#pragma unroll
+                    for (int kv = 0; kv < 2; ++kv) {
+                        const int st = k % kStages;
+                        ok = cwait(smem_u32(&sh->empty[st]), ((k / kStages) & 1) ^ 1, sh, a);
+                        ok = __all_sync(0xffffffffu, ok);
+                        if (!ok) break;
+                        const bool edge = kv && edge_tile(p.it, j);
+                        const uint32_t fb = smem_u32(edge ? &sh->edge[ne & 3] : &sh->full[st]);
+                        ne += edge;
+                        were_edges = were_edges << 1 | (edge ? 1u : 0u);
+                        if (lane == 0) mbar_arrive_expect_tx(fb, C::kTileBytes);
+                        __syncwarp();
+                        if (mine)
+                            tma_load_5d(smem_u32(ring + st * C::kTileBytes + h * C::kHalfBytes + b * kBlk * 128),
+                                        kv ? &vmap : &kmap, fb, h * 64, 0, p.head, cur, a.layer);
+                        ++k;
+                    }
+                }
+            }
+            // every copy has landed before the CTA's shared memory is released
+            for (uint32_t i = k > kStages ? k - kStages : 0; i < k; ++i)
+                if (!(were_edges >> (k - 1 - i) & 1u)) drain(smem_u32(&sh->full[i % kStages]), (i / kStages) & 1);
+            for (uint32_t i = ne > 3 ? ne - 3 : 0; i < ne; ++i) drain(smem_u32(&sh->edge[i & 3]), (i >> 2) & 1);
+        } else if (warp == kWarpQ) {
+            // ---------------- query tiles
+            if (lane == 0) {
+                Walk w(a);
+                Piece p;
+                uint32_t i = 0;
+                while (!a.stall && w.step(p)) {
+                    if (!cwait(smem_u32(&sh->q_empty), (i & 1) ^ 1, sh, a)) break;
+                    const int tiles = p.it.ntok > a.TQ ? 2 : 1;
+                    const uint32_t fb = smem_u32(&sh->q_full);
+                    mbar_arrive_expect_tx(fb, tiles * C::kHalves * qrows * 128);
+                    for (int x = 0; x < tiles; ++x)
+#pragma unroll
+                        for (int h = 0; h < C::kHalves; ++h)
+                            asm volatile(
+                                "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+                                "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_u32(qbuf + x * C::kTileBytes +
+                                                                                 h * C::kHalfBytes)),
+                                "l"(reinterpret_cast<uint64_t>(&qmap)), "r"(h * 64), "r"(p.head * a.G),
+                                "r"(p.it.row0 + x * a.TQ), "r"(fb)
+                                : "memory");
+                    ++i;
+                }
+                if (i > 0) drain(smem_u32(&sh->q_full), (i - 1) & 1);
+            }
+            __syncwarp();
+        } else if (warp == kWarpMma) {
+            // ---------------- MMAs
+            constexpr uint32_t id_qk = idesc_bf16(kTile, kTile);
+            constexpr uint32_t id_pv = idesc_bf16(kTile, D) | (1u << 16);  // V: its dims are contiguous
+            Walk w(a);
+            Piece p;
+            uint32_t k0 = 0;             // ring index of the piece's first K tile
+            uint32_t np[2] = {0, 0};     // weights waited for
+            uint32_t iq = 0;
+            bool ok = true;
+            auto wait_tile = [&](uint32_t k) {
+                ok = ok && cwait(smem_u32(&sh->full[k % kStages]), (k / kStages) & 1, sh, a);
+                ok = __all_sync(0xffffffffu, ok);
+            };
+            auto release = [&](uint32_t k) { mma_commit(smem_u32(&sh->empty[k % kStages])); };
+            while (ok && w.step(p)) {
+                const bool two = p.it.ntok > a.TQ;
+                const Part pt[2] = {part_of(p, 0, a.TQ), part_of(p, 1, a.TQ)};
+                ok = __all_sync(0xffffffffu, cwait(smem_u32(&sh->q_full), iq & 1, sh, a));
+                ++iq;
+                auto qk = [&](int x, int i) {  // logits of query tile x on its i-th key tile
+                    const uint32_t k = k0 + 2 * (pt[x].j + i * pt[x].by - p.j0);
+                    wait_tile(k);
+                    if (!ok) return;
+                    if (lane == 0) {
+                        const uint32_t qa = smem_u32(qbuf + (two ? x : 0) * C::kTileBytes);
+                        const uint32_t ka = smem_u32(ring + (k % kStages) * C::kTileBytes);
+#pragma unroll
+                        for (int ks = 0; ks < D / 16; ++ks) {
+                            const uint32_t o = (ks >> 2) * C::kHalfBytes + (ks & 3) * 32;
+                            mma_bf16(tmem + x * kTile, sdesc_sw128(qa + o), sdesc_sw128(ka + o), id_qk, ks > 0);
+                        }
+                        mma_commit(smem_u32(&sh->s_full[x]));
+                        // a key tile that both query tiles take is tile 1's to release
+                        if (!two || x == 1) release(k);
+                    }
+                    __syncwarp();
+                };
+                auto pv = [&](int x, int i) {
+                    const int j = pt[x].j + i * pt[x].by;
+                    const uint32_t k = k0 + 2 * (j - p.j0) + 1;
+                    wait_tile(k);
+                    ok = ok && cwait(smem_u32(&sh->p_full[x]), np[x] & 1, sh, a);
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) return;
+                    ++np[x];
+                    const uint32_t va = smem_u32(ring + (k % kStages) * C::kTileBytes);
+                    if (lane == 0) {
+                        tc_fence_after();
+#pragma unroll
+                        for (int ks = 0; ks < kTile / 16; ++ks)
+                            mma_bf16_ts(tmem + 256 + x * 128, tmem + x * kTile + ks * 8,
+                                        sdesc_sw128_mn(va + ks * 2048, C::kHalfBytes), id_pv, i > 0 || ks > 0);
+                        if (!two || x == 1) release(k);
+                        if (i + 1 == pt[x].cnt) mma_commit(smem_u32(&sh->o_full[x]));
+                    }
+                    __syncwarp();
+                };
+                for (int x = 0; ok && x < 2; ++x)
+                    if (pt[x].cnt > 0) qk(x, 0);
+                bool q_held = true;
+                const int cnt = max(pt[0].cnt, pt[1].cnt);
+                for (int i = 0; ok && i < cnt; ++i) {
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        if (ok && i < pt[x].cnt) pv(x, i);
+                        if (ok && i + 1 < pt[x].cnt) qk(x, i + 1);
+                    }
+                    if (ok && q_held && i + 2 >= cnt) {  // every logit product of the piece is issued
+                        if (lane == 0) mma_commit(smem_u32(&sh->q_empty));
+                        q_held = false;
+                    }
+                }
+                k0 += 2 * (p.j1 - p.j0);
+            }
+            // the tensor cores are idle before TMEM and shared memory go
+            if (lane == 0) {
+                mma_commit(smem_u32(&sh->done));
+                drain(smem_u32(&sh->done), 0);
+            }
+            __syncwarp();
+        } else if (warp == kWarpFix) {
+            // ---------------- edge tiles of V
+            Walk w(a);
+            Piece p;
+            uint32_t k0 = 0, np = 0, ne = 0;
+            bool ok = true;
+            for (; ok && w.step(p); ++np) {
+                for (int j = max(p.j0, (p.it.pos0 + 1) / kTile); ok && j < p.j1; ++j) {
+                    if (!edge_tile(p.it, j)) continue;
+                    const uint32_t k = k0 + 2 * (j - p.j0) + 1;
+                    ok = __all_sync(0xffffffffu, cwait(smem_u32(&sh->edge[ne & 3]), (ne >> 2) & 1, sh, a));
+                    if (!ok) break;
+                    ++ne;
+                    const int end = min(p.it.len - j * kTile, kTile);     // rows from here on: past the sequence
+                    const int r0 = max(0, min(end, p.it.pos0 + 1 - j * kTile));  // rows from here on: new tokens
+                    const int r1 = (end + kBlk - 1) / kBlk * kBlk;        // rows from here on are zeros already
+                    bool odd = false;
+#pragma unroll
+                    for (int h = 0; h < C::kHalves; ++h) {
+                        uint4 *t = reinterpret_cast<uint4 *>(ring + (k % kStages) * C::kTileBytes + h * C::kHalfBytes);
+#pragma unroll 4
+                        for (int e = r0 * 8 + lane; e < end * 8; e += 32) {
+                            const uint4 v = t[e];
+                            const uint4 f = make_uint4(finite_pair(v.x), finite_pair(v.y), finite_pair(v.z),
+                                                       finite_pair(v.w));
+                            if (f.x != v.x || f.y != v.y || f.z != v.z || f.w != v.w) {
+                                t[e] = f;
+                                odd = true;
+                            }
+                        }
+                        for (int e = end * 8 + lane; e < r1 * 8; e += 32) t[e] = make_uint4(0, 0, 0, 0);
+                    }
+                    odd = __any_sync(0xffffffffu, odd);
+                    if (odd && lane == 0) sh->odd_values[np & 3] = (int32_t)np + 1;
+                    __threadfence_block();
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(smem_u32(&sh->full[k % kStages]));
+                }
+                k0 += 2 * (p.j1 - p.j0);
+            }
+        }
+    } else {
+        // ---------------- softmax: thread = one row of query tile x
+        reg_alloc<kRegsSoft>();
+        const int x = warp >> 2, r = tid & 127;
+        const int tok = r / a.G, hd = r - tok * a.G;
+        const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+        const uint32_t ts = tmem + lanes + x * kTile, to = tmem + lanes + 256 + x * 128;
+        Walk w(a);
+        Piece p;
+        uint32_t ns = 0, no = 0, nj = 0, np = 0;
+        bool ok = true;
+        for (; ok && w.step(p); ++np) {
+            const bool two = p.it.ntok > a.TQ;
+            const Part pt = part_of(p, x, a.TQ);
+            const int t = (two ? x * a.TQ : 0) + tok;  // token of the item
+            const bool live = r < qrows && t < p.it.ntok;
+            const bool any = __any_sync(0xffffffffu, live);
+            // a row without a token is computed like the others and dropped at the end
+            const int32_t pos = live ? p.it.pos0 + t : 0x3fffffff;
+            float m = -INFINITY, z = 0.f;
+            for (int i = 0; i < pt.cnt; ++i) {
+                const int j = pt.j + i * pt.by;
+                ok = cwait(smem_u32(&sh->s_full[x]), ns & 1, sh, a);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                ++ns;
+                if (any) {
+                    tc_fence_after();
+                    uint32_t s[kTile];
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) tmem_ld32(ts + c * 32, s, c * 32);
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) tmem_wait_ld32(s, c * 32);
+                    const int lim = pos - j * kTile;  // last key of the tile that the row sees
+                    if (__any_sync(0xffffffffu, lim < kTile - 1)) {
+#pragma unroll
+                        for (int c = 0; c < kTile; ++c)
+                            if (c > lim) s[c] = 0xff800000u;
+                    }
+                    float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                    for (int c = 0; c < kTile; c += 8)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            mx[e] = fmaxf(mx[e], fmaxf(__uint_as_float(s[c + 2 * e]), __uint_as_float(s[c + 2 * e + 1])));
+                    const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.scale2;
+                    if (i == 0) {
+                        m = mt;
+                    } else {
+                        const bool grew = mt > m + kLazy;
+                        if (__any_sync(0xffffffffu, grew)) {
+                            const float f = grew ? ex2(m - mt) : 1.f;
+                            if (grew) m = mt;
+                            z *= f;
+#pragma unroll
+                            for (int c = 0; c < D; c += 32) {
+                                uint32_t o[32];
+                                tmem_ld32(to + c, o, 0);
+                                tmem_wait_ld32(o, 0);
+#pragma unroll
+                                for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                                tmem_st32(to + c, o, 0);
+                            }
+                            tmem_wait_st();
+                        }
+                    }
+                    const float ref = m == -INFINITY ? 0.f : m;  // a row that saw nothing yet: weights 2^-inf = 0
+                    const uint64_t sc = pack2(a.scale2, a.scale2), mr = pack2(-ref, -ref);
+                    uint64_t sum[2] = {0ull, 0ull};
+#pragma unroll
+                    for (int c = 0; c < kTile; c += 2) {
+                        float lo, hi;
+                        unpack2(fma2(pack2(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), sc, mr), lo, hi);
+                        lo = ex2(lo);
+                        hi = ex2(hi);
+                        sum[(c >> 1) & 1] = add2(sum[(c >> 1) & 1], pack2(lo, hi));
+                        s[c >> 1] = bf16x2(lo, hi);
+                    }
+                    tmem_st32(ts, s, 0);
+                    tmem_st32(ts + 32, s, 32);
+                    float s0, s1;
+                    unpack2(add2(sum[0], sum[1]), s0, s1);
+                    z += s0 + s1;
+                    tmem_wait_st();
+                    tc_fence_before();
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&sh->p_full[x]));
+            }
+            if (ok && pt.cnt > 0) {
+                ok = cwait(smem_u32(&sh->o_full[x]), no & 1, sh, a);
+                ++no;
+            }
+            ok = __all_sync(0xffffffffu, ok);
+            tc_fence_after();
+            // ---- output: O / z, or the partial of a piece
+            const bool joined = !two;
+            float f0 = 1.f, f1 = 0.f;
+            const bool odd = joined && p.j1 - p.j0 > 1;  // the odd key tiles have a partial too
+            if (ok && joined && x == 1) {
+                sh->stat[r] = make_float2(m, z);
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&sh->x_full));
+                // O1 is written again only after warps 0-3 have read it
+                ok = cwait(smem_u32(&sh->x_free), nj & 1, sh, a);
+            } else if (ok && joined) {
+                ok = cwait(smem_u32(&sh->x_full), nj & 1, sh, a);
+                tc_fence_after();
+                if (ok && odd) {
+                    const float2 o = sh->stat[r];
+                    const float M = fmaxf(m, o.x), ref = M == -INFINITY ? 0.f : M;
+                    f0 = ex2(m - ref);
+                    f1 = ex2(o.x - ref);
+                    m = M;
+                    z = z * f0 + o.y * f1;
+                }
+            }
+            ok = __all_sync(0xffffffffu, ok);
+            if (ok && any && (x == 0 || two)) {
+                const float inv = p.whole ? 1.f / z : 1.f;
+                f0 *= inv, f1 *= inv;
+                const int64_t row = p.it.row0 + t;
+                const int rr = (two ? x * kTile : 0) + r;
+                const bool add = *(volatile int32_t *)&sh->odd_values[np & 3] == (int32_t)np + 1;
+                float *pp = a.part + ((int64_t)p.slot * 256 + rr) * D;
+                uint16_t *op = a.out + (row * a.hq + p.head * a.G + hd) * D;
+#pragma unroll
+                for (int c = 0; c < D; c += 32) {
+                    uint32_t o[32];
+                    tmem_ld32(to + c, o, 0);
+                    tmem_wait_ld32(o, 0);
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f0);
+                    if (odd) {
+                        uint32_t o1[32];
+                        tmem_ld32(to + 128 + c, o1, 0);
+                        tmem_wait_ld32(o1, 0);
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            o[e] = __float_as_uint(fmaf(__uint_as_float(o1[e]), f1, __uint_as_float(o[e])));
+                    }
+                    if (!live) continue;
+                    if (add) {
+                        // values of new tokens that are not finite were cleared from V: every row that sees one gets it
+                        for (int32_t y = max(p.it.pos0 + 1, p.j0 * kTile); y <= min(pos, p.j1 * kTile - 1); ++y) {
+                            const int32_t id = a.bt[(int64_t)p.it.seq * a.bt_stride + y / kBlk];
+                            if (id < 0 || id >= a.num_blocks) continue;
+                            const uint16_t *vr = a.v + id * a.block_stride + p.head * a.head_stride +
+                                                 (int64_t)(y % kBlk) * D + c;
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) {
+                                const uint32_t b = vr[e];
+                                if ((b & 0x7f80u) == 0x7f80u)
+                                    o[e] = __float_as_uint(__uint_as_float(o[e]) + __uint_as_float(b << 16));
+                            }
+                        }
+                    }
+                    if (p.whole) {
+#pragma unroll
+                        for (int e = 0; e < 32; e += 8)
+                            *reinterpret_cast<uint4 *>(op + c + e) =
+                                make_uint4(bf16x2(__uint_as_float(o[e]), __uint_as_float(o[e + 1])),
+                                           bf16x2(__uint_as_float(o[e + 2]), __uint_as_float(o[e + 3])),
+                                           bf16x2(__uint_as_float(o[e + 4]), __uint_as_float(o[e + 5])),
+                                           bf16x2(__uint_as_float(o[e + 6]), __uint_as_float(o[e + 7])));
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 32; e += 4)
+                            *reinterpret_cast<uint4 *>(pp + c + e) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+                    }
+                }
+                if (live && !p.whole) a.stat[(int64_t)p.slot * 256 + rr] = make_float2(m, z);
+            }
+            // the next piece's products write O again only after these reads
+            tc_fence_before();
+            if (joined) {
+                ++nj;
+                __syncwarp();
+                if (x == 0 && lane == 0) mbar_arrive(smem_u32(&sh->x_free));
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == kWarpMma) tmem_dealloc(tmem, kTmemCols);
+}
+
+// ---- merge ----------------------------------------------------------------------
+// Block c: the item that the cut before CTA c falls into, if that is the item's
+// first cut: out = sum_i O_i 2^(m_i - M) / sum_i z_i 2^(m_i - M), pieces in CTA order.
+// A warp takes a row at a time.
+template <int D>
+__global__ void __launch_bounds__(256) chunk_merge_kernel(const ChunkArgs a)
+{
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const PlanHead h = *a.head;
+    const int c = blockIdx.x + 1;
+    if (c >= h.ctas) return;
+    const Start s = a.start[c];
+    if (s.off == 0) return;
+    const int64_t units = h.tiles * a.hkv;
+    const Item it = a.items[s.item];
+    const int64_t u0 = cut(units, h.ctas, c) - s.off, u1 = u0 + it.nt;  // the item's units
+    const int64_t before = cut(units, h.ctas, c - 1);
+    if (u0 < before) return;  // an earlier cut of the same item
+    const int first = 2 * (c - 1) + (u0 == before ? 0 : 1);
+    int last = c;
+    while (last + 1 < h.ctas && cut(units, h.ctas, last + 1) < u1) ++last;
+    const bool two = it.ntok > a.TQ;
+    const int lane = threadIdx.x & 31;
+    constexpr int V = D / 32;
+    for (int i = blockIdx.y * 8 + (threadIdx.x >> 5); i < it.ntok * a.G; i += gridDim.y * 8) {
+        const int t = i / a.G, hd = i % a.G;
+        const int rr = two && t >= a.TQ ? kTile + (t - a.TQ) * a.G + hd : t * a.G + hd;
+        float M = -INFINITY;
+        for (int k = c - 1; k <= last; ++k)
+            M = fmaxf(M, a.stat[(int64_t)(k < c ? first : 2 * k) * 256 + rr].x);
+        float den = 0.f, acc[V];
+#pragma unroll
+        for (int e = 0; e < V; ++e) acc[e] = 0.f;
+        for (int k = c - 1; k <= last; ++k) {
+            const int64_t o = (int64_t)(k < c ? first : 2 * k) * 256 + rr;
+            const float2 st = a.stat[o];
+            if (st.x == -INFINITY && st.y == 0.f) continue;  // nothing of this piece is seen by the row
+            const float f = ex2(st.x - M);
+            den = fmaf(st.y, f, den);
+#pragma unroll
+            for (int e = 0; e < V; ++e) acc[e] = fmaf(a.part[o * D + lane * V + e], f, acc[e]);
+        }
+        uint16_t *op = a.out + ((int64_t)(it.row0 + t) * a.hq + s.head * a.G + hd) * D + lane * V;
+#pragma unroll
+        for (int e = 0; e < V; e += 2)
+            *reinterpret_cast<uint32_t *>(op + e) = bf16x2(acc[e] / den, acc[e + 1] / den);
+    }
+}
+
+// Tensor map over q, (d, head, row); a box is one 64-dim half of a query tile.
+cudaError_t query_map(CUtensorMap *m, const void *q, const kara_cache *c, int32_t rows, int G, int TQ)
+{
+    auto fn = tensor_map_encoder();
+    if (!fn) return cudaErrorNotSupported;
+    cuuint64_t dims[3] = {(cuuint64_t)c->head_dim, (cuuint64_t)c->num_q_heads, (cuuint64_t)rows};
+    cuuint64_t strides[2] = {(cuuint64_t)c->head_dim * 2, (cuuint64_t)c->head_dim * c->num_q_heads * 2};
+    cuuint32_t box[3] = {64, (cuuint32_t)G, (cuuint32_t)TQ};
+    cuuint32_t estr[3] = {1, 1, 1};
+    if (fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(q), dims, strides, box, estr,
+           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+        return cudaErrorInvalidValue;
+    return cudaSuccess;
+}
+
+// Workspace: [head][starts][items][items before each sequence][stats][partials].
+struct Layout {
+    size_t start, items, seq, stat, part, total;
+    int32_t cap;
+};
+
+Layout layout(const kara_cache *c, int32_t n, int32_t rows)
+{
+    const int TQ = kTile / (c->num_q_heads / c->num_kv_heads);
+    Layout l;
+    l.cap = rows / (2 * TQ) + n;  // a sequence of m tokens has at most m / (2 TQ) + 1 items
+    size_t o = 256;
+    l.start = o, o += align256(kMaxCtas * sizeof(Start));
+    l.items = o, o += align256((size_t)l.cap * sizeof(Item));
+    l.seq = o, o += align256(((size_t)n + 1) * sizeof(int32_t));
+    l.stat = o, o += align256((size_t)2 * kMaxCtas * 256 * sizeof(float2));
+    l.part = o, o += (size_t)2 * kMaxCtas * 256 * c->head_dim * sizeof(float);
+    l.total = o;
+    return l;
+}
+
+template <class... A>
+cudaError_t launch_dependent(void (*kern)(A...), dim3 grid, int threads, size_t smem, cudaStream_t st, A... args)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
+template <int D>
+cudaError_t launch_all(const CUtensorMap &km, const CUtensorMap &vm, const CUtensorMap &qm, const ChunkArgs &a,
+                       cudaStream_t st)
+{
+    constexpr size_t smem = Cfg<D>::kSmem;
+    static_assert(smem <= 227 * 1024, "shared memory");
+    cudaError_t e = cudaFuncSetAttribute(chunk_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    e = launch_dependent(chunk_plan_kernel, dim3(1), kPlanThreads, 0, st, a);
+    if (e == cudaSuccess)
+        e = launch_dependent(chunk_kernel<D>, dim3((unsigned)a.ctas), kThreads, smem, st, km, vm, qm, a);
+    if (e == cudaSuccess && a.ctas > 1)
+        e = launch_dependent(chunk_merge_kernel<D>, dim3((unsigned)a.ctas - 1, 4), 256, 0, st, a);
+    return e;
 }
 
 }  // namespace
 
-size_t chunk_workspace_bytes(const kara_cache *, int32_t, int32_t) { return 256; }
+size_t chunk_workspace_bytes(const kara_cache *c, int32_t n, int32_t rows) { return layout(c, n, rows).total; }
 
 cudaError_t launch_chunk(const kara_cache *c, int32_t layer, const kara_tokens *t, const int32_t *bt,
-                         int32_t bt_stride, const void *q, void *out, void *, int32_t *err, cudaStream_t st)
+                         int32_t bt_stride, const void *q, void *out, void *ws, int32_t *err, cudaStream_t st)
 {
     ChunkArgs a;
-    a.q = static_cast<const uint16_t *>(q);
-    a.out = static_cast<uint16_t *>(out);
-    a.k = static_cast<const uint16_t *>(c->k) + (int64_t)layer * c->layer_stride;
-    a.v = static_cast<const uint16_t *>(c->v) + (int64_t)layer * c->layer_stride;
-    a.block_stride = c->block_stride;
-    a.head_stride = c->head_stride;
     a.q_start = t->q_start;
     a.len = t->len;
     a.bt = bt;
@@ -125,17 +1040,40 @@ cudaError_t launch_chunk(const kara_cache *c, int32_t layer, const kara_tokens *
     a.rows = t->rows;
     a.bt_stride = bt_stride;
     a.num_blocks = c->num_blocks;
-    a.bs = c->block_size;
+    a.layer = layer;
     a.hq = c->num_q_heads;
-    a.G = c->num_q_heads / c->num_kv_heads;
+    a.hkv = c->num_kv_heads;
+    a.D = c->head_dim;
+    a.G = a.hq / a.hkv;
+    a.TQ = kTile / a.G;
     a.scale2 = 1.4426950408889634f / sqrtf((float)c->head_dim);
-    const int64_t grid = ((int64_t)t->rows * a.hq + kWarps - 1) / kWarps;
-    if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-    if (c->head_dim == 128)
-        chunk_kernel<128><<<(unsigned)grid, kWarps * 32, 0, st>>>(a);
-    else
-        chunk_kernel<64><<<(unsigned)grid, kWarps * 32, 0, st>>>(a);
-    return cudaGetLastError();
+    a.out = static_cast<uint16_t *>(out);
+    a.v = static_cast<const uint16_t *>(c->v) + (int64_t)layer * c->layer_stride;
+    a.block_stride = c->block_stride;
+    a.head_stride = c->head_stride;
+    const Layout l = layout(c, t->n, t->rows);
+    char *w = static_cast<char *>(ws);
+    a.cap_items = l.cap;
+    a.head = reinterpret_cast<PlanHead *>(w);
+    a.start = reinterpret_cast<Start *>(w + l.start);
+    a.items = reinterpret_cast<Item *>(w + l.items);
+    a.seq_items = reinterpret_cast<int32_t *>(w + l.seq);
+    a.stat = reinterpret_cast<float2 *>(w + l.stat);
+    a.part = reinterpret_cast<float *>(w + l.part);
+    const Stall dbg = debug_stall(kTimeoutNs);
+    a.stall = dbg.on;
+    a.wait_ns = dbg.wait_ns;
+    int dev = 0, sms = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e != cudaSuccess) return e;
+    a.ctas = sms < kMaxCtas ? sms : kMaxCtas;
+    CUtensorMap km, vm, qm;
+    e = pool_map(&km, c->k, c);
+    if (e == cudaSuccess) e = pool_map(&vm, c->v, c);
+    if (e == cudaSuccess) e = query_map(&qm, q, c, t->rows, a.G, a.TQ);
+    if (e != cudaSuccess) return e;
+    return c->head_dim == 128 ? launch_all<128>(km, vm, qm, a, st) : launch_all<64>(km, vm, qm, a, st);
 }
 
 }  // namespace kara

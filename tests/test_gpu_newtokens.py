@@ -742,3 +742,17 @@ def test_chunk_workspace_too_small_is_refused():
         kara.kara_chunk_attention(c, 0, t, i32(d["bt"]), q, torch.empty_like(q),
                                   torch.empty(need - 1, dtype=torch.uint8, device=DEV), error_word())
     assert e.value.status == kara.EWORKSPACE
+
+
+def test_stalled_chunk_attention_times_out(monkeypatch):
+    """With KARA_DEBUG_STALL=1 no copy is issued: the bounded waits run out, the call reports it and the
+    next call on the same context is right."""
+    kara = lib()
+    d = chunk_inputs(95, [300, 900, 40], [10, 200, 1], 8, 2, 128)
+    monkeypatch.setenv("KARA_DEBUG_STALL", "1")
+    _, st = run_chunk(kara, d)
+    assert st == kara.ETIMEOUT
+    monkeypatch.delenv("KARA_DEBUG_STALL")
+    got, st = run_chunk(kara, d)
+    assert st == 0
+    check_chunk(d, got)
