@@ -37,6 +37,14 @@
 //     inside an item leaves partial (O, max, sum) in the workspace, joined by
 //     the merge kernel in CTA order, so results do not depend on timing.
 //
+// What set the pace on the way (8192 tokens over 16384 keys, 40/8 heads, D 128; us):
+// one thread issuing every MMA with the waits between them, 2008; its loop with ring
+// positions and descriptors that only advance by additions, 1715; one issuing thread
+// per query tile and one loading warp each for K and V (issuing a 2 KB copy takes about
+// 90 clocks: one warp took 2900 clocks for the K and V tiles that two query tiles multiply
+// in 2048), the two tiles taking turns, 1595; the turn taken before the weights are
+// waited for, 1485.
+//
 // Three launches: the plan (one CTA: checks, items and cuts), the attention
 // (persistent, one CTA per SM) and the merge, programmatic dependents of each
 // other.
@@ -61,13 +69,13 @@ constexpr int kBlkPerTile = kTile / kBlk;
 constexpr int kStages = 5;       // K and V tiles in flight
 static_assert((kStages + 1) / 2 < 4, "V tiles in the ring: Shared::edge and odd_values tell four apart");
 constexpr int kMaxCtas = 160;    // CTAs of the attention kernel, at most (workspace slots)
-constexpr int kThreads = 384;    // two softmax warpgroups, one control warpgroup
-constexpr int kWarpKv = 8, kWarpMma = 9, kWarpQ = 10, kWarpFix = 11;
-// Registers per thread: at launch (65536 / 384, rounded down to 8), then after the
-// warpgroups trade: 256 * kRegsSoft + 128 * kRegsCtl == 384 * kRegsLaunch.
-constexpr int kRegsLaunch = 168;
-constexpr uint32_t kRegsSoft = 208, kRegsCtl = 88;
-static_assert(256 * kRegsSoft + 128 * kRegsCtl == kThreads * kRegsLaunch, "register trade must add up");
+constexpr int kThreads = 512;    // two softmax warpgroups, two control warpgroups
+constexpr int kWarpKv = 8, kWarpMma = 10, kWarpQ = 12;  // 8: K, 9: V; 10, 11: the MMAs of each query tile
+// Registers per thread: at launch (65536 / 512), then after the warpgroups trade:
+// 256 * kRegsSoft + 256 * kRegsCtl == 512 * kRegsLaunch.
+constexpr int kRegsLaunch = 128;
+constexpr uint32_t kRegsSoft = 192, kRegsCtl = 64;
+static_assert(256 * kRegsSoft + 256 * kRegsCtl == kThreads * kRegsLaunch, "register trade must add up");
 constexpr uint32_t kTmemCols = 512;  // S0 S1 (128 columns each), O0 O1 (128 each)
 constexpr float kLazy = 8.f;         // see above: rescale when the maximum grew by more than 2^8
 constexpr uint64_t kTimeoutNs = 1000000000ull;
@@ -260,7 +268,8 @@ struct Shared {
     uint64_t x_full, x_free;  // a single query tile's odd half is ready to be joined; is joined
     uint64_t edge[4];     // an edge tile of V has landed (by their number mod 4: the ring holds at most three);
                           // `full` then says that it is clean
-    uint64_t done;
+    uint64_t turn[2];     // the tensor cores are free for a query tile's next products
+    uint64_t done[2];
     uint32_t tmem;
     int32_t abort;
     int32_t odd_values[4];  // 1 + the last piece (by its number mod 4) whose V had values that are not finite
@@ -305,14 +314,33 @@ __device__ __forceinline__ void drain(uint32_t bar, uint32_t parity)
         if (globaltimer() - t0 > kTimeoutNs) return;
 }
 
-// D[tmem] (+)= A[tmem, bf16] * B[smem], fp32 accumulate; one thread issues.
-__device__ __forceinline__ void mma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
-                                            uint32_t accumulate)
+// One thread of the warp (all of them call it).
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r != 0;
+}
+
+// D[tmem] (+)= A * B[smem], bf16 operands, fp32 accumulate; one thread issues.  A in shared
+// memory (with B's upper descriptor word) or in TMEM; descriptors as 32-bit halves.
+__device__ __forceinline__ void mma_ss(uint32_t d_tmem, uint32_t alo, uint32_t hi, uint32_t blo, uint32_t idesc,
+                                       uint32_t accumulate)
 {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\ttcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::
-            "r"(d_tmem),
-        "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\tmov.b64 a, {%1, %2};\n\tmov.b64 b, {%3, %2};\n\t"
+        "setp.ne.b32 p, %5, 0;\n\ttcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, p;\n\t}" ::"r"(d_tmem),
+        "r"(alo), "r"(hi), "r"(blo), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+__device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint32_t blo, uint32_t bhi, uint32_t idesc,
+                                       uint32_t accumulate)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\tmov.b64 b, {%2, %3};\n\t"
+        "setp.ne.b32 p, %5, 0;\n\ttcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "r"(blo), "r"(bhi), "r"(idesc), "r"(accumulate)
         : "memory");
 }
 
@@ -392,41 +420,42 @@ struct Piece {
     int32_t slot;          // workspace slot of a partial
 };
 
+// (AHEAD: with the next item's description on its way; the softmax warps, short
+// of registers and waiting for logits at that point anyway, read it when due.)
+template <bool AHEAD>
 struct Walk {
     const ChunkArgs &a;
-    int64_t left;
-    int32_t items, head, item, off, cta;
+    int32_t left, head, item, off;
     bool first;
     Item next;
     __device__ Walk(const ChunkArgs &args) : a(args)
     {
-        cta = blockIdx.x;
+        const int cta = blockIdx.x;
         const PlanHead h = *a.head;
-        items = h.items;
         left = 0;
         first = true;
         if (cta < h.ctas) {
             const int64_t units = h.tiles * a.hkv;
-            left = cut(units, h.ctas, cta + 1) - cut(units, h.ctas, cta);
+            left = (int32_t)(cut(units, h.ctas, cta + 1) - cut(units, h.ctas, cta));
             const Start s = a.start[cta];
             head = s.head, item = s.item, off = s.off;
-            next = a.items[item];
+            if (AHEAD) next = a.items[item];
         }
     }
     __device__ bool step(Piece &p)
     {
         if (left <= 0) return false;
-        p.it = next;
+        p.it = AHEAD ? next : a.items[item];
         p.head = head;
         p.j0 = off;
-        p.j1 = (int32_t)min((int64_t)p.it.nt, off + left);
+        p.j1 = min(p.it.nt, off + left);
         p.whole = off == 0 && p.j1 == p.it.nt;
-        p.slot = 2 * cta + (first ? 0 : 1);
+        p.slot = 2 * blockIdx.x + (first ? 0 : 1);
         first = false;
         left -= p.j1 - p.j0;
         off = 0;
-        if (++item == items) item = 0, ++head;
-        if (left > 0) next = a.items[item];
+        if (++item == a.head->items) item = 0, ++head;
+        if (AHEAD && left > 0) next = a.items[item];
         return true;
     }
 };
@@ -464,6 +493,114 @@ __device__ __forceinline__ uint32_t finite_pair(uint32_t w)
     return w;
 }
 
+// The MMAs of query tile X, issued by one thread: of this warp alone, as an issue takes
+// a thread about 40 clocks and the tensor cores 64, so that one thread for both tiles
+// would set the pace.  The warps of both tiles walk every K and V tile in ring order (one
+// that the query tile skips is handed back at once), so each sees every phase of every
+// stage.  With two query tiles they take turns: first one tile's weighted sum and next
+// logits, then the other's, so that one tile is multiplied while the other is
+// exponentiated.  Addresses are constants or 32-bit sums: beside two busy softmax warps
+// every instruction between two MMAs counts.
+template <int D, int X>
+__device__ __forceinline__ void mma_warp(uint32_t qbuf, uint32_t ring, Shared *sh, const ChunkArgs &a)
+{
+    using C = Cfg<D>;
+    if (elect_one()) {
+        constexpr uint32_t id_qk = idesc_bf16(kTile, kTile);
+        constexpr uint32_t id_pv = idesc_bf16(kTile, D) | (1u << 16);  // V: its dims are contiguous
+        constexpr uint32_t kTileDesc = C::kTileBytes >> 4, kHalfDesc = C::kHalfBytes >> 4;
+        constexpr uint32_t ts = X * kTile, to = 256 + X * 128;         // S (and P over it), O in TMEM
+        const uint64_t qd = sdesc_sw128(qbuf), kd = sdesc_sw128(ring), vd = sdesc_sw128_mn(ring, C::kHalfBytes);
+        const uint32_t full0 = smem_u32(&sh->full[0]), empty0 = smem_u32(&sh->empty[0]);
+        const uint32_t sf = smem_u32(&sh->s_full[X]), pf = smem_u32(&sh->p_full[X]);
+        const uint32_t mine = smem_u32(&sh->turn[X]), other = smem_u32(&sh->turn[1 - X]);
+        Walk<true> w(a);
+        Piece p;
+        uint32_t ks = 0, kp = 0, vs = 1, vp = 0;  // next K and V tile: stage, phase
+        uint32_t pp = 0, turn = 1 - X, iq = 0;    // phases of the next weights, turn, query tiles
+        bool ok = true;
+        auto next = [](uint32_t &st, uint32_t &ph) {  // a tile further (K and V alternate)
+            st += 2;
+            if (st >= kStages) st -= kStages, ph ^= 1;
+        };
+        auto skip = [&](uint32_t &st, uint32_t &ph) {
+            ok = ok && cwait(full0 + st * 8, ph, sh, a);
+            mbar_arrive(empty0 + st * 8);
+            next(st, ph);
+        };
+        while (ok && w.step(p)) {
+            const bool two = p.it.ntok > a.TQ;
+            const int n = p.j1 - p.j0, cnt = part_of(p, X, a.TQ).cnt;
+            const int by = two ? 1 : 2, first = two ? 0 : X, last = first + (cnt - 1) * by;
+            const uint32_t ql = (uint32_t)qd + (two && X ? kTileDesc : 0);
+            ok = cwait(smem_u32(&sh->q_full), iq & 1, sh, a);
+            iq ^= 1;
+            if (ok && cnt == 0) mbar_arrive(smem_u32(&sh->q_empty));
+            for (int t = first - by; ok && t < n; t += by) {
+                // weighted sum of tile t, then logits of tile t + by (a single query tile: its own
+                // tiles, between the other warp's)
+                const bool sum = t >= first && t <= last, logits = t + by <= last;
+                if (!two && X == 1 && t >= 0) skip(vs, vp);
+                if (t >= first && t < n) {
+                    ok = ok && cwait(full0 + vs * 8, vp, sh, a);
+                    if (two && ok && t + 1 < n) ok = cwait(full0 + ks * 8, kp, sh, a);
+                    if (two && ok) ok = cwait(mine, turn, sh, a);
+                    if (ok && sum) ok = cwait(pf, pp, sh, a);
+                    if (!ok) break;
+                    if (sum) {
+                        pp ^= 1;
+                        tc_fence_after();
+                        const uint32_t lo = (uint32_t)vd + vs * kTileDesc;
+#pragma unroll
+                        for (int e = 0; e < kTile / 16; ++e)
+                            mma_ts(to, ts + e * 8, lo + e * 128, (uint32_t)(vd >> 32), id_pv, e > 0 || t != first);
+                        if (!two) mma_commit(empty0 + vs * 8);
+                        if (t == last) mma_commit(smem_u32(&sh->o_full[X]));
+                    } else {
+                        mbar_arrive(empty0 + vs * 8);
+                    }
+                }
+                const uint32_t v_done = empty0 + vs * 8;
+                if (t >= first && t < n) next(vs, vp);
+                if (!two && X == 0 && t >= 0 && t + 1 < n) skip(vs, vp);
+                if (!two && X == 1 && t + 1 < n) skip(ks, kp);
+                if (t + by < n) {
+                    if (!two || t < first) ok = ok && cwait(full0 + ks * 8, kp, sh, a);
+                    if (!ok) break;
+                    if (logits) {
+                        const uint32_t lo = (uint32_t)kd + ks * kTileDesc;
+#pragma unroll
+                        for (int e = 0; e < D / 16; ++e)
+                            mma_ss(ts, ql + ((e >> 2) * kHalfDesc + (e & 3) * 2), (uint32_t)(qd >> 32),
+                                   lo + ((e >> 2) * kHalfDesc + (e & 3) * 2), id_qk, e > 0);
+                    }
+                }
+                if (two && t >= first) {
+                    turn ^= 1;
+                    mbar_arrive(other);
+                }
+                if (t + by < n) {
+                    if (logits) {
+                        mma_commit(sf);
+                        mma_commit(empty0 + ks * 8);
+                        if (t + by == last) mma_commit(smem_u32(&sh->q_empty));
+                    } else {
+                        mbar_arrive(empty0 + ks * 8);
+                    }
+                    next(ks, kp);
+                }
+                if (two && sum) mma_commit(v_done);
+                if (!two && X == 0 && t + by + 1 < n) skip(ks, kp);
+            }
+            if (!two && X == 1 && ok && n % 2) skip(vs, vp);
+        }
+        // the tensor cores are idle before TMEM and shared memory go
+        mma_commit(smem_u32(&sh->done[X]));
+        drain(smem_u32(&sh->done[X]), 0);
+    }
+    __syncwarp();
+}
+
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
     chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
@@ -479,10 +616,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (tid == 0) {
         for (int i = 0; i < kStages; ++i) {
             mbar_init(smem_u32(&sh->full[i]), 1);
-            mbar_init(smem_u32(&sh->empty[i]), 1);
+            mbar_init(smem_u32(&sh->empty[i]), 2);
         }
         mbar_init(smem_u32(&sh->q_full), 1);
-        mbar_init(smem_u32(&sh->q_empty), 1);
+        mbar_init(smem_u32(&sh->q_empty), 2);
         for (int x = 0; x < 2; ++x) {
             mbar_init(smem_u32(&sh->s_full[x]), 1);
             mbar_init(smem_u32(&sh->p_full[x]), 4);
@@ -491,7 +628,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init(smem_u32(&sh->x_full), 4);
         mbar_init(smem_u32(&sh->x_free), 4);
         for (int i = 0; i < 4; ++i) mbar_init(smem_u32(&sh->edge[i]), 1);
-        mbar_init(smem_u32(&sh->done), 1);
+        for (int x = 0; x < 2; ++x) {
+            mbar_init(smem_u32(&sh->turn[x]), 1);
+            mbar_init(smem_u32(&sh->done[x]), 1);
+        }
         sh->abort = 0;
         for (int i = 0; i < 4; ++i) sh->odd_values[i] = 0;
         fence_mbarrier_init();
@@ -510,17 +650,21 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = sh->tmem;
+    constexpr uint32_t tmem = 0;  // every column is this CTA's: the allocation starts at 0
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
 
     if (warp >= 8) {
         reg_dealloc<kRegsCtl>();
-        if (warp == kWarpKv) {
-            // ---------------- K and V tiles: 8 blocks x (D/64) halves per tile, a lane per copy
-            Walk w(a);
+        if (warp == kWarpKv || warp == kWarpKv + 1) {
+            // ---------------- K tiles (warp 8) and V tiles (warp 9): a tile is 8 blocks x (D/64)
+            // halves, a lane per copy.  Issuing a 2 KB copy takes about 90 clocks, so one warp for
+            // both would take 2900 clocks for what two query tiles multiply in 2048.
+            const int kv = warp - kWarpKv;
+            const CUtensorMap *map = kv ? &vmap : &kmap;
+            Walk<true> w(a);
             Piece p;
-            uint32_t k = 0;  // tiles issued
+            uint32_t st = kv, ph = 1, k = 0;  // stage and the phase that frees it; tiles issued
             uint32_t ne = 0, were_edges = 0;  // edge tiles issued; which of the last tiles were (bit 0: the last)
             const int b = lane % kBlkPerTile, h = lane / kBlkPerTile;
             const bool mine = h < C::kHalves;
@@ -541,40 +685,48 @@ __global__ void __launch_bounds__(kThreads, 1)
                     return id;
                 };
                 int32_t id = block_id(p.j0);
-                for (int j = p.j0; ok && j < p.j1; ++j) {
+                for (int j = p.j0; j < p.j1; ++j) {
                     const int32_t cur = id;
                     if (j + 1 < p.j1) id = block_id(j + 1);
-#pragma unroll
-                    for (int kv = 0; kv < 2; ++kv) {
-                        const int st = k % kStages;
-                        ok = cwait(smem_u32(&sh->empty[st]), ((k / kStages) & 1) ^ 1, sh, a);
-                        ok = __all_sync(0xffffffffu, ok);
-                        if (!ok) break;
-                        const bool edge = kv && edge_tile(p.it, j);
-                        const uint32_t fb = smem_u32(edge ? &sh->edge[ne & 3] : &sh->full[st]);
-                        ne += edge;
-                        were_edges = were_edges << 1 | (edge ? 1u : 0u);
-                        if (lane == 0) mbar_arrive_expect_tx(fb, C::kTileBytes);
-                        __syncwarp();
-                        if (mine)
-                            tma_load_5d(smem_u32(ring + st * C::kTileBytes + h * C::kHalfBytes + b * kBlk * 128),
-                                        kv ? &vmap : &kmap, fb, h * 64, 0, p.head, cur, a.layer);
-                        ++k;
-                    }
+                    ok = __all_sync(0xffffffffu, cwait(smem_u32(&sh->empty[st]), ph, sh, a));
+                    if (!ok) break;
+                    const bool edge = kv && edge_tile(p.it, j);
+                    const uint32_t fb = smem_u32(edge ? &sh->edge[ne & 3] : &sh->full[st]);
+                    ne += edge;
+                    were_edges = were_edges << 1 | (edge ? 1u : 0u);
+                    if (lane == 0) mbar_arrive_expect_tx(fb, C::kTileBytes);
+                    __syncwarp();
+                    if (mine)
+                        tma_load_5d(smem_u32(ring + st * C::kTileBytes + h * C::kHalfBytes + b * kBlk * 128), map, fb,
+                                    h * 64, 0, p.head, cur, a.layer);
+                    ++k;
+                    st += 2;
+                    if (st >= kStages) st -= kStages, ph ^= 1;
                 }
             }
-            // every copy has landed before the CTA's shared memory is released
-            for (uint32_t i = k > kStages ? k - kStages : 0; i < k; ++i)
-                if (!(were_edges >> (k - 1 - i) & 1u)) drain(smem_u32(&sh->full[i % kStages]), (i / kStages) & 1);
+            // every copy has landed before the CTA's shared memory is released: the ring's last
+            // entries (this warp's tile i is entry 2 i + kv; earlier ones were consumed), and the
+            // edge tiles
+            for (uint32_t i = k > kStages / 2 ? k - kStages / 2 - 1 : 0; i < k; ++i) {
+                const uint32_t e = 2 * i + kv;
+                if (e + kStages >= 2 * k && !(were_edges >> (k - 1 - i) & 1u))
+                    drain(smem_u32(&sh->full[e % kStages]), (e / kStages) & 1);
+            }
             for (uint32_t i = ne > 3 ? ne - 3 : 0; i < ne; ++i) drain(smem_u32(&sh->edge[i & 3]), (i >> 2) & 1);
+        } else if (warp == kWarpMma) {
+            mma_warp<D, 0>(smem_u32(qbuf), smem_u32(ring), sh, a);
+        } else if (warp == kWarpMma + 1) {
+            mma_warp<D, 1>(smem_u32(qbuf), smem_u32(ring), sh, a);
         } else if (warp == kWarpQ) {
-            // ---------------- query tiles
-            if (lane == 0) {
-                Walk w(a);
-                Piece p;
-                uint32_t i = 0;
-                while (!a.stall && w.step(p)) {
-                    if (!cwait(smem_u32(&sh->q_empty), (i & 1) ^ 1, sh, a)) break;
+            // ---------------- query tiles, and the edge tiles of V
+            Walk<true> w(a);
+            Piece p;
+            uint32_t k0 = 0, np = 0, ne = 0;
+            bool ok = true;
+            for (; ok && !a.stall && w.step(p); ++np) {
+                ok = __all_sync(0xffffffffu, cwait(smem_u32(&sh->q_empty), (np & 1) ^ 1, sh, a));
+                if (!ok) break;
+                if (lane == 0) {
                     const int tiles = p.it.ntok > a.TQ ? 2 : 1;
                     const uint32_t fb = smem_u32(&sh->q_full);
                     mbar_arrive_expect_tx(fb, tiles * C::kHalves * qrows * 128);
@@ -588,99 +740,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 "l"(reinterpret_cast<uint64_t>(&qmap)), "r"(h * 64), "r"(p.head * a.G),
                                 "r"(p.it.row0 + x * a.TQ), "r"(fb)
                                 : "memory");
-                    ++i;
                 }
-                if (i > 0) drain(smem_u32(&sh->q_full), (i - 1) & 1);
-            }
-            __syncwarp();
-        } else if (warp == kWarpMma) {
-            // ---------------- MMAs
-            constexpr uint32_t id_qk = idesc_bf16(kTile, kTile);
-            constexpr uint32_t id_pv = idesc_bf16(kTile, D) | (1u << 16);  // V: its dims are contiguous
-            Walk w(a);
-            Piece p;
-            uint32_t k0 = 0;             // ring index of the piece's first K tile
-            uint32_t np[2] = {0, 0};     // weights waited for
-            uint32_t iq = 0;
-            bool ok = true;
-            auto wait_tile = [&](uint32_t k) {
-                ok = ok && cwait(smem_u32(&sh->full[k % kStages]), (k / kStages) & 1, sh, a);
-                ok = __all_sync(0xffffffffu, ok);
-            };
-            auto release = [&](uint32_t k) { mma_commit(smem_u32(&sh->empty[k % kStages])); };
-            while (ok && w.step(p)) {
-                const bool two = p.it.ntok > a.TQ;
-                const Part pt[2] = {part_of(p, 0, a.TQ), part_of(p, 1, a.TQ)};
-                ok = __all_sync(0xffffffffu, cwait(smem_u32(&sh->q_full), iq & 1, sh, a));
-                ++iq;
-                auto qk = [&](int x, int i) {  // logits of query tile x on its i-th key tile
-                    const uint32_t k = k0 + 2 * (pt[x].j + i * pt[x].by - p.j0);
-                    wait_tile(k);
-                    if (!ok) return;
-                    if (lane == 0) {
-                        const uint32_t qa = smem_u32(qbuf + (two ? x : 0) * C::kTileBytes);
-                        const uint32_t ka = smem_u32(ring + (k % kStages) * C::kTileBytes);
-#pragma unroll
-                        for (int ks = 0; ks < D / 16; ++ks) {
-                            const uint32_t o = (ks >> 2) * C::kHalfBytes + (ks & 3) * 32;
-                            mma_bf16(tmem + x * kTile, sdesc_sw128(qa + o), sdesc_sw128(ka + o), id_qk, ks > 0);
-                        }
-                        mma_commit(smem_u32(&sh->s_full[x]));
-                        // a key tile that both query tiles take is tile 1's to release
-                        if (!two || x == 1) release(k);
-                    }
-                    __syncwarp();
-                };
-                auto pv = [&](int x, int i) {
-                    const int j = pt[x].j + i * pt[x].by;
-                    const uint32_t k = k0 + 2 * (j - p.j0) + 1;
-                    wait_tile(k);
-                    ok = ok && cwait(smem_u32(&sh->p_full[x]), np[x] & 1, sh, a);
-                    ok = __all_sync(0xffffffffu, ok);
-                    if (!ok) return;
-                    ++np[x];
-                    const uint32_t va = smem_u32(ring + (k % kStages) * C::kTileBytes);
-                    if (lane == 0) {
-                        tc_fence_after();
-#pragma unroll
-                        for (int ks = 0; ks < kTile / 16; ++ks)
-                            mma_bf16_ts(tmem + 256 + x * 128, tmem + x * kTile + ks * 8,
-                                        sdesc_sw128_mn(va + ks * 2048, C::kHalfBytes), id_pv, i > 0 || ks > 0);
-                        if (!two || x == 1) release(k);
-                        if (i + 1 == pt[x].cnt) mma_commit(smem_u32(&sh->o_full[x]));
-                    }
-                    __syncwarp();
-                };
-                for (int x = 0; ok && x < 2; ++x)
-                    if (pt[x].cnt > 0) qk(x, 0);
-                bool q_held = true;
-                const int cnt = max(pt[0].cnt, pt[1].cnt);
-                for (int i = 0; ok && i < cnt; ++i) {
-#pragma unroll
-                    for (int x = 0; x < 2; ++x) {
-                        if (ok && i < pt[x].cnt) pv(x, i);
-                        if (ok && i + 1 < pt[x].cnt) qk(x, i + 1);
-                    }
-                    if (ok && q_held && i + 2 >= cnt) {  // every logit product of the piece is issued
-                        if (lane == 0) mma_commit(smem_u32(&sh->q_empty));
-                        q_held = false;
-                    }
-                }
-                k0 += 2 * (p.j1 - p.j0);
-            }
-            // the tensor cores are idle before TMEM and shared memory go
-            if (lane == 0) {
-                mma_commit(smem_u32(&sh->done));
-                drain(smem_u32(&sh->done), 0);
-            }
-            __syncwarp();
-        } else if (warp == kWarpFix) {
-            // ---------------- edge tiles of V
-            Walk w(a);
-            Piece p;
-            uint32_t k0 = 0, np = 0, ne = 0;
-            bool ok = true;
-            for (; ok && w.step(p); ++np) {
+                __syncwarp();
                 for (int j = max(p.j0, (p.it.pos0 + 1) / kTile); ok && j < p.j1; ++j) {
                     if (!edge_tile(p.it, j)) continue;
                     const uint32_t k = k0 + 2 * (j - p.j0) + 1;
@@ -715,6 +776,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 k0 += 2 * (p.j1 - p.j0);
             }
+            // the last query tiles have landed too
+            if (np > 0) drain(smem_u32(&sh->q_full), (np - 1) & 1);
         }
     } else {
         // ---------------- softmax: thread = one row of query tile x
@@ -723,7 +786,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int tok = r / a.G, hd = r - tok * a.G;
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t ts = tmem + lanes + x * kTile, to = tmem + lanes + 256 + x * 128;
-        Walk w(a);
+        Walk<false> w(a);
         Piece p;
         uint32_t ns = 0, no = 0, nj = 0, np = 0;
         bool ok = true;
@@ -770,7 +833,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             const float f = grew ? ex2(m - mt) : 1.f;
                             if (grew) m = mt;
                             z *= f;
-#pragma unroll
+#pragma unroll 1
                             for (int c = 0; c < D; c += 32) {
                                 uint32_t o[32];
                                 tmem_ld32(to + c, o, 0);
@@ -902,7 +965,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == kWarpMma) tmem_dealloc(tmem, kTmemCols);
+    if (warp == kWarpMma) tmem_dealloc(sh->tmem, kTmemCols);
 }
 
 // ---- merge ----------------------------------------------------------------------
