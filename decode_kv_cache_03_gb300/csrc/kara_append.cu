@@ -12,14 +12,20 @@
 // Nothing is reused but the table row, so the floor is one read of q, k, v and
 // one write of them: HBM for long chunks, launch latency for a decode step.  D/8
 // lanes hold a row, 16 bytes each, so a warp takes 32 / (D/8) rows at once; a
-// row's sum of squares is a butterfly over its lanes, and the two halves of a
-// rotated pair meet in a shuffle.
+// row's sum of squares is a butterfly over its lanes.  Two kernels: for short
+// calls a warp per pass, everything in registers; for long ones tokens staged
+// through shared memory by bulk copies, because what bounds a long call is the
+// latency of its chain of loads (slot, offset, table row, rows): in registers it
+// reached 4.0 TB/s with four passes a warp (8192 tokens, 40/8 heads of 128, with
+// the ring: 70 us), staged 5.4 TB/s (52 us).
 #include "kara_common.cuh"
+#include "kara_sm100.cuh"
 
 namespace kara {
 namespace {
 
 constexpr int kAppThreads = 256;
+constexpr int kBs = 16;  // tokens per cache block (the supported block size)
 
 struct AppArgs {
     const uint16_t *q, *k, *v;
@@ -34,7 +40,9 @@ struct AppArgs {
     const int32_t *seq, *pos, *len;
     int32_t *err;
     float eps;
-    int32_t n, rows, num_blocks, bs, hq, hkv, W, n_pos, rot, inter, parts;
+    int32_t stall;     // debug: the staged kernel issues no copies (see debug_stall)
+    uint64_t wait_ns;  // limit of its waits
+    int32_t n, rows, num_blocks, hq, hkv, W, n_pos, rot, inter;
 };
 
 __device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
@@ -54,129 +62,395 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi)
     return r;
 }
 
-// A warp takes PASSES groups of 32 / (D/8) rows of one token.
-template <int D, int PASSES>
+__device__ __forceinline__ float4 ldg4(const float *p) { return __ldg(reinterpret_cast<const float4 *>(p)); }
+
+// A warp takes 32 / (D/8) rows of one token: token blockIdx.x * 8 + warp, rows of part blockIdx.y.
+template <int D>
 __global__ void __launch_bounds__(kAppThreads) append_kernel(const AppArgs a)
 {
     constexpr int LPR = D / 8;     // lanes per row
     constexpr int RPP = 32 / LPR;  // rows per pass
-    const int64_t unit = ((int64_t)blockIdx.x * kAppThreads + threadIdx.x) >> 5;
-    const int64_t t = unit / a.parts;
+    const int64_t t = (int64_t)blockIdx.x * (kAppThreads / 32) + (threadIdx.x >> 5);
     if (t >= a.rows) return;
-    const int part = (int)(unit % a.parts);
-    const int lane = threadIdx.x & 31, l = lane % LPR;
+    const int lane = threadIdx.x & 31, l = lane % LPR, d0 = l * 8;
+    const int h = blockIdx.y * RPP + lane / LPR;
+    const int nrow = a.hq + 2 * a.hkv;
 
+    const bool is_v = h >= a.hq + a.hkv, is_q = h < a.hq;
+
+    // the row is on its way before the token's place is known (padding rows are read, not written)
     const int64_t slot = a.slot[t];
-    if (slot == -1) return;  // padding
     const int32_t s = a.seq[t], x = a.pos[t];
+    uint4 u = make_uint4(0, 0, 0, 0);
+    if (h < nrow) {
+        const uint16_t *src = is_q ? a.q + t * a.qs + h * D
+                              : is_v ? a.v + t * a.vs + (h - a.hq - a.hkv) * D
+                                     : a.k + t * a.ks + (h - a.hq) * D;
+        u = *reinterpret_cast<const uint4 *>(src + d0);
+    }
+    if (slot == -1) return;  // padding
     const bool known = s >= 0 && s < a.n;
     // without a rotation every rotary position will do
     const int64_t r = a.rot == 0 ? 0 : (int64_t)x + (known && a.shift ? a.shift[s] : 0);
-    if (slot < 0 || slot >= (int64_t)a.num_blocks * a.bs) {
-        if (part == 0 && lane == 0) set_err(a.err, KARA_EBADBLOCK);
-        return;
-    }
-    if (!known || x < 0 || r < 0 || r >= a.n_pos) {
-        if (part == 0 && lane == 0) set_err(a.err, KARA_EINVAL);
+    if (slot < 0 || slot >= (int64_t)a.num_blocks * kBs || !known || x < 0 || r < 0 || r >= a.n_pos) {
+        if (blockIdx.y == 0 && lane == 0)
+            set_err(a.err, slot < 0 || slot >= (int64_t)a.num_blocks * kBs ? KARA_EBADBLOCK : KARA_EINVAL);
         return;
     }
 
     // this lane's cosines and signed sines, one per value it holds
     float c[8], sn[8];
-    const int half = a.rot >> 1, d0 = l * 8;
+    const int half = a.rot >> 1;
     const bool turned = d0 < a.rot;
 #pragma unroll
     for (int e = 0; e < 8; ++e) c[e] = 1.f, sn[e] = 0.f;
     if (turned) {
         const float *row = a.cos_sin + r * a.rot;
         if (a.inter) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int j = d0 / 2 + e;
-                c[2 * e] = c[2 * e + 1] = row[j];
-                sn[2 * e + 1] = row[half + j];
-                sn[2 * e] = -sn[2 * e + 1];
-            }
+            const float4 cc = ldg4(row + d0 / 2), ss = ldg4(row + half + d0 / 2);
+            c[0] = c[1] = cc.x, c[2] = c[3] = cc.y, c[4] = c[5] = cc.z, c[6] = c[7] = cc.w;
+            sn[1] = ss.x, sn[3] = ss.y, sn[5] = ss.z, sn[7] = ss.w;
+            sn[0] = -ss.x, sn[2] = -ss.y, sn[4] = -ss.z, sn[6] = -ss.w;
         } else {
             const int j0 = d0 < half ? d0 : d0 - half;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                c[e] = row[j0 + e];
-                sn[e] = d0 < half ? -row[half + j0 + e] : row[half + j0 + e];
-            }
+            const float sg = d0 < half ? -1.f : 1.f;
+            const float4 c0 = ldg4(row + j0), c1 = ldg4(row + j0 + 4);
+            const float4 s0 = ldg4(row + half + j0), s1 = ldg4(row + half + j0 + 4);
+            c[0] = c0.x, c[1] = c0.y, c[2] = c0.z, c[3] = c0.w, c[4] = c1.x, c[5] = c1.y, c[6] = c1.z, c[7] = c1.w;
+            sn[0] = sg * s0.x, sn[1] = sg * s0.y, sn[2] = sg * s0.z, sn[3] = sg * s0.w;
+            sn[4] = sg * s1.x, sn[5] = sg * s1.y, sn[6] = sg * s1.z, sn[7] = sg * s1.w;
         }
     }
     // lane that holds the other half of this lane's pairs
     const int other = !turned || a.inter ? lane : d0 < half ? lane + half / 8 : lane - half / 8;
-
-    const int nrow = a.hq + 2 * a.hkv;
-    uint4 in[PASSES];
-#pragma unroll
-    for (int p = 0; p < PASSES; ++p) {
-        const int h = (part * PASSES + p) * RPP + lane / LPR;
-        if (h >= nrow) continue;
-        const uint16_t *src = h < a.hq            ? a.q + t * a.qs + h * D
-                              : h < a.hq + a.hkv ? a.k + t * a.ks + (h - a.hq) * D
-                                                 : a.v + t * a.vs + (h - a.hq - a.hkv) * D;
-        in[p] = *reinterpret_cast<const uint4 *>(src + d0);
+    const int64_t page = (slot / kBs) * a.block_stride + (slot % kBs) * D + d0;
+    uint16_t *ring = nullptr;  // this token's row of the ring, if it is of the last W
+    if (a.ring) {
+        const int32_t L = a.len[s];
+        if (x < L && x >= (int64_t)L - a.W) ring = a.ring + s * a.ring_seq + (int64_t)(x % a.W) * D + d0;
     }
-    const int64_t page = (slot / a.bs) * a.block_stride + (slot % a.bs) * D + d0;
-#pragma unroll
-    for (int p = 0; p < PASSES; ++p) {
-        const int h = (part * PASSES + p) * RPP + lane / LPR;
-        const bool is_v = h >= a.hq + a.hkv, is_q = h < a.hq;
-        uint4 out = in[p];
+    // (a warp whose rows are all values has nothing to compute)
+    if (__any_sync(0xffffffffu, !is_v)) {
         float y[8];
-        unpack8(in[p], y);
+        unpack8(u, y);
         const uint16_t *wp = is_q ? a.qw : a.kw;
-        float ss = 0.f;
+        if (a.qw || a.kw) {
+            float ss = 0.f;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) ss = fmaf(y[e], y[e], ss);
+            for (int e = 0; e < 8; ++e) ss = fmaf(y[e], y[e], ss);
 #pragma unroll
-        for (int o = LPR / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-        if (wp) {
-            float w[8];
-            unpack8(__ldg(reinterpret_cast<const uint4 *>(wp + d0)), w);
-            const float inv = 1.f / sqrtf(ss * (1.f / D) + a.eps);
+            for (int o = LPR / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+            if (wp) {
+                float w[8];
+                unpack8(__ldg(reinterpret_cast<const uint4 *>(wp + d0)), w);
+                const float inv = rsqrtf(ss * (1.f / D) + a.eps);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) y[e] = y[e] * inv * w[e];
+                for (int e = 0; e < 8; ++e) y[e] = y[e] * inv * w[e];
+            }
         }
         float z[8];
+        if (a.inter) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const float far = __shfl_sync(0xffffffffu, y[e], other);
-            z[e] = fmaf(y[e], c[e], (a.inter ? y[e ^ 1] : far) * sn[e]);
-        }
-        if (h >= nrow) continue;
-        if (!is_v) {
-            out.x = pack_bf16(z[0], z[1]), out.y = pack_bf16(z[2], z[3]);
-            out.z = pack_bf16(z[4], z[5]), out.w = pack_bf16(z[6], z[7]);
-        }
-        if (is_q) {
-            *reinterpret_cast<uint4 *>(a.q_out + (t * a.hq + h) * D + d0) = out;
-            if (a.ring) {
-                const int32_t L = a.len[s];
-                if (x < L && x >= (int64_t)L - a.W)
-                    *reinterpret_cast<uint4 *>(a.ring + s * a.ring_seq + h * a.ring_head + (int64_t)(x % a.W) * D +
-                                               d0) = out;
-            }
+            for (int e = 0; e < 8; ++e) z[e] = fmaf(y[e], c[e], y[e ^ 1] * sn[e]);
         } else {
-            uint16_t *pool = is_v ? a.vp : a.kp;
-            const int g = is_v ? h - a.hq - a.hkv : h - a.hq;
-            *reinterpret_cast<uint4 *>(pool + page + g * a.head_stride) = out;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) z[e] = fmaf(y[e], c[e], __shfl_sync(0xffffffffu, y[e], other) * sn[e]);
+        }
+        if (!is_v) {
+            u.x = pack_bf16(z[0], z[1]), u.y = pack_bf16(z[2], z[3]);
+            u.z = pack_bf16(z[4], z[5]), u.w = pack_bf16(z[6], z[7]);
+        }
+    }
+    if (h >= nrow) return;
+    if (is_q) {
+        *reinterpret_cast<uint4 *>(a.q_out + (t * a.hq + h) * D + d0) = u;
+        if (ring) *reinterpret_cast<uint4 *>(ring + h * a.ring_head) = u;
+    } else {
+        uint16_t *pool = is_v ? a.vp : a.kp;
+        const int g = is_v ? h - a.hq - a.hkv : h - a.hq;
+        *reinterpret_cast<uint4 *>(pool + page + g * a.head_stride) = u;
+    }
+}
+
+// ---- long calls: tokens staged through shared memory ------------------------------
+// One warp per CTA brings in tokens by bulk copies (a token's q, k and v rows and its
+// row of the rotation table, four copies), as many tokens ahead as the stages hold; four
+// warps take a token's rows from shared memory (eight: 5 % slower, two: 15 %).  The chain
+// slot, sequence -> offset -> table row is looked up for 32 tokens at once.
+constexpr int kTokWarps = 4;
+constexpr int kTokThreads = 32 * (1 + kTokWarps);
+constexpr int kTokMaxStages = 8;
+// Calls of up to this many head rows (tokens times heads) take the other kernel: all their
+// loads are in flight at once and there is no pipeline to fill.  Measured with 56 heads of 128
+// (staged / a warp per two rows, us): 128 tokens 4.7 / 2.9, 256 5.3 / 4.5, 384 5.8 / 5.9,
+// 1024 9.8 / 12.0, 2048 14.9 / 22.0.
+constexpr int kSmallRows = 20480;
+constexpr uint64_t kTokTimeoutNs = 1000000000ull;
+
+struct TokMeta {
+    int64_t page;    // offset of the token's row in a pool (of KV head 0); -1: no more tokens
+    int64_t ring;    // offset of its row in the ring (of head 0), -1: none
+    int32_t row;     // row of q, k, v
+    int32_t pad[3];
+};
+
+struct TokShared {
+    uint64_t full[kTokMaxStages], empty[kTokMaxStages];
+    TokMeta meta[kTokMaxStages];
+    int32_t abort;
+};
+
+// Bounded wait on phase `parity` of `bar`: gives up after limit_ns, or once another
+// warp of the CTA gave up, recording KARA_ETIMEOUT.
+__device__ __forceinline__ bool twait(uint32_t bar, uint32_t parity, TokShared *sh, const AppArgs &a)
+{
+    uint64_t t0 = 0;
+    for (uint32_t it = 0;; ++it) {
+        if (ptx::mbar_try_wait(bar, parity)) return true;
+        if ((it & 63u) == 63u) {
+            if (*(volatile int32_t *)&sh->abort) return false;
+            const uint64_t now = ptx::globaltimer();
+            if (t0 == 0) {
+                t0 = now;
+            } else if (now - t0 > a.wait_ns) {
+                set_err(a.err, KARA_ETIMEOUT);
+                *(volatile int32_t *)&sh->abort = 1;
+                return false;
+            }
         }
     }
 }
 
-template <int D, int PASSES>
-cudaError_t launch(AppArgs a, cudaStream_t st)
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar)
 {
-    constexpr int RPP = 32 / (D / 8);
-    a.parts = (a.hq + 2 * a.hkv + RPP * PASSES - 1) / (RPP * PASSES);
-    const int64_t warps = (int64_t)a.rows * a.parts;
-    const int64_t grid = (warps * 32 + kAppThreads - 1) / kAppThreads;
-    if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-    append_kernel<D, PASSES><<<(unsigned)grid, kAppThreads, 0, st>>>(a);
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+                 "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(bar)
+                 : "memory");
+}
+
+__host__ __device__ __forceinline__ int tok_stage_bytes(int hq, int hkv, int D, int rot)
+{
+    return (hq + 2 * hkv) * D * 2 + rot * 4;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kTokThreads, 4) append_staged_kernel(const AppArgs a, int stages)
+{
+    constexpr int LPR = D / 8, RPP = 32 / LPR;
+    extern __shared__ __align__(128) uint8_t tsm[];
+    TokShared *sh = reinterpret_cast<TokShared *>(tsm);
+    uint8_t *buf = tsm + (sizeof(TokShared) + 127) / 128 * 128;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int nrow = a.hq + 2 * a.hkv, half = a.rot >> 1;
+    const int row_bytes = nrow * D * 2, stage_bytes = row_bytes + a.rot * 4;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < stages; ++i) {
+            ptx::mbar_init(ptx::smem_u32(&sh->full[i]), 1);
+            ptx::mbar_init(ptx::smem_u32(&sh->empty[i]), kTokWarps);
+        }
+        sh->abort = 0;
+        ptx::fence_mbarrier_init();
+    }
+    __syncthreads();
+
+    if (warp == kTokWarps) {
+        uint32_t st = 0, ph = 1, issued = 0;
+        bool ok = !a.stall;
+        for (int64_t base = blockIdx.x; ok && base < a.rows; base += 32ll * gridDim.x) {
+            // this lane's token
+            const int64_t t = base + (int64_t)lane * gridDim.x;
+            int64_t page = -1, ring = -1, r = 0;
+            if (t < a.rows) {
+                const int64_t slot = a.slot[t];
+                const int32_t s = a.seq[t], x = a.pos[t];
+                const bool known = s >= 0 && s < a.n, inside = slot >= 0 && slot < (int64_t)a.num_blocks * kBs;
+                r = a.rot == 0 ? 0 : (int64_t)x + (known && a.shift ? a.shift[s] : 0);
+                if (slot != -1) {
+                    if (!inside || !known || x < 0 || r < 0 || r >= a.n_pos) {
+                        set_err(a.err, inside ? KARA_EINVAL : KARA_EBADBLOCK);
+                    } else {
+                        page = (slot / kBs) * a.block_stride + (slot % kBs) * D;
+                        if (a.ring) {
+                            const int32_t L = a.len[s];
+                            if (x < L && x >= (int64_t)L - a.W) ring = s * a.ring_seq + (int64_t)(x % a.W) * D;
+                        }
+                    }
+                }
+            }
+            for (unsigned todo = __ballot_sync(0xffffffffu, page >= 0); ok && todo; todo &= todo - 1) {
+                const int src = __ffs(todo) - 1;
+                ok = twait(ptx::smem_u32(&sh->empty[st]), ph, sh, a);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                if (lane == src) {
+                    const uint32_t fb = ptx::smem_u32(&sh->full[st]);
+                    const uint32_t d = ptx::smem_u32(buf + st * stage_bytes);
+                    TokMeta &m = sh->meta[st];
+                    m.page = page, m.ring = ring, m.row = (int32_t)t;
+                    ptx::mbar_arrive_expect_tx(fb, (uint32_t)stage_bytes);
+                    bulk_load(d, a.q + t * a.qs, a.hq * D * 2, fb);
+                    bulk_load(d + a.hq * D * 2, a.k + t * a.ks, a.hkv * D * 2, fb);
+                    bulk_load(d + (a.hq + a.hkv) * D * 2, a.v + t * a.vs, a.hkv * D * 2, fb);
+                    if (a.rot) bulk_load(d + row_bytes, a.cos_sin + r * a.rot, a.rot * 4, fb);
+                }
+                __syncwarp();
+                ++issued;
+                if (++st == (uint32_t)stages) st = 0, ph ^= 1;
+            }
+        }
+        if (ok) ok = __all_sync(0xffffffffu, twait(ptx::smem_u32(&sh->empty[st]), ph, sh, a));
+        if (ok && lane == 0) {  // the end
+            sh->meta[st].page = -1;
+            ptx::mbar_arrive(ptx::smem_u32(&sh->full[st]));
+        }
+        // every copy has landed before the CTA's shared memory is released
+        for (uint32_t i = issued > (uint32_t)stages ? issued - stages : 0; !ok && i < issued; ++i) {
+            const uint64_t t0 = ptx::globaltimer();
+            while (!ptx::mbar_try_wait(ptx::smem_u32(&sh->full[i % stages]), (i / stages) & 1))
+                if (ptx::globaltimer() - t0 > kTokTimeoutNs) break;
+        }
+        return;
+    }
+
+    const int l = lane % LPR, d0 = l * 8, sub = lane / LPR;
+    const bool turned = d0 < a.rot, low = d0 < half;
+    // the other half of this lane's pairs: 16 bytes further on or back (interleaved: in the lane itself)
+    const int o0 = !turned || a.inter ? d0 : low ? d0 + half : d0 - half;
+    // weights of this lane's dims and of their partners (1 without a norm)
+    const uint4 one = make_uint4(0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u);
+    const uint4 wq = a.qw ? *reinterpret_cast<const uint4 *>(a.qw + d0) : one;
+    const uint4 wqo = a.qw ? *reinterpret_cast<const uint4 *>(a.qw + o0) : one;
+    const uint4 wk = a.kw ? *reinterpret_cast<const uint4 *>(a.kw + d0) : one;
+    const uint4 wko = a.kw ? *reinterpret_cast<const uint4 *>(a.kw + o0) : one;
+    uint32_t st = 0, ph = 0;
+    for (;;) {
+        bool ok = twait(ptx::smem_u32(&sh->full[st]), ph, sh, a);
+        if (!__all_sync(0xffffffffu, ok)) return;
+        const TokMeta m = sh->meta[st];
+        if (m.page < 0) return;
+        const uint16_t *rows = reinterpret_cast<const uint16_t *>(buf + st * stage_bytes);
+        const float *tab = reinterpret_cast<const float *>(buf + st * stage_bytes + row_bytes);
+        float c[8], sn[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) c[e] = 1.f, sn[e] = 0.f;
+        if (turned && a.inter) {
+            const float4 cc = *reinterpret_cast<const float4 *>(tab + d0 / 2);
+            const float4 ss = *reinterpret_cast<const float4 *>(tab + half + d0 / 2);
+            c[0] = c[1] = cc.x, c[2] = c[3] = cc.y, c[4] = c[5] = cc.z, c[6] = c[7] = cc.w;
+            sn[1] = ss.x, sn[3] = ss.y, sn[5] = ss.z, sn[7] = ss.w;
+            sn[0] = -ss.x, sn[2] = -ss.y, sn[4] = -ss.z, sn[6] = -ss.w;
+        } else if (turned) {
+            const int j0 = low ? d0 : d0 - half;
+            const float sg = low ? -1.f : 1.f;
+#pragma unroll
+            for (int e = 0; e < 8; e += 4) {
+                const float4 cc = *reinterpret_cast<const float4 *>(tab + j0 + e);
+                const float4 ss = *reinterpret_cast<const float4 *>(tab + half + j0 + e);
+                c[e] = cc.x, c[e + 1] = cc.y, c[e + 2] = cc.z, c[e + 3] = cc.w;
+                sn[e] = sg * ss.x, sn[e + 1] = sg * ss.y, sn[e + 2] = sg * ss.z, sn[e + 3] = sg * ss.w;
+            }
+        }
+        // a query row's factors: weight times cosine, and the partner's weight times sine
+        float qa[8], qb[8];
+        unpack8(wq, qa);
+        unpack8(wqo, qb);
+        if (a.inter) {
+#pragma unroll
+            for (int e = 0; e < 8; e += 2) qb[e] = qa[e + 1], qb[e + 1] = qa[e];
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) qa[e] *= c[e], qb[e] *= sn[e];
+        uint16_t *qrow = a.q_out + (int64_t)m.row * a.hq * D + d0;
+        for (int h = warp * RPP + sub; h - sub < nrow; h += kTokWarps * RPP) {
+            const bool in = h < nrow, is_q = h < a.hq, is_v = h >= a.hq + a.hkv;
+            uint4 u = make_uint4(0, 0, 0, 0), uo = u;
+            if (in) {
+                u = *reinterpret_cast<const uint4 *>(rows + h * D + d0);
+                uo = *reinterpret_cast<const uint4 *>(rows + h * D + o0);
+            }
+            if (__any_sync(0xffffffffu, in && !is_v)) {
+                // z = (x w c + x' w' s) / sqrt(mean(x^2) + eps), x' and w' of the pair's other member
+                float x[8], xo[8];
+                unpack8(u, x);
+                unpack8(uo, xo);
+                float inv = 1.f;
+                if (a.qw || a.kw) {
+                    float ss = 0.f;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], ss);
+#pragma unroll
+                    for (int o = LPR / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+                    if (is_q ? a.qw : a.kw) inv = rsqrtf(ss * (1.f / D) + a.eps);
+                }
+                float z[8];
+                if (a.inter) {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) xo[e] = x[e ^ 1];
+                }
+                if (__all_sync(0xffffffffu, is_q)) {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) z[e] = fmaf(x[e], qa[e], xo[e] * qb[e]) * inv;
+                } else {
+                    float w[8], wo[8];
+                    unpack8(is_q ? wq : wk, w);
+                    unpack8(is_q ? wqo : wko, wo);
+                    if (a.inter) {
+#pragma unroll
+                        for (int e = 0; e < 8; e += 2) wo[e] = w[e + 1], wo[e + 1] = w[e];
+                    }
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) z[e] = fmaf(x[e], w[e] * c[e], xo[e] * (wo[e] * sn[e])) * inv;
+                }
+                if (!is_v) {
+                    u.x = pack_bf16(z[0], z[1]), u.y = pack_bf16(z[2], z[3]);
+                    u.z = pack_bf16(z[4], z[5]), u.w = pack_bf16(z[6], z[7]);
+                }
+            }
+            if (!in) continue;
+            if (is_q) {
+                *reinterpret_cast<uint4 *>(qrow + h * D) = u;
+                if (m.ring >= 0) *reinterpret_cast<uint4 *>(a.ring + m.ring + h * a.ring_head + d0) = u;
+            } else {
+                const int g = is_v ? h - a.hq - a.hkv : h - a.hq;
+                *reinterpret_cast<uint4 *>((is_v ? a.vp : a.kp) + m.page + g * a.head_stride + d0) = u;
+            }
+        }
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&sh->empty[st]));
+        if (++st == (uint32_t)stages) st = 0, ph ^= 1;
+    }
+}
+
+template <int D>
+cudaError_t launch(const AppArgs &a, cudaStream_t st)
+{
+    const size_t head = (sizeof(TokShared) + 127) / 128 * 128;
+    const int sb = tok_stage_bytes(a.hq, a.hkv, D, a.rot);
+    int stages = 0, per_sm = 4;
+    for (; per_sm > 0 && stages < (per_sm > 1 ? 3 : 2); per_sm >>= 1) {
+        // 54, 110 or 222 KB a CTA; three tokens staged at least, two with one CTA per SM
+        const size_t room = (per_sm == 4 ? 54 : per_sm == 2 ? 110 : 222) * 1024;
+        stages = room > head ? (int)((room - head) / sb) : 0;
+        if (stages >= (per_sm > 1 ? 3 : 2)) break;
+    }
+    if ((int64_t)a.rows * (a.hq + 2 * a.hkv) <= kSmallRows || per_sm == 0) {
+        constexpr int RPP = 32 / (D / 8), WPC = kAppThreads / 32;
+        const int parts = (a.hq + 2 * a.hkv + RPP - 1) / RPP;
+        if (parts > 65535) return cudaErrorInvalidConfiguration;
+        const dim3 grid((unsigned)(((int64_t)a.rows + WPC - 1) / WPC), (unsigned)parts);
+        append_kernel<D><<<grid, kAppThreads, 0, st>>>(a);
+        return cudaGetLastError();
+    }
+    if (stages > kTokMaxStages) stages = kTokMaxStages;
+    const size_t smem = head + (size_t)stages * sb;
+    cudaError_t e =
+        cudaFuncSetAttribute(append_staged_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    int dev = 0, sms = 0;
+    if (e == cudaSuccess) e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e != cudaSuccess) return e;
+    const int grid = a.rows < sms * per_sm ? a.rows : sms * per_sm;
+    append_staged_kernel<D><<<grid, kTokThreads, smem, st>>>(a, stages);
     return cudaGetLastError();
 }
 
@@ -211,16 +485,18 @@ cudaError_t launch_append(const kara_cache *c, int32_t layer, const kara_tokens 
     a.len = t->len;
     a.err = err;
     a.eps = r->eps;
+    const Stall dbg = debug_stall(kTokTimeoutNs);
+    a.stall = dbg.on;
+    a.wait_ns = dbg.wait_ns;
     a.n = t->n;
     a.rows = t->rows;
     a.num_blocks = c->num_blocks;
-    a.bs = c->block_size;
     a.hq = c->num_q_heads;
     a.hkv = c->num_kv_heads;
     a.n_pos = r->rot_dim > 0 ? r->n_pos : 1;
     a.rot = r->rot_dim;
     a.inter = r->interleaved;
-    return D == 128 ? launch<128, 1>(a, st) : launch<64, 1>(a, st);
+    return D == 128 ? launch<128>(a, st) : launch<64>(a, st);
 }
 
 }  // namespace kara

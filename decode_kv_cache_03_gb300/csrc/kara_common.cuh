@@ -114,8 +114,8 @@ cudaError_t launch_qring_compact(const kara_cache *c, const kara_params *p, cons
 cudaError_t launch_qring_append(const kara_cache *c, const kara_params *p, const kara_batch *b,
                                 const void *q_new, cudaStream_t st);
 int decode_max_splits(int32_t bt_stride, int32_t block_size);
-cudaError_t launch_extend(int32_t num_blocks, int32_t block_size, const int32_t *len, const int32_t *n_new,
-                          int32_t *bt, int32_t bt_stride, const int32_t *fresh, int64_t n_fresh, const kara_tokens *t,
+cudaError_t launch_extend(int32_t num_blocks, const int32_t *len, const int32_t *n_new, int32_t *bt, int32_t bt_stride,
+                          const int32_t *fresh, int64_t n_fresh, const kara_tokens *t,
                           int32_t *used, int32_t *err, cudaStream_t st);
 cudaError_t launch_append(const kara_cache *c, int32_t layer, const kara_tokens *t, const kara_rope *r, const void *q,
                           int64_t q_stride, const void *k, int64_t k_stride, const void *v, int64_t v_stride,

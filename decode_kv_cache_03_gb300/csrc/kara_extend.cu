@@ -37,7 +37,8 @@ constexpr int kScanItem = 256;          // table entries a warp checks per turn
 constexpr int64_t kOneCta = 4096;
 
 struct ExtArgs {
-    int32_t n, rows, num_blocks, bs, bt_stride, window;
+    int32_t n, rows, num_blocks, bt_stride, window;
+    static constexpr int32_t bs = 16;  // tokens per cache block (the supported block size)
     int64_t n_fresh;
     const int32_t *len, *n_new, *fresh;
     int32_t *bt;
@@ -84,6 +85,17 @@ __device__ __forceinline__ bool seq_ok(const ExtArgs &a, int32_t len, int32_t m)
     return len >= 0 && m >= 0 && ((int64_t)len + m + a.bs - 1) / a.bs <= a.bt_stride;
 }
 
+// A barrier of all threads of the call (their writes to global memory are visible after it).
+__device__ __forceinline__ void meet(int nc)
+{
+    if (nc == 1) {
+        __syncthreads();
+    } else {
+        ptx::cluster_arrive();
+        ptx::cluster_wait();
+    }
+}
+
 __global__ void __launch_bounds__(kExtThreads, 1) extend_kernel(const ExtArgs a)
 {
     extern __shared__ uint32_t ext_smem[];
@@ -93,85 +105,86 @@ __global__ void __launch_bounds__(kExtThreads, 1) extend_kernel(const ExtArgs a)
     __shared__ int flags;   // of the whole cluster, in CTA 0
     __shared__ int wrong;   // this CTA saw a bad length
     cg::cluster_group cluster = cg::this_cluster();
-    const int rank = (int)cluster.block_rank(), nc = (int)cluster.num_blocks();
+    const int rank = (int)cluster.block_rank(), nc = (int)gridDim.x;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int gw = warp * nc + rank, nw = nc * (kExtThreads / 32);  // warps of the cluster, dealt across CTAs
+    const int gw = warp * nc + rank, nw = nc * (kExtThreads / 32);  // warps of the call, dealt across CTAs
 
     if (tid == 0) {
         flags = rank == 0 && *(volatile int32_t *)a.err != 0 ? kEarlier : 0;
         wrong = 0;
     }
+    for (int i = tid; i < a.window / 32; i += kExtThreads) bits[i] = 0;
     __syncthreads();
-    ptx::cluster_arrive();  // CTA 0's flags are set up (waited for before the first CTA adds to them)
+    if (nc > 1) ptx::cluster_arrive();  // CTA 0's flags are set up (waited for before the first CTA adds to them)
 
-    // ---- totals: tokens and blocks (every CTA, from the lengths)
-    longlong2 carry = make_longlong2(0, 0);
+    // ---- totals: tokens and blocks (every CTA, from the lengths); the entry of the block that a
+    // growing sequence continues is looked at on the way, by one CTA
+    int found = 0;
+    longlong2 carry = make_longlong2(0, 0), in = carry;
+    int32_t len = 0, m = 0, need = 0;  // of the last pass over the sequences
     for (int base = 0; base < a.n; base += kExtThreads) {
         const int s = base + tid;
-        longlong2 v = make_longlong2(0, 0);
+        len = m = need = 0;
+        int32_t open = 0;
         if (s < a.n) {
-            const int32_t len = a.len[s], m = a.n_new[s];
-            if (seq_ok(a, len, m)) {
-                v = make_longlong2(m, blocks_of(a, (int64_t)len + m) - blocks_of(a, len));
-            } else {
+            len = a.len[s];
+            m = a.n_new[s];
+            if (!seq_ok(a, len, m)) {
                 wrong = 1;
+                m = 0;
+            } else {
+                need = blocks_of(a, (int64_t)len + m) - blocks_of(a, len);
+                if (warp % nc == rank && m > 0 && len % a.bs) open = a.bt[(int64_t)s * a.bt_stride + len / a.bs];
             }
         }
         longlong2 tot;
-        const longlong2 in = block_scan2(v, scratch, tot);
-        if (a.start_in_smem && s < a.n) start[s] = (int32_t)(carry.x + in.x - v.x);
+        in = block_scan2(make_longlong2(m, need), scratch, tot);
+        if (a.start_in_smem && s < a.n) start[s] = (int32_t)(carry.x + in.x - m);
+        in.x += carry.x, in.y += carry.y;
         carry.x += tot.x, carry.y += tot.y;
+        if (open < 0 || open >= a.num_blocks) found |= kBad;
     }
     if (a.start_in_smem && tid == 0) start[a.n] = (int32_t)carry.x;
     const int64_t total = carry.x, F = carry.y;
     const int plan = wrong || total > a.rows ? KARA_EINVAL : F > a.n_fresh ? KARA_ENOBLOCKS : KARA_OK;
 
-    // ---- checks, dealt over the cluster
-    int found = 0;
-    if (plan == KARA_OK) {
-        // the open block of each growing sequence is read for its slots
-        for (int s = gw * 32 + lane; s < a.n; s += nw * 32) {
-            const int32_t len = a.len[s];
-            if (a.n_new[s] > 0 && len % a.bs) {
-                const int32_t b = a.bt[(int64_t)s * a.bt_stride + len / a.bs];
-                if (b < 0 || b >= a.num_blocks) found |= kBad;
-            }
-        }
-        const int per_row = (a.bt_stride + kScanItem - 1) / kScanItem;
-        for (int w0 = 0; F > 0 && w0 < a.num_blocks; w0 += a.window) {
+    // ---- consumed ids: each once, and in no table of the batch (dealt over the cluster)
+    const int per_row = (a.bt_stride + kScanItem - 1) / kScanItem;
+    for (int w0 = 0; plan == KARA_OK && F > 0 && w0 < a.num_blocks; w0 += a.window) {
+        if (w0 > 0) {
             __syncthreads();
             for (int i = tid; i < a.window / 32; i += kExtThreads) bits[i] = 0;
             __syncthreads();
-            for (int64_t i = tid; i < F; i += kExtThreads) {
-                const int32_t f = a.fresh[i];
-                if (f < 0 || f >= a.num_blocks) found |= kBad;
-                const uint32_t o = (uint32_t)f - (uint32_t)w0;
-                if (o < (uint32_t)a.window && (atomicOr(&bits[o >> 5], 1u << (o & 31)) >> (o & 31) & 1u)) found |= kDup;
+        }
+        for (int64_t i = tid; i < F; i += kExtThreads) {
+            const int32_t f = a.fresh[i];
+            if (f < 0 || f >= a.num_blocks) found |= kBad;
+            const uint32_t o = (uint32_t)f - (uint32_t)w0;
+            if (o < (uint32_t)a.window && (atomicOr(&bits[o >> 5], 1u << (o & 31)) >> (o & 31) & 1u)) found |= kDup;
+        }
+        __syncthreads();
+        for (int64_t it = gw; it < (int64_t)a.n * per_row; it += nw) {
+            const int s = (int)(it / per_row), c0 = (int)(it % per_row) * kScanItem;
+            const int32_t have = blocks_of(a, a.len[s]);
+            const int32_t *row = a.bt + (int64_t)s * a.bt_stride;
+            int32_t id[kScanItem / 32];
+#pragma unroll
+            for (int k = 0; k < kScanItem / 32; ++k) {
+                const int c = c0 + k * 32 + lane;
+                id[k] = c < have ? row[c] : -1;
             }
-            __syncthreads();
-            for (int64_t it = gw; it < (int64_t)a.n * per_row; it += nw) {
-                const int s = (int)(it / per_row), c0 = (int)(it % per_row) * kScanItem;
-                const int32_t have = blocks_of(a, a.len[s]);
-                const int32_t *row = a.bt + (int64_t)s * a.bt_stride;
-                int32_t id[kScanItem / 32];
 #pragma unroll
-                for (int k = 0; k < kScanItem / 32; ++k) {
-                    const int c = c0 + k * 32 + lane;
-                    id[k] = c < have ? row[c] : -1;
-                }
-#pragma unroll
-                for (int k = 0; k < kScanItem / 32; ++k) {
-                    const uint32_t o = (uint32_t)id[k] - (uint32_t)w0;
-                    if (id[k] >= 0 && o < (uint32_t)a.window && (bits[o >> 5] >> (o & 31) & 1u)) found |= kDup;
-                }
+            for (int k = 0; k < kScanItem / 32; ++k) {
+                const uint32_t o = (uint32_t)id[k] - (uint32_t)w0;
+                if (id[k] >= 0 && o < (uint32_t)a.window && (bits[o >> 5] >> (o & 31) & 1u)) found |= kDup;
             }
         }
     }
     found = __reduce_or_sync(0xffffffffu, found);
     __syncwarp();
-    ptx::cluster_wait();
+    if (nc > 1) ptx::cluster_wait();
     if (lane == 0 && found) atomicOr(cluster.map_shared_rank(&flags, 0), found);
-    cluster.sync();
+    meet(nc);
     const int all = *cluster.map_shared_rank(&flags, 0);
     const bool ok = plan == KARA_OK && all == 0;
 
@@ -184,25 +197,31 @@ __global__ void __launch_bounds__(kExtThreads, 1) extend_kernel(const ExtArgs a)
         a.q_start[a.n] = ok ? (int32_t)total : 0;
     }
     const bool in_place = a.new_len == a.len;
+    const bool one_pass = a.n <= kExtThreads;  // the sums of the pass above are still at hand
     carry = make_longlong2(0, 0);
     for (int base = 0; base < a.n; base += kExtThreads) {
         const int s = base + tid;
-        int32_t len = 0, m = 0, need = 0;
-        if (s < a.n) {
-            len = a.len[s];
-            m = ok ? a.n_new[s] : 0;
-            need = blocks_of(a, (int64_t)len + m) - blocks_of(a, len);
-        }
-        longlong2 tot = make_longlong2(0, 0), in = tot;
-        if (ok) in = block_scan2(make_longlong2(m, need), scratch, tot);
-        if (warp % nc == rank && s < a.n) {
-            a.q_start[s] = ok ? (int32_t)(carry.x + in.x - m) : 0;
-            if (!in_place) a.new_len[s] = len + m;
+        if (!one_pass) {
+            len = m = need = 0;
+            if (s < a.n) {
+                len = a.len[s];
+                m = ok ? a.n_new[s] : 0;
+                need = blocks_of(a, (int64_t)len + m) - blocks_of(a, len);
+            }
+            longlong2 tot = make_longlong2(0, 0);
+            in = tot;
+            if (ok) in = block_scan2(make_longlong2(m, need), scratch, tot);
+            in.x += carry.x, in.y += carry.y;
+            carry.x += tot.x, carry.y += tot.y;
         }
         if (warp % nc == rank) {
+            if (s < a.n) {
+                a.q_start[s] = ok ? (int32_t)(in.x - m) : 0;
+                if (!in_place) a.new_len[s] = ok ? len + m : len;
+            }
             // a warp fills the entries of its sequences one after another
-            const int64_t off = carry.y + in.y - need;
-            for (unsigned todo = __ballot_sync(0xffffffffu, need > 0); todo; todo &= todo - 1) {
+            const int64_t off = in.y - need;
+            for (unsigned todo = __ballot_sync(0xffffffffu, ok && need > 0); todo; todo &= todo - 1) {
                 const int src = __ffs(todo) - 1;
                 const int64_t o = __shfl_sync(0xffffffffu, off, src);
                 const int cnt = __shfl_sync(0xffffffffu, need, src);
@@ -211,48 +230,60 @@ __global__ void __launch_bounds__(kExtThreads, 1) extend_kernel(const ExtArgs a)
                 for (int i = lane; i < cnt; i += 32) row[i] = a.fresh[o + i];
             }
         }
-        carry.x += tot.x, carry.y += tot.y;
     }
-    cluster.sync();  // the new entries (and q_start, where it is searched in global memory) are visible
+    meet(nc);  // the new entries (and q_start, where it is searched in global memory) are visible
 
-    // ---- token rows: 32 per warp, each row's sequence by bisection of the first rows
+    // ---- token rows: a warp takes 32 at a time, four times over so that the look-ups overlap; each
+    // row's sequence by bisection of the first rows
     const int32_t *first = a.start_in_smem ? start : a.q_start;
-    for (int64_t t0 = (int64_t)gw * 32; t0 < a.rows; t0 += (int64_t)nw * 32) {
-        const int64_t t = t0 + lane;
-        if (t >= a.rows) break;
-        int64_t slot = -1;
-        int32_t s = -1, x = -1;
-        if (ok && t < total) {
-            int lo = 0, hi = a.n;  // last sequence whose first row is <= t
-            while (hi - lo > 1) {
-                const int mid = (lo + hi) >> 1;
-                if (first[mid] <= t) lo = mid; else hi = mid;
+    constexpr int kU = 4;
+    for (int64_t t0 = (int64_t)gw * 32 + lane; t0 < a.rows; t0 += (int64_t)nw * 32 * kU) {
+        int64_t slot[kU];
+        int32_t s[kU], x[kU], b[kU];
+#pragma unroll
+        for (int u = 0; u < kU; ++u) {
+            const int64_t t = t0 + (int64_t)u * nw * 32;
+            s[u] = x[u] = -1;
+            if (ok && t < total) {
+                int lo = 0, hi = a.n;  // last sequence whose first row is <= t
+                while (hi - lo > 1) {
+                    const int mid = (lo + hi) >> 1;
+                    if (first[mid] <= t) lo = mid; else hi = mid;
+                }
+                s[u] = lo;
+                x[u] = a.len[lo] + (int32_t)(t - first[lo]);
             }
-            s = lo;
-            x = a.len[s] + (int32_t)(t - first[s]);
-            slot = (int64_t)__ldcg(a.bt + (int64_t)s * a.bt_stride + x / a.bs) * a.bs + x % a.bs;
         }
-        a.slot[t] = slot;
-        a.seq[t] = s;
-        a.pos[t] = x;
+#pragma unroll
+        for (int u = 0; u < kU; ++u)
+            b[u] = s[u] >= 0 ? __ldcg(a.bt + (int64_t)s[u] * a.bt_stride + x[u] / a.bs) : 0;
+#pragma unroll
+        for (int u = 0; u < kU; ++u) slot[u] = s[u] >= 0 ? (int64_t)b[u] * a.bs + x[u] % a.bs : -1;
+#pragma unroll
+        for (int u = 0; u < kU; ++u) {
+            const int64_t t = t0 + (int64_t)u * nw * 32;
+            if (t >= a.rows) break;
+            a.slot[t] = slot[u];
+            a.seq[t] = s[u];
+            a.pos[t] = x[u];
+        }
     }
     if (in_place && ok) {
-        cluster.sync();  // every CTA has read the old lengths
+        meet(nc);  // every CTA has read the old lengths
         for (int s = gw * 32 + lane; s < a.n; s += nw * 32) a.new_len[s] += a.n_new[s];
     }
 }
 
 }  // namespace
 
-cudaError_t launch_extend(int32_t num_blocks, int32_t block_size, const int32_t *len, const int32_t *n_new,
-                          int32_t *bt, int32_t bt_stride, const int32_t *fresh, int64_t n_fresh, const kara_tokens *t,
+cudaError_t launch_extend(int32_t num_blocks, const int32_t *len, const int32_t *n_new, int32_t *bt, int32_t bt_stride,
+                          const int32_t *fresh, int64_t n_fresh, const kara_tokens *t,
                           int32_t *used, int32_t *err, cudaStream_t st)
 {
     ExtArgs a;
     a.n = t->n;
     a.rows = t->rows;
     a.num_blocks = num_blocks;
-    a.bs = block_size;
     a.bt_stride = bt_stride;
     a.window = num_blocks < kBitWindow ? (num_blocks + 31) / 32 * 32 : kBitWindow;
     a.n_fresh = n_fresh;

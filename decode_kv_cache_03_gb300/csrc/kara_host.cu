@@ -346,7 +346,7 @@ kara_status kara_extend_tables(int32_t num_blocks, int32_t block_size, const int
     if (out->n > 0 && (!len || !n_new || !block_table || !out->len)) return KARA_EINVAL;
     if ((n_fresh > 0 && !fresh) || !n_used || !err) return KARA_EINVAL;
     if (!out->q_start || (out->rows > 0 && (!out->slot || !out->seq || !out->pos))) return KARA_EINVAL;
-    return cuda_status(launch_extend(num_blocks, block_size, len, n_new, block_table, bt_stride, fresh, n_fresh, out,
+    return cuda_status(launch_extend(num_blocks, len, n_new, block_table, bt_stride, fresh, n_fresh, out,
                                      n_used, err, (cudaStream_t)stream));
 }
 

@@ -204,6 +204,14 @@ def kara_decode_attention(c: Cache, layer: int, lengths: torch.Tensor, block_tab
            "kara_decode_attention")
 
 
+def _raw_stream(err: torch.Tensor, stream):
+    """The stream's handle, the current one of err's device if None (torch.cuda.current_stream costs
+    several microseconds of host time, as much as a whole small call)."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(err.device.index)
+    return stream.cuda_stream
+
+
 def _same_device(err: torch.Tensor, where: str, *tensors):
     """Refuses tensors that are not on the current CUDA device: the launch goes there."""
     d = err.device
@@ -263,7 +271,7 @@ def kara_extend_tables(num_blocks: int, block_size: int, lengths: torch.Tensor, 
             and fresh.is_contiguous())
     _check(_lib.kara_extend_tables(num_blocks, block_size, lengths.data_ptr(), n_new.data_ptr(),
                                    block_table.data_ptr(), block_table.shape[1], fresh.data_ptr(), fresh.numel(),
-                                   t, n_used.data_ptr(), err.data_ptr(), _stream(stream)), "kara_extend_tables")
+                                   t, n_used.data_ptr(), err.data_ptr(), _raw_stream(err, stream)), "kara_extend_tables")
 
 
 def _token_stride(x: torch.Tensor, rows: int, heads: int, d: int) -> int:
@@ -288,7 +296,7 @@ def kara_append_kv(c: Cache, layer: int, t: Tokens, r: Rope, q: torch.Tensor, k:
         assert ring.shape == (t.n, c.num_layers, c.num_q_heads, W, d)
     _check(_lib.kara_append_kv(c, layer, t, r, q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs,
                                q_out.data_ptr(), None if ring is None else ring.data_ptr(), W, err.data_ptr(),
-                               _stream(stream)), "kara_append_kv")
+                               _raw_stream(err, stream)), "kara_append_kv")
 
 
 def kara_chunk_workspace_size(c: Cache, n: int, rows: int) -> int:
@@ -305,7 +313,7 @@ def kara_chunk_attention(c: Cache, layer: int, t: Tokens, block_table: torch.Ten
     assert q.shape == out.shape == (t.rows, c.num_q_heads, c.head_dim)
     _check(_lib.kara_chunk_attention(c, layer, t, block_table.data_ptr(), block_table.shape[1], q.data_ptr(),
                                      out.data_ptr(), ws.data_ptr(), ws.numel() * ws.element_size(), err.data_ptr(),
-                                     _stream(stream)), "kara_chunk_attention")
+                                     _raw_stream(err, stream)), "kara_chunk_attention")
 
 
 def kara_select(p: Params, n_windows: int, scores: torch.Tensor, cand, kept: torch.Tensor, stream=None):

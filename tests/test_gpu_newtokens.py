@@ -756,3 +756,91 @@ def test_stalled_chunk_attention_times_out(monkeypatch):
     got, st = run_chunk(kara, d)
     assert st == 0
     check_chunk(d, got)
+
+
+@pytest.mark.parametrize("hq,hkv,D,rot,inter,norm,W,rows,pad", [
+    (40, 8, 128, 128, False, True, 128, 700, 3), (32, 8, 128, 64, True, False, 0, 801, 0),
+    (4, 2, 64, 64, False, True, 64, 3000, 40), (8, 8, 64, 32, False, True, 0, 1001, 7),
+    (18, 3, 128, 96, False, True, 64, 999, 1), (2, 2, 128, 0, False, True, 0, 5000, 0),
+    (160, 20, 128, 128, False, True, 0, 150, 2), (320, 40, 128, 128, True, True, 0, 70, 1),
+    (512, 256, 128, 128, False, True, 0, 30, 0)])
+def test_append_long_calls(hq, hkv, D, rot, inter, norm, W, rows, pad):
+    """Calls past the short kernel's limit: tokens staged with four, two and one CTAs per SM, and heads
+    that fit no stage; padding in the middle as well as at the end."""
+    kara = lib()
+    r = np.random.default_rng(rows)
+    m = rows // 2
+    bt, fresh = make_tables(np.array([m, rows - m]), int(blocks(rows)) + 1, int(blocks(m) + blocks(rows - m)) + 2, 3)
+    lengths, n_new = np.array([0, 0], np.int32), np.array([m, rows - m], np.int32)
+    table, q_start, ln, slot, seq, pos, _ = plain_extend(lengths, n_new, np.full_like(bt, -1), np.concatenate(
+        [bt[0][bt[0] >= 0], bt[1][bt[1] >= 0], fresh]), rows + pad)
+    hole = r.integers(0, rows, 5)
+    slot[hole] = -1
+    q, k, v = append_inputs(rows, hq, hkv, D, rows + pad)
+    g = torch.Generator().manual_seed(9)
+    qw, kw = ((1 + 0.3 * torch.randn(D, generator=g)).bfloat16() for _ in range(2)) if norm else (None, None)
+    cs = angles(6000, rot) if rot else None
+    nb = int(table.max()) + 3
+    kp = torch.zeros(1, nb, hkv, 16, D, dtype=torch.bfloat16, device=DEV)
+    vp = torch.zeros_like(kp)
+    ring = torch.zeros(2, 1, hq, W, D, dtype=torch.bfloat16, device=DEV) if W else None
+    q_out = torch.full((rows + pad, hq, D), 77.0, dtype=torch.bfloat16, device=DEV)
+    t = kara.tokens(i32(q_start), i32(ln), torch.from_numpy(slot).to(DEV), i32(seq), i32(pos))
+    keep = [x.to(DEV) if x is not None else None for x in (cs, qw, kw)]
+    err = error_word()
+    kara.kara_append_kv(kara.cache(kp, vp, hq), 0, t, kara.rope(keep[0], keep[1], keep[2], 1e-5, inter), *on_gpu(q, k, v),
+                        q_out, err, ring=ring)
+    assert kara.kara_get_error(err) == 0
+    live = np.flatnonzero(slot >= 0)
+    at = torch.from_numpy(pos[live]).long()
+    got = q_out.cpu()
+    gone = np.setdiff1d(np.arange(rows + pad), live)
+    assert (got[gone] == 77.0).all()
+    close_rows(got[live], plain_turn(q[live], qw, 1e-5, cs, at, inter), plain_turn(q[live], qw, 1e-5, None, None, inter))
+    sl = torch.from_numpy(slot[live])
+    kr = kp.cpu()[0].permute(0, 2, 1, 3).reshape(-1, hkv, D)
+    vr = vp.cpu()[0].permute(0, 2, 1, 3).reshape(-1, hkv, D)
+    close_rows(kr[sl], plain_turn(k[live], kw, 1e-5, cs, at, inter), plain_turn(k[live], kw, 1e-5, None, None, inter))
+    assert torch.equal(vr[sl], v[live])
+    rest = torch.ones(nb * 16, dtype=torch.bool)
+    rest[sl] = False
+    assert (kr[rest] == 0).all() and (vr[rest] == 0).all()
+    if W:
+        want = torch.zeros(2, 1, hq, W, D, dtype=torch.bfloat16)
+        for i in live:
+            if pos[i] >= ln[seq[i]] - W:
+                want[seq[i], 0, :, pos[i] % W] = got[i]
+        assert torch.equal(ring.cpu(), want)
+
+
+def test_append_long_call_reports_bad_rows_and_stalls(monkeypatch):
+    """Bad rows among the staged tokens are skipped and reported; with KARA_DEBUG_STALL=1 the waits run
+    out; the next call is right."""
+    kara = lib()
+    hq, hkv, D, rows = 4, 2, 64, 4000
+    q, k, v = append_inputs(8, hq, hkv, D, rows, fused=False)
+    kp = torch.zeros(1, 250, hkv, 16, D, dtype=torch.bfloat16, device=DEV)
+    vp = torch.zeros_like(kp)
+    dq, dk, dv, cs = q.to(DEV), k.to(DEV), v.to(DEV), angles(rows, D).to(DEV)
+
+    def call(slot, seq, pos):
+        t = kara.tokens(i32([0, rows]), i32([rows]), torch.from_numpy(slot).to(DEV), i32(seq), i32(pos))
+        out = torch.full((rows, hq, D), 5.0, dtype=torch.bfloat16, device=DEV)
+        err = error_word()
+        kara.kara_append_kv(kara.cache(kp, vp, hq), 0, t, kara.rope(cs), dq, dk, dv, out, err)
+        return kara.kara_get_error(err), out.cpu()
+
+    slot, seq, pos = np.arange(rows), np.zeros(rows, np.int32), np.arange(rows)
+    monkeypatch.setenv("KARA_DEBUG_STALL", "1")
+    assert call(slot, seq, pos)[0] == kara.ETIMEOUT
+    monkeypatch.delenv("KARA_DEBUG_STALL")
+    st, good = call(slot, seq, pos)
+    assert st == 0 and torch.equal(vp.cpu()[0].permute(0, 2, 1, 3).reshape(-1, hkv, D), v)
+    for what in ("slot", "seq", "pos"):
+        s2, q2, p2 = slot.copy(), seq.copy(), pos.copy()
+        {"slot": s2, "seq": q2, "pos": p2}[what][1234] = 4000 if what != "pos" else -1
+        st, got = call(s2, q2, p2)
+        assert st == (kara.EBADBLOCK if what == "slot" else kara.EINVAL)
+        assert (got[1234] == 5.0).all()
+        keep = np.arange(rows) != 1234
+        assert torch.equal(got[keep], good[keep])
