@@ -78,6 +78,8 @@ __global__ void __launch_bounds__(kAppThreads) append_kernel(const AppArgs a)
 
     const bool is_v = h >= a.hq + a.hkv, is_q = h < a.hq;
 
+    // launched as a programmatic dependent of what precedes it on the stream
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     // the row is on its way before the token's place is known (padding rows are read, not written)
     const int64_t slot = a.slot[t];
     const int32_t s = a.seq[t], x = a.pos[t];
@@ -252,6 +254,8 @@ __global__ void __launch_bounds__(kTokThreads, 4) append_staged_kernel(const App
         ptx::fence_mbarrier_init();
     }
     __syncthreads();
+    // launched as a programmatic dependent of what precedes it on the stream
+    asm volatile("griddepcontrol.wait;" ::: "memory");
 
     if (warp == kTokWarps) {
         uint32_t st = 0, ph = 1, issued = 0;
@@ -438,8 +442,7 @@ cudaError_t launch(const AppArgs &a, cudaStream_t st)
         const int parts = (a.hq + 2 * a.hkv + RPP - 1) / RPP;
         if (parts > 65535) return cudaErrorInvalidConfiguration;
         const dim3 grid((unsigned)(((int64_t)a.rows + WPC - 1) / WPC), (unsigned)parts);
-        append_kernel<D><<<grid, kAppThreads, 0, st>>>(a);
-        return cudaGetLastError();
+        return launch_dependent(append_kernel<D>, grid, kAppThreads, 0, st, a);
     }
     if (stages > kTokMaxStages) stages = kTokMaxStages;
     const size_t smem = head + (size_t)stages * sb;
@@ -450,8 +453,7 @@ cudaError_t launch(const AppArgs &a, cudaStream_t st)
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     if (e != cudaSuccess) return e;
     const int grid = a.rows < sms * per_sm ? a.rows : sms * per_sm;
-    append_staged_kernel<D><<<grid, kTokThreads, smem, st>>>(a, stages);
-    return cudaGetLastError();
+    return launch_dependent(append_staged_kernel<D>, dim3((unsigned)grid), kTokThreads, smem, st, a, stages);
 }
 
 }  // namespace

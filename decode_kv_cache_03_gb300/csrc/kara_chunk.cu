@@ -1055,22 +1055,6 @@ Layout layout(const kara_cache *c, int32_t n, int32_t rows)
     return l;
 }
 
-template <class... A>
-cudaError_t launch_dependent(void (*kern)(A...), dim3 grid, int threads, size_t smem, cudaStream_t st, A... args)
-{
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = grid;
-    cfg.blockDim = dim3((unsigned)threads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = st;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kern, args...);
-}
-
 template <int D>
 cudaError_t launch_all(const CUtensorMap &km, const CUtensorMap &vm, const CUtensorMap &qm, const ChunkArgs &a,
                        cudaStream_t st)

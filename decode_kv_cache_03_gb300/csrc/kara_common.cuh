@@ -87,6 +87,24 @@ __device__ __forceinline__ int64_t pool_off(const Geo &g, int l, int32_t blk, in
 
 __host__ __device__ __forceinline__ size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 
+// Launches `kern` as a programmatic dependent of what precedes it on the stream: its launch overlaps
+// that grid's end, and it reads nothing global before its griddepcontrol.wait.
+template <class... A>
+cudaError_t launch_dependent(void (*kern)(A...), dim3 grid, int threads, size_t smem, cudaStream_t st, A... args)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
 // Host-side argument checks of the entry points; fills the geometry of a call.
 kara_status geo_from_args(const kara_cache *c, const kara_params *p, const kara_batch *b, Geo *g);
 

@@ -31,10 +31,14 @@ constexpr int kExtThreads = 1024;
 constexpr int kExtCtas = 8;             // portable cluster size
 constexpr int kBitWindow = 1 << 20;     // ids per bitmap window: 128 KB of shared memory
 constexpr int kStartCap = 16384;        // sequences whose q_start fits beside it (64 KB)
-constexpr int kScanItem = 256;          // table entries a warp checks per turn
+constexpr int kScanItem = 512;          // table entries a warp checks per turn
 // Up to this many entries to check and rows to write, one CTA does it all: the
 // cluster's barriers then cost more than its width saves.
 constexpr int64_t kOneCta = 4096;
+
+// Calls of more rows leave them to a kernel over all SMs.  Measured (apart / in one kernel, us):
+// 4096 rows 9.1 / 7.3, 8192 8.9 / 7.5, 16384 9.4 / 8.7, 131072 11.6 / 24.7.
+constexpr int kRowsApart = 20480;
 
 struct ExtArgs {
     int32_t n, rows, num_blocks, bt_stride, window;
@@ -45,6 +49,7 @@ struct ExtArgs {
     int32_t *q_start, *new_len, *seq, *pos, *used, *err;
     int64_t *slot;
     int32_t start_in_smem;
+    int32_t rows_apart;  // the token rows are another kernel's
 };
 
 enum : int { kBad = 1, kDup = 2, kEarlier = 4 };
@@ -104,16 +109,19 @@ __global__ void __launch_bounds__(kExtThreads, 1) extend_kernel(const ExtArgs a)
     __shared__ longlong2 scratch[33];
     __shared__ int flags;   // of the whole cluster, in CTA 0
     __shared__ int wrong;   // this CTA saw a bad length
+    __shared__ int32_t taken[kExtThreads + 1];  // ids taken before each sequence of a pass
     cg::cluster_group cluster = cg::this_cluster();
     const int rank = (int)cluster.block_rank(), nc = (int)gridDim.x;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int gw = warp * nc + rank, nw = nc * (kExtThreads / 32);  // warps of the call, dealt across CTAs
 
+    for (int i = tid; i < a.window / 32; i += kExtThreads) bits[i] = 0;
+    // launched as a programmatic dependent of what precedes it on the stream
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     if (tid == 0) {
         flags = rank == 0 && *(volatile int32_t *)a.err != 0 ? kEarlier : 0;
         wrong = 0;
     }
-    for (int i = tid; i < a.window / 32; i += kExtThreads) bits[i] = 0;
     __syncthreads();
     if (nc > 1) ptx::cluster_arrive();  // CTA 0's flags are set up (waited for before the first CTA adds to them)
 
@@ -214,25 +222,31 @@ __global__ void __launch_bounds__(kExtThreads, 1) extend_kernel(const ExtArgs a)
             in.x += carry.x, in.y += carry.y;
             carry.x += tot.x, carry.y += tot.y;
         }
-        if (warp % nc == rank) {
-            if (s < a.n) {
-                a.q_start[s] = ok ? (int32_t)(in.x - m) : 0;
-                if (!in_place) a.new_len[s] = ok ? len + m : len;
-            }
-            // a warp fills the entries of its sequences one after another
-            const int64_t off = in.y - need;
-            for (unsigned todo = __ballot_sync(0xffffffffu, ok && need > 0); todo; todo &= todo - 1) {
-                const int src = __ffs(todo) - 1;
-                const int64_t o = __shfl_sync(0xffffffffu, off, src);
-                const int cnt = __shfl_sync(0xffffffffu, need, src);
-                const int at = __shfl_sync(0xffffffffu, blocks_of(a, len), src);
-                int32_t *row = a.bt + (int64_t)(base + warp * 32 + src) * a.bt_stride + at;
-                for (int i = lane; i < cnt; i += 32) row[i] = a.fresh[o + i];
+        if (warp % nc == rank && s < a.n) {
+            a.q_start[s] = ok ? (int32_t)(in.x - m) : 0;
+            if (!in_place) a.new_len[s] = ok ? len + m : len;
+        }
+        if (ok && F > 0) {
+            // a warp per sequence fills its entries
+            __syncthreads();
+            taken[tid] = (int32_t)(in.y - need);
+            if (tid == kExtThreads - 1) taken[kExtThreads] = (int32_t)in.y;
+            __syncthreads();
+            for (int i = gw; i < kExtThreads && base + i < a.n; i += nw) {
+                const int32_t o = taken[i], cnt = taken[i + 1] - o;
+                if (cnt == 0) continue;
+                int32_t *row = a.bt + (int64_t)(base + i) * a.bt_stride + blocks_of(a, a.len[base + i]);
+                for (int e = lane; e < cnt; e += 32) row[e] = a.fresh[o + e];
             }
         }
     }
     meet(nc);  // the new entries (and q_start, where it is searched in global memory) are visible
 
+    if (a.rows_apart) {
+        if (in_place && ok)
+            for (int s = gw * 32 + lane; s < a.n; s += nw * 32) a.new_len[s] += a.n_new[s];
+        return;
+    }
     // ---- token rows: a warp takes 32 at a time, four times over so that the look-ups overlap; each
     // row's sequence by bisection of the first rows
     const int32_t *first = a.start_in_smem ? start : a.q_start;
@@ -274,6 +288,53 @@ __global__ void __launch_bounds__(kExtThreads, 1) extend_kernel(const ExtArgs a)
     }
 }
 
+// The token rows of a long call, over all SMs: launched as a programmatic dependent of the
+// kernel above, whose first rows, lengths and tables say everything (a call that did
+// nothing left no tokens: every row is padding).
+constexpr int kRowThreads = 256, kRowsPer = 4;  // threads, rows of each
+constexpr int kRowCap = 8192;                   // sequences whose first rows a CTA keeps in shared memory
+
+__global__ void __launch_bounds__(kRowThreads) token_rows_kernel(const ExtArgs a)
+{
+    __shared__ int32_t start[kRowCap];
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int32_t total = a.q_start[a.n];
+    const bool in_smem = a.n <= kRowCap;
+    if (in_smem)
+        for (int i = threadIdx.x; i < a.n; i += kRowThreads) start[i] = a.q_start[i];
+    __syncthreads();
+    const int32_t *first = in_smem ? start : a.q_start;
+    const int64_t t0 = (int64_t)blockIdx.x * (kRowThreads * kRowsPer) + threadIdx.x;
+    int64_t slot[kRowsPer];
+    int32_t s[kRowsPer], x[kRowsPer];
+#pragma unroll
+    for (int u = 0; u < kRowsPer; ++u) {
+        const int64_t t = t0 + u * kRowThreads;
+        s[u] = x[u] = -1;
+        if (t < total) {
+            int lo = 0, hi = a.n;  // last sequence whose first row is <= t
+            while (hi - lo > 1) {
+                const int mid = (lo + hi) >> 1;
+                if (first[mid] <= t) lo = mid; else hi = mid;
+            }
+            s[u] = lo;
+            x[u] = a.new_len[lo] - (int32_t)(a.q_start[lo + 1] - t);
+        }
+    }
+#pragma unroll
+    for (int u = 0; u < kRowsPer; ++u)
+        slot[u] = s[u] < 0 ? -1
+                           : (int64_t)a.bt[(int64_t)s[u] * a.bt_stride + x[u] / a.bs] * a.bs + x[u] % a.bs;
+#pragma unroll
+    for (int u = 0; u < kRowsPer; ++u) {
+        const int64_t t = t0 + u * kRowThreads;
+        if (t >= a.rows) break;
+        a.slot[t] = slot[u];
+        a.seq[t] = s[u];
+        a.pos[t] = x[u];
+    }
+}
+
 }  // namespace
 
 cudaError_t launch_extend(int32_t num_blocks, const int32_t *len, const int32_t *n_new, int32_t *bt, int32_t bt_stride,
@@ -305,19 +366,34 @@ cudaError_t launch_extend(int32_t num_blocks, const int32_t *len, const int32_t 
             cudaFuncSetAttribute(extend_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
         if (e != cudaSuccess) return e;
     }
+    a.rows_apart = t->rows > kRowsApart;
     const int nc = (int64_t)t->n * bt_stride + t->rows <= kOneCta ? 1 : kExtCtas;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)nc);
     cfg.blockDim = dim3(kExtThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
-    cudaLaunchAttribute at[1];
+    cudaLaunchAttribute at[2];
     at[0].id = cudaLaunchAttributeClusterDimension;
     at[0].val.clusterDim.x = (unsigned)nc;
     at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, extend_kernel, a);
+    cfg.numAttrs = 2;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, extend_kernel, a);
+    if (e != cudaSuccess || !a.rows_apart) return e;
+    constexpr int per = kRowThreads * kRowsPer;
+    cudaLaunchConfig_t rows = {};
+    rows.gridDim = dim3((unsigned)(((int64_t)t->rows + per - 1) / per));
+    rows.blockDim = dim3(kRowThreads);
+    rows.stream = st;
+    cudaLaunchAttribute ra[1];
+    ra[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    ra[0].val.programmaticStreamSerializationAllowed = 1;
+    rows.attrs = ra;
+    rows.numAttrs = 1;
+    return cudaLaunchKernelEx(&rows, token_rows_kernel, a);
 }
 
 }  // namespace kara
