@@ -32,10 +32,10 @@
 //     the last block past the sequence's end, whatever they hold, and the values
 //     of the chunk's own tokens that are not finite (earlier tokens share their
 //     tile).  The rows that do see such a value get it added at the end.
-//   * Every CTA gets the same number of key tiles (to within one), whatever the
-//     lengths: all items' key tiles are laid end to end and cut evenly.  A cut
-//     inside an item leaves partial (O, max, sum) in the workspace, joined by
-//     the merge kernel in CTA order, so results do not depend on timing.
+//   * Every CTA gets the same work (to within a key tile), whatever the lengths:
+//     all items' key tiles, weighted by what they cost, are laid end to end and cut
+//     evenly.  A cut inside an item leaves partial (O, max, sum) in the workspace,
+//     joined by the merge kernel in CTA order, so results do not depend on timing.
 //
 // What set the pace on the way (8192 tokens over 16384 keys, 40/8 heads, D 128; us):
 // one thread issuing every MMA with the waits between them, 2008; its loop with ring
@@ -80,7 +80,7 @@ constexpr uint32_t kTmemCols = 512;  // S0 S1 (128 columns each), O0 O1 (128 eac
 constexpr float kLazy = 8.f;         // see above: rescale when the maximum grew by more than 2^8
 constexpr uint64_t kTimeoutNs = 1000000000ull;
 constexpr int kPlanThreads = 1024;
-constexpr int kPlanCap = 4096;       // sequences / items whose prefix sums the plan keeps in shared memory
+constexpr int kPlanCap = 2048;       // sequences / items whose prefix sums the plan keeps in shared memory
 
 // One or two query tiles of a sequence (all KV heads have the same items).
 struct __align__(16) Item {
@@ -90,17 +90,21 @@ struct __align__(16) Item {
     int32_t nt;     // key tiles that its last token sees
     int32_t seq;
     int32_t len;    // cached length of the sequence
-    int32_t before; // key tiles of the items before this one
-    int32_t pad;
+    int64_t before; // cost of the items before this one
 };
 
-// Where a CTA starts: key tile `off` of item `item` for KV head `head`.
+// Where a CTA starts, and the one before it ends: key tile `off` of item `item` for KV
+// head `head` (the end of everything: head hkv, item 0).
 struct __align__(16) Start {
     int32_t head, item, off, pad;
 };
 
+__device__ __forceinline__ bool same_item(const Start &a, const Start &b)
+{
+    return a.head == b.head && a.item == b.item;
+}
+
 struct PlanHead {
-    int64_t tiles;    // key tiles of all items of one KV head
     int32_t items;
     int32_t ctas;     // CTAs that get work
 };
@@ -112,13 +116,14 @@ struct ChunkArgs {
     float scale2;     // log2(e) / sqrt(D)
     uint16_t *out;
     PlanHead *head;
-    Start *start;     // [ctas]
+    Start *start;     // [ctas + 1]
     Item *items;      // [cap_items]
     int32_t *seq_items;  // [n + 1]: items before each sequence
-    float *part;      // [2 * ctas][256][D]
+    float4 *part;     // [2 * ctas][D / 4][256]
     float2 *stat;     // [2 * ctas][256]: (max, sum) in the log2 domain
     const uint16_t *v;   // V pool at the call's layer
     int64_t block_stride, head_stride;
+    int32_t wide;        // out is 32-byte aligned
     int32_t stall;
     uint64_t wait_ns;
 };
@@ -128,8 +133,11 @@ __device__ __forceinline__ bool chunk_ok(const ChunkArgs &a, int32_t r0, int32_t
     return r0 >= 0 && r1 >= r0 && r1 <= a.rows && L >= r1 - r0 && ((int64_t)L + kBlk - 1) / kBlk <= a.bt_stride;
 }
 
-// First unit of CTA c: the key tiles of all heads cut into equal ranges.
-__device__ __forceinline__ int64_t cut(int64_t units, int ctas, int c) { return units * c / ctas; }
+// What a key tile and an item cost a CTA, about 1700 clocks each: two query tiles take
+// 3400 clocks a key tile, one takes 1700; an item's start and end about 7000.
+__device__ __forceinline__ int tile_cost(const ChunkArgs &a, int32_t ntok) { return ntok > a.TQ ? 2 : 1; }
+constexpr int kItemCost = 4;
+constexpr int kTilesPerCta = 2;  // fewer, and CTAs stay without work: a split costs a merge
 
 // ---- plan --------------------------------------------------------------------
 __device__ int64_t plan_scan(int64_t v, int64_t *scratch /* 33 */, int64_t *tot)
@@ -177,7 +185,7 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const ChunkArg
 {
     __shared__ int64_t scratch[33];
     __shared__ int32_t seq_s[kPlanCap];  // items before each sequence
-    __shared__ int32_t item_s[kPlanCap]; // key tiles before each item
+    __shared__ int64_t item_s[kPlanCap]; // cost of the items before each item
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int tid = threadIdx.x;
@@ -209,11 +217,12 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const ChunkArg
     // overlapping rows of a broken q_start could ask for more items than rows allow
     items = min(items, (int64_t)a.cap_items);
     __syncthreads();
-    int64_t tiles = 0;
+    int64_t cost = 0, tiles = 0;
     for (int64_t base = 0; base < items; base += kPlanThreads) {
         const int64_t i = base + tid;
         Item it;
         it.nt = 0;
+        int64_t c = 0;
         if (i < items) {
             const int s = a.n <= kPlanCap ? last_at_most(a.n, i, [&](int x) { return (int64_t)seq_s[x]; })
                                           : last_at_most(a.n, i, [&](int x) { return (int64_t)a.seq_items[x]; });
@@ -225,34 +234,42 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const ChunkArg
             it.ntok = min(per, m - t0);
             it.pos0 = it.len - m + t0;
             it.nt = (it.pos0 + it.ntok - 1) / kTile + 1;
-            it.pad = 0;
+            c = (int64_t)it.nt * tile_cost(a, it.ntok) + kItemCost;
         }
         int64_t tot;
-        const int64_t ex = tiles + plan_scan(it.nt, scratch, &tot);
+        it.before = cost + plan_scan(c, scratch, &tot);
         if (i < items) {
-            it.before = (int32_t)ex;
             if (i < kPlanCap) item_s[i] = it.before;
             a.items[i] = it;
         }
+        cost += tot;
+        plan_scan(it.nt, scratch, &tot);
         tiles += tot;
     }
     __syncthreads();
-    const int64_t units = tiles * a.hkv;
-    const int ctas = (int)min((int64_t)a.ctas, units);
-    for (int c = tid; c < ctas; c += kPlanThreads) {
-        const int64_t u = cut(units, ctas, c), r = u % tiles;
-        const int i = items <= kPlanCap
-                          ? last_at_most((int)items, r, [&](int x) { return (int64_t)item_s[x]; })
-                          : last_at_most((int)items, r, [&](int x) { return (int64_t)a.items[x].before; });
+    const int64_t units = cost * a.hkv;
+    const int ctas = (int)max((int64_t)(items > 0), min((int64_t)a.ctas, tiles * a.hkv / kTilesPerCta));
+    for (int c = tid; c <= ctas; c += kPlanThreads) {
         Start st;
-        st.head = (int32_t)(u / tiles);
-        st.item = i;
-        st.off = (int32_t)(r - (items <= kPlanCap ? item_s[i] : a.items[i].before));
-        st.pad = 0;
+        st.head = a.hkv, st.item = st.off = st.pad = 0;
+        if (c < ctas) {
+            // the tile that the cut falls into, or the next item if it falls behind the last one
+            const int64_t u = units * c / ctas, r = u % cost;
+            const int i = items <= kPlanCap
+                              ? last_at_most((int)items, r, [&](int x) { return item_s[x]; })
+                              : last_at_most((int)items, r, [&](int x) { return a.items[x].before; });
+            const Item it = a.items[i];
+            st.head = (int32_t)(u / cost);
+            st.item = i;
+            st.off = (int32_t)((r - it.before) / tile_cost(a, it.ntok));
+            if (st.off >= it.nt) {
+                st.off = 0;
+                if (++st.item == items) st.item = 0, ++st.head;
+            }
+        }
         a.start[c] = st;
     }
     if (tid == 0) {
-        a.head->tiles = tiles;
         a.head->items = (int32_t)items;
         a.head->ctas = ctas;
     }
@@ -412,6 +429,15 @@ __device__ __forceinline__ uint32_t bf16x2(float lo, float hi)
     return r;
 }
 
+// 32 bytes (32-byte aligned) from v[o..o+7].
+template <int N>
+__device__ __forceinline__ void st_global_32b(void *p, const uint32_t (&v)[N], const int o)
+{
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[o + 0]), "r"(v[o + 1]),
+                 "r"(v[o + 2]), "r"(v[o + 3]), "r"(v[o + 4]), "r"(v[o + 5]), "r"(v[o + 6]), "r"(v[o + 7])
+                 : "memory");
+}
+
 // A CTA's walk over its range of key tiles: piece by piece, the same in every warp.
 struct Piece {
     Item it;
@@ -425,37 +451,38 @@ struct Piece {
 template <bool AHEAD>
 struct Walk {
     const ChunkArgs &a;
-    int32_t left, head, item, off;
+    Start at, end;
     bool first;
     Item next;
     __device__ Walk(const ChunkArgs &args) : a(args)
     {
         const int cta = blockIdx.x;
-        const PlanHead h = *a.head;
-        left = 0;
         first = true;
-        if (cta < h.ctas) {
-            const int64_t units = h.tiles * a.hkv;
-            left = (int32_t)(cut(units, h.ctas, cta + 1) - cut(units, h.ctas, cta));
-            const Start s = a.start[cta];
-            head = s.head, item = s.item, off = s.off;
-            if (AHEAD) next = a.items[item];
+        at.head = end.head = at.item = end.item = at.off = end.off = 0;
+        if (cta < a.head->ctas) {
+            at = a.start[cta];
+            end = a.start[cta + 1];
+            if (AHEAD) next = a.items[at.item];
         }
     }
     __device__ bool step(Piece &p)
     {
-        if (left <= 0) return false;
-        p.it = AHEAD ? next : a.items[item];
-        p.head = head;
-        p.j0 = off;
-        p.j1 = min(p.it.nt, off + left);
-        p.whole = off == 0 && p.j1 == p.it.nt;
+        const bool last = same_item(at, end);
+        if (last && at.off == end.off) return false;
+        p.it = AHEAD ? next : a.items[at.item];
+        p.head = at.head;
+        p.j0 = at.off;
+        p.j1 = last ? end.off : p.it.nt;
+        p.whole = at.off == 0 && !last;
         p.slot = 2 * blockIdx.x + (first ? 0 : 1);
         first = false;
-        left -= p.j1 - p.j0;
-        off = 0;
-        if (++item == a.head->items) item = 0, ++head;
-        if (AHEAD && left > 0) next = a.items[item];
+        if (last) {
+            at.off = end.off;
+        } else {
+            at.off = 0;
+            if (++at.item == a.head->items) at.item = 0, ++at.head;
+            if (AHEAD && at.head < a.hkv) next = a.items[at.item];
+        }
         return true;
     }
 };
@@ -904,7 +931,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int64_t row = p.it.row0 + t;
                 const int rr = (two ? x * kTile : 0) + r;
                 const bool add = *(volatile int32_t *)&sh->odd_values[np & 3] == (int32_t)np + 1;
-                float *pp = a.part + ((int64_t)p.slot * 256 + rr) * D;
+                float4 *pp = a.part + (int64_t)p.slot * (D / 4) * 256 + rr;  // dims d..d+3 at pp[d / 4 * 256]
                 uint16_t *op = a.out + (row * a.hq + p.head * a.G + hd) * D;
 #pragma unroll
                 for (int c = 0; c < D; c += 32) {
@@ -938,17 +965,25 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                     }
                     if (p.whole) {
+                        // a warp's store touches 32 rows: as few and as wide as the alignment allows
+                        uint32_t b[16];
 #pragma unroll
-                        for (int e = 0; e < 32; e += 8)
-                            *reinterpret_cast<uint4 *>(op + c + e) =
-                                make_uint4(bf16x2(__uint_as_float(o[e]), __uint_as_float(o[e + 1])),
-                                           bf16x2(__uint_as_float(o[e + 2]), __uint_as_float(o[e + 3])),
-                                           bf16x2(__uint_as_float(o[e + 4]), __uint_as_float(o[e + 5])),
-                                           bf16x2(__uint_as_float(o[e + 6]), __uint_as_float(o[e + 7])));
+                        for (int e = 0; e < 16; ++e)
+                            b[e] = bf16x2(__uint_as_float(o[2 * e]), __uint_as_float(o[2 * e + 1]));
+                        if (a.wide) {
+                            st_global_32b(op + c, b, 0);
+                            st_global_32b(op + c + 16, b, 8);
+                        } else {
+#pragma unroll
+                            for (int e = 0; e < 16; e += 4)
+                                *reinterpret_cast<uint4 *>(op + c + 2 * e) =
+                                    make_uint4(b[e], b[e + 1], b[e + 2], b[e + 3]);
+                        }
                     } else {
 #pragma unroll
                         for (int e = 0; e < 32; e += 4)
-                            *reinterpret_cast<uint4 *>(pp + c + e) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+                            pp[(c + e) / 4 * 256] = make_float4(__uint_as_float(o[e]), __uint_as_float(o[e + 1]),
+                                                                __uint_as_float(o[e + 2]), __uint_as_float(o[e + 3]));
                     }
                 }
                 if (live && !p.whole) a.stat[(int64_t)p.slot * 256 + rr] = make_float2(m, z);
@@ -969,53 +1004,53 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // ---- merge ----------------------------------------------------------------------
-// Block c: the item that the cut before CTA c falls into, if that is the item's
+// Block (c, y): the item that the cut before CTA c falls into, if that is the item's
 // first cut: out = sum_i O_i 2^(m_i - M) / sum_i z_i 2^(m_i - M), pieces in CTA order.
-// A warp takes a row at a time.
+// A thread takes 8 dims of a row; lanes are rows, as the partials lie.
 template <int D>
 __global__ void __launch_bounds__(256) chunk_merge_kernel(const ChunkArgs a)
 {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const PlanHead h = *a.head;
-    const int c = blockIdx.x + 1;
-    if (c >= h.ctas) return;
-    const Start s = a.start[c];
-    if (s.off == 0) return;
-    const int64_t units = h.tiles * a.hkv;
+    const int ctas = a.head->ctas, c = blockIdx.x + 1;
+    if (c >= ctas) return;
+    const Start s = a.start[c], b = a.start[c - 1];
+    if (s.off == 0 || (same_item(s, b) && b.off > 0)) return;  // no cut, or an earlier one of the same item
     const Item it = a.items[s.item];
-    const int64_t u0 = cut(units, h.ctas, c) - s.off, u1 = u0 + it.nt;  // the item's units
-    const int64_t before = cut(units, h.ctas, c - 1);
-    if (u0 < before) return;  // an earlier cut of the same item
-    const int first = 2 * (c - 1) + (u0 == before ? 0 : 1);
-    int last = c;
-    while (last + 1 < h.ctas && cut(units, h.ctas, last + 1) < u1) ++last;
+    const int rr = (blockIdx.y & 7) * 32 + (threadIdx.x & 31), d4 = ((blockIdx.y >> 3) * 8 + (threadIdx.x >> 5)) * 2;
     const bool two = it.ntok > a.TQ;
-    const int lane = threadIdx.x & 31;
-    constexpr int V = D / 32;
-    for (int i = blockIdx.y * 8 + (threadIdx.x >> 5); i < it.ntok * a.G; i += gridDim.y * 8) {
-        const int t = i / a.G, hd = i % a.G;
-        const int rr = two && t >= a.TQ ? kTile + (t - a.TQ) * a.G + hd : t * a.G + hd;
-        float M = -INFINITY;
-        for (int k = c - 1; k <= last; ++k)
-            M = fmaxf(M, a.stat[(int64_t)(k < c ? first : 2 * k) * 256 + rr].x);
-        float den = 0.f, acc[V];
-#pragma unroll
-        for (int e = 0; e < V; ++e) acc[e] = 0.f;
-        for (int k = c - 1; k <= last; ++k) {
-            const int64_t o = (int64_t)(k < c ? first : 2 * k) * 256 + rr;
-            const float2 st = a.stat[o];
-            if (st.x == -INFINITY && st.y == 0.f) continue;  // nothing of this piece is seen by the row
-            const float f = ex2(st.x - M);
-            den = fmaf(st.y, f, den);
-#pragma unroll
-            for (int e = 0; e < V; ++e) acc[e] = fmaf(a.part[o * D + lane * V + e], f, acc[e]);
-        }
-        uint16_t *op = a.out + ((int64_t)(it.row0 + t) * a.hq + s.head * a.G + hd) * D + lane * V;
-#pragma unroll
-        for (int e = 0; e < V; e += 2)
-            *reinterpret_cast<uint32_t *>(op + e) = bf16x2(acc[e] / den, acc[e + 1] / den);
+    const int x = rr / kTile, r = rr % kTile, t = x * a.TQ + r / a.G, hd = r % a.G;
+    if (r >= a.G * a.TQ || t >= it.ntok || (x == 1 && !two)) return;
+    // the piece of CTA c - 1 (its last; its first too if it starts with the item), then those of the
+    // CTAs that start inside the item
+    const int first = 2 * (c - 1) + (same_item(s, b) ? 0 : 1);
+    int end = c + 1;
+    while (end < ctas && same_item(a.start[end], s)) ++end;
+    const auto empty = [&](int k) {  // CTA k got nothing
+        const Start p = a.start[k], q = a.start[k + 1];
+        return same_item(p, q) && p.off == q.off;
+    };
+    float M = -INFINITY;
+    for (int k = c - 1; k < end; ++k)
+        if (k < c || !empty(k)) M = fmaxf(M, a.stat[(int64_t)(k < c ? first : 2 * k) * 256 + rr].x);
+    float den = 0.f, acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    for (int k = c - 1; k < end; ++k) {
+        if (k >= c && empty(k)) continue;
+        const int64_t slot = k < c ? first : 2 * k;
+        const float2 st = a.stat[slot * 256 + rr];
+        if (st.x == -INFINITY && st.y == 0.f) continue;  // nothing of this piece is seen by the row
+        const float f = ex2(st.x - M);
+        den = fmaf(st.y, f, den);
+        const float4 u = a.part[(slot * (D / 4) + d4) * 256 + rr], v = a.part[(slot * (D / 4) + d4 + 1) * 256 + rr];
+        acc[0] = fmaf(u.x, f, acc[0]), acc[1] = fmaf(u.y, f, acc[1]), acc[2] = fmaf(u.z, f, acc[2]);
+        acc[3] = fmaf(u.w, f, acc[3]), acc[4] = fmaf(v.x, f, acc[4]), acc[5] = fmaf(v.y, f, acc[5]);
+        acc[6] = fmaf(v.z, f, acc[6]), acc[7] = fmaf(v.w, f, acc[7]);
     }
+    const float inv = 1.f / den;
+    uint16_t *op = a.out + ((int64_t)(it.row0 + t) * a.hq + s.head * a.G + hd) * D + d4 * 4;
+    *reinterpret_cast<uint4 *>(op) =
+        make_uint4(bf16x2(acc[0] * inv, acc[1] * inv), bf16x2(acc[2] * inv, acc[3] * inv),
+                   bf16x2(acc[4] * inv, acc[5] * inv), bf16x2(acc[6] * inv, acc[7] * inv));
 }
 
 // Tensor map over q, (d, head, row); a box is one 64-dim half of a query tile.
@@ -1046,7 +1081,7 @@ Layout layout(const kara_cache *c, int32_t n, int32_t rows)
     Layout l;
     l.cap = rows / (2 * TQ) + n;  // a sequence of m tokens has at most m / (2 TQ) + 1 items
     size_t o = 256;
-    l.start = o, o += align256(kMaxCtas * sizeof(Start));
+    l.start = o, o += align256((kMaxCtas + 1) * sizeof(Start));
     l.items = o, o += align256((size_t)l.cap * sizeof(Item));
     l.seq = o, o += align256(((size_t)n + 1) * sizeof(int32_t));
     l.stat = o, o += align256((size_t)2 * kMaxCtas * 256 * sizeof(float2));
@@ -1067,7 +1102,7 @@ cudaError_t launch_all(const CUtensorMap &km, const CUtensorMap &vm, const CUten
     if (e == cudaSuccess)
         e = launch_dependent(chunk_kernel<D>, dim3((unsigned)a.ctas), kThreads, smem, st, km, vm, qm, a);
     if (e == cudaSuccess && a.ctas > 1)
-        e = launch_dependent(chunk_merge_kernel<D>, dim3((unsigned)a.ctas - 1, 4), 256, 0, st, a);
+        e = launch_dependent(chunk_merge_kernel<D>, dim3((unsigned)a.ctas - 1, 8 * (D / 64)), 256, 0, st, a);
     return e;
 }
 
@@ -1106,7 +1141,8 @@ cudaError_t launch_chunk(const kara_cache *c, int32_t layer, const kara_tokens *
     a.items = reinterpret_cast<Item *>(w + l.items);
     a.seq_items = reinterpret_cast<int32_t *>(w + l.seq);
     a.stat = reinterpret_cast<float2 *>(w + l.stat);
-    a.part = reinterpret_cast<float *>(w + l.part);
+    a.part = reinterpret_cast<float4 *>(w + l.part);
+    a.wide = ((uintptr_t)out & 31u) == 0;
     const Stall dbg = debug_stall(kTimeoutNs);
     a.stall = dbg.on;
     a.wait_ns = dbg.wait_ns;
