@@ -28,8 +28,8 @@
 //     flight per SM).  Blocks past a sequence's end, and ids outside the pool,
 //     are copied from past the pool's end: the copy fills zeros.
 //   * A weight of 0 times NaN or infinity is NaN, so what a row must not see is
-//     cleared from V and not only masked in the logits: a warp zeroes the rows of
-//     the last block past the sequence's end, whatever they hold, and the values
+//     cleared from V and not only masked in the logits: four warps zero the rows of
+//     the last block past the sequence's end, whatever they hold, and clear the values
 //     of the chunk's own tokens that are not finite (earlier tokens share their
 //     tile).  The rows that do see such a value get it added at the end.
 //   * Every CTA gets the same work (to within a key tile), whatever the lengths:
@@ -289,6 +289,7 @@ struct Shared {
     uint64_t done[2];
     uint32_t tmem;
     int32_t abort;
+    int32_t fixed;        // edge tiles' quarters cleaned
     int32_t odd_values[4];  // 1 + the last piece (by its number mod 4) whose V had values that are not finite
     float2 stat[kTile];   // (max, sum) of the odd key tiles, for joining a single query tile
 };
@@ -303,11 +304,13 @@ struct Cfg {
 
 // Bounded wait on phase `parity` of `bar`: gives up after limit_ns, or once another
 // warp of the CTA gave up, recording KARA_ETIMEOUT.
+template <int NAP = 0>
 __device__ __forceinline__ bool cwait(uint32_t bar, uint32_t parity, Shared *sh, const ChunkArgs &a)
 {
     if (mbar_try_wait(bar, parity)) return true;
     uint64_t t0 = 0;
     for (uint32_t it = 1;; ++it) {
+        if (NAP) __nanosleep(NAP);
         if (mbar_try_wait(bar, parity)) return true;
         if ((it & 63u) == 0) {
             if (*(volatile int32_t *)&sh->abort) return false;
@@ -520,6 +523,31 @@ __device__ __forceinline__ uint32_t finite_pair(uint32_t w)
     return w;
 }
 
+// Values of new tokens that are not finite were cleared from V: adds those at positions
+// [y0, y1] to a row of the output, or of a partial.
+template <int D>
+__device__ __noinline__ void add_cleared(const ChunkArgs &a, const Item &it, int head, int y0, int y1, uint16_t *out,
+                                         float4 *part)
+{
+    for (int y = y0; y <= y1; ++y) {
+        const int32_t id = a.bt[(int64_t)it.seq * a.bt_stride + y / kBlk];
+        if (id < 0 || id >= a.num_blocks) continue;
+        const uint16_t *v = a.v + id * a.block_stride + head * a.head_stride + (int64_t)(y % kBlk) * D;
+#pragma unroll 1
+        for (int d = 0; d < D; ++d) {
+            const uint32_t b = v[d];
+            if ((b & 0x7f80u) != 0x7f80u) continue;
+            const float f = __uint_as_float(b << 16);
+            if (out) {
+                out[d] = (uint16_t)bf16x2(__uint_as_float((uint32_t)out[d] << 16) + f, 0.f);
+            } else {
+                float *q = reinterpret_cast<float *>(part + d / 4 * 256) + d % 4;
+                *q += f;
+            }
+        }
+    }
+}
+
 // The MMAs of query tile X, issued by one thread: of this warp alone, as an issue takes
 // a thread about 40 clocks and the tensor cores 64, so that one thread for both tiles
 // would set the pace.  The warps of both tiles walk every K and V tile in ring order (one
@@ -659,7 +687,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(smem_u32(&sh->turn[x]), 1);
             mbar_init(smem_u32(&sh->done[x]), 1);
         }
-        sh->abort = 0;
+        sh->abort = sh->fixed = 0;
         for (int i = 0; i < 4; ++i) sh->odd_values[i] = 0;
         fence_mbarrier_init();
     }
@@ -744,67 +772,80 @@ __global__ void __launch_bounds__(kThreads, 1)
             mma_warp<D, 0>(smem_u32(qbuf), smem_u32(ring), sh, a);
         } else if (warp == kWarpMma + 1) {
             mma_warp<D, 1>(smem_u32(qbuf), smem_u32(ring), sh, a);
-        } else if (warp == kWarpQ) {
-            // ---------------- query tiles, and the edge tiles of V
+        } else {
+            // ---------------- query tiles (warp 12), and the edge tiles of V (warps 12-15, a
+            // quarter of the rows each: the products wait for them)
             Walk<true> w(a);
             Piece p;
             uint32_t k0 = 0, np = 0, ne = 0;
             bool ok = true;
             for (; ok && !a.stall && w.step(p); ++np) {
-                ok = __all_sync(0xffffffffu, cwait(smem_u32(&sh->q_empty), (np & 1) ^ 1, sh, a));
-                if (!ok) break;
-                if (lane == 0) {
-                    const int tiles = p.it.ntok > a.TQ ? 2 : 1;
-                    const uint32_t fb = smem_u32(&sh->q_full);
-                    mbar_arrive_expect_tx(fb, tiles * C::kHalves * qrows * 128);
-                    for (int x = 0; x < tiles; ++x)
+                if (warp == kWarpQ) {
+                    ok = __all_sync(0xffffffffu, cwait<200>(smem_u32(&sh->q_empty), (np & 1) ^ 1, sh, a));
+                    if (!ok) break;
+                    if (lane == 0) {
+                        const int tiles = p.it.ntok > a.TQ ? 2 : 1;
+                        const uint32_t fb = smem_u32(&sh->q_full);
+                        mbar_arrive_expect_tx(fb, tiles * C::kHalves * qrows * 128);
+                        for (int x = 0; x < tiles; ++x)
 #pragma unroll
-                        for (int h = 0; h < C::kHalves; ++h)
-                            asm volatile(
-                                "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
-                                "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_u32(qbuf + x * C::kTileBytes +
-                                                                                 h * C::kHalfBytes)),
-                                "l"(reinterpret_cast<uint64_t>(&qmap)), "r"(h * 64), "r"(p.head * a.G),
-                                "r"(p.it.row0 + x * a.TQ), "r"(fb)
-                                : "memory");
+                            for (int h = 0; h < C::kHalves; ++h)
+                                asm volatile(
+                                    "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+                                    "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
+                                        smem_u32(qbuf + x * C::kTileBytes + h * C::kHalfBytes)),
+                                    "l"(reinterpret_cast<uint64_t>(&qmap)), "r"(h * 64), "r"(p.head * a.G),
+                                    "r"(p.it.row0 + x * a.TQ), "r"(fb)
+                                    : "memory");
+                    }
+                    __syncwarp();
                 }
-                __syncwarp();
                 for (int j = max(p.j0, (p.it.pos0 + 1) / kTile); ok && j < p.j1; ++j) {
                     if (!edge_tile(p.it, j)) continue;
-                    const uint32_t k = k0 + 2 * (j - p.j0) + 1;
-                    ok = __all_sync(0xffffffffu, cwait(smem_u32(&sh->edge[ne & 3]), (ne >> 2) & 1, sh, a));
+                    const uint32_t st = (k0 + 2 * (j - p.j0) + 1) % kStages;
+                    ok = __all_sync(0xffffffffu, cwait<200>(smem_u32(&sh->edge[ne & 3]), (ne >> 2) & 1, sh, a));
                     if (!ok) break;
                     ++ne;
                     const int end = min(p.it.len - j * kTile, kTile);     // rows from here on: past the sequence
                     const int r0 = max(0, min(end, p.it.pos0 + 1 - j * kTile));  // rows from here on: new tokens
                     const int r1 = (end + kBlk - 1) / kBlk * kBlk;        // rows from here on are zeros already
-                    bool odd = false;
+                    const int part = (warp - kWarpQ) * 32 + lane;
+                    uint32_t top = 0;  // largest magnitude, as integers: infinities and NaNs are 0x7f80 and up
 #pragma unroll
                     for (int h = 0; h < C::kHalves; ++h) {
-                        uint4 *t = reinterpret_cast<uint4 *>(ring + (k % kStages) * C::kTileBytes + h * C::kHalfBytes);
+                        uint4 *t = reinterpret_cast<uint4 *>(ring + st * C::kTileBytes + h * C::kHalfBytes);
 #pragma unroll 4
-                        for (int e = r0 * 8 + lane; e < end * 8; e += 32) {
+                        for (int e = r0 * 8 + part; e < end * 8; e += 128) {
                             const uint4 v = t[e];
-                            const uint4 f = make_uint4(finite_pair(v.x), finite_pair(v.y), finite_pair(v.z),
-                                                       finite_pair(v.w));
-                            if (f.x != v.x || f.y != v.y || f.z != v.z || f.w != v.w) {
-                                t[e] = f;
-                                odd = true;
+                            top = __vmaxu2(top, __vmaxu2(__vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu),
+                                                         __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu)));
+                        }
+                        for (int e = end * 8 + part; e < r1 * 8; e += 128) t[e] = make_uint4(0, 0, 0, 0);
+                    }
+                    if ((top & 0xffffu) >= 0x7f80u || top >= 0x7f800000u) {
+                        for (int h = 0; h < C::kHalves; ++h) {
+                            uint4 *t = reinterpret_cast<uint4 *>(ring + st * C::kTileBytes + h * C::kHalfBytes);
+                            for (int e = r0 * 8 + part; e < end * 8; e += 128) {
+                                const uint4 v = t[e];
+                                t[e] = make_uint4(finite_pair(v.x), finite_pair(v.y), finite_pair(v.z),
+                                                  finite_pair(v.w));
                             }
                         }
-                        for (int e = end * 8 + lane; e < r1 * 8; e += 32) t[e] = make_uint4(0, 0, 0, 0);
+                        sh->odd_values[np & 3] = (int32_t)np + 1;
                     }
-                    odd = __any_sync(0xffffffffu, odd);
-                    if (odd && lane == 0) sh->odd_values[np & 3] = (int32_t)np + 1;
                     __threadfence_block();
                     fence_proxy_async_smem();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(smem_u32(&sh->full[k % kStages]));
+                    // the last of the four warps hands the tile over
+                    if (lane == 0 && (atomicAdd(&sh->fixed, 1) & 3) == 3) {
+                        __threadfence_block();
+                        mbar_arrive(smem_u32(&sh->full[st]));
+                    }
                 }
                 k0 += 2 * (p.j1 - p.j0);
             }
             // the last query tiles have landed too
-            if (np > 0) drain(smem_u32(&sh->q_full), (np - 1) & 1);
+            if (warp == kWarpQ && np > 0) drain(smem_u32(&sh->q_full), (np - 1) & 1);
         }
     } else {
         // ---------------- softmax: thread = one row of query tile x
@@ -933,7 +974,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const bool add = *(volatile int32_t *)&sh->odd_values[np & 3] == (int32_t)np + 1;
                 float4 *pp = a.part + (int64_t)p.slot * (D / 4) * 256 + rr;  // dims d..d+3 at pp[d / 4 * 256]
                 uint16_t *op = a.out + (row * a.hq + p.head * a.G + hd) * D;
-#pragma unroll
+#pragma unroll 1  // one copy: it runs once an item, out of a cold instruction cache
                 for (int c = 0; c < D; c += 32) {
                     uint32_t o[32];
                     tmem_ld32(to + c, o, 0);
@@ -949,21 +990,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                             o[e] = __float_as_uint(fmaf(__uint_as_float(o1[e]), f1, __uint_as_float(o[e])));
                     }
                     if (!live) continue;
-                    if (add) {
-                        // values of new tokens that are not finite were cleared from V: every row that sees one gets it
-                        for (int32_t y = max(p.it.pos0 + 1, p.j0 * kTile); y <= min(pos, p.j1 * kTile - 1); ++y) {
-                            const int32_t id = a.bt[(int64_t)p.it.seq * a.bt_stride + y / kBlk];
-                            if (id < 0 || id >= a.num_blocks) continue;
-                            const uint16_t *vr = a.v + id * a.block_stride + p.head * a.head_stride +
-                                                 (int64_t)(y % kBlk) * D + c;
-#pragma unroll
-                            for (int e = 0; e < 32; ++e) {
-                                const uint32_t b = vr[e];
-                                if ((b & 0x7f80u) == 0x7f80u)
-                                    o[e] = __float_as_uint(__uint_as_float(o[e]) + __uint_as_float(b << 16));
-                            }
-                        }
-                    }
                     if (p.whole) {
                         // a warp's store touches 32 rows: as few and as wide as the alignment allows
                         uint32_t b[16];
@@ -986,6 +1012,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                                                                 __uint_as_float(o[e + 2]), __uint_as_float(o[e + 3]));
                     }
                 }
+                if (add && live) add_cleared<D>(a, p.it, p.head, max(p.it.pos0 + 1, p.j0 * kTile),
+                                                min(pos, p.j1 * kTile - 1), p.whole ? op : nullptr, pp);
                 if (live && !p.whole) a.stat[(int64_t)p.slot * 256 + rr] = make_float2(m, z);
             }
             // the next piece's products write O again only after these reads
