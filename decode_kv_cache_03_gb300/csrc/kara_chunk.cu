@@ -43,7 +43,9 @@
 // per query tile and one loading warp each for K and V (issuing a 2 KB copy takes about
 // 90 clocks: one warp took 2900 clocks for the K and V tiles that two query tiles multiply
 // in 2048), the two tiles taking turns, 1595; the turn taken before the weights are
-// waited for, 1485.
+// waited for, 1485; cuts by cost, 1455; waits that nap in the warps that have time, 1435;
+// and the instruction caches: one copy of the epilogue's code and the control warps'
+// waiting out of line, 1390 (512 tokens x 32 sequences at 4096 keys: 852 -> 763).
 //
 // Three launches: the plan (one CTA: checks, items and cuts), the attention
 // (persistent, one CTA per SM) and the merge, programmatic dependents of each
@@ -289,7 +291,7 @@ struct Shared {
     uint64_t done[2];
     uint32_t tmem;
     int32_t abort;
-    int32_t fixed;        // edge tiles' quarters cleaned
+    int32_t fixed[4];     // quarters of an edge tile cleaned (by the tile's number mod 4; one warp may be a tile ahead)
     int32_t odd_values[4];  // 1 + the last piece (by its number mod 4) whose V had values that are not finite
     float2 stat[kTile];   // (max, sum) of the odd key tiles, for joining a single query tile
 };
@@ -324,6 +326,20 @@ __device__ __forceinline__ bool cwait(uint32_t bar, uint32_t parity, Shared *sh,
             }
         }
     }
+}
+
+// The same for the control warps, whose code has to stay small beside the softmax's in the
+// instruction caches: the waiting itself is out of line.
+template <int NAP>
+__device__ __noinline__ bool kwait_on(uint32_t bar, uint32_t parity, Shared *sh, const ChunkArgs &a)
+{
+    return cwait<NAP>(bar, parity, sh, a);
+}
+
+template <int NAP = 0>
+__device__ __forceinline__ bool kwait(uint32_t bar, uint32_t parity, Shared *sh, const ChunkArgs &a)
+{
+    return mbar_try_wait(bar, parity) || kwait_on<NAP>(bar, parity, sh, a);
 }
 
 // Wait for work in flight that has to land whatever happened: by time alone.
@@ -579,7 +595,7 @@ __device__ __forceinline__ void mma_warp(uint32_t qbuf, uint32_t ring, Shared *s
             if (st >= kStages) st -= kStages, ph ^= 1;
         };
         auto skip = [&](uint32_t &st, uint32_t &ph) {
-            ok = ok && cwait(full0 + st * 8, ph, sh, a);
+            ok = ok && kwait(full0 + st * 8, ph, sh, a);
             mbar_arrive(empty0 + st * 8);
             next(st, ph);
         };
@@ -588,7 +604,7 @@ __device__ __forceinline__ void mma_warp(uint32_t qbuf, uint32_t ring, Shared *s
             const int n = p.j1 - p.j0, cnt = part_of(p, X, a.TQ).cnt;
             const int by = two ? 1 : 2, first = two ? 0 : X, last = first + (cnt - 1) * by;
             const uint32_t ql = (uint32_t)qd + (two && X ? kTileDesc : 0);
-            ok = cwait(smem_u32(&sh->q_full), iq & 1, sh, a);
+            ok = kwait(smem_u32(&sh->q_full), iq & 1, sh, a);
             iq ^= 1;
             if (ok && cnt == 0) mbar_arrive(smem_u32(&sh->q_empty));
             for (int t = first - by; ok && t < n; t += by) {
@@ -597,10 +613,10 @@ __device__ __forceinline__ void mma_warp(uint32_t qbuf, uint32_t ring, Shared *s
                 const bool sum = t >= first && t <= last, logits = t + by <= last;
                 if (!two && X == 1 && t >= 0) skip(vs, vp);
                 if (t >= first && t < n) {
-                    ok = ok && cwait(full0 + vs * 8, vp, sh, a);
-                    if (two && ok && t + 1 < n) ok = cwait(full0 + ks * 8, kp, sh, a);
-                    if (two && ok) ok = cwait(mine, turn, sh, a);
-                    if (ok && sum) ok = cwait(pf, pp, sh, a);
+                    ok = ok && kwait(full0 + vs * 8, vp, sh, a);
+                    if (two && ok && t + 1 < n) ok = kwait(full0 + ks * 8, kp, sh, a);
+                    if (two && ok) ok = kwait(mine, turn, sh, a);
+                    if (ok && sum) ok = kwait(pf, pp, sh, a);
                     if (!ok) break;
                     if (sum) {
                         pp ^= 1;
@@ -620,7 +636,7 @@ __device__ __forceinline__ void mma_warp(uint32_t qbuf, uint32_t ring, Shared *s
                 if (!two && X == 0 && t >= 0 && t + 1 < n) skip(vs, vp);
                 if (!two && X == 1 && t + 1 < n) skip(ks, kp);
                 if (t + by < n) {
-                    if (!two || t < first) ok = ok && cwait(full0 + ks * 8, kp, sh, a);
+                    if (!two || t < first) ok = ok && kwait(full0 + ks * 8, kp, sh, a);
                     if (!ok) break;
                     if (logits) {
                         const uint32_t lo = (uint32_t)kd + ks * kTileDesc;
@@ -687,8 +703,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(smem_u32(&sh->turn[x]), 1);
             mbar_init(smem_u32(&sh->done[x]), 1);
         }
-        sh->abort = sh->fixed = 0;
-        for (int i = 0; i < 4; ++i) sh->odd_values[i] = 0;
+        sh->abort = 0;
+        for (int i = 0; i < 4; ++i) sh->odd_values[i] = sh->fixed[i] = 0;
         fence_mbarrier_init();
     }
     // rows of the query tiles past G * TQ are never filled: zeros
@@ -743,7 +759,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int j = p.j0; j < p.j1; ++j) {
                     const int32_t cur = id;
                     if (j + 1 < p.j1) id = block_id(j + 1);
-                    ok = __all_sync(0xffffffffu, cwait(smem_u32(&sh->empty[st]), ph, sh, a));
+                    ok = __all_sync(0xffffffffu, kwait(smem_u32(&sh->empty[st]), ph, sh, a));
                     if (!ok) break;
                     const bool edge = kv && edge_tile(p.it, j);
                     const uint32_t fb = smem_u32(edge ? &sh->edge[ne & 3] : &sh->full[st]);
@@ -781,7 +797,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             bool ok = true;
             for (; ok && !a.stall && w.step(p); ++np) {
                 if (warp == kWarpQ) {
-                    ok = __all_sync(0xffffffffu, cwait<200>(smem_u32(&sh->q_empty), (np & 1) ^ 1, sh, a));
+                    ok = __all_sync(0xffffffffu, kwait<200>(smem_u32(&sh->q_empty), (np & 1) ^ 1, sh, a));
                     if (!ok) break;
                     if (lane == 0) {
                         const int tiles = p.it.ntok > a.TQ ? 2 : 1;
@@ -803,9 +819,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int j = max(p.j0, (p.it.pos0 + 1) / kTile); ok && j < p.j1; ++j) {
                     if (!edge_tile(p.it, j)) continue;
                     const uint32_t st = (k0 + 2 * (j - p.j0) + 1) % kStages;
-                    ok = __all_sync(0xffffffffu, cwait<200>(smem_u32(&sh->edge[ne & 3]), (ne >> 2) & 1, sh, a));
+                    ok = __all_sync(0xffffffffu, kwait<200>(smem_u32(&sh->edge[ne & 3]), (ne >> 2) & 1, sh, a));
                     if (!ok) break;
-                    ++ne;
                     const int end = min(p.it.len - j * kTile, kTile);     // rows from here on: past the sequence
                     const int r0 = max(0, min(end, p.it.pos0 + 1 - j * kTile));  // rows from here on: new tokens
                     const int r1 = (end + kBlk - 1) / kBlk * kBlk;        // rows from here on are zeros already
@@ -837,10 +852,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                     fence_proxy_async_smem();
                     __syncwarp();
                     // the last of the four warps hands the tile over
-                    if (lane == 0 && (atomicAdd(&sh->fixed, 1) & 3) == 3) {
+                    if (lane == 0 && (atomicAdd(&sh->fixed[ne & 3], 1) & 3) == 3) {
                         __threadfence_block();
                         mbar_arrive(smem_u32(&sh->full[st]));
                     }
+                    ++ne;
                 }
                 k0 += 2 * (p.j1 - p.j0);
             }
@@ -881,7 +897,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int c = 0; c < 4; ++c) tmem_wait_ld32(s, c * 32);
                     const int lim = pos - j * kTile;  // last key of the tile that the row sees
-                    if (__any_sync(0xffffffffu, lim < kTile - 1)) {
+                    if (__builtin_expect(__any_sync(0xffffffffu, lim < kTile - 1), 0)) {
 #pragma unroll
                         for (int c = 0; c < kTile; ++c)
                             if (c > lim) s[c] = 0xff800000u;
@@ -897,7 +913,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         m = mt;
                     } else {
                         const bool grew = mt > m + kLazy;
-                        if (__any_sync(0xffffffffu, grew)) {
+                        if (__builtin_expect(__any_sync(0xffffffffu, grew), 0)) {
                             const float f = grew ? ex2(m - mt) : 1.f;
                             if (grew) m = mt;
                             z *= f;

@@ -844,3 +844,19 @@ def test_append_long_call_reports_bad_rows_and_stalls(monkeypatch):
         assert (got[1234] == 5.0).all()
         keep = np.arange(rows) != 1234
         assert torch.equal(got[keep], good[keep])
+
+
+def test_chunk_edge_tiles_again_and_again():
+    """Many items with two and three edge tiles in a row (ragged ends, chunks across tile borders): the
+    warps that clear them may be a tile apart."""
+    kara = lib()
+    r = np.random.default_rng(5)
+    n_new = r.integers(100, 400, 12).astype(np.int32)
+    lengths = n_new + r.integers(0, 200, 12).astype(np.int32)
+    d = chunk_inputs(96, lengths, n_new, 8, 2, 128)
+    first, st = run_chunk(kara, d)
+    assert st == 0
+    check_chunk(d, first)
+    for _ in range(30):
+        got, st = run_chunk(kara, d)
+        assert st == 0 and torch.equal(got, first)
