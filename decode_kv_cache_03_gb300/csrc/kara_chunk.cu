@@ -43,9 +43,7 @@
 // per query tile and one loading warp each for K and V (issuing a 2 KB copy takes about
 // 90 clocks: one warp took 2900 clocks for the K and V tiles that two query tiles multiply
 // in 2048), the two tiles taking turns, 1595; the turn taken before the weights are
-// waited for, 1485; cuts by cost, 1455; waits that nap in the warps that have time, 1435;
-// and the instruction caches: one copy of the epilogue's code and the control warps'
-// waiting out of line, 1390 (512 tokens x 32 sequences at 4096 keys: 852 -> 763).
+// waited for, 1485.
 //
 // Three launches: the plan (one CTA: checks, items and cuts), the attention
 // (persistent, one CTA per SM) and the merge, programmatic dependents of each
@@ -282,7 +280,7 @@ struct Shared {
     uint64_t full[kStages], empty[kStages];  // K / V tiles
     uint64_t q_full, q_empty;
     uint64_t s_full[2];   // logits of a query tile are in TMEM (and its earlier products are done)
-    uint64_t p_full[2];   // its weights are in TMEM
+    uint64_t p_half[2], p_full[2];
     uint64_t o_full[2];   // its last product is done
     uint64_t x_full, x_free;  // a single query tile's odd half is ready to be joined; is joined
     uint64_t edge[4];     // an edge tile of V has landed (by their number mod 4: the ring holds at most three);
@@ -583,7 +581,7 @@ __device__ __forceinline__ void mma_warp(uint32_t qbuf, uint32_t ring, Shared *s
         constexpr uint32_t ts = X * kTile, to = 256 + X * 128;         // S (and P over it), O in TMEM
         const uint64_t qd = sdesc_sw128(qbuf), kd = sdesc_sw128(ring), vd = sdesc_sw128_mn(ring, C::kHalfBytes);
         const uint32_t full0 = smem_u32(&sh->full[0]), empty0 = smem_u32(&sh->empty[0]);
-        const uint32_t sf = smem_u32(&sh->s_full[X]), pf = smem_u32(&sh->p_full[X]);
+        const uint32_t sf = smem_u32(&sh->s_full[X]), pf = smem_u32(&sh->p_full[X]), ph = smem_u32(&sh->p_half[X]);
         const uint32_t mine = smem_u32(&sh->turn[X]), other = smem_u32(&sh->turn[1 - X]);
         Walk<true> w(a);
         Piece p;
@@ -616,15 +614,21 @@ __device__ __forceinline__ void mma_warp(uint32_t qbuf, uint32_t ring, Shared *s
                     ok = ok && kwait(full0 + vs * 8, vp, sh, a);
                     if (two && ok && t + 1 < n) ok = kwait(full0 + ks * 8, kp, sh, a);
                     if (two && ok) ok = kwait(mine, turn, sh, a);
-                    if (ok && sum) ok = kwait(pf, pp, sh, a);
+                    if (ok && sum) ok = kwait(ph, pp, sh, a);
                     if (!ok) break;
                     if (sum) {
-                        pp ^= 1;
                         tc_fence_after();
                         const uint32_t lo = (uint32_t)vd + vs * kTileDesc;
 #pragma unroll
-                        for (int e = 0; e < kTile / 16; ++e)
+                        for (int e = 0; e < kTile / 32; ++e)
                             mma_ts(to, ts + e * 8, lo + e * 128, (uint32_t)(vd >> 32), id_pv, e > 0 || t != first);
+                        ok = kwait(pf, pp, sh, a);
+                        if (!ok) break;
+                        pp ^= 1;
+                        tc_fence_after();
+#pragma unroll
+                        for (int e = kTile / 32; e < kTile / 16; ++e)
+                            mma_ts(to, ts + e * 8, lo + e * 128, (uint32_t)(vd >> 32), id_pv, 1);
                         if (!two) mma_commit(empty0 + vs * 8);
                         if (t == last) mma_commit(smem_u32(&sh->o_full[X]));
                     } else {
@@ -693,6 +697,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init(smem_u32(&sh->q_empty), 2);
         for (int x = 0; x < 2; ++x) {
             mbar_init(smem_u32(&sh->s_full[x]), 1);
+            mbar_init(smem_u32(&sh->p_half[x]), 4);
             mbar_init(smem_u32(&sh->p_full[x]), 4);
             mbar_init(smem_u32(&sh->o_full[x]), 1);
         }
@@ -940,8 +945,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                         hi = ex2(hi);
                         sum[(c >> 1) & 1] = add2(sum[(c >> 1) & 1], pack2(lo, hi));
                         s[c >> 1] = bf16x2(lo, hi);
+                        if (c == 62) {
+                            tmem_st32(ts, s, 0);
+                            tmem_wait_st();
+                            tc_fence_before();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(smem_u32(&sh->p_half[x]));
+                        }
                     }
-                    tmem_st32(ts, s, 0);
                     tmem_st32(ts + 32, s, 32);
                     float s0, s1;
                     unpack2(add2(sum[0], sum[1]), s0, s1);
@@ -950,6 +961,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tc_fence_before();
                 }
                 __syncwarp();
+                if (!any && lane == 0) mbar_arrive(smem_u32(&sh->p_half[x]));
                 if (lane == 0) mbar_arrive(smem_u32(&sh->p_full[x]));
             }
             if (ok && pt.cnt > 0) {
