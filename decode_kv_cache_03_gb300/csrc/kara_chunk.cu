@@ -43,7 +43,14 @@
 // per query tile and one loading warp each for K and V (issuing a 2 KB copy takes about
 // 90 clocks: one warp took 2900 clocks for the K and V tiles that two query tiles multiply
 // in 2048), the two tiles taking turns, 1595; the turn taken before the weights are
-// waited for, 1485.
+// waited for, 1485; cuts by cost, 1455; waits that nap in the warps that have time, 1435;
+// the instruction caches (one copy of the epilogue's code, the control warps' waiting out
+// of line), 1390 (512 tokens x 32 sequences at 4096 keys: 852 -> 763); the weighted sum
+// begun on half the weights, 1340 (1.54 PFLOP/s, 0.81 of the measured cuBLAS burst).  What
+// is left: a step of two query tiles takes about 2950 clocks against 2048 of tensor time
+// (logits, exponentials and weighted sum of a tile depend on each other, and TMEM holds
+// one S per tile beside O), and the power limit: under back-to-back calls the clock falls
+// to 1.5 - 1.8 GHz.
 //
 // Three launches: the plan (one CTA: checks, items and cuts), the attention
 // (persistent, one CTA per SM) and the merge, programmatic dependents of each
@@ -133,10 +140,11 @@ __device__ __forceinline__ bool chunk_ok(const ChunkArgs &a, int32_t r0, int32_t
     return r0 >= 0 && r1 >= r0 && r1 <= a.rows && L >= r1 - r0 && ((int64_t)L + kBlk - 1) / kBlk <= a.bt_stride;
 }
 
-// What a key tile and an item cost a CTA, about 1700 clocks each: two query tiles take
-// 3400 clocks a key tile, one takes 1700; an item's start and end about 7000.
-__device__ __forceinline__ int tile_cost(const ChunkArgs &a, int32_t ntok) { return ntok > a.TQ ? 2 : 1; }
-constexpr int kItemCost = 4;
+// What a key tile and an item cost a CTA, in about 800 clocks: a key tile of two query tiles
+// 3000 to 3400, of one 2500, an item's start and end about 6500.  (Two to one for the tiles: the
+// mixed batch of decodes and chunks takes 358 us, four to three 338.)
+__device__ __forceinline__ int tile_cost(const ChunkArgs &a, int32_t ntok) { return ntok > a.TQ ? 4 : 3; }
+constexpr int kItemCost = 8;
 constexpr int kTilesPerCta = 2;  // fewer, and CTAs stay without work: a split costs a merge
 
 // ---- plan --------------------------------------------------------------------
