@@ -44,17 +44,16 @@
 // 90 clocks: one warp took 2900 clocks for the K and V tiles that two query tiles multiply
 // in 2048), the two tiles taking turns, 1595; the turn taken before the weights are
 // waited for, 1485; cuts by cost, 1455; waits that nap in the warps that have time, 1435;
-// the instruction caches (one copy of the epilogue's code, the control warps' waiting out
-// of line), 1390 (512 tokens x 32 sequences at 4096 keys: 852 -> 763); the weighted sum
+// the instruction caches (one copy of the epilogue's code and of the MMAs', the control warps'
+// waiting out of line, one warp that walks over the work and tells the others), 1390 (512 tokens x 32 sequences at 4096 keys: 852 -> 763); the weighted sum
 // begun on half the weights, 1340 (1.54 PFLOP/s, 0.81 of the measured cuBLAS burst).  What
 // is left: a step of two query tiles takes about 2950 clocks against 2048 of tensor time
 // (logits, exponentials and weighted sum of a tile depend on each other, and TMEM holds
 // one S per tile beside O), and the power limit: under back-to-back calls the clock falls
 // to 1.5 - 1.8 GHz.
 //
-// Three launches: the plan (one CTA: checks, items and cuts), the attention
-// (persistent, one CTA per SM) and the merge, programmatic dependents of each
-// other.
+// Two launches: the attention (persistent, one CTA per SM, each of which works out
+// its own range) and the merge, programmatic dependents of what precedes them.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -86,46 +85,37 @@ static_assert(256 * kRegsSoft + 256 * kRegsCtl == kThreads * kRegsLaunch, "regis
 constexpr uint32_t kTmemCols = 512;  // S0 S1 (128 columns each), O0 O1 (128 each)
 constexpr float kLazy = 8.f;         // see above: rescale when the maximum grew by more than 2^8
 constexpr uint64_t kTimeoutNs = 1000000000ull;
-constexpr int kPlanThreads = 1024;
-constexpr int kPlanCap = 2048;       // sequences / items whose prefix sums the plan keeps in shared memory
 
 // One or two query tiles of a sequence (all KV heads have the same items).
-struct __align__(16) Item {
+struct Item {
     int32_t row0;   // first row of q
     int32_t ntok;   // tokens, <= 2 TQ
     int32_t pos0;   // position of the first token
     int32_t nt;     // key tiles that its last token sees
-    int32_t seq;
     int32_t len;    // cached length of the sequence
-    int64_t before; // cost of the items before this one
+    int32_t m;      // new tokens of the sequence; 0: it has no items
 };
 
-// Where a CTA starts, and the one before it ends: key tile `off` of item `item` for KV
-// head `head` (the end of everything: head hkv, item 0).
+// Where a CTA starts, and the one before it ends: key tile `off` of the item of tokens 2 TQ
+// `pair` on of sequence `seq` for KV head `head` (off == nt: behind its last one; the end of
+// everything: head hkv).
 struct __align__(16) Start {
-    int32_t head, item, off, pad;
+    int32_t head, seq, pair, off;
 };
 
 __device__ __forceinline__ bool same_item(const Start &a, const Start &b)
 {
-    return a.head == b.head && a.item == b.item;
+    return a.head == b.head && a.seq == b.seq && a.pair == b.pair;
 }
-
-struct PlanHead {
-    int32_t items;
-    int32_t ctas;     // CTAs that get work
-};
 
 struct ChunkArgs {
     const int32_t *q_start, *len, *bt;
     int32_t *err;
-    int32_t n, rows, bt_stride, num_blocks, layer, hq, hkv, D, G, TQ, ctas, cap_items;
+    int32_t n, rows, bt_stride, num_blocks, layer, hq, hkv, D, G, TQ, ctas;
     float scale2;     // log2(e) / sqrt(D)
     uint16_t *out;
-    PlanHead *head;
-    Start *start;     // [ctas + 1]
-    Item *items;      // [cap_items]
-    int32_t *seq_items;  // [n + 1]: items before each sequence
+    int32_t *used_ctas;  // CTAs that got work
+    Start *start;        // [used_ctas + 1]
     float4 *part;     // [2 * ctas][D / 4][256]
     float2 *stat;     // [2 * ctas][256]: (max, sum) in the log2 domain
     const uint16_t *v;   // V pool at the call's layer
@@ -147,143 +137,24 @@ __device__ __forceinline__ int tile_cost(const ChunkArgs &a, int32_t ntok) { ret
 constexpr int kItemCost = 8;
 constexpr int kTilesPerCta = 2;  // fewer, and CTAs stay without work: a split costs a merge
 
-// ---- plan --------------------------------------------------------------------
-__device__ int64_t plan_scan(int64_t v, int64_t *scratch /* 33 */, int64_t *tot)
+// The item `pair` of sequence `seq`.
+__device__ __forceinline__ Item make_item(const ChunkArgs &a, int seq, int pair)
 {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    int64_t in = v;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int64_t x = __shfl_up_sync(0xffffffffu, in, o);
-        if (lane >= o) in += x;
-    }
-    if (lane == 31) scratch[warp] = in;
-    __syncthreads();
-    if (warp == 0) {
-        const int64_t own = scratch[lane];
-        int64_t w = own;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int64_t x = __shfl_up_sync(0xffffffffu, w, o);
-            if (lane >= o) w += x;
-        }
-        scratch[lane] = w - own;
-        if (lane == 31) scratch[32] = w;
-    }
-    __syncthreads();
-    const int64_t r = scratch[warp] + in - v;
-    *tot = scratch[32];
-    __syncthreads();
-    return r;
-}
-
-// Last index i in [0, n) with f(i) <= x, for f increasing and f(0) <= x.
-template <class F>
-__device__ __forceinline__ int last_at_most(int n, int64_t x, F f)
-{
-    int lo = 0, hi = n;
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (f(mid) <= x) lo = mid; else hi = mid;
-    }
-    return lo;
-}
-
-__global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const ChunkArgs a)
-{
-    __shared__ int64_t scratch[33];
-    __shared__ int32_t seq_s[kPlanCap];  // items before each sequence
-    __shared__ int64_t item_s[kPlanCap]; // cost of the items before each item
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int tid = threadIdx.x;
-    const int per = 2 * a.TQ;  // tokens of an item
-    int64_t items = 0;
-    for (int base = 0; base < a.n; base += kPlanThreads) {
-        const int s = base + tid;
-        int64_t v = 0;
-        if (s < a.n) {
-            const int32_t r0 = a.q_start[s], r1 = a.q_start[s + 1], L = a.len[s];
-            if (chunk_ok(a, r0, r1, L)) {
-                v = (r1 - r0 + per - 1) / per;
-            } else {
-                set_err(a.err, KARA_EINVAL);
-                const int64_t lo = max(r0, 0), hi = min(r1, a.rows);
-                uint32_t *o = reinterpret_cast<uint32_t *>(a.out);
-                const int64_t words = (int64_t)a.hq * a.D / 2;
-                for (int64_t i = lo * words; i < hi * words; ++i) o[i] = 0u;
-            }
-        }
-        int64_t tot;
-        const int64_t ex = items + plan_scan(v, scratch, &tot);
-        if (s < a.n) {
-            if (s < kPlanCap) seq_s[s] = (int32_t)min(ex, (int64_t)a.cap_items);
-            a.seq_items[s] = (int32_t)min(ex, (int64_t)a.cap_items);
-        }
-        items += tot;
-    }
-    // overlapping rows of a broken q_start could ask for more items than rows allow
-    items = min(items, (int64_t)a.cap_items);
-    __syncthreads();
-    int64_t cost = 0, tiles = 0;
-    for (int64_t base = 0; base < items; base += kPlanThreads) {
-        const int64_t i = base + tid;
-        Item it;
-        it.nt = 0;
-        int64_t c = 0;
-        if (i < items) {
-            const int s = a.n <= kPlanCap ? last_at_most(a.n, i, [&](int x) { return (int64_t)seq_s[x]; })
-                                          : last_at_most(a.n, i, [&](int x) { return (int64_t)a.seq_items[x]; });
-            const int32_t r0 = a.q_start[s], m = a.q_start[s + 1] - r0;
-            const int32_t t0 = (int32_t)(i - (a.n <= kPlanCap ? seq_s[s] : a.seq_items[s])) * per;
-            it.seq = s;
-            it.len = a.len[s];
-            it.row0 = r0 + t0;
-            it.ntok = min(per, m - t0);
-            it.pos0 = it.len - m + t0;
-            it.nt = (it.pos0 + it.ntok - 1) / kTile + 1;
-            c = (int64_t)it.nt * tile_cost(a, it.ntok) + kItemCost;
-        }
-        int64_t tot;
-        it.before = cost + plan_scan(c, scratch, &tot);
-        if (i < items) {
-            if (i < kPlanCap) item_s[i] = it.before;
-            a.items[i] = it;
-        }
-        cost += tot;
-        plan_scan(it.nt, scratch, &tot);
-        tiles += tot;
-    }
-    __syncthreads();
-    const int64_t units = cost * a.hkv;
-    const int ctas = (int)max((int64_t)(items > 0), min((int64_t)a.ctas, tiles * a.hkv / kTilesPerCta));
-    for (int c = tid; c <= ctas; c += kPlanThreads) {
-        Start st;
-        st.head = a.hkv, st.item = st.off = st.pad = 0;
-        if (c < ctas) {
-            // the tile that the cut falls into, or the next item if it falls behind the last one
-            const int64_t u = units * c / ctas, r = u % cost;
-            const int i = items <= kPlanCap
-                              ? last_at_most((int)items, r, [&](int x) { return item_s[x]; })
-                              : last_at_most((int)items, r, [&](int x) { return a.items[x].before; });
-            const Item it = a.items[i];
-            st.head = (int32_t)(u / cost);
-            st.item = i;
-            st.off = (int32_t)((r - it.before) / tile_cost(a, it.ntok));
-            if (st.off >= it.nt) {
-                st.off = 0;
-                if (++st.item == items) st.item = 0, ++st.head;
-            }
-        }
-        a.start[c] = st;
-    }
-    if (tid == 0) {
-        a.head->items = (int32_t)items;
-        a.head->ctas = ctas;
-    }
+    Item it;
+    const int32_t r0 = a.q_start[seq], r1 = a.q_start[seq + 1], t0 = pair * 2 * a.TQ;
+    it.len = a.len[seq];
+    it.m = chunk_ok(a, r0, r1, it.len) ? r1 - r0 : 0;
+    it.row0 = r0 + t0;
+    it.ntok = min(2 * a.TQ, it.m - t0);
+    it.pos0 = it.len - it.m + t0;
+    it.nt = (it.pos0 + it.ntok - 1) / kTile + 1;
+    return it;
 }
 
 // ---- attention ------------------------------------------------------------------
+constexpr int kPieces = 4;        // descriptions of pieces under way
+constexpr int kPieceReaders = 15; // warps that read them: softmax 8, V, MMAs 2, edge tiles 4
+
 struct Shared {
     uint64_t full[kStages], empty[kStages];  // K / V tiles
     uint64_t q_full, q_empty;
@@ -299,6 +170,10 @@ struct Shared {
     int32_t abort;
     int32_t fixed[4];     // quarters of an edge tile cleaned (by the tile's number mod 4; one warp may be a tile ahead)
     int32_t odd_values[4];  // 1 + the last piece (by its number mod 4) whose V had values that are not finite
+    Start from, to;       // this CTA's range
+    int4 piece[kPieces][3];                               // pieces of it, by their number mod kPieces
+    uint64_t piece_full[kPieces], piece_empty[kPieces];
+    longlong2 scan[kThreads / 32 + 1];
     float2 stat[kTile];   // (max, sum) of the odd key tiles, for joining a single query tile
 };
 
@@ -463,54 +338,184 @@ __device__ __forceinline__ void st_global_32b(void *p, const uint32_t (&v)[N], c
                  : "memory");
 }
 
-// A CTA's walk over its range of key tiles: piece by piece, the same in every warp.
+// ---- the cut: every CTA works out its own range ---------------------------------------
+// Inclusive scan of two values over the CTA; tot gets the sums.
+__device__ longlong2 cta_scan2(longlong2 v, longlong2 *scratch, longlong2 &tot)
+{
+    constexpr int kWarps = kThreads / 32;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long x = __shfl_up_sync(0xffffffffu, v.x, o), y = __shfl_up_sync(0xffffffffu, v.y, o);
+        if (lane >= o) v.x += x, v.y += y;
+    }
+    if (lane == 31) scratch[warp] = v;
+    __syncthreads();
+    if (warp == 0) {
+        longlong2 w = lane < kWarps ? scratch[lane] : make_longlong2(0, 0);
+        const longlong2 own = w;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long x = __shfl_up_sync(0xffffffffu, w.x, o), y = __shfl_up_sync(0xffffffffu, w.y, o);
+            if (lane >= o) w.x += x, w.y += y;
+        }
+        if (lane < kWarps) scratch[lane] = make_longlong2(w.x - own.x, w.y - own.y);
+        if (lane == kWarps - 1) scratch[kWarps] = w;
+    }
+    __syncthreads();
+    const longlong2 b = scratch[warp];
+    tot = scratch[kWarps];
+    __syncthreads();
+    return make_longlong2(b.x + v.x, b.y + v.y);
+}
+
+// Cost and key tiles of a sequence's items.
+__device__ __forceinline__ longlong2 seq_cost(const ChunkArgs &a, int seq)
+{
+    longlong2 v = make_longlong2(0, 0);
+    Item it = make_item(a, seq, 0);
+    for (int t0 = 0; t0 < it.m; t0 += 2 * a.TQ) {
+        const int32_t ntok = min(2 * a.TQ, it.m - t0), nt = (it.pos0 + t0 + ntok - 1) / kTile + 1;
+        v.x += (int64_t)nt * tile_cost(a, ntok) + kItemCost;
+        v.y += nt;
+    }
+    return v;
+}
+
+// The place at cost r of one head, inside the costs [before, before + its own) of sequence seq.
+__device__ __forceinline__ Start place(const ChunkArgs &a, int head, int seq, int64_t before, int64_t r)
+{
+    Start p;
+    p.head = head, p.seq = seq;
+    for (p.pair = 0;; ++p.pair) {
+        const Item it = make_item(a, seq, p.pair);
+        const int w = tile_cost(a, it.ntok);
+        const int64_t c = (int64_t)it.nt * w + kItemCost;
+        if (r < before + c || (p.pair + 1) * 2 * a.TQ >= it.m) {
+            p.off = (int32_t)min((int64_t)it.nt, (r - before) / w);
+            return p;
+        }
+        before += c;
+    }
+}
+
+// All items' key tiles of all heads, weighted by their cost and laid end to end, are cut into
+// equal ranges; this CTA's goes to sh->from and sh->to (equal: nothing), and to the workspace for
+// the merge.  Prefix sums over the sequences, a thread each (over 512 sequences: in passes, twice
+// over); a plan kernel ahead of this one took 3 us more.
+__device__ void cut_range(const ChunkArgs &a, Shared *sh)
+{
+    const int tid = threadIdx.x, cta = blockIdx.x;
+    const bool one_pass = a.n <= kThreads;
+    longlong2 sum = make_longlong2(0, 0), own = sum, in = sum;
+    if (tid == 0) {
+        sh->from.head = sh->to.head = a.hkv;
+        sh->from.seq = sh->to.seq = sh->from.pair = sh->to.pair = sh->from.off = sh->to.off = 0;
+    }
+    for (int base = 0; base < a.n; base += kThreads) {
+        const int s = base + tid;
+        own = s < a.n ? seq_cost(a, s) : make_longlong2(0, 0);
+        longlong2 tot;
+        in = cta_scan2(own, sh->scan, tot);
+        sum.x += tot.x, sum.y += tot.y;
+    }
+    const int64_t units = sum.x * a.hkv;
+    const int ctas = sum.y == 0 ? 0 : (int)max(1ll, min((long long)a.ctas, sum.y * a.hkv / kTilesPerCta));
+    if (cta < ctas) {
+        // (both ends: r = cost within the head; the last range ends with everything)
+        const int64_t u0 = units * cta / ctas, u1 = units * (cta + 1) / ctas;
+        const int64_t r0 = u0 % sum.x, r1 = u1 % sum.x;
+        int64_t before = 0;
+        for (int base = 0; base < a.n; base += kThreads) {
+            const int s = base + tid;
+            longlong2 tot = sum;
+            if (!one_pass) {
+                own = s < a.n ? seq_cost(a, s) : make_longlong2(0, 0);
+                in = cta_scan2(own, sh->scan, tot);
+            }
+            const int64_t lo = before + in.x - own.x, hi = before + in.x;
+            if (lo <= r0 && r0 < hi) sh->from = place(a, (int)(u0 / sum.x), s, lo, r0);
+            if (lo <= r1 && r1 < hi && cta + 1 < ctas) sh->to = place(a, (int)(u1 / sum.x), s, lo, r1);
+            before += tot.x;
+        }
+    }
+    __syncthreads();
+    if (tid == 0) {
+        if (cta < ctas) a.start[cta] = sh->from;
+        if (cta + 1 == ctas) a.start[ctas] = sh->to;
+        if (cta == 0) *a.used_ctas = ctas;
+    }
+}
+
+// A CTA's range of key tiles, piece by piece.  The warp that loads K, ahead of all others,
+// walks over it and tells them (one copy of the walk's code, and few registers elsewhere).
 struct Piece {
     Item it;
-    int32_t head, j0, j1;  // key tiles [j0, j1)
+    int32_t seq, head, j0, j1;  // key tiles [j0, j1)
     bool whole;            // covers the item: the output is written, not a partial
-    int32_t slot;          // workspace slot of a partial
 };
 
-// (AHEAD: with the next item's description on its way; the softmax warps, short
-// of registers and waiting for logits at that point anyway, read it when due.)
-template <bool AHEAD>
+// A CTA has at most two partials: one that starts inside an item, one that ends there.
+__device__ __forceinline__ int64_t partial_slot(int cta, bool inside) { return 2 * (int64_t)cta + (inside ? 0 : 1); }
+
 struct Walk {
     const ChunkArgs &a;
     Start at, end;
-    bool first;
-    Item next;
-    __device__ Walk(const ChunkArgs &args) : a(args)
+    Item it;  // at `at`
+    __device__ Walk(const ChunkArgs &args, const Shared *sh) : a(args)
     {
-        const int cta = blockIdx.x;
-        first = true;
-        at.head = end.head = at.item = end.item = at.off = end.off = 0;
-        if (cta < a.head->ctas) {
-            at = a.start[cta];
-            end = a.start[cta + 1];
-            if (AHEAD) next = a.items[at.item];
+        at = sh->from, end = sh->to;
+        if (at.head < a.hkv) {
+            it = make_item(a, at.seq, at.pair);
+            if (at.off >= it.nt && !same_item(at, end)) advance();
+        }
+    }
+    __device__ __forceinline__ void advance()
+    {
+        at.off = 0;
+        ++at.pair;
+        if (at.pair * 2 * a.TQ >= it.m) {
+            at.pair = 0;
+            do {
+                if (++at.seq == a.n) at.seq = 0, ++at.head;
+                it = make_item(a, at.seq, 0);
+            } while (it.m == 0);
+        } else {
+            it = make_item(a, at.seq, at.pair);
         }
     }
     __device__ bool step(Piece &p)
     {
+        if (at.head >= a.hkv) return false;
         const bool last = same_item(at, end);
-        if (last && at.off == end.off) return false;
-        p.it = AHEAD ? next : a.items[at.item];
+        p.it = it;
+        p.seq = at.seq;
         p.head = at.head;
         p.j0 = at.off;
-        p.j1 = last ? end.off : p.it.nt;
-        p.whole = at.off == 0 && !last;
-        p.slot = 2 * blockIdx.x + (first ? 0 : 1);
-        first = false;
-        if (last) {
-            at.off = end.off;
-        } else {
-            at.off = 0;
-            if (++at.item == a.head->items) at.item = 0, ++at.head;
-            if (AHEAD && at.head < a.hkv) next = a.items[at.item];
-        }
+        p.j1 = last ? min(end.off, it.nt) : it.nt;
+        if (p.j0 >= p.j1) return false;  // (only at the end)
+        p.whole = p.j0 == 0 && p.j1 == it.nt;
+        if (last) at.head = a.hkv; else advance();
         return true;
     }
 };
+
+// Piece number `n` as the walking warp told it; false: there is none, or a wait ran out.
+// (WARP: a whole warp asks, not one thread.)
+template <bool WARP, class Wait>
+__device__ __forceinline__ bool next_piece(Piece &p, uint32_t n, Shared *sh, bool &ok, int lane, Wait wait)
+{
+    const int i = n % kPieces;
+    ok = wait(smem_u32(&sh->piece_full[i]), n / kPieces & 1);
+    if (!ok) return false;
+    const int4 u = sh->piece[i][0], v = sh->piece[i][1], w = sh->piece[i][2];
+    p.it.row0 = u.x, p.it.ntok = u.y, p.it.pos0 = u.z, p.it.nt = u.w;
+    p.it.len = v.x, p.it.m = v.y, p.seq = v.z, p.head = v.w;
+    p.j0 = w.x, p.j1 = w.y, p.whole = w.z;
+    if (WARP) __syncwarp();
+    if (lane == 0) mbar_arrive(smem_u32(&sh->piece_empty[i]));
+    return p.j1 > 0;
+}
 
 // Key tiles of query tile x in a piece: `cnt` of them, from j, `by` apart.
 struct Part {
@@ -548,11 +553,11 @@ __device__ __forceinline__ uint32_t finite_pair(uint32_t w)
 // Values of new tokens that are not finite were cleared from V: adds those at positions
 // [y0, y1] to a row of the output, or of a partial.
 template <int D>
-__device__ __noinline__ void add_cleared(const ChunkArgs &a, const Item &it, int head, int y0, int y1, uint16_t *out,
+__device__ __noinline__ void add_cleared(const ChunkArgs &a, int seq, int head, int y0, int y1, uint16_t *out,
                                          float4 *part)
 {
     for (int y = y0; y <= y1; ++y) {
-        const int32_t id = a.bt[(int64_t)it.seq * a.bt_stride + y / kBlk];
+        const int32_t id = a.bt[(int64_t)seq * a.bt_stride + y / kBlk];
         if (id < 0 || id >= a.num_blocks) continue;
         const uint16_t *v = a.v + id * a.block_stride + head * a.head_stride + (int64_t)(y % kBlk) * D;
 #pragma unroll 1
@@ -570,31 +575,45 @@ __device__ __noinline__ void add_cleared(const ChunkArgs &a, const Item &it, int
     }
 }
 
+// Records the sequences whose rows or lengths are out of order and zeroes their rows.
+__device__ __noinline__ void refuse_sequences(const ChunkArgs &a)
+{
+    for (int s = threadIdx.x; s < a.n; s += kThreads) {
+        const int32_t r0 = a.q_start[s], r1 = a.q_start[s + 1];
+        if (chunk_ok(a, r0, r1, a.len[s])) continue;
+        set_err(a.err, KARA_EINVAL);
+        const int64_t words = (int64_t)a.hq * a.D / 2, hi = min(r1, a.rows) * words;
+        for (int64_t i = max(r0, 0) * words; i < hi; ++i) reinterpret_cast<uint32_t *>(a.out)[i] = 0u;
+    }
+}
+
 // The MMAs of query tile X, issued by one thread: of this warp alone, as an issue takes
 // a thread about 40 clocks and the tensor cores 64, so that one thread for both tiles
 // would set the pace.  The warps of both tiles walk every K and V tile in ring order (one
 // that the query tile skips is handed back at once), so each sees every phase of every
 // stage.  With two query tiles they take turns: first one tile's weighted sum and next
 // logits, then the other's, so that one tile is multiplied while the other is
-// exponentiated.  Addresses are constants or 32-bit sums: beside two busy softmax warps
-// every instruction between two MMAs counts.
-template <int D, int X>
-__device__ __forceinline__ void mma_warp(uint32_t qbuf, uint32_t ring, Shared *sh, const ChunkArgs &a)
+// exponentiated.  Descriptors are 32-bit sums, and both tiles share one copy of the code:
+// beside two busy softmax warps every instruction between two MMAs counts, and every line
+// of the instruction caches.
+template <int D>
+__device__ __forceinline__ void mma_warp(int x, uint32_t qbuf, uint32_t ring, Shared *sh, const ChunkArgs &a)
 {
     using C = Cfg<D>;
     if (elect_one()) {
         constexpr uint32_t id_qk = idesc_bf16(kTile, kTile);
         constexpr uint32_t id_pv = idesc_bf16(kTile, D) | (1u << 16);  // V: its dims are contiguous
         constexpr uint32_t kTileDesc = C::kTileBytes >> 4, kHalfDesc = C::kHalfBytes >> 4;
-        constexpr uint32_t ts = X * kTile, to = 256 + X * 128;         // S (and P over it), O in TMEM
+        const uint32_t ts = x * kTile, to = 256 + x * 128;         // S (and P over it), O in TMEM
         const uint64_t qd = sdesc_sw128(qbuf), kd = sdesc_sw128(ring), vd = sdesc_sw128_mn(ring, C::kHalfBytes);
         const uint32_t full0 = smem_u32(&sh->full[0]), empty0 = smem_u32(&sh->empty[0]);
-        const uint32_t sf = smem_u32(&sh->s_full[X]), pf = smem_u32(&sh->p_full[X]), ph = smem_u32(&sh->p_half[X]);
-        const uint32_t mine = smem_u32(&sh->turn[X]), other = smem_u32(&sh->turn[1 - X]);
-        Walk<true> w(a);
+        const uint32_t sf = smem_u32(&sh->s_full[x]), pf = smem_u32(&sh->p_full[x]), ph = smem_u32(&sh->p_half[x]);
+        const uint32_t mine = smem_u32(&sh->turn[x]), other = smem_u32(&sh->turn[1 - x]);
         Piece p;
+        const auto wait = [&](uint32_t bar, uint32_t parity) { return kwait(bar, parity, sh, a); };
+        uint32_t np = 0;
         uint32_t ks = 0, kp = 0, vs = 1, vp = 0;  // next K and V tile: stage, phase
-        uint32_t pp = 0, turn = 1 - X, iq = 0;    // phases of the next weights, turn, query tiles
+        uint32_t pp = 0, turn = 1 - x, iq = 0;    // phases of the next weights, turn, query tiles
         bool ok = true;
         auto next = [](uint32_t &st, uint32_t &ph) {  // a tile further (K and V alternate)
             st += 2;
@@ -605,11 +624,12 @@ __device__ __forceinline__ void mma_warp(uint32_t qbuf, uint32_t ring, Shared *s
             mbar_arrive(empty0 + st * 8);
             next(st, ph);
         };
-        while (ok && w.step(p)) {
+        while (ok && next_piece<false>(p, np, sh, ok, 0, wait)) {
+            ++np;
             const bool two = p.it.ntok > a.TQ;
-            const int n = p.j1 - p.j0, cnt = part_of(p, X, a.TQ).cnt;
-            const int by = two ? 1 : 2, first = two ? 0 : X, last = first + (cnt - 1) * by;
-            const uint32_t ql = (uint32_t)qd + (two && X ? kTileDesc : 0);
+            const int n = p.j1 - p.j0, cnt = part_of(p, x, a.TQ).cnt;
+            const int by = two ? 1 : 2, first = two ? 0 : x, last = first + (cnt - 1) * by;
+            const uint32_t ql = (uint32_t)qd + (two && x ? kTileDesc : 0);
             ok = kwait(smem_u32(&sh->q_full), iq & 1, sh, a);
             iq ^= 1;
             if (ok && cnt == 0) mbar_arrive(smem_u32(&sh->q_empty));
@@ -617,7 +637,7 @@ __device__ __forceinline__ void mma_warp(uint32_t qbuf, uint32_t ring, Shared *s
                 // weighted sum of tile t, then logits of tile t + by (a single query tile: its own
                 // tiles, between the other warp's)
                 const bool sum = t >= first && t <= last, logits = t + by <= last;
-                if (!two && X == 1 && t >= 0) skip(vs, vp);
+                if (!two && x == 1 && t >= 0) skip(vs, vp);
                 if (t >= first && t < n) {
                     ok = ok && kwait(full0 + vs * 8, vp, sh, a);
                     if (two && ok && t + 1 < n) ok = kwait(full0 + ks * 8, kp, sh, a);
@@ -638,15 +658,15 @@ __device__ __forceinline__ void mma_warp(uint32_t qbuf, uint32_t ring, Shared *s
                         for (int e = kTile / 32; e < kTile / 16; ++e)
                             mma_ts(to, ts + e * 8, lo + e * 128, (uint32_t)(vd >> 32), id_pv, 1);
                         if (!two) mma_commit(empty0 + vs * 8);
-                        if (t == last) mma_commit(smem_u32(&sh->o_full[X]));
+                        if (t == last) mma_commit(smem_u32(&sh->o_full[x]));
                     } else {
                         mbar_arrive(empty0 + vs * 8);
                     }
                 }
                 const uint32_t v_done = empty0 + vs * 8;
                 if (t >= first && t < n) next(vs, vp);
-                if (!two && X == 0 && t >= 0 && t + 1 < n) skip(vs, vp);
-                if (!two && X == 1 && t + 1 < n) skip(ks, kp);
+                if (!two && x == 0 && t >= 0 && t + 1 < n) skip(vs, vp);
+                if (!two && x == 1 && t + 1 < n) skip(ks, kp);
                 if (t + by < n) {
                     if (!two || t < first) ok = ok && kwait(full0 + ks * 8, kp, sh, a);
                     if (!ok) break;
@@ -673,13 +693,13 @@ __device__ __forceinline__ void mma_warp(uint32_t qbuf, uint32_t ring, Shared *s
                     next(ks, kp);
                 }
                 if (two && sum) mma_commit(v_done);
-                if (!two && X == 0 && t + by + 1 < n) skip(ks, kp);
+                if (!two && x == 0 && t + by + 1 < n) skip(ks, kp);
             }
-            if (!two && X == 1 && ok && n % 2) skip(vs, vp);
+            if (!two && x == 1 && ok && n % 2) skip(vs, vp);
         }
         // the tensor cores are idle before TMEM and shared memory go
-        mma_commit(smem_u32(&sh->done[X]));
-        drain(smem_u32(&sh->done[X]), 0);
+        mma_commit(smem_u32(&sh->done[x]));
+        drain(smem_u32(&sh->done[x]), 0);
     }
     __syncwarp();
 }
@@ -700,6 +720,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = 0; i < kStages; ++i) {
             mbar_init(smem_u32(&sh->full[i]), 1);
             mbar_init(smem_u32(&sh->empty[i]), 2);
+        }
+        for (int i = 0; i < kPieces; ++i) {
+            mbar_init(smem_u32(&sh->piece_full[i]), 1);
+            mbar_init(smem_u32(&sh->piece_empty[i]), kPieceReaders);
         }
         mbar_init(smem_u32(&sh->q_full), 1);
         mbar_init(smem_u32(&sh->q_empty), 2);
@@ -737,6 +761,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr uint32_t tmem = 0;  // every column is this CTA's: the allocation starts at 0
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (blockIdx.x == gridDim.x - 1) refuse_sequences(a);
+    cut_range(a, sh);
 
     if (warp >= 8) {
         reg_dealloc<kRegsCtl>();
@@ -746,15 +772,35 @@ __global__ void __launch_bounds__(kThreads, 1)
             // both would take 2900 clocks for what two query tiles multiply in 2048.
             const int kv = warp - kWarpKv;
             const CUtensorMap *map = kv ? &vmap : &kmap;
-            Walk<true> w(a);
+            Walk w(a, sh);
             Piece p;
+            const auto wait = [&](uint32_t bar, uint32_t parity) {
+                return __all_sync(0xffffffffu, kwait(bar, parity, sh, a));
+            };
+            uint32_t np = 0;
             uint32_t st = kv, ph = 1, k = 0;  // stage and the phase that frees it; tiles issued
             uint32_t ne = 0, were_edges = 0;  // edge tiles issued; which of the last tiles were (bit 0: the last)
             const int b = lane % kBlkPerTile, h = lane / kBlkPerTile;
             const bool mine = h < C::kHalves;
             bool ok = !a.stall;
-            while (ok && w.step(p)) {
-                const int32_t *row = a.bt + (int64_t)p.it.seq * a.bt_stride;
+            while (ok) {
+                if (kv == 0) {
+                    const bool more = w.step(p);
+                    const int i = np % kPieces;
+                    ok = wait(smem_u32(&sh->piece_empty[i]), (np / kPieces & 1) ^ 1);
+                    if (!ok) break;
+                    if (lane == 0) {
+                        sh->piece[i][0] = make_int4(p.it.row0, p.it.ntok, p.it.pos0, p.it.nt);
+                        sh->piece[i][1] = make_int4(p.it.len, p.it.m, p.seq, p.head);
+                        sh->piece[i][2] = make_int4(p.j0, more ? p.j1 : 0, p.whole, 0);
+                        mbar_arrive(smem_u32(&sh->piece_full[i]));
+                    }
+                    if (!more) break;
+                } else if (!next_piece<true>(p, np, sh, ok, lane, wait)) {
+                    break;
+                }
+                ++np;
+                const int32_t *row = a.bt + (int64_t)p.seq * a.bt_stride;
                 const int32_t nblk = (p.it.len + kBlk - 1) / kBlk;
                 auto block_id = [&](int j) -> int32_t {
                     const int i = j * kBlkPerTile + b;
@@ -797,18 +843,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                     drain(smem_u32(&sh->full[e % kStages]), (e / kStages) & 1);
             }
             for (uint32_t i = ne > 3 ? ne - 3 : 0; i < ne; ++i) drain(smem_u32(&sh->edge[i & 3]), (i >> 2) & 1);
-        } else if (warp == kWarpMma) {
-            mma_warp<D, 0>(smem_u32(qbuf), smem_u32(ring), sh, a);
-        } else if (warp == kWarpMma + 1) {
-            mma_warp<D, 1>(smem_u32(qbuf), smem_u32(ring), sh, a);
+        } else if (warp == kWarpMma || warp == kWarpMma + 1) {
+            mma_warp<D>(warp - kWarpMma, smem_u32(qbuf), smem_u32(ring), sh, a);
         } else {
             // ---------------- query tiles (warp 12), and the edge tiles of V (warps 12-15, a
             // quarter of the rows each: the products wait for them)
-            Walk<true> w(a);
             Piece p;
+            const auto wait = [&](uint32_t bar, uint32_t parity) {
+                return __all_sync(0xffffffffu, kwait<200>(bar, parity, sh, a));
+            };
             uint32_t k0 = 0, np = 0, ne = 0;
             bool ok = true;
-            for (; ok && !a.stall && w.step(p); ++np) {
+            for (; ok && !a.stall && next_piece<true>(p, np, sh, ok, lane, wait); ++np) {
                 if (warp == kWarpQ) {
                     ok = __all_sync(0xffffffffu, kwait<200>(smem_u32(&sh->q_empty), (np & 1) ^ 1, sh, a));
                     if (!ok) break;
@@ -883,11 +929,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int tok = r / a.G, hd = r - tok * a.G;
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t ts = tmem + lanes + x * kTile, to = tmem + lanes + 256 + x * 128;
-        Walk<false> w(a);
         Piece p;
+        const auto wait = [&](uint32_t bar, uint32_t parity) {
+            return __all_sync(0xffffffffu, cwait(bar, parity, sh, a));
+        };
         uint32_t ns = 0, no = 0, nj = 0, np = 0;
         bool ok = true;
-        for (; ok && w.step(p); ++np) {
+        for (; ok && next_piece<true>(p, np, sh, ok, lane, wait); ++np) {
             const bool two = p.it.ntok > a.TQ;
             const Part pt = part_of(p, x, a.TQ);
             const int t = (two ? x * a.TQ : 0) + tok;  // token of the item
@@ -1008,7 +1056,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int64_t row = p.it.row0 + t;
                 const int rr = (two ? x * kTile : 0) + r;
                 const bool add = *(volatile int32_t *)&sh->odd_values[np & 3] == (int32_t)np + 1;
-                float4 *pp = a.part + (int64_t)p.slot * (D / 4) * 256 + rr;  // dims d..d+3 at pp[d / 4 * 256]
+                const int64_t slot = partial_slot(blockIdx.x, p.j0 > 0);
+                float4 *pp = a.part + slot * (D / 4) * 256 + rr;  // dims d..d+3 at pp[d / 4 * 256]
                 uint16_t *op = a.out + (row * a.hq + p.head * a.G + hd) * D;
 #pragma unroll 1  // one copy: it runs once an item, out of a cold instruction cache
                 for (int c = 0; c < D; c += 32) {
@@ -1048,9 +1097,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                                                                 __uint_as_float(o[e + 2]), __uint_as_float(o[e + 3]));
                     }
                 }
-                if (add && live) add_cleared<D>(a, p.it, p.head, max(p.it.pos0 + 1, p.j0 * kTile),
+                if (add && live) add_cleared<D>(a, p.seq, p.head, max(p.it.pos0 + 1, p.j0 * kTile),
                                                 min(pos, p.j1 * kTile - 1), p.whole ? op : nullptr, pp);
-                if (live && !p.whole) a.stat[(int64_t)p.slot * 256 + rr] = make_float2(m, z);
+                if (live && !p.whole) a.stat[slot * 256 + rr] = make_float2(m, z);
             }
             // the next piece's products write O again only after these reads
             tc_fence_before();
@@ -1076,31 +1125,30 @@ __global__ void __launch_bounds__(256) chunk_merge_kernel(const ChunkArgs a)
 {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int ctas = a.head->ctas, c = blockIdx.x + 1;
+    const int ctas = *a.used_ctas, c = blockIdx.x + 1;
     if (c >= ctas) return;
     const Start s = a.start[c], b = a.start[c - 1];
     if (s.off == 0 || (same_item(s, b) && b.off > 0)) return;  // no cut, or an earlier one of the same item
-    const Item it = a.items[s.item];
+    const Item it = make_item(a, s.seq, s.pair);
+    if (s.off >= it.nt) return;  // behind the item
     const int rr = (blockIdx.y & 7) * 32 + (threadIdx.x & 31), d4 = ((blockIdx.y >> 3) * 8 + (threadIdx.x >> 5)) * 2;
     const bool two = it.ntok > a.TQ;
     const int x = rr / kTile, r = rr % kTile, t = x * a.TQ + r / a.G, hd = r % a.G;
     if (r >= a.G * a.TQ || t >= it.ntok || (x == 1 && !two)) return;
-    // the piece of CTA c - 1 (its last; its first too if it starts with the item), then those of the
-    // CTAs that start inside the item
-    const int first = 2 * (c - 1) + (same_item(s, b) ? 0 : 1);
+    // the piece that CTA c - 1 began the item with, then those of the CTAs that start inside it
     int end = c + 1;
-    while (end < ctas && same_item(a.start[end], s)) ++end;
-    const auto empty = [&](int k) {  // CTA k got nothing
+    while (end < ctas && same_item(a.start[end], s) && a.start[end].off < it.nt) ++end;
+    const auto empty = [&](int k) {  // CTA k got nothing of the item
         const Start p = a.start[k], q = a.start[k + 1];
-        return same_item(p, q) && p.off == q.off;
+        return same_item(p, q) && p.off >= q.off;
     };
     float M = -INFINITY;
     for (int k = c - 1; k < end; ++k)
-        if (k < c || !empty(k)) M = fmaxf(M, a.stat[(int64_t)(k < c ? first : 2 * k) * 256 + rr].x);
+        if (k < c || !empty(k)) M = fmaxf(M, a.stat[partial_slot(k, k >= c) * 256 + rr].x);
     float den = 0.f, acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
     for (int k = c - 1; k < end; ++k) {
         if (k >= c && empty(k)) continue;
-        const int64_t slot = k < c ? first : 2 * k;
+        const int64_t slot = partial_slot(k, k >= c);
         const float2 st = a.stat[slot * 256 + rr];
         if (st.x == -INFINITY && st.y == 0.f) continue;  // nothing of this piece is seen by the row
         const float f = ex2(st.x - M);
@@ -1133,21 +1181,16 @@ cudaError_t query_map(CUtensorMap *m, const void *q, const kara_cache *c, int32_
     return cudaSuccess;
 }
 
-// Workspace: [head][starts][items][items before each sequence][stats][partials].
+// Workspace: [CTAs with work][starts][stats][partials].
 struct Layout {
-    size_t start, items, seq, stat, part, total;
-    int32_t cap;
+    size_t start, stat, part, total;
 };
 
-Layout layout(const kara_cache *c, int32_t n, int32_t rows)
+Layout layout(const kara_cache *c)
 {
-    const int TQ = kTile / (c->num_q_heads / c->num_kv_heads);
     Layout l;
-    l.cap = rows / (2 * TQ) + n;  // a sequence of m tokens has at most m / (2 TQ) + 1 items
     size_t o = 256;
     l.start = o, o += align256((kMaxCtas + 1) * sizeof(Start));
-    l.items = o, o += align256((size_t)l.cap * sizeof(Item));
-    l.seq = o, o += align256(((size_t)n + 1) * sizeof(int32_t));
     l.stat = o, o += align256((size_t)2 * kMaxCtas * 256 * sizeof(float2));
     l.part = o, o += (size_t)2 * kMaxCtas * 256 * c->head_dim * sizeof(float);
     l.total = o;
@@ -1162,9 +1205,7 @@ cudaError_t launch_all(const CUtensorMap &km, const CUtensorMap &vm, const CUten
     static_assert(smem <= 227 * 1024, "shared memory");
     cudaError_t e = cudaFuncSetAttribute(chunk_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    e = launch_dependent(chunk_plan_kernel, dim3(1), kPlanThreads, 0, st, a);
-    if (e == cudaSuccess)
-        e = launch_dependent(chunk_kernel<D>, dim3((unsigned)a.ctas), kThreads, smem, st, km, vm, qm, a);
+    e = launch_dependent(chunk_kernel<D>, dim3((unsigned)a.ctas), kThreads, smem, st, km, vm, qm, a);
     if (e == cudaSuccess && a.ctas > 1)
         e = launch_dependent(chunk_merge_kernel<D>, dim3((unsigned)a.ctas - 1, 8 * (D / 64)), 256, 0, st, a);
     return e;
@@ -1172,7 +1213,7 @@ cudaError_t launch_all(const CUtensorMap &km, const CUtensorMap &vm, const CUten
 
 }  // namespace
 
-size_t chunk_workspace_bytes(const kara_cache *c, int32_t n, int32_t rows) { return layout(c, n, rows).total; }
+size_t chunk_workspace_bytes(const kara_cache *c) { return layout(c).total; }
 
 cudaError_t launch_chunk(const kara_cache *c, int32_t layer, const kara_tokens *t, const int32_t *bt,
                          int32_t bt_stride, const void *q, void *out, void *ws, int32_t *err, cudaStream_t st)
@@ -1197,13 +1238,10 @@ cudaError_t launch_chunk(const kara_cache *c, int32_t layer, const kara_tokens *
     a.v = static_cast<const uint16_t *>(c->v) + (int64_t)layer * c->layer_stride;
     a.block_stride = c->block_stride;
     a.head_stride = c->head_stride;
-    const Layout l = layout(c, t->n, t->rows);
+    const Layout l = layout(c);
     char *w = static_cast<char *>(ws);
-    a.cap_items = l.cap;
-    a.head = reinterpret_cast<PlanHead *>(w);
+    a.used_ctas = reinterpret_cast<int32_t *>(w);
     a.start = reinterpret_cast<Start *>(w + l.start);
-    a.items = reinterpret_cast<Item *>(w + l.items);
-    a.seq_items = reinterpret_cast<int32_t *>(w + l.seq);
     a.stat = reinterpret_cast<float2 *>(w + l.stat);
     a.part = reinterpret_cast<float4 *>(w + l.part);
     a.wide = ((uintptr_t)out & 31u) == 0;

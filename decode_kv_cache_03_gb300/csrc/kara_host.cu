@@ -378,7 +378,7 @@ kara_status kara_append_kv(const kara_cache *c, int32_t layer, const kara_tokens
 size_t kara_chunk_workspace_size(const kara_cache *c, int32_t n, int32_t rows)
 {
     if (check_cache(c) != KARA_OK || n < 0 || rows < 0) return 0;
-    return chunk_workspace_bytes(c, n, rows);
+    return chunk_workspace_bytes(c);
 }
 
 kara_status kara_chunk_attention(const kara_cache *c, int32_t layer, const kara_tokens *t, const int32_t *block_table,
@@ -393,7 +393,7 @@ kara_status kara_chunk_attention(const kara_cache *c, int32_t layer, const kara_
     if (t->n > kMaxSeqs || (int64_t)bt_stride * c->block_size > 0x7fffffffLL) return KARA_EUNSUPPORTED;
     if (!t->q_start || !t->len || !block_table || !q || !out || !err) return KARA_EINVAL;
     if (!aligned16(q) || !aligned16(out)) return KARA_EINVAL;
-    if (!ws || ws_bytes < chunk_workspace_bytes(c, t->n, t->rows)) return KARA_EWORKSPACE;
+    if (!ws || ws_bytes < chunk_workspace_bytes(c)) return KARA_EWORKSPACE;
     return cuda_status(launch_chunk(c, layer, t, block_table, bt_stride, q, out, ws, err, (cudaStream_t)stream));
 }
 
