@@ -18,8 +18,8 @@
 // latency of its chain of loads (slot, offset, table row, rows): in registers it
 // reached 4.0 TB/s with four passes a warp (8192 tokens, 40/8 heads of 128, with
 // the ring: 70 us), staged 5.4 TB/s (52 us).
-#include "kara_common.cuh"
 #include "kara_sm100.cuh"
+#include "kara_tokens.cuh"
 
 namespace kara {
 namespace {

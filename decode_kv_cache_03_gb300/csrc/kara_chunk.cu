@@ -44,10 +44,12 @@
 // 90 clocks: one warp took 2900 clocks for the K and V tiles that two query tiles multiply
 // in 2048), the two tiles taking turns, 1595; the turn taken before the weights are
 // waited for, 1485; cuts by cost, 1455; waits that nap in the warps that have time, 1435;
-// the instruction caches (one copy of the epilogue's code and of the MMAs', the control warps'
-// waiting out of line, one warp that walks over the work and tells the others), 1390 (512 tokens x 32 sequences at 4096 keys: 852 -> 763); the weighted sum
-// begun on half the weights, 1340 (1.54 PFLOP/s, 0.81 of the measured cuBLAS burst).  What
-// is left: a step of two query tiles takes about 2950 clocks against 2048 of tensor time
+// the instruction caches (one copy of the epilogue's code and of the MMAs', the control
+// warps' waiting out of line, one warp that walks over the work and tells the others), 1390
+// (512 tokens x 32 sequences at 4096 keys: 852 -> 750); the weighted sum begun on half the
+// weights, 1330 to 1370 on several boxes (1.5 PFLOP/s, 0.8 of the measured cuBLAS burst).
+// Few rows over long caches (4 tokens x 128 sequences) read K and V at 6.9 to 7.0 TB/s.
+// What is left: a step of two query tiles takes about 2950 clocks against 2048 of tensor time
 // (logits, exponentials and weighted sum of a tile depend on each other, and TMEM holds
 // one S per tile beside O), and the power limit: under back-to-back calls the clock falls
 // to 1.5 - 1.8 GHz.
@@ -57,13 +59,12 @@
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
-#include "kara_common.cuh"
 #include "kara_sm100.cuh"
+#include "kara_tokens.cuh"
 
 namespace kara {
 
 PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();  // defined beside the scoring kernel
-cudaError_t pool_map(CUtensorMap *m, const void *pool, const kara_cache *c);  // defined beside decode attention
 
 namespace {
 
@@ -116,8 +117,8 @@ struct ChunkArgs {
     uint16_t *out;
     int32_t *used_ctas;  // CTAs that got work
     Start *start;        // [used_ctas + 1]
-    float4 *part;     // [2 * ctas][D / 4][256]
-    float2 *stat;     // [2 * ctas][256]: (max, sum) in the log2 domain
+    float4 *part;        // [2 * ctas][D / 4][256]
+    float2 *stat;        // [2 * ctas][256]: (max, sum) in the log2 domain
     const uint16_t *v;   // V pool at the call's layer
     int64_t block_stride, head_stride;
     int32_t wide;        // out is 32-byte aligned
@@ -153,13 +154,13 @@ __device__ __forceinline__ Item make_item(const ChunkArgs &a, int seq, int pair)
 
 // ---- attention ------------------------------------------------------------------
 constexpr int kPieces = 4;        // descriptions of pieces under way
-constexpr int kPieceReaders = 15; // warps that read them: softmax 8, V, MMAs 2, edge tiles 4
+constexpr int kPieceReaders = 15;  // warps that read them: softmax 8, V, MMAs 2, edge tiles 4
 
 struct Shared {
     uint64_t full[kStages], empty[kStages];  // K / V tiles
     uint64_t q_full, q_empty;
     uint64_t s_full[2];   // logits of a query tile are in TMEM (and its earlier products are done)
-    uint64_t p_half[2], p_full[2];
+    uint64_t p_half[2], p_full[2];  // the first half of its weights are in TMEM; all are
     uint64_t o_full[2];   // its last product is done
     uint64_t x_full, x_free;  // a single query tile's odd half is ready to be joined; is joined
     uint64_t edge[4];     // an edge tile of V has landed (by their number mod 4: the ring holds at most three);
@@ -168,10 +169,11 @@ struct Shared {
     uint64_t done[2];
     uint32_t tmem;
     int32_t abort;
-    int32_t fixed[4];     // quarters of an edge tile cleaned (by the tile's number mod 4; one warp may be a tile ahead)
-    int32_t odd_values[4];  // 1 + the last piece (by its number mod 4) whose V had values that are not finite
+    // quarters of an edge tile cleaned (by the tile's number mod 4: one warp may be a tile ahead), and
+    // 1 + the last piece (by its number mod 4) whose V had values that are not finite
+    int32_t fixed[4], odd_values[4];
     Start from, to;       // this CTA's range
-    int4 piece[kPieces][3];                               // pieces of it, by their number mod kPieces
+    int4 piece[kPieces][3];  // pieces of it, by their number mod kPieces
     uint64_t piece_full[kPieces], piece_empty[kPieces];
     longlong2 scan[kThreads / 32 + 1];
     float2 stat[kTile];   // (max, sum) of the odd key tiles, for joining a single query tile
@@ -587,7 +589,7 @@ __device__ __noinline__ void refuse_sequences(const ChunkArgs &a)
     }
 }
 
-// The MMAs of query tile X, issued by one thread: of this warp alone, as an issue takes
+// The MMAs of query tile x, issued by one thread: of this warp alone, as an issue takes
 // a thread about 40 clocks and the tensor cores 64, so that one thread for both tiles
 // would set the pace.  The warps of both tiles walk every K and V tile in ring order (one
 // that the query tile skips is handed back at once), so each sees every phase of every
@@ -1163,6 +1165,25 @@ __global__ void __launch_bounds__(256) chunk_merge_kernel(const ChunkArgs a)
     *reinterpret_cast<uint4 *>(op) =
         make_uint4(bf16x2(acc[0] * inv, acc[1] * inv), bf16x2(acc[2] * inv, acc[3] * inv),
                    bf16x2(acc[4] * inv, acc[5] * inv), bf16x2(acc[6] * inv, acc[7] * inv));
+}
+
+// Tensor map over one pool, (d, slot, kv head, block, layer) with the cache's
+// strides; a box is one 64-dim half of a (block, head) slice, 128-byte swizzled.
+cudaError_t pool_map(CUtensorMap *m, const void *pool, const kara_cache *c)
+{
+    auto fn = tensor_map_encoder();
+    if (!fn) return cudaErrorNotSupported;
+    cuuint64_t dims[5] = {(cuuint64_t)c->head_dim, (cuuint64_t)kBlk, (cuuint64_t)c->num_kv_heads,
+                          (cuuint64_t)c->num_blocks, (cuuint64_t)c->num_layers};
+    cuuint64_t strides[4] = {(cuuint64_t)c->head_dim * 2, (cuuint64_t)c->head_stride * 2,
+                             (cuuint64_t)c->block_stride * 2, (cuuint64_t)c->layer_stride * 2};
+    cuuint32_t box[5] = {64, (cuuint32_t)kBlk, 1, 1, 1};
+    cuuint32_t estr[5] = {1, 1, 1, 1, 1};
+    if (fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<void *>(pool), dims, strides, box, estr,
+           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+        return cudaErrorInvalidValue;
+    return cudaSuccess;
 }
 
 // Tensor map over q, (d, head, row); a box is one 64-dim half of a query tile.

@@ -87,24 +87,6 @@ __device__ __forceinline__ int64_t pool_off(const Geo &g, int l, int32_t blk, in
 
 __host__ __device__ __forceinline__ size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 
-// Launches `kern` as a programmatic dependent of what precedes it on the stream: its launch overlaps
-// that grid's end, and it reads nothing global before its griddepcontrol.wait.
-template <class... A>
-cudaError_t launch_dependent(void (*kern)(A...), dim3 grid, int threads, size_t smem, cudaStream_t st, A... args)
-{
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = grid;
-    cfg.blockDim = dim3((unsigned)threads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = st;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kern, args...);
-}
-
 // Host-side argument checks of the entry points; fills the geometry of a call.
 kara_status geo_from_args(const kara_cache *c, const kara_params *p, const kara_batch *b, Geo *g);
 
@@ -132,15 +114,6 @@ cudaError_t launch_qring_compact(const kara_cache *c, const kara_params *p, cons
 cudaError_t launch_qring_append(const kara_cache *c, const kara_params *p, const kara_batch *b,
                                 const void *q_new, cudaStream_t st);
 int decode_max_splits(int32_t bt_stride, int32_t block_size);
-cudaError_t launch_extend(int32_t num_blocks, const int32_t *len, const int32_t *n_new, int32_t *bt, int32_t bt_stride,
-                          const int32_t *fresh, int64_t n_fresh, const kara_tokens *t,
-                          int32_t *used, int32_t *err, cudaStream_t st);
-cudaError_t launch_append(const kara_cache *c, int32_t layer, const kara_tokens *t, const kara_rope *r, const void *q,
-                          int64_t q_stride, const void *k, int64_t k_stride, const void *v, int64_t v_stride,
-                          void *q_out, void *ring, int32_t W, int32_t *err, cudaStream_t st);
-size_t chunk_workspace_bytes(const kara_cache *c);
-cudaError_t launch_chunk(const kara_cache *c, int32_t layer, const kara_tokens *t, const int32_t *bt,
-                         int32_t bt_stride, const void *q, void *out, void *ws, int32_t *err, cudaStream_t st);
 cudaError_t launch_score(const Geo &g, float *scores, void *scratch, int32_t *err, cudaStream_t st);
 // SMs the single-pass scorer leaves idle on batch g, and its resident clusters
 // (both 0 when the single-pass kernel does not cover g).

@@ -41,7 +41,6 @@
 namespace kara {
 
 PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();  // defined beside the scoring kernel
-cudaError_t pool_map(CUtensorMap *m, const void *pool, const kara_cache *c);
 
 namespace {
 
@@ -419,6 +418,25 @@ __global__ void __launch_bounds__(D) decode_combine_kernel(const DecodeArgs a)
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
+// Tensor map over one pool, (d, slot, kv head, block, layer) with the cache's
+// strides; a box is one 64-dim half of a (block, head) slice, 128-byte swizzled.
+cudaError_t pool_map(CUtensorMap *m, const void *pool, const kara_cache *c)
+{
+    auto fn = tensor_map_encoder();
+    if (!fn) return cudaErrorNotSupported;
+    cuuint64_t dims[5] = {(cuuint64_t)c->head_dim, (cuuint64_t)kBlk, (cuuint64_t)c->num_kv_heads,
+                          (cuuint64_t)c->num_blocks, (cuuint64_t)c->num_layers};
+    cuuint64_t strides[4] = {(cuuint64_t)c->head_dim * 2, (cuuint64_t)c->head_stride * 2,
+                             (cuuint64_t)c->block_stride * 2, (cuuint64_t)c->layer_stride * 2};
+    cuuint32_t box[5] = {64, (cuuint32_t)kBlk, 1, 1, 1};
+    cuuint32_t estr[5] = {1, 1, 1, 1, 1};
+    if (fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<void *>(pool), dims, strides, box, estr,
+           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+        return cudaErrorInvalidValue;
+    return cudaSuccess;
+}
+
 // A tensor map depends only on the pool's address, shape and strides: the
 // library keeps the last pair it encoded (static storage, under a lock), so a
 // decode loop over the layers of one cache encodes them once.
@@ -497,25 +515,6 @@ cudaError_t launch_split(const CUtensorMap &km, const CUtensorMap &vm, const Dec
 }
 
 }  // namespace
-
-// Tensor map over one pool, (d, slot, kv head, block, layer) with the cache's
-// strides; a box is one 64-dim half of a (block, head) slice, 128-byte swizzled.
-cudaError_t pool_map(CUtensorMap *m, const void *pool, const kara_cache *c)
-{
-    auto fn = tensor_map_encoder();
-    if (!fn) return cudaErrorNotSupported;
-    cuuint64_t dims[5] = {(cuuint64_t)c->head_dim, (cuuint64_t)kBlk, (cuuint64_t)c->num_kv_heads,
-                          (cuuint64_t)c->num_blocks, (cuuint64_t)c->num_layers};
-    cuuint64_t strides[4] = {(cuuint64_t)c->head_dim * 2, (cuuint64_t)c->head_stride * 2,
-                             (cuuint64_t)c->block_stride * 2, (cuuint64_t)c->layer_stride * 2};
-    cuuint32_t box[5] = {64, (cuuint32_t)kBlk, 1, 1, 1};
-    cuuint32_t estr[5] = {1, 1, 1, 1, 1};
-    if (fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<void *>(pool), dims, strides, box, estr,
-           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
-        return cudaErrorInvalidValue;
-    return cudaSuccess;
-}
 
 int decode_max_splits(int32_t bt_stride, int32_t block_size)
 {

@@ -19,8 +19,8 @@
 // 2^20 blocks), so it reads each table entry once.
 #include <cooperative_groups.h>
 
-#include "kara_common.cuh"
 #include "kara_sm100.cuh"
+#include "kara_tokens.cuh"
 
 namespace cg = cooperative_groups;
 

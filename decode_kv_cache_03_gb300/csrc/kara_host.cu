@@ -6,7 +6,7 @@
 
 #include <nvtx3/nvToolsExt.h>
 
-#include "kara_common.cuh"
+#include "kara_tokens.cuh"
 
 using namespace kara;
 
@@ -342,7 +342,8 @@ kara_status kara_extend_tables(int32_t num_blocks, int32_t block_size, const int
     if (block_size != 16) return KARA_EUNSUPPORTED;
     if (!out || out->n < 0 || out->rows < 0 || num_blocks < 1 || bt_stride < 1 || n_fresh < 0) return KARA_EINVAL;
     if (out->n == 0 && out->rows == 0) return KARA_OK;
-    if (out->n > kMaxSeqs || (int64_t)bt_stride * block_size > 0x7fffffffLL) return KARA_EUNSUPPORTED;
+    if (out->n > kMaxSeqs || (int64_t)bt_stride * block_size > 0x7fffffffLL || n_fresh > 0x7fffffffLL)
+        return KARA_EUNSUPPORTED;
     if (out->n > 0 && (!len || !n_new || !block_table || !out->len)) return KARA_EINVAL;
     if ((n_fresh > 0 && !fresh) || !n_used || !err) return KARA_EINVAL;
     if (!out->q_start || (out->rows > 0 && (!out->slot || !out->seq || !out->pos))) return KARA_EINVAL;

@@ -265,8 +265,9 @@ typedef struct {
  * With any of these, or an error already in *err, nothing is committed: tables
  * are unchanged, out->len[s] = len[s], q_start and *n_used are 0 and every row
  * is padding, so that the calls that follow do nothing.
- * One launch; the call may be captured into a CUDA graph.
- * Supported: block_size 16; n <= 65535; bt_stride * block_size < 2^31.
+ * One launch, two when out->rows is above 20480; programmatic dependents of what
+ * precedes them on `stream`; the call may be captured into a CUDA graph.
+ * Supported: block_size 16; n <= 65535; n_fresh and bt_stride * block_size < 2^31.
  */
 kara_status kara_extend_tables(int32_t num_blocks, int32_t block_size, const int32_t *len, const int32_t *n_new,
                                int32_t *block_table, int32_t bt_stride, const int32_t *fresh, int64_t n_fresh,
@@ -298,7 +299,7 @@ typedef struct {
  * contiguous, rows q_stride / k_stride / v_stride elements apart (multiples of
  * 8; views of one fused projection will do), 16-byte aligned.  q_out may be q
  * when q_stride is num_q_heads * D; no other arrays may overlap.
- * Rows with slot -1 are skipped: nothing of theirs is read or written.
+ * Rows with slot -1 are skipped: nothing of theirs is written.
  * Recorded, the row then being skipped too: KARA_EBADBLOCK for a slot outside
  * the pool, KARA_EINVAL for seq outside [0, n), a negative pos or a rotary
  * position outside [0, n_pos).  Two rows with one slot race.
@@ -321,9 +322,18 @@ kara_status kara_append_kv(const kara_cache *c, int32_t layer, const kara_tokens
  * Recorded: KARA_EINVAL for a sequence whose rows do not lie in order within
  * [0, rows], or with fewer cached than new tokens, or a length above
  * bt_stride * bs (its rows inside [0, rows] become 0); KARA_EBADBLOCK for a
- * block id outside the pool (its keys and values count as zeros).
+ * block id outside the pool (its keys and values count as zeros); KARA_ETIMEOUT if
+ * a bounded device-side wait runs out (outputs are then unspecified).
+ * Logits are fp32 sums of exact bf16 products, maxima, sums and the weighted sum
+ * fp32; the weights are rounded to bf16 (2^-8 of each at most) and the output once.
+ * A row's result depends on its own keys and values only, whatever later tokens
+ * or stale rows of a block hold, NaN included; its bits may depend on the batch
+ * (where a sequence's keys are cut), never on timing.
  * ws/ws_bytes: at least kara_chunk_workspace_size(c, n, rows) bytes, used by
- * this call alone until it has run.  The call may be captured into a CUDA graph.
+ * this call alone until it has run (two calls that may overlap need two).
+ * Returns KARA_ECUDA, before any launch, if a TMA tensor map cannot be encoded.
+ * Two launches, programmatic dependents of what precedes them on `stream`; the
+ * call may be captured into a CUDA graph.
  * Supported: the kara_cache shapes above, n <= 65535,
  * bt_stride * block_size < 2^31.
  */

@@ -860,3 +860,55 @@ def test_chunk_edge_tiles_again_and_again():
     for _ in range(30):
         got, st = run_chunk(kara, d)
         assert st == 0 and torch.equal(got, first)
+
+
+@pytest.mark.parametrize("n", [513, 1500])
+def test_chunk_more_sequences_than_one_pass(n):
+    """Batches past one pass of the prefix sums (512 sequences): single tokens, short chunks, sequences
+    without new tokens, and some that are refused in between."""
+    kara = lib()
+    r = np.random.default_rng(n)
+    n_new = r.integers(0, 4, n).astype(np.int32)
+    n_new[r.integers(0, n, 5)] = r.integers(30, 150, 5)
+    lengths = n_new + r.integers(0, 90, n).astype(np.int32)
+    d = chunk_inputs(n, lengths, n_new, 4, 2, 64, extra=2)
+    got, st = run_chunk(kara, d)
+    assert st == 0
+    check_chunk(d, got)
+    bad = dict(d, lengths=d["lengths"].copy())
+    refused = [i for i in (3, n // 2, n - 2) if n_new[i] > 0]
+    for i in refused:
+        bad["lengths"][i] = n_new[i] - 1
+    again, st = run_chunk(kara, bad)
+    assert st == (kara.EINVAL if refused else 0)
+    for s in range(n):
+        rows = slice(d["q_start"][s], d["q_start"][s + 1])
+        assert s not in refused or (again[rows] == 0).all()
+    pick = [t for s in range(n) if s not in refused for t in range(d["q_start"][s], d["q_start"][s + 1])]
+    check_chunk(d, again, rows=pick)
+
+
+def test_chunk_results_repeat_bit_for_bit():
+    """Cuts and merges follow the lengths, not the timing."""
+    kara = lib()
+    d = chunk_inputs(98, [4000, 700, 33, 2048], [3, 400, 33, 1], 8, 2, 128)
+    first, st = run_chunk(kara, d)
+    assert st == 0
+    for _ in range(20):
+        assert torch.equal(run_chunk(kara, d)[0], first)
+
+
+def test_chunk_output_alignment():
+    """Outputs on a 16-byte boundary that is no 32-byte one."""
+    kara = lib()
+    d = chunk_inputs(99, [300, 40], [100, 3], 8, 2, 128)
+    want, _ = run_chunk(kara, d)
+    k, v, q = (d[x].to(DEV) for x in ("k", "v", "q"))
+    c, t = kara.cache(k, v, 8), chunk_tokens(kara, d)
+    flat = torch.full((q.numel() + 8,), 77.0, dtype=torch.bfloat16, device=DEV)
+    out = flat[8:].view(q.shape)
+    assert out.data_ptr() % 32 == 16
+    ws = torch.empty(kara.kara_chunk_workspace_size(c, t.n, t.rows), dtype=torch.uint8, device=DEV)
+    err = error_word()
+    kara.kara_chunk_attention(c, 0, t, i32(d["bt"]), q, out, ws, err)
+    assert kara.kara_get_error(err) == 0 and torch.equal(out.cpu(), want) and (flat[:8] == 77.0).all()
