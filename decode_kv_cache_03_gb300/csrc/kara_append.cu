@@ -235,7 +235,26 @@ __host__ __device__ __forceinline__ int tok_stage_bytes(int hq, int hkv, int D, 
     return (hq + 2 * hkv) * D * 2 + rot * 4;
 }
 
-template <int D>
+// (a*b) on both halves, round-to-nearest.
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b)
+{
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+
+// Eight bf16 as pairs of neighbours, in fp32; with `swap` each pair the other way round.
+__device__ __forceinline__ void pairs4(const uint4 &u, uint64_t (&x)[4], bool swap)
+{
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const float lo = bf_lo(w[e]), hi = bf_hi(w[e]);
+        x[e] = swap ? ptx::pack2(hi, lo) : ptx::pack2(lo, hi);
+    }
+}
+
+template <int D, bool INTER>
 __global__ void __launch_bounds__(kTokThreads, 4) append_staged_kernel(const AppArgs a, int stages)
 {
     constexpr int LPR = D / 8, RPP = 32 / LPR;
@@ -319,7 +338,7 @@ __global__ void __launch_bounds__(kTokThreads, 4) append_staged_kernel(const App
     const int l = lane % LPR, d0 = l * 8, sub = lane / LPR;
     const bool turned = d0 < a.rot, low = d0 < half;
     // the other half of this lane's pairs: 16 bytes further on or back (interleaved: in the lane itself)
-    const int o0 = !turned || a.inter ? d0 : low ? d0 + half : d0 - half;
+    const int o0 = !turned || INTER ? d0 : low ? d0 + half : d0 - half;
     // weights of this lane's dims and of their partners (1 without a norm)
     const uint4 one = make_uint4(0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u);
     const uint4 wq = a.qw ? *reinterpret_cast<const uint4 *>(a.qw + d0) : one;
@@ -334,36 +353,34 @@ __global__ void __launch_bounds__(kTokThreads, 4) append_staged_kernel(const App
         if (m.page < 0) return;
         const uint16_t *rows = reinterpret_cast<const uint16_t *>(buf + st * stage_bytes);
         const float *tab = reinterpret_cast<const float *>(buf + st * stage_bytes + row_bytes);
-        float c[8], sn[8];
+        // cosines and signed sines of this lane's dims, in pairs of neighbours
+        uint64_t c[4], sn[4];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) c[e] = 1.f, sn[e] = 0.f;
-        if (turned && a.inter) {
+        for (int e = 0; e < 4; ++e) c[e] = ptx::pack2(1.f, 1.f), sn[e] = ptx::pack2(0.f, 0.f);
+        if (turned && INTER) {
             const float4 cc = *reinterpret_cast<const float4 *>(tab + d0 / 2);
             const float4 ss = *reinterpret_cast<const float4 *>(tab + half + d0 / 2);
-            c[0] = c[1] = cc.x, c[2] = c[3] = cc.y, c[4] = c[5] = cc.z, c[6] = c[7] = cc.w;
-            sn[1] = ss.x, sn[3] = ss.y, sn[5] = ss.z, sn[7] = ss.w;
-            sn[0] = -ss.x, sn[2] = -ss.y, sn[4] = -ss.z, sn[6] = -ss.w;
+            c[0] = ptx::pack2(cc.x, cc.x), c[1] = ptx::pack2(cc.y, cc.y);
+            c[2] = ptx::pack2(cc.z, cc.z), c[3] = ptx::pack2(cc.w, cc.w);
+            sn[0] = ptx::pack2(-ss.x, ss.x), sn[1] = ptx::pack2(-ss.y, ss.y);
+            sn[2] = ptx::pack2(-ss.z, ss.z), sn[3] = ptx::pack2(-ss.w, ss.w);
         } else if (turned) {
             const int j0 = low ? d0 : d0 - half;
-            const float sg = low ? -1.f : 1.f;
+            const uint64_t sg = low ? ptx::pack2(-1.f, -1.f) : ptx::pack2(1.f, 1.f);
 #pragma unroll
-            for (int e = 0; e < 8; e += 4) {
-                const float4 cc = *reinterpret_cast<const float4 *>(tab + j0 + e);
-                const float4 ss = *reinterpret_cast<const float4 *>(tab + half + j0 + e);
-                c[e] = cc.x, c[e + 1] = cc.y, c[e + 2] = cc.z, c[e + 3] = cc.w;
-                sn[e] = sg * ss.x, sn[e + 1] = sg * ss.y, sn[e + 2] = sg * ss.z, sn[e + 3] = sg * ss.w;
+            for (int e = 0; e < 4; e += 2) {
+                const float4 cc = *reinterpret_cast<const float4 *>(tab + j0 + 2 * e);
+                const float4 ss = *reinterpret_cast<const float4 *>(tab + half + j0 + 2 * e);
+                c[e] = ptx::pack2(cc.x, cc.y), c[e + 1] = ptx::pack2(cc.z, cc.w);
+                sn[e] = mul2(sg, ptx::pack2(ss.x, ss.y)), sn[e + 1] = mul2(sg, ptx::pack2(ss.z, ss.w));
             }
         }
         // a query row's factors: weight times cosine, and the partner's weight times sine
-        float qa[8], qb[8];
-        unpack8(wq, qa);
-        unpack8(wqo, qb);
-        if (a.inter) {
+        uint64_t qa[4], qb[4];
+        pairs4(wq, qa, false);
+        pairs4(wqo, qb, INTER);
 #pragma unroll
-            for (int e = 0; e < 8; e += 2) qb[e] = qa[e + 1], qb[e + 1] = qa[e];
-        }
-#pragma unroll
-        for (int e = 0; e < 8; ++e) qa[e] *= c[e], qb[e] *= sn[e];
+        for (int e = 0; e < 4; ++e) qa[e] = mul2(qa[e], c[e]), qb[e] = mul2(qb[e], sn[e]);
         uint16_t *qrow = a.q_out + (int64_t)m.row * a.hq * D + d0;
         for (int h = warp * RPP + sub; h - sub < nrow; h += kTokWarps * RPP) {
             const bool in = h < nrow, is_q = h < a.hq, is_v = h >= a.hq + a.hkv;
@@ -374,40 +391,42 @@ __global__ void __launch_bounds__(kTokThreads, 4) append_staged_kernel(const App
             }
             if (__any_sync(0xffffffffu, in && !is_v)) {
                 // z = (x w c + x' w' s) / sqrt(mean(x^2) + eps), x' and w' of the pair's other member
-                float x[8], xo[8];
-                unpack8(u, x);
-                unpack8(uo, xo);
+                uint64_t x[4], xo[4], z[4];
+                pairs4(u, x, false);
+                pairs4(uo, xo, INTER);
                 float inv = 1.f;
                 if (a.qw || a.kw) {
-                    float ss = 0.f;
+                    uint64_t s2 = mul2(x[0], x[0]);
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], ss);
+                    for (int e = 1; e < 4; ++e) s2 = ptx::fma2(x[e], x[e], s2);
+                    float ss, hi;
+                    ptx::unpack2(s2, ss, hi);
+                    ss += hi;
 #pragma unroll
                     for (int o = LPR / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
                     if (is_q ? a.qw : a.kw) inv = rsqrtf(ss * (1.f / D) + a.eps);
                 }
-                float z[8];
-                if (a.inter) {
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) xo[e] = x[e ^ 1];
-                }
                 if (__all_sync(0xffffffffu, is_q)) {
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) z[e] = fmaf(x[e], qa[e], xo[e] * qb[e]) * inv;
+                    for (int e = 0; e < 4; ++e) z[e] = ptx::fma2(x[e], qa[e], mul2(xo[e], qb[e]));
                 } else {
-                    float w[8], wo[8];
-                    unpack8(is_q ? wq : wk, w);
-                    unpack8(is_q ? wqo : wko, wo);
-                    if (a.inter) {
+                    uint64_t w[4], wo[4];
+                    pairs4(is_q ? wq : wk, w, false);
+                    pairs4(is_q ? wqo : wko, wo, INTER);
 #pragma unroll
-                        for (int e = 0; e < 8; e += 2) wo[e] = w[e + 1], wo[e + 1] = w[e];
-                    }
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) z[e] = fmaf(x[e], w[e] * c[e], xo[e] * (wo[e] * sn[e])) * inv;
+                    for (int e = 0; e < 4; ++e)
+                        z[e] = ptx::fma2(x[e], mul2(w[e], c[e]), mul2(xo[e], mul2(wo[e], sn[e])));
                 }
                 if (!is_v) {
-                    u.x = pack_bf16(z[0], z[1]), u.y = pack_bf16(z[2], z[3]);
-                    u.z = pack_bf16(z[4], z[5]), u.w = pack_bf16(z[6], z[7]);
+                    const uint64_t i2 = ptx::pack2(inv, inv);
+                    uint32_t r[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        float lo, hi;
+                        ptx::unpack2(mul2(z[e], i2), lo, hi);
+                        r[e] = pack_bf16(lo, hi);
+                    }
+                    u = make_uint4(r[0], r[1], r[2], r[3]);
                 }
             }
             if (!in) continue;
@@ -446,14 +465,14 @@ cudaError_t launch(const AppArgs &a, cudaStream_t st)
     }
     if (stages > kTokMaxStages) stages = kTokMaxStages;
     const size_t smem = head + (size_t)stages * sb;
-    cudaError_t e =
-        cudaFuncSetAttribute(append_staged_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    const auto kern = a.inter ? append_staged_kernel<D, true> : append_staged_kernel<D, false>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     int dev = 0, sms = 0;
     if (e == cudaSuccess) e = cudaGetDevice(&dev);
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     if (e != cudaSuccess) return e;
     const int grid = a.rows < sms * per_sm ? a.rows : sms * per_sm;
-    return launch_dependent(append_staged_kernel<D>, dim3((unsigned)grid), kTokThreads, smem, st, a, stages);
+    return launch_dependent(kern, dim3((unsigned)grid), kTokThreads, smem, st, a, stages);
 }
 
 }  // namespace

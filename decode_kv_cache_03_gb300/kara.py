@@ -208,7 +208,7 @@ def _raw_stream(err: torch.Tensor, stream):
     """The stream's handle, the current one of err's device if None (torch.cuda.current_stream costs
     several microseconds of host time, as much as a whole small call)."""
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(err.device.index)
+        return torch._C._cuda_getCurrentRawStream(err.get_device())
     return stream.cuda_stream
 
 
@@ -274,29 +274,28 @@ def kara_extend_tables(num_blocks: int, block_size: int, lengths: torch.Tensor, 
                                    t, n_used.data_ptr(), err.data_ptr(), _raw_stream(err, stream)), "kara_extend_tables")
 
 
-def _token_stride(x: torch.Tensor, rows: int, heads: int, d: int) -> int:
-    assert x.dtype == torch.bfloat16 and x.shape == (rows, heads, d)
-    assert x.stride(2) == 1 and (heads == 1 or x.stride(1) == d)
-    return x.stride(0) if rows > 1 else heads * d
-
-
 def kara_append_kv(c: Cache, layer: int, t: Tokens, r: Rope, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
                    q_out: torch.Tensor, err: torch.Tensor, ring=None, stream=None):
     """Norm and rotate q [rows][num_q_heads][D] and k [rows][num_kv_heads][D] and write k, v into layer
     `layer` of the cache at t's slots, queries to q_out (and to ring [n][layers][num_q_heads][W][D])."""
     _same_device(err, "kara_append_kv", q, k, v, q_out, ring, c, t, *r.on)
-    d, W = c.head_dim, 0
-    qs, ks, vs = (_token_stride(x, t.rows, h, d) for x, h in
-                  ((q, c.num_q_heads), (k, c.num_kv_heads), (v, c.num_kv_heads)))
-    assert q_out.dtype == torch.bfloat16 and q_out.shape == q.shape and q_out.is_contiguous()
+    hq, hkv, d, rows, W = c.num_q_heads, c.num_kv_heads, c.head_dim, t.rows, 0
+    assert q.dtype == k.dtype == v.dtype == q_out.dtype == torch.bfloat16
+    assert q.shape == q_out.shape == (rows, hq, d) and k.shape == v.shape == (rows, hkv, d)
+    strides = []
+    for x, heads in ((q, hq), (k, hkv), (v, hkv)):   # rows apart as they like, their heads contiguous
+        a, b, e = x.stride()
+        assert e == 1 and (b == d or heads == 1)
+        strides.append(a if rows > 1 else heads * d)
+    assert q_out.is_contiguous()
     assert r.head_dim <= {d} and (r.n is None or r.n == t.n)
     if ring is not None:
         W = ring.shape[3]
         assert ring.dtype == torch.bfloat16 and ring.is_contiguous()
-        assert ring.shape == (t.n, c.num_layers, c.num_q_heads, W, d)
-    _check(_lib.kara_append_kv(c, layer, t, r, q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs,
-                               q_out.data_ptr(), None if ring is None else ring.data_ptr(), W, err.data_ptr(),
-                               _raw_stream(err, stream)), "kara_append_kv")
+        assert ring.shape == (t.n, c.num_layers, hq, W, d)
+    _check(_lib.kara_append_kv(c, layer, t, r, q.data_ptr(), strides[0], k.data_ptr(), strides[1], v.data_ptr(),
+                               strides[2], q_out.data_ptr(), None if ring is None else ring.data_ptr(), W,
+                               err.data_ptr(), _raw_stream(err, stream)), "kara_append_kv")
 
 
 def kara_chunk_workspace_size(c: Cache, n: int, rows: int) -> int:
