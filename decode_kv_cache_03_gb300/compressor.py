@@ -63,7 +63,8 @@ class Compressor:
 
     def chunk(self, layer: int, t, block_table, q, out, stream=None):
         """Enqueue causal attention of the new tokens for one layer over the paged cache,
-        after append() wrote their K and V."""
+        after append() wrote their K and V.  The calls of one Compressor share a workspace:
+        they run one after another, on one stream or ordered by events."""
         need = kara.kara_chunk_workspace_size(self.cache, t.n, t.rows)
         if self._cws.numel() < need:
             self._cws = torch.empty(need, dtype=torch.uint8, device=self.k.device)

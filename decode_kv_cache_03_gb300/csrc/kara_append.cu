@@ -158,6 +158,10 @@ __global__ void __launch_bounds__(kAppThreads) append_kernel(const AppArgs a)
 #pragma unroll
             for (int e = 0; e < 8; ++e) z[e] = fmaf(y[e], c[e], __shfl_sync(0xffffffffu, y[e], other) * sn[e]);
         }
+        if (!turned) {  // (0 times an infinity is no number)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) z[e] = y[e];
+        }
         if (!is_v) {
             u.x = pack_bf16(z[0], z[1]), u.y = pack_bf16(z[2], z[3]);
             u.z = pack_bf16(z[4], z[5]), u.w = pack_bf16(z[6], z[7]);
@@ -416,6 +420,12 @@ __global__ void __launch_bounds__(kTokThreads, 4) append_staged_kernel(const App
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
                         z[e] = ptx::fma2(x[e], mul2(w[e], c[e]), mul2(xo[e], mul2(wo[e], sn[e])));
+                }
+                if (a.rot < D && !turned) {  // (0 times an infinity is no number)
+                    uint64_t w[4];
+                    pairs4(is_q ? wq : wk, w, false);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) z[e] = mul2(x[e], w[e]);
                 }
                 if (!is_v) {
                     const uint64_t i2 = ptx::pack2(inv, inv);

@@ -912,3 +912,33 @@ def test_chunk_output_alignment():
     err = error_word()
     kara.kara_chunk_attention(c, 0, t, i32(d["bt"]), q, out, ws, err)
     assert kara.kara_get_error(err) == 0 and torch.equal(out.cpu(), want) and (flat[:8] == 77.0).all()
+
+
+@pytest.mark.parametrize("rows", [3, 3000])
+@pytest.mark.parametrize("rot,inter", [(0, False), (32, False), (32, True)])
+def test_append_passes_dims_through_bit_for_bit(rows, rot, inter):
+    """Without a norm, dims past rot_dim (all of them without a rotation) keep their bits, infinities, NaN
+    and the sign of zero among them, in short calls and in staged ones."""
+    kara = lib()
+    hq, hkv, D = 4, 2, 64
+    q, k, v = append_inputs(rows + rot, hq, hkv, D, rows, fused=False)
+    for x in (q, k, v):
+        x[0, 0, rot:rot + 5] = torch.tensor([float("inf"), -float("inf"), float("nan"), -0.0, 0.0])
+        x[rows - 1, 1, 40:43] = torch.tensor([-0.0, float("inf"), 3e38])
+    nb = rows // 16 + 1
+    kp = torch.zeros(1, nb, hkv, 16, D, dtype=torch.bfloat16, device=DEV)
+    vp = torch.zeros_like(kp)
+    t = kara.tokens(i32([0, rows]), i32([rows]), torch.arange(rows, device=DEV), i32([0] * rows), i32(range(rows)))
+    out = torch.empty(rows, hq, D, dtype=torch.bfloat16, device=DEV)
+    err = error_word()
+    cs = angles(rows, rot).to(DEV) if rot else None
+    kara.kara_append_kv(kara.cache(kp, vp, hq), 0, t, kara.rope(cs, interleaved=inter), q.to(DEV), k.to(DEV),
+                        v.to(DEV), out, err)
+    assert kara.kara_get_error(err) == 0
+    rows_of = lambda p: p.cpu()[0].permute(0, 2, 1, 3).reshape(-1, hkv, D)[:rows]  # noqa: E731
+    for got, want in ((out.cpu(), q), (rows_of(kp), k)):
+        a, b = got[..., rot:].contiguous().view(torch.int16), want[..., rot:].contiguous().view(torch.int16)
+        nan = torch.isnan(want[..., rot:])
+        assert torch.equal(a[~nan], b[~nan]) and torch.isnan(got[..., rot:][nan]).all()
+        assert torch.isfinite(got[1:-1, :, :rot]).all()
+    assert torch.equal(rows_of(vp).contiguous().view(torch.int16), v.view(torch.int16))
