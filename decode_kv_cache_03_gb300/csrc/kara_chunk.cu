@@ -34,7 +34,8 @@
 //     tile).  The rows that do see such a value get it added at the end.
 //   * Every CTA gets the same work (to within a key tile), whatever the lengths:
 //     all items' key tiles, weighted by what they cost, are laid end to end and cut
-//     evenly.  A cut inside an item leaves partial (O, max, sum) in the workspace,
+//     evenly; in long calls whose items share keys, whole items go round the CTAs
+//     first, so that L2 serves the keys again (share_out).  A cut inside an item leaves partial (O, max, sum) in the workspace,
 //     joined by the merge kernel in CTA order, so results do not depend on timing.
 //
 // What set the pace on the way (8192 tokens over 16384 keys, 40/8 heads, D 128; us):
@@ -47,7 +48,8 @@
 // the instruction caches (one copy of the epilogue's code and of the MMAs', the control
 // warps' waiting out of line, one warp that walks over the work and tells the others), 1390
 // (512 tokens x 32 sequences at 4096 keys: 852 -> 750); the weighted sum begun on half the
-// weights, 1330 to 1370 on several boxes (1.5 PFLOP/s, 0.8 of the measured cuBLAS burst).
+// weights, 1330 to 1370 on several boxes (1.5 PFLOP/s, 0.8 of the measured cuBLAS burst); whole
+// items dealt round, 1310 to 1365 (the 32 sequences: 750 to 780 -> 680 to 705).
 // Few rows over long caches (4 tokens x 128 sequences) read K and V at 6.9 to 7.0 TB/s.
 // What is left: a step of two query tiles takes about 2950 clocks against 2048 of tensor time
 // (logits, exponentials and weighted sum of a tile depend on each other, and TMEM holds
@@ -76,6 +78,7 @@ constexpr int kBlkPerTile = kTile / kBlk;
 constexpr int kStages = 5;       // K and V tiles in flight
 static_assert((kStages + 1) / 2 < 4, "V tiles in the ring: Shared::edge and odd_values tell four apart");
 constexpr int kMaxCtas = 160;    // CTAs of the attention kernel, at most (workspace slots)
+constexpr int kMaxRounds = 64;   // whole items that a CTA takes ahead of its range, at most
 constexpr int kThreads = 512;    // two softmax warpgroups, two control warpgroups
 constexpr int kWarpKv = 8, kWarpMma = 10, kWarpQ = 12;  // 8: K, 9: V; 10, 11: the MMAs of each query tile
 // Registers per thread: at launch (65536 / 512), then after the warpgroups trade:
@@ -97,9 +100,11 @@ struct Item {
     int32_t m;      // new tokens of the sequence; 0: it has no items
 };
 
-// Where a CTA starts, and the one before it ends: key tile `off` of the item of tokens 2 TQ
-// `pair` on of sequence `seq` for KV head `head` (off == nt: behind its last one; the end of
-// everything: head hkv).
+// All items in order: head by head, sequence by sequence, 2 TQ tokens (a `pair` of query tiles)
+// after another.  A CTA takes some whole items, and then a range.
+//
+// Where its range starts, and the one before it ends: key tile `off` of an item (off == nt: behind
+// its last one; the end of everything: head hkv).
 struct __align__(16) Start {
     int32_t head, seq, pair, off;
 };
@@ -117,6 +122,7 @@ struct ChunkArgs {
     uint16_t *out;
     int32_t *used_ctas;  // CTAs that got work
     Start *start;        // [used_ctas + 1]
+    Start *whole;        // [ctas][kMaxRounds]: each CTA's whole items
     float4 *part;        // [2 * ctas][D / 4][256]
     float2 *stat;        // [2 * ctas][256]: (max, sum) in the log2 domain
     const uint16_t *v;   // V pool at the call's layer
@@ -137,6 +143,7 @@ __device__ __forceinline__ bool chunk_ok(const ChunkArgs &a, int32_t r0, int32_t
 __device__ __forceinline__ int tile_cost(const ChunkArgs &a, int32_t ntok) { return ntok > a.TQ ? 4 : 3; }
 constexpr int kItemCost = 8;
 constexpr int kTilesPerCta = 2;  // fewer, and CTAs stay without work: a split costs a merge
+constexpr int kSharedTiles = 128;  // key tiles per CTA from which whole items are dealt round
 
 // The item `pair` of sequence `seq`.
 __device__ __forceinline__ Item make_item(const ChunkArgs &a, int seq, int pair)
@@ -150,6 +157,13 @@ __device__ __forceinline__ Item make_item(const ChunkArgs &a, int seq, int pair)
     it.pos0 = it.len - it.m + t0;
     it.nt = (it.pos0 + it.ntok - 1) / kTile + 1;
     return it;
+}
+
+// Query-tile pairs of a sequence.
+__device__ __forceinline__ int32_t pairs_of(const ChunkArgs &a, int seq)
+{
+    const int32_t m = make_item(a, seq, 0).m, per = 2 * a.TQ;
+    return m / per + (m % per != 0);
 }
 
 // ---- attention ------------------------------------------------------------------
@@ -173,6 +187,8 @@ struct Shared {
     // 1 + the last piece (by its number mod 4) whose V had values that are not finite
     int32_t fixed[4], odd_values[4];
     Start from, to;       // this CTA's range
+    int32_t rounds;       // whole items ahead of it
+    int64_t cut[2];       // its range of the costs of what is not taken whole
     int4 piece[kPieces][3];  // pieces of it, by their number mod kPieces
     uint64_t piece_full[kPieces], piece_empty[kPieces];
     longlong2 scan[kThreads / 32 + 1];
@@ -401,19 +417,118 @@ __device__ __forceinline__ Start place(const ChunkArgs &a, int head, int seq, in
     }
 }
 
-// All items' key tiles of all heads, weighted by their cost and laid end to end, are cut into
-// equal ranges; this CTA's goes to sh->from and sh->to (equal: nothing), and to the workspace for
-// the merge.  Prefix sums over the sequences, a thread each (over 512 sequences: in passes, twice
-// over); a plan kernel ahead of this one took 3 us more.
-__device__ void cut_range(const ChunkArgs &a, Shared *sh)
+// Item i of all, of which each head has per_head; `first` has those ahead of every 2^shift-th sequence.
+__device__ Start find_item(const ChunkArgs &a, const int32_t *first, int shift, int32_t per_head, int32_t i)
+{
+    const int32_t head = i / per_head;
+    int32_t r = i % per_head;
+    int lo = 0, hi = ((a.n - 1) >> shift) + 1;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (first[mid] <= r) lo = mid; else hi = mid;
+    }
+    r -= first[lo];
+    for (int s = lo << shift;; ++s) {
+        const int32_t pairs = pairs_of(a, s);
+        if (r < pairs || s + 1 == a.n) return Start{head, s, r, 0};
+        r -= pairs;
+    }
+}
+
+// Whole items go round the CTAs, as many rounds as leave no CTA above the average cost; the rest is
+// cut so that all come to it.  False: no sequence has more than one pair.  (Items fit in 32 bits: each has 500 bytes or more of query, output, K and V.)
+__device__ __noinline__ bool whole_items(const ChunkArgs &a, Shared *sh, int ctas, int64_t units, int32_t *scratch,
+                                         int scratch_words)
+{
+    const int tid = threadIdx.x, cta = blockIdx.x;
+    bool shared = false;
+    for (int s = tid; s < a.n; s += kThreads) shared = shared || make_item(a, s, 0).m > 2 * a.TQ;
+    if (!__syncthreads_or(shared)) return false;
+    int shift = 0;
+    while (((a.n - 1) >> shift) >= scratch_words / 2) ++shift;
+    const int marks = ((a.n - 1) >> shift) + 1;
+    int32_t per_head = 0;
+    longlong2 tot;
+    for (int base = 0; base < a.n; base += kThreads) {
+        const int s = base + tid;
+        const int32_t own = s < a.n ? pairs_of(a, s) : 0;
+        const longlong2 in = cta_scan2(make_longlong2(own, 0), sh->scan, tot);
+        if (s < a.n && (s & ((1 << shift) - 1)) == 0) scratch[s >> shift] = per_head + (int32_t)in.x - own;
+        per_head += (int32_t)tot.x;
+    }
+    const int32_t items = per_head * a.hkv;
+    if (tid == 0) sh->rounds = kMaxRounds;
+    __syncthreads();
+    // every item's cost, kept if there is room
+    int32_t *cost = items <= scratch_words - marks ? scratch + marks : nullptr;
+    const auto work_out = [&](int32_t i) {
+        const Start p = find_item(a, scratch, shift, per_head, i);
+        const Item it = make_item(a, p.seq, p.pair);
+        return it.nt * tile_cost(a, it.ntok) + kItemCost;
+    };
+    const auto cost_of = [&](int32_t i) { return cost ? cost[i] : work_out(i); };
+    if (cost) {
+        for (int32_t i = tid; i < items; i += kThreads) cost[i] = work_out(i);
+        __syncthreads();
+    }
+    const int64_t mean = units / ctas, more = units % ctas;
+    int64_t mine = 0;
+    if (tid < ctas) {
+        int k = 0;
+        for (; k < kMaxRounds && k * ctas + ctas <= items; ++k) {
+            mine += cost_of(k * ctas + tid);
+            if (mine > mean) break;
+        }
+        atomicMin(&sh->rounds, k);
+    }
+    __syncthreads();
+    const int rounds = sh->rounds;
+    mine = 0;
+    if (tid < ctas)
+        for (int k = 0; k < rounds; ++k) mine += cost_of(k * ctas + tid);
+    const longlong2 lack = make_longlong2(tid < ctas ? mean - mine : 0, 0), in = cta_scan2(lack, sh->scan, tot);
+    if (tid == cta) sh->cut[0] = in.x - lack.x + more * cta / ctas, sh->cut[1] = in.x + more * (cta + 1) / ctas;
+    __syncthreads();
+    int64_t before = 0;
+    for (int32_t base = rounds * ctas; base < items; base += kThreads) {
+        const int32_t i = base + tid;
+        const int32_t own = i < items ? cost_of(i) : 0;
+        const longlong2 x = cta_scan2(make_longlong2(own, 0), sh->scan, tot);
+        const int64_t lo = before + x.x - own, hi = before + x.x;
+        for (int e = 0; e < 2; ++e) {
+            const int64_t u = sh->cut[e];
+            if (lo <= u && u < hi) {
+                Start p = find_item(a, scratch, shift, per_head, i);
+                const Item it = make_item(a, p.seq, p.pair);
+                p.off = (int32_t)min((int64_t)it.nt, (u - lo) / tile_cost(a, it.ntok));
+                if (e) sh->to = p; else sh->from = p;
+            }
+        }
+        before += tot.x;
+    }
+    if (tid < rounds) a.whole[cta * kMaxRounds + tid] = find_item(a, scratch, shift, per_head, tid * ctas + cta);
+    fence_proxy_async_smem();  // the scratch is the ring of the copies that follow
+    return true;
+}
+
+// What this CTA does: sh->rounds whole items (listed in the workspace), then the range from sh->from
+// to sh->to of what no CTA takes whole (equal: nothing; kept in the workspace too, for the merge).
+// All items' key tiles of all heads, weighted by their cost and laid end to end, are cut into equal
+// ranges: prefix sums over the sequences, a thread each (over 512 sequences: in passes, twice over).
+// That alone has a CTA read the same keys again for each pair of query tiles, long after they have
+// left L2 when there are many caches.  So where items share keys, whole items go round the CTAs
+// first, those of the same keys at the same time: 512 tokens x 32 sequences at 4096 keys read 0.70 GB
+// from HBM and not 4.24, and take 680 to 705 us and not 750 to 780.  It takes about 1.5 us more ahead
+// of the first key tile, and gains nothing while a CTA has few: 82 to 86 against 80 us at 40 key tiles
+// a CTA, 128 to 132 against 131.5 at 80, 130.6 against 129.7 at 110.  It starts at kSharedTiles = 128.
+// Every CTA works all of this out for itself, from the lengths; a plan kernel ahead of this one
+// took 3 us more.
+__device__ void share_out(const ChunkArgs &a, Shared *sh, int32_t *scratch, int scratch_words)
 {
     const int tid = threadIdx.x, cta = blockIdx.x;
     const bool one_pass = a.n <= kThreads;
     longlong2 sum = make_longlong2(0, 0), own = sum, in = sum;
-    if (tid == 0) {
-        sh->from.head = sh->to.head = a.hkv;
-        sh->from.seq = sh->to.seq = sh->from.pair = sh->to.pair = sh->from.off = sh->to.off = 0;
-    }
+    if (tid == 0) sh->from = sh->to = Start{a.hkv, 0, 0, 0}, sh->rounds = 0;
     for (int base = 0; base < a.n; base += kThreads) {
         const int s = base + tid;
         own = s < a.n ? seq_cost(a, s) : make_longlong2(0, 0);
@@ -423,7 +538,9 @@ __device__ void cut_range(const ChunkArgs &a, Shared *sh)
     }
     const int64_t units = sum.x * a.hkv;
     const int ctas = sum.y == 0 ? 0 : (int)max(1ll, min((long long)a.ctas, sum.y * a.hkv / kTilesPerCta));
-    if (cta < ctas) {
+    const bool whole = sum.y * a.hkv >= (int64_t)kSharedTiles * a.ctas
+                       && whole_items(a, sh, ctas, units, scratch, scratch_words);
+    if (!whole && cta < ctas) {
         // (both ends: r = cost within the head; the last range ends with everything)
         const int64_t u0 = units * cta / ctas, u1 = units * (cta + 1) / ctas;
         const int64_t r0 = u0 % sum.x, r1 = u1 % sum.x;
@@ -462,10 +579,13 @@ __device__ __forceinline__ int64_t partial_slot(int cta, bool inside) { return 2
 
 struct Walk {
     const ChunkArgs &a;
+    const Start *whole;
+    int rounds, round;
     Start at, end;
     Item it;  // at `at`
     __device__ Walk(const ChunkArgs &args, const Shared *sh) : a(args)
     {
+        whole = a.whole + blockIdx.x * kMaxRounds, rounds = sh->rounds, round = 0;
         at = sh->from, end = sh->to;
         if (at.head < a.hkv) {
             it = make_item(a, at.seq, at.pair);
@@ -488,6 +608,16 @@ struct Walk {
     }
     __device__ bool step(Piece &p)
     {
+        if (round < rounds) {
+            const Start w = whole[round++];
+            p.it = make_item(a, w.seq, w.pair);
+            p.seq = w.seq;
+            p.head = w.head;
+            p.j0 = 0;
+            p.j1 = p.it.nt;
+            p.whole = true;
+            return true;
+        }
         if (at.head >= a.hkv) return false;
         const bool last = same_item(at, end);
         p.it = it;
@@ -764,7 +894,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     if (blockIdx.x == gridDim.x - 1) refuse_sequences(a);
-    cut_range(a, sh);
+    share_out(a, sh, reinterpret_cast<int32_t *>(ring), kStages * C::kTileBytes / 4);
 
     if (warp >= 8) {
         reg_dealloc<kRegsCtl>();
@@ -1202,9 +1332,9 @@ cudaError_t query_map(CUtensorMap *m, const void *q, const kara_cache *c, int32_
     return cudaSuccess;
 }
 
-// Workspace: [CTAs with work][starts][stats][partials].
+// Workspace: [CTAs with work][starts][whole items][stats][partials].
 struct Layout {
-    size_t start, stat, part, total;
+    size_t start, whole, stat, part, total;
 };
 
 Layout layout(const kara_cache *c)
@@ -1212,6 +1342,7 @@ Layout layout(const kara_cache *c)
     Layout l;
     size_t o = 256;
     l.start = o, o += align256((kMaxCtas + 1) * sizeof(Start));
+    l.whole = o, o += align256((size_t)kMaxCtas * kMaxRounds * sizeof(Start));
     l.stat = o, o += align256((size_t)2 * kMaxCtas * 256 * sizeof(float2));
     l.part = o, o += (size_t)2 * kMaxCtas * 256 * c->head_dim * sizeof(float);
     l.total = o;
@@ -1263,6 +1394,7 @@ cudaError_t launch_chunk(const kara_cache *c, int32_t layer, const kara_tokens *
     char *w = static_cast<char *>(ws);
     a.used_ctas = reinterpret_cast<int32_t *>(w);
     a.start = reinterpret_cast<Start *>(w + l.start);
+    a.whole = reinterpret_cast<Start *>(w + l.whole);
     a.stat = reinterpret_cast<float2 *>(w + l.stat);
     a.part = reinterpret_cast<float4 *>(w + l.part);
     a.wide = ((uintptr_t)out & 31u) == 0;

@@ -888,6 +888,39 @@ def test_chunk_more_sequences_than_one_pass(n):
     check_chunk(d, again, rows=pick)
 
 
+@pytest.mark.parametrize("lengths, n_new, hq, hkv, D", [
+    ([9000, 8300, 900, 2600], [1200, 800, 0, 5], 40, 8, 128),   # whole items ahead of the ranges
+    ([2000] * 80, [300] * 80, 8, 8, 64),                        # two costs, in turn
+    ([9000, 400, 300], [1, 400, 290], 16, 4, 64),               # too little work for whole items
+    ([8000], [4000], 32, 4, 128),                               # one sequence, each pair sees more than the last
+    ([2100, 17, 2100, 40], [2100, 1, 1500, 40], 2, 2, 128),
+])
+def test_chunk_items_of_shared_keys(lengths, n_new, hq, hkv, D):
+    """Batches whose pairs of query tiles share keys: CTAs take whole items ahead of their ranges."""
+    kara = lib()
+    d = chunk_inputs(61, lengths, n_new, hq, hkv, D, extra=3)
+    got, st = run_chunk(kara, d)
+    assert st == 0
+    check_chunk(d, got)
+    again, st = run_chunk(kara, d)
+    assert st == 0 and torch.equal(got, again)
+
+
+def test_chunk_more_items_than_shared_memory_holds():
+    """Past 20480 sequences (one count for several of them) and 40960 items (no list of their costs)."""
+    kara = lib()
+    n = 21000
+    r = np.random.default_rng(5)
+    n_new = r.integers(0, 3, n).astype(np.int32)
+    n_new[[0, 7, 20481, n - 1]] = [300, 0, 513, 700]
+    lengths = n_new + r.integers(0, 3, n).astype(np.int32)
+    lengths[[0, n - 1]] += 900
+    d = chunk_inputs(62, lengths, n_new, 4, 4, 64)
+    got, st = run_chunk(kara, d)
+    assert st == 0
+    check_chunk(d, got)
+
+
 def test_chunk_results_repeat_bit_for_bit():
     """Cuts and merges follow the lengths, not the timing."""
     kara = lib()
