@@ -417,66 +417,56 @@ __device__ __forceinline__ Start place(const ChunkArgs &a, int head, int seq, in
     }
 }
 
-// Item i of all, of which each head has per_head; `first` has those ahead of every 2^shift-th sequence.
-__device__ Start find_item(const ChunkArgs &a, const int32_t *first, int shift, int32_t per_head, int32_t i)
+// Item i of all, of which each head has per_head; `first` has those ahead of each sequence.
+__device__ Start find_item(const ChunkArgs &a, const int32_t *first, int32_t per_head, int32_t i)
 {
-    const int32_t head = i / per_head;
-    int32_t r = i % per_head;
-    int lo = 0, hi = ((a.n - 1) >> shift) + 1;
+    const int32_t head = i / per_head, r = i % per_head;
+    int lo = 0, hi = a.n;
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
         if (first[mid] <= r) lo = mid; else hi = mid;
     }
-    r -= first[lo];
-    for (int s = lo << shift;; ++s) {
-        const int32_t pairs = pairs_of(a, s);
-        if (r < pairs || s + 1 == a.n) return Start{head, s, r, 0};
-        r -= pairs;
-    }
+    return Start{head, lo, r - first[lo], 0};
 }
 
 // Whole items go round the CTAs, as many rounds as leave no CTA above the average cost; the rest is
-// cut so that all come to it.  False: no sequence has more than one pair.  (Items fit in 32 bits: each has 500 bytes or more of query, output, K and V.)
+// cut so that all come to it.  False, with nothing done: no sequence has more than one pair of query
+// tiles, or there are more sequences and items than fit in the scratch memory (about 40000, or 20000
+// at D = 64; working their costs out again for each use would take a tenth of such a call).
 __device__ __noinline__ bool whole_items(const ChunkArgs &a, Shared *sh, int ctas, int64_t units, int32_t *scratch,
                                          int scratch_words)
 {
     const int tid = threadIdx.x, cta = blockIdx.x;
     bool shared = false;
     for (int s = tid; s < a.n; s += kThreads) shared = shared || make_item(a, s, 0).m > 2 * a.TQ;
-    if (!__syncthreads_or(shared)) return false;
-    int shift = 0;
-    while (((a.n - 1) >> shift) >= scratch_words / 2) ++shift;
-    const int marks = ((a.n - 1) >> shift) + 1;
-    int32_t per_head = 0;
+    if (!__syncthreads_or(shared) || a.n >= scratch_words) return false;
+    int32_t *first = scratch, *cost = scratch + a.n;
     longlong2 tot;
+    int64_t per_head = 0;
     for (int base = 0; base < a.n; base += kThreads) {
         const int s = base + tid;
-        const int32_t own = s < a.n ? pairs_of(a, s) : 0;
+        const int64_t own = s < a.n ? pairs_of(a, s) : 0;
         const longlong2 in = cta_scan2(make_longlong2(own, 0), sh->scan, tot);
-        if (s < a.n && (s & ((1 << shift) - 1)) == 0) scratch[s >> shift] = per_head + (int32_t)in.x - own;
-        per_head += (int32_t)tot.x;
+        if (s < a.n) first[s] = (int32_t)(per_head + in.x - own);
+        per_head += tot.x;
     }
-    const int32_t items = per_head * a.hkv;
+    fence_proxy_async_smem();  // the scratch is the ring of the copies that follow
+    if (per_head * a.hkv > scratch_words - a.n) return false;
+    const int32_t items = (int32_t)per_head * a.hkv;
     if (tid == 0) sh->rounds = kMaxRounds;
     __syncthreads();
-    // every item's cost, kept if there is room
-    int32_t *cost = items <= scratch_words - marks ? scratch + marks : nullptr;
-    const auto work_out = [&](int32_t i) {
-        const Start p = find_item(a, scratch, shift, per_head, i);
+    for (int32_t i = tid; i < items; i += kThreads) {
+        const Start p = find_item(a, first, (int32_t)per_head, i);
         const Item it = make_item(a, p.seq, p.pair);
-        return it.nt * tile_cost(a, it.ntok) + kItemCost;
-    };
-    const auto cost_of = [&](int32_t i) { return cost ? cost[i] : work_out(i); };
-    if (cost) {
-        for (int32_t i = tid; i < items; i += kThreads) cost[i] = work_out(i);
-        __syncthreads();
+        cost[i] = it.nt * tile_cost(a, it.ntok) + kItemCost;
     }
+    __syncthreads();
     const int64_t mean = units / ctas, more = units % ctas;
     int64_t mine = 0;
     if (tid < ctas) {
         int k = 0;
         for (; k < kMaxRounds && k * ctas + ctas <= items; ++k) {
-            mine += cost_of(k * ctas + tid);
+            mine += cost[k * ctas + tid];
             if (mine > mean) break;
         }
         atomicMin(&sh->rounds, k);
@@ -485,20 +475,20 @@ __device__ __noinline__ bool whole_items(const ChunkArgs &a, Shared *sh, int cta
     const int rounds = sh->rounds;
     mine = 0;
     if (tid < ctas)
-        for (int k = 0; k < rounds; ++k) mine += cost_of(k * ctas + tid);
+        for (int k = 0; k < rounds; ++k) mine += cost[k * ctas + tid];
     const longlong2 lack = make_longlong2(tid < ctas ? mean - mine : 0, 0), in = cta_scan2(lack, sh->scan, tot);
     if (tid == cta) sh->cut[0] = in.x - lack.x + more * cta / ctas, sh->cut[1] = in.x + more * (cta + 1) / ctas;
     __syncthreads();
     int64_t before = 0;
     for (int32_t base = rounds * ctas; base < items; base += kThreads) {
         const int32_t i = base + tid;
-        const int32_t own = i < items ? cost_of(i) : 0;
+        const int32_t own = i < items ? cost[i] : 0;
         const longlong2 x = cta_scan2(make_longlong2(own, 0), sh->scan, tot);
         const int64_t lo = before + x.x - own, hi = before + x.x;
         for (int e = 0; e < 2; ++e) {
             const int64_t u = sh->cut[e];
             if (lo <= u && u < hi) {
-                Start p = find_item(a, scratch, shift, per_head, i);
+                Start p = find_item(a, first, (int32_t)per_head, i);
                 const Item it = make_item(a, p.seq, p.pair);
                 p.off = (int32_t)min((int64_t)it.nt, (u - lo) / tile_cost(a, it.ntok));
                 if (e) sh->to = p; else sh->from = p;
@@ -506,8 +496,8 @@ __device__ __noinline__ bool whole_items(const ChunkArgs &a, Shared *sh, int cta
         }
         before += tot.x;
     }
-    if (tid < rounds) a.whole[cta * kMaxRounds + tid] = find_item(a, scratch, shift, per_head, tid * ctas + cta);
-    fence_proxy_async_smem();  // the scratch is the ring of the copies that follow
+    if (tid < rounds) a.whole[cta * kMaxRounds + tid] = find_item(a, first, (int32_t)per_head, tid * ctas + cta);
+    fence_proxy_async_smem();
     return true;
 }
 

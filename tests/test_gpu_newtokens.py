@@ -907,7 +907,7 @@ def test_chunk_items_of_shared_keys(lengths, n_new, hq, hkv, D):
 
 
 def test_chunk_more_items_than_shared_memory_holds():
-    """Past 20480 sequences (one count for several of them) and 40960 items (no list of their costs)."""
+    """Long calls whose items are too many to be dealt round keep equal ranges."""
     kara = lib()
     n = 21000
     r = np.random.default_rng(5)
