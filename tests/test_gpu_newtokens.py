@@ -921,6 +921,52 @@ def test_chunk_more_items_than_shared_memory_holds():
     check_chunk(d, got)
 
 
+def test_chunk_captured_call_follows_the_lengths():
+    """One captured call, replayed over lengths that are shared out differently: long chunks that share
+    keys, single tokens, nothing, and the long ones again, on a workspace that nobody clears."""
+    kara = lib()
+    n = 20
+    d = chunk_inputs(63, [4000] * n, [400] * n, 16, 8, 128)
+    k, v, q, bt = d["k"].to(DEV), d["v"].to(DEV), d["q"].to(DEV), i32(d["bt"])
+    c, t = kara.cache(k, v, 16), chunk_tokens(kara, d)
+    q_start = t.keep[0]
+    ws = torch.full((kara.kara_chunk_workspace_size(c, n, t.rows),), 0xff, dtype=torch.uint8, device=DEV)
+    out = torch.full(d["q"].shape, 77.0, dtype=torch.bfloat16, device=DEV)
+    err = error_word()
+    graph, s = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    kara.kara_chunk_attention(c, 0, t, bt, q, out, ws, err)   # the kernels are loaded before the capture
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph, stream=s):
+        kara.kara_chunk_attention(c, 0, t, bt, q, out, ws, err, torch.cuda.current_stream())
+    first = None
+    for new in ([400] * n, [1] * n, [0] * n, [400] * n, [0] * (n - 1) + [300]):
+        at = np.concatenate([[0], np.cumsum(new)]).astype(np.int32)
+        q_start.copy_(i32(at))
+        out.fill_(77.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert kara.kara_get_error(err) == 0
+        got = out.cpu()
+        if first is not None and new[0] == 400:
+            assert torch.equal(got, first)
+            continue
+        first = got if new[0] == 400 else first
+        check_chunk(dict(d, q_start=at), got)
+
+
+def test_stalled_long_chunk_attention_times_out(monkeypatch):
+    """The same for a call that deals whole items round."""
+    kara = lib()
+    d = chunk_inputs(64, [4000] * 20, [400] * 20, 16, 8, 128)
+    monkeypatch.setenv("KARA_DEBUG_STALL", "1")
+    _, st = run_chunk(kara, d)
+    assert st == kara.ETIMEOUT
+    monkeypatch.delenv("KARA_DEBUG_STALL")
+    got, st = run_chunk(kara, d)
+    assert st == 0
+    check_chunk(d, got, rows=list(range(0, 8000, 7)))
+
+
 def test_chunk_results_repeat_bit_for_bit():
     """Cuts and merges follow the lengths, not the timing."""
     kara = lib()
