@@ -117,6 +117,18 @@ T *at(void *ws, size_t off) { return reinterpret_cast<T *>(static_cast<char *>(w
 
 kara_status cuda_status(cudaError_t e) { return e == cudaSuccess ? KARA_OK : KARA_ECUDA; }
 
+// Zeroes one word in stream order, if it is memory that CUDA knows.
+cudaError_t zero_word(int32_t *p, cudaStream_t st)
+{
+    cudaPointerAttributes at;
+    if (!p) return cudaSuccess;
+    if (cudaPointerGetAttributes(&at, p) != cudaSuccess) {
+        cudaGetLastError();  // (no device: nothing of the step's can be there either)
+        return cudaSuccess;
+    }
+    return at.type == cudaMemoryTypeUnregistered ? cudaSuccess : cudaMemsetAsync(p, 0, sizeof(int32_t), st);
+}
+
 // ---- pipelined batches ------------------------------------------------------
 // The single-pass scorer holds one CTA per SM on the SMs its resident clusters
 // cover and leaves the rest idle (on GB300, 36 clusters of 4 CTAs take 144 of
@@ -341,7 +353,10 @@ kara_status kara_extend_tables(int32_t num_blocks, int32_t block_size, const int
     const Range range("kara_extend_tables");
     if (block_size != 16) return KARA_EUNSUPPORTED;
     if (!out || out->n < 0 || out->rows < 0 || num_blocks < 1 || bt_stride < 1 || n_fresh < 0) return KARA_EINVAL;
-    if (out->n == 0 && out->rows == 0) return KARA_OK;
+    if (out->n == 0 && out->rows == 0) {  // nothing to check and nothing taken
+        const cudaError_t e = zero_word(n_used, (cudaStream_t)stream);
+        return cuda_status(e != cudaSuccess ? e : zero_word(out->q_start, (cudaStream_t)stream));
+    }
     if (out->n > kMaxSeqs || (int64_t)bt_stride * block_size > 0x7fffffffLL || n_fresh > 0x7fffffffLL)
         return KARA_EUNSUPPORTED;
     if (out->n > 0 && (!len || !n_new || !block_table || !out->len)) return KARA_EINVAL;

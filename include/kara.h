@@ -266,7 +266,8 @@ typedef struct {
  * are unchanged, out->len[s] = len[s], q_start and *n_used are 0 and every row
  * is padding, so that the calls that follow do nothing.
  * One launch, two when out->rows is above 20480; programmatic dependents of what
- * precedes them on `stream`; the call may be captured into a CUDA graph.
+ * precedes them on `stream`; the call may be captured into a CUDA graph.  With n
+ * and rows 0 it sets q_start[0] and *n_used to 0 and launches no kernel.
  * Supported: block_size 16; n <= 65535; n_fresh and bt_stride * block_size < 2^31.
  */
 kara_status kara_extend_tables(int32_t num_blocks, int32_t block_size, const int32_t *len, const int32_t *n_new,
