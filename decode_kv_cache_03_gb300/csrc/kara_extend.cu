@@ -158,7 +158,7 @@ __global__ void __launch_bounds__(kExtThreads, 1) extend_kernel(const ExtArgs a)
 
     // ---- consumed ids: each once, and in no table of the batch (dealt over the cluster)
     const int per_row = (a.bt_stride + kScanItem - 1) / kScanItem;
-    for (int w0 = 0; plan == KARA_OK && F > 0 && w0 < a.num_blocks; w0 += a.window) {
+    for (int64_t w0 = 0; plan == KARA_OK && F > 0 && w0 < a.num_blocks; w0 += a.window) {
         if (w0 > 0) {
             __syncthreads();
             for (int i = tid; i < a.window / 32; i += kExtThreads) bits[i] = 0;

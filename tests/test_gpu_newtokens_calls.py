@@ -4,7 +4,8 @@ import pytest
 import torch
 
 from _gpu import lib
-from test_gpu_newtokens import DEV, i32, new_tokens
+from _newtokens import plain_extend
+from test_gpu_newtokens import DEV, assert_nothing_done, i32, new_tokens, run_extend
 
 pytestmark = pytest.mark.gpu
 
@@ -36,3 +37,21 @@ def test_extend_of_no_sequences_and_no_rows():
             graph.replay()
             assert used.item() == 0 and b["q_start"].tolist() == [0]
         assert fresh.tolist() == [5, 6]
+
+
+def test_extend_takes_the_largest_pool():
+    """Ids up to 2^31 - 2: every window of the bitmap is looked at, once."""
+    kara = lib()
+    nb = (1 << 31) - 1
+    lengths, n_new = np.array([20, 0], np.int32), np.array([30, 17], np.int32)
+    bt = np.array([[7, nb - 3, -1, -1], [-1, -1, -1, -1]], np.int32)
+    fresh = np.array([nb - 1, 0, (1 << 30) + 5, nb - 2], np.int32)
+    want = plain_extend(lengths, n_new, bt, fresh, 50)
+    st, got = run_extend(kara, lengths, n_new, bt, fresh, 50, nb)
+    assert st == 0 and all(np.array_equal(g, w) for g, w in zip(got, want))
+    for at, bad, code in ((2, nb - 1, kara.EDUPBLOCK), (0, nb - 3, kara.EDUPBLOCK), (1, nb, kara.EBADBLOCK)):
+        f = fresh.copy().astype(np.int64)
+        f[at] = bad
+        st, got = run_extend(kara, lengths, n_new, bt, f.astype(np.int32), 50, nb)
+        assert st == code
+        assert_nothing_done(got, lengths, bt)
