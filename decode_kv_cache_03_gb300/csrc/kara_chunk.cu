@@ -169,6 +169,11 @@ __device__ __forceinline__ int32_t pairs_of(const ChunkArgs &a, int seq)
 // ---- attention ------------------------------------------------------------------
 constexpr int kPieces = 4;        // descriptions of pieces under way
 constexpr int kPieceReaders = 15;  // warps that read them: softmax 8, V, MMAs 2, edge tiles 4
+// The warps that clear V may be kPieces pieces ahead of a softmax warp that has yet to look whether it
+// has values to add (it gave the description back when it read it), and no more: the description of
+// piece n + kPieces + 1 goes where that of n + 1 is, which the softmax warp reads after it is done with n.
+constexpr int kOddSlots = 2 * kPieces;
+static_assert(kOddSlots > kPieces && (kOddSlots & (kOddSlots - 1)) == 0, "a slot is not written while it is read");
 
 struct Shared {
     uint64_t full[kStages], empty[kStages];  // K / V tiles
@@ -184,8 +189,8 @@ struct Shared {
     uint32_t tmem;
     int32_t abort;
     // quarters of an edge tile cleaned (by the tile's number mod 4: one warp may be a tile ahead), and
-    // 1 + the last piece (by its number mod 4) whose V had values that are not finite
-    int32_t fixed[4], odd_values[4];
+    // 1 + the last piece (by its number mod kOddSlots) whose V had values that are not finite
+    int32_t fixed[4], odd_values[kOddSlots];
     Start from, to;       // this CTA's range
     int32_t rounds;       // whole items ahead of it
     int64_t cut[2];       // its range of the costs of what is not taken whole
@@ -863,7 +868,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(smem_u32(&sh->done[x]), 1);
         }
         sh->abort = 0;
-        for (int i = 0; i < 4; ++i) sh->odd_values[i] = sh->fixed[i] = 0;
+        for (int i = 0; i < 4; ++i) sh->fixed[i] = 0;
+        for (int i = 0; i < kOddSlots; ++i) sh->odd_values[i] = 0;
         fence_mbarrier_init();
     }
     // rows of the query tiles past G * TQ are never filled: zeros
@@ -1027,7 +1033,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                                   finite_pair(v.w));
                             }
                         }
-                        sh->odd_values[np & 3] = (int32_t)np + 1;
+                        sh->odd_values[np % kOddSlots] = (int32_t)np + 1;
                     }
                     __threadfence_block();
                     fence_proxy_async_smem();
@@ -1177,7 +1183,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 f0 *= inv, f1 *= inv;
                 const int64_t row = p.it.row0 + t;
                 const int rr = (two ? x * kTile : 0) + r;
-                const bool add = *(volatile int32_t *)&sh->odd_values[np & 3] == (int32_t)np + 1;
+                const bool add = *(volatile int32_t *)&sh->odd_values[np % kOddSlots] == (int32_t)np + 1;
                 const int64_t slot = partial_slot(blockIdx.x, p.j0 > 0);
                 float4 *pp = a.part + slot * (D / 4) * 256 + rr;  // dims d..d+3 at pp[d / 4 * 256]
                 uint16_t *op = a.out + (row * a.hq + p.head * a.G + hd) * D;

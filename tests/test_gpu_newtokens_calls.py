@@ -4,8 +4,8 @@ import pytest
 import torch
 
 from _gpu import lib
-from _newtokens import plain_extend
-from test_gpu_newtokens import DEV, assert_nothing_done, i32, new_tokens, run_extend
+from _newtokens import plain_chunk, plain_extend
+from test_gpu_newtokens import DEV, assert_nothing_done, chunk_inputs, i32, new_tokens, run_chunk, run_extend
 
 pytestmark = pytest.mark.gpu
 
@@ -55,3 +55,34 @@ def test_extend_takes_the_largest_pool():
         st, got = run_extend(kara, lengths, n_new, bt, f.astype(np.int32), 50, nb)
         assert st == code
         assert_nothing_done(got, lengths, bt)
+
+
+def test_chunk_values_of_short_items_that_follow_each_other():
+    """Every sequence has new values that are not finite: items of two query tiles, each followed by four of
+    one query tile and one key tile, whose values are cleared while the first is still being finished."""
+    kara = lib()
+    n_new = [64, 3, 1, 32, 2] * 130
+    lengths = [m + (s * 7) % 50 * (m < 64) for s, m in enumerate(n_new)]
+    d = chunk_inputs(73, lengths, n_new, 8, 2, 128, extra=1)
+    for s, (L, m) in enumerate(zip(lengths, n_new)):
+        x = L - m + (s * 5) % m
+        d["v"][0, d["bt"][s, x // 16], :, x % 16, s % 128] = [float("inf"), -float("inf"), float("nan")][s % 3]
+    want = plain_chunk(d["q"], d["k"], d["v"], 0, d["bt"], d["q_start"], d["lengths"])
+    first = None
+    for _ in range(20):
+        got, st = run_chunk(kara, d)
+        assert st == 0
+        n = want.shape[0] - 1
+        if first is None:
+            ok = torch.isfinite(want[:n])
+            assert torch.equal(torch.isfinite(got[:n]), ok)
+            assert torch.equal(torch.isnan(got[:n]), torch.isnan(want[:n]))
+            assert torch.equal(got[:n].double()[torch.isinf(want[:n])], want[:n][torch.isinf(want[:n])])
+            # every finite value: the dims that hold none of those, against values without them
+            clean = dict(d, v=torch.nan_to_num(d["v"], 0.0, 0.0, 0.0))
+            ref = plain_chunk(d["q"], d["k"], clean["v"], 0, d["bt"], d["q_start"], d["lengths"])
+            scale = plain_chunk(d["q"], d["k"], clean["v"], 0, d["bt"], d["q_start"], d["lengths"], absolute=True)
+            lim = ref.abs() * 2.0 ** -8 + scale * (2.0 ** -8 + 2.0 ** -10)
+            assert ((got.double() - ref).abs()[:n][ok] <= lim[:n][ok]).all()
+            first = got.view(torch.int16)
+        assert torch.equal(got.view(torch.int16), first)
