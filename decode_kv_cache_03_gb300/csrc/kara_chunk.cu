@@ -76,7 +76,12 @@ constexpr int kTile = 128;       // rows of a query tile, keys of a key tile
 constexpr int kBlk = 16;         // tokens per cache block (the supported block size)
 constexpr int kBlkPerTile = kTile / kBlk;
 constexpr int kStages = 5;       // K and V tiles in flight
-static_assert((kStages + 1) / 2 < 4, "V tiles in the ring: Shared::edge and odd_values tell four apart");
+// V tiles issued and not cleaned yet, at most.  V tile i takes the stage of K tile i - (kStages - 1) / 2, and
+// when both MMA warps have given that one back, every V tile two or more before it is clean: with two query
+// tiles its logits are issued behind the weighted sum of the V tile before; with one, a warp passes the V
+// tile two before it, clean, ahead of this K tile.
+constexpr int kEdges = (kStages - 1) / 2 + 2;
+static_assert(kEdges == 4 && kStages % 2 == 1, "Shared::edge tells four edge tiles apart, K and V take turns");
 constexpr int kMaxCtas = 160;    // CTAs of the attention kernel, at most (workspace slots)
 constexpr int kMaxRounds = 64;   // whole items that a CTA takes ahead of its range, at most
 constexpr int kThreads = 512;    // two softmax warpgroups, two control warpgroups
@@ -182,15 +187,15 @@ struct Shared {
     uint64_t p_half[2], p_full[2];  // the first half of its weights are in TMEM; all are
     uint64_t o_full[2];   // its last product is done
     uint64_t x_full, x_free;  // a single query tile's odd half is ready to be joined; is joined
-    uint64_t edge[4];     // an edge tile of V has landed (by their number mod 4: the ring holds at most three);
-                          // `full` then says that it is clean
+    uint64_t edge[kEdges];  // an edge tile of V has landed (by their number); `full` then says that it is clean
     uint64_t turn[2];     // the tensor cores are free for a query tile's next products
     uint64_t done[2];
     uint32_t tmem;
     int32_t abort;
-    // quarters of an edge tile cleaned (by the tile's number mod 4: one warp may be a tile ahead), and
+    int4 issued[2];       // K and V: tiles issued, edge tiles issued, which of the last tiles were (bit 0: the last)
+    // quarters of an edge tile cleaned (by the tile's number: one warp may be a tile ahead), and
     // 1 + the last piece (by its number mod kOddSlots) whose V had values that are not finite
-    int32_t fixed[4], odd_values[kOddSlots];
+    int32_t fixed[kEdges], odd_values[kOddSlots];
     Start from, to;       // this CTA's range
     int32_t rounds;       // whole items ahead of it
     int64_t cut[2];       // its range of the costs of what is not taken whole
@@ -252,6 +257,22 @@ __device__ __forceinline__ void drain(uint32_t bar, uint32_t parity)
     const uint64_t t0 = globaltimer();
     while (!mbar_try_wait(bar, parity))
         if (globaltimer() - t0 > kTimeoutNs) return;
+}
+
+// Every K (kv 0) or V (1) tile has landed before the CTA's shared memory is released, also when a wait ran
+// out and nobody consumed it: the last issued of each stage (tile i is entry 2 i + kv of the ring; an entry
+// kStages further on took the same stage, and took it only behind this one), and the last edge tiles.
+__device__ __noinline__ void drain_tiles(Shared *sh, int kv)
+{
+    const uint32_t k = (uint32_t)sh->issued[kv].x, ne = (uint32_t)sh->issued[kv].y;
+    const uint32_t edges = (uint32_t)sh->issued[kv].z, others = (uint32_t)sh->issued[1 - kv].x;
+    for (uint32_t d = 1; d <= kEdges && d <= k; ++d) {
+        const uint32_t e = 2 * (k - d) + kv;
+        if ((e + kStages) / 2 >= others && !(edges >> (d - 1) & 1u))
+            drain(smem_u32(&sh->full[e % kStages]), e / kStages & 1);
+    }
+    for (uint32_t i = ne > kEdges ? ne - kEdges : 0; i < ne; ++i)
+        drain(smem_u32(&sh->edge[i % kEdges]), i / kEdges & 1);
 }
 
 // One thread of the warp (all of them call it).
@@ -748,7 +769,7 @@ __device__ __forceinline__ void mma_warp(int x, uint32_t qbuf, uint32_t ring, Sh
         };
         auto skip = [&](uint32_t &st, uint32_t &ph) {
             ok = ok && kwait(full0 + st * 8, ph, sh, a);
-            mbar_arrive(empty0 + st * 8);
+            if (ok) mbar_arrive(empty0 + st * 8);
             next(st, ph);
         };
         while (ok && next_piece<false>(p, np, sh, ok, 0, wait)) {
@@ -862,13 +883,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         mbar_init(smem_u32(&sh->x_full), 4);
         mbar_init(smem_u32(&sh->x_free), 4);
-        for (int i = 0; i < 4; ++i) mbar_init(smem_u32(&sh->edge[i]), 1);
+        for (int i = 0; i < kEdges; ++i) mbar_init(smem_u32(&sh->edge[i]), 1);
         for (int x = 0; x < 2; ++x) {
             mbar_init(smem_u32(&sh->turn[x]), 1);
             mbar_init(smem_u32(&sh->done[x]), 1);
         }
         sh->abort = 0;
-        for (int i = 0; i < 4; ++i) sh->fixed[i] = 0;
+        for (int i = 0; i < kEdges; ++i) sh->fixed[i] = 0;
         for (int i = 0; i < kOddSlots; ++i) sh->odd_values[i] = 0;
         fence_mbarrier_init();
     }
@@ -907,7 +928,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             };
             uint32_t np = 0;
             uint32_t st = kv, ph = 1, k = 0;  // stage and the phase that frees it; tiles issued
-            uint32_t ne = 0, were_edges = 0;  // edge tiles issued; which of the last tiles were (bit 0: the last)
+            uint32_t ne = 0, were_edges = 0;  // edge tiles issued; which of the last tiles were
             const int b = lane % kBlkPerTile, h = lane / kBlkPerTile;
             const bool mine = h < C::kHalves;
             bool ok = !a.stall;
@@ -949,7 +970,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     ok = __all_sync(0xffffffffu, kwait(smem_u32(&sh->empty[st]), ph, sh, a));
                     if (!ok) break;
                     const bool edge = kv && edge_tile(p.it, j);
-                    const uint32_t fb = smem_u32(edge ? &sh->edge[ne & 3] : &sh->full[st]);
+                    const uint32_t fb = smem_u32(edge ? &sh->edge[ne % kEdges] : &sh->full[st]);
                     ne += edge;
                     were_edges = were_edges << 1 | (edge ? 1u : 0u);
                     if (lane == 0) mbar_arrive_expect_tx(fb, C::kTileBytes);
@@ -962,15 +983,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (st >= kStages) st -= kStages, ph ^= 1;
                 }
             }
-            // every copy has landed before the CTA's shared memory is released: the ring's last
-            // entries (this warp's tile i is entry 2 i + kv; earlier ones were consumed), and the
-            // edge tiles
-            for (uint32_t i = k > kStages / 2 ? k - kStages / 2 - 1 : 0; i < k; ++i) {
-                const uint32_t e = 2 * i + kv;
-                if (e + kStages >= 2 * k && !(were_edges >> (k - 1 - i) & 1u))
-                    drain(smem_u32(&sh->full[e % kStages]), (e / kStages) & 1);
-            }
-            for (uint32_t i = ne > 3 ? ne - 3 : 0; i < ne; ++i) drain(smem_u32(&sh->edge[i & 3]), (i >> 2) & 1);
+            if (lane == 0) sh->issued[kv] = make_int4((int)k, (int)ne, (int)were_edges, 0);
         } else if (warp == kWarpMma || warp == kWarpMma + 1) {
             mma_warp<D>(warp - kWarpMma, smem_u32(qbuf), smem_u32(ring), sh, a);
         } else {
@@ -1006,7 +1019,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int j = max(p.j0, (p.it.pos0 + 1) / kTile); ok && j < p.j1; ++j) {
                     if (!edge_tile(p.it, j)) continue;
                     const uint32_t st = (k0 + 2 * (j - p.j0) + 1) % kStages;
-                    ok = __all_sync(0xffffffffu, kwait<200>(smem_u32(&sh->edge[ne & 3]), (ne >> 2) & 1, sh, a));
+                    ok = __all_sync(0xffffffffu, kwait<200>(smem_u32(&sh->edge[ne % kEdges]), ne / kEdges & 1, sh, a));
                     if (!ok) break;
                     const int end = min(p.it.len - j * kTile, kTile);     // rows from here on: past the sequence
                     const int r0 = max(0, min(end, p.it.pos0 + 1 - j * kTile));  // rows from here on: new tokens
@@ -1039,7 +1052,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     fence_proxy_async_smem();
                     __syncwarp();
                     // the last of the four warps hands the tile over
-                    if (lane == 0 && (atomicAdd(&sh->fixed[ne & 3], 1) & 3) == 3) {
+                    if (lane == 0 && (atomicAdd(&sh->fixed[ne % kEdges], 1) & 3) == 3) {
                         __threadfence_block();
                         mbar_arrive(smem_u32(&sh->full[st]));
                     }
@@ -1242,6 +1255,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     tc_fence_after();
     if (warp == kWarpMma) tmem_dealloc(sh->tmem, kTmemCols);
+    if (warp == kWarpKv || warp == kWarpKv + 1) drain_tiles(sh, warp - kWarpKv);
 }
 
 // ---- merge ----------------------------------------------------------------------
