@@ -186,6 +186,7 @@ __global__ void __launch_bounds__(kAppThreads) append_kernel(const AppArgs a)
 constexpr int kTokWarps = 4;
 constexpr int kTokThreads = 32 * (1 + kTokWarps);
 constexpr int kTokMaxStages = 8;
+constexpr int kTokMaxSmem = 222 * 1024;  // of a CTA that has an SM to itself
 // Calls of up to this many head rows (tokens times heads) take the other kernel: all their
 // loads are in flight at once and there is no pipeline to fill.  Measured with 56 heads of 128
 // (staged / a warp per two rows, us): 128 tokens 4.7 / 2.9, 256 5.3 / 4.5, 384 5.8 / 5.9,
@@ -462,7 +463,7 @@ cudaError_t launch(const AppArgs &a, cudaStream_t st)
     int stages = 0, per_sm = 4;
     for (; per_sm > 0 && stages < (per_sm > 1 ? 3 : 2); per_sm >>= 1) {
         // 54, 110 or 222 KB a CTA; three tokens staged at least, two with one CTA per SM
-        const size_t room = (per_sm == 4 ? 54 : per_sm == 2 ? 110 : 222) * 1024;
+        const size_t room = (per_sm == 4 ? 54 * 1024 : per_sm == 2 ? 110 * 1024 : kTokMaxSmem);
         stages = room > head ? (int)((room - head) / sb) : 0;
         if (stages >= (per_sm > 1 ? 3 : 2)) break;
     }
@@ -476,7 +477,8 @@ cudaError_t launch(const AppArgs &a, cudaStream_t st)
     if (stages > kTokMaxStages) stages = kTokMaxStages;
     const size_t smem = head + (size_t)stages * sb;
     const auto kern = a.inter ? append_staged_kernel<D, true> : append_staged_kernel<D, false>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    // (one limit for every shape: it is the kernel's, and another host thread may set it ahead of this launch)
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kTokMaxSmem);
     int dev = 0, sms = 0;
     if (e == cudaSuccess) e = cudaGetDevice(&dev);
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);

@@ -31,6 +31,7 @@ constexpr int kExtThreads = 1024;
 constexpr int kExtCtas = 8;             // portable cluster size
 constexpr int kBitWindow = 1 << 20;     // ids per bitmap window: 128 KB of shared memory
 constexpr int kStartCap = 16384;        // sequences whose q_start fits beside it (64 KB)
+constexpr int kMaxSmem = kBitWindow / 8 + (int)sizeof(int32_t) * (kStartCap + 1);
 constexpr int kScanItem = 512;          // table entries a warp checks per turn
 // Up to this many entries to check and rows to write, one CTA does it all: the
 // cluster's barriers then cost more than its width saves.
@@ -362,8 +363,9 @@ cudaError_t launch_extend(int32_t num_blocks, const int32_t *len, const int32_t 
     a.start_in_smem = t->n <= kStartCap;
     const size_t smem = (size_t)a.window / 8 + (a.start_in_smem ? sizeof(int32_t) * ((size_t)t->n + 1) : 0);
     if (smem > 40 * 1024) {
+        // (one limit for every size: it is the kernel's, and another host thread may set it ahead of this launch)
         const cudaError_t e =
-            cudaFuncSetAttribute(extend_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+            cudaFuncSetAttribute(extend_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
         if (e != cudaSuccess) return e;
     }
     a.rows_apart = t->rows > kRowsApart;

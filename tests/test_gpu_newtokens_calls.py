@@ -1,13 +1,71 @@
 """New-token calls as a program makes them: empty steps, several host threads, streams, other lengths."""
+import ctypes
+import threading
+
 import numpy as np
 import pytest
 import torch
 
 from _gpu import lib
 from _newtokens import plain_chunk, plain_extend
-from test_gpu_newtokens import DEV, assert_nothing_done, chunk_inputs, i32, new_tokens, run_chunk, run_extend
+from test_gpu_newtokens import (DEV, angles, append_inputs, assert_nothing_done, chunk_inputs, error_word, i32,
+                                new_tokens, run_chunk, run_extend)
 
 pytestmark = pytest.mark.gpu
+
+
+class NodeParams(ctypes.Structure):   # of the driver's second version of the call
+    _fields_ = [("func", ctypes.c_void_p), ("grid", ctypes.c_uint * 3), ("block", ctypes.c_uint * 3),
+                ("smem", ctypes.c_uint), ("params", ctypes.c_void_p), ("extra", ctypes.c_void_p),
+                ("kern", ctypes.c_void_p), ("ctx", ctypes.c_void_p)]
+
+
+def launches(call):
+    """The kernels that call(stream) would launch, captured and not run: (grid, dynamic shared memory, the
+    limit of that which the function has now)."""
+    cu = ctypes.CDLL("libcuda.so.1")
+    s = torch.cuda.Stream()
+    handle, graph, n = ctypes.c_void_p(s.cuda_stream), ctypes.c_void_p(), ctypes.c_size_t(0)
+
+    def do(f, *args):
+        assert getattr(cu, f)(*args) == 0, f
+
+    do("cuStreamBeginCapture_v2", handle, 1)   # of this thread alone
+    try:
+        call(s)
+    finally:
+        ended = cu.cuStreamEndCapture(handle, ctypes.byref(graph))
+    assert ended == 0
+    do("cuGraphGetNodes", graph, None, ctypes.byref(n))
+    nodes = (ctypes.c_void_p * n.value)()
+    do("cuGraphGetNodes", graph, nodes, ctypes.byref(n))
+    out = []
+    for node in nodes:
+        kind = ctypes.c_int(-1)
+        do("cuGraphNodeGetType", ctypes.c_void_p(node), ctypes.byref(kind))
+        if kind.value != 0:
+            continue
+        p, limit = NodeParams(), ctypes.c_int(0)
+        do("cuGraphKernelNodeGetParams_v2", ctypes.c_void_p(node), ctypes.byref(p))
+        func = ctypes.c_void_p(p.func)
+        if not p.func:
+            do("cuKernelGetFunction", ctypes.byref(func), ctypes.c_void_p(p.kern))
+        do("cuFuncGetAttribute", ctypes.byref(limit), 8, func)   # the most dynamic shared memory
+        out.append((tuple(p.grid), p.smem, limit.value))
+    do("cuGraphDestroy", graph)
+    return out
+
+
+def append_call(kara, hq, hkv, D, rows, rot=0, inter=False):
+    """An append of `rows` tokens of one sequence, as a function of the stream; q_out, the pools, the error word."""
+    q, k, v = (x.to(DEV) for x in append_inputs(hq + rows, hq, hkv, D, rows, fused=False))
+    nb = (rows + 15) // 16
+    kp = torch.zeros(1, nb, hkv, 16, D, dtype=torch.bfloat16, device=DEV)
+    vp, out, err = torch.zeros_like(kp), torch.zeros_like(q), error_word()
+    t = kara.tokens(i32([0, rows]), i32([rows]), torch.arange(rows, device=DEV), i32([0] * rows), i32(range(rows)))
+    c, r = kara.cache(kp, vp, hq), kara.rope(angles(rows, rot).to(DEV) if rot else None, interleaved=inter)
+    torch.cuda.synchronize()
+    return (lambda s=None: kara.kara_append_kv(c, 0, t, r, q, k, v, out, err, stream=s)), out, (kp, vp), err
 
 
 def test_extend_of_no_sequences_and_no_rows():
@@ -86,3 +144,51 @@ def test_chunk_values_of_short_items_that_follow_each_other():
             assert ((got.double() - ref).abs()[:n][ok] <= lim[:n][ok]).all()
             first = got.view(torch.int16)
         assert torch.equal(got.view(torch.int16), first)
+
+
+def test_calls_of_other_shapes_keep_the_shared_memory_limit():
+    """A kernel's limit of dynamic shared memory is one value for all host threads: a call of another shape
+    does not lower it between a larger call's setting of it and its launch."""
+    kara = lib()
+    big, small = append_call(kara, 160, 20, 128, 600), append_call(kara, 4, 2, 128, 3000)
+    (_, need, had), = launches(big[0])
+    (_, less, now), = launches(small[0])
+    assert less < need <= had and now >= need
+    b, t = new_tokens(kara, 1, 4)
+    err, used, table, fresh = error_word(), i32([0]), i32([[1, -1]]), i32([2])
+    lengths, n_new = i32([16]), i32([4])
+    ext = lambda nb: lambda s: kara.kara_extend_tables(  # noqa: E731
+        nb, 16, lengths, n_new, table, fresh, t, used, err, s)
+    torch.cuda.synchronize()
+    (_, need, had), = launches(ext(1 << 20))
+    (_, less, now), = launches(ext(500000))
+    assert less < need <= had and now >= need
+
+
+def test_two_host_threads_with_other_shapes():
+    """A wide and a narrow model append from two threads, each on a stream of its own."""
+    kara = lib()
+    calls = [append_call(kara, 160, 20, 128, 300), append_call(kara, 4, 2, 128, 3000)]
+    for call, *_ in calls:
+        call()
+    torch.cuda.synchronize()
+    want = [(out.clone(), kp.clone(), vp.clone()) for _, out, (kp, vp), _ in calls]
+    failed = []
+
+    def work(call):
+        s = torch.cuda.Stream()
+        try:
+            for _ in range(2000):
+                call(s)
+        except Exception as e:   # noqa: BLE001 (told to the test's thread)
+            failed.append(e)
+        s.synchronize()
+
+    threads = [threading.Thread(target=work, args=(call,)) for call, *_ in calls]
+    for th in threads:
+        th.start()
+    for th in threads:
+        th.join()
+    assert not failed
+    for (_, out, (kp, vp), err), now in zip(calls, want):
+        assert err.item() == 0 and all(torch.equal(a, b) for a, b in zip((out, kp, vp), now))
