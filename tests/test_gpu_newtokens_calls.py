@@ -8,8 +8,8 @@ import torch
 
 from _gpu import lib
 from _newtokens import plain_chunk, plain_extend
-from test_gpu_newtokens import (DEV, angles, append_inputs, assert_nothing_done, chunk_inputs, error_word, i32,
-                                new_tokens, run_chunk, run_extend)
+from test_gpu_newtokens import (DEV, angles, append_inputs, assert_nothing_done, check_chunk, chunk_inputs,
+                                chunk_tokens, error_word, i32, new_tokens, run_chunk, run_extend)
 
 pytestmark = pytest.mark.gpu
 
@@ -192,3 +192,67 @@ def test_two_host_threads_with_other_shapes():
     assert not failed
     for (_, out, (kp, vp), err), now in zip(calls, want):
         assert err.item() == 0 and all(torch.equal(a, b) for a, b in zip((out, kp, vp), now))
+
+
+@pytest.mark.parametrize("what", ["chunk", "decode", "workspace"])
+def test_compressor_workspace_belongs_to_its_stream(what):
+    """The workspace of a call on a given stream is that stream's memory: not a block that the current stream
+    has just given back, and may still be using."""
+    from decode_kv_cache_03_gb300 import Compressor
+    kara = lib()
+    d = chunk_inputs(71, [300, 90], [1, 1], 8, 2, 128)
+    k, v, q, bt, ln = d["k"].to(DEV), d["v"].to(DEV), d["q"].to(DEV), i32(d["bt"]), i32(d["lengths"])
+    t = chunk_tokens(kara, d)
+    comp = Compressor(k, v, 8, 64, 16, 8, 20)
+    side, out = torch.cuda.Stream(), torch.empty_like(q)
+    out32 = torch.empty(q.shape, dtype=torch.float32, device=DEV)
+    size = {"chunk": kara.kara_chunk_workspace_size(comp.cache, t.n, t.rows),
+            "decode": kara.kara_decode_workspace_size(comp.cache, *bt.shape),
+            "workspace": kara.kara_workspace_size(comp.cache, comp.params, 2)}[what]
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    given_back = torch.empty(size, dtype=torch.uint8, device=DEV)
+    at = given_back.data_ptr()
+    del given_back
+    if what == "chunk":
+        comp.chunk(0, t, bt, q, out, stream=side)
+        ws = comp._cws
+    elif what == "decode":
+        comp.decode(0, ln, bt, q, out32, stream=side)
+        ws = comp._dws
+    else:
+        ws = comp.workspace(2, stream=side)
+    assert ws.numel() >= size and ws.data_ptr() != at
+    again = torch.empty(size, dtype=torch.uint8, device=DEV)   # (the current stream still has its block)
+    assert again.data_ptr() == at
+    side.synchronize()
+    if what == "chunk":
+        check_chunk(d, out.cpu())
+    assert comp.error() == 0
+
+
+def test_compressor_workspace_outlives_calls_on_other_streams():
+    """Dropped while a call on another stream than its own may still run, a workspace is not handed out
+    until that call has run, and the error word is not."""
+    from decode_kv_cache_03_gb300 import Compressor
+    kara = lib()
+    d = chunk_inputs(72, [300, 90], [1, 1], 8, 2, 128)
+    k, v, q, bt = d["k"].to(DEV), d["v"].to(DEV), d["q"].to(DEV), i32(d["bt"])
+    t, side, out = chunk_tokens(kara, d), torch.cuda.Stream(), torch.empty_like(q)
+    comp = Compressor(k, v, 8, 64, 16, 8, 20)
+    comp.chunk(0, t, bt, q, out)              # the workspace is the current stream's
+    at, size, word = comp._cws.data_ptr(), comp._cws.numel(), comp.err.data_ptr()
+    busy, dump = torch.randn(8192, 8192, device=DEV), torch.empty(8192, 8192, device=DEV)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        for _ in range(10):                    # milliseconds ahead of the call
+            torch.mm(busy, busy, out=dump)
+    comp.chunk(0, t, bt, q, out, stream=side)
+    held = not side.query()
+    del comp
+    again = torch.empty(size, dtype=torch.uint8, device=DEV)
+    words = [torch.empty(1, dtype=torch.int32, device=DEV) for _ in range(50)]
+    assert held and not side.query() and again.data_ptr() != at
+    assert all(w.data_ptr() != word for w in words)
+    side.synchronize()
+    check_chunk(d, out.cpu())
