@@ -410,6 +410,7 @@ kara_status kara_chunk_attention(const kara_cache *c, int32_t layer, const kara_
     if (!t->q_start || !t->len || !block_table || !q || !out || !err) return KARA_EINVAL;
     if (!aligned16(q) || !aligned16(out)) return KARA_EINVAL;
     if (!ws || ws_bytes < chunk_workspace_bytes(c)) return KARA_EWORKSPACE;
+    if (!aligned16(ws)) return KARA_EINVAL;
     return cuda_status(launch_chunk(c, layer, t, block_table, bt_stride, q, out, ws, err, (cudaStream_t)stream));
 }
 

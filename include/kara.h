@@ -330,8 +330,9 @@ kara_status kara_append_kv(const kara_cache *c, int32_t layer, const kara_tokens
  * A row's result depends on its own keys and values only, whatever later tokens
  * or stale rows of a block hold, NaN included; its bits may depend on the batch
  * (where a sequence's keys are cut), never on timing.
- * ws/ws_bytes: at least kara_chunk_workspace_size(c, n, rows) bytes, used by
- * this call alone until it has run (two calls that may overlap need two).
+ * ws/ws_bytes: at least kara_chunk_workspace_size(c, n, rows) bytes, 16-byte
+ * aligned, used by this call alone until it has run (two calls that may overlap
+ * need two).
  * Returns KARA_ECUDA, before any launch, if a TMA tensor map cannot be encoded.
  * Two launches, programmatic dependents of what precedes them on `stream`; the
  * call may be captured into a CUDA graph.

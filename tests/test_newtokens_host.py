@@ -174,3 +174,11 @@ def test_plain_chunk_single_key_and_causality():
     v2[0, 1] = 99.0
     b = plain_chunk(q, k, v2, 0, bt, [0, 20], [20])
     assert torch.equal(a[:16], b[:16]) and not torch.equal(a[16:], b[16:])
+
+
+def test_chunk_refuses_a_workspace_off_its_alignment(kara):
+    """Partials are stored 16 bytes at a time: a view that starts in between never reaches a launch."""
+    for at in (4097, 4098, 4100, 4104):
+        st = kara._lib.kara_chunk_attention(fake_cache(kara), 0, fake_tokens(kara), PTR, 4, PTR, PTR,
+                                            ctypes.c_void_p(at), 1 << 40, PTR, None)
+        assert st == kara.EINVAL, at
