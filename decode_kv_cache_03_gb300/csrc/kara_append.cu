@@ -186,7 +186,7 @@ __global__ void __launch_bounds__(kAppThreads) append_kernel(const AppArgs a)
 constexpr int kTokWarps = 4;
 constexpr int kTokThreads = 32 * (1 + kTokWarps);
 constexpr int kTokMaxStages = 8;
-constexpr int kTokMaxSmem = 222 * 1024;  // of a CTA that has an SM to itself
+constexpr int kTokMaxSmem = 110 * 1024;  // of a CTA, two of which share an SM
 // Calls of up to this many head rows (tokens times heads) take the other kernel: all their
 // loads are in flight at once and there is no pipeline to fill.  Measured with 56 heads of 128
 // (staged / a warp per two rows, us): 128 tokens 4.7 / 2.9, 256 5.3 / 4.5, 384 5.8 / 5.9,
@@ -460,14 +460,18 @@ cudaError_t launch(const AppArgs &a, cudaStream_t st)
 {
     const size_t head = (sizeof(TokShared) + 127) / 128 * 128;
     const int sb = tok_stage_bytes(a.hq, a.hkv, D, a.rot);
+    // As many CTAs per SM, up to four, as hold a token each: it is their warps that count, more than the tokens
+    // staged.  Fewer than two (more than about 435 head rows of 128): the other kernel.  Measured, 4096 tokens, at 4 / 3
+    // / 2 / 1 CTAs with what then fits, and the other kernel (us): 64 and 2 x 64 heads of 128 (1, 1, 2, 4 tokens)
+    // 88.6 / 102 / 119 / 209, 151; 192 and 2 x 24 - / 132 / 181 / 279, 194; 256 and 2 x 64 - / - / 271 / 430,
+    // 308; 320 and 2 x 80 - / - / - / 582, 384.
     int stages = 0, per_sm = 4;
-    for (; per_sm > 0 && stages < (per_sm > 1 ? 3 : 2); per_sm >>= 1) {
-        // 54, 110 or 222 KB a CTA; three tokens staged at least, two with one CTA per SM
-        const size_t room = (per_sm == 4 ? 54 * 1024 : per_sm == 2 ? 110 * 1024 : kTokMaxSmem);
-        stages = room > head ? (int)((room - head) / sb) : 0;
-        if (stages >= (per_sm > 1 ? 3 : 2)) break;
+    for (; per_sm > 1; --per_sm) {
+        const size_t room = per_sm == 4 ? 54 * 1024 : per_sm == 3 ? 74 * 1024 : kTokMaxSmem;
+        stages = (int)((room - head) / sb);
+        if (stages > 0) break;
     }
-    if ((int64_t)a.rows * (a.hq + 2 * a.hkv) <= kSmallRows || per_sm == 0) {
+    if ((int64_t)a.rows * (a.hq + 2 * a.hkv) <= kSmallRows || stages == 0) {
         constexpr int RPP = 32 / (D / 8), WPC = kAppThreads / 32;
         const int parts = (a.hq + 2 * a.hkv + RPP - 1) / RPP;
         if (parts > 65535) return cudaErrorInvalidConfiguration;

@@ -7,9 +7,9 @@ import pytest
 import torch
 
 from _gpu import lib
-from _newtokens import plain_chunk, plain_extend
+from _newtokens import blocks, make_tables, plain_chunk, plain_extend, plain_turn
 from test_gpu_newtokens import (DEV, angles, append_inputs, assert_nothing_done, check_chunk, chunk_inputs,
-                                chunk_tokens, error_word, i32, new_tokens, run_chunk, run_extend)
+                                chunk_tokens, close_rows, error_word, i32, new_tokens, on_gpu, run_chunk, run_extend)
 
 pytestmark = pytest.mark.gpu
 
@@ -256,3 +256,56 @@ def test_compressor_workspace_outlives_calls_on_other_streams():
     assert all(w.data_ptr() != word for w in words)
     side.synchronize()
     check_chunk(d, out.cpu())
+
+
+@pytest.mark.parametrize("hq,hkv,rot,ctas,stages", [
+    (4, 2, 64, 4, 8), (40, 8, 128, 4, 3), (64, 16, 128, 4, 2), (64, 32, 128, 4, 1), (64, 64, 128, 4, 1),
+    (128, 32, 128, 4, 1), (128, 16, 128, 4, 1), (160, 20, 128, 4, 1), (192, 24, 128, 3, 1), (256, 64, 128, 2, 1),
+    (320, 80, 128, 0, 0)])
+def test_append_has_as_many_ctas_as_hold_a_token(hq, hkv, rot, ctas, stages):
+    """Long calls: four CTAs per SM, three or two, whatever tokens then fit in each; none with the widest."""
+    kara = lib()
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    rows = 20480 // (hq + 2 * hkv) + 4 * sms
+    held = append_call(kara, hq, hkv, 128, rows, rot)
+    (grid, smem, _), = launches(held[0])
+    assert smem // ((hq + 2 * hkv) * 256 + rot * 4) == stages
+    assert grid == (sms * ctas, 1, 1) if ctas else grid == ((rows + 7) // 8, (hq + 2 * hkv) // 2, 1)
+
+
+@pytest.mark.parametrize("hq,hkv,D,rot,inter,W,rows", [
+    (64, 64, 128, 128, False, 64, 700), (160, 20, 128, 64, True, 0, 701), (192, 24, 128, 128, False, 0, 650),
+    (256, 64, 128, 32, True, 64, 333), (320, 80, 128, 128, False, 0, 211), (128, 128, 64, 64, False, 64, 800)])
+def test_append_long_calls_of_wide_shapes(hq, hkv, D, rot, inter, W, rows):
+    """Values of long calls whose CTAs hold one token or few, four, three and two CTAs per SM, and none."""
+    kara = lib()
+    lengths, n_new = np.array([31, 300]), np.array([rows // 3, rows - rows // 3])
+    width = int(blocks(lengths + n_new).max())
+    nb = int(blocks(lengths + n_new).sum()) + 1
+    bt, fresh = make_tables(lengths, width, nb, 4)
+    _, q_start, ln, slot, seq, pos, _ = plain_extend(lengths, n_new, bt, fresh, rows + 2)
+    q, k, v = append_inputs(hq, hq, hkv, D, rows + 2)
+    g = torch.Generator().manual_seed(2)
+    qw, kw = ((1 + 0.3 * torch.randn(D, generator=g)).bfloat16() for _ in range(2))
+    cs = angles(1200, rot)
+    kp = torch.zeros(1, nb, hkv, 16, D, dtype=torch.bfloat16, device=DEV)
+    vp = torch.zeros_like(kp)
+    ring = torch.zeros(2, 1, hq, W, D, dtype=torch.bfloat16, device=DEV) if W else None
+    out, err = torch.full((rows + 2, hq, D), 77.0, dtype=torch.bfloat16, device=DEV), error_word()
+    t = kara.tokens(i32(q_start), i32(ln), torch.from_numpy(slot).to(DEV), i32(seq), i32(pos))
+    r = kara.rope(cs.to(DEV), qw.to(DEV), kw.to(DEV), 1e-5, inter)
+    kara.kara_append_kv(kara.cache(kp, vp, hq), 0, t, r, *on_gpu(q, k, v), out, err, ring=ring)
+    assert kara.kara_get_error(err) == 0
+    at, got = torch.from_numpy(pos[:rows]).long(), out.cpu()
+    turned = lambda x, w: (plain_turn(x[:rows], w, 1e-5, cs, at, inter),  # noqa: E731
+                           plain_turn(x[:rows], w, 1e-5, None, None, inter))
+    close_rows(got[:rows], *turned(q, qw))
+    assert (got[rows:] == 77.0).all()
+    flat = lambda p: p.cpu()[0].permute(0, 2, 1, 3).reshape(-1, hkv, D)[torch.from_numpy(slot[:rows])]  # noqa: E731
+    close_rows(flat(kp), *turned(k, kw))
+    assert torch.equal(flat(vp), v[:rows])
+    if W:
+        rg = ring.cpu()[:, 0].permute(0, 2, 1, 3)   # [sequence][row][head][D]
+        for s in (0, 1):
+            last = torch.arange(int(ln[s]) - W, int(ln[s]))
+            assert torch.equal(rg[s, last % W], got[int(q_start[s]) + last - int(lengths[s])])
