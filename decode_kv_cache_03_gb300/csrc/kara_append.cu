@@ -12,9 +12,9 @@
 // Nothing is reused but the table row, so the floor is one read of q, k, v and
 // one write of them: HBM for long chunks, launch latency for a decode step.  D/8
 // lanes hold a row, 16 bytes each, so a warp takes 32 / (D/8) rows at once; a
-// row's sum of squares is a butterfly over its lanes.  Two kernels: for short
-// calls a warp per pass, everything in registers; for long ones tokens staged
-// through shared memory by bulk copies, because what bounds a long call is the
+// row's sum of squares is a butterfly over its lanes.  Two kernels, which give a
+// token the same bits (one arithmetic, below): for short calls a warp per pass,
+// everything in registers; for long ones tokens staged through shared memory by bulk copies, because what bounds a long call is the
 // latency of its chain of loads (slot, offset, table row, rows): in registers it
 // reached 4.0 TB/s with four passes a warp (8192 tokens, 40/8 heads of 128, with
 // the ring: 70 us), staged 5.4 TB/s (52 us).
@@ -48,12 +48,6 @@ struct AppArgs {
 __device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 
-__device__ __forceinline__ void unpack8(const uint4 &u, float (&x)[8])
-{
-    x[0] = bf_lo(u.x), x[1] = bf_hi(u.x), x[2] = bf_lo(u.y), x[3] = bf_hi(u.y);
-    x[4] = bf_lo(u.z), x[5] = bf_hi(u.z), x[6] = bf_lo(u.w), x[7] = bf_hi(u.w);
-}
-
 // (lo, hi) rounded to nearest-even bf16, lo in the low half.
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi)
 {
@@ -64,9 +58,63 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi)
 
 __device__ __forceinline__ float4 ldg4(const float *p) { return __ldg(reinterpret_cast<const float4 *>(p)); }
 
+// (a*b) on both halves, round-to-nearest.
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b)
+{
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+
+// Eight bf16 as pairs of neighbours, in fp32; with `swap` each pair the other way round.
+__device__ __forceinline__ void pairs4(const uint4 &u, uint64_t (&x)[4], bool swap)
+{
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const float lo = bf_lo(w[e]), hi = bf_hi(w[e]);
+        x[e] = swap ? ptx::pack2(hi, lo) : ptx::pack2(lo, hi);
+    }
+}
+
+// The arithmetic of a lane's eight values, one for both kernels, so that a token's bits do not depend on the
+// length of the call that brings it.  This lane's part of the row's sum of squares:
+__device__ __forceinline__ float squares(const uint64_t (&x)[4])
+{
+    uint64_t s2 = mul2(x[0], x[0]);
+#pragma unroll
+    for (int e = 1; e < 4; ++e) s2 = ptx::fma2(x[e], x[e], s2);
+    float lo, hi;
+    ptx::unpack2(s2, lo, hi);
+    return lo + hi;
+}
+
+// x wc + x' ws': a pair's cosines times weights, and its partners times theirs and signed sines.
+__device__ __forceinline__ uint64_t turn2(uint64_t x, uint64_t wc, uint64_t xo, uint64_t ws)
+{
+    return ptx::fma2(x, wc, mul2(xo, ws));
+}
+
+__device__ __forceinline__ float inverse_norm(float sum, float per, float eps) { return rsqrtf(fmaf(sum, per, eps)); }
+
+// z / the norm, rounded.
+__device__ __forceinline__ uint4 finish(const uint64_t (&z)[4], float inv)
+{
+    const uint64_t i2 = ptx::pack2(inv, inv);
+    uint32_t r[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        float lo, hi;
+        ptx::unpack2(mul2(z[e], i2), lo, hi);
+        r[e] = pack_bf16(lo, hi);
+    }
+    return make_uint4(r[0], r[1], r[2], r[3]);
+}
+
 // A warp takes 32 / (D/8) rows of one token: token blockIdx.x * 8 + warp, rows of part blockIdx.y.
-template <int D>
-__global__ void __launch_bounds__(kAppThreads) append_kernel(const AppArgs a)
+// (Five blocks per SM: 48 registers.  Left at 68, 4096 tokens of 320 and 2 x 80 heads take 525 us, so 346.)
+template <int D, bool INTER>
+__global__ void __launch_bounds__(kAppThreads, 5) append_kernel(const AppArgs a)
 {
     constexpr int LPR = D / 8;     // lanes per row
     constexpr int RPP = 32 / LPR;  // rows per pass
@@ -100,31 +148,33 @@ __global__ void __launch_bounds__(kAppThreads) append_kernel(const AppArgs a)
         return;
     }
 
-    // this lane's cosines and signed sines, one per value it holds
-    float c[8], sn[8];
+    // this lane's cosines and signed sines, in pairs of neighbours
+    uint64_t c[4], sn[4];
     const int half = a.rot >> 1;
-    const bool turned = d0 < a.rot;
+    const bool turned = d0 < a.rot, low = d0 < half;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) c[e] = 1.f, sn[e] = 0.f;
+    for (int e = 0; e < 4; ++e) c[e] = ptx::pack2(1.f, 1.f), sn[e] = ptx::pack2(0.f, 0.f);
     if (turned) {
         const float *row = a.cos_sin + r * a.rot;
-        if (a.inter) {
+        if (INTER) {
             const float4 cc = ldg4(row + d0 / 2), ss = ldg4(row + half + d0 / 2);
-            c[0] = c[1] = cc.x, c[2] = c[3] = cc.y, c[4] = c[5] = cc.z, c[6] = c[7] = cc.w;
-            sn[1] = ss.x, sn[3] = ss.y, sn[5] = ss.z, sn[7] = ss.w;
-            sn[0] = -ss.x, sn[2] = -ss.y, sn[4] = -ss.z, sn[6] = -ss.w;
+            c[0] = ptx::pack2(cc.x, cc.x), c[1] = ptx::pack2(cc.y, cc.y);
+            c[2] = ptx::pack2(cc.z, cc.z), c[3] = ptx::pack2(cc.w, cc.w);
+            sn[0] = ptx::pack2(-ss.x, ss.x), sn[1] = ptx::pack2(-ss.y, ss.y);
+            sn[2] = ptx::pack2(-ss.z, ss.z), sn[3] = ptx::pack2(-ss.w, ss.w);
         } else {
-            const int j0 = d0 < half ? d0 : d0 - half;
-            const float sg = d0 < half ? -1.f : 1.f;
-            const float4 c0 = ldg4(row + j0), c1 = ldg4(row + j0 + 4);
-            const float4 s0 = ldg4(row + half + j0), s1 = ldg4(row + half + j0 + 4);
-            c[0] = c0.x, c[1] = c0.y, c[2] = c0.z, c[3] = c0.w, c[4] = c1.x, c[5] = c1.y, c[6] = c1.z, c[7] = c1.w;
-            sn[0] = sg * s0.x, sn[1] = sg * s0.y, sn[2] = sg * s0.z, sn[3] = sg * s0.w;
-            sn[4] = sg * s1.x, sn[5] = sg * s1.y, sn[6] = sg * s1.z, sn[7] = sg * s1.w;
+            const int j0 = low ? d0 : d0 - half;
+            const uint64_t sg = low ? ptx::pack2(-1.f, -1.f) : ptx::pack2(1.f, 1.f);
+#pragma unroll
+            for (int e = 0; e < 4; e += 2) {
+                const float4 cc = ldg4(row + j0 + 2 * e), ss = ldg4(row + half + j0 + 2 * e);
+                c[e] = ptx::pack2(cc.x, cc.y), c[e + 1] = ptx::pack2(cc.z, cc.w);
+                sn[e] = mul2(sg, ptx::pack2(ss.x, ss.y)), sn[e + 1] = mul2(sg, ptx::pack2(ss.z, ss.w));
+            }
         }
     }
     // lane that holds the other half of this lane's pairs
-    const int other = !turned || a.inter ? lane : d0 < half ? lane + half / 8 : lane - half / 8;
+    const int other = !turned || INTER ? lane : low ? lane + half / 8 : lane - half / 8;
     const int64_t page = (slot / kBs) * a.block_stride + (slot % kBs) * D + d0;
     uint16_t *ring = nullptr;  // this token's row of the ring, if it is of the last W
     if (a.ring) {
@@ -133,39 +183,33 @@ __global__ void __launch_bounds__(kAppThreads) append_kernel(const AppArgs a)
     }
     // (a warp whose rows are all values has nothing to compute)
     if (__any_sync(0xffffffffu, !is_v)) {
-        float y[8];
-        unpack8(u, y);
+        // z = (x w c + x' w' s) / sqrt(mean(x^2) + eps), x' and w' of the pair's other member
+        const uint4 one = make_uint4(0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u);
         const uint16_t *wp = is_q ? a.qw : a.kw;
+        const uint4 uw = wp ? __ldg(reinterpret_cast<const uint4 *>(wp + d0)) : one;
+        uint4 uo = u, uwo = uw;
+        if (!INTER && a.rot > 0) {
+            uo.x = __shfl_sync(0xffffffffu, u.x, other), uo.y = __shfl_sync(0xffffffffu, u.y, other);
+            uo.z = __shfl_sync(0xffffffffu, u.z, other), uo.w = __shfl_sync(0xffffffffu, u.w, other);
+            if (wp) uwo = __ldg(reinterpret_cast<const uint4 *>(wp + (turned ? low ? d0 + half : d0 - half : d0)));
+        }
+        uint64_t x[4], xo[4], w[4], wo[4], z[4];
+        pairs4(u, x, false), pairs4(uo, xo, INTER);
+        pairs4(uw, w, false), pairs4(uwo, wo, INTER);
+        float inv = 1.f;
         if (a.qw || a.kw) {
-            float ss = 0.f;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) ss = fmaf(y[e], y[e], ss);
+            float ss = squares(x);
 #pragma unroll
             for (int o = LPR / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-            if (wp) {
-                float w[8];
-                unpack8(__ldg(reinterpret_cast<const uint4 *>(wp + d0)), w);
-                const float inv = rsqrtf(ss * (1.f / D) + a.eps);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) y[e] = y[e] * inv * w[e];
-            }
+            if (wp) inv = inverse_norm(ss, 1.f / D, a.eps);
         }
-        float z[8];
-        if (a.inter) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) z[e] = fmaf(y[e], c[e], y[e ^ 1] * sn[e]);
-        } else {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) z[e] = fmaf(y[e], c[e], __shfl_sync(0xffffffffu, y[e], other) * sn[e]);
-        }
+        for (int e = 0; e < 4; ++e) z[e] = turn2(x[e], mul2(w[e], c[e]), xo[e], mul2(wo[e], sn[e]));
         if (!turned) {  // (0 times an infinity is no number)
 #pragma unroll
-            for (int e = 0; e < 8; ++e) z[e] = y[e];
+            for (int e = 0; e < 4; ++e) z[e] = mul2(x[e], w[e]);
         }
-        if (!is_v) {
-            u.x = pack_bf16(z[0], z[1]), u.y = pack_bf16(z[2], z[3]);
-            u.z = pack_bf16(z[4], z[5]), u.w = pack_bf16(z[6], z[7]);
-        }
+        if (!is_v) u = finish(z, inv);
     }
     if (h >= nrow) return;
     if (is_q) {
@@ -189,8 +233,8 @@ constexpr int kTokMaxStages = 8;
 constexpr int kTokMaxSmem = 110 * 1024;  // of a CTA, two of which share an SM
 // Calls of up to this many head rows (tokens times heads) take the other kernel: all their
 // loads are in flight at once and there is no pipeline to fill.  Measured with 56 heads of 128
-// (staged / a warp per two rows, us): 128 tokens 4.7 / 2.9, 256 5.3 / 4.5, 384 5.8 / 5.9,
-// 1024 9.8 / 12.0, 2048 14.9 / 22.0.
+// (staged / a warp per two rows, us): 128 tokens 4.6 / 2.6, 256 4.9 / 4.1, 384 5.4 / 4.9, 512 5.8 / 6.1,
+// 1024 9.0 / 10.6.
 constexpr int kSmallRows = 20480;
 constexpr uint64_t kTokTimeoutNs = 1000000000ull;
 
@@ -238,25 +282,6 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_
 __host__ __device__ __forceinline__ int tok_stage_bytes(int hq, int hkv, int D, int rot)
 {
     return (hq + 2 * hkv) * D * 2 + rot * 4;
-}
-
-// (a*b) on both halves, round-to-nearest.
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b)
-{
-    uint64_t d;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-    return d;
-}
-
-// Eight bf16 as pairs of neighbours, in fp32; with `swap` each pair the other way round.
-__device__ __forceinline__ void pairs4(const uint4 &u, uint64_t (&x)[4], bool swap)
-{
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        const float lo = bf_lo(w[e]), hi = bf_hi(w[e]);
-        x[e] = swap ? ptx::pack2(hi, lo) : ptx::pack2(lo, hi);
-    }
 }
 
 template <int D, bool INTER>
@@ -401,26 +426,20 @@ __global__ void __launch_bounds__(kTokThreads, 4) append_staged_kernel(const App
                 pairs4(uo, xo, INTER);
                 float inv = 1.f;
                 if (a.qw || a.kw) {
-                    uint64_t s2 = mul2(x[0], x[0]);
-#pragma unroll
-                    for (int e = 1; e < 4; ++e) s2 = ptx::fma2(x[e], x[e], s2);
-                    float ss, hi;
-                    ptx::unpack2(s2, ss, hi);
-                    ss += hi;
+                    float ss = squares(x);
 #pragma unroll
                     for (int o = LPR / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-                    if (is_q ? a.qw : a.kw) inv = rsqrtf(ss * (1.f / D) + a.eps);
+                    if (is_q ? a.qw : a.kw) inv = inverse_norm(ss, 1.f / D, a.eps);
                 }
                 if (__all_sync(0xffffffffu, is_q)) {
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) z[e] = ptx::fma2(x[e], qa[e], mul2(xo[e], qb[e]));
+                    for (int e = 0; e < 4; ++e) z[e] = turn2(x[e], qa[e], xo[e], qb[e]);
                 } else {
                     uint64_t w[4], wo[4];
                     pairs4(is_q ? wq : wk, w, false);
                     pairs4(is_q ? wqo : wko, wo, INTER);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        z[e] = ptx::fma2(x[e], mul2(w[e], c[e]), mul2(xo[e], mul2(wo[e], sn[e])));
+                    for (int e = 0; e < 4; ++e) z[e] = turn2(x[e], mul2(w[e], c[e]), xo[e], mul2(wo[e], sn[e]));
                 }
                 if (a.rot < D && !turned) {  // (0 times an infinity is no number)
                     uint64_t w[4];
@@ -428,17 +447,7 @@ __global__ void __launch_bounds__(kTokThreads, 4) append_staged_kernel(const App
 #pragma unroll
                     for (int e = 0; e < 4; ++e) z[e] = mul2(x[e], w[e]);
                 }
-                if (!is_v) {
-                    const uint64_t i2 = ptx::pack2(inv, inv);
-                    uint32_t r[4];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        float lo, hi;
-                        ptx::unpack2(mul2(z[e], i2), lo, hi);
-                        r[e] = pack_bf16(lo, hi);
-                    }
-                    u = make_uint4(r[0], r[1], r[2], r[3]);
-                }
+                if (!is_v) u = finish(z, inv);
             }
             if (!in) continue;
             if (is_q) {
@@ -463,8 +472,8 @@ cudaError_t launch(const AppArgs &a, cudaStream_t st)
     // As many CTAs per SM, up to four, as hold a token each: it is their warps that count, more than the tokens
     // staged.  Fewer than two (more than about 435 head rows of 128): the other kernel.  Measured, 4096 tokens, at 4 / 3
     // / 2 / 1 CTAs with what then fits, and the other kernel (us): 64 and 2 x 64 heads of 128 (1, 1, 2, 4 tokens)
-    // 88.6 / 102 / 119 / 209, 151; 192 and 2 x 24 - / 132 / 181 / 279, 194; 256 and 2 x 64 - / - / 271 / 430,
-    // 308; 320 and 2 x 80 - / - / - / 582, 384.
+    // 88.3 / 102 / 119 / 209, 135; 192 and 2 x 24 - / 132 / 181 / 279, 177; 256 and 2 x 64 - / - / 270 / 429,
+    // 278; 320 and 2 x 80 - / - / - / 582, 346.
     int stages = 0, per_sm = 4;
     for (; per_sm > 1; --per_sm) {
         const size_t room = per_sm == 4 ? 54 * 1024 : per_sm == 3 ? 74 * 1024 : kTokMaxSmem;
@@ -476,7 +485,7 @@ cudaError_t launch(const AppArgs &a, cudaStream_t st)
         const int parts = (a.hq + 2 * a.hkv + RPP - 1) / RPP;
         if (parts > 65535) return cudaErrorInvalidConfiguration;
         const dim3 grid((unsigned)(((int64_t)a.rows + WPC - 1) / WPC), (unsigned)parts);
-        return launch_dependent(append_kernel<D>, grid, kAppThreads, 0, st, a);
+        return launch_dependent(a.inter ? append_kernel<D, true> : append_kernel<D, false>, grid, kAppThreads, 0, st, a);
     }
     if (stages > kTokMaxStages) stages = kTokMaxStages;
     const size_t smem = head + (size_t)stages * sb;

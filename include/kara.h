@@ -292,8 +292,9 @@ typedef struct {
  * slot[t] >= 0 and each head:
  *     y = x / sqrt(mean(x^2) + eps) * weight       (y = x without a weight)
  *     z_a = y_a cos - y_b sin,  z_b = y_b cos + y_a sin   for each rotated pair
- * in fp32 with one rounding to bf16; queries to q_out [rows][num_q_heads][D],
- * keys and (unchanged) values to the pool rows of slot[t].  With `ring` (the
+ * in fp32 with one rounding to bf16 (a token gets the same bits in calls of any
+ * length); queries to q_out [rows][num_q_heads][D], keys and (unchanged) values
+ * to the pool rows of slot[t].  With `ring` (the
  * window-query ring, bf16 [n][num_layers][num_q_heads][W][D]) the queries of the
  * last W positions of each sequence also go to ring row pos mod W.
  * q [rows][num_q_heads][D], k, v [rows][num_kv_heads][D]: bf16, heads of a row

@@ -309,3 +309,31 @@ def test_append_long_calls_of_wide_shapes(hq, hkv, D, rot, inter, W, rows):
         for s in (0, 1):
             last = torch.arange(int(ln[s]) - W, int(ln[s]))
             assert torch.equal(rg[s, last % W], got[int(q_start[s]) + last - int(lengths[s])])
+
+
+@pytest.mark.parametrize("hq,hkv,D,rot,inter,norms", [
+    (40, 8, 128, 128, False, "qk"), (32, 8, 128, 128, False, ""), (4, 2, 64, 64, True, "qk"), (6, 2, 128, 48, True, "k"),
+    (7, 1, 64, 32, False, "q"), (18, 3, 128, 96, False, "qk"), (2, 2, 128, 0, False, "qk")])
+def test_append_bits_do_not_depend_on_the_calls_length(hq, hkv, D, rot, inter, norms):
+    """A token's stored bits are the same whether it comes alone, with a few, or in a long call."""
+    kara = lib()
+    rows = 20480 // (hq + 2 * hkv) + 100
+    q, k, v = (x.to(DEV) for x in append_inputs(hq + D, hq, hkv, D, rows, fused=False))
+    g = torch.Generator().manual_seed(3)
+    w = [(1 + 0.3 * torch.randn(D, generator=g)).bfloat16().to(DEV) for _ in "qk"]
+    cs = angles(rows, rot).to(DEV) if rot else None
+    r = kara.rope(cs, w[0] if "q" in norms else None, w[1] if "k" in norms else None, interleaved=inter)
+    nb, got = (rows + 15) // 16, []
+    slot, pos, zero = torch.arange(rows, device=DEV), i32(range(rows)), i32([0] * rows)
+    for step in (rows, 37):
+        kp = torch.zeros(1, nb, hkv, 16, D, dtype=torch.bfloat16, device=DEV)
+        vp, out, err = torch.zeros_like(kp), torch.zeros_like(q), error_word()
+        c = kara.cache(kp, vp, hq)
+        for a in range(0, rows, step):
+            b = min(rows, a + step)
+            t = kara.tokens(i32([0, b - a]), i32([b]), slot[a:b], zero[a:b], pos[a:b])
+            kara.kara_append_kv(c, 0, t, r, q[a:b], k[a:b], v[a:b], out[a:b], err)
+        assert kara.kara_get_error(err) == 0
+        got.append([x.view(torch.int16) for x in (out, kp, vp)])
+    for one, other in zip(*got):
+        assert torch.equal(one, other)
