@@ -192,6 +192,7 @@ struct Shared {
     uint64_t done[2];
     uint32_t tmem;
     int32_t abort;
+    uint32_t loaded;      // K tiles issued so far
     int4 issued[2];       // K and V: tiles issued, edge tiles issued, which of the last tiles were (bit 0: the last)
     // quarters of an edge tile cleaned (by the tile's number: one warp may be a tile ahead), and
     // 1 + the last piece (by its number mod kOddSlots) whose V had values that are not finite
@@ -213,21 +214,25 @@ struct Cfg {
     static constexpr size_t kSmem = 1024 + (size_t)(2 + kStages) * kTileBytes + sizeof(Shared);
 };
 
-// Bounded wait on phase `parity` of `bar`: gives up after limit_ns, or once another
-// warp of the CTA gave up, recording KARA_ETIMEOUT.
+// Bounded wait on phase `parity` of `bar`: gives up after wait_ns, or once another
+// warp of the CTA gave up, recording KARA_ETIMEOUT.  The waits that nap are those of warps with
+// nothing to do for as long as an item takes (over 10^8 keys, a second): theirs begin anew
+// while key tiles are being loaded.
 template <int NAP = 0>
 __device__ __forceinline__ bool cwait(uint32_t bar, uint32_t parity, Shared *sh, const ChunkArgs &a)
 {
     if (mbar_try_wait(bar, parity)) return true;
     uint64_t t0 = 0;
+    uint32_t seen = 0;
     for (uint32_t it = 1;; ++it) {
         if (NAP) __nanosleep(NAP);
         if (mbar_try_wait(bar, parity)) return true;
         if ((it & 63u) == 0) {
             if (*(volatile int32_t *)&sh->abort) return false;
             const uint64_t now = globaltimer();
-            if (t0 == 0) {
-                t0 = now;
+            const uint32_t loaded = NAP ? *(volatile uint32_t *)&sh->loaded : 0;
+            if (t0 == 0 || loaded != seen) {
+                t0 = now, seen = loaded;
             } else if (now - t0 > a.wait_ns) {
                 set_err(a.err, KARA_ETIMEOUT);
                 *(volatile int32_t *)&sh->abort = 1;
@@ -889,6 +894,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(smem_u32(&sh->done[x]), 1);
         }
         sh->abort = 0;
+        sh->loaded = 0;
         for (int i = 0; i < kEdges; ++i) sh->fixed[i] = 0;
         for (int i = 0; i < kOddSlots; ++i) sh->odd_values[i] = 0;
         fence_mbarrier_init();
@@ -979,6 +985,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         tma_load_5d(smem_u32(ring + st * C::kTileBytes + h * C::kHalfBytes + b * kBlk * 128), map, fb,
                                     h * 64, 0, p.head, cur, a.layer);
                     ++k;
+                    if (kv == 0 && lane == 0) *(volatile uint32_t *)&sh->loaded = k;
                     st += 2;
                     if (st >= kStages) st -= kStages, ph ^= 1;
                 }
@@ -1410,7 +1417,7 @@ cudaError_t launch_chunk(const kara_cache *c, int32_t layer, const kara_tokens *
     a.wide = ((uintptr_t)out & 31u) == 0;
     const Stall dbg = debug_stall(kTimeoutNs);
     a.stall = dbg.on;
-    a.wait_ns = dbg.wait_ns;
+    a.wait_ns = dbg.on ? dbg.wait_ns : debug_wait(kTimeoutNs);
     int dev = 0, sms = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);

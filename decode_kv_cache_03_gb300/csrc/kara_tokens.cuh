@@ -5,6 +5,14 @@
 
 namespace kara {
 
+// Limit of the bounded waits of a call that stages its copies as usual, for tests: KARA_DEBUG_WAIT_NS
+// nanoseconds if that is in the environment.
+inline uint64_t debug_wait(uint64_t normal_ns)
+{
+    const char *v = getenv("KARA_DEBUG_WAIT_NS");
+    return v ? strtoull(v, nullptr, 10) : normal_ns;
+}
+
 // Launches `kern` as a programmatic dependent of what precedes it on the stream: its launch overlaps
 // that grid's end, and it reads nothing global before its griddepcontrol.wait.
 template <class... A>

@@ -337,3 +337,33 @@ def test_append_bits_do_not_depend_on_the_calls_length(hq, hkv, D, rot, inter, n
         got.append([x.view(torch.int16) for x in (out, kp, vp)])
     for one, other in zip(*got):
         assert torch.equal(one, other)
+
+
+def test_chunk_items_may_take_longer_than_a_wait(monkeypatch):
+    """Warps with nothing to do while an item's key tiles go by do not take that for a stall: here an item's
+    share of a CTA takes several times the limit.  Equal keys: the values' mean, exact in fp32."""
+    kara = lib()
+    L, m, hq, D = 12_000_000, 32, 8, 64
+    nb = L // 16
+    k = torch.zeros(1, nb, 1, 16, D, dtype=torch.bfloat16, device=DEV)
+    v = torch.empty_like(k)
+    v[:] = 2.0 ** (torch.arange(D, device=DEV) % 5 - 2)
+    q = torch.randn(m, hq, D, device=DEV).bfloat16()
+    z, z4 = torch.empty(m, dtype=torch.int64, device=DEV), torch.empty(m, dtype=torch.int32, device=DEV)
+    t, c = kara.tokens(i32([0, m]), i32([L]), z, z4, z4), kara.cache(k, v, hq)
+    bt = torch.arange(nb, dtype=torch.int32, device=DEV)[None]
+    ws = torch.empty(kara.kara_chunk_workspace_size(c, 1, m), dtype=torch.uint8, device=DEV)
+    out, err = torch.empty_like(q), error_word()
+    call = lambda: kara.kara_chunk_attention(c, 0, t, bt, q, out, ws, err)  # noqa: E731
+    call()
+    start, end = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+    start.record()
+    call()
+    end.record()
+    torch.cuda.synchronize()
+    assert start.elapsed_time(end) > 0.5
+    out.fill_(77.0)
+    monkeypatch.setenv("KARA_DEBUG_WAIT_NS", "150000")
+    call()
+    assert kara.kara_get_error(err) == 0
+    assert (out == v[0, 0, 0, 0]).all()
