@@ -1222,8 +1222,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         for (int e = 0; e < 32; ++e)
                             o[e] = __float_as_uint(fmaf(__uint_as_float(o1[e]), f1, __uint_as_float(o[e])));
                     }
-                    if (!live) continue;
-                    if (p.whole) {
+                    if (live && p.whole) {
                         // a warp's store touches 32 rows: as few and as wide as the alignment allows
                         uint32_t b[16];
 #pragma unroll
@@ -1238,12 +1237,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 *reinterpret_cast<uint4 *>(op + c + 2 * e) =
                                     make_uint4(b[e], b[e + 1], b[e + 2], b[e + 3]);
                         }
-                    } else {
+                    } else if (live) {
 #pragma unroll
                         for (int e = 0; e < 32; e += 4)
                             pp[(c + e) / 4 * 256] = make_float4(__uint_as_float(o[e]), __uint_as_float(o[e + 1]),
                                                                 __uint_as_float(o[e + 2]), __uint_as_float(o[e + 3]));
                     }
+                    __syncwarp();  // all lanes load the next columns
                 }
                 if (add && live) add_cleared<D>(a, p.seq, p.head, max(p.it.pos0 + 1, p.j0 * kTile),
                                                 min(pos, p.j1 * kTile - 1), p.whole ? op : nullptr, pp);
