@@ -136,7 +136,8 @@ def params(W, B, K, R, lam, score_mode=SCORE_BIDIRECTIONAL, select_mode=SELECT_T
 
 def cache(k: torch.Tensor, v: torch.Tensor, num_q_heads: int) -> Cache:
     """Describe bf16 pools laid out [layers][num_blocks][hkv][block][d] (rows contiguous)."""
-    assert k.dtype == torch.bfloat16 and v.shape == k.shape and v.stride() == k.stride()
+    assert k.dtype == v.dtype == torch.bfloat16 and v.shape == k.shape and v.stride() == k.stride()
+    assert v.device == k.device
     Lyr, nb, hkv, bs, d = k.shape
     assert k.stride(4) == 1 and k.stride(3) == d
     c = Cache(k.data_ptr(), v.data_ptr(), k.stride(0), k.stride(1), k.stride(2), Lyr, nb, hkv,

@@ -182,3 +182,12 @@ def test_chunk_refuses_a_workspace_off_its_alignment(kara):
         st = kara._lib.kara_chunk_attention(fake_cache(kara), 0, fake_tokens(kara), PTR, 4, PTR, PTR,
                                             ctypes.c_void_p(at), 1 << 40, PTR, None)
         assert st == kara.EINVAL, at
+
+
+def test_cache_refuses_values_unlike_the_keys(kara):
+    """The values' pool is of the keys' type and device: nothing checks them after this."""
+    k = torch.zeros(1, 4, 2, 16, 64, dtype=torch.bfloat16)
+    kara.cache(k, k.clone(), 4)
+    for v in (k.float(), k.half(), k.to("meta"), k[:, :3], k.transpose(1, 2)):
+        with pytest.raises(AssertionError):
+            kara.cache(k, v, 4)
