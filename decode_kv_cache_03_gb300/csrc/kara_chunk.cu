@@ -189,6 +189,7 @@ struct Shared {
     uint64_t x_full, x_free;  // a single query tile's odd half is ready to be joined; is joined
     uint64_t edge[kEdges];  // an edge tile of V has landed (by their number); `full` then says that it is clean
     uint64_t turn[2];     // the tensor cores are free for a query tile's next products
+    uint64_t pv[2];       // a query tile's last weighted sum is done: its weights may be overwritten
     uint64_t done[2];
     uint32_t tmem;
     int32_t abort;
@@ -746,9 +747,14 @@ __device__ __noinline__ void refuse_sequences(const ChunkArgs &a)
 // that the query tile skips is handed back at once), so each sees every phase of every
 // stage.  With two query tiles they take turns: first one tile's weighted sum and next
 // logits, then the other's, so that one tile is multiplied while the other is
-// exponentiated.  Descriptors are 32-bit sums, and both tiles share one copy of the code:
-// beside two busy softmax warps every instruction between two MMAs counts, and every line
-// of the instruction caches.
+// exponentiated.  A tile's next logits overwrite its weights in TMEM, so they wait until the
+// weighted sum is done: PTX keeps two MMAs in order only if they have the same accumulator
+// and shape.  (The wait takes the long prompt from 1330 to 1355 us, the mixed batch from 335
+// to 341, and costs few rows nothing.  Passing the turn on ahead of it, so that the other
+// tile's sum is multiplied meanwhile: 1420 and 357.  Polling: 1410 and 349.)
+// Descriptors are 32-bit sums, and both tiles share one copy of the code: beside two busy
+// softmax warps every instruction between two MMAs counts, and every line of the
+// instruction caches.
 template <int D>
 __device__ __forceinline__ void mma_warp(int x, uint32_t qbuf, uint32_t ring, Shared *sh, const ChunkArgs &a)
 {
@@ -761,12 +767,13 @@ __device__ __forceinline__ void mma_warp(int x, uint32_t qbuf, uint32_t ring, Sh
         const uint64_t qd = sdesc_sw128(qbuf), kd = sdesc_sw128(ring), vd = sdesc_sw128_mn(ring, C::kHalfBytes);
         const uint32_t full0 = smem_u32(&sh->full[0]), empty0 = smem_u32(&sh->empty[0]);
         const uint32_t sf = smem_u32(&sh->s_full[x]), pf = smem_u32(&sh->p_full[x]), ph = smem_u32(&sh->p_half[x]);
-        const uint32_t mine = smem_u32(&sh->turn[x]), other = smem_u32(&sh->turn[1 - x]);
+        const uint32_t pv = smem_u32(&sh->pv[x]), mine = smem_u32(&sh->turn[x]), other = smem_u32(&sh->turn[1 - x]);
         Piece p;
         const auto wait = [&](uint32_t bar, uint32_t parity) { return kwait(bar, parity, sh, a); };
         uint32_t np = 0;
         uint32_t ks = 0, kp = 0, vs = 1, vp = 0;  // next K and V tile: stage, phase
         uint32_t pp = 0, turn = 1 - x, iq = 0;    // phases of the next weights, turn, query tiles
+        uint32_t sums = 0;                        // weighted sums issued
         bool ok = true;
         auto next = [](uint32_t &st, uint32_t &ph) {  // a tile further (K and V alternate)
             st += 2;
@@ -810,6 +817,8 @@ __device__ __forceinline__ void mma_warp(int x, uint32_t qbuf, uint32_t ring, Sh
 #pragma unroll
                         for (int e = kTile / 32; e < kTile / 16; ++e)
                             mma_ts(to, ts + e * 8, lo + e * 128, (uint32_t)(vd >> 32), id_pv, 1);
+                        mma_commit(pv);
+                        ++sums;
                         if (!two) mma_commit(empty0 + vs * 8);
                         if (t == last) mma_commit(smem_u32(&sh->o_full[x]));
                     } else {
@@ -824,6 +833,10 @@ __device__ __forceinline__ void mma_warp(int x, uint32_t qbuf, uint32_t ring, Sh
                     if (!two || t < first) ok = ok && kwait(full0 + ks * 8, kp, sh, a);
                     if (!ok) break;
                     if (logits) {
+                        // they go where the weights are: only once the sum of those is done
+                        if (sums > 0) ok = kwait(pv, (sums - 1) & 1, sh, a);
+                        if (!ok) break;
+                        tc_fence_after();
                         const uint32_t lo = (uint32_t)kd + ks * kTileDesc;
 #pragma unroll
                         for (int e = 0; e < D / 16; ++e)
@@ -891,6 +904,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = 0; i < kEdges; ++i) mbar_init(smem_u32(&sh->edge[i]), 1);
         for (int x = 0; x < 2; ++x) {
             mbar_init(smem_u32(&sh->turn[x]), 1);
+            mbar_init(smem_u32(&sh->pv[x]), 1);
             mbar_init(smem_u32(&sh->done[x]), 1);
         }
         sh->abort = 0;
