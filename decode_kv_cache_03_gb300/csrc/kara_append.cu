@@ -14,10 +14,12 @@
 // lanes hold a row, 16 bytes each, so a warp takes 32 / (D/8) rows at once; a
 // row's sum of squares is a butterfly over its lanes.  Two kernels, which give a
 // token the same bits (one arithmetic, below): for short calls a warp per pass,
-// everything in registers; for long ones tokens staged through shared memory by bulk copies, because what bounds a long call is the
-// latency of its chain of loads (slot, offset, table row, rows): in registers it
-// reached 4.0 TB/s with four passes a warp (8192 tokens, 40/8 heads of 128, with
-// the ring: 70 us), staged 5.4 TB/s (52 us).
+// everything in registers; for long ones tokens staged through shared memory by
+// bulk copies, because what bounds a long call is the latency of its chain of
+// loads (slot, offset, table row, rows): in registers it reached 4.0 TB/s with four
+// passes a warp (8192 tokens, 40/8 heads of 128, with the ring: 70 us), staged
+// 5.4 TB/s (52 us).  Pairs of neighbours take 50 us, a rotation of half the dims 56
+// (54), the same at D = 64 with as many heads 32 us (4.3 TB/s).
 #include "kara_sm100.cuh"
 #include "kara_tokens.cuh"
 
@@ -112,7 +114,8 @@ __device__ __forceinline__ uint4 finish(const uint64_t (&z)[4], float inv)
 }
 
 // A warp takes 32 / (D/8) rows of one token: token blockIdx.x * 8 + warp, rows of part blockIdx.y.
-// (Five blocks per SM: 48 registers.  Left at 68, 4096 tokens of 320 and 2 x 80 heads take 525 us, so 346.)
+// (Five blocks per SM, 48 registers: 4096 tokens of 320 and 2 x 80 heads take 346 us; as the compiler likes it,
+// with 56, 407 us.)
 template <int D, bool INTER>
 __global__ void __launch_bounds__(kAppThreads, 5) append_kernel(const AppArgs a)
 {
@@ -470,10 +473,10 @@ cudaError_t launch(const AppArgs &a, cudaStream_t st)
     const size_t head = (sizeof(TokShared) + 127) / 128 * 128;
     const int sb = tok_stage_bytes(a.hq, a.hkv, D, a.rot);
     // As many CTAs per SM, up to four, as hold a token each: it is their warps that count, more than the tokens
-    // staged.  Fewer than two (more than about 435 head rows of 128): the other kernel.  Measured, 4096 tokens, at 4 / 3
-    // / 2 / 1 CTAs with what then fits, and the other kernel (us): 64 and 2 x 64 heads of 128 (1, 1, 2, 4 tokens)
-    // 88.3 / 102 / 119 / 209, 135; 192 and 2 x 24 - / 132 / 181 / 279, 177; 256 and 2 x 64 - / - / 270 / 429,
-    // 278; 320 and 2 x 80 - / - / - / 582, 346.
+    // staged.  Fewer than two (more than about 435 head rows of 128): the other kernel.  Measured, 4096 tokens,
+    // at 4 / 3 / 2 / 1 CTAs with what then fits, and the other kernel (us): 64 and 2 x 64 heads of 128 (1, 1, 2
+    // and 4 tokens) 88.3 / 102 / 119 / 209, 135; 192 and 2 x 24 - / 132 / 181 / 279, 177; 256 and 2 x 64
+    // - / - / 270 / 429, 278; 320 and 2 x 80 - / - / - / 582, 346.
     int stages = 0, per_sm = 4;
     for (; per_sm > 1; --per_sm) {
         const size_t room = per_sm == 4 ? 54 * 1024 : per_sm == 3 ? 74 * 1024 : kTokMaxSmem;
@@ -485,7 +488,8 @@ cudaError_t launch(const AppArgs &a, cudaStream_t st)
         const int parts = (a.hq + 2 * a.hkv + RPP - 1) / RPP;
         if (parts > 65535) return cudaErrorInvalidConfiguration;
         const dim3 grid((unsigned)(((int64_t)a.rows + WPC - 1) / WPC), (unsigned)parts);
-        return launch_dependent(a.inter ? append_kernel<D, true> : append_kernel<D, false>, grid, kAppThreads, 0, st, a);
+        const auto kern = a.inter ? append_kernel<D, true> : append_kernel<D, false>;
+        return launch_dependent(kern, grid, kAppThreads, 0, st, a);
     }
     if (stages > kTokMaxStages) stages = kTokMaxStages;
     const size_t smem = head + (size_t)stages * sb;

@@ -22,7 +22,10 @@
 //     holds them as well as below 1, and O is rescaled in TMEM a few times per
 //     row and not per tile.  The weights are rounded to bf16 for the second
 //     product (2^-8 of each at most; the output's own rounding is as large);
-//     logits, maxima, sums and O are fp32.
+//     logits, maxima, sums and O are fp32.  (A second bf16 term of the weights
+//     would add half again to the tensor time of two query tiles.  With one, whose
+//     time is HBM's, it took the error from 0.0023 to 0.00166 in the 2-norm; but its
+//     terms are 0 or negative as well, and an infinite cached value became NaN.)
 //   * K and V come by TMA, one (block, KV head) slice of 16 rows at a time,
 //     128-byte swizzled, as 128-row tiles in a ring of 5 stages (160 KB in
 //     flight per SM).  Blocks past a sequence's end, and ids outside the pool,
@@ -35,26 +38,32 @@
 //   * Every CTA gets the same work (to within a key tile), whatever the lengths:
 //     all items' key tiles, weighted by what they cost, are laid end to end and cut
 //     evenly; in long calls whose items share keys, whole items go round the CTAs
-//     first, so that L2 serves the keys again (share_out).  A cut inside an item leaves partial (O, max, sum) in the workspace,
-//     joined by the merge kernel in CTA order, so results do not depend on timing.
+//     first, so that L2 serves the keys again (share_out).  A cut inside an item
+//     leaves partial (O, max, sum) in the workspace, joined by the merge kernel in
+//     CTA order, so results do not depend on timing.
 //
-// What set the pace on the way (8192 tokens over 16384 keys, 40/8 heads, D 128; us):
-// one thread issuing every MMA with the waits between them, 2008; its loop with ring
-// positions and descriptors that only advance by additions, 1715; one issuing thread
-// per query tile and one loading warp each for K and V (issuing a 2 KB copy takes about
+// What set the pace on the way (8192 tokens over 16384 keys, 40/8 heads, D 128; us, 20 calls
+// in a captured graph): one thread issuing every MMA with the waits between them, 2008; its
+// loop with ring positions and descriptors that only advance by additions, 1715; one issuing
+// thread per query tile and one loading warp each for K and V (issuing a 2 KB copy takes about
 // 90 clocks: one warp took 2900 clocks for the K and V tiles that two query tiles multiply
 // in 2048), the two tiles taking turns, 1595; the turn taken before the weights are
 // waited for, 1485; cuts by cost, 1455; waits that nap in the warps that have time, 1435;
 // the instruction caches (one copy of the epilogue's code and of the MMAs', the control
 // warps' waiting out of line, one warp that walks over the work and tells the others), 1390
 // (512 tokens x 32 sequences at 4096 keys: 852 -> 750); the weighted sum begun on half the
-// weights, 1330 to 1370 on several boxes (1.5 PFLOP/s, 0.8 of the measured cuBLAS burst); whole
-// items dealt round, 1310 to 1365 (the 32 sequences: 750 to 780 -> 680 to 705).
+// weights, 1330 to 1370 on several boxes; whole items dealt round, 1285 to 1340 (the 32
+// sequences: 750 to 780 -> 675 to 715); logits that wait for the weighted sum whose weights
+// they overwrite, 1335 to 1380 (705 to 730): 1.5 PFLOP/s, 0.8 of the measured cuBLAS burst.
+// Uncaptured calls in a loop run longer and hotter and take 1440 and 768.
 // Few rows over long caches (4 tokens x 128 sequences) read K and V at 6.9 to 7.0 TB/s.
-// What is left: a step of two query tiles takes about 2950 clocks against 2048 of tensor time
+// What is left: a step of two query tiles takes about 3050 clocks against 2048 of tensor time
 // (logits, exponentials and weighted sum of a tile depend on each other, and TMEM holds
 // one S per tile beside O), and the power limit: under back-to-back calls the clock falls
-// to 1.5 - 1.8 GHz.
+// to 1.5 - 1.8 GHz.  At D = 64 a step has half the tensor time and the same exponentials:
+// 0.85 to 0.9 PFLOP/s, with 128 columns of TMEM unused.  Items of one to four key tiles are
+// bound by their start and end: 256 sequences of 1 to 4 tokens over 64 to 512 keys take
+// 102 us, 2.2 times their bytes.
 //
 // Two launches: the attention (persistent, one CTA per SM, each of which works out
 // its own range) and the merge, programmatic dependents of what precedes them.
@@ -143,8 +152,8 @@ __device__ __forceinline__ bool chunk_ok(const ChunkArgs &a, int32_t r0, int32_t
 }
 
 // What a key tile and an item cost a CTA, in about 800 clocks: a key tile of two query tiles
-// 3000 to 3400, of one 2500, an item's start and end about 6500.  (Two to one for the tiles: the
-// mixed batch of decodes and chunks takes 358 us, four to three 338.)
+// 3000 to 3400, of one 2500, an item's start and end about 6500; all at D = 128.  (Two to one for
+// the tiles: the mixed batch of decodes and chunks takes 358 us, four to three 338, captured.)
 __device__ __forceinline__ int tile_cost(const ChunkArgs &a, int32_t ntok) { return ntok > a.TQ ? 4 : 3; }
 constexpr int kItemCost = 8;
 constexpr int kTilesPerCta = 2;  // fewer, and CTAs stay without work: a split costs a merge
@@ -540,7 +549,7 @@ __device__ __noinline__ bool whole_items(const ChunkArgs &a, Shared *sh, int cta
 // That alone has a CTA read the same keys again for each pair of query tiles, long after they have
 // left L2 when there are many caches.  So where items share keys, whole items go round the CTAs
 // first, those of the same keys at the same time: 512 tokens x 32 sequences at 4096 keys read 0.70 GB
-// from HBM and not 4.24, and take 680 to 705 us and not 750 to 780.  It takes about 1.5 us more ahead
+// from HBM and not 4.24, and take 675 to 715 us captured and not 750 to 780.  It takes about 1.5 us more ahead
 // of the first key tile, and gains nothing while a CTA has few: 82 to 86 against 80 us at 40 key tiles
 // a CTA, 128 to 132 against 131.5 at 80, 130.6 against 129.7 at 110.  It starts at kSharedTiles = 128.
 // Every CTA works all of this out for itself, from the lengths; a plan kernel ahead of this one

@@ -333,7 +333,9 @@ kara_status kara_append_kv(const kara_cache *c, int32_t layer, const kara_tokens
  * (where a sequence's keys are cut), never on timing.
  * ws/ws_bytes: at least kara_chunk_workspace_size(c, n, rows) bytes, 16-byte
  * aligned, used by this call alone until it has run (two calls that may overlap
- * need two).
+ * need two).  The size follows the cache's shape alone (42 MB at head_dim 128):
+ * where a call's work is cut depends on the cached lengths, which only the device
+ * knows, and each of up to 160 CTAs may hold two partials.
  * Returns KARA_ECUDA, before any launch, if a TMA tensor map cannot be encoded.
  * Two launches, programmatic dependents of what precedes them on `stream`; the
  * call may be captured into a CUDA graph.
