@@ -14,7 +14,7 @@ from test_gpu_newtokens import (DEV, angles, append_inputs, assert_nothing_done,
 pytestmark = pytest.mark.gpu
 
 
-class NodeParams(ctypes.Structure):   # of the driver's second version of the call
+class NodeParams(ctypes.Structure):   # CUDA_KERNEL_NODE_PARAMS_v2
     _fields_ = [("func", ctypes.c_void_p), ("grid", ctypes.c_uint * 3), ("block", ctypes.c_uint * 3),
                 ("smem", ctypes.c_uint), ("params", ctypes.c_void_p), ("extra", ctypes.c_void_p),
                 ("kern", ctypes.c_void_p), ("ctx", ctypes.c_void_p)]
@@ -312,8 +312,8 @@ def test_append_long_calls_of_wide_shapes(hq, hkv, D, rot, inter, W, rows):
 
 
 @pytest.mark.parametrize("hq,hkv,D,rot,inter,norms", [
-    (40, 8, 128, 128, False, "qk"), (32, 8, 128, 128, False, ""), (4, 2, 64, 64, True, "qk"), (6, 2, 128, 48, True, "k"),
-    (7, 1, 64, 32, False, "q"), (18, 3, 128, 96, False, "qk"), (2, 2, 128, 0, False, "qk")])
+    (40, 8, 128, 128, False, "qk"), (32, 8, 128, 128, False, ""), (4, 2, 64, 64, True, "qk"),
+    (6, 2, 128, 48, True, "k"), (7, 1, 64, 32, False, "q"), (18, 3, 128, 96, False, "qk"), (2, 2, 128, 0, False, "qk")])
 def test_append_bits_do_not_depend_on_the_calls_length(hq, hkv, D, rot, inter, norms):
     """A token's stored bits are the same whether it comes alone, with a few, or in a long call."""
     kara = lib()
