@@ -1,0 +1,363 @@
+// New tokens into the 8-bit cache: per-head norms of q and k, the position rotation, and
+// the write of K and V, rounded to e4m3 with a scale for each block and head, in one pass.
+//
+// Rows are normed and turned as in the bf16 cache (kara_rows.cuh: a query gets the same
+// bits there).  The new rows of a block and head, at most 16, are a run.  With z the fp32
+// results (V: the inputs) and s0 the block's scale if the run continues it, else 0:
+//     s = max(s0, the smallest power of two with max |z| <= 448 s)
+//     code = rn(z / s),   and, if s > s0, code = rn(code s0 / s) for the rows ahead
+// One rounding from fp32; nothing is rounded to bf16 on the way.  A run needs its largest
+// value before its first code, so a warp holds a whole run of one head: all its loads are
+// in flight at once, and the rows stay in registers between the maximum and the rounding.
+// Queries go as in the bf16 append, a warp per token and a few heads.
+//
+// Runs follow from the slots alone: row t continues row t - 1 if its slot is the next one
+// and not the first of a block.  A warp looks at a window of `win` rows and takes the runs
+// that begin there.
+#include "kara_cache8.cuh"
+#include "kara_rows.cuh"
+#include "kara_tokens.cuh"
+
+namespace kara {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+constexpr int kBs = 16;      // tokens per cache block (the supported block size)
+constexpr int kQPasses = 4;  // passes of query rows a warp has in flight
+
+struct Append8Args {
+    const uint16_t *q, *k, *v;
+    int64_t qs, ks, vs;  // token strides (elements)
+    uint16_t *q_out, *ring;
+    uint8_t *kp, *vp;          // codes, at the call's layer
+    float *k_scale, *v_scale;  // [num_blocks][hkv], at the call's layer
+    int64_t block_stride, head_stride;
+    int64_t ring_seq, ring_head;  // strides of the ring (elements), at the call's layer
+    const uint16_t *qw, *kw;
+    const float *cos_sin;
+    const int32_t *shift;
+    const int64_t *slot;
+    const int32_t *seq, *pos, *len;
+    int32_t *err;
+    float eps;
+    int32_t n, rows, num_blocks, hq, hkv, W, n_pos, rot;
+    int32_t win, kv_blocks;  // rows of a window; CTAs that take runs
+};
+
+// Where a token goes; ok: its row is to be written.
+struct Place {
+    int64_t slot, r;  // slot, row of the rotation table
+    int32_t seq, pos;
+    bool ok;
+};
+
+__device__ __forceinline__ Place place_of(const Append8Args &a, int64_t t, bool record)
+{
+    Place p;
+    p.slot = a.slot[t];
+    p.seq = a.seq[t];
+    p.pos = a.pos[t];
+    const bool known = p.seq >= 0 && p.seq < a.n, inside = p.slot >= 0 && p.slot < (int64_t)a.num_blocks * kBs;
+    // without a rotation every rotary position will do
+    p.r = a.rot == 0 ? 0 : (int64_t)p.pos + (known && a.shift ? a.shift[p.seq] : 0);
+    p.ok = inside && known && p.pos >= 0 && p.r >= 0 && p.r < a.n_pos;
+    if (record && !p.ok && p.slot != -1) set_err(a.err, inside ? KARA_EINVAL : KARA_EBADBLOCK);
+    return p;
+}
+
+// What a lane does with its eight dims of every row: which of them turn, with which lane.
+template <int D, bool INTER>
+struct LaneDims {
+    int d0, half, other;
+    bool turned, low;
+    __device__ LaneDims(const Append8Args &a, int lane)
+    {
+        d0 = lane % (D / 8) * 8;
+        half = a.rot >> 1;
+        turned = d0 < a.rot, low = d0 < half;
+        // lane that holds the other half of this lane's pairs
+        other = !turned || INTER ? lane : low ? lane + half / 8 : lane - half / 8;
+    }
+    // cosines and signed sines, in pairs of neighbours
+    __device__ __forceinline__ void factors(const Append8Args &a, int64_t r, uint64_t (&c)[4], uint64_t (&sn)[4]) const
+    {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) c[e] = ptx::pack2(1.f, 1.f), sn[e] = ptx::pack2(0.f, 0.f);
+        if (!turned) return;
+        const float *row = a.cos_sin + r * a.rot;
+        if (INTER) {
+            const float4 cc = ldg4(row + d0 / 2), ss = ldg4(row + half + d0 / 2);
+            c[0] = ptx::pack2(cc.x, cc.x), c[1] = ptx::pack2(cc.y, cc.y);
+            c[2] = ptx::pack2(cc.z, cc.z), c[3] = ptx::pack2(cc.w, cc.w);
+            sn[0] = ptx::pack2(-ss.x, ss.x), sn[1] = ptx::pack2(-ss.y, ss.y);
+            sn[2] = ptx::pack2(-ss.z, ss.z), sn[3] = ptx::pack2(-ss.w, ss.w);
+        } else {
+            const int j0 = low ? d0 : d0 - half;
+            const uint64_t sg = low ? ptx::pack2(-1.f, -1.f) : ptx::pack2(1.f, 1.f);
+#pragma unroll
+            for (int e = 0; e < 4; e += 2) {
+                const float4 cc = ldg4(row + j0 + 2 * e), ss = ldg4(row + half + j0 + 2 * e);
+                c[e] = ptx::pack2(cc.x, cc.y), c[e + 1] = ptx::pack2(cc.z, cc.w);
+                sn[e] = mul2(sg, ptx::pack2(ss.x, ss.y)), sn[e + 1] = mul2(sg, ptx::pack2(ss.z, ss.w));
+            }
+        }
+    }
+    // a norm's weights of this lane's dims and of their partners (1 without one)
+    __device__ __forceinline__ void weights(const uint16_t *wp, uint4 &w, uint4 &wo) const
+    {
+        w = wo = make_uint4(0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u);
+        if (!wp) return;
+        w = __ldg(reinterpret_cast<const uint4 *>(wp + d0));
+        wo = INTER ? w : __ldg(reinterpret_cast<const uint4 *>(wp + (turned ? low ? d0 + half : d0 - half : d0)));
+    }
+    // z = (x w c + x' w' s), x' and w' of the pair's other member, and 1 / the norm; the whole warp
+    __device__ __forceinline__ void turn(const Append8Args &a, const uint4 &u, const uint16_t *wp, const uint4 &uw,
+                                         const uint4 &uwo, const uint64_t (&c)[4], const uint64_t (&sn)[4],
+                                         uint64_t (&z)[4], float &inv) const
+    {
+        uint4 uo = u;
+        if (!INTER && a.rot > 0) {
+            uo.x = __shfl_sync(0xffffffffu, u.x, other), uo.y = __shfl_sync(0xffffffffu, u.y, other);
+            uo.z = __shfl_sync(0xffffffffu, u.z, other), uo.w = __shfl_sync(0xffffffffu, u.w, other);
+        }
+        uint64_t x[4], xo[4], w[4], wo[4];
+        pairs4(u, x, false), pairs4(uo, xo, INTER);
+        pairs4(uw, w, false), pairs4(uwo, wo, INTER);
+        inv = 1.f;
+        if (wp) {
+            float ss = squares(x);
+#pragma unroll
+            for (int o = D / 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+            inv = inverse_norm(ss, 1.f / D, a.eps);
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) z[e] = turn2(x[e], mul2(w[e], c[e]), xo[e], mul2(wo[e], sn[e]));
+        if (!turned) {  // (0 times an infinity is no number)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) z[e] = mul2(x[e], w[e]);
+        }
+    }
+};
+
+// A run: m rows from t0 on, into the rows from `at` on of block blk; lane i of the warp has the
+// rotation table's row of the window's token i - 1, and `first` is the run's first lane.
+template <int D, bool INTER>
+__device__ __forceinline__ void store_run(const Append8Args &a, const LaneDims<D, INTER> &dims, bool is_v, int g,
+                                          int64_t t0, int m, int64_t blk, int at, int64_t r, int first, int lane)
+{
+    constexpr int LPR = D / 8, RPP = 32 / LPR, NP = kBs / RPP;
+    const int sub = lane / LPR;
+    const uint16_t *src = (is_v ? a.v + g * D : a.k + g * D) + dims.d0;
+    const int64_t stride = is_v ? a.vs : a.ks;
+    uint4 u[NP];
+#pragma unroll
+    for (int p = 0; p < NP; ++p) {
+        const int i = p * RPP + sub;
+        u[p] = i < m ? *reinterpret_cast<const uint4 *>(src + (t0 + i) * stride) : make_uint4(0, 0, 0, 0);
+    }
+    float *sp = (is_v ? a.v_scale : a.k_scale) + blk * a.hkv + g;
+    const float old = at > 0 ? *sp : 0.f;
+    uint8_t *codes = (is_v ? a.vp : a.kp) + blk * a.block_stride + g * a.head_stride;
+    uint64_t z[NP][4];
+    if (is_v) {
+#pragma unroll
+        for (int p = 0; p < NP; ++p) pairs4(u[p], z[p], false);
+    } else {
+        uint4 uw, uwo;
+        dims.weights(a.kw, uw, uwo);
+#pragma unroll
+        for (int p = 0; p < NP; ++p) {
+            if (p * RPP >= m) break;
+            uint64_t c[4], sn[4];
+            const int64_t row = __shfl_sync(0xffffffffu, r, min(first + p * RPP + sub, first + m - 1));
+            dims.factors(a, row, c, sn);
+            float inv;
+            dims.turn(a, u[p], a.kw, uw, uwo, c, sn, z[p], inv);
+            const uint64_t i2 = ptx::pack2(inv, inv);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) z[p][e] = mul2(z[p][e], i2);
+        }
+    }
+    float top = 0.f;
+    bool odd = false;  // a value that is not finite
+#pragma unroll
+    for (int p = 0; p < NP; ++p) {
+        if (p * RPP + sub >= m) continue;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            float lo, hi;
+            ptx::unpack2(z[p][e], lo, hi);
+            if (finite(lo)) top = fmaxf(top, fabsf(lo)); else odd = true;
+            if (finite(hi)) top = fmaxf(top, fabsf(hi)); else odd = true;
+        }
+    }
+    top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));
+    odd = __any_sync(0xffffffffu, odd);
+    const float before = fabsf(old), s = fmaxf(before, scale_for(top)), inv = inverse_scale(s);
+    if (s > before && at > 0) {
+        const float ratio = before * inv;
+        for (int i = lane; i < at * D / 16; i += 32) {
+            uint4 *p = reinterpret_cast<uint4 *>(codes) + i;
+            uint4 w = *p;
+            w.x = rescale4(w.x, ratio), w.y = rescale4(w.y, ratio);
+            w.z = rescale4(w.z, ratio), w.w = rescale4(w.w, ratio);
+            *p = w;
+        }
+    }
+    const uint64_t i2 = ptx::pack2(inv, inv);
+#pragma unroll
+    for (int p = 0; p < NP; ++p) {
+        const int i = p * RPP + sub;
+        if (i >= m) continue;
+        uint32_t w[2] = {0u, 0u};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            float lo, hi;
+            ptx::unpack2(mul2(z[p][e], i2), lo, hi);
+            if (odd) {  // e4m3 has no infinity: NaN (0 times an infinity is one already)
+                if (!finite(lo)) lo = __uint_as_float(0x7fffffffu);
+                if (!finite(hi)) hi = __uint_as_float(0x7fffffffu);
+            }
+            w[e >> 1] |= e4m3x2(lo, hi) << (16 * (e & 1));
+        }
+        *reinterpret_cast<uint2 *>(codes + (at + i) * D + dims.d0) = make_uint2(w[0], w[1]);
+    }
+    // the sign says that the block may hold a NaN
+    if (lane == 0) *sp = odd || signbit(old) ? -s : s;
+}
+
+template <int D, bool INTER>
+__device__ __forceinline__ void store_window(const Append8Args &a, const LaneDims<D, INTER> &dims, int64_t task, int lane)
+{
+    const int h = (int)(task % (2 * a.hkv));
+    const bool is_v = h >= a.hkv;
+    const int g = is_v ? h - a.hkv : h;
+    // lane i: row t0 - 1 + i.  Runs that begin in the window (lanes 1 .. win) end by lane win + 15.
+    const int64_t t0 = task / (2 * a.hkv) * a.win, t = t0 - 1 + lane;
+    Place p{};
+    p.slot = -1;
+    if (t >= 0 && t < a.rows && lane < a.win + kBs) p = place_of(a, t, h == 0 && lane >= 1 && lane <= a.win);
+    const int64_t ahead = __shfl_up_sync(0xffffffffu, p.ok ? p.slot : -2, 1);
+    const bool follows = p.ok && lane > 0 && ahead + 1 == p.slot && p.slot % kBs != 0;
+    const unsigned cont = __ballot_sync(0xffffffffu, follows);
+    unsigned heads = __ballot_sync(0xffffffffu, p.ok && !follows && lane >= 1 && lane <= a.win);
+    for (; heads; heads &= heads - 1) {
+        const int first = __ffs(heads) - 1;
+        // rows that follow, up to the end of the block
+        const int m = __ffs(~(cont >> (first + 1)));
+        const int64_t slot = __shfl_sync(0xffffffffu, p.slot, first);
+        store_run<D, INTER>(a, dims, is_v, g, t0 - 1 + first, m, slot / kBs, (int)(slot % kBs), p.r, first, lane);
+    }
+}
+
+template <int D, bool INTER>
+__global__ void __launch_bounds__(kThreads, 2) append8_kernel(const Append8Args a)
+{
+    constexpr int LPR = D / 8, RPP = 32 / LPR, HPW = kQPasses * RPP;  // query heads a warp takes
+    const int lane = threadIdx.x & 31;
+    const LaneDims<D, INTER> dims(a, lane);
+    // launched as a programmatic dependent of what precedes it on the stream
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (blockIdx.x < a.kv_blocks) {
+        const int64_t task = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
+        if (task < ((int64_t)a.rows + a.win - 1) / a.win * (2 * a.hkv)) store_window<D, INTER>(a, dims, task, lane);
+        return;
+    }
+    const int parts = (a.hq + HPW - 1) / HPW;
+    const int64_t task = (int64_t)(blockIdx.x - a.kv_blocks) * kWarps + (threadIdx.x >> 5), t = task / parts;
+    if (t >= a.rows) return;
+    const int h0 = (int)(task % parts) * HPW + lane / LPR;
+    // the rows are on their way before the token's place is known (padding rows are read, not written)
+    uint4 u[kQPasses];
+#pragma unroll
+    for (int p = 0; p < kQPasses; ++p) {
+        const int h = h0 + p * RPP;
+        u[p] = h < a.hq ? *reinterpret_cast<const uint4 *>(a.q + t * a.qs + h * D + dims.d0) : make_uint4(0, 0, 0, 0);
+    }
+    const Place pl = place_of(a, t, false);
+    if (!pl.ok) return;
+    uint64_t c[4], sn[4];
+    dims.factors(a, pl.r, c, sn);
+    uint4 uw, uwo;
+    dims.weights(a.qw, uw, uwo);
+    uint16_t *ring = nullptr;  // this token's row of the ring, if it is of the last W
+    if (a.ring) {
+        const int32_t L = a.len[pl.seq];
+        if (pl.pos < L && pl.pos >= (int64_t)L - a.W)
+            ring = a.ring + pl.seq * a.ring_seq + (int64_t)(pl.pos % a.W) * D + dims.d0;
+    }
+#pragma unroll
+    for (int p = 0; p < kQPasses; ++p) {
+        const int h = h0 + p * RPP;
+        if (h - lane / LPR >= a.hq) break;
+        uint64_t z[4];
+        float inv;
+        dims.turn(a, u[p], a.qw, uw, uwo, c, sn, z, inv);
+        const uint4 y = finish(z, inv);
+        if (h >= a.hq) continue;
+        *reinterpret_cast<uint4 *>(a.q_out + (t * a.hq + h) * D + dims.d0) = y;
+        if (ring) *reinterpret_cast<uint4 *>(ring + h * a.ring_head) = y;
+    }
+}
+
+template <int D>
+cudaError_t launch(Append8Args &a, bool inter, cudaStream_t st)
+{
+    constexpr int HPW = kQPasses * (32 / (D / 8));
+    // short calls: a warp for each row that may begin a run; long ones look at four rows each
+    a.win = a.rows <= 512 ? 1 : 4;
+    const int64_t runs = ((int64_t)a.rows + a.win - 1) / a.win * (2 * a.hkv);
+    const int64_t queries = (int64_t)a.rows * ((a.hq + HPW - 1) / HPW);
+    const int64_t kv = (runs + kWarps - 1) / kWarps, blocks = kv + (queries + kWarps - 1) / kWarps;
+    if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+    a.kv_blocks = (int32_t)kv;
+    const auto kern = inter ? append8_kernel<D, true> : append8_kernel<D, false>;
+    return launch_dependent(kern, dim3((unsigned)blocks), kThreads, 0, st, (const Append8Args)a);
+}
+
+}  // namespace
+
+cudaError_t launch_append8(const kara_cache8 *c, int32_t layer, const kara_tokens *t, const kara_rope *r, const void *q,
+                           int64_t q_stride, const void *k, int64_t k_stride, const void *v, int64_t v_stride,
+                           void *q_out, void *ring, int32_t W, int32_t *err, cudaStream_t st)
+{
+    const int D = c->head_dim;
+    const int64_t scales = (int64_t)layer * c->num_blocks * c->num_kv_heads;
+    Append8Args a;
+    a.q = static_cast<const uint16_t *>(q);
+    a.k = static_cast<const uint16_t *>(k);
+    a.v = static_cast<const uint16_t *>(v);
+    a.qs = q_stride, a.ks = k_stride, a.vs = v_stride;
+    a.q_out = static_cast<uint16_t *>(q_out);
+    a.kp = static_cast<uint8_t *>(c->k) + (int64_t)layer * c->layer_stride;
+    a.vp = static_cast<uint8_t *>(c->v) + (int64_t)layer * c->layer_stride;
+    a.k_scale = c->k_scale + scales;
+    a.v_scale = c->v_scale + scales;
+    a.block_stride = c->block_stride;
+    a.head_stride = c->head_stride;
+    a.W = ring ? W : 1;
+    a.ring_head = (int64_t)W * D;
+    a.ring_seq = (int64_t)c->num_layers * c->num_q_heads * a.ring_head;
+    a.ring = ring ? static_cast<uint16_t *>(ring) + (int64_t)layer * c->num_q_heads * a.ring_head : nullptr;
+    a.qw = static_cast<const uint16_t *>(r->q_weight);
+    a.kw = static_cast<const uint16_t *>(r->k_weight);
+    a.cos_sin = r->cos_sin;
+    a.shift = r->pos_offset;
+    a.slot = t->slot;
+    a.seq = t->seq;
+    a.pos = t->pos;
+    a.len = t->len;
+    a.err = err;
+    a.eps = r->eps;
+    a.n = t->n;
+    a.rows = t->rows;
+    a.num_blocks = c->num_blocks;
+    a.hq = c->num_q_heads;
+    a.hkv = c->num_kv_heads;
+    a.n_pos = r->rot_dim > 0 ? r->n_pos : 1;
+    a.rot = r->rot_dim;
+    return D == 128 ? launch<128>(a, r->interleaved, st) : launch<64>(a, r->interleaved, st);
+}
+
+}  // namespace kara

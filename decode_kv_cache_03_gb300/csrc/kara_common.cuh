@@ -99,6 +99,7 @@ cudaError_t launch_compact(const Geo &g, const SeqPlan *plan, const int32_t *kep
 // then points at the group's first entry; offsets into fresh stay the batch's).
 cudaError_t launch_fresh_check(const Geo &g, const SeqPlan *plan, const int32_t *fresh, int64_t n_fresh,
                                int32_t *err, cudaStream_t st);
+cudaError_t launch_kept_check(const Geo &g, const int32_t *kept, int32_t *err, cudaStream_t st);
 cudaError_t launch_kept_copy(const Geo &g, const SeqPlan *plan, const int32_t *kept, const int32_t *fresh,
                              int64_t n_fresh, int32_t *err, cudaStream_t st);
 cudaError_t launch_commit(const Geo &g, const SeqPlan *plan, const int32_t *fresh, int32_t *freed,

@@ -6,6 +6,7 @@
 
 #include <nvtx3/nvToolsExt.h>
 
+#include "kara_cache8.cuh"
 #include "kara_tokens.cuh"
 
 using namespace kara;
@@ -35,9 +36,10 @@ kara_status check_params(const kara_params *p)
     return KARA_OK;
 }
 
-kara_status check_cache(const kara_cache *c)
+// The shapes of a cache, in 16 or 8 bits.
+template <class Cache>
+kara_status check_shape(const Cache *c)
 {
-    if (!c || !c->k || !c->v) return KARA_EINVAL;
     if (c->head_dim != 64 && c->head_dim != 128) return KARA_EUNSUPPORTED;
     if (c->block_size != 16) return KARA_EUNSUPPORTED;
     if (c->num_kv_heads < 1 || c->num_q_heads < 1 || c->num_q_heads % c->num_kv_heads != 0)
@@ -45,9 +47,47 @@ kara_status check_cache(const kara_cache *c)
     if (c->num_q_heads / c->num_kv_heads > kMaxG) return KARA_EUNSUPPORTED;
     if (c->num_layers < 1 || c->num_blocks < 1) return KARA_EINVAL;
     if (!aligned16(c->k) || !aligned16(c->v)) return KARA_EINVAL;
-    if (c->layer_stride % 8 || c->block_stride % 8 || c->head_stride % 8) return KARA_EINVAL;
     if (c->layer_stride < 0 || c->block_stride < 0 || c->head_stride < 0) return KARA_EINVAL;
     return KARA_OK;
+}
+
+kara_status check_cache(const kara_cache *c)
+{
+    if (!c || !c->k || !c->v) return KARA_EINVAL;
+    const kara_status st = check_shape(c);
+    if (st != KARA_OK) return st;
+    return c->layer_stride % 8 || c->block_stride % 8 || c->head_stride % 8 ? KARA_EINVAL : KARA_OK;
+}
+
+kara_status check_cache8(const kara_cache8 *c)
+{
+    if (!c || !c->k || !c->v || !c->k_scale || !c->v_scale) return KARA_EINVAL;
+    const kara_status st = check_shape(c);
+    if (st != KARA_OK) return st;
+    if (((uintptr_t)c->k_scale | (uintptr_t)c->v_scale) & 3u) return KARA_EINVAL;
+    return c->layer_stride % 16 || c->block_stride % 16 || c->head_stride % 16 ? KARA_EINVAL : KARA_OK;
+}
+
+// The arguments of an append beside the cache.
+template <class Cache>
+kara_status check_append(const Cache *c, int32_t layer, const kara_tokens *t, const kara_rope *r, const void *q,
+                         int64_t q_stride, const void *k, int64_t k_stride, const void *v, int64_t v_stride,
+                         const void *q_out, const void *ring, int32_t W, const int32_t *err)
+{
+    if (layer < 0 || layer >= c->num_layers || !t || t->n < 0 || t->rows < 0 || !r) return KARA_EINVAL;
+    if (r->rot_dim < 0 || r->rot_dim > c->head_dim || r->rot_dim % 16 || !(r->eps >= 0.f)) return KARA_EINVAL;
+    if (r->interleaved != 0 && r->interleaved != 1) return KARA_EINVAL;
+    if (r->rot_dim > 0 && (!r->cos_sin || !aligned16(r->cos_sin) || r->n_pos < 1)) return KARA_EINVAL;
+    if (!aligned16(r->q_weight) || !aligned16(r->k_weight)) return KARA_EINVAL;
+    if (ring && (W < 1 || !aligned16(ring))) return KARA_EINVAL;
+    if (t->rows == 0) return KARA_OK;
+    if (!t->slot || !t->seq || !t->pos || (ring && t->n > 0 && !t->len)) return KARA_EINVAL;
+    if (!q || !k || !v || !q_out || !err) return KARA_EINVAL;
+    if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(q_out)) return KARA_EINVAL;
+    const int64_t qd = (int64_t)c->num_q_heads * c->head_dim, kd = (int64_t)c->num_kv_heads * c->head_dim;
+    if (q_stride < qd || k_stride < kd || v_stride < kd || q_stride % 8 || k_stride % 8 || v_stride % 8)
+        return KARA_EINVAL;
+    return q_out == q && q_stride != qd ? KARA_EINVAL : KARA_OK;
 }
 
 kara_status make_geo(const kara_cache *c, const kara_params *p, const kara_batch *b, Geo *g)
@@ -371,24 +411,23 @@ kara_status kara_append_kv(const kara_cache *c, int32_t layer, const kara_tokens
                            void *q_out, void *ring, int32_t W, int32_t *err, kara_stream_t stream)
 {
     const Range range("kara_append_kv");
-    const kara_status st = check_cache(c);
-    if (st != KARA_OK) return st;
-    if (layer < 0 || layer >= c->num_layers || !t || t->n < 0 || t->rows < 0 || !r) return KARA_EINVAL;
-    if (r->rot_dim < 0 || r->rot_dim > c->head_dim || r->rot_dim % 16 || !(r->eps >= 0.f)) return KARA_EINVAL;
-    if (r->interleaved != 0 && r->interleaved != 1) return KARA_EINVAL;
-    if (r->rot_dim > 0 && (!r->cos_sin || !aligned16(r->cos_sin) || r->n_pos < 1)) return KARA_EINVAL;
-    if (!aligned16(r->q_weight) || !aligned16(r->k_weight)) return KARA_EINVAL;
-    if (ring && (W < 1 || !aligned16(ring))) return KARA_EINVAL;
-    if (t->rows == 0) return KARA_OK;
-    if (!t->slot || !t->seq || !t->pos || (ring && t->n > 0 && !t->len)) return KARA_EINVAL;
-    if (!q || !k || !v || !q_out || !err) return KARA_EINVAL;
-    if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(q_out)) return KARA_EINVAL;
-    const int64_t qd = (int64_t)c->num_q_heads * c->head_dim, kd = (int64_t)c->num_kv_heads * c->head_dim;
-    if (q_stride < qd || k_stride < kd || v_stride < kd || q_stride % 8 || k_stride % 8 || v_stride % 8)
-        return KARA_EINVAL;
-    if (q_out == q && q_stride != qd) return KARA_EINVAL;
+    kara_status st = check_cache(c);
+    if (st == KARA_OK) st = check_append(c, layer, t, r, q, q_stride, k, k_stride, v, v_stride, q_out, ring, W, err);
+    if (st != KARA_OK || t->rows == 0) return st;
     return cuda_status(launch_append(c, layer, t, r, q, q_stride, k, k_stride, v, v_stride, q_out, ring, W, err,
                                      (cudaStream_t)stream));
+}
+
+kara_status kara_append_kv8(const kara_cache8 *c, int32_t layer, const kara_tokens *t, const kara_rope *r,
+                            const void *q, int64_t q_stride, const void *k, int64_t k_stride, const void *v,
+                            int64_t v_stride, void *q_out, void *ring, int32_t W, int32_t *err, kara_stream_t stream)
+{
+    const Range range("kara_append_kv8");
+    kara_status st = check_cache8(c);
+    if (st == KARA_OK) st = check_append(c, layer, t, r, q, q_stride, k, k_stride, v, v_stride, q_out, ring, W, err);
+    if (st != KARA_OK || t->rows == 0) return st;
+    return cuda_status(launch_append8(c, layer, t, r, q, q_stride, k, k_stride, v, v_stride, q_out, ring, W, err,
+                                      (cudaStream_t)stream));
 }
 
 size_t kara_chunk_workspace_size(const kara_cache *c, int32_t n, int32_t rows)
@@ -412,6 +451,101 @@ kara_status kara_chunk_attention(const kara_cache *c, int32_t layer, const kara_
     if (!ws || ws_bytes < chunk_workspace_bytes(c)) return KARA_EWORKSPACE;
     if (!aligned16(ws)) return KARA_EINVAL;
     return cuda_status(launch_chunk(c, layer, t, block_table, bt_stride, q, out, ws, err, (cudaStream_t)stream));
+}
+
+size_t kara_decode8_workspace_size(const kara_cache8 *c, int32_t n, int32_t bt_stride)
+{
+    if (check_cache8(c) != KARA_OK || n < 0 || bt_stride < 1) return 0;
+    return decode8_workspace_bytes(c, n, bt_stride);
+}
+
+kara_status kara_decode_attention8(const kara_cache8 *c, int32_t layer, int32_t n, const int32_t *len,
+                                   const int32_t *block_table, int32_t bt_stride, const void *q, void *out, void *ws,
+                                   size_t ws_bytes, int32_t *err, kara_stream_t stream)
+{
+    const Range range("kara_decode_attention8");
+    const kara_status st = check_cache8(c);
+    if (st != KARA_OK) return st;
+    if (layer < 0 || layer >= c->num_layers || n < 0 || bt_stride < 1) return KARA_EINVAL;
+    if (n == 0) return KARA_OK;
+    if (!len || !block_table || !q || !out || !err) return KARA_EINVAL;
+    if (!aligned16(q) || !aligned16(out)) return KARA_EINVAL;
+    if (n > kMaxSeqs || c->num_q_heads > 65535) return KARA_EUNSUPPORTED;
+    if ((int64_t)bt_stride * c->block_size > 0x7fffffffLL) return KARA_EUNSUPPORTED;
+    if (decode8_max_splits(bt_stride) > 65535) return KARA_EUNSUPPORTED;  // grid z
+    if (!ws || ws_bytes < decode8_workspace_bytes(c, n, bt_stride)) return KARA_EWORKSPACE;
+    if (!aligned16(ws)) return KARA_EINVAL;
+    return cuda_status(launch_decode8(c, layer, n, len, block_table, bt_stride, q, out, ws, err,
+                                      (cudaStream_t)stream));
+}
+
+kara_status kara_expand8(const kara_cache8 *c, const kara_cache *out, int32_t W, int32_t n, const int32_t *len,
+                         const int32_t *block_table, int32_t bt_stride, int32_t *out_table, int32_t *err,
+                         kara_stream_t stream)
+{
+    const Range range("kara_expand8");
+    kara_status st = check_cache8(c);
+    if (st == KARA_OK) st = check_cache(out);
+    if (st != KARA_OK) return st;
+    if (W < 1 || W % c->block_size || n < 0 || bt_stride < 1) return KARA_EINVAL;
+    if (out->num_layers != c->num_layers || out->num_kv_heads != c->num_kv_heads || out->head_dim != c->head_dim)
+        return KARA_EINVAL;
+    if (n == 0) return KARA_OK;
+    if (!len || !block_table || !out_table || out_table == block_table || !err) return KARA_EINVAL;
+    if ((int64_t)bt_stride * c->block_size > 0x7fffffffLL || (int64_t)c->num_layers * c->num_kv_heads > 65535)
+        return KARA_EUNSUPPORTED;
+    if ((int64_t)n * (W / c->block_size + 1) > out->num_blocks) return KARA_ENOBLOCKS;
+    return cuda_status(launch_expand8(c, out, W, n, len, block_table, bt_stride, out_table, err,
+                                      (cudaStream_t)stream));
+}
+
+size_t kara_compact8_workspace_size(const kara_cache8 *c, const kara_params *p, int32_t n)
+{
+    if (check_params(p) != KARA_OK || check_cache8(c) != KARA_OK || n < 0) return 0;
+    return align256((size_t)(n > 0 ? n : 1) * sizeof(SeqPlan));
+}
+
+kara_status kara_compact8(const kara_cache8 *c, const kara_params *p, int32_t n, const int32_t *len,
+                          int32_t *block_table, int32_t bt_stride, const int32_t *kept, const int32_t *fresh,
+                          int64_t n_fresh, int32_t *freed, int32_t *new_len, void *ws, size_t ws_bytes, int32_t *err,
+                          kara_stream_t stream)
+{
+    const Range range("kara_compact8");
+    kara_status st = check_params(p);
+    if (st == KARA_OK) st = check_cache8(c);
+    if (st != KARA_OK) return st;
+    if (n < 0) return KARA_EINVAL;
+    if (n == 0) return KARA_OK;
+    if (!len || !block_table || bt_stride < 1) return KARA_EINVAL;
+    if (!kept || !new_len || !err || n_fresh < 0 || (n_fresh > 0 && !fresh) || !freed) return KARA_EINVAL;
+    if ((int64_t)c->num_layers * c->num_kv_heads > 0x7fffffffLL) return KARA_EUNSUPPORTED;
+    if (!ws || ws_bytes < kara_compact8_workspace_size(c, p, n)) return KARA_EWORKSPACE;
+    if (!aligned16(ws)) return KARA_EINVAL;
+    // what the plan, the checks and the commit read of a cache
+    Geo g;
+    memset(&g, 0, sizeof g);
+    g.layers = c->num_layers;
+    g.num_blocks = c->num_blocks;
+    g.hkv = c->num_kv_heads;
+    g.D = c->head_dim;
+    g.bs = c->block_size;
+    g.W = p->W;
+    g.B = p->B;
+    g.C = p->W - p->B;
+    g.R = p->R;
+    g.n = n;
+    g.bt_stride = bt_stride;
+    g.len = len;
+    g.bt = block_table;
+    g.nwin = (int64_t)n * c->num_layers * c->num_kv_heads;
+    cudaStream_t s = (cudaStream_t)stream;
+    SeqPlan *plan = static_cast<SeqPlan *>(ws);
+    cudaError_t e = launch_plan(g, n_fresh, plan, err, s);
+    if (e == cudaSuccess) e = launch_fresh_check(g, plan, fresh, n_fresh, err, s);
+    if (e == cudaSuccess) e = launch_kept_check(g, kept, err, s);
+    if (e == cudaSuccess) e = launch_copy8(c, g, plan, kept, fresh, n_fresh, err, s);
+    if (e == cudaSuccess) e = launch_commit(g, plan, fresh, freed, new_len, block_table, err, s);
+    return cuda_status(e);
 }
 
 kara_status kara_select(const kara_params *p, int64_t n_windows, const float *scores, int32_t *cand,

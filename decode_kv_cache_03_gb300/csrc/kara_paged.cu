@@ -271,15 +271,22 @@ cudaError_t launch_fresh_check(const Geo &g, const SeqPlan *plan, const int32_t 
     return cudaGetLastError();
 }
 
+cudaError_t launch_kept_check(const Geo &g, const int32_t *kept, int32_t *err, cudaStream_t st)
+{
+    const int64_t nk = g.nwin * g.R;
+    const int64_t kb = (nk + kChkThreads - 1) / kChkThreads;
+    kept_check_kernel<<<(unsigned)(kb < 4096 ? kb : 4096), kChkThreads, 0, st>>>(nk, g.R, g.C, kept, err);
+    return cudaGetLastError();
+}
+
 // The kept-row check, then the copy (which runs only if no error was recorded).
 cudaError_t launch_kept_copy(const Geo &g, const SeqPlan *plan, const int32_t *kept, const int32_t *fresh,
                              int64_t n_fresh, int32_t *err, cudaStream_t st)
 {
     const int64_t blocks = g.nwin * 2;
     if (blocks == 0) return cudaSuccess;
-    const int64_t nk = g.nwin * g.R;
-    const int64_t kb = (nk + kChkThreads - 1) / kChkThreads;
-    kept_check_kernel<<<(unsigned)(kb < 4096 ? kb : 4096), kChkThreads, 0, st>>>(nk, g.R, g.C, kept, err);
+    const cudaError_t e = launch_kept_check(g, kept, err, st);
+    if (e != cudaSuccess) return e;
     if (g.D == 128)
         compact_kernel<128><<<(unsigned)blocks, 256, 0, st>>>(g, plan, kept, fresh, n_fresh, err);
     else

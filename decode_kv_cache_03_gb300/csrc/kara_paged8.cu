@@ -1,0 +1,247 @@
+// The compression step's copies on the 8-bit cache: the windows' keys back in bf16 for the
+// scorer (expand), and the gather-compaction (compact).
+//
+// Follows the gist.science summary of Kara (arXiv 2607.01237), section "3. KvLLM Framework
+// and Periodic Compression", as the bf16 compaction does: the plan, the checks of fresh ids
+// and kept rows and the table commit are that one's.  What is new is that the 16 rows of a
+// rebuilt block come from up to 16 blocks with scales of their own: with x = code * |scale|
+// of the gathered rows,
+//     s = the smallest power of two with max |x| <= 448 s,   code' = rn(x / s).
+// Powers of two: x / s is exact unless it falls among e4m3's subnormals.
+// Both are bound by HBM (a read and a write of every code, or of its bf16 value).
+#include "kara_cache8.cuh"
+#include "kara_tokens.cuh"
+
+namespace kara {
+namespace {
+
+constexpr int kBs = 16;  // tokens per cache block (the supported block size)
+constexpr int kThreads = 256;
+constexpr int kSlices = 4;  // slices a thread has in flight
+
+struct Pool8 {
+    const uint8_t *codes[2];
+    const float *scale[2];
+    int64_t layer_stride, block_stride, head_stride;
+    int32_t num_blocks, hkv, heads;  // heads: layers * hkv
+
+    // slice lh = layer * hkv + head of a block, and its scale
+    __device__ __forceinline__ int64_t slice(int lh, int32_t blk) const
+    {
+        return lh / hkv * layer_stride + blk * block_stride + lh % hkv * head_stride;
+    }
+    __device__ __forceinline__ int64_t scale_at(int lh, int32_t blk) const
+    {
+        return ((int64_t)(lh / hkv) * num_blocks + blk) * hkv + lh % hkv;
+    }
+};
+
+__device__ __forceinline__ uint32_t bf16x2(float lo, float hi)
+{
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+struct ExpandArgs {
+    Pool8 in;
+    uint16_t *out[2];
+    int64_t layer_stride, block_stride, head_stride;  // of out, elements
+    int32_t n, W, nw, bt_stride, pools;
+    const int32_t *len, *bt;
+    int32_t *out_table, *err;
+};
+
+// Block (x, y): block j of sequence s's window (x = s * nw + j), slices y * kSlices * SPB and on of all
+// layers and heads (and of V after those of K).  A thread takes 16 codes of a slice.
+template <int D>
+__global__ void __launch_bounds__(kThreads) expand8_kernel(const ExpandArgs a)
+{
+    constexpr int SPB = kThreads / D;  // slices side by side (a slice: D threads)
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int s = blockIdx.x / a.nw, j = blockIdx.x % a.nw;
+    const int32_t L = a.len[s];
+    if (L < a.W || ((int64_t)L + kBs - 1) / kBs > a.bt_stride) {
+        if (j == 0 && blockIdx.y == 0 && threadIdx.x == 0) set_err(a.err, KARA_EINVAL);
+        return;
+    }
+    const int32_t col = (L - a.W) / kBs + j;
+    if (col >= (L + kBs - 1) / kBs) return;
+    const int64_t entry = (int64_t)s * a.bt_stride + col;
+    const int32_t id = a.bt[entry], to = blockIdx.x;
+    const bool inside = id >= 0 && id < a.in.num_blocks;
+    if (blockIdx.y == 0 && threadIdx.x == 0) {
+        if (!inside) set_err(a.err, KARA_EBADBLOCK);
+        a.out_table[entry] = to;
+    }
+    const int part = threadIdx.x % D, row = part * 16 / D;
+    const bool live = inside && (int64_t)col * kBs + row < L;
+    const int first = blockIdx.y * kSlices * SPB + threadIdx.x / D, total = a.pools * a.in.heads;
+    uint4 w[kSlices];
+    float f[kSlices];
+#pragma unroll
+    for (int i = 0; i < kSlices; ++i) {
+        const int lh = first + i * SPB, p = lh >= a.in.heads, h = p ? lh - a.in.heads : lh;
+        w[i] = make_uint4(0, 0, 0, 0);
+        f[i] = 0.f;
+        if (live && lh < total) {
+            w[i] = *reinterpret_cast<const uint4 *>(a.in.codes[p] + a.in.slice(h, id) + part * 16);
+            f[i] = fabsf(a.in.scale[p][a.in.scale_at(h, id)]);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < kSlices; ++i) {
+        const int lh = first + i * SPB, p = lh >= a.in.heads, h = p ? lh - a.in.heads : lh;
+        if (lh >= total) break;
+        const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+        uint32_t r[8];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            float x[4];
+            values4(u[e], x);
+            r[2 * e] = bf16x2(x[0] * f[i], x[1] * f[i]);
+            r[2 * e + 1] = bf16x2(x[2] * f[i], x[3] * f[i]);
+        }
+        uint4 *o = reinterpret_cast<uint4 *>(a.out[p] + h / a.in.hkv * a.layer_stride + to * a.block_stride +
+                                             h % a.in.hkv * a.head_stride + part * 16);
+        o[0] = make_uint4(r[0], r[1], r[2], r[3]);
+        o[1] = make_uint4(r[4], r[5], r[6], r[7]);
+    }
+}
+
+struct CompactArgs {
+    Pool8 in;
+    uint8_t *codes[2];
+    float *scale[2];
+    const SeqPlan *plan;
+    const int32_t *kept, *fresh, *bt;
+    int64_t n_fresh, units;
+    int32_t B, C, R, bt_stride, max_new;
+    int32_t *err;
+};
+
+// A warp rebuilds one block of one head and pool: unit ((s * layers + l) * hkv + g) * 2 + pool, new block j.
+template <int D>
+__global__ void __launch_bounds__(kThreads) compact8_kernel(const CompactArgs a)
+{
+    constexpr int LPR = D / 16, RPP = 32 / LPR, NP = kBs / RPP;  // lanes per row, rows per pass, passes
+    // nothing is written once an earlier kernel (plan, checks) recorded an error
+    if (*(volatile const int32_t *)a.err != 0) return;
+    const int64_t task = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
+    const int64_t unit = task / a.max_new;
+    const int j = (int)(task % a.max_new), lane = threadIdx.x & 31;
+    if (unit >= a.units) return;
+    const int pool = (int)(unit & 1), lh = (int)((unit >> 1) % a.in.heads), s = (int)((unit >> 1) / a.in.heads);
+    const SeqPlan p = a.plan[s];
+    if (p.p0 < 0 || j >= p.n_new || (int64_t)p.off_new + p.n_new > a.n_fresh) return;
+    const int32_t to = a.fresh[p.off_new + j];
+    if (to < 0 || to >= a.in.num_blocks) return;  // recorded by the check
+    const int32_t *kept = a.kept + (unit >> 1) * a.R, *bt = a.bt + (int64_t)s * a.bt_stride;
+    const int c = lane % LPR, x0 = (p.p0 + j) * kBs;
+    uint4 w[NP];
+    float f[NP];
+    bool live[NP];
+#pragma unroll
+    for (int i = 0; i < NP; ++i) {
+        const int x = x0 + i * RPP + lane / LPR;
+        w[i] = make_uint4(0, 0, 0, 0);
+        f[i] = 0.f;
+        live[i] = x < p.Lnew;
+        if (!live[i]) continue;
+        int old = x;
+        if (x >= p.ws) old = x < p.ws + a.R ? p.ws + min(max(kept[x - p.ws], 0), a.C - 1) : p.L - a.B + (x - p.ws - a.R);
+        const int32_t id = bt[old / kBs];
+        if (id < 0 || id >= a.in.num_blocks) {
+            set_err(a.err, KARA_EBADBLOCK);
+            continue;
+        }
+        w[i] = *reinterpret_cast<const uint4 *>(a.in.codes[pool] + a.in.slice(lh, id) + old % kBs * D + c * 16);
+        f[i] = fabsf(a.in.scale[pool][a.in.scale_at(lh, id)]);
+    }
+    float top = 0.f;
+    bool odd = false;
+#pragma unroll
+    for (int i = 0; i < NP; ++i) {
+        const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+        float t = 0.f;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            float x[4];
+            values4(u[e], x);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                t = fmaxf(t, fabsf(x[k]));  // (passes over a NaN)
+                odd = odd || x[k] != x[k];
+            }
+        }
+        top = fmaxf(top, t * f[i]);
+    }
+    top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));
+    odd = __any_sync(0xffffffffu, odd);
+    const float sc = scale_for(top), inv = inverse_scale(sc);
+    uint8_t *out = a.codes[pool] + a.in.slice(lh, to) + c * 16;
+#pragma unroll
+    for (int i = 0; i < NP; ++i) {
+        if (!live[i]) continue;
+        const float ratio = f[i] * inv;
+        if (ratio != 1.f) {
+            w[i].x = rescale4(w[i].x, ratio), w[i].y = rescale4(w[i].y, ratio);
+            w[i].z = rescale4(w[i].z, ratio), w[i].w = rescale4(w[i].w, ratio);
+        }
+        *reinterpret_cast<uint4 *>(out + (i * RPP + lane / LPR) * D) = w[i];
+    }
+    if (lane == 0) a.scale[pool][a.in.scale_at(lh, to)] = odd ? -sc : sc;
+}
+
+Pool8 pool8(const kara_cache8 *c)
+{
+    Pool8 p;
+    p.codes[0] = static_cast<const uint8_t *>(c->k), p.codes[1] = static_cast<const uint8_t *>(c->v);
+    p.scale[0] = c->k_scale, p.scale[1] = c->v_scale;
+    p.layer_stride = c->layer_stride, p.block_stride = c->block_stride, p.head_stride = c->head_stride;
+    p.num_blocks = c->num_blocks, p.hkv = c->num_kv_heads;
+    p.heads = c->num_layers * c->num_kv_heads;
+    return p;
+}
+
+}  // namespace
+
+cudaError_t launch_expand8(const kara_cache8 *c, const kara_cache *out, int32_t W, int32_t n, const int32_t *len,
+                           const int32_t *bt, int32_t bt_stride, int32_t *out_table, int32_t *err, cudaStream_t st)
+{
+    ExpandArgs a;
+    a.in = pool8(c);
+    a.out[0] = static_cast<uint16_t *>(out->k), a.out[1] = static_cast<uint16_t *>(out->v);
+    a.layer_stride = out->layer_stride, a.block_stride = out->block_stride, a.head_stride = out->head_stride;
+    a.n = n, a.W = W, a.nw = W / kBs + 1, a.bt_stride = bt_stride;
+    a.pools = out->v == out->k ? 1 : 2;
+    a.len = len, a.bt = bt, a.out_table = out_table, a.err = err;
+    const int per = kSlices * (kThreads / c->head_dim);
+    const int64_t x = (int64_t)n * a.nw, y = ((int64_t)a.pools * a.in.heads + per - 1) / per;
+    if (x > 0x7fffffffLL || y > 65535) return cudaErrorInvalidConfiguration;
+    const auto kern = c->head_dim == 128 ? expand8_kernel<128> : expand8_kernel<64>;
+    return launch_dependent(kern, dim3((unsigned)x, (unsigned)y), kThreads, 0, st, (const ExpandArgs)a);
+}
+
+cudaError_t launch_copy8(const kara_cache8 *c, const Geo &g, const SeqPlan *plan, const int32_t *kept,
+                         const int32_t *fresh, int64_t n_fresh, int32_t *err, cudaStream_t st)
+{
+    CompactArgs a;
+    a.in = pool8(c);
+    a.codes[0] = static_cast<uint8_t *>(c->k), a.codes[1] = static_cast<uint8_t *>(c->v);
+    a.scale[0] = c->k_scale, a.scale[1] = c->v_scale;
+    a.plan = plan, a.kept = kept, a.fresh = fresh, a.bt = g.bt;
+    a.n_fresh = n_fresh, a.units = g.nwin * 2;
+    a.B = g.B, a.C = g.C, a.R = g.R, a.bt_stride = g.bt_stride;
+    a.max_new = (kBs - 1 + g.R + g.B + kBs - 1) / kBs;  // the window may start at any row of a block
+    a.err = err;
+    const int64_t blocks = (a.units * a.max_new + kThreads / 32 - 1) / (kThreads / 32);
+    if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+    if (g.D == 128)
+        compact8_kernel<128><<<(unsigned)blocks, kThreads, 0, st>>>(a);
+    else
+        compact8_kernel<64><<<(unsigned)blocks, kThreads, 0, st>>>(a);
+    return cudaGetLastError();
+}
+
+}  // namespace kara

@@ -45,6 +45,15 @@ class Cache(ctypes.Structure):
                 ("head_dim", ctypes.c_int32), ("block_size", ctypes.c_int32)]
 
 
+class Cache8(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("layer_stride", ctypes.c_int64),
+                ("block_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64),
+                ("num_layers", ctypes.c_int32), ("num_blocks", ctypes.c_int32),
+                ("num_kv_heads", ctypes.c_int32), ("num_q_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("block_size", ctypes.c_int32)]
+
+
 class Batch(ctypes.Structure):
     _fields_ = [("n", ctypes.c_int32), ("len", ctypes.c_void_p), ("block_table", ctypes.c_void_p),
                 ("bt_stride", ctypes.c_int32), ("q", ctypes.c_void_p)]
@@ -68,7 +77,7 @@ def _load():
     lib = ctypes.CDLL(LIB_PATH)
     P = ctypes.c_void_p
     PP, PC, PB = ctypes.POINTER(Params), ctypes.POINTER(Cache), ctypes.POINTER(Batch)
-    PT, PR = ctypes.POINTER(Tokens), ctypes.POINTER(Rope)
+    PT, PR, PC8 = ctypes.POINTER(Tokens), ctypes.POINTER(Rope), ctypes.POINTER(Cache8)
     I32, I64, SZ = ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
     sig = {
         "kara_status_string": ([ctypes.c_int], ctypes.c_char_p),
@@ -88,6 +97,12 @@ def _load():
         "kara_decode_attention": ([PC, I32, I32, P, P, I32, P, P, P, SZ, P, P], ctypes.c_int),
         "kara_extend_tables": ([I32, I32, P, P, P, I32, P, I64, PT, P, P, P], ctypes.c_int),
         "kara_append_kv": ([PC, I32, PT, PR, P, I64, P, I64, P, I64, P, P, I32, P, P], ctypes.c_int),
+        "kara_append_kv8": ([PC8, I32, PT, PR, P, I64, P, I64, P, I64, P, P, I32, P, P], ctypes.c_int),
+        "kara_decode8_workspace_size": ([PC8, I32, I32], SZ),
+        "kara_decode_attention8": ([PC8, I32, I32, P, P, I32, P, P, P, SZ, P, P], ctypes.c_int),
+        "kara_expand8": ([PC8, PC, I32, I32, P, P, I32, P, P, P], ctypes.c_int),
+        "kara_compact8_workspace_size": ([PC8, PP, I32], SZ),
+        "kara_compact8": ([PC8, PP, I32, P, P, I32, P, P, I64, P, P, P, SZ, P, P], ctypes.c_int),
         "kara_chunk_workspace_size": ([PC, I32, I32], SZ),
         "kara_chunk_attention": ([PC, I32, PT, P, I32, P, P, P, SZ, P, P], ctypes.c_int),
     }
@@ -103,7 +118,8 @@ EXPORTED = ("kara_status_string", "kara_version", "kara_plan", "kara_workspace_s
             "kara_select", "kara_compact", "kara_compress_batch", "kara_get_error", "kara_compact_static",
             "kara_decode_workspace_size", "kara_decode_attention", "kara_compact_queries", "kara_append_queries",
             "kara_batch_groups", "kara_extend_tables", "kara_append_kv", "kara_chunk_workspace_size",
-            "kara_chunk_attention")
+            "kara_chunk_attention", "kara_append_kv8", "kara_decode8_workspace_size", "kara_decode_attention8",
+            "kara_expand8", "kara_compact8_workspace_size", "kara_compact8")
 STATIC_MAX_SEQS = 8192     # KARA_STATIC_MAX_SEQS
 
 
@@ -142,6 +158,22 @@ def cache(k: torch.Tensor, v: torch.Tensor, num_q_heads: int) -> Cache:
     assert k.stride(4) == 1 and k.stride(3) == d
     c = Cache(k.data_ptr(), v.data_ptr(), k.stride(0), k.stride(1), k.stride(2), Lyr, nb, hkv,
               int(num_q_heads), d, bs)
+    c.device = k.device
+    return c
+
+
+def cache8(k: torch.Tensor, v: torch.Tensor, k_scale: torch.Tensor, v_scale: torch.Tensor, num_q_heads: int) -> Cache8:
+    """Describe pools of e4m3 codes (torch.float8_e4m3fn, or their bits as torch.uint8) laid out
+    [layers][num_blocks][hkv][block][d] (rows contiguous), with scales float [layers][num_blocks][hkv]."""
+    assert k.dtype == v.dtype and k.dtype in (torch.float8_e4m3fn, torch.uint8)
+    assert v.shape == k.shape and v.stride() == k.stride()
+    Lyr, nb, hkv, bs, d = k.shape
+    assert k.stride(4) == 1 and k.stride(3) == d
+    for s in (k_scale, v_scale):
+        assert s.dtype == torch.float32 and s.shape == (Lyr, nb, hkv) and s.is_contiguous()
+    assert v.device == k_scale.device == v_scale.device == k.device
+    c = Cache8(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), k.stride(0), k.stride(1),
+               k.stride(2), Lyr, nb, hkv, int(num_q_heads), d, bs)
     c.device = k.device
     return c
 
@@ -275,11 +307,9 @@ def kara_extend_tables(num_blocks: int, block_size: int, lengths: torch.Tensor, 
                                    t, n_used.data_ptr(), err.data_ptr(), _raw_stream(err, stream)), "kara_extend_tables")
 
 
-def kara_append_kv(c: Cache, layer: int, t: Tokens, r: Rope, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
-                   q_out: torch.Tensor, err: torch.Tensor, ring=None, stream=None):
-    """Norm and rotate q [rows][num_q_heads][D] and k [rows][num_kv_heads][D] and write k, v into layer
-    `layer` of the cache at t's slots, queries to q_out (and to ring [n][layers][num_q_heads][W][D])."""
-    _same_device(err, "kara_append_kv", q, k, v, q_out, ring, c, t, *r.on)
+def _append(entry, where: str, c, layer: int, t: Tokens, r: Rope, q, k, v, q_out, err, ring, stream):
+    """The checks and the call of an append into a cache of either type."""
+    _same_device(err, where, q, k, v, q_out, ring, c, t, *r.on)
     hq, hkv, d, rows, W = c.num_q_heads, c.num_kv_heads, c.head_dim, t.rows, 0
     assert q.dtype == k.dtype == v.dtype == q_out.dtype == torch.bfloat16
     assert q.shape == q_out.shape == (rows, hq, d) and k.shape == v.shape == (rows, hkv, d)
@@ -294,9 +324,22 @@ def kara_append_kv(c: Cache, layer: int, t: Tokens, r: Rope, q: torch.Tensor, k:
         W = ring.shape[3]
         assert ring.dtype == torch.bfloat16 and ring.is_contiguous()
         assert ring.shape == (t.n, c.num_layers, hq, W, d)
-    _check(_lib.kara_append_kv(c, layer, t, r, q.data_ptr(), strides[0], k.data_ptr(), strides[1], v.data_ptr(),
-                               strides[2], q_out.data_ptr(), None if ring is None else ring.data_ptr(), W,
-                               err.data_ptr(), _raw_stream(err, stream)), "kara_append_kv")
+    _check(entry(c, layer, t, r, q.data_ptr(), strides[0], k.data_ptr(), strides[1], v.data_ptr(), strides[2],
+                 q_out.data_ptr(), None if ring is None else ring.data_ptr(), W, err.data_ptr(),
+                 _raw_stream(err, stream)), where)
+
+
+def kara_append_kv(c: Cache, layer: int, t: Tokens, r: Rope, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
+                   q_out: torch.Tensor, err: torch.Tensor, ring=None, stream=None):
+    """Norm and rotate q [rows][num_q_heads][D] and k [rows][num_kv_heads][D] and write k, v into layer
+    `layer` of the cache at t's slots, queries to q_out (and to ring [n][layers][num_q_heads][W][D])."""
+    _append(_lib.kara_append_kv, "kara_append_kv", c, layer, t, r, q, k, v, q_out, err, ring, stream)
+
+
+def kara_append_kv8(c: Cache8, layer: int, t: Tokens, r: Rope, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
+                    q_out: torch.Tensor, err: torch.Tensor, ring=None, stream=None):
+    """kara_append_kv into an 8-bit cache: k and v rounded to e4m3, a scale for each block and head."""
+    _append(_lib.kara_append_kv8, "kara_append_kv8", c, layer, t, r, q, k, v, q_out, err, ring, stream)
 
 
 def kara_chunk_workspace_size(c: Cache, n: int, rows: int) -> int:
@@ -314,6 +357,57 @@ def kara_chunk_attention(c: Cache, layer: int, t: Tokens, block_table: torch.Ten
     _check(_lib.kara_chunk_attention(c, layer, t, block_table.data_ptr(), block_table.shape[1], q.data_ptr(),
                                      out.data_ptr(), ws.data_ptr(), ws.numel() * ws.element_size(), err.data_ptr(),
                                      _raw_stream(err, stream)), "kara_chunk_attention")
+
+
+def kara_decode8_workspace_size(c: Cache8, n: int, bt_stride: int) -> int:
+    return int(_lib.kara_decode8_workspace_size(ctypes.byref(c), int(n), int(bt_stride)))
+
+
+def kara_decode_attention8(c: Cache8, layer: int, lengths: torch.Tensor, block_table: torch.Tensor,
+                           q: torch.Tensor, out: torch.Tensor, ws: torch.Tensor, err: torch.Tensor, stream=None):
+    """Decode attention of q [n][num_q_heads][head_dim] (bf16) over layer `layer` of an 8-bit cache, read
+    through block_table [n][bt_stride]; out is bf16, zeros for a sequence of length 0."""
+    _same_device(err, "kara_decode_attention8", lengths, block_table, q, out, ws, c)
+    n, bt_stride = block_table.shape
+    assert lengths.dtype == block_table.dtype == torch.int32 and lengths.shape == (n,)
+    assert lengths.is_contiguous() and block_table.is_contiguous()
+    assert q.dtype == out.dtype == torch.bfloat16 and q.is_contiguous() and out.is_contiguous()
+    assert q.shape == out.shape == (n, c.num_q_heads, c.head_dim)
+    _check(_lib.kara_decode_attention8(c, layer, n, lengths.data_ptr(), block_table.data_ptr(), bt_stride,
+                                       q.data_ptr(), out.data_ptr(), ws.data_ptr(), ws.numel() * ws.element_size(),
+                                       err.data_ptr(), _raw_stream(err, stream)), "kara_decode_attention8")
+
+
+def kara_expand8(c: Cache8, out: Cache, W: int, lengths: torch.Tensor, block_table: torch.Tensor,
+                 out_table: torch.Tensor, err: torch.Tensor, stream=None):
+    """The windows (last W tokens) of an 8-bit cache as bf16 blocks of `out`, n * (W/16 + 1) of them, their
+    ids in out_table: what kara_score takes.  With out.v == out.k only the keys are written."""
+    _same_device(err, "kara_expand8", lengths, block_table, out_table, c, out)
+    n, bt_stride = block_table.shape
+    assert lengths.dtype == block_table.dtype == out_table.dtype == torch.int32 and lengths.shape == (n,)
+    assert lengths.is_contiguous() and block_table.is_contiguous()
+    assert out_table.shape == block_table.shape and out_table.is_contiguous()
+    _check(_lib.kara_expand8(c, out, W, n, lengths.data_ptr(), block_table.data_ptr(), bt_stride,
+                             out_table.data_ptr(), err.data_ptr(), _raw_stream(err, stream)), "kara_expand8")
+
+
+def kara_compact8_workspace_size(c: Cache8, p: Params, n: int) -> int:
+    return int(_lib.kara_compact8_workspace_size(ctypes.byref(c), ctypes.byref(p), int(n)))
+
+
+def kara_compact8(c: Cache8, p: Params, lengths: torch.Tensor, block_table: torch.Tensor, kept: torch.Tensor,
+                  fresh: torch.Tensor, freed: torch.Tensor, new_len: torch.Tensor, ws: torch.Tensor,
+                  err: torch.Tensor, stream=None):
+    """kara_compact on an 8-bit cache: kept [n][layers][hkv][R] rows into fresh blocks with new scales."""
+    _same_device(err, "kara_compact8", lengths, block_table, kept, fresh, freed, new_len, ws, c)
+    n, bt_stride = block_table.shape
+    for t in (lengths, block_table, kept, fresh, freed, new_len):
+        assert t.dtype == torch.int32 and t.is_contiguous()
+    assert lengths.shape == new_len.shape == (n,) and kept.shape == (n, c.num_layers, c.num_kv_heads, p.R)
+    _check(_lib.kara_compact8(c, p, n, lengths.data_ptr(), block_table.data_ptr(), bt_stride, kept.data_ptr(),
+                              fresh.data_ptr(), fresh.numel(), freed.data_ptr(), new_len.data_ptr(), ws.data_ptr(),
+                              ws.numel() * ws.element_size(), err.data_ptr(), _raw_stream(err, stream)),
+           "kara_compact8")
 
 
 def kara_select(p: Params, n_windows: int, scores: torch.Tensor, cand, kept: torch.Tensor, stream=None):

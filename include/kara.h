@@ -348,6 +348,98 @@ kara_status kara_chunk_attention(const kara_cache *c, int32_t layer, const kara_
                                  kara_stream_t stream);
 
 /*
+ * ---- The cache in 8 bits ------------------------------------------------------
+ * The same paged cache at half the bytes, for the memory constraints that the
+ * pages are about (summary, "Problem Statement", item 1; they name no such form).
+ * K and V are e4m3 codes (sign, 4 exponent and 3 mantissa bits, bias 7, largest
+ * value 448, no infinity, 0x7f and 0xff NaN), each block and KV head of each pool
+ * with a scale: a value is its code times |scale|.
+ * A scale is a power of two from 2^-63 to 2^63, or 0 if all of the block's codes
+ * are 0; its sign bit is set if a code of the block may be NaN.  (Other scales, or
+ * NaN codes under a scale without that sign, are never a fault, but give
+ * unspecified values.)  A scale of a block that no call has written is not read.
+ * Code element (l, blk, g, slot, d) of a pool lives at byte
+ *   base + l*layer_stride + blk*block_stride + g*head_stride + slot*head_dim + d;
+ * the scale arrays are [num_layers][num_blocks][num_kv_heads], contiguous.
+ * Pools are 16-byte aligned, strides multiples of 16.  The supported shapes are
+ * those of kara_cache.  kara_extend_tables serves this cache as it is.
+ */
+typedef struct {
+    void *k;
+    void *v;
+    float *k_scale;
+    float *v_scale;
+    int64_t layer_stride, block_stride, head_stride;
+    int32_t num_layers, num_blocks, num_kv_heads, num_q_heads, head_dim, block_size;
+} kara_cache8;
+
+/*
+ * New tokens into layer `layer` of an 8-bit cache: kara_append_kv, with the same
+ * arguments, checks, norms, rotation, query output and ring (queries get the same
+ * bits).  The new rows of a block and head, with z their fp32 keys after norm and
+ * rotation (their values as they are) and s0 the block's scale if rows precede
+ * them in the block, else 0, are stored as
+ *     s = max(s0, smallest power of two with max|z| <= 448 s),  code = rn(z / s),
+ * one rounding from fp32; if s > s0 the codes of the rows ahead become
+ * rn(code * s0 / s).  s stays within 2^-63 .. 2^63: larger values become 448 s.
+ * Values that are not finite are stored as NaN and do not count for the scale.
+ * Rows of the block behind the last new one are left as they were.
+ * The new rows of one block are consecutive rows of a call with consecutive slots,
+ * as kara_extend_tables makes them; rows of one block that are not race for its
+ * scale (after a row that was skipped with an error, too).
+ */
+kara_status kara_append_kv8(const kara_cache8 *c, int32_t layer, const kara_tokens *t, const kara_rope *r,
+                            const void *q, int64_t q_stride, const void *k, int64_t k_stride, const void *v,
+                            int64_t v_stride, void *q_out, void *ring, int32_t W, int32_t *err, kara_stream_t stream);
+
+/*
+ * Decode attention over an 8-bit cache: kara_decode_attention with k_x and v_x the
+ * stored values, and these differences.  out is bf16 [n][num_q_heads][head_dim]
+ * (16-byte aligned, not overlapping q), rounded once from fp32.  A sequence of
+ * length 0 gives zeros and no error.  Queries enter the logits scaled by a power of
+ * two for each head, in f16 (exact within 2^-29 of the head's largest element,
+ * 2^-40 of it off below); weights times V's scales likewise, rounded to f16: 2^-12
+ * of a weight, for those below 2^-29 of the largest 2^-40 of that.  ws is 16-byte
+ * aligned, and used by this call alone until it has run.
+ */
+size_t kara_decode8_workspace_size(const kara_cache8 *c, int32_t n, int32_t bt_stride);
+kara_status kara_decode_attention8(const kara_cache8 *c, int32_t layer, int32_t n, const int32_t *len,
+                                   const int32_t *block_table, int32_t bt_stride, const void *q, void *out, void *ws,
+                                   size_t ws_bytes, int32_t *err, kara_stream_t stream);
+
+/*
+ * The windows of an 8-bit cache in bf16, for kara_score (a compression scores bf16
+ * keys).  Block j of sequence s's window, the logical block (len[s] - W)/bs + j for
+ * j <= W/bs, is written as block s * (W/bs + 1) + j of `out` in all layers and heads
+ * (its rows past len[s] as zeros), and out_table [n][bt_stride] gets that id in the
+ * place of the block's own (other entries are left as they are).  Values are exact.
+ * With out->v == out->k keys alone are written, which is all that kara_score reads;
+ * else values go to out->v.  out has c's layers, KV heads, head_dim and block_size,
+ * and at least n * (W/bs + 1) blocks; W is a positive multiple of bs.
+ * Recorded: KARA_EINVAL for a length below W or above bt_stride * bs (nothing of that
+ * sequence is written); KARA_EBADBLOCK for a block id outside the pool (zeros).
+ * One launch, a programmatic dependent of what precedes it on `stream`.
+ */
+kara_status kara_expand8(const kara_cache8 *c, const kara_cache *out, int32_t W, int32_t n, const int32_t *len,
+                         const int32_t *block_table, int32_t bt_stride, int32_t *out_table, int32_t *err,
+                         kara_stream_t stream);
+
+/*
+ * kara_compact on an 8-bit cache: the same gather, checks, outputs, table rewrite and
+ * commit rule (of p, B, R and W count).  The codes of a rebuilt block's rows, x their
+ * stored values, become
+ *     s = smallest power of two with max|x| <= 448 s (2^-63 .. 2^63),  code = rn(x / s),
+ * and s the scale of the block and head.  Rows of a rebuilt block past the new length
+ * keep their codes.
+ * len [n], block_table [n][bt_stride] as in kara_batch; ws of kara_compact8_workspace_size.
+ */
+size_t kara_compact8_workspace_size(const kara_cache8 *c, const kara_params *p, int32_t n);
+kara_status kara_compact8(const kara_cache8 *c, const kara_params *p, int32_t n, const int32_t *len,
+                          int32_t *block_table, int32_t bt_stride, const int32_t *kept, const int32_t *fresh,
+                          int64_t n_fresh, int32_t *freed, int32_t *new_len, void *ws, size_t ws_bytes, int32_t *err,
+                          kara_stream_t stream);
+
+/*
  * Top-K and Token2Chunk (summary section 1 "Selection"; section 2 "Process").
  * (select_mode KARA_SELECT_TOP_R and KARA_SELECT_FIXED_CHUNK replace the
  * chunk step, keeping cand as below: kept is the R first positions in the
