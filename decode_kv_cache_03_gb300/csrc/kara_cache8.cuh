@@ -74,8 +74,8 @@ __device__ __forceinline__ bool finite(float x) { return (__float_as_uint(x) & 0
 PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();  // defined beside the scoring kernel
 
 // Tensor map over one pool of codes, (d, slot, kv head, block, layer) with the cache's strides; a box is
-// a (block, head) slice, swizzled by its row size.
-inline cudaError_t pool_map8(CUtensorMap *m, const void *pool, const kara_cache8 *c)
+// a (block, head) slice, `swizzled` by its row size or as it lies in memory.
+inline cudaError_t pool_map8(CUtensorMap *m, const void *pool, const kara_cache8 *c, bool swizzled)
 {
     auto fn = tensor_map_encoder();
     if (!fn) return cudaErrorNotSupported;
@@ -85,7 +85,8 @@ inline cudaError_t pool_map8(CUtensorMap *m, const void *pool, const kara_cache8
                              (cuuint64_t)c->layer_stride};
     cuuint32_t box[5] = {(cuuint32_t)c->head_dim, (cuuint32_t)c->block_size, 1, 1, 1};
     cuuint32_t estr[5] = {1, 1, 1, 1, 1};
-    const CUtensorMapSwizzle swizzle = c->head_dim == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B;
+    const CUtensorMapSwizzle swizzle = !swizzled ? CU_TENSOR_MAP_SWIZZLE_NONE
+                                       : c->head_dim == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B;
     return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 5, const_cast<void *>(pool), dims, strides, box, estr,
               CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
@@ -98,6 +99,8 @@ int decode8_max_splits(int32_t bt_stride);
 size_t decode8_workspace_bytes(const kara_cache8 *c, int32_t n, int32_t bt_stride);
 cudaError_t launch_decode8(const kara_cache8 *c, int32_t layer, int32_t n, const int32_t *len, const int32_t *bt,
                            int32_t bt_stride, const void *q, void *out, void *ws, int32_t *err, cudaStream_t st);
+cudaError_t launch_chunk8(const kara_cache8 *c, int32_t layer, const kara_tokens *t, const int32_t *bt,
+                          int32_t bt_stride, const void *q, void *out, void *ws, int32_t *err, cudaStream_t st);
 cudaError_t launch_expand8(const kara_cache8 *c, const kara_cache *out, int32_t W, int32_t n, const int32_t *len,
                            const int32_t *bt, int32_t bt_stride, int32_t *out_table, int32_t *err, cudaStream_t st);
 cudaError_t launch_copy8(const kara_cache8 *c, const Geo &g, const SeqPlan *plan, const int32_t *kept,

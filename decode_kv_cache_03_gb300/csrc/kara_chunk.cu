@@ -67,15 +67,11 @@
 //
 // Two launches: the attention (persistent, one CTA per SM, each of which works out
 // its own range) and the merge, programmatic dependents of what precedes them.
-#include <cuda.h>
-#include <cudaTypedefs.h>
-
+#include "kara_cache8.cuh"
 #include "kara_sm100.cuh"
 #include "kara_tokens.cuh"
 
 namespace kara {
-
-PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();  // defined beside the scoring kernel
 
 namespace {
 
@@ -84,7 +80,9 @@ using namespace ptx;
 constexpr int kTile = 128;       // rows of a query tile, keys of a key tile
 constexpr int kBlk = 16;         // tokens per cache block (the supported block size)
 constexpr int kBlkPerTile = kTile / kBlk;
-constexpr int kStages = 5;       // K and V tiles in flight
+constexpr int kStages = 5;       // K and V tiles in flight (of a bf16 cache)
+constexpr int kStages8 = 3;      // the same of an 8-bit cache, whose
+constexpr int kRaw8 = 2;         // tiles of codes in flight, of K and of V each, lie beside them
 // V tiles issued and not cleaned yet, at most.  V tile i takes the stage of K tile i - (kStages - 1) / 2, and
 // when both MMA warps have given that one back, every V tile two or more before it is clean: with two query
 // tiles its logits are issued behind the weighted sum of the V tile before; with one, a warp passes the V
@@ -98,7 +96,7 @@ constexpr int kWarpKv = 8, kWarpMma = 10, kWarpQ = 12;  // 8: K, 9: V; 10, 11: t
 // Registers per thread: at launch (65536 / 512), then after the warpgroups trade:
 // 256 * kRegsSoft + 256 * kRegsCtl == 512 * kRegsLaunch.
 constexpr int kRegsLaunch = 128;
-constexpr uint32_t kRegsSoft = 192, kRegsCtl = 64;
+constexpr uint32_t kRegsSoft = 184, kRegsCtl = 72;
 static_assert(256 * kRegsSoft + 256 * kRegsCtl == kThreads * kRegsLaunch, "register trade must add up");
 constexpr uint32_t kTmemCols = 512;  // S0 S1 (128 columns each), O0 O1 (128 each)
 constexpr float kLazy = 8.f;         // see above: rescale when the maximum grew by more than 2^8
@@ -140,6 +138,8 @@ struct ChunkArgs {
     float4 *part;        // [2 * ctas][D / 4][256]
     float2 *stat;        // [2 * ctas][256]: (max, sum) in the log2 domain
     const uint16_t *v;   // V pool at the call's layer
+    const uint8_t *v8;   // or, of the 8-bit cache, its codes,
+    const float *k_scale, *v_scale;  // and K's and V's scales [num_blocks][hkv]
     int64_t block_stride, head_stride;
     int32_t wide;        // out is 32-byte aligned
     int32_t stall;
@@ -212,16 +212,29 @@ struct Shared {
     int64_t cut[2];       // its range of the costs of what is not taken whole
     int4 piece[kPieces][3];  // pieces of it, by their number mod kPieces
     uint64_t piece_full[kPieces], piece_empty[kPieces];
-    longlong2 scan[kThreads / 32 + 1];
-    float2 stat[kTile];   // (max, sum) of the odd key tiles, for joining a single query tile
+    union {
+        longlong2 scan[kThreads / 32 + 1];  // while the work is shared out
+        float2 stat[kTile];   // (max, sum) of the odd key tiles, for joining a single query tile
+    };
 };
 
-template <int D>
+// The same of the 8-bit cache, beside it: tiles of codes (K's, then V's, each by their number mod
+// kRaw8) and their blocks' scales.
+struct Shared8 {
+    uint64_t full[2 * kRaw8], empty[2 * kRaw8];
+    float scale[2 * kRaw8][kBlkPerTile];
+};
+
+template <int D, bool E8>
 struct Cfg {
     static constexpr int kHalves = D / 64;
     static constexpr int kHalfBytes = kTile * 128;            // 128 rows of 64 dims
     static constexpr int kTileBytes = kHalves * kHalfBytes;
-    static constexpr size_t kSmem = 1024 + (size_t)(2 + kStages) * kTileBytes + sizeof(Shared);
+    static constexpr int kRing = E8 ? kStages8 : kStages;     // tiles of the ring
+    static constexpr int kRawBytes = kTile * D;               // a tile of codes
+    static constexpr size_t kRawAll = E8 ? (size_t)2 * kRaw8 * kRawBytes : 0;
+    static constexpr size_t kSmem = 1024 + (size_t)(2 + kRing) * kTileBytes + kRawAll + sizeof(Shared) +
+                                    (E8 ? sizeof(Shared8) : 0);
 };
 
 // Bounded wait on phase `parity` of `bar`: gives up after wait_ns, or once another
@@ -715,17 +728,17 @@ __device__ __forceinline__ uint32_t finite_pair(uint32_t w)
 
 // Values of new tokens that are not finite were cleared from V: adds those at positions
 // [y0, y1] to a row of the output, or of a partial.
-template <int D>
+template <int D, bool E8>
 __device__ __noinline__ void add_cleared(const ChunkArgs &a, int seq, int head, int y0, int y1, uint16_t *out,
                                          float4 *part)
 {
     for (int y = y0; y <= y1; ++y) {
         const int32_t id = a.bt[(int64_t)seq * a.bt_stride + y / kBlk];
         if (id < 0 || id >= a.num_blocks) continue;
-        const uint16_t *v = a.v + id * a.block_stride + head * a.head_stride + (int64_t)(y % kBlk) * D;
+        const int64_t at = id * a.block_stride + head * a.head_stride + (int64_t)(y % kBlk) * D;
 #pragma unroll 1
         for (int d = 0; d < D; ++d) {
-            const uint32_t b = v[d];
+            const uint32_t b = E8 ? ((a.v8[at + d] & 0x7fu) == 0x7fu ? 0x7fffu : 0u) : a.v[at + d];
             if ((b & 0x7f80u) != 0x7f80u) continue;
             const float f = __uint_as_float(b << 16);
             if (out) {
@@ -736,6 +749,166 @@ __device__ __noinline__ void add_cleared(const ChunkArgs &a, int seq, int head, 
             }
         }
     }
+}
+
+// The query tiles of a piece; one thread issues.
+template <int D, bool E8>
+__device__ __forceinline__ void load_queries(const Piece &p, uint8_t *qbuf, const CUtensorMap *qmap, int qrows, Shared *sh,
+                                             const ChunkArgs &a)
+{
+    using C = Cfg<D, E8>;
+    const int tiles = p.it.ntok > a.TQ ? 2 : 1;
+    const uint32_t fb = smem_u32(&sh->q_full);
+    mbar_arrive_expect_tx(fb, tiles * C::kHalves * qrows * 128);
+    for (int x = 0; x < tiles; ++x)
+#pragma unroll
+        for (int h = 0; h < C::kHalves; ++h)
+            asm volatile(
+                "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+                "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_u32(qbuf + x * C::kTileBytes + h * C::kHalfBytes)),
+                "l"(reinterpret_cast<uint64_t>(qmap)), "r"(h * 64), "r"(p.head * a.G), "r"(p.it.row0 + x * a.TQ),
+                "r"(fb)
+                : "memory");
+}
+
+// ---- the 8-bit cache: codes to bf16 tiles -------------------------------------------
+// Two codes (bytes 2e and 2e + 1 of w) as bf16 of their values times 2^-120: sign-extended to 16 bits
+// and moved up by four, the exponent and mantissa bits are where bf16 has them, and the
+// exponent's upper bits are cleared.
+template <int E>
+__device__ __forceinline__ uint32_t spread2(uint32_t w)
+{
+    uint32_t r;
+    asm("prmt.b32 %0, %1, 0, %2;" : "=r"(r) : "r"(w), "n"(E ? 0xB3A2 : 0x9180));
+    return (r << 4) & 0x87f087f0u;
+}
+
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b)
+{
+    uint32_t r;
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
+// Rows of 16 codes as bf16, in the 128-byte swizzled layout of the products' operands.  `marked`: the
+// block may hold NaN codes; those of rows from `clear` on become 0 and are reported.
+template <int D, bool MARKED>
+__device__ __forceinline__ bool convert_block(const uint8_t *raw, uint8_t *tile, int row0, int end, int clear, float scale,
+                                              int lane)
+{
+    constexpr int CPR = D / 16, kHalfBytes = kTile * 128;  // 16-byte chunks of a row of codes
+    // the scale times 2^120; above 2^127 the product is taken in two steps
+    const uint32_t e = (__float_as_uint(scale) >> 23) & 255u, up = e == 0 ? 0u : min(e + 120u, 254u);
+    const uint32_t f = up << 7 | up << 23, rest = e + 120u > 254u ? e + 120u - 254u + 127u : 0u;
+    const uint32_t g = rest << 7 | rest << 23;
+    bool found = false;
+#pragma unroll 1
+    for (int i = lane; i < kBlk * CPR; i += 32) {
+        const int row = row0 + i / CPR, c = i % CPR;
+        uint4 w = *reinterpret_cast<const uint4 *>(raw + row * D + c * 16);
+        if (row >= end) w = make_uint4(0, 0, 0, 0);
+        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+        uint32_t r[8];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) r[2 * k] = spread2<0>(u[k]), r[2 * k + 1] = spread2<1>(u[k]);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const uint32_t t = r[k];
+            r[k] = mul_bf16x2(t, f);
+            if (rest) r[k] = mul_bf16x2(r[k], g);
+            if (MARKED) {
+                const bool lo = (t & 0x07f0u) == 0x07f0u, hi = (t & 0x07f00000u) == 0x07f00000u, gone = row >= clear;
+                found = found || (gone && (lo || hi));
+                if (lo) r[k] = (r[k] & 0xffff0000u) | (gone ? 0u : 0x7fffu);
+                if (hi) r[k] = (r[k] & 0x0000ffffu) | (gone ? 0u : 0x7fff0000u);
+            }
+        }
+        // two 16-byte chunks of a 64-dim half; lanes of the upper half begin with the second, so that
+        // eight lanes write to all banks
+        uint8_t *o = tile + (c >> 2) * kHalfBytes + row * 128;
+        const int at = 2 * (c & 3), x = row & 7, odd = c >> 2 & 1;
+        const uint4 first = make_uint4(r[0], r[1], r[2], r[3]), second = make_uint4(r[4], r[5], r[6], r[7]);
+        *reinterpret_cast<uint4 *>(o + (((at + odd) ^ x) << 4)) = odd ? second : first;
+        *reinterpret_cast<uint4 *>(o + (((at + 1 - odd) ^ x) << 4)) = odd ? first : second;
+    }
+    return found;
+}
+
+// Warps 12 to 15: a tile of codes at a time (K, V, K, ...; two blocks of it a warp) becomes a bf16 tile
+// of the ring, with what rows must not see cleared on the way.  The first of them loads the query tiles,
+// whenever the last ones are done with while it waits for something else: a tile it waits for may
+// depend on them.
+template <int D>
+__device__ __forceinline__ void convert_tiles(int cw, uint8_t *qbuf, uint8_t *ring, const uint8_t *raw, Shared *sh,
+                                              Shared8 *sh8, const CUtensorMap *qmap, int qrows, const ChunkArgs &a)
+{
+    using C = Cfg<D, true>;
+    const int lane = threadIdx.x & 31;
+    Piece p;
+    uint32_t np = 0, nq = 0, k = 0;   // pieces, query tiles issued, key tiles
+    uint32_t st = 0, ph = 1;          // the next stage of the ring and the phase that frees it
+    bool ok = true, due = false;      // due: the piece's queries are not issued yet
+    const auto queries = [&]() {
+        if (due && __all_sync(0xffffffffu, mbar_try_wait(smem_u32(&sh->q_empty), (nq & 1) ^ 1))) {
+            if (lane == 0) load_queries<D, true>(p, qbuf, qmap, qrows, sh, a);
+            __syncwarp();
+            ++nq;
+            due = false;
+        }
+    };
+    // in small steps while queries are due, else like the other control warps
+    const auto wait = [&](uint32_t bar, uint32_t parity) {
+        uint64_t t0 = 0;
+        while (due) {
+            if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+            queries();
+            const uint64_t now = globaltimer();
+            if (t0 == 0) t0 = now;
+            if (__any_sync(0xffffffffu, now - t0 > a.wait_ns)) break;  // kwait gives the verdict
+        }
+        return __all_sync(0xffffffffu, kwait<20>(bar, parity, sh, a)) != 0;
+    };
+    for (; ok && !a.stall; ++np) {
+        if (due) {
+            ok = wait(smem_u32(&sh->q_empty), (nq & 1) ^ 1);
+            if (ok) queries();
+            if (due) break;
+        }
+        if (!next_piece<true>(p, np, sh, ok, lane, wait)) break;
+        due = cw == 0;
+        queries();
+        for (int j = p.j0; ok && j < p.j1; ++j, ++k) {
+#pragma unroll 1
+            for (int kv = 0; kv < 2; ++kv) {
+                const uint32_t r = kv * kRaw8 + k % kRaw8;
+                ok = wait(smem_u32(&sh8->full[r]), k / kRaw8 & 1) && wait(smem_u32(&sh->empty[st]), ph);
+                if (!ok) break;
+                // rows from `end` on: past the sequence; from `clear` on: not seen by every row of the item
+                const int end = kv ? p.it.len - j * kTile : kTile, clear = kv ? p.it.pos0 + 1 - j * kTile : kTile;
+                bool found = false;
+#pragma unroll 1
+                for (int b = 2 * cw; b < 2 * cw + 2; ++b) {
+                    const float s = sh8->scale[r][b];
+                    const uint8_t *src = raw + r * C::kRawBytes;
+                    uint8_t *dst = ring + st * C::kTileBytes;
+                    if (__builtin_expect(signbit(s), 0))
+                        found = convert_block<D, true>(src, dst, b * kBlk, end, clear, s, lane) || found;
+                    else
+                        convert_block<D, false>(src, dst, b * kBlk, end, clear, s, lane);
+                }
+                if (found) sh->odd_values[np % kOddSlots] = (int32_t)np + 1;
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(smem_u32(&sh->full[st]));
+                    mbar_arrive(smem_u32(&sh8->empty[r]));
+                }
+                if (++st == C::kRing) st = 0, ph ^= 1;
+            }
+        }
+    }
+    // the last query tiles have landed too
+    if (cw == 0 && nq > 0) drain(smem_u32(&sh->q_full), (nq - 1) & 1);
 }
 
 // Records the sequences whose rows or lengths are out of order and zeroes their rows.
@@ -764,10 +937,10 @@ __device__ __noinline__ void refuse_sequences(const ChunkArgs &a)
 // Descriptors are 32-bit sums, and both tiles share one copy of the code: beside two busy
 // softmax warps every instruction between two MMAs counts, and every line of the
 // instruction caches.
-template <int D>
+template <int D, bool E8>
 __device__ __forceinline__ void mma_warp(int x, uint32_t qbuf, uint32_t ring, Shared *sh, const ChunkArgs &a)
 {
-    using C = Cfg<D>;
+    using C = Cfg<D, E8>;
     if (elect_one()) {
         constexpr uint32_t id_qk = idesc_bf16(kTile, kTile);
         constexpr uint32_t id_pv = idesc_bf16(kTile, D) | (1u << 16);  // V: its dims are contiguous
@@ -786,7 +959,7 @@ __device__ __forceinline__ void mma_warp(int x, uint32_t qbuf, uint32_t ring, Sh
         bool ok = true;
         auto next = [](uint32_t &st, uint32_t &ph) {  // a tile further (K and V alternate)
             st += 2;
-            if (st >= kStages) st -= kStages, ph ^= 1;
+            if (st >= C::kRing) st -= C::kRing, ph ^= 1;
         };
         auto skip = [&](uint32_t &st, uint32_t &ph) {
             ok = ok && kwait(full0 + st * 8, ph, sh, a);
@@ -879,22 +1052,28 @@ __device__ __forceinline__ void mma_warp(int x, uint32_t qbuf, uint32_t ring, Sh
     __syncwarp();
 }
 
-template <int D>
+template <int D, bool E8>
 __global__ void __launch_bounds__(kThreads, 1)
     chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
-                 const __grid_constant__ CUtensorMap qmap, const ChunkArgs a)
+                 const __grid_constant__ CUtensorMap qmap, const __grid_constant__ ChunkArgs a)
 {
-    using C = Cfg<D>;
+    using C = Cfg<D, E8>;
     extern __shared__ uint8_t csm_raw[];
     uint8_t *qbuf = csm_raw + ((1024u - (smem_u32(csm_raw) & 1023u)) & 1023u);  // two query tiles
     uint8_t *ring = qbuf + 2 * C::kTileBytes;
-    Shared *sh = reinterpret_cast<Shared *>(ring + kStages * C::kTileBytes);
+    uint8_t *raw = ring + C::kRing * C::kTileBytes;
+    Shared *sh = reinterpret_cast<Shared *>(raw + C::kRawAll);
+    Shared8 *sh8 = reinterpret_cast<Shared8 *>(sh + 1);  // (of the 8-bit cache)
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
     if (tid == 0) {
         for (int i = 0; i < kStages; ++i) {
-            mbar_init(smem_u32(&sh->full[i]), 1);
+            mbar_init(smem_u32(&sh->full[i]), E8 ? 4 : 1);  // 4: the warps that convert it
             mbar_init(smem_u32(&sh->empty[i]), 2);
+        }
+        for (int i = 0; E8 && i < 2 * kRaw8; ++i) {
+            mbar_init(smem_u32(&sh8->full[i]), 1);
+            mbar_init(smem_u32(&sh8->empty[i]), 4);
         }
         for (int i = 0; i < kPieces; ++i) {
             mbar_init(smem_u32(&sh->piece_full[i]), 1);
@@ -940,7 +1119,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     if (blockIdx.x == gridDim.x - 1) refuse_sequences(a);
-    share_out(a, sh, reinterpret_cast<int32_t *>(ring), kStages * C::kTileBytes / 4);
+    share_out(a, sh, reinterpret_cast<int32_t *>(ring), C::kRing * C::kTileBytes / 4);
 
     if (warp >= 8) {
         reg_dealloc<kRegsCtl>();
@@ -959,7 +1138,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint32_t st = kv, ph = 1, k = 0;  // stage and the phase that frees it; tiles issued
             uint32_t ne = 0, were_edges = 0;  // edge tiles issued; which of the last tiles were
             const int b = lane % kBlkPerTile, h = lane / kBlkPerTile;
-            const bool mine = h < C::kHalves;
+            const bool mine = E8 ? h == 0 : h < C::kHalves;
             bool ok = !a.stall;
             while (ok) {
                 if (kv == 0) {
@@ -992,6 +1171,33 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     return id;
                 };
+                if constexpr (E8) {
+                    // a tile of codes and its blocks' scales; ids are looked up two tiles ahead, scales one
+                    const float *scales = (kv ? a.v_scale : a.k_scale) + p.head;
+                    const auto scale = [&](int32_t id) {
+                        return id < a.num_blocks ? scales[(int64_t)id * a.hkv] : 0.f;
+                    };
+                    int32_t id = block_id(p.j0), next_id = p.j0 + 1 < p.j1 ? block_id(p.j0 + 1) : a.num_blocks;
+                    float sc = scale(id);
+                    for (int j = p.j0; j < p.j1; ++j) {
+                        const uint32_t r = kv * kRaw8 + k % kRaw8, fb = smem_u32(&sh8->full[r]);
+                        ok = __all_sync(0xffffffffu, kwait(smem_u32(&sh8->empty[r]), (k / kRaw8 & 1) ^ 1, sh, a));
+                        if (!ok) break;
+                        if (mine) sh8->scale[r][b] = sc;
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive_expect_tx(fb, C::kRawBytes);
+                        __syncwarp();
+                        if (mine)
+                            tma_load_5d(smem_u32(raw + r * C::kRawBytes + b * kBlk * D), map, fb, 0, 0, p.head, id,
+                                        a.layer);
+                        ++k;
+                        if (kv == 0 && lane == 0) *(volatile uint32_t *)&sh->loaded = k;
+                        id = next_id;
+                        sc = scale(id);
+                        if (j + 2 < p.j1) next_id = block_id(j + 2);
+                    }
+                    continue;
+                }
                 int32_t id = block_id(p.j0);
                 for (int j = p.j0; j < p.j1; ++j) {
                     const int32_t cur = id;
@@ -1015,7 +1221,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (lane == 0) sh->issued[kv] = make_int4((int)k, (int)ne, (int)were_edges, 0);
         } else if (warp == kWarpMma || warp == kWarpMma + 1) {
-            mma_warp<D>(warp - kWarpMma, smem_u32(qbuf), smem_u32(ring), sh, a);
+            mma_warp<D, E8>(warp - kWarpMma, smem_u32(qbuf), smem_u32(ring), sh, a);
+        } else if constexpr (E8) {
+            convert_tiles<D>(warp - kWarpQ, qbuf, ring, raw, sh, sh8, &qmap, qrows, a);
         } else {
             // ---------------- query tiles (warp 12), and the edge tiles of V (warps 12-15, a
             // quarter of the rows each: the products wait for them)
@@ -1029,21 +1237,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (warp == kWarpQ) {
                     ok = __all_sync(0xffffffffu, kwait<200>(smem_u32(&sh->q_empty), (np & 1) ^ 1, sh, a));
                     if (!ok) break;
-                    if (lane == 0) {
-                        const int tiles = p.it.ntok > a.TQ ? 2 : 1;
-                        const uint32_t fb = smem_u32(&sh->q_full);
-                        mbar_arrive_expect_tx(fb, tiles * C::kHalves * qrows * 128);
-                        for (int x = 0; x < tiles; ++x)
-#pragma unroll
-                            for (int h = 0; h < C::kHalves; ++h)
-                                asm volatile(
-                                    "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
-                                    "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
-                                        smem_u32(qbuf + x * C::kTileBytes + h * C::kHalfBytes)),
-                                    "l"(reinterpret_cast<uint64_t>(&qmap)), "r"(h * 64), "r"(p.head * a.G),
-                                    "r"(p.it.row0 + x * a.TQ), "r"(fb)
-                                    : "memory");
-                    }
+                    if (lane == 0) load_queries<D, E8>(p, qbuf, &qmap, qrows, sh, a);
                     __syncwarp();
                 }
                 for (int j = max(p.j0, (p.it.pos0 + 1) / kTile); ok && j < p.j1; ++j) {
@@ -1268,8 +1462,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     __syncwarp();  // all lanes load the next columns
                 }
-                if (add && live) add_cleared<D>(a, p.seq, p.head, max(p.it.pos0 + 1, p.j0 * kTile),
-                                                min(pos, p.j1 * kTile - 1), p.whole ? op : nullptr, pp);
+                if (add && live) add_cleared<D, E8>(a, p.seq, p.head, max(p.it.pos0 + 1, p.j0 * kTile),
+                                                    min(pos, p.j1 * kTile - 1), p.whole ? op : nullptr, pp);
                 if (live && !p.whole) a.stat[slot * 256 + rr] = make_float2(m, z);
             }
             // the next piece's products write O again only after these reads
@@ -1285,7 +1479,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     tc_fence_after();
     if (warp == kWarpMma) tmem_dealloc(sh->tmem, kTmemCols);
-    if (warp == kWarpKv || warp == kWarpKv + 1) drain_tiles(sh, warp - kWarpKv);
+    if (warp == kWarpKv || warp == kWarpKv + 1) {
+        if constexpr (E8) {
+            const uint32_t k = (uint32_t)sh->issued[warp - kWarpKv].x;
+            for (uint32_t i = k > kRaw8 ? k - kRaw8 : 0; i < k; ++i)
+                drain(smem_u32(&sh8->full[(warp - kWarpKv) * kRaw8 + i % kRaw8]), i / kRaw8 & 1);
+        } else {
+            drain_tiles(sh, warp - kWarpKv);
+        }
+    }
 }
 
 // ---- merge ----------------------------------------------------------------------
@@ -1357,7 +1559,8 @@ cudaError_t pool_map(CUtensorMap *m, const void *pool, const kara_cache *c)
 }
 
 // Tensor map over q, (d, head, row); a box is one 64-dim half of a query tile.
-cudaError_t query_map(CUtensorMap *m, const void *q, const kara_cache *c, int32_t rows, int G, int TQ)
+template <class Cache>
+cudaError_t query_map(CUtensorMap *m, const void *q, const Cache *c, int32_t rows, int G, int TQ)
 {
     auto fn = tensor_map_encoder();
     if (!fn) return cudaErrorNotSupported;
@@ -1377,40 +1580,38 @@ struct Layout {
     size_t start, whole, stat, part, total;
 };
 
-Layout layout(const kara_cache *c)
+Layout layout(int32_t D)
 {
     Layout l;
     size_t o = 256;
     l.start = o, o += align256((kMaxCtas + 1) * sizeof(Start));
     l.whole = o, o += align256((size_t)kMaxCtas * kMaxRounds * sizeof(Start));
     l.stat = o, o += align256((size_t)2 * kMaxCtas * 256 * sizeof(float2));
-    l.part = o, o += (size_t)2 * kMaxCtas * 256 * c->head_dim * sizeof(float);
+    l.part = o, o += (size_t)2 * kMaxCtas * 256 * D * sizeof(float);
     l.total = o;
     return l;
 }
 
-template <int D>
+template <int D, bool E8>
 cudaError_t launch_all(const CUtensorMap &km, const CUtensorMap &vm, const CUtensorMap &qm, const ChunkArgs &a,
                        cudaStream_t st)
 {
-    constexpr size_t smem = Cfg<D>::kSmem;
+    constexpr size_t smem = Cfg<D, E8>::kSmem;
     static_assert(smem <= 227 * 1024, "shared memory");
-    cudaError_t e = cudaFuncSetAttribute(chunk_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    cudaError_t e = cudaFuncSetAttribute(chunk_kernel<D, E8>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    e = launch_dependent(chunk_kernel<D>, dim3((unsigned)a.ctas), kThreads, smem, st, km, vm, qm, a);
+    e = launch_dependent(chunk_kernel<D, E8>, dim3((unsigned)a.ctas), kThreads, smem, st, km, vm, qm, a);
     if (e == cudaSuccess && a.ctas > 1)
         e = launch_dependent(chunk_merge_kernel<D>, dim3((unsigned)a.ctas - 1, 8 * (D / 64)), 256, 0, st, a);
     return e;
 }
 
-}  // namespace
-
-size_t chunk_workspace_bytes(const kara_cache *c) { return layout(c).total; }
-
-cudaError_t launch_chunk(const kara_cache *c, int32_t layer, const kara_tokens *t, const int32_t *bt,
-                         int32_t bt_stride, const void *q, void *out, void *ws, int32_t *err, cudaStream_t st)
+// A call's arguments but for where the cache lies, and the map of its queries.
+template <class Cache>
+cudaError_t chunk_args(ChunkArgs *p, CUtensorMap *qm, const Cache *c, int32_t layer, const kara_tokens *t,
+                       const int32_t *bt, int32_t bt_stride, const void *q, void *out, void *ws, int32_t *err)
 {
-    ChunkArgs a;
+    ChunkArgs &a = *p;
     a.q_start = t->q_start;
     a.len = t->len;
     a.bt = bt;
@@ -1427,10 +1628,12 @@ cudaError_t launch_chunk(const kara_cache *c, int32_t layer, const kara_tokens *
     a.TQ = kTile / a.G;
     a.scale2 = 1.4426950408889634f / sqrtf((float)c->head_dim);
     a.out = static_cast<uint16_t *>(out);
-    a.v = static_cast<const uint16_t *>(c->v) + (int64_t)layer * c->layer_stride;
+    a.v = nullptr;
+    a.v8 = nullptr;
+    a.k_scale = a.v_scale = nullptr;
     a.block_stride = c->block_stride;
     a.head_stride = c->head_stride;
-    const Layout l = layout(c);
+    const Layout l = layout(c->head_dim);
     char *w = static_cast<char *>(ws);
     a.used_ctas = reinterpret_cast<int32_t *>(w);
     a.start = reinterpret_cast<Start *>(w + l.start);
@@ -1446,12 +1649,40 @@ cudaError_t launch_chunk(const kara_cache *c, int32_t layer, const kara_tokens *
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     if (e != cudaSuccess) return e;
     a.ctas = sms < kMaxCtas ? sms : kMaxCtas;
+    return query_map(qm, q, c, t->rows, a.G, a.TQ);
+}
+
+}  // namespace
+
+size_t chunk_workspace_bytes(int32_t head_dim) { return layout(head_dim).total; }
+
+cudaError_t launch_chunk(const kara_cache *c, int32_t layer, const kara_tokens *t, const int32_t *bt,
+                         int32_t bt_stride, const void *q, void *out, void *ws, int32_t *err, cudaStream_t st)
+{
+    ChunkArgs a;
     CUtensorMap km, vm, qm;
-    e = pool_map(&km, c->k, c);
+    cudaError_t e = chunk_args(&a, &qm, c, layer, t, bt, bt_stride, q, out, ws, err);
+    a.v = static_cast<const uint16_t *>(c->v) + (int64_t)layer * c->layer_stride;
+    if (e == cudaSuccess) e = pool_map(&km, c->k, c);
     if (e == cudaSuccess) e = pool_map(&vm, c->v, c);
-    if (e == cudaSuccess) e = query_map(&qm, q, c, t->rows, a.G, a.TQ);
     if (e != cudaSuccess) return e;
-    return c->head_dim == 128 ? launch_all<128>(km, vm, qm, a, st) : launch_all<64>(km, vm, qm, a, st);
+    return c->head_dim == 128 ? launch_all<128, false>(km, vm, qm, a, st) : launch_all<64, false>(km, vm, qm, a, st);
+}
+
+cudaError_t launch_chunk8(const kara_cache8 *c, int32_t layer, const kara_tokens *t, const int32_t *bt,
+                          int32_t bt_stride, const void *q, void *out, void *ws, int32_t *err, cudaStream_t st)
+{
+    ChunkArgs a;
+    CUtensorMap km, vm, qm;
+    cudaError_t e = chunk_args(&a, &qm, c, layer, t, bt, bt_stride, q, out, ws, err);
+    const int64_t scales = (int64_t)layer * c->num_blocks * c->num_kv_heads;
+    a.v8 = static_cast<const uint8_t *>(c->v) + (int64_t)layer * c->layer_stride;
+    a.k_scale = c->k_scale + scales;
+    a.v_scale = c->v_scale + scales;
+    if (e == cudaSuccess) e = pool_map8(&km, c->k, c, false);
+    if (e == cudaSuccess) e = pool_map8(&vm, c->v, c, false);
+    if (e != cudaSuccess) return e;
+    return c->head_dim == 128 ? launch_all<128, true>(km, vm, qm, a, st) : launch_all<64, true>(km, vm, qm, a, st);
 }
 
 }  // namespace kara

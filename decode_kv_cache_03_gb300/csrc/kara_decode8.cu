@@ -513,8 +513,8 @@ cudaError_t launch_decode8(const kara_cache8 *c, int32_t layer, int32_t n, const
                            int32_t bt_stride, const void *q, void *out, void *ws, int32_t *err, cudaStream_t st)
 {
     CUtensorMap km, vm;
-    cudaError_t e = pool_map8(&km, c->k, c);
-    if (e == cudaSuccess) e = pool_map8(&vm, c->v, c);
+    cudaError_t e = pool_map8(&km, c->k, c, true);
+    if (e == cudaSuccess) e = pool_map8(&vm, c->v, c, true);
     if (e != cudaSuccess) return e;
     const int64_t scales = (int64_t)layer * c->num_blocks * c->num_kv_heads;
     Decode8Args a;

@@ -90,6 +90,22 @@ kara_status check_append(const Cache *c, int32_t layer, const kara_tokens *t, co
     return q_out == q && q_stride != qd ? KARA_EINVAL : KARA_OK;
 }
 
+// The arguments of a chunk's attention beside the cache; nothing: there are no tokens.
+template <class Cache>
+kara_status check_chunk(const Cache *c, int32_t layer, const kara_tokens *t, const int32_t *block_table,
+                        int32_t bt_stride, const void *q, const void *out, const void *ws, size_t ws_bytes,
+                        const int32_t *err, bool *nothing)
+{
+    if (layer < 0 || layer >= c->num_layers || !t || t->n < 0 || t->rows < 0 || bt_stride < 1) return KARA_EINVAL;
+    *nothing = t->n == 0 || t->rows == 0;
+    if (*nothing) return KARA_OK;
+    if (t->n > kMaxSeqs || (int64_t)bt_stride * c->block_size > 0x7fffffffLL) return KARA_EUNSUPPORTED;
+    if (!t->q_start || !t->len || !block_table || !q || !out || !err) return KARA_EINVAL;
+    if (!aligned16(q) || !aligned16(out)) return KARA_EINVAL;
+    if (!ws || ws_bytes < chunk_workspace_bytes(c->head_dim)) return KARA_EWORKSPACE;
+    return aligned16(ws) ? KARA_OK : KARA_EINVAL;
+}
+
 kara_status make_geo(const kara_cache *c, const kara_params *p, const kara_batch *b, Geo *g)
 {
     kara_status st = check_params(p);
@@ -433,7 +449,7 @@ kara_status kara_append_kv8(const kara_cache8 *c, int32_t layer, const kara_toke
 size_t kara_chunk_workspace_size(const kara_cache *c, int32_t n, int32_t rows)
 {
     if (check_cache(c) != KARA_OK || n < 0 || rows < 0) return 0;
-    return chunk_workspace_bytes(c);
+    return chunk_workspace_bytes(c->head_dim);
 }
 
 kara_status kara_chunk_attention(const kara_cache *c, int32_t layer, const kara_tokens *t, const int32_t *block_table,
@@ -441,16 +457,29 @@ kara_status kara_chunk_attention(const kara_cache *c, int32_t layer, const kara_
                                  kara_stream_t stream)
 {
     const Range range("kara_chunk_attention");
-    const kara_status st = check_cache(c);
-    if (st != KARA_OK) return st;
-    if (layer < 0 || layer >= c->num_layers || !t || t->n < 0 || t->rows < 0 || bt_stride < 1) return KARA_EINVAL;
-    if (t->n == 0 || t->rows == 0) return KARA_OK;
-    if (t->n > kMaxSeqs || (int64_t)bt_stride * c->block_size > 0x7fffffffLL) return KARA_EUNSUPPORTED;
-    if (!t->q_start || !t->len || !block_table || !q || !out || !err) return KARA_EINVAL;
-    if (!aligned16(q) || !aligned16(out)) return KARA_EINVAL;
-    if (!ws || ws_bytes < chunk_workspace_bytes(c)) return KARA_EWORKSPACE;
-    if (!aligned16(ws)) return KARA_EINVAL;
+    kara_status st = check_cache(c);
+    bool nothing = false;
+    if (st == KARA_OK) st = check_chunk(c, layer, t, block_table, bt_stride, q, out, ws, ws_bytes, err, &nothing);
+    if (st != KARA_OK || nothing) return st;
     return cuda_status(launch_chunk(c, layer, t, block_table, bt_stride, q, out, ws, err, (cudaStream_t)stream));
+}
+
+size_t kara_chunk8_workspace_size(const kara_cache8 *c, int32_t n, int32_t rows)
+{
+    if (check_cache8(c) != KARA_OK || n < 0 || rows < 0) return 0;
+    return chunk_workspace_bytes(c->head_dim);
+}
+
+kara_status kara_chunk_attention8(const kara_cache8 *c, int32_t layer, const kara_tokens *t,
+                                  const int32_t *block_table, int32_t bt_stride, const void *q, void *out, void *ws,
+                                  size_t ws_bytes, int32_t *err, kara_stream_t stream)
+{
+    const Range range("kara_chunk_attention8");
+    kara_status st = check_cache8(c);
+    bool nothing = false;
+    if (st == KARA_OK) st = check_chunk(c, layer, t, block_table, bt_stride, q, out, ws, ws_bytes, err, &nothing);
+    if (st != KARA_OK || nothing) return st;
+    return cuda_status(launch_chunk8(c, layer, t, block_table, bt_stride, q, out, ws, err, (cudaStream_t)stream));
 }
 
 size_t kara_decode8_workspace_size(const kara_cache8 *c, int32_t n, int32_t bt_stride)

@@ -37,7 +37,7 @@ cudaError_t launch_extend(int32_t num_blocks, const int32_t *len, const int32_t 
 cudaError_t launch_append(const kara_cache *c, int32_t layer, const kara_tokens *t, const kara_rope *r, const void *q,
                           int64_t q_stride, const void *k, int64_t k_stride, const void *v, int64_t v_stride,
                           void *q_out, void *ring, int32_t W, int32_t *err, cudaStream_t st);
-size_t chunk_workspace_bytes(const kara_cache *c);
+size_t chunk_workspace_bytes(int32_t head_dim);
 cudaError_t launch_chunk(const kara_cache *c, int32_t layer, const kara_tokens *t, const int32_t *bt,
                          int32_t bt_stride, const void *q, void *out, void *ws, int32_t *err, cudaStream_t st);
 

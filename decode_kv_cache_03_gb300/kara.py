@@ -100,6 +100,8 @@ def _load():
         "kara_append_kv8": ([PC8, I32, PT, PR, P, I64, P, I64, P, I64, P, P, I32, P, P], ctypes.c_int),
         "kara_decode8_workspace_size": ([PC8, I32, I32], SZ),
         "kara_decode_attention8": ([PC8, I32, I32, P, P, I32, P, P, P, SZ, P, P], ctypes.c_int),
+        "kara_chunk8_workspace_size": ([PC8, I32, I32], SZ),
+        "kara_chunk_attention8": ([PC8, I32, PT, P, I32, P, P, P, SZ, P, P], ctypes.c_int),
         "kara_expand8": ([PC8, PC, I32, I32, P, P, I32, P, P, P], ctypes.c_int),
         "kara_compact8_workspace_size": ([PC8, PP, I32], SZ),
         "kara_compact8": ([PC8, PP, I32, P, P, I32, P, P, I64, P, P, P, SZ, P, P], ctypes.c_int),
@@ -119,7 +121,7 @@ EXPORTED = ("kara_status_string", "kara_version", "kara_plan", "kara_workspace_s
             "kara_decode_workspace_size", "kara_decode_attention", "kara_compact_queries", "kara_append_queries",
             "kara_batch_groups", "kara_extend_tables", "kara_append_kv", "kara_chunk_workspace_size",
             "kara_chunk_attention", "kara_append_kv8", "kara_decode8_workspace_size", "kara_decode_attention8",
-            "kara_expand8", "kara_compact8_workspace_size", "kara_compact8")
+            "kara_chunk8_workspace_size", "kara_chunk_attention8", "kara_expand8", "kara_compact8_workspace_size", "kara_compact8")
 STATIC_MAX_SEQS = 8192     # KARA_STATIC_MAX_SEQS
 
 
@@ -346,17 +348,31 @@ def kara_chunk_workspace_size(c: Cache, n: int, rows: int) -> int:
     return int(_lib.kara_chunk_workspace_size(ctypes.byref(c), int(n), int(rows)))
 
 
+def _chunk(entry, where: str, c, layer: int, t: Tokens, block_table, q, out, ws, err, stream):
+    """The checks and the call of a chunk's attention over a cache of either type."""
+    _same_device(err, where, block_table, q, out, ws, c, t)
+    assert block_table.dtype == torch.int32 and block_table.is_contiguous() and block_table.shape[0] == t.n
+    assert q.dtype == out.dtype == torch.bfloat16 and q.is_contiguous() and out.is_contiguous()
+    assert q.shape == out.shape == (t.rows, c.num_q_heads, c.head_dim)
+    _check(entry(c, layer, t, block_table.data_ptr(), block_table.shape[1], q.data_ptr(), out.data_ptr(), ws.data_ptr(),
+                 ws.numel() * ws.element_size(), err.data_ptr(), _raw_stream(err, stream)), where)
+
+
 def kara_chunk_attention(c: Cache, layer: int, t: Tokens, block_table: torch.Tensor, q: torch.Tensor,
                          out: torch.Tensor, ws: torch.Tensor, err: torch.Tensor, stream=None):
     """Causal attention of the new tokens q [rows][num_q_heads][head_dim] (bf16) over layer `layer` of
     the paged cache, read through block_table [n][bt_stride]; out like q, padding rows untouched."""
-    _same_device(err, "kara_chunk_attention", block_table, q, out, ws, c, t)
-    assert block_table.dtype == torch.int32 and block_table.is_contiguous() and block_table.shape[0] == t.n
-    assert q.dtype == out.dtype == torch.bfloat16 and q.is_contiguous() and out.is_contiguous()
-    assert q.shape == out.shape == (t.rows, c.num_q_heads, c.head_dim)
-    _check(_lib.kara_chunk_attention(c, layer, t, block_table.data_ptr(), block_table.shape[1], q.data_ptr(),
-                                     out.data_ptr(), ws.data_ptr(), ws.numel() * ws.element_size(), err.data_ptr(),
-                                     _raw_stream(err, stream)), "kara_chunk_attention")
+    _chunk(_lib.kara_chunk_attention, "kara_chunk_attention", c, layer, t, block_table, q, out, ws, err, stream)
+
+
+def kara_chunk8_workspace_size(c: Cache8, n: int, rows: int) -> int:
+    return int(_lib.kara_chunk8_workspace_size(ctypes.byref(c), int(n), int(rows)))
+
+
+def kara_chunk_attention8(c: Cache8, layer: int, t: Tokens, block_table: torch.Tensor, q: torch.Tensor,
+                          out: torch.Tensor, ws: torch.Tensor, err: torch.Tensor, stream=None):
+    """kara_chunk_attention over an 8-bit cache."""
+    _chunk(_lib.kara_chunk_attention8, "kara_chunk_attention8", c, layer, t, block_table, q, out, ws, err, stream)
 
 
 def kara_decode8_workspace_size(c: Cache8, n: int, bt_stride: int) -> int:

@@ -408,6 +408,18 @@ kara_status kara_decode_attention8(const kara_cache8 *c, int32_t layer, int32_t 
                                    size_t ws_bytes, int32_t *err, kara_stream_t stream);
 
 /*
+ * Causal attention of new tokens over an 8-bit cache: kara_chunk_attention with k_x
+ * and v_x the stored values, its arguments, checks, errors and arithmetic (the output
+ * has the bits that kara_chunk_attention gives over a bf16 cache of those values,
+ * which holds all of them).  A key or value that is NaN reaches only the rows that
+ * see it.
+ */
+size_t kara_chunk8_workspace_size(const kara_cache8 *c, int32_t n, int32_t rows);
+kara_status kara_chunk_attention8(const kara_cache8 *c, int32_t layer, const kara_tokens *t,
+                                  const int32_t *block_table, int32_t bt_stride, const void *q, void *out, void *ws,
+                                  size_t ws_bytes, int32_t *err, kara_stream_t stream);
+
+/*
  * The windows of an 8-bit cache in bf16, for kara_score (a compression scores bf16
  * keys).  Block j of sequence s's window, the logical block (len[s] - W)/bs + j for
  * j <= W/bs, is written as block s * (W/bs + 1) + j of `out` in all layers and heads

@@ -67,6 +67,11 @@ def decode(kara, c=None, layer=0, n=2, ln=PTR, bt=PTR, bts=4, q=PTR, out=PTR, ws
     return kara._lib.kara_decode_attention8(c or fake8(kara), layer, n, ln, bt, bts, q, out, ws, wb, err, None)
 
 
+def chunk(kara, c=None, layer=0, t=None, bt=PTR, bts=4, q=PTR, out=PTR, ws=PTR, wb=1 << 40, err=PTR):
+    return kara._lib.kara_chunk_attention8(c or fake8(kara), layer, t or fake_tokens(kara), bt, bts, q, out, ws, wb, err,
+                                           None)
+
+
 def expand(kara, c=None, o=None, W=64, n=2, ln=PTR, bt=PTR, bts=8, ot=ctypes.c_void_p(8192), err=PTR):
     return kara._lib.kara_expand8(c or fake8(kara), o or fake16(kara), W, n, ln, bt, bts, ot, err, None)
 
@@ -77,12 +82,13 @@ def compact(kara, c=None, p=None, n=2, ln=PTR, bt=PTR, bts=8, kept=PTR, fresh=PT
                                    freed, nl, ws, wb, err, None)
 
 
-@pytest.mark.parametrize("call", [append, decode, expand, compact])
+@pytest.mark.parametrize("call", [append, decode, chunk, expand, compact])
 def test_every_call_refuses_bad_caches(kara, call):
     for kw, want in BAD_CACHES:
         assert call(kara, c=fake8(kara, **kw)) == getattr(kara, want), kw
     for kw, want in BAD_CACHES:
         assert kara.kara_decode8_workspace_size(fake8(kara, **kw), 1, 1) == 0, kw
+        assert kara.kara_chunk8_workspace_size(fake8(kara, **kw), 1, 1) == 0, kw
         assert kara.kara_compact8_workspace_size(fake8(kara, **kw), kara.params(64, 16, 1, 16, 0.1), 1) == 0, kw
 
 
@@ -108,6 +114,18 @@ def test_decode_refuses(kara):
     assert decode(kara, ws=None) == decode(kara, wb=100) == kara.EWORKSPACE
     assert decode(kara, n=0) == kara.OK
     assert kara.kara_decode8_workspace_size(fake8(kara), 3, 65) >= 3 * 4 * 2 * (64 * 4 + 8)
+
+
+def test_chunk_refuses(kara):
+    for kw in (dict(layer=-1), dict(layer=2), dict(bt=None), dict(bts=0), dict(q=None), dict(out=None), dict(err=None),
+               dict(q=ODD), dict(out=ODD), dict(ws=ODD)):
+        assert chunk(kara, **kw) == kara.EINVAL, kw
+    for kw in (dict(n=-1), dict(rows=-1), dict(q_start=None), dict(len=None)):
+        assert chunk(kara, t=fake_tokens(kara, **kw)) == kara.EINVAL, kw
+    assert chunk(kara, t=fake_tokens(kara, n=65536)) == chunk(kara, bts=1 << 27) == kara.EUNSUPPORTED
+    assert chunk(kara, ws=None) == chunk(kara, wb=1) == kara.EWORKSPACE
+    assert chunk(kara, t=fake_tokens(kara, rows=0)) == chunk(kara, t=fake_tokens(kara, n=0)) == kara.OK
+    assert kara.kara_chunk8_workspace_size(fake8(kara), 1, 1) > 0
 
 
 def test_expand_refuses(kara):
@@ -152,6 +170,7 @@ def test_binding_refuses_host_tensors(kara):
     w = torch.zeros(1 << 16, dtype=torch.uint8)
     for call in (lambda: kara.kara_append_kv8(c, 0, t, kara.rope(None), q, q[:, :2], q[:, 2:], q, i32(1)),
                  lambda: kara.kara_decode_attention8(c, 0, i32(4), i32(4, 2), q, q, w, i32(1)),
+                 lambda: kara.kara_chunk_attention8(c, 0, t, i32(1, 2), q, q, w, i32(1)),
                  lambda: kara.kara_expand8(c, kara.cache(pool, pool, 4), 16, i32(1), i32(1, 2), i32(1, 2), i32(1)),
                  lambda: kara.kara_compact8(c, kara.params(64, 16, 1, 16, 0.1), i32(1), i32(1, 2), i32(1, 1, 2, 16), i32(2),
                                             i32(2), i32(1), w, i32(1))):

@@ -9,6 +9,8 @@ append   fp32 sums and products of one row (about 20 roundings of 2^-24, against
 decode   logits: fp32 sums of exact products and two multiplications; with |logit| <= 40 and 128 terms below
          2^-11 of a weight.  A weight is rounded to f16 once (2^-11 of it, or 2^-40 of the split's largest).  One
          rounding of the output: |got - ref| <= 2^-8 |ref| + 2^-10 sum_x w_x |v_x| + 2^-30 max|v|.
+chunk    the bits of kara_chunk_attention over a bf16 cache of the same values, which holds them exactly; against 64
+         bits its tolerance, 2^-8 |ref| + (2^-8 + 2^-10) sum_x w_x |v_x|.
 expand, compact   equal: code times scale is exact, and a code is rounded once from an exact quotient."""
 
 import numpy as np
@@ -18,7 +20,7 @@ import torch
 from _cache8 import (BS, dense, divide, plain_compact, plain_decode, quantise, random_pool, round_code, runs, scale_of,
                      source_rows, value)
 from _gpu import lib
-from _newtokens import blocks, make_tables, plain_extend, plain_turn
+from _newtokens import blocks, make_tables, plain_chunk, plain_extend, plain_turn
 
 pytestmark = pytest.mark.gpu
 
@@ -434,6 +436,183 @@ def test_decode_strided_pools_and_long_table():
     err = error_word()
     kara.kara_decode_attention8(c, 1, i32(lengths), i32(wide), q.to(DEV), out, ws, err)
     assert status(kara, err) == 0 and torch.equal(out.cpu(), want)
+
+
+# ---- chunk attention ------------------------------------------------------------
+
+def chunk_case(seed, lengths, n_new, hq, hkv, d, layers=1, pad=0, qmag=1.5):
+    """Lengths include the new tokens; rows of a block where no token lives hold NaN, in marked blocks."""
+    g = torch.Generator().manual_seed(seed)
+    lengths, bt, k, ks, v, vs, _ = decode_case(seed, lengths, 1, 1, 64)
+    nb = k.shape[1]
+    k, ks = random_pool((layers, nb, hkv, BS, d), seed + 1, 1)
+    v, vs = random_pool((layers, nb, hkv, BS, d), seed + 2)
+    used = np.zeros((nb, BS), bool)
+    for s, L in enumerate(lengths):
+        for x in range(int(L)):
+            used[bt[s, x // BS], x % BS] = True
+    for codes, scale in ((k, ks), (v, vs)):
+        codes.permute(1, 3, 0, 2, 4)[torch.from_numpy(~used)] = 0xff
+        scale[:, torch.from_numpy(~used.all(1))] *= -1
+    q_start = np.concatenate([[0], np.cumsum(n_new)]).astype(np.int32)
+    q = (qmag * torch.randn(int(q_start[-1]) + pad, hq, d, generator=g)).bfloat16()
+    return dict(q=q, k=k, v=v, ks=ks, vs=vs, bt=bt, q_start=q_start, lengths=lengths)
+
+
+def chunk_descriptor(kara, d):
+    rows = d["q"].shape[0]
+    z, z4 = (torch.empty(rows, dtype=t, device=DEV) for t in (torch.int64, torch.int32))
+    return kara.tokens(i32(d["q_start"]), i32(d["lengths"]), z, z4, z4)
+
+
+def run_chunk(d, layer=0, bf16=False, pools=None, fill=77.0):
+    """The output over the 8-bit cache, or over a bf16 cache of its values."""
+    kara, hq = lib(), d["q"].shape[1]
+    t, out, err = chunk_descriptor(kara, d), torch.full(d["q"].shape, fill, dtype=torch.bfloat16, device=DEV), error_word()
+    if bf16:
+        keep = [dense(d[x], d[x + "s"]).bfloat16().to(DEV) for x in "kv"]
+        c, size, call = kara.cache(*keep, hq), kara.kara_chunk_workspace_size, kara.kara_chunk_attention
+    else:
+        keep = [d[x].to(DEV) for x in ("k", "v", "ks", "vs")] if pools is None else pools
+        c, size, call = kara.cache8(*keep, hq), kara.kara_chunk8_workspace_size, kara.kara_chunk_attention8
+    ws = torch.empty(size(c, t.n, t.rows), dtype=torch.uint8, device=DEV)
+    call(c, layer, t, i32(d["bt"]), d["q"].to(DEV), out, ws, err)
+    return status(kara, err), out.cpu()
+
+
+def same_bits(a, b):
+    return torch.equal(a.view(torch.int16), b.view(torch.int16))
+
+
+CHUNKS = [([1, 17, 128, 129, 300, 64, 513, 255, 700], [1, 17, 1, 129, 4, 0, 140, 255, 33]),
+          ([2500], [1]), ([5000, 3], [3, 3]), ([900] * 40, [1] * 40), ([1500], [1500]), ([16] * 130, [16] * 130)]
+
+
+@pytest.mark.parametrize("case", range(len(CHUNKS)))
+@pytest.mark.parametrize("hq,hkv,d", [(2, 2, 64), (4, 2, 128), (6, 2, 64), (8, 2, 128), (10, 2, 128), (7, 1, 128),
+                                      (16, 2, 64)])
+def test_chunk_has_the_bits_of_the_bf16_cache(case, hq, hkv, d):
+    """Every group size and head dim, single tokens to whole prompts, on both caches: the same output."""
+    lengths, n_new = CHUNKS[case]
+    c = chunk_case(case * 31 + hq, lengths, n_new, hq, hkv, d, layers=2, pad=3)
+    for layer in (0, 1):
+        st, got = run_chunk(c, layer)
+        st2, want = run_chunk(c, layer, bf16=True)
+        assert st == st2 == 0
+        assert torch.isfinite(got).all() and same_bits(got, want) and (got[-3:] == 77.0).all()
+
+
+@pytest.mark.parametrize("hq,hkv,d", [(4, 2, 64), (10, 2, 128)])
+def test_chunk_matches_plain(hq, hkv, d):
+    """Against 64 bits: the weights' rounding to bf16 and the output's."""
+    c = chunk_case(hq, CHUNKS[0][0], CHUNKS[0][1], hq, hkv, d, pad=2)
+    st, got = run_chunk(c)
+    kv = [dense(c[x], c[x + "s"]) for x in "kv"]
+    ref = plain_chunk(c["q"], *kv, 0, c["bt"], c["q_start"], c["lengths"])
+    size = plain_chunk(c["q"], *kv, 0, c["bt"], c["q_start"], c["lengths"], absolute=True)
+    n = int(c["q_start"][-1])
+    lim = (ref.abs() * 2.0 ** -8 + size * (2.0 ** -8 + 2.0 ** -10))[:n]
+    assert st == 0 and ((got.double() - ref).abs()[:n] <= lim).all()
+
+
+def test_chunk_scales_at_their_limits():
+    """Scales of 2^-63, 2^63 and 0, above the range of one product too: the bits of the bf16 cache."""
+    c = chunk_case(4, [200, 333, 100], [60, 200, 1], 8, 2, 128, qmag=0.01)
+    for i, e in enumerate((-63, -40, 5, 7, 8, 9, 30)):
+        c["ks"][0, int(c["bt"][0, i])] = 2.0 ** e if e < 9 else 2.0 ** -20
+        c["vs"][0, int(c["bt"][1, i])] = 2.0 ** e
+    c["vs"][0, int(c["bt"][2, 1])] = 2.0 ** 63
+    c["vs"][0, int(c["bt"][2, 2])] = 0.0
+    c["v"][0, int(c["bt"][2, 2])] = 0
+    st, got = run_chunk(c)
+    assert st == 0 and same_bits(got, run_chunk(c, bf16=True)[1])
+
+
+@pytest.mark.parametrize("pool", ["k", "v"])
+@pytest.mark.parametrize("at", [3, 55, 120])
+def test_chunk_nan_reaches_those_who_see_it(pool, at):
+    """A NaN among the earlier tokens, or among the chunk's own: rows before it keep their bits, rows behind it
+    show it, in its dim (a value) or altogether (a key), of its KV head."""
+    c = chunk_case(9, [150, 300], [100, 290], 4, 2, 128)
+    want = run_chunk(c)[1]
+    b = int(c["bt"][0, at // BS])
+    c[pool][0, b, 1, at % BS, 7] = 0x7f
+    c[pool + "s"][0, b, 1] = -c[pool + "s"][0, b, 1].abs()
+    st, got = run_chunk(c)
+    assert st == 0
+    first = max(0, at - 50)     # the row of the first token that sees it
+    if pool == "v":
+        assert torch.isnan(got[first:100, 2:, 7]).all()
+        got[first:100, 2:, 7] = want[first:100, 2:, 7]
+    else:
+        assert torch.isnan(got[first:100, 2:]).all()
+        got[first:100, 2:] = want[first:100, 2:]
+    assert same_bits(got, want)
+
+
+def test_chunk_bad_lengths_and_blocks():
+    """The refusals on the device of kara_chunk_attention."""
+    kara = lib()
+    c = chunk_case(61, [100, 90, 80, 70], [10, 20, 30, 5], 4, 2, 64)
+    want = run_chunk(c)[1]
+    for L in (19, BS * c["bt"].shape[1] + 1):
+        bad = dict(c, lengths=c["lengths"].copy())
+        bad["lengths"][1] = L
+        st, got = run_chunk(bad)
+        assert st == kara.EINVAL and (got[10:30] == 0).all()
+        assert same_bits(got[:10], want[:10]) and same_bits(got[30:], want[30:])
+    for bid in (-1, c["k"].shape[1]):
+        bad = dict(c, bt=c["bt"].copy())
+        bad["bt"][2, 1] = bid
+        st, got = run_chunk(bad)
+        assert st == kara.EBADBLOCK and same_bits(got, run_chunk(bad, bf16=True)[1])
+    for qs in ([0, 10, 5, 60, 65], [0, 10, 30, 60, 900], [-3, 10, 30, 60, 65]):
+        assert run_chunk(dict(c, q_start=np.array(qs, np.int32)))[0] == kara.EINVAL
+
+
+def test_chunk_nothing_to_do_and_strided_pools():
+    c = chunk_case(71, [50, 60], [0, 0], 4, 2, 64, pad=4)
+    st, got = run_chunk(c)
+    assert st == 0 and (got == 77.0).all()
+    c = chunk_case(41, [300, 77], [50, 77], 8, 2, 128, layers=2)
+    L, nb, hkv, _, D = c["k"].shape
+    big = [torch.full((L + 1, nb, hkv + 3, BS, D), 0x7f, dtype=torch.uint8, device=DEV) for _ in range(2)]
+    k, v = (x[:L, :, 1:1 + hkv] for x in big)
+    k.copy_(c["k"]), v.copy_(c["v"])
+    for layer in (0, 1):
+        st, got = run_chunk(c, layer, pools=[k, v, c["ks"].to(DEV), c["vs"].to(DEV)])
+        assert st == 0 and same_bits(got, run_chunk(c, layer, bf16=True)[1])
+
+
+@pytest.mark.parametrize("lengths,n_new,hq,hkv,d", [
+    ([4096 + 512] * 12, [512] * 12, 8, 4, 128), ([700 + 3 * i for i in range(200)], [1 + i % 5 for i in range(200)], 4, 2, 64),
+    ([3000, 20, 9000], [2900, 20, 40], 8, 2, 128), ([40] * 1500, [2] * 1500, 4, 2, 128)])
+def test_chunk_large_calls(lengths, n_new, hq, hkv, d):
+    """Whole items dealt round, many sequences, partials that are joined, several times over: the same bits."""
+    c = chunk_case(len(lengths), lengths, n_new, hq, hkv, d)
+    want = run_chunk(c, bf16=True)[1]
+    for _ in range(3):
+        st, got = run_chunk(c)
+        assert st == 0 and same_bits(got, want)
+
+
+# ---- bounded waits --------------------------------------------------------------
+
+def test_stalled_attention_times_out(monkeypatch):
+    """With copies that are never issued both attentions report KARA_ETIMEOUT, and the next call is right."""
+    kara = lib()
+    dc = decode_case(3, [600, 40], 8, 2, 128)
+    cc = chunk_case(5, [300, 500], [200, 3], 8, 2, 128)
+    want = run_chunk(cc)[1]
+    monkeypatch.setenv("KARA_DEBUG_STALL", "1")
+    assert run_decode(*dc)[0] == kara.ETIMEOUT
+    assert run_chunk(cc)[0] == kara.ETIMEOUT
+    monkeypatch.delenv("KARA_DEBUG_STALL")
+    st, out = run_decode(*dc)
+    assert st == 0
+    check_decode(out, *dc)
+    st, got = run_chunk(cc)
+    assert st == 0 and same_bits(got, want)
 
 
 # ---- expand and compact ---------------------------------------------------------
