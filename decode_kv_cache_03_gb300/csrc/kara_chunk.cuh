@@ -82,8 +82,10 @@ using namespace ptx;
 constexpr int kTile = 128;       // rows of a query tile, keys of a key tile
 constexpr int kBlk = 16;         // tokens per cache block (the supported block size)
 constexpr int kBlkPerTile = kTile / kBlk;
-// (kStages, the tiles of K and V that the ring holds, is the including source's, and kEdges.)
-constexpr int kRaw8 = 2;         // tiles of codes of an 8-bit cache in flight, of K and of V each
+// (kStages, the bf16 tiles of K and V, or of V alone, that the ring holds, is the including source's, and kEdges.)
+constexpr int kK8 = 3;           // of an 8-bit cache: tiles of K's codes in flight,
+constexpr int kRaw8 = 2;         // and of V's
+constexpr int kScales8 = 8;      // K tiles whose scales are kept: the warps that read them are not this far behind
 constexpr int kMaxCtas = 160;    // CTAs of the attention kernel, at most (workspace slots)
 constexpr int kMaxRounds = 64;   // whole items that a CTA takes ahead of its range, at most
 constexpr int kThreads = 512;    // two softmax warpgroups, two control warpgroups
@@ -136,7 +138,8 @@ struct ChunkArgs {
     float4 *part;        // [2 * ctas][D / 4][256]
     float2 *stat;        // [2 * ctas][256]: (max, sum) in the log2 domain
     const uint16_t *v;   // V pool at the call's layer
-    const uint8_t *v8;   // or, of the 8-bit cache, its codes,
+    const uint16_t *q;   // of the 8-bit cache: the queries,
+    const uint8_t *v8;   // V's codes
     const float *k_scale, *v_scale;  // and K's and V's scales [num_blocks][hkv]
     int64_t block_stride, head_stride;
     int32_t wide;        // out is 32-byte aligned
@@ -216,22 +219,25 @@ struct Shared {
     };
 };
 
-// The same of the 8-bit cache, beside it: tiles of codes (K's, then V's, each by their number mod
-// kRaw8) and their blocks' scales.
+// The same of the 8-bit cache, beside it.
 struct Shared8 {
-    uint64_t full[2 * kRaw8], empty[2 * kRaw8];
-    float scale[2 * kRaw8][kBlkPerTile];
+    uint64_t kfull[kK8], kempty[kK8];      // tiles of K's codes
+    uint64_t rfull[kRaw8], rempty[kRaw8];  // tiles of V's codes, which become bf16 tiles of the ring
+    float vscale[kRaw8][kBlkPerTile], kscale[kScales8][kBlkPerTile];
+    // of each row of the query tiles, by the piece's number mod 2: the next piece's are written as soon as this
+    // one's last logits are there, and read for its first; those of the one after only behind the next one's logits
+    float qscale[2][2][kTile];
 };
 
+// Shared memory: query tiles, the ring, (8 bits: K's codes, V's codes,) barriers and tables.
 template <int D, bool E8>
 struct Cfg {
     static constexpr int kHalves = D / 64;
     static constexpr int kHalfBytes = kTile * 128;            // 128 rows of 64 dims
-    static constexpr int kTileBytes = kHalves * kHalfBytes;
+    static constexpr int kTileBytes = kHalves * kHalfBytes;   // (8 bits: a query tile is two tiles of codes)
     static constexpr int kRawBytes = kTile * D;               // a tile of codes
-    static constexpr size_t kRawAll = E8 ? (size_t)2 * kRaw8 * kRawBytes : 0;
-    static constexpr size_t kSmem = 1024 + (size_t)(2 + kStages) * kTileBytes + kRawAll + sizeof(Shared) +
-                                    (E8 ? sizeof(Shared8) : 0);
+    static constexpr int kRingBytes = kStages * kTileBytes + (E8 ? (kK8 + kRaw8) * kRawBytes : 0);
+    static constexpr size_t kSmem = 1024 + 2 * kTileBytes + kRingBytes + sizeof(Shared) + (E8 ? sizeof(Shared8) : 0);
 };
 
 // Bounded wait on phase `parity` of `bar`: gives up after wait_ns, or once another
@@ -320,6 +326,37 @@ __device__ __forceinline__ void mma_ss(uint32_t d_tmem, uint32_t alo, uint32_t h
         : "memory");
 }
 
+// The same with e4m3 operands.
+__device__ __forceinline__ void mma_ss_e4m3(uint32_t d_tmem, uint32_t alo, uint32_t ahi, uint32_t blo, uint32_t bhi,
+                                            uint32_t idesc, uint32_t accumulate)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\tmov.b64 a, {%1, %2};\n\tmov.b64 b, {%3, %4};\n\t"
+        "setp.ne.b32 p, %6, 0;\n\ttcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %5, p;\n\t}" ::"r"(d_tmem),
+        "r"(alo), "r"(ahi), "r"(blo), "r"(bhi), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+// Instruction descriptor: kind::f8f6f4 with e4m3 A and B, fp32 D, both K-major.
+__host__ __device__ constexpr uint32_t idesc_e4m3(int M, int N)
+{
+    return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+
+// Descriptor of a K-major operand of codes, rows of D bytes swizzled by their size (128 or 64 bytes), groups of
+// eight rows one after another.
+template <int D>
+__device__ __forceinline__ uint64_t sdesc_codes(uint32_t saddr)
+{
+    uint64_t d = 0;
+    d |= (uint64_t)((saddr & 0x3FFFFu) >> 4);
+    d |= (uint64_t)1 << 16;
+    d |= (uint64_t)(8 * D >> 4) << 32;
+    d |= (uint64_t)1 << 46;
+    d |= (uint64_t)(D == 128 ? 2 : 4) << 61;
+    return d;
+}
+
 __device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint32_t blo, uint32_t bhi, uint32_t idesc,
                                        uint32_t accumulate)
 {
@@ -388,6 +425,13 @@ __device__ __forceinline__ void tmem_wait_ld32(uint32_t (&v)[N], const int o)
                  :
                  : "memory");
     asm volatile("" : "+r"(v[o + 30]), "+r"(v[o + 31]) : : "memory");
+}
+
+__device__ __forceinline__ float ld_shared(uint32_t addr)
+{
+    float x;
+    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(x) : "r"(addr));
+    return x;
 }
 
 // (lo, hi) rounded to nearest-even bf16, lo in the low half.
@@ -748,27 +792,82 @@ __device__ __noinline__ void add_cleared(const ChunkArgs &a, int seq, int head, 
     }
 }
 
-// The query tiles of a piece; one thread issues.
-template <int D, bool E8>
-__device__ __forceinline__ void load_queries(const Piece &p, uint8_t *qbuf, const CUtensorMap *qmap, int qrows, Shared *sh,
-                                             const ChunkArgs &a)
+// ---- the 8-bit cache ------------------------------------------------------------------
+// K's codes are an operand of the tensor cores as they are, if the queries are codes too.  A bf16
+// value has eight significant bits and a code four: with q' = q 2^k, the row's largest within (224, 448],
+//     q' = hi + lo,   hi = rn(q'),  lo = rn(q' - hi)
+// exactly while |q'| >= 1/4, and 2^-10 off at most below (2^-17 of the row's largest, or 2^-50).  The logits are then
+// Q_hi K^T + Q_lo K^T, at twice the rate of bf16 operands, so in the same time; 2^-k and K's scales multiply them
+// in the softmax, where the factor log2(e) / sqrt(D) is anyway.
+// V's codes become bf16 tiles (code times scale is exact) of the ring, as its scales belong to the
+// summed dimension: put into weights, they would need weights in 8 bits, or another two terms.
+
+// Rows [32 w, 32 w + 32) of each query tile of a piece as two tiles of codes, and their 2^-k.
+template <int D>
+__device__ __forceinline__ void split_queries(const Piece &p, int w, uint8_t *qbuf, float (*qscale)[kTile],
+                                              const ChunkArgs &a)
 {
-    using C = Cfg<D, E8>;
+    constexpr int LPR = D / 8, RPP = 32 / LPR, kTerm = kTile * D;
+    const int lane = threadIdx.x & 31, l = lane % LPR;
     const int tiles = p.it.ntok > a.TQ ? 2 : 1;
-    const uint32_t fb = smem_u32(&sh->q_full);
-    mbar_arrive_expect_tx(fb, tiles * C::kHalves * qrows * 128);
-    for (int x = 0; x < tiles; ++x)
+#pragma unroll 1
+    for (int x = 0; x < tiles; ++x) {
+        uint8_t *hi = qbuf + x * 2 * kTerm, *lo = hi + kTerm;
+#pragma unroll 1
+        for (int r0 = w * 32; r0 < w * 32 + 32; r0 += 2 * RPP) {
+            uint4 u[2];
 #pragma unroll
-        for (int h = 0; h < C::kHalves; ++h)
-            asm volatile(
-                "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
-                "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_u32(qbuf + x * C::kTileBytes + h * C::kHalfBytes)),
-                "l"(reinterpret_cast<uint64_t>(qmap)), "r"(h * 64), "r"(p.head * a.G), "r"(p.it.row0 + x * a.TQ),
-                "r"(fb)
-                : "memory");
+            for (int i = 0; i < 2; ++i) {
+                const int r = r0 + i * RPP + lane / LPR, tok = r / a.G, t = x * a.TQ + tok;
+                u[i] = make_uint4(0, 0, 0, 0);
+                if (tok < a.TQ && t < p.it.ntok)
+                    u[i] = *reinterpret_cast<const uint4 *>(
+                        a.q + ((int64_t)(p.it.row0 + t) * a.hq + p.head * a.G + r - tok * a.G) * D + l * 8);
+            }
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int r = r0 + i * RPP + lane / LPR;
+                const uint32_t v[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
+                // the largest finite magnitude, as bits: of 16-bit patterns below 0x7f80
+                uint32_t top = 0;
+                bool odd = false;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const uint32_t m0 = v[e] & 0x7fffu, m1 = v[e] >> 16 & 0x7fffu;
+                    if (m0 < 0x7f80u) top = max(top, m0); else odd = true;
+                    if (m1 < 0x7f80u) top = max(top, m1); else odd = true;
+                }
+#pragma unroll
+                for (int o = LPR / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+                // the exponent of q' is 8 for mantissas up to 1.75 (448), 7 above; 2^-k at least 2^-40, so that
+                // times the smallest scale it is no 0 (which a masked logit's infinity would turn to NaN)
+                const int down = min(max((int)((top + 0x1fu) >> 7) - 8, 127 - 40), 253);
+                const float f = __uint_as_float((uint32_t)(254 - down) << 23);
+                if (l == 0) qscale[x][r] = __uint_as_float((uint32_t)down << 23);
+                uint32_t h[2] = {0u, 0u}, g[2] = {0u, 0u};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    float q0 = __uint_as_float(v[e] << 16) * f, q1 = __uint_as_float(v[e] & 0xffff0000u) * f;
+                    if (odd) {  // NaN for what is not finite: the row's logits are
+                        if (!finite(q0)) q0 = __uint_as_float(0x7fffffffu);
+                        if (!finite(q1)) q1 = __uint_as_float(0x7fffffffu);
+                    }
+                    const uint32_t c = e4m3x2(q0, q1);
+                    float c0, c1;
+                    f32_of_f16x2(f16_of_e4m3x2(c), c0, c1);
+                    h[e >> 1] |= c << (16 * (e & 1));
+                    g[e >> 1] |= e4m3x2(q0 - c0, q1 - c1) << (16 * (e & 1));
+                }
+                // eight codes of chunk l / 2 of the row, swizzled by the rows' size
+                const int sw = D == 128 ? r & 7 : r >> 1 & 3;
+                const int at = r * D + (((l >> 1) ^ sw) << 4) + (l & 1) * 8;
+                *reinterpret_cast<uint2 *>(hi + at) = make_uint2(h[0], h[1]);
+                *reinterpret_cast<uint2 *>(lo + at) = make_uint2(g[0], g[1]);
+            }
+        }
+    }
 }
 
-// ---- the 8-bit cache: codes to bf16 tiles -------------------------------------------
 // Two codes (bytes 2e and 2e + 1 of w) as bf16 of their values times 2^-120: sign-extended to 16 bits
 // and moved up by four, the exponent and mantissa bits are where bf16 has them, and the
 // exponent's upper bits are cleared.
@@ -879,82 +978,56 @@ __device__ __noinline__ bool convert_odd_block(const uint8_t *raw, uint8_t *tile
     return found;
 }
 
-// Warps 12 to 15: a tile of codes at a time (K, V, K, ...; two blocks of it a warp) becomes a bf16 tile
-// of the ring, with what rows must not see cleared on the way.  The first of them loads the query tiles,
-// whenever the last ones are done with while it waits for something else: a tile it waits for may
-// depend on them.
+// Warps 12 to 15: a piece's queries (a quarter of their rows each), then its V tiles (two blocks each), with
+// what rows must not see cleared on the way.
 template <int D>
 __device__ __forceinline__ void convert_tiles(int cw, uint8_t *qbuf, uint8_t *ring, const uint8_t *raw, Shared *sh,
-                                              Shared8 *sh8, const CUtensorMap *qmap, int qrows, const ChunkArgs &a)
+                                              Shared8 *sh8, const ChunkArgs &a)
 {
     using C = Cfg<D, true>;
     const int lane = threadIdx.x & 31;
     const LaneChunk<D> lc(lane);
     Piece p;
-    uint32_t np = 0, nq = 0, k = 0;   // pieces, query tiles issued, key tiles
-    uint32_t st = 0, ph = 1;          // the next stage of the ring and the phase that frees it
-    bool ok = true, due = false;      // due: the piece's queries are not issued yet
-    const auto queries = [&]() {
-        if (due && __all_sync(0xffffffffu, mbar_try_wait(smem_u32(&sh->q_empty), (nq & 1) ^ 1))) {
-            if (lane == 0) load_queries<D, true>(p, qbuf, qmap, qrows, sh, a);
-            __syncwarp();
-            ++nq;
-            due = false;
-        }
-    };
-    // in small steps while queries are due, else like the other control warps
+    uint32_t np = 0, k = 0;   // pieces, V tiles
+    uint32_t st = 0, ph = 1;  // the next stage of the ring and the phase that frees it
+    bool ok = true;
     const auto wait = [&](uint32_t bar, uint32_t parity) {
-        uint64_t t0 = 0;
-        while (due) {
-            if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
-            queries();
-            const uint64_t now = globaltimer();
-            if (t0 == 0) t0 = now;
-            if (__any_sync(0xffffffffu, now - t0 > a.wait_ns)) break;  // kwait gives the verdict
-        }
         return __all_sync(0xffffffffu, kwait<20>(bar, parity, sh, a)) != 0;
     };
-    for (; ok && !a.stall; ++np) {
-        if (due) {
-            ok = wait(smem_u32(&sh->q_empty), (nq & 1) ^ 1);
-            if (ok) queries();
-            if (due) break;
-        }
-        if (!next_piece<true>(p, np, sh, ok, lane, wait)) break;
-        due = cw == 0;
-        queries();
-        for (int j = p.j0; ok && j < p.j1; ++j, ++k) {
+    for (; ok && !a.stall && next_piece<true>(p, np, sh, ok, lane, wait); ++np) {
+        ok = wait(smem_u32(&sh->q_empty), (np & 1) ^ 1);
+        if (!ok) break;
+        split_queries<D>(p, cw, qbuf, sh8->qscale[np & 1], a);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&sh->q_full));
+        for (int j = p.j0; j < p.j1; ++j, ++k) {
+            const uint32_t r = k % kRaw8;
+            ok = wait(smem_u32(&sh8->rfull[r]), k / kRaw8 & 1) && wait(smem_u32(&sh->empty[st]), ph);
+            if (!ok) break;
+            // rows from `end` on: past the sequence; from `clear` on: not seen by every row of the item
+            const int end = p.it.len - j * kTile, clear = p.it.pos0 + 1 - j * kTile;
+            bool found = false;
 #pragma unroll 1
-            for (int kv = 0; kv < 2; ++kv) {
-                const uint32_t r = kv * kRaw8 + k % kRaw8;
-                ok = wait(smem_u32(&sh8->full[r]), k / kRaw8 & 1) && wait(smem_u32(&sh->empty[st]), ph);
-                if (!ok) break;
-                // rows from `end` on: past the sequence; from `clear` on: not seen by every row of the item
-                const int end = kv ? p.it.len - j * kTile : kTile, clear = kv ? p.it.pos0 + 1 - j * kTile : kTile;
-                bool found = false;
-#pragma unroll 1
-                for (int b = 2 * cw; b < 2 * cw + 2; ++b) {
-                    const float s = sh8->scale[r][b];
-                    const uint8_t *src = raw + r * C::kRawBytes + b * kBlk * D;
-                    uint8_t *dst = ring + st * C::kTileBytes + b * kBlk * 128;
-                    if (__builtin_expect(__float_as_uint(s) <= 0x43000000u && end >= (b + 1) * kBlk, 1))
-                        convert_block<D>(src, dst, s, lc);
-                    else
-                        found = convert_odd_block<D>(src, dst, end - b * kBlk, clear - b * kBlk, s, lane) || found;
-                }
-                if (found) sh->odd_values[np % kOddSlots] = (int32_t)np + 1;
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(smem_u32(&sh->full[st]));
-                    mbar_arrive(smem_u32(&sh8->empty[r]));
-                }
-                if (++st == kStages) st = 0, ph ^= 1;
+            for (int b = 2 * cw; b < 2 * cw + 2; ++b) {
+                const float s = sh8->vscale[r][b];
+                const uint8_t *src = raw + r * C::kRawBytes + b * kBlk * D;
+                uint8_t *dst = ring + st * C::kTileBytes + b * kBlk * 128;
+                if (__builtin_expect(__float_as_uint(s) <= 0x43000000u && end >= (b + 1) * kBlk, 1))
+                    convert_block<D>(src, dst, s, lc);
+                else
+                    found = convert_odd_block<D>(src, dst, end - b * kBlk, clear - b * kBlk, s, lane) || found;
             }
+            if (found) sh->odd_values[np % kOddSlots] = (int32_t)np + 1;
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(smem_u32(&sh->full[st]));
+                mbar_arrive(smem_u32(&sh8->rempty[r]));
+            }
+            if (++st == kStages) st = 0, ph ^= 1;
         }
     }
-    // the last query tiles have landed too
-    if (cw == 0 && nq > 0) drain(smem_u32(&sh->q_full), (nq - 1) & 1);
 }
 
 // Records the sequences whose rows or lengths are out of order and zeroes their rows.
@@ -984,33 +1057,45 @@ __device__ __noinline__ void refuse_sequences(const ChunkArgs &a)
 // softmax warps every instruction between two MMAs counts, and every line of the
 // instruction caches.
 template <int D, bool E8>
-__device__ __forceinline__ void mma_warp(int x, uint32_t qbuf, uint32_t ring, Shared *sh, const ChunkArgs &a)
+__device__ __forceinline__ void mma_warp(int x, uint32_t qbuf, uint32_t ring, Shared *sh, Shared8 *sh8, const ChunkArgs &a)
 {
     using C = Cfg<D, E8>;
     if (elect_one()) {
-        constexpr uint32_t id_qk = idesc_bf16(kTile, kTile);
+        constexpr uint32_t id_qk = E8 ? idesc_e4m3(kTile, kTile) : idesc_bf16(kTile, kTile);
         constexpr uint32_t id_pv = idesc_bf16(kTile, D) | (1u << 16);  // V: its dims are contiguous
         constexpr uint32_t kTileDesc = C::kTileBytes >> 4, kHalfDesc = C::kHalfBytes >> 4;
         const uint32_t ts = x * kTile, to = 256 + x * 128;         // S (and P over it), O in TMEM
-        const uint64_t qd = sdesc_sw128(qbuf), kd = sdesc_sw128(ring), vd = sdesc_sw128_mn(ring, C::kHalfBytes);
+        const uint32_t kring = E8 ? ring + kStages * C::kTileBytes : ring;
+        const uint64_t qd = E8 ? sdesc_codes<D>(qbuf) : sdesc_sw128(qbuf);
+        const uint64_t kd = E8 ? sdesc_codes<D>(kring) : sdesc_sw128(kring), vd = sdesc_sw128_mn(ring, C::kHalfBytes);
+        constexpr uint32_t kKeyDesc = E8 ? C::kRawBytes >> 4 : kTileDesc;
         const uint32_t full0 = smem_u32(&sh->full[0]), empty0 = smem_u32(&sh->empty[0]);
+        // K's tiles share the ring with V's, or have one of their own
+        const uint32_t kfull0 = E8 ? smem_u32(&sh8->kfull[0]) : full0, kempty0 = E8 ? smem_u32(&sh8->kempty[0]) : empty0;
         const uint32_t sf = smem_u32(&sh->s_full[x]), pf = smem_u32(&sh->p_full[x]), ph = smem_u32(&sh->p_half[x]);
         const uint32_t pv = smem_u32(&sh->pv[x]), mine = smem_u32(&sh->turn[x]), other = smem_u32(&sh->turn[1 - x]);
         Piece p;
         const auto wait = [&](uint32_t bar, uint32_t parity) { return kwait(bar, parity, sh, a); };
         uint32_t np = 0;
-        uint32_t ks = 0, kp = 0, vs = 1, vp = 0;  // next K and V tile: stage, phase
+        uint32_t ks = 0, kp = 0, vs = E8 ? 0 : 1, vp = 0;  // next K and V tile: stage, phase
         uint32_t pp = 0, turn = 1 - x, iq = 0;    // phases of the next weights, turn, query tiles
         uint32_t sums = 0;                        // weighted sums issued
         bool ok = true;
-        auto next = [](uint32_t &st, uint32_t &ph) {  // a tile further (K and V alternate)
-            st += 2;
-            if (st >= kStages) st -= kStages, ph ^= 1;
+        auto next = [](uint32_t &st, uint32_t &ph, int stages) {  // a tile further (K and V alternate)
+            st += E8 ? 1 : 2;
+            if (st >= stages) st -= stages, ph ^= 1;
         };
-        auto skip = [&](uint32_t &st, uint32_t &ph) {
-            ok = ok && kwait(full0 + st * 8, ph, sh, a);
-            if (ok) mbar_arrive(empty0 + st * 8);
-            next(st, ph);
+        auto next_k = [&]() { next(ks, kp, E8 ? kK8 : kStages); };
+        auto next_v = [&]() { next(vs, vp, kStages); };
+        auto skip_k = [&]() {
+            ok = ok && kwait(kfull0 + ks * 8, kp, sh, a);
+            if (ok) mbar_arrive(kempty0 + ks * 8);
+            next_k();
+        };
+        auto skip_v = [&]() {
+            ok = ok && kwait(full0 + vs * 8, vp, sh, a);
+            if (ok) mbar_arrive(empty0 + vs * 8);
+            next_v();
         };
         while (ok && next_piece<false>(p, np, sh, ok, 0, wait)) {
             ++np;
@@ -1025,10 +1110,10 @@ __device__ __forceinline__ void mma_warp(int x, uint32_t qbuf, uint32_t ring, Sh
                 // weighted sum of tile t, then logits of tile t + by (a single query tile: its own
                 // tiles, between the other warp's)
                 const bool sum = t >= first && t <= last, logits = t + by <= last;
-                if (!two && x == 1 && t >= 0) skip(vs, vp);
+                if (!two && x == 1 && t >= 0) skip_v();
                 if (t >= first && t < n) {
                     ok = ok && kwait(full0 + vs * 8, vp, sh, a);
-                    if (two && ok && t + 1 < n) ok = kwait(full0 + ks * 8, kp, sh, a);
+                    if (two && ok && t + 1 < n) ok = kwait(kfull0 + ks * 8, kp, sh, a);
                     if (two && ok) ok = kwait(mine, turn, sh, a);
                     if (ok && sum) ok = kwait(ph, pp, sh, a);
                     if (!ok) break;
@@ -1054,22 +1139,29 @@ __device__ __forceinline__ void mma_warp(int x, uint32_t qbuf, uint32_t ring, Sh
                     }
                 }
                 const uint32_t v_done = empty0 + vs * 8;
-                if (t >= first && t < n) next(vs, vp);
-                if (!two && x == 0 && t >= 0 && t + 1 < n) skip(vs, vp);
-                if (!two && x == 1 && t + 1 < n) skip(ks, kp);
+                if (t >= first && t < n) next_v();
+                if (!two && x == 0 && t >= 0 && t + 1 < n) skip_v();
+                if (!two && x == 1 && t + 1 < n) skip_k();
                 if (t + by < n) {
-                    if (!two || t < first) ok = ok && kwait(full0 + ks * 8, kp, sh, a);
+                    if (!two || t < first) ok = ok && kwait(kfull0 + ks * 8, kp, sh, a);
                     if (!ok) break;
                     if (logits) {
                         // they go where the weights are: only once the sum of those is done
                         if (sums > 0) ok = kwait(pv, (sums - 1) & 1, sh, a);
                         if (!ok) break;
                         tc_fence_after();
-                        const uint32_t lo = (uint32_t)kd + ks * kTileDesc;
+                        const uint32_t lo = (uint32_t)kd + ks * kKeyDesc;
+                        if constexpr (E8) {
+#pragma unroll
+                            for (int e = 0; e < D / 16; ++e)  // 32 dims of the first term, then of the second
+                                mma_ss_e4m3(ts, ql + ((e & 1) * kKeyDesc + (e >> 1) * 2), (uint32_t)(qd >> 32),
+                                            lo + (e >> 1) * 2, (uint32_t)(kd >> 32), id_qk, e > 0);
+                        } else {
 #pragma unroll
                         for (int e = 0; e < D / 16; ++e)
                             mma_ss(ts, ql + ((e >> 2) * kHalfDesc + (e & 3) * 2), (uint32_t)(qd >> 32),
                                    lo + ((e >> 2) * kHalfDesc + (e & 3) * 2), id_qk, e > 0);
+                        }
                     }
                 }
                 if (two && t >= first) {
@@ -1079,17 +1171,17 @@ __device__ __forceinline__ void mma_warp(int x, uint32_t qbuf, uint32_t ring, Sh
                 if (t + by < n) {
                     if (logits) {
                         mma_commit(sf);
-                        mma_commit(empty0 + ks * 8);
+                        mma_commit(kempty0 + ks * 8);
                         if (t + by == last) mma_commit(smem_u32(&sh->q_empty));
                     } else {
-                        mbar_arrive(empty0 + ks * 8);
+                        mbar_arrive(kempty0 + ks * 8);
                     }
-                    next(ks, kp);
+                    next_k();
                 }
                 if (two && sum) mma_commit(v_done);
-                if (!two && x == 0 && t + by + 1 < n) skip(ks, kp);
+                if (!two && x == 0 && t + by + 1 < n) skip_k();
             }
-            if (!two && x == 1 && ok && n % 2) skip(vs, vp);
+            if (!two && x == 1 && ok && n % 2) skip_v();
         }
         // the tensor cores are idle before TMEM and shared memory go
         mma_commit(smem_u32(&sh->done[x]));
@@ -1107,8 +1199,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     extern __shared__ uint8_t csm_raw[];
     uint8_t *qbuf = csm_raw + ((1024u - (smem_u32(csm_raw) & 1023u)) & 1023u);  // two query tiles
     uint8_t *ring = qbuf + 2 * C::kTileBytes;
-    uint8_t *raw = ring + kStages * C::kTileBytes;
-    Shared *sh = reinterpret_cast<Shared *>(raw + C::kRawAll);
+    Shared *sh = reinterpret_cast<Shared *>(ring + C::kRingBytes);
     Shared8 *sh8 = reinterpret_cast<Shared8 *>(sh + 1);  // (of the 8-bit cache)
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
@@ -1117,15 +1208,19 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(smem_u32(&sh->full[i]), E8 ? 4 : 1);  // 4: the warps that convert it
             mbar_init(smem_u32(&sh->empty[i]), 2);
         }
-        for (int i = 0; E8 && i < 2 * kRaw8; ++i) {
-            mbar_init(smem_u32(&sh8->full[i]), 1);
-            mbar_init(smem_u32(&sh8->empty[i]), 4);
+        for (int i = 0; E8 && i < kK8; ++i) {
+            mbar_init(smem_u32(&sh8->kfull[i]), 1);
+            mbar_init(smem_u32(&sh8->kempty[i]), 2);
+        }
+        for (int i = 0; E8 && i < kRaw8; ++i) {
+            mbar_init(smem_u32(&sh8->rfull[i]), 1);
+            mbar_init(smem_u32(&sh8->rempty[i]), 4);
         }
         for (int i = 0; i < kPieces; ++i) {
             mbar_init(smem_u32(&sh->piece_full[i]), 1);
             mbar_init(smem_u32(&sh->piece_empty[i]), kPieceReaders);
         }
-        mbar_init(smem_u32(&sh->q_full), 1);
+        mbar_init(smem_u32(&sh->q_full), E8 ? 4 : 1);
         mbar_init(smem_u32(&sh->q_empty), 2);
         for (int x = 0; x < 2; ++x) {
             mbar_init(smem_u32(&sh->s_full[x]), 1);
@@ -1149,7 +1244,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     // rows of the query tiles past G * TQ are never filled: zeros
     const int qrows = a.G * a.TQ;
-    for (int i = tid; i < (kTile - qrows) * 8 * 2 * C::kHalves; i += kThreads) {
+    for (int i = tid; !E8 && i < (kTile - qrows) * 8 * 2 * C::kHalves; i += kThreads) {
         const int b = i / ((kTile - qrows) * 8), r = i % ((kTile - qrows) * 8);
         reinterpret_cast<uint4 *>(qbuf + b * C::kHalfBytes + qrows * 128)[r] = make_uint4(0, 0, 0, 0);
     }
@@ -1165,7 +1260,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     if (blockIdx.x == gridDim.x - 1) refuse_sequences(a);
-    share_out(a, sh, reinterpret_cast<int32_t *>(ring), kStages * C::kTileBytes / 4);
+    share_out(a, sh, reinterpret_cast<int32_t *>(ring), C::kRingBytes / 4);
 
     if (warp >= 8) {
         reg_dealloc<Regs<E8>::kCtl>();
@@ -1181,7 +1276,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 return __all_sync(0xffffffffu, kwait(bar, parity, sh, a));
             };
             uint32_t np = 0;
-            uint32_t st = kv, ph = 1, k = 0;  // stage and the phase that frees it; tiles issued
+            uint32_t st = E8 ? 0 : kv, ph = 1, k = 0;  // stage and the phase that frees it; tiles issued
             uint32_t ne = 0, were_edges = 0;  // edge tiles issued; which of the last tiles were
             const int b = lane % kBlkPerTile, h = lane / kBlkPerTile;
             const bool mine = E8 ? h == 0 : h < C::kHalves;
@@ -1219,6 +1314,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 };
                 if constexpr (E8) {
                     // a tile of codes and its blocks' scales; ids are looked up two tiles ahead, scales one
+                    const int stages = kv ? kRaw8 : kK8;
+                    uint8_t *codes = ring + kStages * C::kTileBytes + kv * kK8 * C::kRawBytes;
                     const float *scales = (kv ? a.v_scale : a.k_scale) + p.head;
                     const auto scale = [&](int32_t id) {
                         return id < a.num_blocks ? scales[(int64_t)id * a.hkv] : 0.f;
@@ -1226,18 +1323,24 @@ __global__ void __launch_bounds__(kThreads, 1)
                     int32_t id = block_id(p.j0), next_id = p.j0 + 1 < p.j1 ? block_id(p.j0 + 1) : a.num_blocks;
                     float sc = scale(id);
                     for (int j = p.j0; j < p.j1; ++j) {
-                        const uint32_t r = kv * kRaw8 + k % kRaw8, fb = smem_u32(&sh8->full[r]);
-                        ok = __all_sync(0xffffffffu, kwait(smem_u32(&sh8->empty[r]), (k / kRaw8 & 1) ^ 1, sh, a));
+                        const uint32_t fb = smem_u32((kv ? sh8->rfull : sh8->kfull) + st);
+                        ok = __all_sync(0xffffffffu, kwait(smem_u32((kv ? sh8->rempty : sh8->kempty) + st), ph, sh, a));
                         if (!ok) break;
-                        if (mine) sh8->scale[r][b] = sc;
+                        if (mine) {
+                            // (K: codes of zeros alone are what they are at any scale, and 0 times a masked
+                            // logit's infinity is none)
+                            if (kv) sh8->vscale[st][b] = sc;
+                            else sh8->kscale[k % kScales8][b] = sc == 0.f ? 1.f : fabsf(sc);
+                        }
                         __syncwarp();
                         if (lane == 0) mbar_arrive_expect_tx(fb, C::kRawBytes);
                         __syncwarp();
                         if (mine)
-                            tma_load_5d(smem_u32(raw + r * C::kRawBytes + b * kBlk * D), map, fb, 0, 0, p.head, id,
+                            tma_load_5d(smem_u32(codes + st * C::kRawBytes + b * kBlk * D), map, fb, 0, 0, p.head, id,
                                         a.layer);
                         ++k;
                         if (kv == 0 && lane == 0) *(volatile uint32_t *)&sh->loaded = k;
+                        if (++st == stages) st = 0, ph ^= 1;
                         id = next_id;
                         sc = scale(id);
                         if (j + 2 < p.j1) next_id = block_id(j + 2);
@@ -1267,9 +1370,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (lane == 0) sh->issued[kv] = make_int4((int)k, (int)ne, (int)were_edges, 0);
         } else if (warp == kWarpMma || warp == kWarpMma + 1) {
-            mma_warp<D, E8>(warp - kWarpMma, smem_u32(qbuf), smem_u32(ring), sh, a);
+            mma_warp<D, E8>(warp - kWarpMma, smem_u32(qbuf), smem_u32(ring), sh, sh8, a);
         } else if constexpr (E8) {
-            convert_tiles<D>(warp - kWarpQ, qbuf, ring, raw, sh, sh8, &qmap, qrows, a);
+            convert_tiles<D>(warp - kWarpQ, qbuf, ring, ring + kStages * C::kTileBytes + kK8 * C::kRawBytes, sh, sh8, a);
         } else {
             // ---------------- query tiles (warp 12), and the edge tiles of V (warps 12-15, a
             // quarter of the rows each: the products wait for them)
@@ -1283,7 +1386,21 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (warp == kWarpQ) {
                     ok = __all_sync(0xffffffffu, kwait<200>(smem_u32(&sh->q_empty), (np & 1) ^ 1, sh, a));
                     if (!ok) break;
-                    if (lane == 0) load_queries<D, E8>(p, qbuf, &qmap, qrows, sh, a);
+                    if (lane == 0) {
+                        const int tiles = p.it.ntok > a.TQ ? 2 : 1;
+                        const uint32_t fb = smem_u32(&sh->q_full);
+                        mbar_arrive_expect_tx(fb, tiles * C::kHalves * qrows * 128);
+                        for (int x = 0; x < tiles; ++x)
+#pragma unroll
+                            for (int h = 0; h < C::kHalves; ++h)
+                                asm volatile(
+                                    "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+                                    "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
+                                        smem_u32(qbuf + x * C::kTileBytes + h * C::kHalfBytes)),
+                                    "l"(reinterpret_cast<uint64_t>(&qmap)), "r"(h * 64), "r"(p.head * a.G),
+                                    "r"(p.it.row0 + x * a.TQ), "r"(fb)
+                                    : "memory");
+                    }
                     __syncwarp();
                 }
                 for (int j = max(p.j0, (p.it.pos0 + 1) / kTile); ok && j < p.j1; ++j) {
@@ -1345,6 +1462,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             return __all_sync(0xffffffffu, cwait(bar, parity, sh, a));
         };
         uint32_t ns = 0, no = 0, nj = 0, np = 0;
+        uint32_t nk = 0;  // K tiles of the pieces before
         bool ok = true;
         for (; ok && next_piece<true>(p, np, sh, ok, lane, wait); ++np) {
             const bool two = p.it.ntok > a.TQ;
@@ -1355,6 +1473,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // a row without a token is computed like the others and dropped at the end
             const int32_t pos = live ? p.it.pos0 + t : 0x3fffffff;
             float m = -INFINITY, z = 0.f;
+            float scale2 = a.scale2;
             for (int i = 0; i < pt.cnt; ++i) {
                 const int j = pt.j + i * pt.by;
                 ok = cwait(smem_u32(&sh->s_full[x]), ns & 1, sh, a);
@@ -1374,13 +1493,33 @@ __global__ void __launch_bounds__(kThreads, 1)
                         for (int c = 0; c < kTile; ++c)
                             if (c > lim) s[c] = 0xff800000u;
                     }
-                    float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                    float mt;
+                    const uint32_t ks = smem_u32(sh8->kscale[(nk + j - p.j0) % kScales8]);
+                    if constexpr (E8) {
+                        // a block's keys have a scale of their own (read where it is used: registers are short)
+                        if (i == 0) scale2 = a.scale2 * sh8->qscale[np & 1][two ? x : 0][r];
+                        mt = -INFINITY;
 #pragma unroll
-                    for (int c = 0; c < kTile; c += 8)
+                        for (int b = 0; b < kBlkPerTile; ++b) {
+                            float mx[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            mx[e] = fmaxf(mx[e], fmaxf(__uint_as_float(s[c + 2 * e]), __uint_as_float(s[c + 2 * e + 1])));
-                    const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.scale2;
+                            for (int c = b * kBlk; c < b * kBlk + kBlk; c += 4)
+#pragma unroll
+                                for (int e = 0; e < 2; ++e)
+                                    mx[e] = fmaxf(mx[e], fmaxf(__uint_as_float(s[c + 2 * e]),
+                                                               __uint_as_float(s[c + 2 * e + 1])));
+                            mt = fmaxf(mt, fmaxf(mx[0], mx[1]) * ld_shared(ks + b * 4));
+                        }
+                        mt *= scale2;
+                    } else {
+                        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                        for (int c = 0; c < kTile; c += 8)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                mx[e] = fmaxf(mx[e], fmaxf(__uint_as_float(s[c + 2 * e]), __uint_as_float(s[c + 2 * e + 1])));
+                        mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.scale2;
+                    }
                     if (i == 0) {
                         m = mt;
                     } else {
@@ -1402,10 +1541,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                     }
                     const float ref = m == -INFINITY ? 0.f : m;  // a row that saw nothing yet: weights 2^-inf = 0
-                    const uint64_t sc = pack2(a.scale2, a.scale2), mr = pack2(-ref, -ref);
+                    uint64_t sc = pack2(scale2, scale2);
+                    const uint64_t mr = pack2(-ref, -ref);
                     uint64_t sum[2] = {0ull, 0ull};
 #pragma unroll
                     for (int c = 0; c < kTile; c += 2) {
+                        if (E8 && c % kBlk == 0) {
+                            const float f = scale2 * ld_shared(ks + c / kBlk * 4);
+                            sc = pack2(f, f);
+                        }
                         float lo, hi;
                         unpack2(fma2(pack2(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), sc, mr), lo, hi);
                         lo = ex2(lo);
@@ -1512,6 +1656,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                                     min(pos, p.j1 * kTile - 1), p.whole ? op : nullptr, pp);
                 if (live && !p.whole) a.stat[slot * 256 + rr] = make_float2(m, z);
             }
+            nk += p.j1 - p.j0;
             // the next piece's products write O again only after these reads
             tc_fence_before();
             if (joined) {
@@ -1527,9 +1672,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == kWarpMma) tmem_dealloc(sh->tmem, kTmemCols);
     if (warp == kWarpKv || warp == kWarpKv + 1) {
         if constexpr (E8) {
-            const uint32_t k = (uint32_t)sh->issued[warp - kWarpKv].x;
-            for (uint32_t i = k > kRaw8 ? k - kRaw8 : 0; i < k; ++i)
-                drain(smem_u32(&sh8->full[(warp - kWarpKv) * kRaw8 + i % kRaw8]), i / kRaw8 & 1);
+            const int kv = warp - kWarpKv;
+            const uint32_t k = (uint32_t)sh->issued[kv].x, stages = kv ? kRaw8 : kK8;
+            for (uint32_t i = k > stages ? k - stages : 0; i < k; ++i)
+                drain(smem_u32((kv ? sh8->rfull : sh8->kfull) + i % stages), i / stages & 1);
         } else {
             drain_tiles(sh, warp - kWarpKv);
         }
@@ -1656,6 +1802,7 @@ cudaError_t chunk_args(ChunkArgs *p, CUtensorMap *qm, const Cache *c, int32_t la
     a.scale2 = 1.4426950408889634f / sqrtf((float)c->head_dim);
     a.out = static_cast<uint16_t *>(out);
     a.v = nullptr;
+    a.q = static_cast<const uint16_t *>(q);
     a.v8 = nullptr;
     a.k_scale = a.v_scale = nullptr;
     a.block_stride = c->block_stride;

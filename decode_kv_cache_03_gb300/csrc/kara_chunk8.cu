@@ -2,7 +2,7 @@
 namespace kara {
 namespace {
 
-constexpr int kStages = 3;  // K and V tiles, beside which the tiles of codes in flight lie
+constexpr int kStages = 2;  // bf16 tiles of V, beside which the tiles of codes in flight lie
 constexpr int kEdges = 1;   // (no edge tiles of V: what converts a tile clears it)
 
 }  // namespace
@@ -22,7 +22,7 @@ cudaError_t launch_chunk8(const kara_cache8 *c, int32_t layer, const kara_tokens
     a.v8 = static_cast<const uint8_t *>(c->v) + (int64_t)layer * c->layer_stride;
     a.k_scale = c->k_scale + scales;
     a.v_scale = c->v_scale + scales;
-    if (e == cudaSuccess) e = pool_map8(&km, c->k, c, false);
+    if (e == cudaSuccess) e = pool_map8(&km, c->k, c, true);
     if (e == cudaSuccess) e = pool_map8(&vm, c->v, c, false);
     if (e != cudaSuccess) return e;
     return c->head_dim == 128 ? launch_all<128, true>(km, vm, qm, a, st) : launch_all<64, true>(km, vm, qm, a, st);

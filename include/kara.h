@@ -409,10 +409,11 @@ kara_status kara_decode_attention8(const kara_cache8 *c, int32_t layer, int32_t 
 
 /*
  * Causal attention of new tokens over an 8-bit cache: kara_chunk_attention with k_x
- * and v_x the stored values, its arguments, checks, errors and arithmetic (the output
- * has the bits that kara_chunk_attention gives over a bf16 cache of those values,
- * which holds all of them).  A key or value that is NaN reaches only the rows that
- * see it.
+ * and v_x the stored values, its arguments, checks, errors and arithmetic, but that
+ * queries enter the logits as two e4m3 terms of a power of two times themselves:
+ * elements within 2^-10 of a row's largest are exact, smaller ones off by at most
+ * 2^-17 of the largest (or 2^-50).  A key or value that is NaN reaches only the rows
+ * that see it.
  */
 size_t kara_chunk8_workspace_size(const kara_cache8 *c, int32_t n, int32_t rows);
 kara_status kara_chunk_attention8(const kara_cache8 *c, int32_t layer, const kara_tokens *t,

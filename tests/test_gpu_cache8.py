@@ -9,8 +9,9 @@ append   fp32 sums and products of one row (about 20 roundings of 2^-24, against
 decode   logits: fp32 sums of exact products and two multiplications; with |logit| <= 40 and 128 terms below
          2^-11 of a weight.  A weight is rounded to f16 once (2^-11 of it, or 2^-40 of the split's largest).  One
          rounding of the output: |got - ref| <= 2^-8 |ref| + 2^-10 sum_x w_x |v_x| + 2^-30 max|v|.
-chunk    the bits of kara_chunk_attention over a bf16 cache of the same values, which holds them exactly; against 64
-         bits its tolerance, 2^-8 |ref| + (2^-8 + 2^-10) sum_x w_x |v_x|.
+chunk    that of kara_chunk_attention, whose arithmetic it is but for 2^-17 of a query's largest element in the small
+         ones: 2^-8 |ref| + (2^-8 + 2^-10) sum_x w_x |v_x| against 64 bits; twice that against kara_chunk_attention
+         over a bf16 cache of the same values, which holds them exactly (and whose output stands for the sums, 2 % off).
 expand, compact   equal: code times scale is exact, and a code is rounded once from an exact quotient."""
 
 import numpy as np
@@ -480,6 +481,17 @@ def run_chunk(d, layer=0, bf16=False, pools=None, fill=77.0):
     return status(kara, err), out.cpu()
 
 
+def near_bf16(c, layer, got):
+    """Whether the output is as near to the bf16 cache's as two results within the tolerance are."""
+    st, want = run_chunk(c, layer, bf16=True)
+    _, size = run_chunk(dict(c, v=c["v"] & 0x7f), layer, bf16=True)
+    want, size = want.double(), size.double()
+    off = (got.double() - want).abs() - 1.02 * (2.0 ** -7 * want.abs() + (2.0 ** -7 + 2.0 ** -9) * size)
+    pad = want == 77.0
+    assert st == 0 and torch.equal(got.double()[pad], want[pad])
+    assert off[~pad].max() <= 0, off[~pad].max()
+
+
 def same_bits(a, b):
     return torch.equal(a.view(torch.int16), b.view(torch.int16))
 
@@ -491,15 +503,14 @@ CHUNKS = [([1, 17, 128, 129, 300, 64, 513, 255, 700], [1, 17, 1, 129, 4, 0, 140,
 @pytest.mark.parametrize("case", range(len(CHUNKS)))
 @pytest.mark.parametrize("hq,hkv,d", [(2, 2, 64), (4, 2, 128), (6, 2, 64), (8, 2, 128), (10, 2, 128), (7, 1, 128),
                                       (16, 2, 64)])
-def test_chunk_has_the_bits_of_the_bf16_cache(case, hq, hkv, d):
-    """Every group size and head dim, single tokens to whole prompts, on both caches: the same output."""
+def test_chunk_is_near_the_bf16_cache(case, hq, hkv, d):
+    """Every group size and head dim, single tokens to whole prompts, on both caches."""
     lengths, n_new = CHUNKS[case]
     c = chunk_case(case * 31 + hq, lengths, n_new, hq, hkv, d, layers=2, pad=3)
     for layer in (0, 1):
         st, got = run_chunk(c, layer)
-        st2, want = run_chunk(c, layer, bf16=True)
-        assert st == st2 == 0
-        assert torch.isfinite(got).all() and same_bits(got, want) and (got[-3:] == 77.0).all()
+        assert st == 0 and torch.isfinite(got).all() and (got[-3:] == 77.0).all()
+        near_bf16(c, layer, got)
 
 
 @pytest.mark.parametrize("hq,hkv,d", [(4, 2, 64), (10, 2, 128)])
@@ -516,7 +527,7 @@ def test_chunk_matches_plain(hq, hkv, d):
 
 
 def test_chunk_scales_at_their_limits():
-    """Scales of 2^-63, 2^63 and 0, above the range of one product too: the bits of the bf16 cache."""
+    """Scales of 2^-63, 2^63 and 0, above the range of one product too; queries of zeros and tiny ones."""
     c = chunk_case(4, [200, 333, 100], [60, 200, 1], 8, 2, 128, qmag=0.01)
     for i, e in enumerate((-63, -40, 5, 7, 8, 9, 30)):
         c["ks"][0, int(c["bt"][0, i])] = 2.0 ** e if e < 9 else 2.0 ** -20
@@ -524,8 +535,13 @@ def test_chunk_scales_at_their_limits():
     c["vs"][0, int(c["bt"][2, 1])] = 2.0 ** 63
     c["vs"][0, int(c["bt"][2, 2])] = 0.0
     c["v"][0, int(c["bt"][2, 2])] = 0
+    c["ks"][0, int(c["bt"][0, 9])] = 0.0
+    c["k"][0, int(c["bt"][0, 9])] = 0
+    c["q"][5] = 0.0
+    c["q"][6] *= 2.0 ** -60
     st, got = run_chunk(c)
-    assert st == 0 and same_bits(got, run_chunk(c, bf16=True)[1])
+    assert st == 0 and torch.isfinite(got).all()
+    near_bf16(c, 0, got)
 
 
 @pytest.mark.parametrize("pool", ["k", "v"])
@@ -565,7 +581,10 @@ def test_chunk_bad_lengths_and_blocks():
         bad = dict(c, bt=c["bt"].copy())
         bad["bt"][2, 1] = bid
         st, got = run_chunk(bad)
-        assert st == kara.EBADBLOCK and same_bits(got, run_chunk(bad, bf16=True)[1])
+        assert st == kara.EBADBLOCK and same_bits(got[:30], want[:30]) and same_bits(got[60:], want[60:])
+        pools = [torch.cat([bad[x], torch.zeros_like(bad[x][:, :1])], 1) for x in ("k", "v", "ks", "vs")]
+        bad["bt"][2, 1] = c["k"].shape[1]       # a block of zeros
+        assert same_bits(got, run_chunk(dict(bad, **dict(zip(("k", "v", "ks", "vs"), pools))))[1])
     for qs in ([0, 10, 5, 60, 65], [0, 10, 30, 60, 900], [-3, 10, 30, 60, 65]):
         assert run_chunk(dict(c, q_start=np.array(qs, np.int32)))[0] == kara.EINVAL
 
@@ -581,16 +600,17 @@ def test_chunk_nothing_to_do_and_strided_pools():
     k.copy_(c["k"]), v.copy_(c["v"])
     for layer in (0, 1):
         st, got = run_chunk(c, layer, pools=[k, v, c["ks"].to(DEV), c["vs"].to(DEV)])
-        assert st == 0 and same_bits(got, run_chunk(c, layer, bf16=True)[1])
+        assert st == 0 and same_bits(got, run_chunk(c, layer)[1])
 
 
 @pytest.mark.parametrize("lengths,n_new,hq,hkv,d", [
     ([4096 + 512] * 12, [512] * 12, 8, 4, 128), ([700 + 3 * i for i in range(200)], [1 + i % 5 for i in range(200)], 4, 2, 64),
     ([3000, 20, 9000], [2900, 20, 40], 8, 2, 128), ([40] * 1500, [2] * 1500, 4, 2, 128)])
 def test_chunk_large_calls(lengths, n_new, hq, hkv, d):
-    """Whole items dealt round, many sequences, partials that are joined, several times over: the same bits."""
+    """Whole items dealt round, many sequences, partials that are joined, several times over."""
     c = chunk_case(len(lengths), lengths, n_new, hq, hkv, d)
-    want = run_chunk(c, bf16=True)[1]
+    want = run_chunk(c)[1]
+    near_bf16(c, 0, want)
     for _ in range(3):
         st, got = run_chunk(c)
         assert st == 0 and same_bits(got, want)
