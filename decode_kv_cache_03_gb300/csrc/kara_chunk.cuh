@@ -138,8 +138,7 @@ struct ChunkArgs {
     float4 *part;        // [2 * ctas][D / 4][256]
     float2 *stat;        // [2 * ctas][256]: (max, sum) in the log2 domain
     const uint16_t *v;   // V pool at the call's layer
-    const uint16_t *q;   // of the 8-bit cache: the queries,
-    const uint8_t *v8;   // V's codes
+    const uint8_t *v8;   // of the 8-bit cache: V's codes,
     const float *k_scale, *v_scale;  // and K's and V's scales [num_blocks][hkv]
     int64_t block_stride, head_stride;
     int32_t wide;        // out is 32-byte aligned
@@ -223,6 +222,7 @@ struct Shared {
 struct Shared8 {
     uint64_t kfull[kK8], kempty[kK8];      // tiles of K's codes
     uint64_t rfull[kRaw8], rempty[kRaw8];  // tiles of V's codes, which become bf16 tiles of the ring
+    uint64_t landed;                       // bf16 query tiles, which become codes
     float vscale[kRaw8][kBlkPerTile], kscale[kScales8][kBlkPerTile];
     // of each row of the query tiles, by the piece's number mod 2: the next piece's are written as soon as this
     // one's last logits are there, and read for its first; those of the one after only behind the next one's logits
@@ -802,68 +802,84 @@ __device__ __noinline__ void add_cleared(const ChunkArgs &a, int seq, int head, 
 // V's codes become bf16 tiles (code times scale is exact) of the ring, as its scales belong to the
 // summed dimension: put into weights, they would need weights in 8 bits, or another two terms.
 
-// Rows [32 w, 32 w + 32) of each query tile of a piece as two tiles of codes, and their 2^-k.
+// The bf16 query tiles of a piece; one thread issues.
 template <int D>
-__device__ __forceinline__ void split_queries(const Piece &p, int w, uint8_t *qbuf, float (*qscale)[kTile],
-                                              const ChunkArgs &a)
+__device__ __forceinline__ void load_queries(const Piece &p, uint8_t *qbuf, const CUtensorMap *qmap, uint32_t bar, int qrows,
+                                             const ChunkArgs &a)
 {
-    constexpr int LPR = D / 8, RPP = 32 / LPR, kTerm = kTile * D;
-    const int lane = threadIdx.x & 31, l = lane % LPR;
+    using C = Cfg<D, true>;
     const int tiles = p.it.ntok > a.TQ ? 2 : 1;
-#pragma unroll 1
-    for (int x = 0; x < tiles; ++x) {
-        uint8_t *hi = qbuf + x * 2 * kTerm, *lo = hi + kTerm;
-#pragma unroll 1
-        for (int r0 = w * 32; r0 < w * 32 + 32; r0 += 2 * RPP) {
-            uint4 u[2];
+    mbar_arrive_expect_tx(bar, tiles * C::kHalves * qrows * 128);
+    for (int x = 0; x < tiles; ++x)
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int r = r0 + i * RPP + lane / LPR, tok = r / a.G, t = x * a.TQ + tok;
-                u[i] = make_uint4(0, 0, 0, 0);
-                if (tok < a.TQ && t < p.it.ntok)
-                    u[i] = *reinterpret_cast<const uint4 *>(
-                        a.q + ((int64_t)(p.it.row0 + t) * a.hq + p.head * a.G + r - tok * a.G) * D + l * 8);
+        for (int h = 0; h < C::kHalves; ++h)
+            asm volatile(
+                "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+                "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_u32(qbuf + x * C::kTileBytes + h * C::kHalfBytes)),
+                "l"(reinterpret_cast<uint64_t>(qmap)), "r"(h * 64), "r"(p.head * a.G), "r"(p.it.row0 + x * a.TQ),
+                "r"(bar)
+                : "memory");
+}
+
+// Rows [32 w, 32 w + 32) of each query tile as codes, in place, and their 2^-k.  D = 128: of a bf16 row's two
+// 128-byte halves the first becomes hi and the second lo; D = 64: its 128 bytes are hi, then lo.  (Loaded into
+// registers from global memory instead, two rows at a time, they kept the products waiting for 15 us an item.)
+template <int D>
+__device__ __forceinline__ void split_queries(int tiles, int w, uint8_t *qbuf, float (*qscale)[kTile])
+{
+    using C = Cfg<D, true>;
+    constexpr int LPR = D / 8, RPP = 32 / LPR, kAhead = 4;
+    const int lane = threadIdx.x & 31, l = lane % LPR;
+#pragma unroll 1
+    for (int r0 = 0; r0 < tiles * 32; r0 += kAhead * RPP) {
+        const int x = r0 >> 5, rx = w * 32 + (r0 & 31) + lane / LPR;
+        uint8_t *q = qbuf + x * C::kTileBytes;
+        uint4 u[kAhead];
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+            const int r = rx + i * RPP;
+            u[i] = *reinterpret_cast<const uint4 *>(q + (l >> 3) * C::kHalfBytes + r * 128 + (((l & 7) ^ (r & 7)) << 4));
+        }
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+            const int r = rx + i * RPP;
+            const uint32_t v[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
+            // the largest finite magnitude, as bits: of 16-bit patterns below 0x7f80
+            uint32_t top = 0;
+            bool odd = false;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const uint32_t m0 = v[e] & 0x7fffu, m1 = v[e] >> 16 & 0x7fffu;
+                if (m0 < 0x7f80u) top = max(top, m0); else odd = true;
+                if (m1 < 0x7f80u) top = max(top, m1); else odd = true;
             }
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int r = r0 + i * RPP + lane / LPR;
-                const uint32_t v[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
-                // the largest finite magnitude, as bits: of 16-bit patterns below 0x7f80
-                uint32_t top = 0;
-                bool odd = false;
+            for (int o = LPR / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+            // the exponent of q' is 8 for mantissas up to 1.75 (448), 7 above; 2^-k at least 2^-40, so that
+            // times the smallest scale it is no 0 (which a masked logit's infinity would turn to NaN)
+            const int down = min(max((int)((top + 0x1fu) >> 7) - 8, 127 - 40), 253);
+            const float f = __uint_as_float((uint32_t)(254 - down) << 23);
+            if (l == 0) qscale[x][r] = __uint_as_float((uint32_t)down << 23);
+            uint32_t h[2] = {0u, 0u}, g[2] = {0u, 0u};
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const uint32_t m0 = v[e] & 0x7fffu, m1 = v[e] >> 16 & 0x7fffu;
-                    if (m0 < 0x7f80u) top = max(top, m0); else odd = true;
-                    if (m1 < 0x7f80u) top = max(top, m1); else odd = true;
+            for (int e = 0; e < 4; ++e) {
+                float q0 = __uint_as_float(v[e] << 16) * f, q1 = __uint_as_float(v[e] & 0xffff0000u) * f;
+                if (odd) {  // NaN for what is not finite: the row's logits are
+                    if (!finite(q0)) q0 = __uint_as_float(0x7fffffffu);
+                    if (!finite(q1)) q1 = __uint_as_float(0x7fffffffu);
                 }
-#pragma unroll
-                for (int o = LPR / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-                // the exponent of q' is 8 for mantissas up to 1.75 (448), 7 above; 2^-k at least 2^-40, so that
-                // times the smallest scale it is no 0 (which a masked logit's infinity would turn to NaN)
-                const int down = min(max((int)((top + 0x1fu) >> 7) - 8, 127 - 40), 253);
-                const float f = __uint_as_float((uint32_t)(254 - down) << 23);
-                if (l == 0) qscale[x][r] = __uint_as_float((uint32_t)down << 23);
-                uint32_t h[2] = {0u, 0u}, g[2] = {0u, 0u};
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    float q0 = __uint_as_float(v[e] << 16) * f, q1 = __uint_as_float(v[e] & 0xffff0000u) * f;
-                    if (odd) {  // NaN for what is not finite: the row's logits are
-                        if (!finite(q0)) q0 = __uint_as_float(0x7fffffffu);
-                        if (!finite(q1)) q1 = __uint_as_float(0x7fffffffu);
-                    }
-                    const uint32_t c = e4m3x2(q0, q1);
-                    float c0, c1;
-                    f32_of_f16x2(f16_of_e4m3x2(c), c0, c1);
-                    h[e >> 1] |= c << (16 * (e & 1));
-                    g[e >> 1] |= e4m3x2(q0 - c0, q1 - c1) << (16 * (e & 1));
-                }
-                // eight codes of chunk l / 2 of the row, swizzled by the rows' size
-                const int sw = D == 128 ? r & 7 : r >> 1 & 3;
-                const int at = r * D + (((l >> 1) ^ sw) << 4) + (l & 1) * 8;
-                *reinterpret_cast<uint2 *>(hi + at) = make_uint2(h[0], h[1]);
-                *reinterpret_cast<uint2 *>(lo + at) = make_uint2(g[0], g[1]);
+                const uint32_t c = e4m3x2(q0, q1);
+                float c0, c1;
+                f32_of_f16x2(f16_of_e4m3x2(c), c0, c1);
+                h[e >> 1] |= c << (16 * (e & 1));
+                g[e >> 1] |= e4m3x2(q0 - c0, q1 - c1) << (16 * (e & 1));
             }
+            __syncwarp();  // (the whole row has been read)
+            // eight codes, half of a 16-byte chunk, of hi and of lo
+            uint8_t *o = q + r * 128 + (l & 1) * 8;
+            const int c = l >> 1, d = D == 128 ? c : c + 4, sw = r & 7;
+            *reinterpret_cast<uint2 *>(o + ((c ^ sw) << 4)) = make_uint2(h[0], h[1]);
+            *reinterpret_cast<uint2 *>(o + (D == 128 ? C::kHalfBytes : 0) + ((d ^ sw) << 4)) = make_uint2(g[0], g[1]);
         }
     }
 }
@@ -982,22 +998,29 @@ __device__ __noinline__ bool convert_odd_block(const uint8_t *raw, uint8_t *tile
 // what rows must not see cleared on the way.
 template <int D>
 __device__ __forceinline__ void convert_tiles(int cw, uint8_t *qbuf, uint8_t *ring, const uint8_t *raw, Shared *sh,
-                                              Shared8 *sh8, const ChunkArgs &a)
+                                              Shared8 *sh8, const CUtensorMap *qmap, int qrows, const ChunkArgs &a)
 {
     using C = Cfg<D, true>;
     const int lane = threadIdx.x & 31;
     const LaneChunk<D> lc(lane);
     Piece p;
-    uint32_t np = 0, k = 0;   // pieces, V tiles
+    uint32_t np = 0, nq = 0, k = 0;   // pieces, query tiles issued, V tiles
     uint32_t st = 0, ph = 1;  // the next stage of the ring and the phase that frees it
     bool ok = true;
     const auto wait = [&](uint32_t bar, uint32_t parity) {
         return __all_sync(0xffffffffu, kwait<20>(bar, parity, sh, a)) != 0;
     };
     for (; ok && !a.stall && next_piece<true>(p, np, sh, ok, lane, wait); ++np) {
-        ok = wait(smem_u32(&sh->q_empty), (np & 1) ^ 1);
+        if (cw == 0) {
+            ok = wait(smem_u32(&sh->q_empty), (np & 1) ^ 1);
+            if (!ok) break;
+            if (lane == 0) load_queries<D>(p, qbuf, qmap, smem_u32(&sh8->landed), qrows, a);
+            __syncwarp();
+            ++nq;
+        }
+        ok = wait(smem_u32(&sh8->landed), np & 1);
         if (!ok) break;
-        split_queries<D>(p, cw, qbuf, sh8->qscale[np & 1], a);
+        split_queries<D>(p.it.ntok > a.TQ ? 2 : 1, cw, qbuf, sh8->qscale[np & 1]);
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&sh->q_full));
@@ -1028,6 +1051,8 @@ __device__ __forceinline__ void convert_tiles(int cw, uint8_t *qbuf, uint8_t *ri
             if (++st == kStages) st = 0, ph ^= 1;
         }
     }
+    // the last query tiles have landed too
+    if (nq > 0) drain(smem_u32(&sh8->landed), (nq - 1) & 1);
 }
 
 // Records the sequences whose rows or lengths are out of order and zeroes their rows.
@@ -1066,7 +1091,7 @@ __device__ __forceinline__ void mma_warp(int x, uint32_t qbuf, uint32_t ring, Sh
         constexpr uint32_t kTileDesc = C::kTileBytes >> 4, kHalfDesc = C::kHalfBytes >> 4;
         const uint32_t ts = x * kTile, to = 256 + x * 128;         // S (and P over it), O in TMEM
         const uint32_t kring = E8 ? ring + kStages * C::kTileBytes : ring;
-        const uint64_t qd = E8 ? sdesc_codes<D>(qbuf) : sdesc_sw128(qbuf);
+        const uint64_t qd = sdesc_sw128(qbuf);
         const uint64_t kd = E8 ? sdesc_codes<D>(kring) : sdesc_sw128(kring), vd = sdesc_sw128_mn(ring, C::kHalfBytes);
         constexpr uint32_t kKeyDesc = E8 ? C::kRawBytes >> 4 : kTileDesc;
         const uint32_t full0 = smem_u32(&sh->full[0]), empty0 = smem_u32(&sh->empty[0]);
@@ -1154,7 +1179,7 @@ __device__ __forceinline__ void mma_warp(int x, uint32_t qbuf, uint32_t ring, Sh
                         if constexpr (E8) {
 #pragma unroll
                             for (int e = 0; e < D / 16; ++e)  // 32 dims of the first term, then of the second
-                                mma_ss_e4m3(ts, ql + ((e & 1) * kKeyDesc + (e >> 1) * 2), (uint32_t)(qd >> 32),
+                                mma_ss_e4m3(ts, ql + ((e & 1) * (D == 128 ? kHalfDesc : 4) + (e >> 1) * 2), (uint32_t)(qd >> 32),
                                             lo + (e >> 1) * 2, (uint32_t)(kd >> 32), id_qk, e > 0);
                         } else {
 #pragma unroll
@@ -1212,6 +1237,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(smem_u32(&sh8->kfull[i]), 1);
             mbar_init(smem_u32(&sh8->kempty[i]), 2);
         }
+        if (E8) mbar_init(smem_u32(&sh8->landed), 1);
         for (int i = 0; E8 && i < kRaw8; ++i) {
             mbar_init(smem_u32(&sh8->rfull[i]), 1);
             mbar_init(smem_u32(&sh8->rempty[i]), 4);
@@ -1372,7 +1398,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         } else if (warp == kWarpMma || warp == kWarpMma + 1) {
             mma_warp<D, E8>(warp - kWarpMma, smem_u32(qbuf), smem_u32(ring), sh, sh8, a);
         } else if constexpr (E8) {
-            convert_tiles<D>(warp - kWarpQ, qbuf, ring, ring + kStages * C::kTileBytes + kK8 * C::kRawBytes, sh, sh8, a);
+            convert_tiles<D>(warp - kWarpQ, qbuf, ring, ring + kStages * C::kTileBytes + kK8 * C::kRawBytes, sh, sh8,
+                             &qmap, qrows, a);
         } else {
             // ---------------- query tiles (warp 12), and the edge tiles of V (warps 12-15, a
             // quarter of the rows each: the products wait for them)
@@ -1802,7 +1829,6 @@ cudaError_t chunk_args(ChunkArgs *p, CUtensorMap *qm, const Cache *c, int32_t la
     a.scale2 = 1.4426950408889634f / sqrtf((float)c->head_dim);
     a.out = static_cast<uint16_t *>(out);
     a.v = nullptr;
-    a.q = static_cast<const uint16_t *>(q);
     a.v8 = nullptr;
     a.k_scale = a.v_scale = nullptr;
     a.block_stride = c->block_stride;
