@@ -24,6 +24,7 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kBs = 16;      // tokens per cache block (the supported block size)
+constexpr int kSplitRows = 20480;  // head rows of a call from which queries and runs are two launches
 constexpr int kQPasses = 4;  // passes of query rows a warp has in flight
 
 struct Append8Args {
@@ -302,13 +303,13 @@ __global__ void __launch_bounds__(kThreads, 2) append8_kernel(const Append8Args 
 }
 
 template <int D>
-cudaError_t launch(Append8Args &a, bool inter, cudaStream_t st)
+cudaError_t launch(Append8Args &a, bool inter, bool with_queries, cudaStream_t st)
 {
     constexpr int HPW = kQPasses * (32 / (D / 8));
-    // short calls: a warp for each row that may begin a run; long ones look at four rows each
-    a.win = a.rows <= 512 ? 1 : 4;
+    // short calls: a warp for each row that may begin a run; long ones look at several rows each
+    a.win = a.rows <= 512 ? 1 : a.rows / 16 < a.n ? 4 : 8;
     const int64_t runs = ((int64_t)a.rows + a.win - 1) / a.win * (2 * a.hkv);
-    const int64_t queries = (int64_t)a.rows * ((a.hq + HPW - 1) / HPW);
+    const int64_t queries = with_queries ? (int64_t)a.rows * ((a.hq + HPW - 1) / HPW) : 0;
     const int64_t kv = (runs + kWarps - 1) / kWarps, blocks = kv + (queries + kWarps - 1) / kWarps;
     if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
     a.kv_blocks = (int32_t)kv;
@@ -357,7 +358,13 @@ cudaError_t launch_append8(const kara_cache8 *c, int32_t layer, const kara_token
     a.hkv = c->num_kv_heads;
     a.n_pos = r->rot_dim > 0 ? r->n_pos : 1;
     a.rot = r->rot_dim;
-    return D == 128 ? launch<128>(a, r->interleaved, st) : launch<64>(a, r->interleaved, st);
+    // long calls: the queries, most of what there is to read and write, by the kernel that stages tokens
+    const bool split = (int64_t)t->rows * (c->num_q_heads + 2 * c->num_kv_heads) > kSplitRows;
+    if (split) {
+        const cudaError_t e = launch_append_queries(c, layer, t, r, q, q_stride, q_out, ring, W, err, st);
+        if (e != cudaSuccess) return e;
+    }
+    return D == 128 ? launch<128>(a, r->interleaved, !split, st) : launch<64>(a, r->interleaved, !split, st);
 }
 
 }  // namespace kara

@@ -90,20 +90,23 @@ __host__ __device__ __forceinline__ size_t align256(size_t x) { return (x + 255)
 // Host-side argument checks of the entry points; fills the geometry of a call.
 kara_status geo_from_args(const kara_cache *c, const kara_params *p, const kara_batch *b, Geo *g);
 
-// Launchers (each returns the launch error, if any).
-cudaError_t launch_plan(const Geo &g, int64_t n_fresh, SeqPlan *plan, int32_t *err, cudaStream_t st);
+// Launchers (each returns the launch error, if any; dependent: as a programmatic dependent of what
+// precedes it on the stream).
+cudaError_t launch_plan(const Geo &g, int64_t n_fresh, SeqPlan *plan, int32_t *err, cudaStream_t st,
+                        bool dependent = false);
 cudaError_t launch_compact(const Geo &g, const SeqPlan *plan, const int32_t *kept, const int32_t *fresh,
                            int64_t n_fresh, int32_t *err, cudaStream_t st);
 // The two halves of launch_compact: the fresh-id check of a whole batch, and the
 // kept-row check plus the copy of a batch or of a group of its sequences (plan
 // then points at the group's first entry; offsets into fresh stay the batch's).
 cudaError_t launch_fresh_check(const Geo &g, const SeqPlan *plan, const int32_t *fresh, int64_t n_fresh,
-                               int32_t *err, cudaStream_t st);
-cudaError_t launch_kept_check(const Geo &g, const int32_t *kept, int32_t *err, cudaStream_t st);
+                               int32_t *err, cudaStream_t st, bool dependent = false);
+cudaError_t launch_kept_check(const Geo &g, const int32_t *kept, int32_t *err, cudaStream_t st, bool dependent = false);
 cudaError_t launch_kept_copy(const Geo &g, const SeqPlan *plan, const int32_t *kept, const int32_t *fresh,
                              int64_t n_fresh, int32_t *err, cudaStream_t st);
 cudaError_t launch_commit(const Geo &g, const SeqPlan *plan, const int32_t *fresh, int32_t *freed,
-                          int32_t *new_len, int32_t *bt, const int32_t *err, cudaStream_t st);
+                          int32_t *new_len, int32_t *bt, const int32_t *err, cudaStream_t st,
+                          bool dependent = false);
 cudaError_t launch_select(int64_t nwin, int C, int K, int R, float lambda, int mode, int chunk, const float *scores,
                           int32_t *cand, int32_t *kept, cudaStream_t st);
 size_t score_scratch_bytes(const Geo &g);

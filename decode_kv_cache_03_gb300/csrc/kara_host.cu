@@ -569,11 +569,11 @@ kara_status kara_compact8(const kara_cache8 *c, const kara_params *p, int32_t n,
     g.nwin = (int64_t)n * c->num_layers * c->num_kv_heads;
     cudaStream_t s = (cudaStream_t)stream;
     SeqPlan *plan = static_cast<SeqPlan *>(ws);
-    cudaError_t e = launch_plan(g, n_fresh, plan, err, s);
-    if (e == cudaSuccess) e = launch_fresh_check(g, plan, fresh, n_fresh, err, s);
-    if (e == cudaSuccess) e = launch_kept_check(g, kept, err, s);
+    cudaError_t e = launch_plan(g, n_fresh, plan, err, s, true);
+    if (e == cudaSuccess) e = launch_fresh_check(g, plan, fresh, n_fresh, err, s, true);
+    if (e == cudaSuccess) e = launch_kept_check(g, kept, err, s, true);
     if (e == cudaSuccess) e = launch_copy8(c, g, plan, kept, fresh, n_fresh, err, s);
-    if (e == cudaSuccess) e = launch_commit(g, plan, fresh, freed, new_len, block_table, err, s);
+    if (e == cudaSuccess) e = launch_commit(g, plan, fresh, freed, new_len, block_table, err, s, true);
     return cuda_status(e);
 }
 

@@ -6,12 +6,24 @@
 // memory.  The retained rows of each window are packed, in order, into fresh
 // blocks supplied by the caller; the old tail blocks are released only after
 // every copy is done and only if no error was recorded.
-#include "kara_common.cuh"
+#include "kara_tokens.cuh"
 
 namespace kara {
 namespace {
 
 constexpr int kPlanThreads = 1024;
+
+// The plan, checks and commit may be launched as programmatic dependents of what precedes them on the
+// stream (`dependent` of their launchers): nothing global is read before that has completed.
+__device__ __forceinline__ void dependent_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+template <class... A>
+cudaError_t launch(bool dependent, void (*kern)(A...), unsigned blocks, int threads, cudaStream_t st, A... args)
+{
+    if (dependent) return launch_dependent(kern, dim3(blocks), threads, 0, st, args...);
+    kern<<<blocks, threads, 0, st>>>(args...);
+    return cudaGetLastError();
+}
 
 __device__ __forceinline__ int warp_incl_scan(int v)
 {
@@ -51,6 +63,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(Geo g, int64_t n_fre
 {
     __shared__ int scratch[33];
     __shared__ long long carry_new, carry_old;
+    dependent_wait();
     if (threadIdx.x == 0) { carry_new = 0; carry_old = 0; }
     __syncthreads();
     for (int base = 0; base < g.n; base += blockDim.x) {
@@ -112,6 +125,7 @@ __global__ void __launch_bounds__(kChkThreads) fresh_check_kernel(Geo g, const S
                                                                   int64_t n_fresh, int32_t *err)
 {
     __shared__ int32_t tile[kChkTile];
+    dependent_wait();
     const SeqPlan last = plan[g.n - 1];
     const int64_t F = (int64_t)last.off_new + last.n_new;  // fresh ids the plan consumes
     if (F > n_fresh) return;                                // KARA_ENOBLOCKS is recorded
@@ -157,6 +171,7 @@ __global__ void __launch_bounds__(kChkThreads) fresh_check_kernel(Geo g, const S
 __global__ void __launch_bounds__(kChkThreads) kept_check_kernel(int64_t n, int R, int C,
                                                                  const int32_t *__restrict__ kept, int32_t *err)
 {
+    dependent_wait();
     for (int64_t i = (int64_t)blockIdx.x * kChkThreads + threadIdx.x; i < n; i += (int64_t)gridDim.x * kChkThreads) {
         const int r = (int)(i % R);
         const int32_t k = kept[i];
@@ -232,6 +247,7 @@ __global__ void __launch_bounds__(256) commit_kernel(Geo g, const SeqPlan *__res
                                                      int32_t *freed, int32_t *new_len, int32_t *bt,
                                                      const int32_t *err)
 {
+    dependent_wait();
     const int s = blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
     const int lane = threadIdx.x & 31;
     if (s >= g.n) return;
@@ -252,31 +268,30 @@ __global__ void __launch_bounds__(256) commit_kernel(Geo g, const SeqPlan *__res
 
 }  // namespace
 
-cudaError_t launch_plan(const Geo &g, int64_t n_fresh, SeqPlan *plan, int32_t *err, cudaStream_t st)
+cudaError_t launch_plan(const Geo &g, int64_t n_fresh, SeqPlan *plan, int32_t *err, cudaStream_t st, bool dependent)
 {
-    plan_kernel<<<1, kPlanThreads, 0, st>>>(g, n_fresh, plan, err);
-    return cudaGetLastError();
+    return launch<Geo, int64_t, SeqPlan *, int32_t *>(dependent, plan_kernel, 1, kPlanThreads, st, g, n_fresh, plan, err);
 }
 
 // The fresh-id check of the whole batch (before any copy of any group).
 cudaError_t launch_fresh_check(const Geo &g, const SeqPlan *plan, const int32_t *fresh, int64_t n_fresh,
-                               int32_t *err, cudaStream_t st)
+                               int32_t *err, cudaStream_t st, bool dependent)
 {
     if (g.nwin == 0) return cudaSuccess;
     const int64_t probes = n_fresh + (int64_t)g.n * g.bt_stride;
     const int64_t per = (int64_t)kChkThreads * kChkProbes;
     const int64_t nb = (probes + per - 1) / per;
     if (nb > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-    fresh_check_kernel<<<(unsigned)nb, kChkThreads, 0, st>>>(g, plan, fresh, n_fresh, err);
-    return cudaGetLastError();
+    return launch<Geo, const SeqPlan *, const int32_t *, int64_t, int32_t *>(
+        dependent, fresh_check_kernel, (unsigned)nb, kChkThreads, st, g, plan, fresh, n_fresh, err);
 }
 
-cudaError_t launch_kept_check(const Geo &g, const int32_t *kept, int32_t *err, cudaStream_t st)
+cudaError_t launch_kept_check(const Geo &g, const int32_t *kept, int32_t *err, cudaStream_t st, bool dependent)
 {
     const int64_t nk = g.nwin * g.R;
     const int64_t kb = (nk + kChkThreads - 1) / kChkThreads;
-    kept_check_kernel<<<(unsigned)(kb < 4096 ? kb : 4096), kChkThreads, 0, st>>>(nk, g.R, g.C, kept, err);
-    return cudaGetLastError();
+    return launch<int64_t, int, int, const int32_t *, int32_t *>(
+        dependent, kept_check_kernel, (unsigned)(kb < 4096 ? kb : 4096), kChkThreads, st, nk, g.R, g.C, kept, err);
 }
 
 // The kept-row check, then the copy (which runs only if no error was recorded).
@@ -303,12 +318,11 @@ cudaError_t launch_compact(const Geo &g, const SeqPlan *plan, const int32_t *kep
 }
 
 cudaError_t launch_commit(const Geo &g, const SeqPlan *plan, const int32_t *fresh, int32_t *freed,
-                          int32_t *new_len, int32_t *bt, const int32_t *err, cudaStream_t st)
+                          int32_t *new_len, int32_t *bt, const int32_t *err, cudaStream_t st, bool dependent)
 {
     if (g.n == 0) return cudaSuccess;
-    const int blocks = (g.n + 7) / 8;
-    commit_kernel<<<blocks, 256, 0, st>>>(g, plan, fresh, freed, new_len, bt, err);
-    return cudaGetLastError();
+    return launch<Geo, const SeqPlan *, const int32_t *, int32_t *, int32_t *, int32_t *, const int32_t *>(
+        dependent, commit_kernel, (unsigned)(g.n + 7) / 8, 256, st, g, plan, fresh, freed, new_len, bt, err);
 }
 
 }  // namespace kara

@@ -9,6 +9,8 @@
 //     s = the smallest power of two with max |x| <= 448 s,   code' = rn(x / s).
 // Powers of two: x / s is exact unless it falls among e4m3's subnormals.
 // Both are bound by HBM (a read and a write of every code, or of its bf16 value).
+#include <cuda_fp16.h>
+
 #include "kara_cache8.cuh"
 #include "kara_tokens.cuh"
 
@@ -115,82 +117,128 @@ struct CompactArgs {
     float *scale[2];
     const SeqPlan *plan;
     const int32_t *kept, *fresh, *bt;
-    int64_t n_fresh, units;
+    int64_t n_fresh, windows;
     int32_t B, C, R, bt_stride, max_new;
     int32_t *err;
 };
 
-// A warp rebuilds one block of one head and pool: unit ((s * layers + l) * hkv + g) * 2 + pool, new block j.
+// Largest magnitude among four codes, as 16-bit pairs of even and odd bytes: codes without their sign order
+// like their values.
+__device__ __forceinline__ uint32_t top_code(uint32_t top, uint32_t w)
+{
+    return __vmaxu2(top, __vmaxu2(w & 0x007f007fu, w >> 8 & 0x007f007fu));
+}
+
+// Codes times a power of two from 2^-24 to 2^15, or 0: f16 holds every product exactly that does not round
+// to code 0 anyway.
+__device__ __forceinline__ uint32_t shift4(uint32_t w, __half2 f)
+{
+    const uint32_t lo = f16_of_e4m3x2(w & 0xffffu), hi = f16_of_e4m3x2(w >> 16);
+    const __half2 x = __hmul2(*reinterpret_cast<const __half2 *>(&lo), f);
+    const __half2 y = __hmul2(*reinterpret_cast<const __half2 *>(&hi), f);
+    uint16_t a, b;
+    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(a) : "r"(*reinterpret_cast<const uint32_t *>(&x)));
+    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(b) : "r"(*reinterpret_cast<const uint32_t *>(&y)));
+    return a | (uint32_t)b << 16;
+}
+
+// A warp rebuilds one block of one head, K and V (they come from the same rows): window (s * layers + l) * hkv
+// + g, new block j.  The chain of loads plan, kept row, table entry, codes is long: all rows of both pools are in
+// flight at its end.  Conversions set the pace beside that (they run at 16 lanes a clock): the largest value
+// is found on the codes, and rows whose scale stays are copied as they are.
 template <int D>
 __global__ void __launch_bounds__(kThreads) compact8_kernel(const CompactArgs a)
 {
     constexpr int LPR = D / 16, RPP = 32 / LPR, NP = kBs / RPP;  // lanes per row, rows per pass, passes
-    // nothing is written once an earlier kernel (plan, checks) recorded an error
-    if (*(volatile const int32_t *)a.err != 0) return;
-    const int64_t task = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
-    const int64_t unit = task / a.max_new;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int64_t task = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5), window = task / a.max_new;
     const int j = (int)(task % a.max_new), lane = threadIdx.x & 31;
-    if (unit >= a.units) return;
-    const int pool = (int)(unit & 1), lh = (int)((unit >> 1) % a.in.heads), s = (int)((unit >> 1) / a.in.heads);
+    if (window >= a.windows) return;
+    const int lh = (int)(window % a.in.heads), s = (int)(window / a.in.heads);
+    const int32_t failed = *(volatile const int32_t *)a.err;
     const SeqPlan p = a.plan[s];
-    if (p.p0 < 0 || j >= p.n_new || (int64_t)p.off_new + p.n_new > a.n_fresh) return;
+    // nothing is written once an earlier kernel (plan, checks) recorded an error
+    if (failed != 0 || p.p0 < 0 || j >= p.n_new || (int64_t)p.off_new + p.n_new > a.n_fresh) return;
     const int32_t to = a.fresh[p.off_new + j];
-    if (to < 0 || to >= a.in.num_blocks) return;  // recorded by the check
-    const int32_t *kept = a.kept + (unit >> 1) * a.R, *bt = a.bt + (int64_t)s * a.bt_stride;
+    const int32_t *kept = a.kept + window * a.R, *bt = a.bt + (int64_t)s * a.bt_stride;
     const int c = lane % LPR, x0 = (p.p0 + j) * kBs;
-    uint4 w[NP];
-    float f[NP];
-    bool live[NP];
+    int32_t id[NP], at[NP];
 #pragma unroll
     for (int i = 0; i < NP; ++i) {
         const int x = x0 + i * RPP + lane / LPR;
-        w[i] = make_uint4(0, 0, 0, 0);
-        f[i] = 0.f;
-        live[i] = x < p.Lnew;
-        if (!live[i]) continue;
         int old = x;
         if (x >= p.ws) old = x < p.ws + a.R ? p.ws + min(max(kept[x - p.ws], 0), a.C - 1) : p.L - a.B + (x - p.ws - a.R);
-        const int32_t id = bt[old / kBs];
-        if (id < 0 || id >= a.in.num_blocks) {
-            set_err(a.err, KARA_EBADBLOCK);
-            continue;
-        }
-        w[i] = *reinterpret_cast<const uint4 *>(a.in.codes[pool] + a.in.slice(lh, id) + old % kBs * D + c * 16);
-        f[i] = fabsf(a.in.scale[pool][a.in.scale_at(lh, id)]);
+        at[i] = old % kBs * D + c * 16;
+        id[i] = x < p.Lnew ? bt[old / kBs] : -2;
     }
-    float top = 0.f;
-    bool odd = false;
+    if (to < 0 || to >= a.in.num_blocks) return;  // recorded by the check
+    uint4 w[2][NP];
+    float f[2][NP];
 #pragma unroll
     for (int i = 0; i < NP; ++i) {
-        const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
-        float t = 0.f;
+        const bool in = id[i] >= 0 && id[i] < a.in.num_blocks;
+        if (!in && id[i] != -2) set_err(a.err, KARA_EBADBLOCK);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            float x[4];
-            values4(u[e], x);
+        for (int k = 0; k < 2; ++k) {
+            w[k][i] = make_uint4(0, 0, 0, 0);
+            f[k][i] = 0.f;
+            if (!in) continue;
+            w[k][i] = *reinterpret_cast<const uint4 *>(a.in.codes[k] + a.in.slice(lh, id[i]) + at[i]);
+            f[k][i] = a.in.scale[k][a.in.scale_at(lh, id[i])];
+        }
+    }
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                t = fmaxf(t, fabsf(x[k]));  // (passes over a NaN)
-                odd = odd || x[k] != x[k];
+    for (int k = 0; k < 2; ++k) {
+        float top = 0.f;
+        bool odd = false;  // a row of a block that may hold NaN codes
+#pragma unroll
+        for (int i = 0; i < NP; ++i) {
+            uint32_t t = top_code(top_code(top_code(top_code(0u, w[k][i].x), w[k][i].y), w[k][i].z), w[k][i].w);
+            t = max(t & 0xffffu, t >> 16);
+            float lo, hi;
+            f32_of_f16x2(f16_of_e4m3x2(t), lo, hi);
+            top = fmaxf(top, lo * f[k][i]);
+            odd = odd || signbit(f[k][i]);
+        }
+        const bool marked = __any_sync(0xffffffffu, odd);
+        if (__builtin_expect(marked, 0)) {  // again, value by value
+            top = 0.f, odd = false;
+#pragma unroll
+            for (int i = 0; i < NP; ++i) {
+                float x[4];
+                f[k][i] = fabsf(f[k][i]);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    values4(e == 0 ? w[k][i].x : e == 1 ? w[k][i].y : e == 2 ? w[k][i].z : w[k][i].w, x);
+#pragma unroll
+                    for (int v = 0; v < 4; ++v) {
+                        odd = odd || x[v] != x[v];
+                        top = fmaxf(top, fabsf(x[v]) * f[k][i]);  // (passes over a NaN)
+                    }
+                }
             }
+            odd = __any_sync(0xffffffffu, odd);
         }
-        top = fmaxf(top, t * f[i]);
-    }
-    top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));
-    odd = __any_sync(0xffffffffu, odd);
-    const float sc = scale_for(top), inv = inverse_scale(sc);
-    uint8_t *out = a.codes[pool] + a.in.slice(lh, to) + c * 16;
+        top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));
+        const float sc = scale_for(top), inv = inverse_scale(sc);
+        uint8_t *out = a.codes[k] + a.in.slice(lh, to) + c * 16;
 #pragma unroll
-    for (int i = 0; i < NP; ++i) {
-        if (!live[i]) continue;
-        const float ratio = f[i] * inv;
-        if (ratio != 1.f) {
-            w[i].x = rescale4(w[i].x, ratio), w[i].y = rescale4(w[i].y, ratio);
-            w[i].z = rescale4(w[i].z, ratio), w[i].w = rescale4(w[i].w, ratio);
+        for (int i = 0; i < NP; ++i) {
+            const float ratio = f[k][i] * inv;
+            if (ratio != 1.f) {
+                const __half2 h = __float2half2_rn(fminf(ratio, 32768.f));
+                w[k][i].x = shift4(w[k][i].x, h), w[k][i].y = shift4(w[k][i].y, h);
+                w[k][i].z = shift4(w[k][i].z, h), w[k][i].w = shift4(w[k][i].w, h);
+                if (ratio > 32768.f) {  // (2^17 at most: what is left of it)
+                    const __half2 g = __float2half2_rn(ratio * (1.f / 32768.f));
+                    w[k][i].x = shift4(w[k][i].x, g), w[k][i].y = shift4(w[k][i].y, g);
+                    w[k][i].z = shift4(w[k][i].z, g), w[k][i].w = shift4(w[k][i].w, g);
+                }
+            }
+            if (id[i] != -2) *reinterpret_cast<uint4 *>(out + (i * RPP + lane / LPR) * D) = w[k][i];
         }
-        *reinterpret_cast<uint4 *>(out + (i * RPP + lane / LPR) * D) = w[i];
+        if (lane == 0) a.scale[k][a.in.scale_at(lh, to)] = odd ? -sc : sc;
     }
-    if (lane == 0) a.scale[pool][a.in.scale_at(lh, to)] = odd ? -sc : sc;
 }
 
 Pool8 pool8(const kara_cache8 *c)
@@ -231,17 +279,14 @@ cudaError_t launch_copy8(const kara_cache8 *c, const Geo &g, const SeqPlan *plan
     a.codes[0] = static_cast<uint8_t *>(c->k), a.codes[1] = static_cast<uint8_t *>(c->v);
     a.scale[0] = c->k_scale, a.scale[1] = c->v_scale;
     a.plan = plan, a.kept = kept, a.fresh = fresh, a.bt = g.bt;
-    a.n_fresh = n_fresh, a.units = g.nwin * 2;
+    a.n_fresh = n_fresh, a.windows = g.nwin;
     a.B = g.B, a.C = g.C, a.R = g.R, a.bt_stride = g.bt_stride;
     a.max_new = (kBs - 1 + g.R + g.B + kBs - 1) / kBs;  // the window may start at any row of a block
     a.err = err;
-    const int64_t blocks = (a.units * a.max_new + kThreads / 32 - 1) / (kThreads / 32);
+    const int64_t blocks = (a.windows * a.max_new + kThreads / 32 - 1) / (kThreads / 32);
     if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-    if (g.D == 128)
-        compact8_kernel<128><<<(unsigned)blocks, kThreads, 0, st>>>(a);
-    else
-        compact8_kernel<64><<<(unsigned)blocks, kThreads, 0, st>>>(a);
-    return cudaGetLastError();
+    const auto kern = g.D == 128 ? compact8_kernel<128> : compact8_kernel<64>;
+    return launch_dependent(kern, dim3((unsigned)blocks), kThreads, 0, st, (const CompactArgs)a);
 }
 
 }  // namespace kara
