@@ -7,12 +7,12 @@
 //     s = max(s0, the smallest power of two with max |z| <= 448 s)
 //     code = rn(z / s),   and, if s > s0, code = rn(code s0 / s) for the rows ahead
 // One rounding from fp32; nothing is rounded to bf16 on the way.  A run needs its largest
-// value before its first code, so a warp holds a whole run of one head: all its loads are
+// value before its first code, so two warps hold a whole run of one head: all its loads are
 // in flight at once, and the rows stay in registers between the maximum and the rounding.
 // Queries go as in the bf16 append, a warp per token and a few heads.
 //
 // Runs follow from the slots alone: row t continues row t - 1 if its slot is the next one
-// and not the first of a block.  A warp looks at a window of `win` rows and takes the runs
+// and not the first of a block.  A CTA looks at a window of `win` rows and takes the runs
 // that begin there.
 #include "kara_cache8.cuh"
 #include "kara_rows.cuh"
@@ -25,6 +25,7 @@ constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kBs = 16;      // tokens per cache block (the supported block size)
 constexpr int kSplitRows = 20480;  // head rows of a call from which queries and runs are two launches
+constexpr int kMaxWin = 16;  // rows that a CTA looks at for the beginnings of runs, at most
 constexpr int kQPasses = 4;  // passes of query rows a warp has in flight
 
 struct Append8Args {
@@ -81,14 +82,19 @@ struct LaneDims {
         other = !turned || INTER ? lane : low ? lane + half / 8 : lane - half / 8;
     }
     // cosines and signed sines, in pairs of neighbours
-    __device__ __forceinline__ void factors(const Append8Args &a, int64_t r, uint64_t (&c)[4], uint64_t (&sn)[4]) const
+    template <bool SHARED>
+    static __device__ __forceinline__ float4 ld4(const float *p)
+    {
+        return SHARED ? *reinterpret_cast<const float4 *>(p) : ldg4(p);
+    }
+    template <bool SHARED>
+    __device__ __forceinline__ void factors(const float *row, uint64_t (&c)[4], uint64_t (&sn)[4]) const
     {
 #pragma unroll
         for (int e = 0; e < 4; ++e) c[e] = ptx::pack2(1.f, 1.f), sn[e] = ptx::pack2(0.f, 0.f);
         if (!turned) return;
-        const float *row = a.cos_sin + r * a.rot;
         if (INTER) {
-            const float4 cc = ldg4(row + d0 / 2), ss = ldg4(row + half + d0 / 2);
+            const float4 cc = ld4<SHARED>(row + d0 / 2), ss = ld4<SHARED>(row + half + d0 / 2);
             c[0] = ptx::pack2(cc.x, cc.x), c[1] = ptx::pack2(cc.y, cc.y);
             c[2] = ptx::pack2(cc.z, cc.z), c[3] = ptx::pack2(cc.w, cc.w);
             sn[0] = ptx::pack2(-ss.x, ss.x), sn[1] = ptx::pack2(-ss.y, ss.y);
@@ -98,7 +104,7 @@ struct LaneDims {
             const uint64_t sg = low ? ptx::pack2(-1.f, -1.f) : ptx::pack2(1.f, 1.f);
 #pragma unroll
             for (int e = 0; e < 4; e += 2) {
-                const float4 cc = ldg4(row + j0 + 2 * e), ss = ldg4(row + half + j0 + 2 * e);
+                const float4 cc = ld4<SHARED>(row + j0 + 2 * e), ss = ld4<SHARED>(row + half + j0 + 2 * e);
                 c[e] = ptx::pack2(cc.x, cc.y), c[e + 1] = ptx::pack2(cc.z, cc.w);
                 sn[e] = mul2(sg, ptx::pack2(ss.x, ss.y)), sn[e + 1] = mul2(sg, ptx::pack2(ss.z, ss.w));
             }
@@ -141,128 +147,194 @@ struct LaneDims {
     }
 };
 
-// A run: m rows from t0 on, into the rows from `at` on of block blk; lane i of the warp has the
-// rotation table's row of the window's token i - 1, and `first` is the run's first lane.
-template <int D, bool INTER>
-__device__ __forceinline__ void store_run(const Append8Args &a, const LaneDims<D, INTER> &dims, bool is_v, int g,
-                                          int64_t t0, int m, int64_t blk, int at, int64_t r, int first, int lane)
+// What the two warps of a run tell each other: their largest magnitudes and whether they met a value that is
+// not finite, in turn (one may be a run ahead).
+struct Meet {
+    float top[2][2];
+    int32_t odd[2][2];
+};
+
+// Takes eight values into the running maximum; odd becomes NaN with the first one that is not finite.
+__device__ __forceinline__ void take(const uint64_t (&z)[4], float &top, uint64_t &odd)
 {
-    constexpr int LPR = D / 8, RPP = 32 / LPR, NP = kBs / RPP;
-    const int sub = lane / LPR;
-    const uint16_t *src = (is_v ? a.v + g * D : a.k + g * D) + dims.d0;
-    const int64_t stride = is_v ? a.vs : a.ks;
-    uint4 u[NP];
 #pragma unroll
-    for (int p = 0; p < NP; ++p) {
-        const int i = p * RPP + sub;
-        u[p] = i < m ? *reinterpret_cast<const uint4 *>(src + (t0 + i) * stride) : make_uint4(0, 0, 0, 0);
+    for (int e = 0; e < 4; ++e) {
+        float lo, hi;
+        ptx::unpack2(z[e], lo, hi);
+        top = fmaxf(top, fmaxf(fabsf(lo), fabsf(hi)));
+        odd = ptx::fma2(z[e], 0ull, odd);
     }
-    float *sp = (is_v ? a.v_scale : a.k_scale) + blk * a.hkv + g;
-    const float old = at > 0 ? *sp : 0.f;
-    uint8_t *codes = (is_v ? a.vp : a.kp) + blk * a.block_stride + g * a.head_stride;
-    uint64_t z[NP][4];
-    if (is_v) {
-#pragma unroll
-        for (int p = 0; p < NP; ++p) pairs4(u[p], z[p], false);
-    } else {
-        uint4 uw, uwo;
-        dims.weights(a.kw, uw, uwo);
-#pragma unroll
-        for (int p = 0; p < NP; ++p) {
-            if (p * RPP >= m) break;
-            uint64_t c[4], sn[4];
-            const int64_t row = __shfl_sync(0xffffffffu, r, min(first + p * RPP + sub, first + m - 1));
-            dims.factors(a, row, c, sn);
-            float inv;
-            dims.turn(a, u[p], a.kw, uw, uwo, c, sn, z[p], inv);
-            const uint64_t i2 = ptx::pack2(inv, inv);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) z[p][e] = mul2(z[p][e], i2);
-        }
-    }
-    float top = 0.f;
-    bool odd = false;  // a value that is not finite
-#pragma unroll
-    for (int p = 0; p < NP; ++p) {
-        if (p * RPP + sub >= m) continue;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            float lo, hi;
-            ptx::unpack2(z[p][e], lo, hi);
-            if (finite(lo)) top = fmaxf(top, fabsf(lo)); else odd = true;
-            if (finite(hi)) top = fmaxf(top, fabsf(hi)); else odd = true;
-        }
-    }
-    top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));
-    odd = __any_sync(0xffffffffu, odd);
-    const float before = fabsf(old), s = fmaxf(before, scale_for(top)), inv = inverse_scale(s);
-    if (s > before && at > 0) {
-        const float ratio = before * inv;
-        for (int i = lane; i < at * D / 16; i += 32) {
-            uint4 *p = reinterpret_cast<uint4 *>(codes) + i;
-            uint4 w = *p;
-            w.x = rescale4(w.x, ratio), w.y = rescale4(w.y, ratio);
-            w.z = rescale4(w.z, ratio), w.w = rescale4(w.w, ratio);
-            *p = w;
-        }
-    }
-    const uint64_t i2 = ptx::pack2(inv, inv);
-#pragma unroll
-    for (int p = 0; p < NP; ++p) {
-        const int i = p * RPP + sub;
-        if (i >= m) continue;
-        uint32_t w[2] = {0u, 0u};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            float lo, hi;
-            ptx::unpack2(mul2(z[p][e], i2), lo, hi);
-            if (odd) {  // e4m3 has no infinity: NaN (0 times an infinity is one already)
-                if (!finite(lo)) lo = __uint_as_float(0x7fffffffu);
-                if (!finite(hi)) hi = __uint_as_float(0x7fffffffu);
-            }
-            w[e >> 1] |= e4m3x2(lo, hi) << (16 * (e & 1));
-        }
-        *reinterpret_cast<uint2 *>(codes + (at + i) * D + dims.d0) = make_uint2(w[0], w[1]);
-    }
-    // the sign says that the block may hold a NaN
-    if (lane == 0) *sp = odd || signbit(old) ? -s : s;
 }
 
-template <int D, bool INTER>
-__device__ __forceinline__ void store_window(const Append8Args &a, const LaneDims<D, INTER> &dims, int64_t task, int lane)
+// The largest of eight that are finite.
+__device__ __forceinline__ float finite_top(const uint64_t (&z)[4])
 {
-    const int h = (int)(task % (2 * a.hkv));
-    const bool is_v = h >= a.hkv;
-    const int g = is_v ? h - a.hkv : h;
+    float top = 0.f;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        float lo, hi;
+        ptx::unpack2(z[e], lo, hi);
+        if (finite(lo)) top = fmaxf(top, fabsf(lo));
+        if (finite(hi)) top = fmaxf(top, fabsf(hi));
+    }
+    return top;
+}
+
+// Codes of eight values times f; `odd`: NaN for those that are not finite, as e4m3 has no infinity.
+__device__ __forceinline__ uint2 codes8(const uint64_t (&z)[4], float f, bool odd)
+{
+    const uint64_t f2 = ptx::pack2(f, f);
+    uint32_t w[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        float lo, hi;
+        ptx::unpack2(mul2(z[e], f2), lo, hi);
+        if (odd) {  // (0 times an infinity is NaN already)
+            if (!finite(lo)) lo = __uint_as_float(0x7fffffffu);
+            if (!finite(hi)) hi = __uint_as_float(0x7fffffffu);
+        }
+        w[e] = e4m3x2(lo, hi);
+    }
+    return make_uint2(w[0] | w[1] << 16, w[2] | w[3] << 16);
+}
+
+// The runs that begin in a window, for four of the 2 hkv (K, then V) heads of a CTA; two warps share a run
+// of a head, eight rows each: alone, with all rows in registers, so few fit on an SM that the chain of loads
+// (slot, offset, table row) set the pace.  The CTA brings in the window's rows of the rotation table together,
+// while the first run's rows are on their way.
+// (LONG: windows of several rows.  With one each row's factors come straight from global memory.)
+template <int D, bool INTER, bool LONG>
+__device__ __forceinline__ void store_window(const Append8Args &a, const LaneDims<D, INTER> &dims, int64_t window, int h,
+                                             float *table, Meet *meet)
+{
+    constexpr int LPR = D / 8, RPP = 32 / LPR, NP = kBs / RPP / 2;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, half = warp & 1;
+    const bool mine = h < 2 * a.hkv, is_v = h >= a.hkv;
+    const int g = is_v ? h - a.hkv : h, row0 = half * (kBs / 2) + lane / LPR;
     // lane i: row t0 - 1 + i.  Runs that begin in the window (lanes 1 .. win) end by lane win + 15.
-    const int64_t t0 = task / (2 * a.hkv) * a.win, t = t0 - 1 + lane;
+    const int64_t t0 = window * a.win, t = t0 - 1 + lane;
     Place p{};
     p.slot = -1;
-    if (t >= 0 && t < a.rows && lane < a.win + kBs) p = place_of(a, t, h == 0 && lane >= 1 && lane <= a.win);
+    if (t >= 0 && t < a.rows && lane < a.win + kBs) p = place_of(a, t, h == 0 && half == 0 && lane >= 1 && lane <= a.win);
     const int64_t ahead = __shfl_up_sync(0xffffffffu, p.ok ? p.slot : -2, 1);
     const bool follows = p.ok && lane > 0 && ahead + 1 == p.slot && p.slot % kBs != 0;
-    const unsigned cont = __ballot_sync(0xffffffffu, follows);
+    const unsigned good = __ballot_sync(0xffffffffu, p.ok), cont = __ballot_sync(0xffffffffu, follows);
     unsigned heads = __ballot_sync(0xffffffffu, p.ok && !follows && lane >= 1 && lane <= a.win);
-    for (; heads; heads &= heads - 1) {
-        const int first = __ffs(heads) - 1;
-        // rows that follow, up to the end of the block
-        const int m = __ffs(~(cont >> (first + 1)));
-        const int64_t slot = __shfl_sync(0xffffffffu, p.slot, first);
-        store_run<D, INTER>(a, dims, is_v, g, t0 - 1 + first, m, slot / kBs, (int)(slot % kBs), p.r, first, lane);
+    const uint16_t *src = (is_v ? a.v : a.k) + g * D + dims.d0;
+    const int64_t stride = is_v ? a.vs : a.ks;
+    bool staged = false;
+    for (int turn = 0; heads; heads &= heads - 1, turn ^= 1) {
+        // m rows from lane `first` on go into the rows from `at` on of block blk
+        const int first = __ffs(heads) - 1, m = __ffs(~(cont >> (first + 1)));
+        const int64_t slot = __shfl_sync(0xffffffffu, p.slot, first), blk = slot / kBs;
+        const int at = (int)(slot % kBs);
+        uint4 u[NP];
+#pragma unroll
+        for (int k = 0; k < NP; ++k) {
+            const int i = k * RPP + row0;
+            u[k] = mine && i < m ? *reinterpret_cast<const uint4 *>(src + (t0 - 1 + first + i) * stride)
+                                 : make_uint4(0, 0, 0, 0);
+        }
+        float *sp = (is_v ? a.v_scale : a.k_scale) + blk * a.hkv + g;
+        const float old = mine && at > 0 ? *sp : 0.f;
+        if (LONG && !staged) {
+            staged = true;
+            if (a.rot > 0) {
+                for (int i = 1 + warp; i < a.win + kBs; i += kWarps) {
+                    const int64_t r = __shfl_sync(0xffffffffu, p.r, i);
+                    if ((good >> i & 1u) && lane < a.rot / 4)
+                        reinterpret_cast<float4 *>(table + i * D)[lane] = ldg4(a.cos_sin + r * a.rot + lane * 4);
+                }
+                __syncthreads();
+            }
+        }
+        if (!mine) continue;
+        // (rows past the run are zeros, and stay zeros)
+        float top = 0.f, inv[NP];
+        uint64_t z[NP][4], nan = 0ull;
+        bool odd_here = false;
+        if (is_v) {
+#pragma unroll
+            for (int k = 0; k < NP; ++k) {
+                pairs4(u[k], z[k], false);
+                take(z[k], top, nan);
+                inv[k] = 1.f;
+            }
+        } else {
+            uint4 uw, uwo;
+            dims.weights(a.kw, uw, uwo);
+#pragma unroll
+            for (int k = 0; k < NP; ++k) {
+                const int i = k * RPP + row0;
+                uint64_t c[4], sn[4];
+                const int from = first + min(i, m - 1);
+                const int64_t r = LONG ? 0 : __shfl_sync(0xffffffffu, p.r, from);
+                if (LONG)
+                    dims.template factors<true>(table + from * D, c, sn);
+                else
+                    dims.template factors<false>(a.cos_sin + r * a.rot, c, sn);
+                dims.turn(a, u[k], a.kw, uw, uwo, c, sn, z[k], inv[k]);
+                float of_row = 0.f;
+                take(z[k], of_row, nan);
+                top = fmaxf(top, of_row * inv[k]);
+                odd_here = odd_here || (i < m && !finite(inv[k]));
+            }
+        }
+        float lo, hi;
+        ptx::unpack2(nan, lo, hi);
+        odd_here = __any_sync(0xffffffffu, odd_here || lo != lo || hi != hi);
+        if (__builtin_expect(odd_here, 0)) {
+            top = 0.f;
+#pragma unroll
+            for (int k = 0; k < NP; ++k) {
+                const uint64_t i2 = ptx::pack2(inv[k], inv[k]);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) z[k][e] = mul2(z[k][e], i2);
+                inv[k] = 1.f;
+                top = fmaxf(top, finite_top(z[k]));
+            }
+        }
+        top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));
+        if (lane == 0) meet->top[turn][half] = top, meet->odd[turn][half] = odd_here;
+        ptx::named_barrier(1 + (warp >> 1), 64);
+        top = fmaxf(meet->top[turn][0], meet->top[turn][1]);
+        const bool odd = meet->odd[turn][0] || meet->odd[turn][1];
+        const float before = fabsf(old), s = fmaxf(before, scale_for(top)), f = inverse_scale(s);
+        uint8_t *codes = (is_v ? a.vp : a.kp) + blk * a.block_stride + g * a.head_stride;
+        if (s > before && at > 0) {
+            const float ratio = before * f;
+            for (int i = half * 32 + lane; i < at * D / 16; i += 64) {
+                uint4 *q = reinterpret_cast<uint4 *>(codes) + i;
+                uint4 w = *q;
+                w.x = rescale4(w.x, ratio), w.y = rescale4(w.y, ratio);
+                w.z = rescale4(w.z, ratio), w.w = rescale4(w.w, ratio);
+                *q = w;
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < NP; ++k) {
+            const int i = k * RPP + row0;
+            if (i < m) *reinterpret_cast<uint2 *>(codes + (at + i) * D + dims.d0) = codes8(z[k], inv[k] * f, odd_here);
+        }
+        // the sign says that the block may hold a NaN
+        if (half == 0 && lane == 0) *sp = odd || signbit(old) ? -s : s;
     }
 }
 
-template <int D, bool INTER>
-__global__ void __launch_bounds__(kThreads, 2) append8_kernel(const Append8Args a)
+template <int D, bool INTER, bool LONG>
+__global__ void __launch_bounds__(kThreads, LONG ? 3 : 2) append8_kernel(const Append8Args a)
 {
     constexpr int LPR = D / 8, RPP = 32 / LPR, HPW = kQPasses * RPP;  // query heads a warp takes
     const int lane = threadIdx.x & 31;
     const LaneDims<D, INTER> dims(a, lane);
     // launched as a programmatic dependent of what precedes it on the stream
     asm volatile("griddepcontrol.wait;" ::: "memory");
+    __shared__ Meet meet[kWarps / 2];
+    __shared__ __align__(16) float table[LONG ? (kMaxWin + kBs) * D : 4];
     if (blockIdx.x < a.kv_blocks) {
-        const int64_t task = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
-        if (task < ((int64_t)a.rows + a.win - 1) / a.win * (2 * a.hkv)) store_window<D, INTER>(a, dims, task, lane);
+        const int groups = (2 * a.hkv + kWarps / 2 - 1) / (kWarps / 2), pair = threadIdx.x >> 6;
+        store_window<D, INTER, LONG>(a, dims, blockIdx.x / groups, blockIdx.x % groups * (kWarps / 2) + pair, table,
+                               meet + pair);
         return;
     }
     const int parts = (a.hq + HPW - 1) / HPW;
@@ -279,7 +351,7 @@ __global__ void __launch_bounds__(kThreads, 2) append8_kernel(const Append8Args 
     const Place pl = place_of(a, t, false);
     if (!pl.ok) return;
     uint64_t c[4], sn[4];
-    dims.factors(a, pl.r, c, sn);
+    dims.template factors<false>(a.cos_sin + pl.r * a.rot, c, sn);
     uint4 uw, uwo;
     dims.weights(a.qw, uw, uwo);
     uint16_t *ring = nullptr;  // this token's row of the ring, if it is of the last W
@@ -307,13 +379,15 @@ cudaError_t launch(Append8Args &a, bool inter, bool with_queries, cudaStream_t s
 {
     constexpr int HPW = kQPasses * (32 / (D / 8));
     // short calls: a warp for each row that may begin a run; long ones look at several rows each
-    a.win = a.rows <= 512 ? 1 : a.rows / 16 < a.n ? 4 : 8;
-    const int64_t runs = ((int64_t)a.rows + a.win - 1) / a.win * (2 * a.hkv);
+    a.win = a.rows <= 512 ? 1 : a.rows / 16 < a.n ? 4 : kMaxWin;
+    static_assert(kMaxWin + kBs <= 32, "a lane for each row of a window's runs");
     const int64_t queries = with_queries ? (int64_t)a.rows * ((a.hq + HPW - 1) / HPW) : 0;
-    const int64_t kv = (runs + kWarps - 1) / kWarps, blocks = kv + (queries + kWarps - 1) / kWarps;
+    const int64_t kv = ((int64_t)a.rows + a.win - 1) / a.win * ((2 * a.hkv + kWarps / 2 - 1) / (kWarps / 2));
+    const int64_t blocks = kv + (queries + kWarps - 1) / kWarps;
     if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
     a.kv_blocks = (int32_t)kv;
-    const auto kern = inter ? append8_kernel<D, true> : append8_kernel<D, false>;
+    const auto kern = a.win > 1 ? (inter ? append8_kernel<D, true, true> : append8_kernel<D, false, true>)
+                                : (inter ? append8_kernel<D, true, false> : append8_kernel<D, false, false>);
     return launch_dependent(kern, dim3((unsigned)blocks), kThreads, 0, st, (const Append8Args)a);
 }
 
