@@ -107,7 +107,8 @@ cudaError_t launch_chunk8(const kara_cache8 *c, int32_t layer, const kara_tokens
                           int32_t bt_stride, const void *q, void *out, void *ws, int32_t *err, cudaStream_t st);
 cudaError_t launch_expand8(const kara_cache8 *c, const kara_cache *out, int32_t W, int32_t n, const int32_t *len,
                            const int32_t *bt, int32_t bt_stride, int32_t *out_table, int32_t *err, cudaStream_t st);
-cudaError_t launch_copy8(const kara_cache8 *c, const Geo &g, const SeqPlan *plan, const int32_t *kept,
-                         const int32_t *fresh, int64_t n_fresh, int32_t *err, cudaStream_t st);
+cudaError_t launch_compact8(const kara_cache8 *c, const Geo &g, SeqPlan *plan, int32_t *done, const int32_t *kept,
+                            const int32_t *fresh, int64_t n_fresh, int32_t *freed, int32_t *new_len, int32_t *table,
+                            int32_t *err, cudaStream_t st);
 
 }  // namespace kara

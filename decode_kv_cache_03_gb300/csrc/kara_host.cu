@@ -531,7 +531,7 @@ kara_status kara_expand8(const kara_cache8 *c, const kara_cache *out, int32_t W,
 size_t kara_compact8_workspace_size(const kara_cache8 *c, const kara_params *p, int32_t n)
 {
     if (check_params(p) != KARA_OK || check_cache8(c) != KARA_OK || n < 0) return 0;
-    return align256((size_t)(n > 0 ? n : 1) * sizeof(SeqPlan));
+    return align256((size_t)(n > 0 ? n : 1) * sizeof(SeqPlan)) + 256;  // the plan and a counter
 }
 
 kara_status kara_compact8(const kara_cache8 *c, const kara_params *p, int32_t n, const int32_t *len,
@@ -567,14 +567,10 @@ kara_status kara_compact8(const kara_cache8 *c, const kara_params *p, int32_t n,
     g.len = len;
     g.bt = block_table;
     g.nwin = (int64_t)n * c->num_layers * c->num_kv_heads;
-    cudaStream_t s = (cudaStream_t)stream;
     SeqPlan *plan = static_cast<SeqPlan *>(ws);
-    cudaError_t e = launch_plan(g, n_fresh, plan, err, s, true);
-    if (e == cudaSuccess) e = launch_fresh_check(g, plan, fresh, n_fresh, err, s, true);
-    if (e == cudaSuccess) e = launch_kept_check(g, kept, err, s, true);
-    if (e == cudaSuccess) e = launch_copy8(c, g, plan, kept, fresh, n_fresh, err, s);
-    if (e == cudaSuccess) e = launch_commit(g, plan, fresh, freed, new_len, block_table, err, s, true);
-    return cuda_status(e);
+    int32_t *done = at<int32_t>(ws, align256((size_t)n * sizeof(SeqPlan)));
+    return cuda_status(launch_compact8(c, g, plan, done, kept, fresh, n_fresh, freed, new_len, block_table, err,
+                                       (cudaStream_t)stream));
 }
 
 kara_status kara_select(const kara_params *p, int64_t n_windows, const float *scores, int32_t *cand,

@@ -58,12 +58,10 @@ __device__ int block_excl_scan(int v, int *scratch /* >= 33 ints */, int *total)
 
 // One block computes every sequence's plan and the offsets of its fresh and
 // freed ids (exclusive prefix sums in sequence order).
-__global__ void __launch_bounds__(kPlanThreads) plan_kernel(Geo g, int64_t n_fresh, SeqPlan *plan,
-                                                            int32_t *err)
+__device__ void plan_all(const Geo &g, int64_t n_fresh, SeqPlan *plan, int32_t *err)
 {
     __shared__ int scratch[33];
     __shared__ long long carry_new, carry_old;
-    dependent_wait();
     if (threadIdx.x == 0) { carry_new = 0; carry_old = 0; }
     __syncthreads();
     for (int base = 0; base < g.n; base += blockDim.x) {
@@ -96,6 +94,13 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(Geo g, int64_t n_fre
         __syncthreads();
     }
     if (threadIdx.x == 0 && carry_new > n_fresh) set_err(err, KARA_ENOBLOCKS);
+}
+
+__global__ void __launch_bounds__(kPlanThreads) plan_kernel(Geo g, int64_t n_fresh, SeqPlan *plan,
+                                                            int32_t *err)
+{
+    dependent_wait();
+    plan_all(g, n_fresh, plan, err);
 }
 
 // The inputs the copy must not run with, checked before it writes anything:
@@ -179,6 +184,44 @@ __global__ void __launch_bounds__(kChkThreads) kept_check_kernel(int64_t n, int 
     }
 }
 
+// The plan and the checks (of kept rows if there are any) of a small batch in one launch of one block, and a
+// zero in *done: what these compare is little, and three launches of a few microseconds are most of a small
+// compaction.
+__global__ void __launch_bounds__(kPlanThreads) prepare_kernel(Geo g, const int32_t *__restrict__ kept,
+                                                               const int32_t *__restrict__ fresh, int64_t n_fresh,
+                                                               SeqPlan *plan, int32_t *done, int32_t *err)
+{
+    dependent_wait();
+    if (threadIdx.x == 0) *done = 0;
+    plan_all(g, n_fresh, plan, err);
+    __syncthreads();
+    const SeqPlan last = plan[g.n - 1];
+    const int64_t F = (int64_t)last.off_new + last.n_new, P = F + (int64_t)g.n * g.bt_stride;
+    for (int64_t p = threadIdx.x; F <= n_fresh && p < P; p += kPlanThreads) {
+        int32_t v = 0;
+        int64_t lim = 0;
+        if (p < F) {
+            v = fresh[p];
+            lim = p;
+            if (v < 0 || v >= g.num_blocks) atomicCAS(err, 0, KARA_EBADBLOCK);
+        } else {
+            const int64_t q = p - F, L = g.len[q / g.bt_stride];
+            if (L > 0 && q % g.bt_stride < (L + g.bs - 1) / g.bs) {
+                v = g.bt[q];
+                lim = F;
+            }
+        }
+        bool dup = false;
+        for (int64_t i = 0; i < lim; ++i) dup |= fresh[i] == v;
+        if (dup) record_dup(err);
+    }
+    __syncthreads();
+    for (int64_t i = threadIdx.x; kept && i < g.nwin * g.R; i += kPlanThreads) {
+        const int32_t k = kept[i];
+        if (k < 0 || k >= g.C || (i % g.R > 0 && kept[i - 1] >= k)) set_err(err, KARA_EINVAL);
+    }
+}
+
 // One block per (window, K|V): copies o + R + B rows of D bf16 with 16-byte
 // vector loads/stores, old rows read through the old table, new rows written
 // into the sequence's fresh blocks.
@@ -251,19 +294,7 @@ __global__ void __launch_bounds__(256) commit_kernel(Geo g, const SeqPlan *__res
     const int s = blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
     const int lane = threadIdx.x & 31;
     if (s >= g.n) return;
-    const int32_t e = *err;
-    const SeqPlan p = plan[s];
-    if (e != 0 || p.p0 < 0) {
-        if (lane == 0) new_len[s] = g.len[s];
-        return;
-    }
-    int32_t *row = bt + (int64_t)s * g.bt_stride + p.p0;
-    for (int t = lane; t < p.n_old; t += 32) {
-        const int32_t old = row[t];
-        freed[p.off_old + t] = old;
-        row[t] = t < p.n_new ? fresh[p.off_new + t] : -1;
-    }
-    if (lane == 0) new_len[s] = p.Lnew;
+    commit_sequence(g, plan[s], *err, fresh, freed, new_len, bt, s, lane, 32);
 }
 
 }  // namespace
@@ -271,6 +302,13 @@ __global__ void __launch_bounds__(256) commit_kernel(Geo g, const SeqPlan *__res
 cudaError_t launch_plan(const Geo &g, int64_t n_fresh, SeqPlan *plan, int32_t *err, cudaStream_t st, bool dependent)
 {
     return launch<Geo, int64_t, SeqPlan *, int32_t *>(dependent, plan_kernel, 1, kPlanThreads, st, g, n_fresh, plan, err);
+}
+
+cudaError_t launch_prepare(const Geo &g, const int32_t *kept, const int32_t *fresh, int64_t n_fresh, SeqPlan *plan,
+                           int32_t *done, int32_t *err, cudaStream_t st)
+{
+    return launch<Geo, const int32_t *, const int32_t *, int64_t, SeqPlan *, int32_t *, int32_t *>(
+        true, prepare_kernel, 1, kPlanThreads, st, g, kept, fresh, n_fresh, plan, done, err);
 }
 
 // The fresh-id check of the whole batch (before any copy of any group).

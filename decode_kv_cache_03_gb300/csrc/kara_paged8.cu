@@ -117,9 +117,12 @@ struct CompactArgs {
     float *scale[2];
     const SeqPlan *plan;
     const int32_t *kept, *fresh, *bt;
-    int64_t n_fresh, windows;
-    int32_t B, C, R, bt_stride, max_new;
+    int64_t n_fresh;
+    int32_t B, C, R, bt_stride;
     int32_t *err;
+    // the last block to finish commits, if `done` counts them
+    int32_t *done, *freed, *new_len, *table;
+    Geo g;
 };
 
 // Largest magnitude among four codes, as 16-bit pairs of even and odd bytes: codes without their sign order
@@ -142,36 +145,36 @@ __device__ __forceinline__ uint32_t shift4(uint32_t w, __half2 f)
     return a | (uint32_t)b << 16;
 }
 
-// A warp rebuilds one block of one head, K and V (they come from the same rows): window (s * layers + l) * hkv
-// + g, new block j.  The chain of loads plan, kept row, table entry, codes is long: all rows of both pools are in
-// flight at its end.  Conversions set the pace beside that (they run at 16 lanes a clock): the largest value
-// is found on the codes, and rows whose scale stays are copied as they are.
+// A warp rebuilds one block of one head, K and V (they come from the same rows): window blockIdx.x = (s * layers + l)
+// * hkv + g, new block j.  The chain of loads plan, kept row, table entry, codes is long, and many warps hide it (one
+// that took four blocks and looked up the next ones' rows ahead needed 111 registers: 162 us against 138).
+// Conversions set the pace beside that (they run at 16 lanes a clock): the largest value is found on the
+// codes, and rows whose scale stays are copied as they are.
 template <int D>
-__global__ void __launch_bounds__(kThreads) compact8_kernel(const CompactArgs a)
+__device__ __forceinline__ void rebuild(const CompactArgs &a)
 {
     constexpr int LPR = D / 16, RPP = 32 / LPR, NP = kBs / RPP;  // lanes per row, rows per pass, passes
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int64_t task = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5), window = task / a.max_new;
-    const int j = (int)(task % a.max_new), lane = threadIdx.x & 31;
-    if (window >= a.windows) return;
-    const int lh = (int)(window % a.in.heads), s = (int)(window / a.in.heads);
+    const uint32_t window = blockIdx.x;
+    const int lh = (int)(window % (uint32_t)a.in.heads), s = (int)(window / (uint32_t)a.in.heads);
+    const int j = blockIdx.y * (blockDim.x >> 5) + (threadIdx.x >> 5), lane = threadIdx.x & 31;
     const int32_t failed = *(volatile const int32_t *)a.err;
     const SeqPlan p = a.plan[s];
     // nothing is written once an earlier kernel (plan, checks) recorded an error
     if (failed != 0 || p.p0 < 0 || j >= p.n_new || (int64_t)p.off_new + p.n_new > a.n_fresh) return;
-    const int32_t to = a.fresh[p.off_new + j];
-    const int32_t *kept = a.kept + window * a.R, *bt = a.bt + (int64_t)s * a.bt_stride;
-    const int c = lane % LPR, x0 = (p.p0 + j) * kBs;
+    const int32_t dst = a.fresh[p.off_new + j];
+    const int32_t *kept = a.kept + (int64_t)window * a.R, *bt = a.bt + (int64_t)s * a.bt_stride;
+    const int c = lane % LPR, row = lane / LPR, x0 = (p.p0 + j) * kBs + row;
     int32_t id[NP], at[NP];
 #pragma unroll
     for (int i = 0; i < NP; ++i) {
-        const int x = x0 + i * RPP + lane / LPR;
+        const int x = x0 + i * RPP;
         int old = x;
         if (x >= p.ws) old = x < p.ws + a.R ? p.ws + min(max(kept[x - p.ws], 0), a.C - 1) : p.L - a.B + (x - p.ws - a.R);
-        at[i] = old % kBs * D + c * 16;
-        id[i] = x < p.Lnew ? bt[old / kBs] : -2;
+        at[i] = (old & (kBs - 1)) * D + c * 16;
+        id[i] = x < p.Lnew ? bt[(uint32_t)old / kBs] : -2;
     }
-    if (to < 0 || to >= a.in.num_blocks) return;  // recorded by the check
+    if (dst < 0 || dst >= a.in.num_blocks) return;  // recorded by the check
+    const int64_t head = a.in.slice(lh, 0), head_scale = a.in.scale_at(lh, 0);
     uint4 w[2][NP];
     float f[2][NP];
 #pragma unroll
@@ -183,8 +186,8 @@ __global__ void __launch_bounds__(kThreads) compact8_kernel(const CompactArgs a)
             w[k][i] = make_uint4(0, 0, 0, 0);
             f[k][i] = 0.f;
             if (!in) continue;
-            w[k][i] = *reinterpret_cast<const uint4 *>(a.in.codes[k] + a.in.slice(lh, id[i]) + at[i]);
-            f[k][i] = a.in.scale[k][a.in.scale_at(lh, id[i])];
+            w[k][i] = *reinterpret_cast<const uint4 *>(a.in.codes[k] + head + id[i] * a.in.block_stride + at[i]);
+            f[k][i] = a.in.scale[k][head_scale + (int64_t)id[i] * a.in.hkv];
         }
     }
 #pragma unroll
@@ -221,7 +224,7 @@ __global__ void __launch_bounds__(kThreads) compact8_kernel(const CompactArgs a)
         }
         top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));
         const float sc = scale_for(top), inv = inverse_scale(sc);
-        uint8_t *out = a.codes[k] + a.in.slice(lh, to) + c * 16;
+        uint8_t *out = a.codes[k] + head + dst * a.in.block_stride + row * D + c * 16;
 #pragma unroll
         for (int i = 0; i < NP; ++i) {
             const float ratio = f[k][i] * inv;
@@ -235,10 +238,28 @@ __global__ void __launch_bounds__(kThreads) compact8_kernel(const CompactArgs a)
                     w[k][i].z = shift4(w[k][i].z, g), w[k][i].w = shift4(w[k][i].w, g);
                 }
             }
-            if (id[i] != -2) *reinterpret_cast<uint4 *>(out + (i * RPP + lane / LPR) * D) = w[k][i];
+            if (id[i] != -2) *reinterpret_cast<uint4 *>(out + i * RPP * D) = w[k][i];
         }
-        if (lane == 0) a.scale[k][a.in.scale_at(lh, to)] = odd ? -sc : sc;
+        if (lane == 0) a.scale[k][head_scale + (int64_t)dst * a.in.hkv] = odd ? -sc : sc;
     }
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 4) compact8_kernel(const CompactArgs a)
+{
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    rebuild<D>(a);
+    if (!a.done) return;
+    __shared__ bool last;
+    __threadfence();
+    __syncthreads();
+    if (threadIdx.x == 0) last = atomicAdd(a.done, 1) == (int32_t)(gridDim.x * gridDim.y) - 1;
+    __syncthreads();
+    if (!last) return;
+    __threadfence();
+    const int32_t error = *(volatile const int32_t *)a.err;
+    for (int s = threadIdx.x >> 5; s < a.g.n; s += blockDim.x >> 5)
+        commit_sequence(a.g, a.plan[s], error, a.fresh, a.freed, a.new_len, a.table, s, threadIdx.x & 31, 32);
 }
 
 Pool8 pool8(const kara_cache8 *c)
@@ -271,22 +292,46 @@ cudaError_t launch_expand8(const kara_cache8 *c, const kara_cache *out, int32_t 
     return launch_dependent(kern, dim3((unsigned)x, (unsigned)y), kThreads, 0, st, (const ExpandArgs)a);
 }
 
-cudaError_t launch_copy8(const kara_cache8 *c, const Geo &g, const SeqPlan *plan, const int32_t *kept,
-                         const int32_t *fresh, int64_t n_fresh, int32_t *err, cudaStream_t st)
+// Comparisons of ids up to which one block plans and compares them in one launch, and kept entries up to which
+// it checks those too: the copy's launch is then the other one of the call.  (One sequence of one layer, captured:
+// 11.9 us in five launches, 9.5 in two.)
+constexpr int64_t kSmallCompare = 1 << 21, kSmallKept = 1 << 14;
+
+cudaError_t launch_compact8(const kara_cache8 *c, const Geo &g, SeqPlan *plan, int32_t *done, const int32_t *kept,
+                            const int32_t *fresh, int64_t n_fresh, int32_t *freed, int32_t *new_len, int32_t *table,
+                            int32_t *err, cudaStream_t st)
 {
     CompactArgs a;
     a.in = pool8(c);
     a.codes[0] = static_cast<uint8_t *>(c->k), a.codes[1] = static_cast<uint8_t *>(c->v);
     a.scale[0] = c->k_scale, a.scale[1] = c->v_scale;
     a.plan = plan, a.kept = kept, a.fresh = fresh, a.bt = g.bt;
-    a.n_fresh = n_fresh, a.windows = g.nwin;
+    a.n_fresh = n_fresh;
     a.B = g.B, a.C = g.C, a.R = g.R, a.bt_stride = g.bt_stride;
-    a.max_new = (kBs - 1 + g.R + g.B + kBs - 1) / kBs;  // the window may start at any row of a block
+    const int max_new = (kBs - 1 + g.R + g.B + kBs - 1) / kBs;  // the window may start at any row of a block
     a.err = err;
-    const int64_t blocks = (a.windows * a.max_new + kThreads / 32 - 1) / (kThreads / 32);
-    if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+    a.freed = freed, a.new_len = new_len, a.table = table;
+    a.g = g;
+    // up to eight new blocks of a window to a CTA, evenly
+    const int parts = (max_new + kThreads / 32 - 1) / (kThreads / 32), warps = (max_new + parts - 1) / parts;
+    if (g.nwin * parts > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+    const dim3 grid((unsigned)g.nwin, (unsigned)parts);
+    const int64_t most = (int64_t)g.n * max_new, used = most < n_fresh ? most : n_fresh;
+    const bool one_block = (used + (int64_t)g.n * g.bt_stride) * used <= kSmallCompare;
+    const bool small = one_block && g.nwin * g.R <= kSmallKept;
+    a.done = small ? done : nullptr;
+    cudaError_t e = cudaSuccess;
+    if (one_block) {
+        e = launch_prepare(g, small ? kept : nullptr, fresh, n_fresh, plan, done, err, st);
+    } else {
+        e = launch_plan(g, n_fresh, plan, err, st, true);
+        if (e == cudaSuccess) e = launch_fresh_check(g, plan, fresh, n_fresh, err, st, true);
+    }
+    if (e == cudaSuccess && !small) e = launch_kept_check(g, kept, err, st, true);
     const auto kern = g.D == 128 ? compact8_kernel<128> : compact8_kernel<64>;
-    return launch_dependent(kern, dim3((unsigned)blocks), kThreads, 0, st, (const CompactArgs)a);
+    if (e == cudaSuccess) e = launch_dependent(kern, grid, 32 * warps, 0, st, (const CompactArgs)a);
+    if (e == cudaSuccess && !small) e = launch_commit(g, plan, fresh, freed, new_len, table, err, st, true);
+    return e;
 }
 
 }  // namespace kara

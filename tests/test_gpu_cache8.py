@@ -718,7 +718,8 @@ def run_compact(lengths, bt, fresh, k, ks, v, vs, kept, W, B, R, err=None):
 
 @pytest.mark.parametrize("W,B,R,hkv,d,layers,lengths", [
     (64, 16, 16, 2, 64, 1, [250]), (64, 0, 1, 2, 128, 2, [64, 79, 300]), (128, 63, 30, 3, 64, 2, [128, 143, 144, 500]),
-    (512, 64, 89, 8, 128, 2, [512, 1000]), (192, 16, 176, 1, 128, 3, [200, 333])])
+    (512, 64, 89, 8, 128, 2, [512, 1000]), (192, 16, 176, 1, 128, 3, [200, 333]),
+    (64, 16, 16, 8, 64, 40, [70, 64, 1000, 255])])   # the last: more than one block compares
 def test_compact_matches_plain(W, B, R, hkv, d, layers, lengths):
     """Rebuilt blocks, their scales, tables, freed ids and lengths; NaN codes mark their new block."""
     r = np.random.default_rng(W + B)
@@ -762,12 +763,15 @@ def test_compact_matches_plain(W, B, R, hkv, d, layers, lengths):
 
 @pytest.mark.parametrize("what", ["fresh twice", "fresh listed", "fresh outside", "few", "kept order", "kept range",
                                   "short", "earlier", "old outside"])
-def test_compact_refuses_on_the_device(what):
-    """The statuses of kara_compact, and no block of the pools written (but for an old block met while copying)."""
+@pytest.mark.parametrize("layers,width", [(2, 0), (160, 0), (2, 80000)])
+def test_compact_refuses_on_the_device(what, layers, width):
+    """The statuses of kara_compact, and no block of the pools written (but for an old block met while copying);
+    checked by one block, kept rows by several, or everything by several (a wide table)."""
     kara = lib()
     W, B, R = 64, 16, 20
-    lengths, bt, fresh, k, ks, v, vs = window_case(3, [100, 200, 300], W, 2, 64, 2, extra=40)
-    kept = np.broadcast_to(np.arange(R, dtype=np.int32), (3, 2, 2, R)).copy()
+    lengths, bt, fresh, k, ks, v, vs = window_case(3, [100, 200, 300], W, 2, 64, layers, extra=40)
+    bt = np.concatenate([bt, np.full((3, width), -1, np.int32)], 1)
+    kept = np.broadcast_to(np.arange(R, dtype=np.int32), (3, layers, 2, R)).copy()
     err = None
     if what == "fresh twice":
         fresh[4], want = fresh[1], kara.EDUPBLOCK
