@@ -294,8 +294,8 @@ cudaError_t launch_expand8(const kara_cache8 *c, const kara_cache *out, int32_t 
 
 // Comparisons of ids up to which one block plans and compares them in one launch, and kept entries up to which
 // it checks those too: the copy's launch is then the other one of the call.  (One sequence of one layer, captured:
-// 11.9 us in five launches, 9.5 in two.)
-constexpr int64_t kSmallCompare = 1 << 21, kSmallKept = 1 << 14;
+// 11.9 us in five launches, 8.6 in two; 1.7 million comparisons in one block: 20 us more than in several.)
+constexpr int64_t kSmallCompare = 1 << 19, kSmallKept = 1 << 14;
 
 cudaError_t launch_compact8(const kara_cache8 *c, const Geo &g, SeqPlan *plan, int32_t *done, const int32_t *kept,
                             const int32_t *fresh, int64_t n_fresh, int32_t *freed, int32_t *new_len, int32_t *table,
