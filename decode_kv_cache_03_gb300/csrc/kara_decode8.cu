@@ -77,10 +77,20 @@ struct Shared {
     uint64_t full[kStages], empty[kStages];
     int32_t blk[kBlocks];             // physical ids of the split's blocks; -1: outside the pool
     float ks[kBlocks], vs[kBlocks];   // their scales
-    float2 stat[8];                   // per head: (max, sum) of the split in the log2 domain
-    float up[8], down[8];             // per head: the power of two that brings the weights to f16, its inverse
+    float most[kNC][8], sum[kNC][8], top[kNC][8];  // each warp's part: largest logit (in the log2 domain), sum
+                                                   // of weights, largest weight times scale
     int32_t abort;
 };
+
+// The warps' parts of a head's value, joined in their order.
+template <class F>
+__device__ __forceinline__ float over_warps(const float (&x)[kNC][8], int h, F join)
+{
+    float v = x[0][h];
+#pragma unroll
+    for (int w = 1; w < kNC; ++w) v = join(v, x[w][h]);
+    return v;
+}
 
 // Bounded wait on phase `parity` of `bar`.  Gives up after limit_ns, or when
 // another warp of the CTA gave up, recording KARA_ETIMEOUT.
@@ -162,6 +172,26 @@ template <int G>
 constexpr size_t smem_bytes()
 {
     return 1024 + (size_t)kStages * kStageBytes + sizeof(float) * G * kLs + sizeof(Shared);
+}
+
+// The weighted sum of a block of V: chunks of 16 dims, even dims in the upper eight rows of the product, odd dims in
+// the lower; MASKED: keys 2tq, 2tq + 1 and those eight further on under lo and hi.
+template <int NC, bool MASKED>
+__device__ __forceinline__ void weigh(float (&acc)[NC][4], uint32_t sb, uint32_t b0, uint32_t b1, uint32_t lo, uint32_t hi)
+{
+#pragma unroll
+    for (int c = 0; c < NC; c += 2) {
+        uint32_t r[4];
+        ldsm_x4_t(sb ^ (c << 4), r);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            // (two dims of a key, two dims of the next) -> (a dim of both keys, the other of both)
+            const uint32_t u = __byte_perm(MASKED ? r[2 * e] & lo : r[2 * e], 0u, 0x3120);
+            const uint32_t v = __byte_perm(MASKED ? r[2 * e + 1] & hi : r[2 * e + 1], 0u, 0x3120);
+            mma_16816(acc[c + e], f16_of_e4m3x2(u), f16_of_e4m3x2(u >> 16), f16_of_e4m3x2(v),
+                      f16_of_e4m3x2(v >> 16), b0, b1);
+        }
+    }
 }
 
 template <int D, int G>
@@ -294,21 +324,23 @@ __global__ void __launch_bounds__(kThreads, min_ctas<G>())
     // this lane's row of the ldmatrix tiles: tiles 0 and 1 are rows 0-7 and 8-15 of a chunk, 2 and 3 of
     // the next; 16-byte chunk c of row t lies at chunk c ^ (t & 7) (D = 64: c ^ (t / 2 & 3))
     const int lt = lane & 15, lc = lane >> 4, lx = D == 128 ? lt & 7 : lt >> 1 & 3;
+    const uint32_t lane_at = ptx::smem_u32(ring) + lt * D + ((lc ^ lx) << 4);  // chunk c + lc (c even): this ^ c << 4
 
     // ---- logits
+    float m0 = -INFINITY, m1 = -INFINITY;  // the largest of heads h0 and h0 + 1 (passing over a NaN)
     for (int i = cw; i < ns; i += kNC) {
         const int st = i % kStages;
         if (!dwait(ptx::smem_u32(&sh->full[st]), (i / kStages) & 1, sh, a.err, a.wait_ns)) break;
         float acc[BPS][4];
 #pragma unroll
         for (int b = 0; b < BPS; ++b) {
-            const uint32_t sb = ptx::smem_u32(ring + st * kStageBytes + b * BB) + lt * D;
+            const uint32_t sb = lane_at + st * kStageBytes + b * BB;
 #pragma unroll
             for (int e = 0; e < 4; ++e) acc[b][e] = 0.f;
 #pragma unroll
             for (int c = 0; c < NC; c += 2) {
                 uint32_t r[4];
-                ldsm_x4(sb + (((c + lc) ^ lx) << 4), r);
+                ldsm_x4(sb ^ (c << 4), r);
                 mma_16816(acc[b], f16_of_e4m3x2(r[0]), f16_of_e4m3x2(r[1]), f16_of_e4m3x2(r[0] >> 16),
                           f16_of_e4m3x2(r[1] >> 16), qb[c][0], qb[c][1]);
                 mma_16816(acc[b], f16_of_e4m3x2(r[2]), f16_of_e4m3x2(r[3]), f16_of_e4m3x2(r[2] >> 16),
@@ -325,44 +357,56 @@ __global__ void __launch_bounds__(kThreads, min_ctas<G>())
             if (x >= nk) continue;
             const bool in = sh->blk[blk] >= 0;  // a block outside the pool: zeros
             const float f = sh->ks[blk];
+            const auto put = [&](int h, int y, float l, float &most) {
+                logit[h * kLs + y] = l;
+                most = fmaxf(most, l);
+            };
             if (h0 < G) {
-                logit[h0 * kLs + x] = in ? acc[b][0] * f * f0 : 0.f;
-                if (x + 8 < nk) logit[h0 * kLs + x + 8] = in ? acc[b][2] * f * f0 : 0.f;
+                put(h0, x, in ? acc[b][0] * f * f0 : 0.f, m0);
+                if (x + 8 < nk) put(h0, x + 8, in ? acc[b][2] * f * f0 : 0.f, m0);
             }
             if (h0 + 1 < G) {
-                logit[(h0 + 1) * kLs + x] = in ? acc[b][1] * f * f1 : 0.f;
-                if (x + 8 < nk) logit[(h0 + 1) * kLs + x + 8] = in ? acc[b][3] * f * f1 : 0.f;
+                put(h0 + 1, x, in ? acc[b][1] * f * f1 : 0.f, m1);
+                if (x + 8 < nk) put(h0 + 1, x + 8, in ? acc[b][3] * f * f1 : 0.f, m1);
             }
         }
     }
+#pragma unroll
+    for (int o = 4; o < 32; o <<= 1) {
+        m0 = fmaxf(m0, __shfl_xor_sync(0xffffffffu, m0, o));
+        m1 = fmaxf(m1, __shfl_xor_sync(0xffffffffu, m1, o));
+    }
+    if (lane < 4) sh->most[cw][h0] = m0, sh->most[cw][h0 + 1] = m1;
     ptx::named_barrier(1, kNC * 32);
 
-    // ---- softmax of each head over the split (warp cw: heads cw, cw + kNC); what stays are the
-    // weights times V's scales
-    for (int h = cw; h < G; h += kNC) {
-        float *lr = logit + h * kLs;
-        float m = -INFINITY;
-        for (int x = lane; x < nk; x += 32) m = fmaxf(m, lr[x]);
+    // ---- softmax: a quarter of the keys to a warp, all heads; what stays are the weights times V's scales.
+    // (With a warp for a head three wait for the fifth head's, and the ring is full meanwhile.)
+    {
+        float z[G], top[G];
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-        float z = 0.f, top = 0.f;
-        for (int x = lane; x < nk; x += 32) {
-            const float p = ptx::ex2(lr[x] - m), w = p * sh->vs[x / kBlk];
-            lr[x] = w;
-            z += p;
-            top = fmaxf(top, w);
+        for (int h = 0; h < G; ++h) {
+            const float m = over_warps(sh->most, h, [](float x, float y) { return fmaxf(x, y); });
+            const float ref = m == -INFINITY ? 0.f : m;
+            float *lr = logit + h * kLs;
+            z[h] = 0.f, top[h] = 0.f;
+            for (int x = cw * (kSplit / kNC) + lane; x < min(nk, (cw + 1) * (kSplit / kNC)); x += 32) {
+                const float p = ptx::ex2(lr[x] - ref), w = p * sh->vs[x / kBlk];
+                lr[x] = w;
+                z[h] += p;
+                top[h] = fmaxf(top[h], w);
+            }
+            for (int x = nk + ctid; x < ns * BPS * kBlk; x += kNC * 32) lr[x] = 0.f;  // rows past the end weigh 0
         }
-        for (int x = nk + lane; x < ns * BPS * kBlk; x += 32) lr[x] = 0.f;  // rows past the end weigh 0
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-            z += __shfl_xor_sync(0xffffffffu, z, o);
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-        }
-        if (lane == 0) {
-            float up, down;
-            to_f16_range(top, up, down);
-            sh->stat[h] = make_float2(m, z), sh->up[h] = up, sh->down[h] = down;
-        }
+        for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+            for (int h = 0; h < G; ++h) {
+                z[h] += __shfl_xor_sync(0xffffffffu, z[h], o);
+                top[h] = fmaxf(top[h], __shfl_xor_sync(0xffffffffu, top[h], o));
+            }
+        if (lane == 0)
+#pragma unroll
+            for (int h = 0; h < G; ++h) sh->sum[cw][h] = z[h], sh->top[cw][h] = top[h];
     }
     ptx::named_barrier(1, kNC * 32);
 
@@ -372,7 +416,9 @@ __global__ void __launch_bounds__(kThreads, min_ctas<G>())
     for (int c = 0; c < NC; ++c)
 #pragma unroll
         for (int e = 0; e < 4; ++e) acc[c][e] = 0.f;
-    const float up = r8 < G ? sh->up[r8] : 0.f;
+    const auto most = [](float x, float y) { return fmaxf(x, y); };
+    float up, unused;
+    to_f16_range(over_warps(sh->top, min(r8, G - 1), most), up, unused);
     for (int i = cw; i < ns; i += kNC) {
         const int j = ns + i, st = j % kStages;
         if (!dwait(ptx::smem_u32(&sh->full[st]), (j / kStages) & 1, sh, a.err, a.wait_ns)) break;
@@ -390,24 +436,13 @@ __global__ void __launch_bounds__(kThreads, min_ctas<G>())
             // rows of the last block past the end hold whatever the block held (NaN
             // included): their halves of the fragments are zeroed
             const int tmax = nk - blk * kBlk;
-            uint32_t m_lo = 0xffffffffu, m_hi = 0xffffffffu;
-            if (tmax < kBlk) {
-                m_lo = (2 * tq < tmax ? 0x0000ffffu : 0u) | (2 * tq + 1 < tmax ? 0xffff0000u : 0u);
-                m_hi = (2 * tq + 8 < tmax ? 0x0000ffffu : 0u) | (2 * tq + 9 < tmax ? 0xffff0000u : 0u);
-            }
-            const uint32_t sb = ptx::smem_u32(ring + st * kStageBytes + b * BB) + lt * D;
-#pragma unroll
-            for (int c = 0; c < NC; c += 2) {
-                uint32_t r[4];
-                ldsm_x4_t(sb + (((c + lc) ^ lx) << 4), r);
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    // (two dims of a key, two dims of the next) -> (a dim of both keys, the other of both)
-                    const uint32_t u = __byte_perm(r[2 * e] & m_lo, 0u, 0x3120);
-                    const uint32_t v = __byte_perm(r[2 * e + 1] & m_hi, 0u, 0x3120);
-                    mma_16816(acc[c + e], f16_of_e4m3x2(u), f16_of_e4m3x2(u >> 16), f16_of_e4m3x2(v),
-                              f16_of_e4m3x2(v >> 16), b0, b1);
-                }
+            const uint32_t sb = lane_at + st * kStageBytes + b * BB;
+            if (tmax >= kBlk) {
+                weigh<NC, false>(acc, sb, b0, b1, 0u, 0u);
+            } else {
+                const uint32_t lo = (2 * tq < tmax ? 0x0000ffffu : 0u) | (2 * tq + 1 < tmax ? 0xffff0000u : 0u);
+                const uint32_t hi = (2 * tq + 8 < tmax ? 0x0000ffffu : 0u) | (2 * tq + 9 < tmax ? 0xffff0000u : 0u);
+                weigh<NC, true>(acc, sb, b0, b1, lo, hi);
             }
         }
         __syncwarp();
@@ -433,10 +468,13 @@ __global__ void __launch_bounds__(kThreads, min_ctas<G>())
             const float2 y = *reinterpret_cast<const float2 *>(red + (w * G + h) * D + d);
             v.x += y.x, v.y += y.y;
         }
-        const float f = sh->down[h];
+        float up, f;
+        to_f16_range(over_warps(sh->top, h, most), up, f);
         const int64_t row = (int64_t)s * a.hq + g * G + h, idx = row * a.max_splits + sp;
         *reinterpret_cast<float2 *>(a.part + idx * D + d) = make_float2(v.x * f, v.y * f);
-        if (d == 0) a.stat[idx] = sh->stat[h];
+        if (d == 0)
+            a.stat[idx] = make_float2(over_warps(sh->most, h, most),
+                                      over_warps(sh->sum, h, [](float x, float y) { return x + y; }));
     }
     // the merge kernel may be scheduled once every CTA of this grid got here
     // or exited; it still waits for this grid's completion before reading
@@ -455,10 +493,11 @@ __global__ void __launch_bounds__(D) decode8_merge_kernel(const Decode8Args a)
     const int64_t row = (int64_t)s * a.hq + h, base = row * a.max_splits;
     float M = -INFINITY;
     for (int sp = 0; sp < nsp; ++sp) M = fmaxf(M, a.stat[base + sp].x);
+    const float ref = M == -INFINITY ? 0.f : M;
     float den = 0.f, num = 0.f;
     for (int sp = 0; sp < nsp; ++sp) {
         const float2 st = a.stat[base + sp];
-        const float w = exp2f(st.x - M);
+        const float w = exp2f(st.x - ref);
         den = fmaf(st.y, w, den);
         num = fmaf(a.part[(base + sp) * D + d], w, num);
     }
