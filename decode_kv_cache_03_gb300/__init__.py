@@ -3,9 +3,9 @@
 The work runs in ``libkara.so`` (hand-written CUDA, C ABI in include/kara.h);
 ``decode_kv_cache_03_gb300.kara`` is its ctypes binding and raises on import if
 the library is missing.  ``decode_kv_cache_03_gb300.build`` compiles it.
-``Compressor`` wraps the workspace and error word for one cache.  Names are
-resolved lazily so that the build module can be imported before the library
-exists.
+``Compressor`` wraps the workspace and error word for one cache, ``Compressor8``
+those of a cache in 8 bits.  Names are resolved lazily so that the build module
+can be imported before the library exists.
 """
 from __future__ import annotations
 
@@ -14,6 +14,7 @@ import importlib
 _LAZY = {
     "kara": ("kara", None),
     "Compressor": ("compressor", "Compressor"),
+    "Compressor8": ("compressor", "Compressor8"),
     "periodic": ("periodic", None),
     "BlockPool": ("periodic", "BlockPool"),
     "PeriodicSchedule": ("periodic", "PeriodicSchedule"),
@@ -31,6 +32,14 @@ _LAZY = {
     "kara_append_kv": ("kara", "kara_append_kv"),
     "kara_chunk_attention": ("kara", "kara_chunk_attention"),
     "kara_chunk_workspace_size": ("kara", "kara_chunk_workspace_size"),
+    "kara_append_kv8": ("kara", "kara_append_kv8"),
+    "kara_decode_attention8": ("kara", "kara_decode_attention8"),
+    "kara_decode8_workspace_size": ("kara", "kara_decode8_workspace_size"),
+    "kara_chunk_attention8": ("kara", "kara_chunk_attention8"),
+    "kara_chunk8_workspace_size": ("kara", "kara_chunk8_workspace_size"),
+    "kara_expand8": ("kara", "kara_expand8"),
+    "kara_compact8": ("kara", "kara_compact8"),
+    "kara_compact8_workspace_size": ("kara", "kara_compact8_workspace_size"),
 }
 
 __all__ = sorted(_LAZY)

@@ -17,9 +17,11 @@ class Compressor:
 
     def __init__(self, k: torch.Tensor, v: torch.Tensor, num_q_heads: int, W: int, B: int, K: int, R: int,
                  lam: float = 0.1, score_mode: int = 0, select_mode: int = 0, chunk: int = 0):
-        self.k, self.v = k, v
-        self.cache = kara.cache(k, v, num_q_heads)
-        self.params = kara.params(W, B, K, R, lam, score_mode, select_mode, chunk)
+        self._keep(k, v, kara.cache(k, v, num_q_heads),
+                   kara.params(W, B, K, R, lam, score_mode, select_mode, chunk))
+
+    def _keep(self, k, v, cache, params):
+        self.k, self.v, self.cache, self.params = k, v, cache, params
         self._ws = torch.empty(0, dtype=torch.uint8, device=k.device)
         self._dws = torch.empty(0, dtype=torch.uint8, device=k.device)
         self._cws = torch.empty(0, dtype=torch.uint8, device=k.device)
@@ -93,3 +95,93 @@ class Compressor:
 
     def error(self, stream=None) -> int:
         return kara.kara_get_error(self.err, stream)
+
+
+def _pieces(sizes):
+    """Offsets of pieces of these byte sizes, each on 256 bytes, and the bytes of all."""
+    at, offsets = 0, []
+    for size in sizes:
+        offsets.append(at)
+        at += (size + 255) // 256 * 256
+    return offsets, at
+
+
+class Compressor8(Compressor):
+    """The same over an 8-bit cache (kara.cache8): pools of e4m3 codes, float scales for each block and head.
+
+    compress() brings the windows' keys back to bf16 in a workspace, scores them there and compacts the codes;
+    `windows` then describes those keys (what kara_compact_queries takes for the ring).  decode() and chunk()
+    give bf16.
+    """
+
+    def __init__(self, k: torch.Tensor, v: torch.Tensor, k_scale: torch.Tensor, v_scale: torch.Tensor,
+                 num_q_heads: int, W: int, B: int, K: int, R: int, lam: float = 0.1, score_mode: int = 0,
+                 select_mode: int = 0, chunk: int = 0):
+        self._keep(k, v, kara.cache8(k, v, k_scale, v_scale, num_q_heads),
+                   kara.params(W, B, K, R, lam, score_mode, select_mode, chunk))
+        self.k_scale, self.v_scale, self.windows = k_scale, v_scale, None
+        self._xws = torch.empty(0, dtype=torch.uint8, device=k.device)
+
+    def _window_cache(self, ws: torch.Tensor, n: int):
+        """The bf16 keys of n windows as a cache at the start of `ws`."""
+        c = self.cache
+        blocks = n * (self.params.W // c.block_size + 1)
+        shape = (c.num_layers, blocks, c.num_kv_heads, c.block_size, c.head_dim)
+        keys = ws[:2 * torch.Size(shape).numel()].view(torch.bfloat16).view(shape)
+        return kara.cache(keys, keys, c.num_q_heads)
+
+    def _compress_sizes(self, n: int, bt_stride: int):
+        """Bytes of a compression's window keys, their table, the scorer's workspace, scores, candidates, kept
+        rows and the compaction's workspace."""
+        c, p = self.cache, self.params
+        windows, slice_ = n * c.num_layers * c.num_kv_heads, c.block_size * c.head_dim * 2
+        cache16 = kara.Cache(c.k, c.v, 0, 0, 0, c.num_layers, c.num_blocks, c.num_kv_heads, c.num_q_heads, c.head_dim,
+                             c.block_size)
+        return (windows * (p.W // c.block_size + 1) * slice_, n * bt_stride * 4,
+                kara.kara_workspace_size(cache16, p, n), windows * (p.W - p.B) * 4, windows * p.K * 4,
+                windows * p.R * 4, kara.kara_compact8_workspace_size(c, p, n))
+
+    def workspace(self, n: int, stream=None, bt_stride: int = 1) -> torch.Tensor:
+        return self._space("_xws", _pieces(self._compress_sizes(n, bt_stride))[1], stream)
+
+    def compress(self, lengths, block_table, q, fresh, freed, new_len, scores=None, cand=None, kept=None,
+                 stream=None):
+        """Enqueue the whole step: expand, score, select, compact; block_table is rewritten in place on success."""
+        n, bt_stride = block_table.shape
+        if n == 0:
+            return
+        sizes = self._compress_sizes(n, bt_stride)
+        at, total = _pieces(sizes)
+        ws, err = self._space("_xws", total, stream), self._used("err", stream)
+        piece = [ws[a:a + size] for a, size in zip(at, sizes)]
+        c, p = self.cache, self.params
+        windows = (n, c.num_layers, c.num_kv_heads)
+        shaped = lambda x, i, t, last: piece[i].view(t).view(*windows, last) if x is None else x  # noqa: E731
+        table = piece[1].view(torch.int32).view(n, bt_stride)
+        scores, cand, kept = (shaped(scores, 3, torch.float32, p.W - p.B), shaped(cand, 4, torch.int32, p.K),
+                              shaped(kept, 5, torch.int32, p.R))
+        self.windows = self._window_cache(piece[0], n)
+        with torch.cuda.stream(stream):
+            err.zero_()
+        kara.kara_expand8(c, self.windows, p.W, lengths, block_table, table, err, stream)
+        kara.kara_score(self.windows, p, kara.batch(lengths, table, q), scores, piece[2], err, stream)
+        kara.kara_select(p, n * c.num_layers * c.num_kv_heads, scores, cand, kept, stream)
+        kara.kara_compact8(c, p, lengths, block_table, kept, fresh, freed, new_len, piece[6], err, stream)
+
+    def decode(self, layer: int, lengths, block_table, q, out, stream=None):
+        """Enqueue decode attention for one layer over the paged cache; out is bf16, zeros for an empty sequence."""
+        n, bt_stride = block_table.shape
+        ws = self._space("_dws", kara.kara_decode8_workspace_size(self.cache, n, bt_stride), stream)
+        kara.kara_decode_attention8(self.cache, layer, lengths, block_table, q, out, ws, self._used("err", stream),
+                                    stream)
+
+    def append(self, layer: int, t, rope, q, k, v, q_out, ring=None, stream=None):
+        """Enqueue norms, rotation, rounding to codes and the cache write of the new tokens for one layer;
+        with `ring` (the q that compress() takes) the window queries are kept too."""
+        kara.kara_append_kv8(self.cache, layer, t, rope, q, k, v, q_out, self._used("err", stream), ring, stream)
+
+    def chunk(self, layer: int, t, block_table, q, out, stream=None):
+        """Enqueue causal attention of the new tokens for one layer over the paged cache, after append() wrote
+        their K and V.  The calls of one Compressor8 share a workspace, as those of a Compressor do."""
+        ws = self._space("_cws", kara.kara_chunk8_workspace_size(self.cache, t.n, t.rows), stream)
+        kara.kara_chunk_attention8(self.cache, layer, t, block_table, q, out, ws, self._used("err", stream), stream)

@@ -73,7 +73,7 @@ def compress_selected(comp, seqs, lengths_host, table_host, q_window, pool: Bloc
                       scores=None, kept=None):
     """Compress the trailing windows of `seqs` with kara_compress_batch.
 
-    comp: a Compressor; q_window: device bf16 [len(seqs)][layers][Hq][W][D].
+    comp: a Compressor or Compressor8; q_window: device bf16 [len(seqs)][layers][Hq][W][D].
     Updates lengths_host / table_host in place and returns
     (freed ids, device status).  events: optional (start, end) CUDA events
     recorded around the library call only; scores / kept: optional device
