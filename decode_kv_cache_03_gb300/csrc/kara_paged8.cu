@@ -171,7 +171,7 @@ __device__ __forceinline__ void rebuild(const CompactArgs &a)
         int old = x;
         if (x >= p.ws) old = x < p.ws + a.R ? p.ws + min(max(kept[x - p.ws], 0), a.C - 1) : p.L - a.B + (x - p.ws - a.R);
         at[i] = (old & (kBs - 1)) * D + c * 16;
-        id[i] = x < p.Lnew ? bt[(uint32_t)old / kBs] : -2;
+        id[i] = x < p.Lnew ? max(bt[(uint32_t)old / kBs], -1) : -2;  // (-2: past the end)
     }
     if (dst < 0 || dst >= a.in.num_blocks) return;  // recorded by the check
     const int64_t head = a.in.slice(lh, 0), head_scale = a.in.scale_at(lh, 0);

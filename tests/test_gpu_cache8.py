@@ -762,7 +762,7 @@ def test_compact_matches_plain(W, B, R, hkv, d, layers, lengths):
 
 
 @pytest.mark.parametrize("what", ["fresh twice", "fresh listed", "fresh outside", "few", "kept order", "kept range",
-                                  "short", "earlier", "old outside"])
+                                  "short", "earlier", "old outside", "old -2"])
 @pytest.mark.parametrize("layers,width", [(2, 0), (160, 0), (2, 80000)])
 def test_compact_refuses_on_the_device(what, layers, width):
     """The statuses of kara_compact, and no block of the pools written (but for an old block met while copying);
@@ -790,11 +790,11 @@ def test_compact_refuses_on_the_device(what, layers, width):
     elif what == "earlier":
         err, want = torch.full((1,), kara.ETIMEOUT, dtype=torch.int32, device=DEV), kara.ETIMEOUT
     else:
-        bt[1, 9], want = -3, kara.EBADBLOCK
+        bt[1, 9], want = -2 if what == "old -2" else -3, kara.EBADBLOCK
     st, got, table, freed, new_len = run_compact(lengths, bt, fresh, k, ks, v, vs, kept, W, B, R, err)
     assert st == want
     assert np.array_equal(table, bt) and (freed == -7).all() and np.array_equal(new_len, lengths)
-    if what == "old outside":   # live blocks are never written
+    if what.startswith("old"):   # live blocks are never written
         old = [int(b) for b in bt.ravel() if 0 <= b < k.shape[1]]
         assert torch.equal(got[0][:, old], k[:, old]) and torch.equal(got[3][:, old], vs[:, old])
     else:
