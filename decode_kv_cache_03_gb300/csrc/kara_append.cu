@@ -20,7 +20,6 @@
 // passes a warp (8192 tokens, 40/8 heads of 128, with the ring: 70 us), staged
 // 5.4 TB/s (52 us).  Pairs of neighbours take 50 us, a rotation of half the dims 56
 // (54), the same at D = 64 with as many heads 32 us (4.3 TB/s).
-#include "kara_cache8.cuh"
 #include "kara_rows.cuh"
 #include "kara_sm100.cuh"
 #include "kara_tokens.cuh"
@@ -281,10 +280,8 @@ __global__ void __launch_bounds__(kTokThreads, 4) append_staged_kernel(const App
                     m.page = page, m.ring = ring, m.row = (int32_t)t;
                     ptx::mbar_arrive_expect_tx(fb, (uint32_t)stage_bytes);
                     bulk_load(d, a.q + t * a.qs, a.hq * D * 2, fb);
-                    if (a.hkv > 0) {
-                        bulk_load(d + a.hq * D * 2, a.k + t * a.ks, a.hkv * D * 2, fb);
-                        bulk_load(d + (a.hq + a.hkv) * D * 2, a.v + t * a.vs, a.hkv * D * 2, fb);
-                    }
+                    bulk_load(d + a.hq * D * 2, a.k + t * a.ks, a.hkv * D * 2, fb);
+                    bulk_load(d + (a.hq + a.hkv) * D * 2, a.v + t * a.vs, a.hkv * D * 2, fb);
                     if (a.rot) bulk_load(d + row_bytes, a.cos_sin + r * a.rot, a.rot * 4, fb);
                 }
                 __syncwarp();
@@ -442,17 +439,25 @@ cudaError_t launch(const AppArgs &a, cudaStream_t st)
     return launch_dependent(kern, dim3((unsigned)grid), kTokThreads, smem, st, a, stages);
 }
 
-// A call's arguments but for keys, values and the pools.
-template <class Cache>
-AppArgs query_args(const Cache *c, int32_t layer, const kara_tokens *t, const kara_rope *r, const void *q,
-                   int64_t q_stride, void *q_out, void *ring, int32_t W, int32_t *err)
+}  // namespace
+
+cudaError_t launch_append(const kara_cache *c, int32_t layer, const kara_tokens *t, const kara_rope *r, const void *q,
+                          int64_t q_stride, const void *k, int64_t k_stride, const void *v, int64_t v_stride,
+                          void *q_out, void *ring, int32_t W, int32_t *err, cudaStream_t st)
 {
-    AppArgs a = {};
+    const int D = c->head_dim;
+    AppArgs a;
     a.q = static_cast<const uint16_t *>(q);
-    a.qs = q_stride;
+    a.k = static_cast<const uint16_t *>(k);
+    a.v = static_cast<const uint16_t *>(v);
+    a.qs = q_stride, a.ks = k_stride, a.vs = v_stride;
     a.q_out = static_cast<uint16_t *>(q_out);
+    a.kp = static_cast<uint16_t *>(c->k) + (int64_t)layer * c->layer_stride;
+    a.vp = static_cast<uint16_t *>(c->v) + (int64_t)layer * c->layer_stride;
+    a.block_stride = c->block_stride;
+    a.head_stride = c->head_stride;
     a.W = ring ? W : 1;
-    a.ring_head = (int64_t)W * c->head_dim;
+    a.ring_head = (int64_t)W * D;
     a.ring_seq = (int64_t)c->num_layers * c->num_q_heads * a.ring_head;
     a.ring = ring ? static_cast<uint16_t *>(ring) + (int64_t)layer * c->num_q_heads * a.ring_head : nullptr;
     a.qw = static_cast<const uint16_t *>(r->q_weight);
@@ -472,36 +477,11 @@ AppArgs query_args(const Cache *c, int32_t layer, const kara_tokens *t, const ka
     a.rows = t->rows;
     a.num_blocks = c->num_blocks;
     a.hq = c->num_q_heads;
+    a.hkv = c->num_kv_heads;
     a.n_pos = r->rot_dim > 0 ? r->n_pos : 1;
     a.rot = r->rot_dim;
     a.inter = r->interleaved;
-    return a;
-}
-
-}  // namespace
-
-cudaError_t launch_append(const kara_cache *c, int32_t layer, const kara_tokens *t, const kara_rope *r, const void *q,
-                          int64_t q_stride, const void *k, int64_t k_stride, const void *v, int64_t v_stride,
-                          void *q_out, void *ring, int32_t W, int32_t *err, cudaStream_t st)
-{
-    AppArgs a = query_args(c, layer, t, r, q, q_stride, q_out, ring, W, err);
-    a.k = static_cast<const uint16_t *>(k);
-    a.v = static_cast<const uint16_t *>(v);
-    a.ks = k_stride, a.vs = v_stride;
-    a.kp = static_cast<uint16_t *>(c->k) + (int64_t)layer * c->layer_stride;
-    a.vp = static_cast<uint16_t *>(c->v) + (int64_t)layer * c->layer_stride;
-    a.block_stride = c->block_stride;
-    a.head_stride = c->head_stride;
-    a.hkv = c->num_kv_heads;
-    return c->head_dim == 128 ? launch<128>(a, st) : launch<64>(a, st);
-}
-
-cudaError_t launch_append_queries(const kara_cache8 *c, int32_t layer, const kara_tokens *t, const kara_rope *r,
-                                  const void *q, int64_t q_stride, void *q_out, void *ring, int32_t W, int32_t *err,
-                                  cudaStream_t st)
-{
-    const AppArgs a = query_args(c, layer, t, r, q, q_stride, q_out, ring, W, err);
-    return c->head_dim == 128 ? launch<128>(a, st) : launch<64>(a, st);
+    return D == 128 ? launch<128>(a, st) : launch<64>(a, st);
 }
 
 }  // namespace kara

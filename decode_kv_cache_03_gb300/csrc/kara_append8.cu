@@ -9,7 +9,7 @@
 // One rounding from fp32; nothing is rounded to bf16 on the way.  A run needs its largest
 // value before its first code, so two warps hold a whole run of one head: all its loads are
 // in flight at once, and the rows stay in registers between the maximum and the rounding.
-// Queries go as in the bf16 append, a warp per token and a few heads.
+// Queries go with them, a warp per token and a few heads.
 //
 // Runs follow from the slots alone: row t continues row t - 1 if its slot is the next one
 // and not the first of a block.  A CTA looks at a window of `win` rows and takes the runs
@@ -24,7 +24,6 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kBs = 16;      // tokens per cache block (the supported block size)
-constexpr int kSplitRows = 20480;  // head rows of a call from which queries and runs are two launches
 constexpr int kMaxWin = 16;  // rows that a CTA looks at for the beginnings of runs, at most
 constexpr int kQPasses = 4;  // passes of query rows a warp has in flight
 
@@ -375,13 +374,19 @@ __global__ void __launch_bounds__(kThreads, LONG ? 3 : 2) append8_kernel(const A
 }
 
 template <int D>
-cudaError_t launch(Append8Args &a, bool inter, bool with_queries, cudaStream_t st)
+cudaError_t launch(Append8Args &a, bool inter, cudaStream_t st)
 {
     constexpr int HPW = kQPasses * (32 / (D / 8));
-    // short calls: a warp for each row that may begin a run; long ones look at several rows each
-    a.win = a.rows <= 512 ? 1 : a.rows / 16 < a.n ? 4 : kMaxWin;
+    // A CTA's runs go one after another, about 2.7 us each, and looking for them costs the same for a window of any
+    // length: windows of several rows pay where the call has enough of them to hide that chain, 16 win (n / rows + 1/16)
+    // runs.  (us with windows of 1, 4 and 16 rows, 40 and 2 x 8 heads of 128, the choice in brackets:
+    // 256 sequences of 1 row [12.6] 17.1 45.5, 512 of 1 [23.2] 23.7 57, 1024 of 1 44 [40] 74, 4096 of 1 188 [148] 149;
+    // 128 of 4 15.4 [12.3] 21.2, 256 of 4 27.5 [19.3] 27.9, 512 of 4 54 37 [31.8]; 64 of 12 17.8 [12.0] 15.4,
+    // 64 of 20 27 15.9 [16.1]; 1 of 448 9.8 7.3 [6.4], 4 of 2048 180 88 [76].)
+    const double runs = a.n + a.rows / 16.0;
+    a.win = (double)a.rows * a.rows >= 6144 * runs ? kMaxWin : a.rows > 512 ? 4 : 1;
     static_assert(kMaxWin + kBs <= 32, "a lane for each row of a window's runs");
-    const int64_t queries = with_queries ? (int64_t)a.rows * ((a.hq + HPW - 1) / HPW) : 0;
+    const int64_t queries = (int64_t)a.rows * ((a.hq + HPW - 1) / HPW);
     const int64_t kv = ((int64_t)a.rows + a.win - 1) / a.win * ((2 * a.hkv + kWarps / 2 - 1) / (kWarps / 2));
     const int64_t blocks = kv + (queries + kWarps - 1) / kWarps;
     if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
@@ -432,13 +437,7 @@ cudaError_t launch_append8(const kara_cache8 *c, int32_t layer, const kara_token
     a.hkv = c->num_kv_heads;
     a.n_pos = r->rot_dim > 0 ? r->n_pos : 1;
     a.rot = r->rot_dim;
-    // long calls: the queries, most of what there is to read and write, by the kernel that stages tokens
-    const bool split = (int64_t)t->rows * (c->num_q_heads + 2 * c->num_kv_heads) > kSplitRows;
-    if (split) {
-        const cudaError_t e = launch_append_queries(c, layer, t, r, q, q_stride, q_out, ring, W, err, st);
-        if (e != cudaSuccess) return e;
-    }
-    return D == 128 ? launch<128>(a, r->interleaved, !split, st) : launch<64>(a, r->interleaved, !split, st);
+    return D == 128 ? launch<128>(a, r->interleaved, st) : launch<64>(a, r->interleaved, st);
 }
 
 }  // namespace kara

@@ -92,10 +92,6 @@ inline cudaError_t pool_map8(CUtensorMap *m, const void *pool, const kara_cache8
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-// The queries' part of an append alone, by the kernels of the bf16 cache.
-cudaError_t launch_append_queries(const kara_cache8 *c, int32_t layer, const kara_tokens *t, const kara_rope *r,
-                                  const void *q, int64_t q_stride, void *q_out, void *ring, int32_t W, int32_t *err,
-                                  cudaStream_t st);
 cudaError_t launch_append8(const kara_cache8 *c, int32_t layer, const kara_tokens *t, const kara_rope *r, const void *q,
                            int64_t q_stride, const void *k, int64_t k_stride, const void *v, int64_t v_stride,
                            void *q_out, void *ring, int32_t W, int32_t *err, cudaStream_t st);

@@ -293,9 +293,11 @@ cudaError_t launch_expand8(const kara_cache8 *c, const kara_cache *out, int32_t 
 }
 
 // Comparisons of ids up to which one block plans and compares them in one launch, and kept entries up to which
-// it checks those too: the copy's launch is then the other one of the call.  (One sequence of one layer, captured:
-// 11.9 us in five launches, 8.6 in two; 1.7 million comparisons in one block: 20 us more than in several.)
-constexpr int64_t kSmallCompare = 1 << 19, kSmallKept = 1 << 14;
+// it checks those too and the copy's last block commits: two launches.  (Captured, with the copy of the table: one
+// launch more for the checks against several blocks, 7280 comparisons 11.4 us and 12.7, 118 thousand 14.9 and 15.5,
+// 470 thousand 24.1 and 20.0.  Two launches against three or four, 32 entries 10.0 us both, 2144 12.5 and 11.4,
+// but at 32 a step's host has 4 us less to do.)
+constexpr int64_t kSmallCompare = 1 << 17, kSmallKept = 1 << 10;
 
 cudaError_t launch_compact8(const kara_cache8 *c, const Geo &g, SeqPlan *plan, int32_t *done, const int32_t *kept,
                             const int32_t *fresh, int64_t n_fresh, int32_t *freed, int32_t *new_len, int32_t *table,

@@ -350,18 +350,6 @@ def test_append_bits_do_not_depend_on_the_calls_length():
         assert all(torch.equal(x, y) for x, y in zip(got[0], other))
 
 
-def test_long_appends_stall_and_recover(monkeypatch):
-    """A long call's queries are staged by bulk copies: with none issued it reports KARA_ETIMEOUT."""
-    kara = lib()
-    a = Append(60, [0], [800], 40, 8, 128, W=64)
-    want = a.run()[1]
-    monkeypatch.setenv("KARA_DEBUG_STALL", "1")
-    assert a.run()[0] == kara.ETIMEOUT
-    monkeypatch.delenv("KARA_DEBUG_STALL")
-    st, got = a.run()
-    assert st == 0 and all(torch.equal(got[x].view(torch.uint8), want[x].view(torch.uint8)) for x in got)
-
-
 def test_offsets_past_two_to_the_31st():
     """A pool of more than 2^31 codes, a table that names its far end: append, decode, chunk, expand, compact."""
     kara = lib()
