@@ -25,7 +25,10 @@ constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kBs = 16;      // tokens per cache block (the supported block size)
 constexpr int kMaxWin = 16;  // rows that a CTA looks at for the beginnings of runs, at most
-constexpr int kQPasses = 4;  // passes of query rows a warp has in flight
+
+// Passes of query rows a warp has in flight (8192 tokens: 2, 4, 5 and 10 take 92, 76, 72 and 75 us; five or ten
+// times as many heads a warp, one round after another, 73; a decode step of 128 tokens 7.4, 7.5, 7.75 with 2, 4, 5).
+__host__ __device__ constexpr int query_passes(bool many) { return many ? 5 : 4; }
 
 struct Append8Args {
     const uint16_t *q, *k, *v;
@@ -323,7 +326,7 @@ __device__ __forceinline__ void store_window(const Append8Args &a, const LaneDim
 template <int D, bool INTER, bool LONG>
 __global__ void __launch_bounds__(kThreads, LONG ? 3 : 2) append8_kernel(const Append8Args a)
 {
-    constexpr int LPR = D / 8, RPP = 32 / LPR, HPW = kQPasses * RPP;  // query heads a warp takes
+    constexpr int LPR = D / 8, RPP = 32 / LPR, NQ = query_passes(LONG), HPW = NQ * RPP;  // a warp's query heads
     const int lane = threadIdx.x & 31;
     const LaneDims<D, INTER> dims(a, lane);
     // launched as a programmatic dependent of what precedes it on the stream
@@ -341,9 +344,9 @@ __global__ void __launch_bounds__(kThreads, LONG ? 3 : 2) append8_kernel(const A
     if (t >= a.rows) return;
     const int h0 = (int)(task % parts) * HPW + lane / LPR;
     // the rows are on their way before the token's place is known (padding rows are read, not written)
-    uint4 u[kQPasses];
+    uint4 u[NQ];
 #pragma unroll
-    for (int p = 0; p < kQPasses; ++p) {
+    for (int p = 0; p < NQ; ++p) {
         const int h = h0 + p * RPP;
         u[p] = h < a.hq ? *reinterpret_cast<const uint4 *>(a.q + t * a.qs + h * D + dims.d0) : make_uint4(0, 0, 0, 0);
     }
@@ -360,7 +363,7 @@ __global__ void __launch_bounds__(kThreads, LONG ? 3 : 2) append8_kernel(const A
             ring = a.ring + pl.seq * a.ring_seq + (int64_t)(pl.pos % a.W) * D + dims.d0;
     }
 #pragma unroll
-    for (int p = 0; p < kQPasses; ++p) {
+    for (int p = 0; p < NQ; ++p) {
         const int h = h0 + p * RPP;
         if (h - lane / LPR >= a.hq) break;
         uint64_t z[4];
@@ -376,7 +379,6 @@ __global__ void __launch_bounds__(kThreads, LONG ? 3 : 2) append8_kernel(const A
 template <int D>
 cudaError_t launch(Append8Args &a, bool inter, cudaStream_t st)
 {
-    constexpr int HPW = kQPasses * (32 / (D / 8));
     // A CTA's runs go one after another, about 2.7 us each, and looking for them costs the same for a window of any
     // length: windows of several rows pay where the call has enough of them to hide that chain, 16 win (n / rows + 1/16)
     // runs.  (us with windows of 1, 4 and 16 rows, 40 and 2 x 8 heads of 128, the choice in brackets:
@@ -386,7 +388,8 @@ cudaError_t launch(Append8Args &a, bool inter, cudaStream_t st)
     const double runs = a.n + a.rows / 16.0;
     a.win = (double)a.rows * a.rows >= 6144 * runs ? kMaxWin : a.rows > 512 ? 4 : 1;
     static_assert(kMaxWin + kBs <= 32, "a lane for each row of a window's runs");
-    const int64_t queries = (int64_t)a.rows * ((a.hq + HPW - 1) / HPW);
+    const int per = query_passes(a.win > 1) * (32 / (D / 8));
+    const int64_t queries = (int64_t)a.rows * ((a.hq + per - 1) / per);
     const int64_t kv = ((int64_t)a.rows + a.win - 1) / a.win * ((2 * a.hkv + kWarps / 2 - 1) / (kWarps / 2));
     const int64_t blocks = kv + (queries + kWarps - 1) / kWarps;
     if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
