@@ -82,7 +82,7 @@ using namespace ptx;
 constexpr int kTile = 128;       // rows of a query tile, keys of a key tile
 constexpr int kBlk = 16;         // tokens per cache block (the supported block size)
 constexpr int kBlkPerTile = kTile / kBlk;
-// (kStages, the bf16 tiles of K and V, or of V alone, that the ring holds, is the including source's, and kEdges.)
+// (kStages, the bf16 tiles of K and V, or of V alone (f16), that the ring holds, is the including source's, and kEdges.)
 constexpr int kK8 = 3;           // of an 8-bit cache: tiles of K's codes in flight,
 constexpr int kRaw8 = 2;         // and of V's
 constexpr int kScales8 = 8;      // K tiles whose scales are kept: the warps that read them are not this far behind
@@ -100,6 +100,8 @@ struct Regs {
 };
 constexpr uint32_t kTmemCols = 512;  // S0 S1 (128 columns each), O0 O1 (128 each)
 constexpr float kLazy = 8.f;         // see above: rescale when the maximum grew by more than 2^8
+constexpr float kUp8 = 7.f;          // 8 bits: weights are up to 2^(kLazy + kUp8), which f16 holds,
+constexpr int kUpV8 = 6;             // and values up to 448 * 2^kUpV8
 constexpr uint64_t kTimeoutNs = 1000000000ull;
 
 // One or two query tiles of a sequence (all KV heads have the same items).
@@ -221,9 +223,11 @@ struct Shared {
 // The same of the 8-bit cache, beside it.
 struct Shared8 {
     uint64_t kfull[kK8], kempty[kK8];      // tiles of K's codes
-    uint64_t rfull[kRaw8], rempty[kRaw8];  // tiles of V's codes, which become bf16 tiles of the ring
+    uint64_t rfull[kRaw8], rempty[kRaw8];  // tiles of V's codes, which become f16 tiles of the ring
     uint64_t landed;                       // bf16 query tiles, which become codes
-    float vscale[kRaw8][kBlkPerTile], kscale[kScales8][kBlkPerTile];
+    uint32_t vfactor[kRaw8][kBlkPerTile];  // of V's blocks in their tile (f16, twice); the sign: a mark
+    float kscale[kScales8][kBlkPerTile];
+    float2 vtile[kScales8];                // of V's tiles: log2 of the scale, and its reciprocal
     // of each row of the query tiles, by the piece's number mod 2: the next piece's are written as soon as this
     // one's last logits are there, and read for its first; those of the one after only behind the next one's logits
     float qscale[2][2][kTile];
@@ -343,6 +347,12 @@ __host__ __device__ constexpr uint32_t idesc_e4m3(int M, int N)
     return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
 
+// Instruction descriptor: kind::f16 with f16 A and B, fp32 D.
+__host__ __device__ constexpr uint32_t idesc_f16(int M, int N)
+{
+    return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+
 // Descriptor of a K-major operand of codes, rows of D bytes swizzled by their size (128 or 64 bytes), groups of
 // eight rows one after another.
 template <int D>
@@ -432,6 +442,14 @@ __device__ __forceinline__ float ld_shared(uint32_t addr)
     float x;
     asm volatile("ld.shared.f32 %0, [%1];" : "=f"(x) : "r"(addr));
     return x;
+}
+
+// (lo, hi) rounded to nearest-even f16, lo in the low half.
+__device__ __forceinline__ uint32_t f16x2(float lo, float hi)
+{
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
 }
 
 // (lo, hi) rounded to nearest-even bf16, lo in the low half.
@@ -799,8 +817,15 @@ __device__ __noinline__ void add_cleared(const ChunkArgs &a, int seq, int head, 
 // exactly while |q'| >= 1/4, and 2^-10 off at most below (2^-17 of the row's largest, or 2^-50).  The logits are then
 // Q_hi K^T + Q_lo K^T, at twice the rate of bf16 operands, so in the same time; 2^-k and K's scales multiply them
 // in the softmax, where the factor log2(e) / sqrt(D) is anyway.
-// V's codes become bf16 tiles (code times scale is exact) of the ring, as its scales belong to the
-// summed dimension: put into weights, they would need weights in 8 bits, or another two terms.
+// V's codes become f16 tiles of the ring, times their block's scale over 2^e, e of the tile's largest; 2^e goes into
+// the weights, which are rounded to f16:
+//     w_x = 2^(l_x + e - M + kUp8),   O = sum_x w_x (v_x 2^-e),   z = sum over tiles of 2^-e sum_x w_x,
+// M the largest l_x + e so far (lazily, as above).  Values within 2^-20 of the tile's largest scale are exact, smaller
+// ones off by 2^-40 of it.  Weights within 2^-21 of the largest keep eleven bits, smaller ones are off by
+// at most 2^-32 of it, and with the maximum's growth of 2^8 the largest stay within f16.
+// (As bf16, exact at any scale, two codes took four instructions instead of two, and weights kept eight bits: 64
+// sequences of 1 to 128 tokens 387 us and 379, four tokens for each of 128 sequences 611 and 604, one prompt alike.
+// With a scale for each block in the weights, and one instruction, the softmax took longer: 409 and 613.)
 
 // The bf16 query tiles of a piece; one thread issues.
 template <int D>
@@ -884,35 +909,27 @@ __device__ __forceinline__ void split_queries(int tiles, int w, uint8_t *qbuf, f
     }
 }
 
-// Two codes (bytes 2e and 2e + 1 of w) as bf16 of their values times 2^-120: sign-extended to 16 bits
-// and moved up by four, the exponent and mantissa bits are where bf16 has them, and the
-// exponent's upper bits are cleared.
-template <int E>
-__device__ __forceinline__ uint32_t spread2(uint32_t w)
+// A scale's log2, between -63 and 63 whatever it is (-63 for 0).
+__device__ __forceinline__ int scale_log2(float s)
 {
-    uint32_t r;
-    asm("prmt.b32 %0, %1, 0, %2;" : "=r"(r) : "r"(w), "n"(E ? 0xB3A2 : 0x9180));
-    return (r << 4) & 0x87f087f0u;
+    return min(max((int)(__float_as_uint(s) >> 23 & 255u) - 127, -63), 63);
 }
 
-__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b)
+// 2^e as f16 in both halves, e <= 15: subnormal from 2^-15 on, 0 below 2^-24.
+__device__ __forceinline__ uint32_t f16_power2(int e)
+{
+    const uint32_t h = e >= -14 ? (uint32_t)(e + 15) << 10 : e >= -24 ? 1u << (e + 24) : 0u;
+    return h | h << 16;
+}
+
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b)
 {
     uint32_t r;
-    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
     return r;
 }
 
-// Sixteen codes as bf16 of their values times f (the scale times 2^120, a power of two).
-__device__ __forceinline__ void convert16(const uint32_t (&u)[4], uint32_t f, uint32_t (&r)[8])
-{
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-        r[2 * k] = mul_bf16x2(spread2<0>(u[k]), f);
-        r[2 * k + 1] = mul_bf16x2(spread2<1>(u[k]), f);
-    }
-}
-
-// Where a lane's 16-byte chunk of codes (of rows 32 / (D/16) apart) goes in a bf16 tile of the 128-byte
+// Where a lane's 16-byte chunk of codes (of rows 32 / (D/16) apart) goes in an f16 tile of the 128-byte
 // swizzled layout: two chunks of a 64-dim half.  Lanes of the upper half begin with the second, so that
 // eight lanes write to all banks.
 template <int D>
@@ -941,13 +958,21 @@ struct LaneChunk {
     }
 };
 
-// A block of codes as bf16 rows.  Four instructions for two codes: at that a warp for each
-// quarter of an SM keeps up with the products.
+// Sixteen codes times f, as f16.
+__device__ __forceinline__ void convert16(const uint32_t (&u)[4], uint32_t f, uint32_t (&r)[8])
+{
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        r[2 * k] = mul_f16x2(f16_of_e4m3x2(u[k] & 0xffffu), f);
+        r[2 * k + 1] = mul_f16x2(f16_of_e4m3x2(u[k] >> 16), f);
+    }
+}
+
+// A block of codes as f16 rows.
 template <int D>
-__device__ __forceinline__ void convert_block(const uint8_t *raw, uint8_t *tile, float scale, const LaneChunk<D> &lc)
+__device__ __forceinline__ void convert_block(const uint8_t *raw, uint8_t *tile, uint32_t f, const LaneChunk<D> &lc)
 {
     constexpr int NP = kBlk / LaneChunk<D>::kRows;
-    const uint32_t e = __float_as_uint(scale) >> 23, up = e == 0 ? 0u : e + 120u, f = up << 7 | up << 23;
     uint4 w[NP];
 #pragma unroll
     for (int i = 0; i < NP; ++i) w[i] = *reinterpret_cast<const uint4 *>(raw + lc.src + i * LaneChunk<D>::kRows * D);
@@ -960,15 +985,12 @@ __device__ __forceinline__ void convert_block(const uint8_t *raw, uint8_t *tile,
     }
 }
 
-// The same of a block with something out of the ordinary: rows from `end` on, which become zeros; a scale
-// above 2^7, whose product is taken in two steps; a mark, NaN codes: those of rows from `clear` on become 0
-// and are reported.
+// The same of a block with something out of the ordinary: rows from `end` on, which become zeros; a mark, NaN
+// codes: those of rows from `clear` on become 0 and are reported.
 template <int D>
-__device__ __noinline__ bool convert_odd_block(const uint8_t *raw, uint8_t *tile, int end, int clear, float scale, int lane)
+__device__ __noinline__ bool convert_odd_block(const uint8_t *raw, uint8_t *tile, int end, int clear, uint32_t f, int lane)
 {
     const LaneChunk<D> lc(lane);
-    const uint32_t e = __float_as_uint(scale) >> 23 & 255u, up = e == 0 ? 0u : min(e + 120u, 254u);
-    const uint32_t f = up << 7 | up << 23, rest = e + 120u > 254u ? e + 120u - 254u + 127u : 127u, g = rest << 7 | rest << 23;
     bool found = false;
 #pragma unroll 1
     for (int i = 0; i < kBlk / LaneChunk<D>::kRows; ++i) {
@@ -977,16 +999,14 @@ __device__ __noinline__ bool convert_odd_block(const uint8_t *raw, uint8_t *tile
                                   : make_uint4(0, 0, 0, 0);
         uint32_t u[4], r[8];
         lc.swapped(w, u);
-        convert16(u, f, r);
+        convert16(u, f & 0x7fff7fffu, r);
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
-            r[k] = mul_bf16x2(r[k], g);
             const uint32_t t = k & 1 ? u[k / 2] >> 16 : u[k / 2];
-            const bool lo = (t & 0x7fu) == 0x7fu, hi = (t & 0x7f00u) == 0x7f00u, gone = row >= clear;
-            if (signbit(scale) && (lo || hi)) {
-                found = found || gone;
-                if (lo) r[k] = (r[k] & 0xffff0000u) | (gone ? 0u : 0x7fffu);
-                if (hi) r[k] = (r[k] & 0x0000ffffu) | (gone ? 0u : 0x7fff0000u);
+            const bool lo = (t & 0x7fu) == 0x7fu, hi = (t & 0x7f00u) == 0x7f00u;
+            if (row >= clear && (lo || hi)) {
+                found = true;
+                r[k] &= (lo ? 0u : 0xffffu) | (hi ? 0u : 0xffff0000u);
             }
         }
         lc.store(tile, i, r);
@@ -1033,13 +1053,13 @@ __device__ __forceinline__ void convert_tiles(int cw, uint8_t *qbuf, uint8_t *ri
             bool found = false;
 #pragma unroll 1
             for (int b = 2 * cw; b < 2 * cw + 2; ++b) {
-                const float s = sh8->vscale[r][b];
+                const uint32_t f = sh8->vfactor[r][b];
                 const uint8_t *src = raw + r * C::kRawBytes + b * kBlk * D;
                 uint8_t *dst = ring + st * C::kTileBytes + b * kBlk * 128;
-                if (__builtin_expect(__float_as_uint(s) <= 0x43000000u && end >= (b + 1) * kBlk, 1))
-                    convert_block<D>(src, dst, s, lc);
+                if (__builtin_expect((int32_t)f >= 0 && end >= (b + 1) * kBlk, 1))
+                    convert_block<D>(src, dst, f, lc);
                 else
-                    found = convert_odd_block<D>(src, dst, end - b * kBlk, clear - b * kBlk, s, lane) || found;
+                    found = convert_odd_block<D>(src, dst, end - b * kBlk, clear - b * kBlk, f, lane) || found;
             }
             if (found) sh->odd_values[np % kOddSlots] = (int32_t)np + 1;
             fence_proxy_async_smem();
@@ -1087,7 +1107,8 @@ __device__ __forceinline__ void mma_warp(int x, uint32_t qbuf, uint32_t ring, Sh
     using C = Cfg<D, E8>;
     if (elect_one()) {
         constexpr uint32_t id_qk = E8 ? idesc_e4m3(kTile, kTile) : idesc_bf16(kTile, kTile);
-        constexpr uint32_t id_pv = idesc_bf16(kTile, D) | (1u << 16);  // V: its dims are contiguous
+        // V: its dims are contiguous
+        constexpr uint32_t id_pv = (E8 ? idesc_f16(kTile, D) : idesc_bf16(kTile, D)) | (1u << 16);
         constexpr uint32_t kTileDesc = C::kTileBytes >> 4, kHalfDesc = C::kHalfBytes >> 4;
         const uint32_t ts = x * kTile, to = 256 + x * 128;         // S (and P over it), O in TMEM
         const uint32_t kring = E8 ? ring + kStages * C::kTileBytes : ring;
@@ -1342,21 +1363,25 @@ __global__ void __launch_bounds__(kThreads, 1)
                     // a tile of codes and its blocks' scales; ids are looked up two tiles ahead, scales one
                     const int stages = kv ? kRaw8 : kK8;
                     uint8_t *codes = ring + kStages * C::kTileBytes + kv * kK8 * C::kRawBytes;
-                    const float *scales = (kv ? a.v_scale : a.k_scale) + p.head;
-                    const auto scale = [&](int32_t id) {
-                        return id < a.num_blocks ? scales[(int64_t)id * a.hkv] : 0.f;
+                    const auto scale = [&](const float *scales, int32_t id) {
+                        return id < a.num_blocks ? scales[(int64_t)id * a.hkv + p.head] : 0.f;
                     };
                     int32_t id = block_id(p.j0), next_id = p.j0 + 1 < p.j1 ? block_id(p.j0 + 1) : a.num_blocks;
-                    float sc = scale(id);
+                    float vs = scale(a.v_scale, id), ks = kv ? 0.f : scale(a.k_scale, id);
                     for (int j = p.j0; j < p.j1; ++j) {
                         const uint32_t fb = smem_u32((kv ? sh8->rfull : sh8->kfull) + st);
                         ok = __all_sync(0xffffffffu, kwait(smem_u32((kv ? sh8->rempty : sh8->kempty) + st), ph, sh, a));
                         if (!ok) break;
-                        if (mine) {
-                            // (K: codes of zeros alone are what they are at any scale, and 0 times a masked
-                            // logit's infinity is none)
-                            if (kv) sh8->vscale[st][b] = sc;
-                            else sh8->kscale[k % kScales8][b] = sc == 0.f ? 1.f : fabsf(sc);
+                        const int e = mine ? scale_log2(vs) : -63;
+                        const int et = __reduce_max_sync(0xffffffffu, e) - kUpV8;
+                        if (kv) {
+                            if (mine) sh8->vfactor[st][b] = f16_power2(e - et) | (__float_as_uint(vs) & 0x80000000u);
+                        } else {
+                            // (codes of zeros alone are what they are at any scale, and 0 times a
+                            // masked logit's infinity is none)
+                            if (mine) sh8->kscale[k % kScales8][b] = ks == 0.f ? 1.f : fabsf(ks);
+                            if (lane == 0)
+                                sh8->vtile[k % kScales8] = make_float2((float)et, __uint_as_float((uint32_t)(127 - et) << 23));
                         }
                         __syncwarp();
                         if (lane == 0) mbar_arrive_expect_tx(fb, C::kRawBytes);
@@ -1368,7 +1393,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (kv == 0 && lane == 0) *(volatile uint32_t *)&sh->loaded = k;
                         if (++st == stages) st = 0, ph ^= 1;
                         id = next_id;
-                        sc = scale(id);
+                        vs = scale(a.v_scale, id);
+                        if (kv == 0) ks = scale(a.k_scale, id);
                         if (j + 2 < p.j1) next_id = block_id(j + 2);
                     }
                     continue;
@@ -1522,6 +1548,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     float mt;
                     const uint32_t ks = smem_u32(sh8->kscale[(nk + j - p.j0) % kScales8]);
+                    const uint32_t vt = smem_u32(sh8->vtile + (nk + j - p.j0) % kScales8);
                     if constexpr (E8) {
                         // a block's keys have a scale of their own (read where it is used: registers are short)
                         if (i == 0) scale2 = a.scale2 * sh8->qscale[np & 1][two ? x : 0][r];
@@ -1537,7 +1564,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                                                __uint_as_float(s[c + 2 * e + 1])));
                             mt = fmaxf(mt, fmaxf(mx[0], mx[1]) * ld_shared(ks + b * 4));
                         }
-                        mt *= scale2;
+                        mt = fmaf(mt, scale2, ld_shared(vt));
                     } else {
                         float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
@@ -1569,7 +1596,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     const float ref = m == -INFINITY ? 0.f : m;  // a row that saw nothing yet: weights 2^-inf = 0
                     uint64_t sc = pack2(scale2, scale2);
-                    const uint64_t mr = pack2(-ref, -ref);
+                    const float mr1 = E8 ? ld_shared(vt) + kUp8 - ref : -ref;
+                    const uint64_t mr = pack2(mr1, mr1);
                     uint64_t sum[2] = {0ull, 0ull};
 #pragma unroll
                     for (int c = 0; c < kTile; c += 2) {
@@ -1582,7 +1610,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         lo = ex2(lo);
                         hi = ex2(hi);
                         sum[(c >> 1) & 1] = add2(sum[(c >> 1) & 1], pack2(lo, hi));
-                        s[c >> 1] = bf16x2(lo, hi);
+                        s[c >> 1] = E8 ? f16x2(lo, hi) : bf16x2(lo, hi);
                         if (c == 62) {
                             tmem_st32(ts, s, 0);
                             tmem_wait_st();
@@ -1594,7 +1622,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tmem_st32(ts + 32, s, 32);
                     float s0, s1;
                     unpack2(add2(sum[0], sum[1]), s0, s1);
-                    z += s0 + s1;
+                    z = E8 ? fmaf(s0 + s1, ld_shared(vt + 4), z) : z + s0 + s1;
                     tmem_wait_st();
                     tc_fence_before();
                 }

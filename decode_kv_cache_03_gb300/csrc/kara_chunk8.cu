@@ -2,7 +2,7 @@
 namespace kara {
 namespace {
 
-constexpr int kStages = 2;  // bf16 tiles of V, beside which the tiles of codes in flight lie
+constexpr int kStages = 2;  // f16 tiles of V, beside which the tiles of codes in flight lie
 constexpr int kEdges = 1;   // (no edge tiles of V: what converts a tile clears it)
 
 }  // namespace
