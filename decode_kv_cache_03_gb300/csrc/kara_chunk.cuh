@@ -1,4 +1,4 @@
-// Attention of a chunk of new tokens over the paged cache.
+// Attention of a chunk of new tokens over the paged cache, bf16 or 8 bits.
 //
 // Row t of q is the new token at position p of sequence s (its K and V are in
 // the cache already); query head h belongs to KV head g = h / G:
@@ -65,6 +65,14 @@
 // bound by their start and end: 256 sequences of 1 to 4 tokens over 64 to 512 keys take
 // 102 us, 2.2 times their bytes.
 //
+// The 8-bit cache (E8; the comment ahead of load_queries has the arithmetic): tiles of K's codes are operands as
+// they lie, tiles of V's codes pass through four warps that write them as f16, so the ring of 5 tiles is
+// 2 (f16) + 3 + 2 (codes).  Four tokens x 128 sequences 604 us (bf16 745), 64 sequences of 1 to 128 tokens 379
+// (355), 8192 tokens over 8192 keys 1620 (1405).  No unit is full (tensor 41 and 52 %, issue slots 32 and 48 %, HBM 53 %
+// of the copy rate for few tokens): a step waits for logits, weights, and the conversion ahead of the weighted sum, whose
+// tiles leave room for two.  (Few rows: a softmax a quarter as long, by rows loaded four times, one more tile of
+// codes, or both kinds of codes a tile further ahead bring 0 to 1.5 %, and cost the others 1 to 5.)
+//
 // Two launches: the attention (persistent, one CTA per SM, each of which works out
 // its own range) and the merge, programmatic dependents of what precedes them.
 #pragma once
@@ -82,7 +90,7 @@ using namespace ptx;
 constexpr int kTile = 128;       // rows of a query tile, keys of a key tile
 constexpr int kBlk = 16;         // tokens per cache block (the supported block size)
 constexpr int kBlkPerTile = kTile / kBlk;
-// (kStages, the bf16 tiles of K and V, or of V alone (f16), that the ring holds, is the including source's, and kEdges.)
+// (kStages, the tiles of K and V that the ring holds, or the f16 tiles of V alone, is the including source's, and kEdges.)
 constexpr int kK8 = 3;           // of an 8-bit cache: tiles of K's codes in flight,
 constexpr int kRaw8 = 2;         // and of V's
 constexpr int kScales8 = 8;      // K tiles whose scales are kept: the warps that read them are not this far behind

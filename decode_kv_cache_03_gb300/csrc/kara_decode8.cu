@@ -25,6 +25,10 @@
 //     share little weight beside one that takes nearly all keep their digits; without the
 //     factor, weights below 2^-14 would lose theirs.
 // Softmax, sums and the merge of the splits are fp32; the output is rounded to bf16 once.
+//
+// 128 sequences of 2048 to 16384 keys, 40/8 heads of 128: 457 us, 5.9 TB/s (0.87 of the copy rate); without the
+// products and the softmax the loads alone take 423.  ALU pipe 42 %, issue slots 44 %.  Not better: e4m3 operands
+// with K = 32 (478, more registers), splits of 2048 keys, 12 stages, stages of 8 KB.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 

@@ -8,7 +8,10 @@
 // of the gathered rows,
 //     s = the smallest power of two with max |x| <= 448 s,   code' = rn(x / s).
 // Powers of two: x / s is exact unless it falls among e4m3's subnormals.
-// Both are bound by HBM (a read and a write of every code, or of its bf16 value).
+// Both are bound by HBM (a read and a write of every code, or of its bf16 value).  Expansion of 16 windows of
+// 512 keys in 36 layers of 8 heads takes 140 us, the copy rate.  Compaction of 8 sequences (windows of
+// 1024, 396 rows kept) in 40 layers takes 113 us: the copy 88, at 0.85 of the copy rate, and the checks of kept rows and
+// fresh ids, and the plan, ahead of it.
 #include <cuda_fp16.h>
 
 #include "kara_cache8.cuh"

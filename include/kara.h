@@ -23,8 +23,8 @@
  *     caller's device word `err` (int32): the first error code wins, later
  *     ones are dropped.  The caller zeroes `err` before a step;
  *     kara_compress_batch zeroes it itself.  Read it with kara_get_error.
- *   - bf16 everywhere for Q, K and V; rows of head_dim elements are
- *     contiguous and 16-byte aligned.
+ *   - bf16 everywhere for Q, K and V (but for the pools of kara_cache8); rows of
+ *     head_dim elements are contiguous and 16-byte aligned.
  *
  * Notation: L cached length, W window, ws = L - W, B protected buffer,
  * C = W - B compressible keys, G = num_q_heads / num_kv_heads (query heads
