@@ -115,9 +115,11 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(Geo g, int64_t n_fre
 //     [0, C) (Top-K and Token2Chunk produce ascending positions): KARA_EINVAL.
 // Each probe value (a consumed fresh id or a table entry) is compared with the
 // consumed fresh ids through tiles staged in shared memory: no scratch memory,
-// and the work is (total_new + n * bt_stride) * total_new comparisons.
+// and the work is (total_new + n * bt_stride) * total_new comparisons.  A thread
+// has one probe and counts its matches, four ids to a load: two instructions a
+// comparison, over as many SMs as there are probes for.  (Four probes a thread, each against its own
+// part of the list: 3.6 million comparisons took 15 us, now 4.)
 constexpr int kChkThreads = 256;
-constexpr int kChkProbes = 4;     // probe values per thread
 constexpr int kChkTile = 2048;    // fresh ids per shared-memory tile
 
 __device__ __forceinline__ void record_dup(int32_t *err)
@@ -129,46 +131,44 @@ __global__ void __launch_bounds__(kChkThreads) fresh_check_kernel(Geo g, const S
                                                                   const int32_t *__restrict__ fresh,
                                                                   int64_t n_fresh, int32_t *err)
 {
-    __shared__ int32_t tile[kChkTile];
+    __shared__ __align__(16) int32_t tile[kChkTile];
     dependent_wait();
     const SeqPlan last = plan[g.n - 1];
     const int64_t F = (int64_t)last.off_new + last.n_new;  // fresh ids the plan consumes
     if (F > n_fresh) return;                                // KARA_ENOBLOCKS is recorded
     const int64_t P = F + (int64_t)g.n * g.bt_stride;       // probes: consumed ids, then table slots
-    int32_t v[kChkProbes];
-    int64_t lim[kChkProbes];                                // compare with fresh[j], j < lim
+    const int64_t p = (int64_t)blockIdx.x * kChkThreads + threadIdx.x;
+    int32_t v = 0;
+    int allowed = INT_MAX;  // matches: an id's with itself, any of a thread without a value
     bool bad = false;
-#pragma unroll
-    for (int k = 0; k < kChkProbes; ++k) {
-        const int64_t p = ((int64_t)blockIdx.x * kChkProbes + k) * kChkThreads + threadIdx.x;
-        v[k] = 0;
-        lim[k] = 0;
-        if (p < F) {
-            v[k] = fresh[p];
-            lim[k] = p;
-            bad |= v[k] < 0 || v[k] >= g.num_blocks;
-        } else if (p < P) {
-            const int64_t q = p - F;
-            const int s = (int)(q / g.bt_stride), lb = (int)(q % g.bt_stride);
-            const int64_t L = g.len[s];
-            if (L > 0 && lb < (L + g.bs - 1) / g.bs) {
-                v[k] = g.bt[q];
-                lim[k] = F;
-            }
+    if (p < F) {
+        v = fresh[p];
+        allowed = 1;
+        bad = v < 0 || v >= g.num_blocks;
+    } else if (p < P) {
+        const int64_t q = p - F;
+        const int s = (int)(q / g.bt_stride), lb = (int)(q % g.bt_stride);
+        const int64_t L = g.len[s];
+        if (L > 0 && lb < (L + g.bs - 1) / g.bs) {
+            v = g.bt[q];
+            allowed = 0;
         }
     }
-    bool dup = false;
+    int matches = 0;
     for (int64_t t0 = 0; t0 < F; t0 += kChkTile) {
         const int n = (int)min((int64_t)kChkTile, F - t0);
         __syncthreads();
         for (int i = threadIdx.x; i < n; i += kChkThreads) tile[i] = fresh[t0 + i];
         __syncthreads();
-        for (int i = 0; i < n; ++i) {
-            const int32_t f = tile[i];
-#pragma unroll
-            for (int k = 0; k < kChkProbes; ++k) dup |= f == v[k] && t0 + i < lim[k];
+        int i = 0;
+#pragma unroll 4
+        for (; i + 4 <= n; i += 4) {
+            const int4 f = *reinterpret_cast<const int4 *>(tile + i);
+            matches += (f.x == v) + (f.y == v) + (f.z == v) + (f.w == v);
         }
+        for (; i < n; ++i) matches += tile[i] == v;
     }
+    const bool dup = matches > allowed;
     if (bad) atomicCAS(err, 0, KARA_EBADBLOCK);
     if (dup) record_dup(err);
 }
@@ -317,8 +317,7 @@ cudaError_t launch_fresh_check(const Geo &g, const SeqPlan *plan, const int32_t 
 {
     if (g.nwin == 0) return cudaSuccess;
     const int64_t probes = n_fresh + (int64_t)g.n * g.bt_stride;
-    const int64_t per = (int64_t)kChkThreads * kChkProbes;
-    const int64_t nb = (probes + per - 1) / per;
+    const int64_t nb = (probes + kChkThreads - 1) / kChkThreads;
     if (nb > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
     return launch<Geo, const SeqPlan *, const int32_t *, int64_t, int32_t *>(
         dependent, fresh_check_kernel, (unsigned)nb, kChkThreads, st, g, plan, fresh, n_fresh, err);

@@ -10,7 +10,7 @@
 // Powers of two: x / s is exact unless it falls among e4m3's subnormals.
 // Both are bound by HBM (a read and a write of every code, or of its bf16 value).  Expansion of 16 windows of
 // 512 keys in 36 layers of 8 heads takes 140 us, the copy rate.  Compaction of 8 sequences (windows of
-// 1024, 396 rows kept) in 40 layers takes 113 us: the copy 88, at 0.85 of the copy rate, and the checks of kept rows and
+// 1024, 396 rows kept) in 40 layers takes 108 us: the copy 88, at 0.85 of the copy rate, and the checks of kept rows and
 // fresh ids, and the plan, ahead of it.
 #include <cuda_fp16.h>
 
@@ -297,10 +297,10 @@ cudaError_t launch_expand8(const kara_cache8 *c, const kara_cache *out, int32_t 
 
 // Comparisons of ids up to which one block plans and compares them in one launch, and kept entries up to which
 // it checks those too and the copy's last block commits: two launches.  (Captured, with the copy of the table: one
-// launch more for the checks against several blocks, 7280 comparisons 11.4 us and 12.7, 118 thousand 14.9 and 15.5,
-// 470 thousand 24.1 and 20.0.  Two launches against three or four, 32 entries 10.0 us both, 2144 12.5 and 11.4,
-// but at 32 a step's host has 4 us less to do.)
-constexpr int64_t kSmallCompare = 1 << 17, kSmallKept = 1 << 10;
+// launch more for the checks against several blocks, 7280 comparisons 11.7 us and 12.3, 27 thousand 21.8 and 21.2,
+// 118 thousand 15.7 and 13.1.  Two launches against three or four, 32 entries 10.2 us and 9.5, 2144 12.4 and 11.7,
+// but at 32 the host has 4 us less to do, and the kernels wait for it.)
+constexpr int64_t kSmallCompare = 1 << 14, kSmallKept = 1 << 10;
 
 cudaError_t launch_compact8(const kara_cache8 *c, const Geo &g, SeqPlan *plan, int32_t *done, const int32_t *kept,
                             const int32_t *fresh, int64_t n_fresh, int32_t *freed, int32_t *new_len, int32_t *table,
