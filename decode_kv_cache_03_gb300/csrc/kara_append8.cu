@@ -79,15 +79,16 @@ __device__ __forceinline__ Place place_of(const Append8Args &a, int64_t t, bool 
 }
 
 // What a lane does with its eight dims of every row: which of them turn, with which lane.
-template <int D, bool INTER>
+// (FULL: all D turn; INTER: pairs are neighbours.)
+template <int D, bool INTER, bool FULL>
 struct LaneDims {
     int d0, half, other;
     bool turned, low;
     __device__ LaneDims(const Append8Args &a, int lane)
     {
         d0 = lane % (D / 8) * 8;
-        half = a.rot >> 1;
-        turned = d0 < a.rot, low = d0 < half;
+        half = FULL ? D / 2 : a.rot >> 1;
+        turned = FULL || d0 < a.rot, low = d0 < half;
         // lane that holds the other half of this lane's pairs
         other = !turned || INTER ? lane : low ? lane + half / 8 : lane - half / 8;
     }
@@ -134,7 +135,7 @@ struct LaneDims {
                                          uint64_t (&z)[4], float &inv) const
     {
         uint4 uo = u;
-        if (!INTER && a.rot > 0) {
+        if (!INTER && (FULL || a.rot > 0)) {
             uo.x = __shfl_sync(0xffffffffu, u.x, other), uo.y = __shfl_sync(0xffffffffu, u.y, other);
             uo.z = __shfl_sync(0xffffffffu, u.z, other), uo.w = __shfl_sync(0xffffffffu, u.w, other);
         }
@@ -213,8 +214,8 @@ __device__ __forceinline__ uint2 codes8(const uint64_t (&z)[4], float f, bool od
 // (slot, offset, table row) set the pace.  The CTA brings in the window's rows of the rotation table together,
 // while the first run's rows are on their way.
 // (LONG: windows of several rows.  With one each row's factors come straight from global memory.)
-template <int D, bool INTER, bool LONG>
-__device__ __forceinline__ void store_window(const Append8Args &a, const LaneDims<D, INTER> &dims, int64_t window, int h,
+template <int D, bool INTER, bool FULL, bool LONG>
+__device__ __forceinline__ void store_window(const Append8Args &a, const LaneDims<D, INTER, FULL> &dims, int64_t window, int h,
                                              float *table, Meet *meet)
 {
     constexpr int LPR = D / 8, RPP = 32 / LPR, NP = kBs / RPP / 2;
@@ -331,19 +332,19 @@ __device__ __forceinline__ void store_window(const Append8Args &a, const LaneDim
     }
 }
 
-template <int D, bool INTER, bool LONG>
+template <int D, bool INTER, bool FULL, bool LONG>
 __global__ void __launch_bounds__(kThreads, LONG ? 3 : 2) append8_kernel(const Append8Args a)
 {
     constexpr int LPR = D / 8, RPP = 32 / LPR, NQ = query_passes(LONG), HPW = NQ * RPP;  // a warp's query heads
     const int lane = threadIdx.x & 31;
-    const LaneDims<D, INTER> dims(a, lane);
+    const LaneDims<D, INTER, FULL> dims(a, lane);
     // launched as a programmatic dependent of what precedes it on the stream
     asm volatile("griddepcontrol.wait;" ::: "memory");
     __shared__ Meet meet[kWarps / 2];
     __shared__ __align__(16) float table[LONG ? (kMaxWin + kBs) * D : 4];
     if (blockIdx.x < a.kv_blocks) {
         const int groups = (2 * a.hkv + kWarps / 2 - 1) / (kWarps / 2), pair = threadIdx.x >> 6;
-        store_window<D, INTER, LONG>(a, dims, blockIdx.x / groups, blockIdx.x % groups * (kWarps / 2) + pair, table,
+        store_window<D, INTER, FULL, LONG>(a, dims, blockIdx.x / groups, blockIdx.x % groups * (kWarps / 2) + pair, table,
                                meet + pair);
         return;
     }
@@ -384,9 +385,10 @@ __global__ void __launch_bounds__(kThreads, LONG ? 3 : 2) append8_kernel(const A
     }
 }
 
-template <int D>
-cudaError_t launch(Append8Args &a, bool inter, cudaStream_t st)
+template <int D, bool INTER>
+cudaError_t launch(Append8Args &a, cudaStream_t st)
 {
+    const bool full = a.rot == D;
     // A CTA's runs go one after another, about 2.7 us each, and looking for them costs the same for a window of any
     // length: windows of several rows pay where the call has enough of them to hide that chain, 16 win (n / rows + 1/16)
     // runs.  (us with windows of 1, 4 and 16 rows, 40 and 2 x 8 heads of 128, the choice in brackets:
@@ -402,8 +404,8 @@ cudaError_t launch(Append8Args &a, bool inter, cudaStream_t st)
     const int64_t blocks = kv + (queries + kWarps - 1) / kWarps;
     if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
     a.kv_blocks = (int32_t)kv;
-    const auto kern = a.win > 1 ? (inter ? append8_kernel<D, true, true> : append8_kernel<D, false, true>)
-                                : (inter ? append8_kernel<D, true, false> : append8_kernel<D, false, false>);
+    const auto kern = full ? (a.win > 1 ? append8_kernel<D, INTER, true, true> : append8_kernel<D, INTER, true, false>)
+                           : (a.win > 1 ? append8_kernel<D, INTER, false, true> : append8_kernel<D, INTER, false, false>);
     return launch_dependent(kern, dim3((unsigned)blocks), kThreads, 0, st, (const Append8Args)a);
 }
 
@@ -448,7 +450,8 @@ cudaError_t launch_append8(const kara_cache8 *c, int32_t layer, const kara_token
     a.hkv = c->num_kv_heads;
     a.n_pos = r->rot_dim > 0 ? r->n_pos : 1;
     a.rot = r->rot_dim;
-    return D == 128 ? launch<128>(a, r->interleaved, st) : launch<64>(a, r->interleaved, st);
+    if (D == 128) return r->interleaved ? launch<128, true>(a, st) : launch<128, false>(a, st);
+    return r->interleaved ? launch<64, true>(a, st) : launch<64, false>(a, st);
 }
 
 }  // namespace kara

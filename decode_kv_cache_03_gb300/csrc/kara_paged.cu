@@ -118,7 +118,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(Geo g, int64_t n_fre
 // and the work is (total_new + n * bt_stride) * total_new comparisons.  A thread
 // has one probe and counts its matches, four ids to a load: two instructions a
 // comparison, over as many SMs as there are probes for.  (Four probes a thread, each against its own
-// part of the list: 3.6 million comparisons took 15 us, now 4.)
+// part of the list: a call with 3.6 million comparisons took 29 us, now 18.)
 constexpr int kChkThreads = 256;
 constexpr int kChkTile = 2048;    // fresh ids per shared-memory tile
 
