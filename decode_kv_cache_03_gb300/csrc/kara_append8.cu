@@ -93,19 +93,13 @@ struct LaneDims {
         other = !turned || INTER ? lane : low ? lane + half / 8 : lane - half / 8;
     }
     // cosines and signed sines, in pairs of neighbours
-    template <bool SHARED>
-    static __device__ __forceinline__ float4 ld4(const float *p)
-    {
-        return SHARED ? *reinterpret_cast<const float4 *>(p) : ldg4(p);
-    }
-    template <bool SHARED>
     __device__ __forceinline__ void factors(const float *row, uint64_t (&c)[4], uint64_t (&sn)[4]) const
     {
 #pragma unroll
         for (int e = 0; e < 4; ++e) c[e] = ptx::pack2(1.f, 1.f), sn[e] = ptx::pack2(0.f, 0.f);
         if (!turned) return;
         if (INTER) {
-            const float4 cc = ld4<SHARED>(row + d0 / 2), ss = ld4<SHARED>(row + half + d0 / 2);
+            const float4 cc = ldg4(row + d0 / 2), ss = ldg4(row + half + d0 / 2);
             c[0] = ptx::pack2(cc.x, cc.x), c[1] = ptx::pack2(cc.y, cc.y);
             c[2] = ptx::pack2(cc.z, cc.z), c[3] = ptx::pack2(cc.w, cc.w);
             sn[0] = ptx::pack2(-ss.x, ss.x), sn[1] = ptx::pack2(-ss.y, ss.y);
@@ -115,7 +109,7 @@ struct LaneDims {
             const uint64_t sg = low ? ptx::pack2(-1.f, -1.f) : ptx::pack2(1.f, 1.f);
 #pragma unroll
             for (int e = 0; e < 4; e += 2) {
-                const float4 cc = ld4<SHARED>(row + j0 + 2 * e), ss = ld4<SHARED>(row + half + j0 + 2 * e);
+                const float4 cc = ldg4(row + j0 + 2 * e), ss = ldg4(row + half + j0 + 2 * e);
                 c[e] = ptx::pack2(cc.x, cc.y), c[e + 1] = ptx::pack2(cc.z, cc.w);
                 sn[e] = mul2(sg, ptx::pack2(ss.x, ss.y)), sn[e + 1] = mul2(sg, ptx::pack2(ss.z, ss.w));
             }
@@ -129,32 +123,40 @@ struct LaneDims {
         w = __ldg(reinterpret_cast<const uint4 *>(wp + d0));
         wo = INTER ? w : __ldg(reinterpret_cast<const uint4 *>(wp + (turned ? low ? d0 + half : d0 - half : d0)));
     }
-    // z = (x w c + x' w' s), x' and w' of the pair's other member, and 1 / the norm; the whole warp
-    __device__ __forceinline__ void turn(const Append8Args &a, const uint4 &u, const uint16_t *wp, const uint4 &uw,
-                                         const uint4 &uwo, const uint64_t (&c)[4], const uint64_t (&sn)[4],
-                                         uint64_t (&z)[4], float &inv) const
+    // z = (x w c + x' w' s), x' and w' of the pair's other member, and 1 / the norm; the whole warp.  wc, ws: the products
+    __device__ __forceinline__ void turn(const Append8Args &a, const uint4 &u, bool norm, const uint64_t (&wc)[4],
+                                         const uint64_t (&ws)[4], uint64_t (&z)[4], float &inv) const
     {
         uint4 uo = u;
         if (!INTER && (FULL || a.rot > 0)) {
             uo.x = __shfl_sync(0xffffffffu, u.x, other), uo.y = __shfl_sync(0xffffffffu, u.y, other);
             uo.z = __shfl_sync(0xffffffffu, u.z, other), uo.w = __shfl_sync(0xffffffffu, u.w, other);
         }
-        uint64_t x[4], xo[4], w[4], wo[4];
+        uint64_t x[4], xo[4];
         pairs4(u, x, false), pairs4(uo, xo, INTER);
-        pairs4(uw, w, false), pairs4(uwo, wo, INTER);
         inv = 1.f;
-        if (wp) {
+        if (norm) {
             float ss = squares(x);
 #pragma unroll
             for (int o = D / 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
             inv = inverse_norm(ss, 1.f / D, a.eps);
         }
 #pragma unroll
-        for (int e = 0; e < 4; ++e) z[e] = turn2(x[e], mul2(w[e], c[e]), xo[e], mul2(wo[e], sn[e]));
+        for (int e = 0; e < 4; ++e) z[e] = turn2(x[e], wc[e], xo[e], ws[e]);
         if (!turned) {  // (0 times an infinity is no number)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) z[e] = mul2(x[e], w[e]);
+            for (int e = 0; e < 4; ++e) z[e] = mul2(x[e], wc[e]);
         }
+    }
+    __device__ __forceinline__ void turn(const Append8Args &a, const uint4 &u, const uint16_t *wp, const uint4 &uw,
+                                         const uint4 &uwo, const uint64_t (&c)[4], const uint64_t (&sn)[4],
+                                         uint64_t (&z)[4], float &inv) const
+    {
+        uint64_t w[4], wo[4], wc[4], ws[4];
+        pairs4(uw, w, false), pairs4(uwo, wo, INTER);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) wc[e] = mul2(w[e], c[e]), ws[e] = mul2(wo[e], sn[e]);
+        turn(a, u, wp != nullptr, wc, ws, z, inv);
     }
 };
 
@@ -209,17 +211,58 @@ __device__ __forceinline__ uint2 codes8(const uint64_t (&z)[4], float f, bool od
     return make_uint2(w[0] | w[1] << 16, w[2] | w[3] << 16);
 }
 
+// What a key is multiplied by: of a row of the rotation table, for all D dims, cosines times weights and then
+// the signed sines times the partners' weights (the same products as a lane forms for itself), each as the first
+// halves of the lanes' eight dims, then the second, so that 16-byte loads meet no bank twice.  A warp takes a row.
+template <int D, bool INTER, bool FULL>
+struct RowFactors {
+    int d, half;
+    bool turned, low;
+    float w[4], wo[4];
+    __device__ RowFactors(const Append8Args &a, int lane)
+    {
+        d = lane * 4 % D, half = FULL ? D / 2 : a.rot >> 1;
+        turned = FULL || d < a.rot, low = d < half;
+        const int other = !turned || INTER ? d : low ? d + half : d - half;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            w[e] = a.kw ? __uint_as_float((uint32_t)__ldg(a.kw + d + e) << 16) : 1.f;
+            wo[e] = a.kw ? __uint_as_float((uint32_t)__ldg(a.kw + other + (INTER ? e ^ 1 : e)) << 16) : 1.f;
+        }
+    }
+    __device__ __forceinline__ void store(const float *row, float *to, int lane) const
+    {
+        float4 wc = make_float4(w[0], w[1], w[2], w[3]), ws = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (lane >= D / 4) return;
+        if (turned && INTER) {
+            const float2 c = __ldg(reinterpret_cast<const float2 *>(row + d / 2));
+            const float2 s = __ldg(reinterpret_cast<const float2 *>(row + half + d / 2));
+            wc = make_float4(w[0] * c.x, w[1] * c.x, w[2] * c.y, w[3] * c.y);
+            ws = make_float4(wo[0] * -s.x, wo[1] * s.x, wo[2] * -s.y, wo[3] * s.y);
+        } else if (turned) {
+            const float *at = row + (low ? d : d - half);
+            const float4 c = ldg4(at), s = ldg4(at + half);
+            const float g = low ? -1.f : 1.f;
+            wc = make_float4(w[0] * c.x, w[1] * c.y, w[2] * c.z, w[3] * c.w);
+            ws = make_float4(wo[0] * (g * s.x), wo[1] * (g * s.y), wo[2] * (g * s.z), wo[3] * (g * s.w));
+        }
+        to += (d >> 3) * 4 + (d & 4 ? D / 2 : 0);
+        *reinterpret_cast<float4 *>(to) = wc;
+        *reinterpret_cast<float4 *>(to + D) = ws;
+    }
+};
+
 // The runs that begin in a window, for four of the 2 hkv (K, then V) heads of a CTA; two warps share a run
 // of a head, eight rows each: alone, with all rows in registers, so few fit on an SM that the chain of loads
-// (slot, offset, table row) set the pace.  The CTA brings in the window's rows of the rotation table together,
-// while the first run's rows are on their way.
+// (slot, offset, table row) set the pace.  A CTA with keys brings in what the window's rows of the rotation table
+// multiply them by, while the first run's rows are on their way.
 // (LONG: windows of several rows.  With one each row's factors come straight from global memory.)
 template <int D, bool INTER, bool FULL, bool LONG>
-__device__ __forceinline__ void store_window(const Append8Args &a, const LaneDims<D, INTER, FULL> &dims, int64_t window, int h,
-                                             float *table, Meet *meet)
+__device__ __forceinline__ void store_window(const Append8Args &a, const LaneDims<D, INTER, FULL> &dims, int64_t window,
+                                             int h0, int pair, float *table, Meet *meet)
 {
     constexpr int LPR = D / 8, RPP = 32 / LPR, NP = kBs / RPP / 2;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, half = warp & 1;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, half = warp & 1, h = h0 + pair;
     const bool mine = h < 2 * a.hkv, is_v = h >= a.hkv;
     const int g = is_v ? h - a.hkv : h, row0 = half * (kBs / 2) + lane / LPR;
     // lane i: row t0 - 1 + i.  Runs that begin in the window (lanes 1 .. win) end by lane win + 15.
@@ -248,16 +291,14 @@ __device__ __forceinline__ void store_window(const Append8Args &a, const LaneDim
         }
         float *sp = (is_v ? a.v_scale : a.k_scale) + blk * a.hkv + g;
         const float old = mine && at > 0 ? *sp : 0.f;
-        if (LONG && !staged) {
+        if (LONG && !staged && h0 < a.hkv) {
             staged = true;
-            if (a.rot > 0) {
-                for (int i = 1 + warp; i < a.win + kBs; i += kWarps) {
-                    const int64_t r = __shfl_sync(0xffffffffu, p.r, i);
-                    if ((good >> i & 1u) && lane < a.rot / 4)
-                        reinterpret_cast<float4 *>(table + i * D)[lane] = ldg4(a.cos_sin + r * a.rot + lane * 4);
-                }
-                __syncthreads();
+            const RowFactors<D, INTER, FULL> f(a, lane);
+            for (int i = 1 + warp; i < a.win + kBs; i += kWarps) {
+                const int64_t r = __shfl_sync(0xffffffffu, p.r, i);
+                if (good >> i & 1u) f.store(a.cos_sin + r * a.rot, table + i * 2 * D, lane);
             }
+            __syncthreads();
         }
         if (!mine) continue;
         // (rows past the run are zeros, and stay zeros)
@@ -273,18 +314,20 @@ __device__ __forceinline__ void store_window(const Append8Args &a, const LaneDim
             }
         } else {
             uint4 uw, uwo;
-            dims.weights(a.kw, uw, uwo);
+            if (!LONG) dims.weights(a.kw, uw, uwo);
 #pragma unroll
             for (int k = 0; k < NP; ++k) {
-                const int i = k * RPP + row0;
-                uint64_t c[4], sn[4];
-                const int from = first + min(i, m - 1);
-                const int64_t r = LONG ? 0 : __shfl_sync(0xffffffffu, p.r, from);
-                if (LONG)
-                    dims.template factors<true>(table + from * D, c, sn);
-                else
-                    dims.template factors<false>(a.cos_sin + r * a.rot, c, sn);
-                dims.turn(a, u[k], a.kw, uw, uwo, c, sn, z[k], inv[k]);
+                const int i = k * RPP + row0, from = first + min(i, m - 1);
+                if (LONG) {
+                    const ulonglong2 *f = reinterpret_cast<const ulonglong2 *>(table + from * 2 * D + dims.d0 / 2);
+                    const ulonglong2 c0 = f[0], c1 = f[D / 8], s0 = f[D / 4], s1 = f[D / 4 + D / 8];
+                    dims.turn(a, u[k], a.kw != nullptr, {c0.x, c0.y, c1.x, c1.y}, {s0.x, s0.y, s1.x, s1.y}, z[k], inv[k]);
+                } else {
+                    uint64_t c[4], sn[4];
+                    const int64_t r = __shfl_sync(0xffffffffu, p.r, from);
+                    dims.factors(a.cos_sin + r * a.rot, c, sn);
+                    dims.turn(a, u[k], a.kw, uw, uwo, c, sn, z[k], inv[k]);
+                }
                 float of_row = 0.f;
                 take(z[k], of_row, nan);
                 top = fmaxf(top, of_row * inv[k]);
@@ -341,11 +384,11 @@ __global__ void __launch_bounds__(kThreads, LONG ? 3 : 2) append8_kernel(const A
     // launched as a programmatic dependent of what precedes it on the stream
     asm volatile("griddepcontrol.wait;" ::: "memory");
     __shared__ Meet meet[kWarps / 2];
-    __shared__ __align__(16) float table[LONG ? (kMaxWin + kBs) * D : 4];
+    __shared__ __align__(16) float table[LONG ? (kMaxWin + kBs) * 2 * D : 4];
     if (blockIdx.x < a.kv_blocks) {
         const int groups = (2 * a.hkv + kWarps / 2 - 1) / (kWarps / 2), pair = threadIdx.x >> 6;
-        store_window<D, INTER, FULL, LONG>(a, dims, blockIdx.x / groups, blockIdx.x % groups * (kWarps / 2) + pair, table,
-                               meet + pair);
+        store_window<D, INTER, FULL, LONG>(a, dims, blockIdx.x / groups, blockIdx.x % groups * (kWarps / 2), pair, table,
+                                           meet + pair);
         return;
     }
     const int parts = (a.hq + HPW - 1) / HPW;
@@ -362,7 +405,7 @@ __global__ void __launch_bounds__(kThreads, LONG ? 3 : 2) append8_kernel(const A
     const Place pl = place_of(a, t, false);
     if (!pl.ok) return;
     uint64_t c[4], sn[4];
-    dims.template factors<false>(a.cos_sin + pl.r * a.rot, c, sn);
+    dims.factors(a.cos_sin + pl.r * a.rot, c, sn);
     uint4 uw, uwo;
     dims.weights(a.qw, uw, uwo);
     uint16_t *ring = nullptr;  // this token's row of the ring, if it is of the last W
