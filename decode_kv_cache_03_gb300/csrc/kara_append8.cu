@@ -15,13 +15,14 @@
 // and not the first of a block.  A CTA looks at a window of `win` rows and takes the runs
 // that begin there.
 //
-// Bound by HBM and issue slots: 8192 tokens, 40 and 2 x 8 heads of 128, with the ring, 72 us in a loop for 264 MB
-// (3.7 TB/s; slots 53 %, ALU 39 %, 35 % of the warps, as the rows in registers allow).  On the way: a warp a run
-// 102; two warps a run and the window's table rows in shared memory 76.5; five passes of query rows 72.  (Queries
-// by the bf16 append's staged kernel, in a launch of their own, 76.6, and slower by that launch in shorter calls:
-// 512 sequences of a token 26.5 against 23.2, 512 tokens 11.2 against 7.4.  With two CTAs to an SM
-// instead of three 92; with four, and spills, 72, but 71 for 64 with 1024 sequences of four tokens.)  128 sequences of a token take 7.5 us captured: the chain
-// of slot, table row, rows, largest value.
+// Bound by HBM and issue slots: 8192 tokens, 40 and 2 x 8 heads of 128, with the ring, 60.5 us captured for 264 MB
+// (4.4 TB/s).  On the way: a warp a run 102; two warps a run and the window's table rows in shared memory 76; five
+// passes of query rows 72.5; a form for rotations of all dims 66; a key's factors formed once for a CTA 60.5.
+// (Queries by the bf16 append's staged kernel, in a launch of their own: as fast at 76, and slower by that launch
+// in shorter calls, 512 sequences of a token 26.5 against 23.2, 512 tokens 11.2 against 7.4.  Four CTAs to an SM
+// instead of three, with spills: 57, but 512 tokens 7.1 for 6.5, 256 sequences of four 16.4 for 15.2; two heads to a pair of warps:
+// 58, but 8.0 and 16.0.)  128 sequences of a token take 7.2 us captured: the chain of slot, table row, rows,
+// largest value.
 #include "kara_cache8.cuh"
 #include "kara_rows.cuh"
 #include "kara_tokens.cuh"
@@ -34,8 +35,8 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kBs = 16;      // tokens per cache block (the supported block size)
 constexpr int kMaxWin = 16;  // rows that a CTA looks at for the beginnings of runs, at most
 
-// Passes of query rows a warp has in flight (8192 tokens: 2, 4, 5 and 10 take 92, 76, 72 and 75 us; five or ten
-// times as many heads a warp, one round after another, 73; a decode step of 128 tokens 7.4, 7.5, 7.75 with 2, 4, 5).
+// Passes of query rows a warp has in flight (8192 tokens: 4, 5 and 10 take 64, 60.5 and 59.6 us, 256 sequences of four
+// 15.3, 15.2 and 16.2; a decode step of 128 tokens 7.4, 7.5 and 7.75 with 2, 4 and 5).
 __host__ __device__ constexpr int query_passes(bool many) { return many ? 5 : 4; }
 
 struct Append8Args {
@@ -432,14 +433,15 @@ template <int D, bool INTER>
 cudaError_t launch(Append8Args &a, cudaStream_t st)
 {
     const bool full = a.rot == D;
-    // A CTA's runs go one after another, about 2.7 us each, and looking for them costs the same for a window of any
+    // A CTA's runs go one after another, about 2 us each, and looking for them costs the same for a window of any
     // length: windows of several rows pay where the call has enough of them to hide that chain, 16 win (n / rows + 1/16)
     // runs.  (us with windows of 1, 4 and 16 rows, 40 and 2 x 8 heads of 128, the choice in brackets:
-    // 256 sequences of 1 row [12.6] 17.1 45.5, 512 of 1 [23.2] 23.7 57, 1024 of 1 44 [40] 74, 4096 of 1 188 [148] 149;
-    // 128 of 4 15.4 [12.3] 21.2, 256 of 4 27.5 [19.3] 27.9, 512 of 4 54 37 [31.8]; 64 of 12 17.8 [12.0] 15.4,
-    // 64 of 20 27 15.9 [16.1]; 1 of 448 9.8 7.3 [6.4], 4 of 2048 180 88 [76].)
+    // 256 sequences of 1 row [11.6] 12.2 32.8, 384 of 1 16.5 [14.2] 32.4, 1024 of 1 40 [27.5] 46, 4096 of 1 172 [112] 104;
+    // 96 of 4 10.6 [7.9] 15.4, 256 of 4 25 [15.1] 18.8, 512 of 4 49 28.4 [24.3]; 64 of 12 16 [10.1] 11.9,
+    // 64 of 20 24 13.2 [12.2]; 16 of 20 [7.5] 8.0 8.6; 1 of 192 [5.6] 5.1 4.8, 1 of 448 8.9 6.1 [5.9],
+    // 4 of 2048 163 74 [60].)
     const double runs = a.n + a.rows / 16.0;
-    a.win = (double)a.rows * a.rows >= 6144 * runs ? kMaxWin : a.rows > 512 ? 4 : 1;
+    a.win = (double)a.rows * a.rows >= 6144 * runs ? kMaxWin : a.rows > 320 ? 4 : 1;
     static_assert(kMaxWin + kBs <= 32, "a lane for each row of a window's runs");
     const int per = query_passes(a.win > 1) * (32 / (D / 8));
     const int64_t queries = (int64_t)a.rows * ((a.hq + per - 1) / per);

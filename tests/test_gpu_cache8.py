@@ -148,6 +148,13 @@ APPENDS = [
     ([0, 7], [700, 41], 18, 3, 128, True, None, True, 64, 9),
     ([1] * 90, [7] * 90, 4, 2, 64, False, 16, False, 0, 0),
     ([9, 100], [300, 333], 5, 1, 128, True, 0, False, 0, 1),
+    # long calls, of every kind of rotation
+    ([3, 0], [600, 90], 8, 2, 64, True, None, True, 64, 2),
+    ([3, 0], [600, 90], 8, 2, 128, True, 64, True, 0, 0),
+    ([2] * 80, [9] * 80, 8, 2, 128, True, 32, False, 64, 0),
+    ([0, 33], [500, 300], 6, 3, 64, True, 32, False, 0, 0),
+    ([0, 33], [500, 300], 40, 8, 128, True, None, False, 64, 0),
+    ([0, 33], [500, 300], 40, 8, 128, False, None, False, 0, 0),
 ]
 
 
