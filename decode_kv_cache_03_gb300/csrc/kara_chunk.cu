@@ -12,6 +12,11 @@ constexpr int kStages = 5;       // K and V tiles in flight
 constexpr int kEdges = (kStages - 1) / 2 + 2;
 static_assert(kEdges == 4 && kStages % 2 == 1, "Shared::edge tells four edge tiles apart, K and V take turns");
 
+// In about 800 clocks: a key tile of two query tiles 3000 to 3400, of one 2500, an item's start and end about 6500;
+// all at D = 128.  (Two to one for the tiles: the mixed batch of decodes and chunks takes 358 us, four to three
+// 338, captured.)
+constexpr int kPairCost = 4, kSingleCost = 3, kItemCost = 8;
+
 }  // namespace
 }  // namespace kara
 

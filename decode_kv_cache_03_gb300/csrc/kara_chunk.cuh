@@ -90,7 +90,8 @@ using namespace ptx;
 constexpr int kTile = 128;       // rows of a query tile, keys of a key tile
 constexpr int kBlk = 16;         // tokens per cache block (the supported block size)
 constexpr int kBlkPerTile = kTile / kBlk;
-// (kStages, the tiles of K and V that the ring holds, or the f16 tiles of V alone, is the including source's, and kEdges.)
+// (The including source has kStages, the tiles of K and V that the ring holds, or the f16 tiles of V alone,
+// kEdges and the costs by which the work is cut.)
 constexpr int kK8 = 3;           // of an 8-bit cache: tiles of K's codes in flight,
 constexpr int kRaw8 = 2;         // and of V's
 constexpr int kScales8 = 8;      // K tiles whose scales are kept: the warps that read them are not this far behind
@@ -161,11 +162,8 @@ __device__ __forceinline__ bool chunk_ok(const ChunkArgs &a, int32_t r0, int32_t
     return r0 >= 0 && r1 >= r0 && r1 <= a.rows && L >= r1 - r0 && ((int64_t)L + kBlk - 1) / kBlk <= a.bt_stride;
 }
 
-// What a key tile and an item cost a CTA, in about 800 clocks: a key tile of two query tiles
-// 3000 to 3400, of one 2500, an item's start and end about 6500; all at D = 128.  (Two to one for
-// the tiles: the mixed batch of decodes and chunks takes 358 us, four to three 338, captured.)
-__device__ __forceinline__ int tile_cost(const ChunkArgs &a, int32_t ntok) { return ntok > a.TQ ? 4 : 3; }
-constexpr int kItemCost = 8;
+// What a key tile costs a CTA (the including source's constants, with kItemCost, an item's start and end).
+__device__ __forceinline__ int tile_cost(const ChunkArgs &a, int32_t ntok) { return ntok > a.TQ ? kPairCost : kSingleCost; }
 constexpr int kTilesPerCta = 2;  // fewer, and CTAs stay without work: a split costs a merge
 constexpr int kSharedTiles = 128;  // key tiles per CTA from which whole items are dealt round
 
@@ -234,7 +232,7 @@ struct Shared8 {
     uint64_t rfull[kRaw8], rempty[kRaw8];  // tiles of V's codes, which become f16 tiles of the ring
     uint64_t landed;                       // bf16 query tiles, which become codes
     uint32_t vfactor[kRaw8][kBlkPerTile];  // of V's blocks in their tile (f16, twice); the sign: a mark
-    float kscale[kScales8][kBlkPerTile];
+    __align__(16) float kscale[kScales8][kBlkPerTile];
     float2 vtile[kScales8];                // of V's tiles: log2 of the scale, and its reciprocal
     // of each row of the query tiles, by the piece's number mod 2: the next piece's are written as soon as this
     // one's last logits are there, and read for its first; those of the one after only behind the next one's logits
@@ -443,6 +441,11 @@ __device__ __forceinline__ void tmem_wait_ld32(uint32_t (&v)[N], const int o)
                  :
                  : "memory");
     asm volatile("" : "+r"(v[o + 30]), "+r"(v[o + 31]) : : "memory");
+}
+
+__device__ __forceinline__ void ld_shared4(uint32_t addr, float (&x)[4])
+{
+    asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(x[0]), "=f"(x[1]), "=f"(x[2]), "=f"(x[3]) : "r"(addr));
 }
 
 __device__ __forceinline__ float ld_shared(uint32_t addr)
@@ -1561,8 +1564,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                         // a block's keys have a scale of their own (read where it is used: registers are short)
                         if (i == 0) scale2 = a.scale2 * sh8->qscale[np & 1][two ? x : 0][r];
                         mt = -INFINITY;
+                        float kf[4];
 #pragma unroll
                         for (int b = 0; b < kBlkPerTile; ++b) {
+                            if (b % 4 == 0) ld_shared4(ks + b * 4, kf);
                             float mx[2] = {-INFINITY, -INFINITY};
 #pragma unroll
                             for (int c = b * kBlk; c < b * kBlk + kBlk; c += 4)
@@ -1570,7 +1575,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 for (int e = 0; e < 2; ++e)
                                     mx[e] = fmaxf(mx[e], fmaxf(__uint_as_float(s[c + 2 * e]),
                                                                __uint_as_float(s[c + 2 * e + 1])));
-                            mt = fmaxf(mt, fmaxf(mx[0], mx[1]) * ld_shared(ks + b * 4));
+                            mt = fmaxf(mt, fmaxf(mx[0], mx[1]) * kf[b % 4]);
                         }
                         mt = fmaf(mt, scale2, ld_shared(vt));
                     } else {
@@ -1607,10 +1612,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const float mr1 = E8 ? ld_shared(vt) + kUp8 - ref : -ref;
                     const uint64_t mr = pack2(mr1, mr1);
                     uint64_t sum[2] = {0ull, 0ull};
+                    float kf[4];
 #pragma unroll
                     for (int c = 0; c < kTile; c += 2) {
+                        if (E8 && c % (4 * kBlk) == 0) ld_shared4(ks + c / kBlk * 4, kf);
                         if (E8 && c % kBlk == 0) {
-                            const float f = scale2 * ld_shared(ks + c / kBlk * 4);
+                            const float f = scale2 * kf[c / kBlk % 4];
                             sc = pack2(f, f);
                         }
                         float lo, hi;

@@ -5,6 +5,12 @@ namespace {
 constexpr int kStages = 2;  // f16 tiles of V, beside which the tiles of codes in flight lie
 constexpr int kEdges = 1;   // (no edge tiles of V: what converts a tile clears it)
 
+// A key tile of two query tiles, of one, an item's start and end, in 490 clocks: 3900, 2440, and what serves best
+// (its queries are split, its tiles of codes fetched and converted before the first product).  64 sequences of 1 to 128
+// tokens, 48 of 1 to 200, 32 of 1 to 60, 64 of 1 to 8 over short caches: with the bf16 cache's costs 375, 294,
+// 167 and 62.6 us, with these 364, 272, 158 and 62.3; 8 5 20 366 277 159 62.7, 8 5 40 364 269 158 62.2, 8 4 32 377 265 168 62.
+constexpr int kPairCost = 8, kSingleCost = 5, kItemCost = 30;
+
 }  // namespace
 }  // namespace kara
 
