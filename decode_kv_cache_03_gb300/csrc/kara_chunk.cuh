@@ -239,6 +239,8 @@ struct Shared8 {
     float qscale[2][2][kTile];
 };
 
+static_assert(sizeof(Shared) % alignof(Shared8) == 0 && alignof(Shared) >= alignof(Shared8), "Shared8 follows Shared");
+
 // Shared memory: query tiles, the ring, (8 bits: K's codes, V's codes,) barriers and tables.
 template <int D, bool E8>
 struct Cfg {

@@ -352,6 +352,16 @@ def test_decode_matches_plain(hq, hkv, d):
     check_decode(out, *c)
 
 
+@pytest.mark.parametrize("hq,hkv,d", [(4, 2, 64), (40, 8, 128), (8, 1, 128)])
+@pytest.mark.parametrize("lengths", [[0, 1, 17, 1008], [1024, 0, 1025, 3, 2048], [1]])
+def test_decode_around_one_split(lengths, hq, hkv, d):
+    """Sequences of up to 1024 keys, alone (a table that holds no more) and beside longer ones."""
+    case = decode_case(len(lengths) + hq, lengths, hq, hkv, d)
+    st, out = run_decode(*case)
+    assert st == 0
+    check_decode(out, *case)
+
+
 @pytest.mark.parametrize("d", [64, 128])
 def test_decode_far_apart_scales(d):
     """Blocks whose magnitudes differ by up to 2^24, and queries with a few large elements."""
