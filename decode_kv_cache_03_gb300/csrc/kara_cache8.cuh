@@ -95,7 +95,7 @@ inline cudaError_t pool_map8(CUtensorMap *m, const void *pool, const kara_cache8
 cudaError_t launch_append8(const kara_cache8 *c, int32_t layer, const kara_tokens *t, const kara_rope *r, const void *q,
                            int64_t q_stride, const void *k, int64_t k_stride, const void *v, int64_t v_stride,
                            void *q_out, void *ring, int32_t W, int32_t *err, cudaStream_t st);
-int decode8_max_splits(int32_t bt_stride);
+int decode8_max_splits(const kara_cache8 *c, int32_t n, int32_t bt_stride);
 size_t decode8_workspace_bytes(const kara_cache8 *c, int32_t n, int32_t bt_stride);
 cudaError_t launch_decode8(const kara_cache8 *c, int32_t layer, int32_t n, const int32_t *len, const int32_t *bt,
                            int32_t bt_stride, const void *q, void *out, void *ws, int32_t *err, cudaStream_t st);

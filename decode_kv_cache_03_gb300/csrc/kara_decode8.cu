@@ -3,7 +3,7 @@
 //
 // Bound by HBM, at half the bytes of the bf16 cache, so twice as many keys pass through
 // an SM in the same time.  The frame is that of the bf16 kernel: one CTA per (sequence, KV
-// head, split of 1024 keys); a producer warp streams the split's K, then its V, through a
+// head, split of 1024 keys or fewer); a producer warp streams the split's K, then its V, through a
 // ring of 4 KB stages by TMA; four consumer warps turn 16 keys at a time into two small
 // matrix products on the warp-level MMA,
 //     S^T[16 keys][8 heads] = K[16][D] . Q^T[D][8],   O^T[D][8] += V^T[D][16] . P^T[16][8].
@@ -40,7 +40,7 @@ namespace kara {
 
 namespace {
 
-constexpr int kSplit = 1024;        // keys per CTA
+constexpr int kSplit = 1024;        // keys per CTA, at most
 constexpr int kBlk = 16;            // tokens per cache block (the supported block size)
 constexpr int kBlocks = kSplit / kBlk;
 constexpr int kNC = 4;              // consumer warps
@@ -58,7 +58,7 @@ struct Decode8Args {
     int32_t layer, num_blocks, hkv, hq;
     const int32_t *len;
     const int32_t *bt;
-    int32_t bt_stride, max_splits;
+    int32_t bt_stride, split, max_splits;
     const uint16_t *q;   // [n][hq][D]
     const float *k_scale, *v_scale;  // [num_blocks][hkv], at the call's layer
     float *part;         // [n][hq][max_splits][D]
@@ -170,7 +170,7 @@ __device__ __forceinline__ void to_f16_range(float x, float &up, float &down)
 // then the consumers' partial outputs), Shared.
 // Four CTAs per SM up to G = 5; wider groups' logits leave room for three.
 template <int G>
-constexpr int min_ctas() { return G >= 6 ? 3 : 4; }
+constexpr int min_ctas() { return G >= 6 ? 3 : 4; }  // (few_ctas counts on it)
 
 template <int G>
 constexpr size_t smem_bytes()
@@ -236,9 +236,9 @@ __global__ void __launch_bounds__(kThreads, min_ctas<G>())
         }
         return;
     }
-    const int32_t k0 = sp * kSplit;
+    const int32_t k0 = sp * a.split;
     if (k0 >= L) return;
-    const int nk = min(kSplit, L - k0);
+    const int nk = min(a.split, L - k0);
     const int nb = (nk + kBlk - 1) / kBlk, ns = (nb + BPS - 1) / BPS;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
@@ -401,7 +401,7 @@ __global__ void __launch_bounds__(kThreads, min_ctas<G>())
             const float ref = m == -INFINITY ? 0.f : m;
             float *lr = logit + h * kLs;
             z[h] = 0.f, top[h] = 0.f;
-            for (int x = cw * (kSplit / kNC) + lane; x < min(nk, (cw + 1) * (kSplit / kNC)); x += 32) {
+            for (int x = cw * (a.split / kNC) + lane; x < min(nk, (cw + 1) * (a.split / kNC)); x += 32) {
                 const float p = ptx::ex2(lr[x] - ref), w = p * sh->vs[x / kBlk];
                 lr[x] = w;
                 z[h] += p;
@@ -485,7 +485,7 @@ __global__ void __launch_bounds__(kThreads, min_ctas<G>())
         const int64_t row = (int64_t)s * a.hq + g * G + h, idx = row * a.max_splits + sp;
         const auto sum = [&] { return over_warps(sh->sum, h, [](float x, float y) { return x + y; }); };
         v.x *= f, v.y *= f;
-        if (L <= kSplit) {  // nothing to merge
+        if (L <= a.split) {  // nothing to merge
             const float z = sum();
             *reinterpret_cast<uint32_t *>(a.out + row * D + d) = bf16x2(v.x / z, v.y / z);
             continue;
@@ -506,8 +506,8 @@ __global__ void __launch_bounds__(D) decode8_merge_kernel(const Decode8Args a)
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int h = blockIdx.x, s = blockIdx.y, d = threadIdx.x;
     const int32_t L = a.len[s];
-    if (!length_ok(a, L) || L <= kSplit) return;  // written already
-    const int nsp = (L + kSplit - 1) / kSplit;
+    if (!length_ok(a, L) || L <= a.split) return;  // written already
+    const int nsp = (L + a.split - 1) / a.split;
     const int64_t row = (int64_t)s * a.hq + h, base = row * a.max_splits;
     float M = -INFINITY;
     for (int sp = 0; sp < nsp; ++sp) M = fmaxf(M, a.stat[base + sp].x);
@@ -556,11 +556,42 @@ cudaError_t launch(const CUtensorMap &km, const CUtensorMap &vm, const Decode8Ar
 
 }  // namespace
 
-int decode8_max_splits(int32_t bt_stride) { return (int)(((int64_t)bt_stride * kBlk + kSplit - 1) / kSplit); }
+// Keys per CTA: 1024, which serve full batches best, half or a quarter of it while the grid would leave half of the
+// places for CTAs on the SMs empty, the merge has no more than 64 splits to go through, and a table holds more than
+// 512 keys: a single split needs no merge (256 keys: 5.6 us with one, 4.7 without).  (us, captured, with splits of
+// 256, 512 and 1024 keys, the choice in brackets; 40/8 heads of 128: one sequence of 1000 keys [8.8] 11.9 15.2, of
+// 4000 [10.5] 12.5 18.6, of 16000 [16.9] 16.2 20.3, of 64000 63 44 [33]; 4 of 4000 [13.5] 13.8 18.9, 8 of 4000 19.7 [16.5]
+// 20.2, 16 of 4000 38 32 [28]; 16/2 heads: one of 8000 [12.4] 14.5 20.1, of 64000 38 26.7 [26.0], 32 of 4000 28.8 24.7 [21.8].
+// Splits of 128 keys bring one sequence of 1000 to 8.0, and one of 4000 to 11.4.)
+constexpr int kLeast = 256, kMostSplits = 64;
 
+static int64_t splits_of(int32_t bt_stride, int split) { return ((int64_t)bt_stride * kBlk + split - 1) / split; }
+
+// CTAs that fill half of the places.
+static int64_t few_ctas(const kara_cache8 *c) { return 152 * (c->num_q_heads / c->num_kv_heads >= 6 ? 3 : 4) / 2; }
+
+static int split_of(const kara_cache8 *c, int32_t n, int32_t bt_stride)
+{
+    const int64_t rows = (int64_t)n * c->num_kv_heads;
+    int split = kSplit;
+    if (splits_of(bt_stride, 2 * kLeast) == 1) return split;
+    while (split > kLeast && rows * splits_of(bt_stride, split) <= few_ctas(c) &&
+           splits_of(bt_stride, split / 2) <= kMostSplits)
+        split /= 2;
+    return split;
+}
+
+int decode8_max_splits(const kara_cache8 *c, int32_t n, int32_t bt_stride)
+{
+    return (int)splits_of(bt_stride, split_of(c, n, bt_stride));
+}
+
+// Enough for this batch and every smaller one, whose splits may be more: halved splits are at most twice few_ctas.
 size_t decode8_workspace_bytes(const kara_cache8 *c, int32_t n, int32_t bt_stride)
 {
-    const size_t npart = (size_t)n * c->num_q_heads * decode8_max_splits(bt_stride);
+    const int64_t rows = (int64_t)n * c->num_kv_heads, least = rows * splits_of(bt_stride, kSplit);
+    const int64_t most = rows * splits_of(bt_stride, kLeast), halved = most < 2 * few_ctas(c) ? most : 2 * few_ctas(c);
+    const size_t npart = (size_t)(least > halved ? least : halved) * (c->num_q_heads / c->num_kv_heads);
     return align256(npart * c->head_dim * sizeof(float)) + align256(npart * sizeof(float2));
 }
 
@@ -580,7 +611,8 @@ cudaError_t launch_decode8(const kara_cache8 *c, int32_t layer, int32_t n, const
     a.len = len;
     a.bt = bt;
     a.bt_stride = bt_stride;
-    a.max_splits = decode8_max_splits(bt_stride);
+    a.split = split_of(c, n, bt_stride);
+    a.max_splits = decode8_max_splits(c, n, bt_stride);
     a.q = static_cast<const uint16_t *>(q);
     a.k_scale = c->k_scale + scales;
     a.v_scale = c->v_scale + scales;

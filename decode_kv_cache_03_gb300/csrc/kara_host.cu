@@ -501,7 +501,7 @@ kara_status kara_decode_attention8(const kara_cache8 *c, int32_t layer, int32_t 
     if (!aligned16(q) || !aligned16(out)) return KARA_EINVAL;
     if (n > kMaxSeqs || c->num_q_heads > 65535) return KARA_EUNSUPPORTED;
     if ((int64_t)bt_stride * c->block_size > 0x7fffffffLL) return KARA_EUNSUPPORTED;
-    if (decode8_max_splits(bt_stride) > 65535) return KARA_EUNSUPPORTED;  // grid z
+    if (decode8_max_splits(c, n, bt_stride) > 65535) return KARA_EUNSUPPORTED;  // grid z
     if (!ws || ws_bytes < decode8_workspace_bytes(c, n, bt_stride)) return KARA_EWORKSPACE;
     if (!aligned16(ws)) return KARA_EINVAL;
     return cuda_status(launch_decode8(c, layer, n, len, block_table, bt_stride, q, out, ws, err,

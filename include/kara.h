@@ -399,8 +399,10 @@ kara_status kara_append_kv8(const kara_cache8 *c, int32_t layer, const kara_toke
  * length 0 gives zeros and no error.  Queries enter the logits scaled by a power of
  * two for each head, in f16 (exact within 2^-29 of the head's largest element,
  * 2^-40 of it off below); weights times V's scales likewise, rounded to f16: 2^-12
- * of a weight, for those below 2^-29 of the largest 2^-40 of that.  ws is 16-byte
- * aligned, and used by this call alone until it has run.
+ * of a weight, for those below 2^-29 of the largest 2^-40 of that.  Small batches are
+ * cut into shorter splits of the keys (by n, num_kv_heads and bt_stride), so the last
+ * bits depend on those.  ws is 16-byte aligned, and used by this call alone until it
+ * has run; one of kara_decode8_workspace_size serves smaller n and bt_stride too.
  */
 size_t kara_decode8_workspace_size(const kara_cache8 *c, int32_t n, int32_t bt_stride);
 kara_status kara_decode_attention8(const kara_cache8 *c, int32_t layer, int32_t n, const int32_t *len,

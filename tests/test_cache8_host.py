@@ -116,6 +116,17 @@ def test_decode_refuses(kara):
     assert kara.kara_decode8_workspace_size(fake8(kara), 3, 65) >= 3 * 4 * 2 * (64 * 4 + 8)
 
 
+def test_decode_workspace_serves_smaller_batches(kara):
+    """Small batches are split further, but never need more than a larger batch over tables as wide does."""
+    for hq, hkv in ((8, 1), (8, 8), (4, 2), (40, 8)):
+        c = fake8(kara, num_q_heads=hq, num_kv_heads=hkv)
+        for bts in (1, 17, 64, 65, 130, 500, 1000, 4000):
+            sizes = [kara.kara_decode8_workspace_size(c, n, bts) for n in range(1, 80)]
+            assert sizes == sorted(sizes)
+            wide = [kara.kara_decode8_workspace_size(c, n, bts + 1) for n in range(1, 80)]
+            assert all(a <= b for a, b in zip(sizes, wide))
+
+
 def test_chunk_refuses(kara):
     for kw in (dict(layer=-1), dict(layer=2), dict(bt=None), dict(bts=0), dict(q=None), dict(out=None), dict(err=None),
                dict(q=ODD), dict(out=ODD), dict(ws=ODD)):

@@ -353,9 +353,11 @@ def test_decode_matches_plain(hq, hkv, d):
 
 
 @pytest.mark.parametrize("hq,hkv,d", [(4, 2, 64), (40, 8, 128), (8, 1, 128)])
-@pytest.mark.parametrize("lengths", [[0, 1, 17, 1008], [1024, 0, 1025, 3, 2048], [1]])
-def test_decode_around_one_split(lengths, hq, hkv, d):
-    """Sequences of up to 1024 keys, alone (a table that holds no more) and beside longer ones."""
+@pytest.mark.parametrize("lengths", [[0, 1, 17, 255, 256], [1024, 0, 257, 3, 2048], [1], [5000],
+                                     [700, 511, 512, 513, 2049, 255, 256, 257, 1], [1008] * 45, [1024, 1025] * 22])
+def test_decode_splits(lengths, hq, hkv, d):
+    """Splits of 256, 512 and 1024 keys: sequences of one, which write their outputs at once, alone (a table that
+    holds no more) and beside longer ones."""
     case = decode_case(len(lengths) + hq, lengths, hq, hkv, d)
     st, out = run_decode(*case)
     assert st == 0
@@ -442,7 +444,6 @@ def test_decode_strided_pools_and_long_table():
     lengths, bt, k, ks, v, vs, q = decode_case(11, [70, 1100], 10, 2, 64)
     wide = np.full((2, 4000), -1, np.int32)
     wide[:, :bt.shape[1]] = bt
-    want = run_decode(lengths, bt, k, ks, v, vs, q)[1]
     kara = lib()
     big = [torch.full((2, k.shape[1] + 3, 5, BS, 64), 0x7f, dtype=torch.uint8, device=DEV) for _ in range(2)]
     kk, vv = (x[:, 2:-1, 1:3] for x in big)
@@ -453,7 +454,9 @@ def test_decode_strided_pools_and_long_table():
     ws = torch.empty(kara.kara_decode8_workspace_size(c, 2, 4000), dtype=torch.uint8, device=DEV)
     err = error_word()
     kara.kara_decode_attention8(c, 1, i32(lengths), i32(wide), q.to(DEV), out, ws, err)
-    assert status(kara, err) == 0 and torch.equal(out.cpu(), want)
+    # (the width decides on the splits, whose partial sums are added in fp32: not the bits of a narrow table)
+    assert status(kara, err) == 0
+    check_decode(out.cpu(), lengths, bt, k, ks, v, vs, q)
 
 
 # ---- chunk attention ------------------------------------------------------------
