@@ -10,7 +10,7 @@
 // Powers of two: x / s is exact unless it falls among e4m3's subnormals.
 // Both are bound by HBM (a read and a write of every code, or of its bf16 value).  Expansion of 16 windows of
 // 512 keys in 36 layers of 8 heads takes 140 us, the copy rate.  Compaction of 8 sequences (windows of
-// 1024, 396 rows kept) in 40 layers takes 108 us: the copy 88, at 0.85 of the copy rate, and the checks of kept rows and
+// 1024, 396 rows kept) in 40 layers takes 103.5 us: the copy about 84, at 0.9 of the copy rate, and the checks of kept rows and
 // fresh ids, and the plan, ahead of it.
 #include <cuda_fp16.h>
 
@@ -22,7 +22,11 @@ namespace {
 
 constexpr int kBs = 16;  // tokens per cache block (the supported block size)
 constexpr int kThreads = 256;
-constexpr int kSlices = 4;  // slices a thread has in flight
+// Slices that an expanding thread has in flight (16 windows in 36 layers: 2, 4 and 8 take 145, 140 and 160 us).
+constexpr int kSlices = 4;
+// Warps of a compacting CTA, at most: its place is free again when the slowest is done (8 sequences in 40 layers:
+// 16, 8, 4, 2 and 1 take 113, 108, 103.5, 103 and 103 us).
+constexpr int kCopyWarps = 4;
 
 struct Pool8 {
     const uint8_t *codes[2];
@@ -248,7 +252,7 @@ __device__ __forceinline__ void rebuild(const CompactArgs &a)
 }
 
 template <int D>
-__global__ void __launch_bounds__(kThreads, 4) compact8_kernel(const CompactArgs a)
+__global__ void __launch_bounds__(32 * kCopyWarps, 8) compact8_kernel(const CompactArgs a)
 {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     rebuild<D>(a);
@@ -317,8 +321,8 @@ cudaError_t launch_compact8(const kara_cache8 *c, const Geo &g, SeqPlan *plan, i
     a.err = err;
     a.freed = freed, a.new_len = new_len, a.table = table;
     a.g = g;
-    // up to eight new blocks of a window to a CTA, evenly
-    const int parts = (max_new + kThreads / 32 - 1) / (kThreads / 32), warps = (max_new + parts - 1) / parts;
+    // up to kCopyWarps new blocks of a window to a CTA, evenly
+    const int parts = (max_new + kCopyWarps - 1) / kCopyWarps, warps = (max_new + parts - 1) / parts;
     if (g.nwin * parts > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
     const dim3 grid((unsigned)g.nwin, (unsigned)parts);
     const int64_t most = (int64_t)g.n * max_new, used = most < n_fresh ? most : n_fresh;
