@@ -819,3 +819,23 @@ def test_compact_refuses_on_the_device(what, layers, width):
         assert torch.equal(got[0][:, old], k[:, old]) and torch.equal(got[3][:, old], vs[:, old])
     else:
         assert torch.equal(got[0], k) and torch.equal(got[1], v) and torch.equal(got[2], ks) and torch.equal(got[3], vs)
+
+
+def test_compact_compares_more_ids_than_a_tile():
+    """2600 fresh ids: none twice, one twice far apart, one that the last table lists."""
+    W, B, R, n = 256, 40, 200, 160
+    lengths, bt, fresh, k, ks, v, vs = window_case(8, [W + 5] * n, W, 1, 64, 1, extra=2800)
+    kept = np.broadcast_to(np.arange(R, dtype=np.int32), (n, 1, 1, R)).copy()
+    used = n * blocks(5 + R + B)
+    assert used > 2048 and len(fresh) > used
+    st, _, table, freed, new_len = run_compact(lengths, bt, fresh, k, ks, v, vs, kept, W, B, R)
+    assert st == 0 and (new_len == 5 + R + B).all() and table[-1, 0] == fresh[used - blocks(5 + R + B)]
+    again, listed = fresh.copy(), fresh.copy()
+    again[used - 1], listed[3] = fresh[1], bt[n - 1, 2]
+    for ids in (again, listed):
+        st, got, table, freed, new_len = run_compact(lengths, bt, ids, k, ks, v, vs, kept, W, B, R)
+        assert st == lib().EDUPBLOCK and np.array_equal(table, bt) and (freed == -7).all()
+        assert torch.equal(got[0], k) and torch.equal(got[3], vs)
+    again = fresh.copy()
+    again[used] = fresh[0]   # behind the ids that the call takes
+    assert run_compact(lengths, bt, again, k, ks, v, vs, kept, W, B, R)[0] == 0
