@@ -139,8 +139,8 @@ __device__ __forceinline__ uint32_t top_code(uint32_t top, uint32_t w)
     return __vmaxu2(top, __vmaxu2(w & 0x007f007fu, w >> 8 & 0x007f007fu));
 }
 
-// Codes times a power of two from 2^-24 to 2^15, or 0: f16 holds every product exactly that does not round
-// to code 0 anyway.
+// Codes times a power of two up to 2^15, or 0 (below 2^-24 it is): f16 holds every product exactly that does not
+// round to code 0 anyway.
 __device__ __forceinline__ uint32_t shift4(uint32_t w, __half2 f)
 {
     const uint32_t lo = f16_of_e4m3x2(w & 0xffffu), hi = f16_of_e4m3x2(w >> 16);
@@ -234,12 +234,14 @@ __device__ __forceinline__ void rebuild(const CompactArgs &a)
         uint8_t *out = a.codes[k] + head + dst * a.in.block_stride + row * D + c * 16;
 #pragma unroll
         for (int i = 0; i < NP; ++i) {
-            const float ratio = f[k][i] * inv;
+            // (2^17 at most for a row with a code that is not 0: 448 of the new scale against 2^-9 of the old one.  Rows of
+            // zeros set no scale, and times an infinity they would be no numbers)
+            const float ratio = fminf(f[k][i] * inv, 131072.f);
             if (ratio != 1.f) {
                 const __half2 h = __float2half2_rn(fminf(ratio, 32768.f));
                 w[k][i].x = shift4(w[k][i].x, h), w[k][i].y = shift4(w[k][i].y, h);
                 w[k][i].z = shift4(w[k][i].z, h), w[k][i].w = shift4(w[k][i].w, h);
-                if (ratio > 32768.f) {  // (2^17 at most: what is left of it)
+                if (ratio > 32768.f) {  // what is left of it
                     const __half2 g = __float2half2_rn(ratio * (1.f / 32768.f));
                     w[k][i].x = shift4(w[k][i].x, g), w[k][i].y = shift4(w[k][i].y, g);
                     w[k][i].z = shift4(w[k][i].z, g), w[k][i].w = shift4(w[k][i].w, g);
