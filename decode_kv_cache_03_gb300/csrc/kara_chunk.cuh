@@ -94,6 +94,8 @@ constexpr int kBlkPerTile = kTile / kBlk;
 // kEdges and the costs by which the work is cut.)
 constexpr int kK8 = 3;           // of an 8-bit cache: tiles of K's codes in flight,
 constexpr int kRaw8 = 2;         // and of V's
+constexpr int kApart8 = 8;       // scales of a tile of V this many powers of two apart, at most: one exponent for the tile
+constexpr float kFar8 = 0x1p126f;  // stands for that exponent where they are further apart
 constexpr int kScales8 = 8;      // K tiles whose scales are kept: the warps that read them are not this far behind
 constexpr int kMaxCtas = 160;    // CTAs of the attention kernel, at most (workspace slots)
 constexpr int kMaxRounds = 64;   // whole items that a CTA takes ahead of its range, at most
@@ -233,7 +235,9 @@ struct Shared8 {
     uint64_t landed;                       // bf16 query tiles, which become codes
     uint32_t vfactor[kRaw8][kBlkPerTile];  // of V's blocks in their tile (f16, twice); the sign: a mark
     __align__(16) float kscale[kScales8][kBlkPerTile];
-    float2 vtile[kScales8];                // of V's tiles: log2 of the scale, and its reciprocal
+    float vexp[kScales8][kBlkPerTile];     // log2 of V's scales over 2^kUpV8
+    // of V's tiles: log2 of the scale, its reciprocal and log2 again; blocks apart: kFar8, 0 and 0
+    __align__(16) float vtile[kScales8][4];
     // of each row of the query tiles, by the piece's number mod 2: the next piece's are written as soon as this
     // one's last logits are there, and read for its first; those of the one after only behind the next one's logits
     float qscale[2][2][kTile];
@@ -833,9 +837,15 @@ __device__ __noinline__ void add_cleared(const ChunkArgs &a, int seq, int head, 
 // V's codes become f16 tiles of the ring, times their block's scale over 2^e, e of the tile's largest; 2^e goes into
 // the weights, which are rounded to f16:
 //     w_x = 2^(l_x + e - M + kUp8),   O = sum_x w_x (v_x 2^-e),   z = sum over tiles of 2^-e sum_x w_x,
-// M the largest l_x + e so far (lazily, as above).  Values within 2^-20 of the tile's largest scale are exact, smaller
-// ones off by 2^-40 of it.  Weights within 2^-21 of the largest keep eleven bits, smaller ones are off by
-// at most 2^-32 of it, and with the maximum's growth of 2^8 the largest stay within f16.
+// M the largest l_x + e so far (lazily, as above): weights within 2^-21 of it keep eleven bits, smaller ones are off by
+// 2^-32 of it, and with the maximum's growth of 2^8 the largest stay within f16.  That is for tiles whose blocks' scales
+// are no more than 2^kApart8 apart: f16 holds their values exactly, and M is at most that much above a row's largest
+// weight times its own block's scale, whose 2^-24 bounds the error.  Further apart, a block that a row does not see, or gives no
+// weight, would take the others' digits: then each block has an e of its own (logits_apart, out of line: the logits are
+// written anew, V's tile holds the codes themselves, and z is summed from weights without e).  K's and V's loading warps tell
+// such tiles apart.  A row meets one where its largest logit seems to grow beyond all bounds (vtile), in the branch that it takes
+// then anyway: a check of its own in every tile took the mixed batch from 368 to 398 us, this takes it to 372, the prompt
+// from 1620 to 1640.
 // (As bf16, exact at any scale, two codes took four instructions instead of two, and weights kept eight bits: 64
 // sequences of 1 to 128 tokens 387 us and 379, four tokens for each of 128 sequences 611 and 604, one prompt alike.
 // With a scale for each block in the weights, and one instruction, the softmax took longer: 409 and 613.)
@@ -1086,6 +1096,66 @@ __device__ __forceinline__ void convert_tiles(int cw, uint8_t *qbuf, uint8_t *ri
     }
     // the last query tiles have landed too
     if (nq > 0) drain(smem_u32(&sh8->landed), (nq - 1) & 1);
+}
+
+// The reference m of a row's exponentials becomes mt if that is much larger, and its sums z and O (in TMEM) follow.
+template <int D>
+__device__ __forceinline__ void raise_reference(uint32_t to, float mt, float &m, float &z)
+{
+    const bool grew = mt > m + kLazy;
+    const float f = grew ? ex2(m - mt) : 1.f;
+    if (grew) m = mt;
+    z *= f;
+#pragma unroll 1
+    for (int c = 0; c < D; c += 32) {
+        uint32_t o[32];
+        tmem_ld32(to + c, o, 0);
+        tmem_wait_ld32(o, 0);
+#pragma unroll
+        for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+        tmem_st32(to + c, o, 0);
+    }
+    tmem_wait_st();
+}
+
+// A row's logits in a key tile whose blocks of V are apart: log2 of a block's scale, and not of the tile's, goes into its
+// keys' logits (in TMEM; -infinity for those that the row does not see), and the weights without it into z.  Returns
+// the row's m and z.  (In the registers of the loop that calls it this made the ordinary tiles 10 % slower.)
+template <int D>
+__device__ __noinline__ float2 logits_apart(uint32_t ts, uint32_t to, const float *kscale, const float *vexp, float scale2,
+                                            int lim, bool first, float2 mz)
+{
+    float mt = -INFINITY;
+#pragma unroll 1
+    for (int c = 0; c < kTile; c += 32) {
+        uint32_t s[32];
+        tmem_ld32(ts + c, s, 0);
+        tmem_wait_ld32(s, 0);
+#pragma unroll
+        for (int e = 0; e < 32; ++e) {
+            const float f = scale2 * kscale[(c + e) / kBlk];
+            const float l = c + e <= lim ? __uint_as_float(s[e]) + vexp[(c + e) / kBlk] / f : -INFINITY;
+            mt = fmaxf(mt, l * f);
+            s[e] = __float_as_uint(l);
+        }
+        tmem_st32(ts + c, s, 0);
+    }
+    tmem_wait_st();
+    if (first)
+        mz.x = mt;
+    else if (__any_sync(0xffffffffu, mt > mz.x + kLazy))
+        raise_reference<D>(to, mt, mz.x, mz.y);
+    const float up = kUp8 - (mz.x == -INFINITY ? 0.f : mz.x);
+#pragma unroll 1
+    for (int c = 0; c < kTile; c += 32) {
+        uint32_t s[32];
+        tmem_ld32(ts + c, s, 0);
+        tmem_wait_ld32(s, 0);
+#pragma unroll
+        for (int e = 0; e < 32; ++e)
+            mz.y += ex2(fmaf(__uint_as_float(s[e]), scale2 * kscale[(c + e) / kBlk], up - vexp[(c + e) / kBlk]));
+    }
+    return mz;
 }
 
 // Records the sequences whose rows or lengths are out of order and zeroes their rows.
@@ -1385,16 +1455,23 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const uint32_t fb = smem_u32((kv ? sh8->rfull : sh8->kfull) + st);
                         ok = __all_sync(0xffffffffu, kwait(smem_u32((kv ? sh8->rempty : sh8->kempty) + st), ph, sh, a));
                         if (!ok) break;
+                        const bool live = mine && j * kBlkPerTile + b < nblk;
                         const int e = mine ? scale_log2(vs) : -63;
                         const int et = __reduce_max_sync(0xffffffffu, e) - kUpV8;
+                        const bool apart = __any_sync(0xffffffffu, live && e < et + kUpV8 - kApart8);
                         if (kv) {
-                            if (mine) sh8->vfactor[st][b] = f16_power2(e - et) | (__float_as_uint(vs) & 0x80000000u);
+                            if (mine)
+                                sh8->vfactor[st][b] =
+                                    f16_power2(apart ? kUpV8 : e - et) | (__float_as_uint(vs) & 0x80000000u);
                         } else {
                             // (codes of zeros alone are what they are at any scale, and 0 times a
                             // masked logit's infinity is none)
                             if (mine) sh8->kscale[k % kScales8][b] = ks == 0.f ? 1.f : fabsf(ks);
+                            if (mine) sh8->vexp[k % kScales8][b] = (float)(e - kUpV8);
                             if (lane == 0)
-                                sh8->vtile[k % kScales8] = make_float2((float)et, __uint_as_float((uint32_t)(127 - et) << 23));
+                                *reinterpret_cast<float4 *>(sh8->vtile[k % kScales8]) =
+                                    apart ? make_float4(kFar8, 0.f, 0.f, 0.f)
+                                          : make_float4((float)et, __uint_as_float((uint32_t)(127 - et) << 23), (float)et, 0.f);
                         }
                         __syncwarp();
                         if (lane == 0) mbar_arrive_expect_tx(fb, C::kRawBytes);
@@ -1549,11 +1626,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (any) {
                     tc_fence_after();
                     uint32_t s[kTile];
+                    const int lim = pos - j * kTile;  // last key of the tile that the row sees
 #pragma unroll
                     for (int c = 0; c < 4; ++c) tmem_ld32(ts + c * 32, s, c * 32);
 #pragma unroll
                     for (int c = 0; c < 4; ++c) tmem_wait_ld32(s, c * 32);
-                    const int lim = pos - j * kTile;  // last key of the tile that the row sees
                     if (__builtin_expect(__any_sync(0xffffffffu, lim < kTile - 1), 0)) {
 #pragma unroll
                         for (int c = 0; c < kTile; ++c)
@@ -1561,7 +1638,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     float mt;
                     const uint32_t ks = smem_u32(sh8->kscale[(nk + j - p.j0) % kScales8]);
-                    const uint32_t vt = smem_u32(sh8->vtile + (nk + j - p.j0) % kScales8);
+                    const uint32_t vt = smem_u32(sh8->vtile[(nk + j - p.j0) % kScales8]);
                     if constexpr (E8) {
                         // a block's keys have a scale of their own (read where it is used: registers are short)
                         if (i == 0) scale2 = a.scale2 * sh8->qscale[np & 1][two ? x : 0][r];
@@ -1589,29 +1666,34 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 mx[e] = fmaxf(mx[e], fmaxf(__uint_as_float(s[c + 2 * e]), __uint_as_float(s[c + 2 * e + 1])));
                         mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.scale2;
                     }
-                    if (i == 0) {
-                        m = mt;
-                    } else {
-                        const bool grew = mt > m + kLazy;
-                        if (__builtin_expect(__any_sync(0xffffffffu, grew), 0)) {
-                            const float f = grew ? ex2(m - mt) : 1.f;
-                            if (grew) m = mt;
-                            z *= f;
-#pragma unroll 1
-                            for (int c = 0; c < D; c += 32) {
-                                uint32_t o[32];
-                                tmem_ld32(to + c, o, 0);
-                                tmem_wait_ld32(o, 0);
+                    if constexpr (E8) {
+                        if (__builtin_expect(i == 0 || __any_sync(0xffffffffu, mt > m + kLazy), 0)) {
+                            // (a tile of blocks apart has logits this large)
+                            if (__any_sync(0xffffffffu, mt >= kFar8 / 2) && ld_shared(vt + 4) == 0.f) {
+                                const int slot = (nk + j - p.j0) % kScales8;
+                                const float2 mz = logits_apart<D>(ts, to, sh8->kscale[slot], sh8->vexp[slot], scale2, lim,
+                                                                  i == 0, make_float2(m, z));
+                                m = mz.x, z = mz.y;
 #pragma unroll
-                                for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                                tmem_st32(to + c, o, 0);
+                                for (int c = 0; c < 4; ++c) tmem_ld32(ts + c * 32, s, c * 32);
+#pragma unroll
+                                for (int c = 0; c < 4; ++c) tmem_wait_ld32(s, c * 32);
+                            } else if (i == 0) {
+                                m = mt;
+                            } else {
+                                raise_reference<D>(to, mt, m, z);
                             }
-                            tmem_wait_st();
+                        }
+                    } else {
+                        if (i == 0) {
+                            m = mt;
+                        } else if (__builtin_expect(__any_sync(0xffffffffu, mt > m + kLazy), 0)) {
+                            raise_reference<D>(to, mt, m, z);
                         }
                     }
                     const float ref = m == -INFINITY ? 0.f : m;  // a row that saw nothing yet: weights 2^-inf = 0
                     uint64_t sc = pack2(scale2, scale2);
-                    const float mr1 = E8 ? ld_shared(vt) + kUp8 - ref : -ref;
+                    const float mr1 = E8 ? ld_shared(vt + 8) + kUp8 - ref : -ref;
                     const uint64_t mr = pack2(mr1, mr1);
                     uint64_t sum[2] = {0ull, 0ull};
                     float kf[4];

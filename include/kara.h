@@ -415,10 +415,10 @@ kara_status kara_decode_attention8(const kara_cache8 *c, int32_t layer, int32_t 
  * queries enter the logits as two e4m3 terms of a power of two times themselves:
  * elements within 2^-10 of a row's largest are exact, smaller ones off by at most
  * 2^-17 of the largest (or 2^-50); and that weights are rounded to f16, with V's
- * scales in them: by 2^-11 of a weight, or 2^-32 of the largest weight times scale
- * of the row.  V's values are exact within 2^-20 of the largest scale among the 128
- * keys around, 2^-40 of it off below.  A key or value that is NaN reaches only the
- * rows that see it.
+ * scales in them: by 2^-11 of a weight, or a weight times its scale by 2^-24 of the
+ * row's largest such product.  V's values are exact.  A key or value that is NaN
+ * reaches only the rows that see it.  A row's last bits may depend on V's scales in
+ * all blocks of the 128 keys around one that it sees, later tokens' blocks too.
  */
 size_t kara_chunk8_workspace_size(const kara_cache8 *c, int32_t n, int32_t rows);
 kara_status kara_chunk_attention8(const kara_cache8 *c, int32_t layer, const kara_tokens *t,

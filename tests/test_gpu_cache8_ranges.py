@@ -1,12 +1,23 @@
-"""GPU tests of the 8-bit cache's calls where blocks' scales lie far apart, against 64 bits."""
+"""GPU tests of the 8-bit cache's calls where blocks' scales lie far apart, against 64 bits.
+
+Chunk attention's tolerance, before the first run, from what include/kara.h states (a rounding is off by at most half a
+step: bf16 2^-8, f16 2^-11).  With p_x a row's weights, s_x the scale of the block that key x lies in, in V, and P the
+row's largest p_x s_x:
+    output   2^-8 |ref|
+    weights  sum_x max(2^-11 p_x, 2^-24 P / s_x) |v_x|: an f16 rounding, or half of f16's smallest step, 2^-25, where the
+             largest weight times scale is 2^-1 at least (2^7, but for scales of a tile that are up to 2^8 apart)
+    logits   a weight is off by its logit's error, and the sum of all by as much: twice 2^-17 of the query's largest
+             element times the keys' dims whose query element is below 2^-10 of it; 2^-20 of the sum of the products'
+             magnitudes (256 fp32 additions of exact products, at 2^-28 to 2^-22 of the largest partial sum); 2^-15 for
+             the logit's scaling, the subtraction of the row's reference (up to 2^7 in log2: 2^-17) and the exponential."""
 
 import numpy as np
 import pytest
 import torch
 
-from _cache8 import BS, plain_compact, source_rows, value
+from _cache8 import BS, dense, plain_compact, quantise, source_rows, value
 from _newtokens import blocks
-from test_gpu_cache8 import run_compact, window_case
+from test_gpu_cache8 import chunk_case, run_chunk, run_compact, window_case
 
 pytestmark = pytest.mark.gpu
 
@@ -43,3 +54,74 @@ def test_compact_zero_rows_of_a_large_block(d, apart):
             for j, (wc, ws) in enumerate(want):
                 assert torch.equal(got[2 + pool][0, fresh[j], g], ws.float())
                 assert torch.equal(got[pool][0, fresh[j], g, :len(wc)], wc)
+
+
+# ---- chunk attention ------------------------------------------------------------
+
+def check_chunk(c, got, rows=None):
+    """Rows of a chunk's output (all, or those of the given numbers) within the tolerance above."""
+    hq, D = c["q"].shape[1:]
+    hkv = c["k"].shape[2]
+    G, worst = hq // hkv, 0.0
+    k_all, v_all = (dense(c[x], c[x + "s"])[0] for x in "kv")
+    for s, L in enumerate(int(x) for x in c["lengths"]):
+        t0, t1 = int(c["q_start"][s]), int(c["q_start"][s + 1])
+        ids = torch.as_tensor(c["bt"][s, :blocks(L)]).long()
+        for g in range(hkv):
+            k, v = (x[ids, g].reshape(-1, D)[:L] for x in (k_all, v_all))
+            sv = c["vs"][0, ids, g].double().abs().repeat_interleave(BS)[:L]
+            for t in range(t0, t1):
+                if rows is not None and t not in rows:
+                    continue
+                n = L - (t1 - t) + 1
+                q = c["q"][t, g * G:(g + 1) * G].double()
+                p = torch.softmax(q @ k[:n].T / D ** 0.5, -1)
+                top = q.abs().amax(-1, keepdim=True)
+                small = torch.where(q.abs() < 2.0 ** -10 * top, top, 0.0)
+                logit = 2.0 ** -17 * small @ k[:n].abs().T + 2.0 ** -20 * (q.abs() @ k[:n].abs().T)
+                most = (p * sv[:n]).amax(-1, keepdim=True)
+                w = torch.maximum(2.0 ** -11 * p, 2.0 ** -24 * most / torch.where(sv[:n] > 0, sv[:n], torch.inf))
+                w = w + p * 2 * (logit.amax(-1, keepdim=True) / D ** 0.5 + 2.0 ** -15)
+                ref, lim = p @ v[:n], w @ v[:n].abs()
+                off = (got[t, g * G:(g + 1) * G].double() - ref).abs() / (ref.abs() * 2.0 ** -8 + lim)
+                assert (ref.abs() * 2.0 ** -8 + lim > 0).all() and off.max() <= 1, (s, g, t, float(off.max()))
+                worst = max(worst, float(off.max()))
+    return worst
+
+
+SHAPES = [(8, 2, 128), (4, 2, 64), (5, 1, 128)]
+
+
+@pytest.mark.parametrize("hq,hkv,d", SHAPES)
+@pytest.mark.parametrize("n_new", [100, 5])
+@pytest.mark.parametrize("up", [9, 20, 40, 60])
+def test_chunk_rows_before_a_large_value(hq, hkv, d, n_new, up):
+    """Blocks of V that hold later tokens only, 2^up above the others: rows that do not see them are what they are
+    without them, within the tolerance of their own values."""
+    L = 300
+    c = chunk_case(up + d, [L, L - 7], [n_new, n_new], hq, hkv, d)
+    for s in range(2):
+        c["vs"][0, int(c["bt"][s, (L - 1 - 7 * s) // BS])] *= 2.0 ** up
+    st, got = run_chunk(c)
+    assert st == 0
+    check_chunk(c, got)
+
+
+@pytest.mark.parametrize("hq,hkv,d", SHAPES)
+@pytest.mark.parametrize("n_new", [60, 1])
+@pytest.mark.parametrize("up,down", [(9, 5), (20, 15), (30, 30), (40, 60), (60, 60), (60, 90), (-60, 0), (-40, -20)])
+def test_chunk_large_values_of_small_weight(hq, hkv, d, n_new, up, down):
+    """A block that every row sees, with V 2^up above (below) the others and logits about 2^down times less (more)
+    likely: what it adds counts, and takes nothing from the rest."""
+    L = 400
+    c = chunk_case(1000 + up + 2 * down + d, [L], [n_new], hq, hkv, d)
+    g = torch.Generator().manual_seed(up + 107)
+    lean = 1.0 + torch.randint(0, 2, (d,), generator=g).double()     # what all queries have in common
+    c["q"] = (lean + 0.1 * torch.randn(c["q"].shape, generator=g)).bfloat16()
+    at = int(c["bt"][0, 20])                                         # positions 320 to 335, in the same tile as the end
+    far = -down * np.log(2.0) * d ** 0.5 * lean / (lean * lean).sum() * torch.ones(hkv, BS, 1)
+    c["k"][0, at], c["ks"][0, at] = quantise(far + 0.01 * torch.randn(hkv, BS, d, generator=g))
+    c["vs"][0, at] *= 2.0 ** up
+    st, got = run_chunk(c)
+    assert st == 0
+    check_chunk(c, got)
