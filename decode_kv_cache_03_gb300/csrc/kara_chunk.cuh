@@ -95,7 +95,8 @@ constexpr int kBlkPerTile = kTile / kBlk;
 constexpr int kK8 = 3;           // of an 8-bit cache: tiles of K's codes in flight,
 constexpr int kRaw8 = 2;         // and of V's
 constexpr int kApart8 = 8;       // scales of a tile of V this many powers of two apart, at most: one exponent for the tile
-constexpr float kFar8 = 0x1p126f;  // stands for that exponent where they are further apart
+constexpr int kLeast8 = -40;     // and that exponent not below this
+constexpr float kFar8 = 0x1p126f;  // stands for it where there is none
 constexpr int kScales8 = 8;      // K tiles whose scales are kept: the warps that read them are not this far behind
 constexpr int kMaxCtas = 160;    // CTAs of the attention kernel, at most (workspace slots)
 constexpr int kMaxRounds = 64;   // whole items that a CTA takes ahead of its range, at most
@@ -842,10 +843,12 @@ __device__ __noinline__ void add_cleared(const ChunkArgs &a, int seq, int head, 
 // are no more than 2^kApart8 apart: f16 holds their values exactly, and M is at most that much above a row's largest
 // weight times its own block's scale, whose 2^-24 bounds the error.  Further apart, a block that a row does not see, or gives no
 // weight, would take the others' digits: then each block has an e of its own (logits_apart, out of line: the logits are
-// written anew, V's tile holds the codes themselves, and z is summed from weights without e).  K's and V's loading warps tell
+// written anew, V's tile holds the codes themselves, and z is summed from weights without e).  So have the blocks of tiles
+// with an e below kLeast8, of zeros for one: with M from a tile at 2^57, the scaled weights of keys that count in z would
+// leave fp32's range (w is 2^(kUp8 - 24 + kLeast8 - 57) = 2^-114 at least for those within 2^-24 of the largest weight).  K's and V's loading warps tell
 // such tiles apart.  A row meets one where its largest logit seems to grow beyond all bounds (vtile), in the branch that it takes
-// then anyway: a check of its own in every tile took the mixed batch from 368 to 398 us, this takes it to 372, the prompt
-// from 1620 to 1640.
+// then anyway: a check of its own in every tile took the mixed batch from 368 to 398 us, this takes it to 370, four tokens for
+// each of 128 sequences from 607 to 612, the prompt from 1620 to 1625.
 // (As bf16, exact at any scale, two codes took four instructions instead of two, and weights kept eight bits: 64
 // sequences of 1 to 128 tokens 387 us and 379, four tokens for each of 128 sequences 611 and 604, one prompt alike.
 // With a scale for each block in the weights, and one instruction, the softmax took longer: 409 and 613.)
@@ -1098,14 +1101,24 @@ __device__ __forceinline__ void convert_tiles(int cw, uint8_t *qbuf, uint8_t *ri
     if (nq > 0) drain(smem_u32(&sh8->landed), (nq - 1) & 1);
 }
 
+// z times 2^x, x up to 0.  With the 8-bit cache's V scales in its reference a sum of weights may be far above 1, and count
+// although 2^x itself is below fp32's range: half of x at a time.
+template <bool E8>
+__device__ __forceinline__ float scale_sum(float z, float x, float f)
+{
+    if (!E8) return z * f;
+    const float h = ex2(0.5f * x);
+    return z * h * h;
+}
+
 // The reference m of a row's exponentials becomes mt if that is much larger, and its sums z and O (in TMEM) follow.
-template <int D>
+template <int D, bool E8>
 __device__ __forceinline__ void raise_reference(uint32_t to, float mt, float &m, float &z)
 {
     const bool grew = mt > m + kLazy;
     const float f = grew ? ex2(m - mt) : 1.f;
+    z = scale_sum<E8>(z, grew ? m - mt : 0.f, f);
     if (grew) m = mt;
-    z *= f;
 #pragma unroll 1
     for (int c = 0; c < D; c += 32) {
         uint32_t o[32];
@@ -1144,7 +1157,7 @@ __device__ __noinline__ float2 logits_apart(uint32_t ts, uint32_t to, const floa
     if (first)
         mz.x = mt;
     else if (__any_sync(0xffffffffu, mt > mz.x + kLazy))
-        raise_reference<D>(to, mt, mz.x, mz.y);
+        raise_reference<D, true>(to, mt, mz.x, mz.y);
     const float up = kUp8 - (mz.x == -INFINITY ? 0.f : mz.x);
 #pragma unroll 1
     for (int c = 0; c < kTile; c += 32) {
@@ -1458,7 +1471,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const bool live = mine && j * kBlkPerTile + b < nblk;
                         const int e = mine ? scale_log2(vs) : -63;
                         const int et = __reduce_max_sync(0xffffffffu, e) - kUpV8;
-                        const bool apart = __any_sync(0xffffffffu, live && e < et + kUpV8 - kApart8);
+                        const bool apart = et < kLeast8 || __any_sync(0xffffffffu, live && e < et + kUpV8 - kApart8);
                         if (kv) {
                             if (mine)
                                 sh8->vfactor[st][b] =
@@ -1681,14 +1694,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                             } else if (i == 0) {
                                 m = mt;
                             } else {
-                                raise_reference<D>(to, mt, m, z);
+                                raise_reference<D, E8>(to, mt, m, z);
                             }
                         }
                     } else {
                         if (i == 0) {
                             m = mt;
                         } else if (__builtin_expect(__any_sync(0xffffffffu, mt > m + kLazy), 0)) {
-                            raise_reference<D>(to, mt, m, z);
+                            raise_reference<D, E8>(to, mt, m, z);
                         }
                     }
                     const float ref = m == -INFINITY ? 0.f : m;  // a row that saw nothing yet: weights 2^-inf = 0
@@ -1754,8 +1767,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const float M = fmaxf(m, o.x), ref = M == -INFINITY ? 0.f : M;
                     f0 = ex2(m - ref);
                     f1 = ex2(o.x - ref);
+                    z = E8 ? scale_sum<E8>(z, m - ref, f0) + scale_sum<E8>(o.y, o.x - ref, f1) : z * f0 + o.y * f1;
                     m = M;
-                    z = z * f0 + o.y * f1;
                 }
             }
             ok = __all_sync(0xffffffffu, ok);
@@ -1840,7 +1853,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 // Block (c, y): the item that the cut before CTA c falls into, if that is the item's
 // first cut: out = sum_i O_i 2^(m_i - M) / sum_i z_i 2^(m_i - M), pieces in CTA order.
 // A thread takes 8 dims of a row; lanes are rows, as the partials lie.
-template <int D>
+template <int D, bool E8>
 __global__ void __launch_bounds__(256) chunk_merge_kernel(const ChunkArgs a)
 {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -1872,7 +1885,7 @@ __global__ void __launch_bounds__(256) chunk_merge_kernel(const ChunkArgs a)
         const float2 st = a.stat[slot * 256 + rr];
         if (st.x == -INFINITY && st.y == 0.f) continue;  // nothing of this piece is seen by the row
         const float f = ex2(st.x - M);
-        den = fmaf(st.y, f, den);
+        den = E8 ? den + scale_sum<E8>(st.y, st.x - M, f) : fmaf(st.y, f, den);
         const float4 u = a.part[(slot * (D / 4) + d4) * 256 + rr], v = a.part[(slot * (D / 4) + d4 + 1) * 256 + rr];
         acc[0] = fmaf(u.x, f, acc[0]), acc[1] = fmaf(u.y, f, acc[1]), acc[2] = fmaf(u.z, f, acc[2]);
         acc[3] = fmaf(u.w, f, acc[3]), acc[4] = fmaf(v.x, f, acc[4]), acc[5] = fmaf(v.y, f, acc[5]);
@@ -1929,7 +1942,7 @@ cudaError_t launch_all(const CUtensorMap &km, const CUtensorMap &vm, const CUten
     if (e != cudaSuccess) return e;
     e = launch_dependent(chunk_kernel<D, E8>, dim3((unsigned)a.ctas), kThreads, smem, st, km, vm, qm, a);
     if (e == cudaSuccess && a.ctas > 1)
-        e = launch_dependent(chunk_merge_kernel<D>, dim3((unsigned)a.ctas - 1, 8 * (D / 64)), 256, 0, st, a);
+        e = launch_dependent(chunk_merge_kernel<D, E8>, dim3((unsigned)a.ctas - 1, 8 * (D / 64)), 256, 0, st, a);
     return e;
 }
 

@@ -125,3 +125,50 @@ def test_chunk_large_values_of_small_weight(hq, hkv, d, n_new, up, down):
     st, got = run_chunk(c)
     assert st == 0
     check_chunk(c, got)
+
+
+@pytest.mark.parametrize("n_new", [1, 3, 150])
+@pytest.mark.parametrize("zeros", [True, False])
+@pytest.mark.parametrize("up", [63, 60, 50, 30])
+@pytest.mark.parametrize("where", ["first", "middle", "last"])
+def test_chunk_tiles_of_far_apart_scales(n_new, zeros, up, where):
+    """One tile of V at 2^up, all others zeros or at 2^-63, each key with its part of the weight: more than a
+    thousandth of it to about half of it in the one tile."""
+    tiles, d, hq, hkv = 36, 64, 4, 2
+    L = tiles * 128
+    c = chunk_case(7 + up, [L, 700], [n_new, 2], hq, hkv, d, qmag=1.0)
+    g = torch.Generator().manual_seed(up)
+    lean = 1.0 + torch.randint(0, 2, (d,), generator=g).double()
+    c["q"] = (lean + 0.3 * torch.randn(c["q"].shape, generator=g)).bfloat16()
+    one = {"first": 0, "middle": 17, "last": tiles - 2}[where]
+    ids = torch.as_tensor(c["bt"][0, :blocks(L)]).long()
+    big = ids[8 * one:8 * one + 8]
+    c["vs"][0, ids] = 0.0 if zeros else 2.0 ** -63
+    if zeros:
+        c["v"][0, ids] = 0
+    c["v"][0, big], c["vs"][0, big] = quantise(torch.randn(8, hkv, BS, d, generator=g))
+    c["vs"][0, big] = 2.0 ** up
+    for i, bits in enumerate([0, 3, 6]):     # of a third of the tile: its keys' weight over the others', log2
+        blk = big[i::3]
+        up_by = bits * np.log(2.0) * d ** 0.5 * lean / (lean * lean).sum() * torch.ones(len(blk), hkv, BS, 1)
+        c["k"][0, blk], c["ks"][0, blk] = quantise(up_by + 0.01 * torch.randn(up_by.shape, generator=g))
+    far = torch.ones(len(ids), dtype=torch.bool)
+    far[8 * one:8 * one + 8] = False
+    c["k"][0, ids[far]], c["ks"][0, ids[far]] = quantise(0.05 * torch.randn(int(far.sum()), hkv, BS, d, generator=g))
+    st, got = run_chunk(c)
+    assert st == 0
+    check_chunk(c, got, rows=None if n_new < 100 else list(range(0, n_new, 13)) + [n_new, n_new + 1])
+
+
+@pytest.mark.parametrize("lo,hi", [(-63, 63), (-63, 0), (0, 63), (-20, 20)])
+def test_chunk_scales_at_random(lo, hi):
+    """Every block of V with a scale of its own, and of K too; one call in one tile, one cut into many pieces."""
+    for L, n_new, hq, hkv, d in ((100, 40, 8, 2, 64), (5000, 7, 4, 2, 128)):
+        c = chunk_case(L + lo + hi + 200, [L, 33], [n_new, 5], hq, hkv, d, qmag=1.0)
+        g = torch.Generator().manual_seed(L + hi)
+        shape = c["vs"][0].shape
+        c["vs"][0] = c["vs"][0].sign() * 2.0 ** torch.randint(lo, hi + 1, shape, generator=g).float()
+        c["ks"][0] = c["ks"][0].sign() * 2.0 ** torch.randint(-9, -6, shape, generator=g).float()
+        st, got = run_chunk(c)
+        assert st == 0
+        check_chunk(c, got)
