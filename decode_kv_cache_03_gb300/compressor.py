@@ -141,7 +141,8 @@ class Compressor8(Compressor):
                 kara.kara_workspace_size(cache16, p, n), windows * (p.W - p.B) * 4, windows * p.K * 4,
                 windows * p.R * 4, kara.kara_compact8_workspace_size(c, p, n))
 
-    def workspace(self, n: int, stream=None, bt_stride: int = 1) -> torch.Tensor:
+    def workspace(self, n: int, stream=None, *, bt_stride: int) -> torch.Tensor:
+        """What compress() of n sequences uses, with block tables of bt_stride columns: the windows have a table too."""
         return self._space("_xws", _pieces(self._compress_sizes(n, bt_stride))[1], stream)
 
     def compress(self, lengths, block_table, q, fresh, freed, new_len, scores=None, cand=None, kept=None,

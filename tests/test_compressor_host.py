@@ -1,0 +1,25 @@
+"""The workspaces of Compressor and Compressor8, without a GPU: the pools lie in host memory and no call is made."""
+
+import pytest
+import torch
+
+
+def make8(layers=2, nb=9, hkv=2, d=64, hq=4, W=64):
+    from decode_kv_cache_03_gb300 import Compressor8, build
+    build.build()
+    codes = [torch.zeros(layers, nb, hkv, 16, d, dtype=torch.uint8) for _ in range(2)]
+    scales = [torch.zeros(layers, nb, hkv) for _ in range(2)]
+    return Compressor8(*codes, *scales, hq, W, 16, 8, 16)
+
+
+def test_workspace_needs_the_width_of_the_tables():
+    """A compression over the 8-bit cache has a table of its own in its workspace: reserved without the tables'
+    width it would be too small, and allocated anew inside the first call, a captured one too."""
+    comp = make8()
+    with pytest.raises(TypeError):
+        comp.workspace(3)
+    ws = comp.workspace(3, bt_stride=40)
+    assert comp.workspace(3, None, bt_stride=40).data_ptr() == ws.data_ptr()
+    for n, width in ((3, 40), (3, 7), (1, 40)):
+        sizes = comp._compress_sizes(n, width)
+        assert sizes[1] == 4 * n * width and comp._space("_xws", sum(sizes), None).data_ptr() == ws.data_ptr()
