@@ -128,7 +128,9 @@ class Compressor8(Compressor):
         blocks = n * (self.params.W // c.block_size + 1)
         shape = (c.num_layers, blocks, c.num_kv_heads, c.block_size, c.head_dim)
         keys = ws[:2 * torch.Size(shape).numel()].view(torch.bfloat16).view(shape)
-        return kara.cache(keys, keys, c.num_q_heads)
+        windows = kara.cache(keys, keys, c.num_q_heads)
+        windows.keep = keys   # the workspace may be replaced by a larger one while `windows` is in use
+        return windows
 
     def _compress_sizes(self, n: int, bt_stride: int):
         """Bytes of a compression's window keys, their table, the scorer's workspace, scores, candidates, kept

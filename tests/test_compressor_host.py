@@ -23,3 +23,12 @@ def test_workspace_needs_the_width_of_the_tables():
     for n, width in ((3, 40), (3, 7), (1, 40)):
         sizes = comp._compress_sizes(n, width)
         assert sizes[1] == 4 * n * width and comp._space("_xws", sum(sizes), None).data_ptr() == ws.data_ptr()
+
+
+def test_windows_keep_their_memory():
+    """What `windows` describes stays allocated while it is held, also when the workspace grew since."""
+    comp = make8()
+    windows = comp._window_cache(comp.workspace(1, bt_stride=4), 1)
+    comp.workspace(3, bt_stride=40)
+    where = windows.keep.untyped_storage()
+    assert where.data_ptr() <= windows.k < where.data_ptr() + where.nbytes()
