@@ -12,7 +12,8 @@ class Compressor:
     Holds the device workspaces and error word; the cache, tables and fresh
     block ids stay owned by the caller.  A workspace is memory of the stream that
     first used it; dropped, it and the error word are given back once every stream
-    that used them has run its calls.
+    that used them has run its calls.  What calls captured into a graph use stays as
+    long as this object does, which must outlive the graph.
     """
 
     def __init__(self, k: torch.Tensor, v: torch.Tensor, num_q_heads: int, W: int, B: int, K: int, R: int,
@@ -27,12 +28,21 @@ class Compressor:
         self._cws = torch.empty(0, dtype=torch.uint8, device=k.device)
         self.err = torch.zeros(1, dtype=torch.int32, device=k.device)
         self._users = {"err": {self._handle(None)}}   # handles of the streams that the allocator knows to use each
+        self._captured, self._in_graphs = set(), []   # workspaces that a graph uses; those of them since replaced
 
     def _handle(self, stream):
         if stream is not None:
             return stream.cuda_stream
         device = self.k.device
         return torch._C._cuda_getCurrentRawStream(device.index) if device.type == "cuda" else None
+
+    def _capturing(self, stream) -> bool:
+        if self.k.device.type != "cuda":
+            return False
+        if stream is None or stream.cuda_stream == self._handle(None):
+            return torch.cuda.is_current_stream_capturing()
+        with torch.cuda.stream(stream):
+            return torch.cuda.is_current_stream_capturing()
 
     def _used(self, name: str, stream) -> torch.Tensor:
         """A buffer of this object's that a call on `stream` (None: the current one) uses: once dropped it is
@@ -46,9 +56,14 @@ class Compressor:
     def _space(self, name: str, need: int, stream) -> torch.Tensor:
         """Workspace `name` of at least `need` bytes, for a call on `stream`."""
         if getattr(self, name).numel() < need or name not in self._users:
+            if name in self._captured:
+                self._in_graphs.append(getattr(self, name))
+                self._captured.remove(name)
             with torch.cuda.stream(stream):   # of that stream's memory: what others gave back may be in use yet
                 setattr(self, name, torch.empty(need, dtype=torch.uint8, device=self.k.device))
             self._users[name] = {self._handle(stream)}
+        if name not in self._captured and self._capturing(stream):
+            self._captured.add(name)
         return self._used(name, stream)
 
     def workspace(self, n: int, stream=None) -> torch.Tensor:

@@ -32,3 +32,16 @@ def test_windows_keep_their_memory():
     comp.workspace(3, bt_stride=40)
     where = windows.keep.untyped_storage()
     assert where.data_ptr() <= windows.k < where.data_ptr() + where.nbytes()
+
+
+@pytest.mark.parametrize("name", ["_dws", "_cws", "_xws", "_ws"])
+def test_captured_workspaces_outlive_their_growth(name, monkeypatch):
+    """A workspace that a captured call uses is not given back when a later call needs a larger one: the graph
+    writes to it whenever it is replayed.  One that no graph uses is."""
+    comp = make8()
+    capturing = False
+    monkeypatch.setattr(comp, "_capturing", lambda stream: capturing, raising=False)
+    for capturing, size in ((False, 100), (True, 200), (True, 150), (False, 300), (False, 400)):
+        comp._space(name, size, None)
+    kept = [getattr(comp, name), *getattr(comp, "_in_graphs", [])]
+    assert sorted(x.numel() for x in kept) == [200, 400]
