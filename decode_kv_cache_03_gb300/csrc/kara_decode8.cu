@@ -17,11 +17,11 @@
 //     become the upper eight rows of the product and the odd ones the lower.
 //   * Queries are scaled by a power of two for each head so that their largest element is
 //     in [2^14, 2^15): bf16 values down to 2^-29 of it are exact in f16, and smaller ones
-//     off by 2^-40 of it.
+//     off by 2^-39 of it at most.
 //   * K's scales multiply the logits, V's the weights, which then are brought to f16
 //     with a power of two for each head that puts the largest of a split in
-//     [2^14, 2^15): 2^-12 of a weight is lost for those within 2^-29 of the largest
-//     (times its block's scale), 2^-40 of the largest for smaller ones.  So keys that
+//     [2^14, 2^15): half of an f16 step, 2^-11 of a weight, for those within 2^-29 of the
+//     largest (times its block's scale), 2^-39 of the largest for smaller ones.  So keys that
 //     share little weight beside one that takes nearly all keep their digits; without the
 //     factor, weights below 2^-14 would lose theirs.
 // Softmax, sums and the merge of the splits are fp32; the output is rounded to bf16 once.

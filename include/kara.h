@@ -398,8 +398,8 @@ kara_status kara_append_kv8(const kara_cache8 *c, int32_t layer, const kara_toke
  * (16-byte aligned, not overlapping q), rounded once from fp32.  A sequence of
  * length 0 gives zeros and no error.  Queries enter the logits scaled by a power of
  * two for each head, in f16 (exact within 2^-29 of the head's largest element,
- * 2^-40 of it off below); weights times V's scales likewise, rounded to f16: 2^-12
- * of a weight, for those below 2^-29 of the largest 2^-40 of that.  Small batches are
+ * 2^-39 of it off below); weights times V's scales likewise, rounded to f16: 2^-11
+ * of a weight, for those below 2^-29 of the largest 2^-39 of that.  Small batches are
  * cut into shorter splits of the keys (by n, num_kv_heads and bt_stride), so the last
  * bits depend on those.  ws is 16-byte aligned, and used by this call alone until it
  * has run; one of kara_decode8_workspace_size serves smaller n and bt_stride too.
@@ -413,7 +413,7 @@ kara_status kara_decode_attention8(const kara_cache8 *c, int32_t layer, int32_t 
  * Causal attention of new tokens over an 8-bit cache: kara_chunk_attention with k_x
  * and v_x the stored values, its arguments, checks, errors and arithmetic, but that
  * queries enter the logits as two e4m3 terms of a power of two times themselves:
- * elements within 2^-10 of a row's largest are exact, smaller ones off by at most
+ * elements within 2^-9 of a row's largest are exact, smaller ones off by at most
  * 2^-17 of the largest (or 2^-50); and that weights are rounded to f16, with V's
  * scales in them: by 2^-11 of a weight, or a weight times its scale by 2^-24 of the
  * row's largest such product.  V's values are exact.  A key or value that is NaN

@@ -7,9 +7,11 @@ row's largest p_x s_x:
     weights  sum_x max(2^-11 p_x, 2^-24 P / s_x) |v_x|: an f16 rounding, or half of f16's smallest step, 2^-25, where the
              largest weight times scale is 2^-1 at least (2^7, but for scales of a tile that are up to 2^8 apart)
     logits   a weight is off by its logit's error, and the sum of all by as much: twice 2^-17 of the query's largest
-             element times the keys' dims whose query element is below 2^-10 of it; 2^-20 of the sum of the products'
+             element times the keys' dims whose query element is below 2^-9 of it; 2^-20 of the sum of the products'
              magnitudes (256 fp32 additions of exact products, at 2^-28 to 2^-22 of the largest partial sum); 2^-15 for
-             the logit's scaling, the subtraction of the row's reference (up to 2^7 in log2: 2^-17) and the exponential."""
+             the logit's scaling, the subtraction of the row's reference (up to 2^7 in log2: 2^-17) and the exponential.
+Decode attention's is the same but for weights, sum_x max(2^-11 p_x, 2^-39 P / s_x) |v_x|, and queries, 2^-39 of the head's
+largest element for those below 2^-29 of it."""
 
 import numpy as np
 import pytest
@@ -17,7 +19,7 @@ import torch
 
 from _cache8 import BS, dense, plain_compact, quantise, source_rows, value
 from _newtokens import blocks
-from test_gpu_cache8 import chunk_case, run_chunk, run_compact, window_case
+from test_gpu_cache8 import CHUNKS, chunk_case, decode_case, run_chunk, run_compact, run_decode, window_case
 
 pytestmark = pytest.mark.gpu
 
@@ -58,11 +60,26 @@ def test_compact_zero_rows_of_a_large_block(d, apart):
 
 # ---- chunk attention ------------------------------------------------------------
 
+def bound(q, k, v, sv, chunk=True):
+    """Output and tolerance of queries [G][D] over keys and values [n][D] with V's scales sv [n]."""
+    D = q.shape[-1]
+    near, query, weight = (2.0 ** -9, 2.0 ** -17, 2.0 ** -24) if chunk else (2.0 ** -29, 2.0 ** -39, 2.0 ** -39)
+    p = torch.softmax(q @ k.T / D ** 0.5, -1)
+    top = q.abs().amax(-1, keepdim=True)
+    small = torch.where(q.abs() < near * top, top, 0.0)
+    logit = query * small @ k.abs().T + 2.0 ** -20 * (q.abs() @ k.abs().T)
+    most = (p * sv).amax(-1, keepdim=True)
+    w = torch.maximum(2.0 ** -11 * p, weight * most / torch.where(sv > 0, sv, torch.inf))
+    w = w + p * 2 * (logit.amax(-1, keepdim=True) / D ** 0.5 + 2.0 ** -15)
+    ref = p @ v
+    return ref, ref.abs() * 2.0 ** -8 + w @ v.abs()
+
+
 def check_chunk(c, got, rows=None):
     """Rows of a chunk's output (all, or those of the given numbers) within the tolerance above."""
     hq, D = c["q"].shape[1:]
     hkv = c["k"].shape[2]
-    G, worst = hq // hkv, 0.0
+    G = hq // hkv
     k_all, v_all = (dense(c[x], c[x + "s"])[0] for x in "kv")
     for s, L in enumerate(int(x) for x in c["lengths"]):
         t0, t1 = int(c["q_start"][s]), int(c["q_start"][s + 1])
@@ -71,22 +88,11 @@ def check_chunk(c, got, rows=None):
             k, v = (x[ids, g].reshape(-1, D)[:L] for x in (k_all, v_all))
             sv = c["vs"][0, ids, g].double().abs().repeat_interleave(BS)[:L]
             for t in range(t0, t1):
-                if rows is not None and t not in rows:
-                    continue
-                n = L - (t1 - t) + 1
-                q = c["q"][t, g * G:(g + 1) * G].double()
-                p = torch.softmax(q @ k[:n].T / D ** 0.5, -1)
-                top = q.abs().amax(-1, keepdim=True)
-                small = torch.where(q.abs() < 2.0 ** -10 * top, top, 0.0)
-                logit = 2.0 ** -17 * small @ k[:n].abs().T + 2.0 ** -20 * (q.abs() @ k[:n].abs().T)
-                most = (p * sv[:n]).amax(-1, keepdim=True)
-                w = torch.maximum(2.0 ** -11 * p, 2.0 ** -24 * most / torch.where(sv[:n] > 0, sv[:n], torch.inf))
-                w = w + p * 2 * (logit.amax(-1, keepdim=True) / D ** 0.5 + 2.0 ** -15)
-                ref, lim = p @ v[:n], w @ v[:n].abs()
-                off = (got[t, g * G:(g + 1) * G].double() - ref).abs() / (ref.abs() * 2.0 ** -8 + lim)
-                assert (ref.abs() * 2.0 ** -8 + lim > 0).all() and off.max() <= 1, (s, g, t, float(off.max()))
-                worst = max(worst, float(off.max()))
-    return worst
+                if rows is None or t in rows:
+                    n = L - (t1 - t) + 1
+                    ref, lim = bound(c["q"][t, g * G:(g + 1) * G].double(), k[:n], v[:n], sv[:n])
+                    off = ((got[t, g * G:(g + 1) * G].double() - ref).abs() / lim).max()
+                    assert (lim > 0).all() and off <= 1, (s, g, t, float(off))
 
 
 SHAPES = [(8, 2, 128), (4, 2, 64), (5, 1, 128)]
@@ -172,3 +178,42 @@ def test_chunk_scales_at_random(lo, hi):
         st, got = run_chunk(c)
         assert st == 0
         check_chunk(c, got)
+
+
+@pytest.mark.parametrize("outliers", [False, True])
+@pytest.mark.parametrize("hq,hkv,d", SHAPES)
+def test_chunk_within_its_stated_errors(hq, hkv, d, outliers):
+    """Lengths around blocks and tiles; V's scales within a tile's one exponent.  With outliers, three dims of each query
+    2^12 and more above the rest, which then are where the queries' two terms lose digits."""
+    c = chunk_case(hq + 5, CHUNKS[0][0], CHUNKS[0][1], hq, hkv, d, pad=2)
+    if outliers:
+        c["q"][:, :, 3:] *= 2.0 ** -7
+        c["q"][:, :, :3] *= 2.0 ** 4
+        c["k"][..., :3] = 0x20       # 2^-4 times the scale: the large dims do not decide alone
+    st, got = run_chunk(c)
+    assert st == 0
+    check_chunk(c, got)
+
+
+@pytest.mark.parametrize("hq,hkv,d", SHAPES)
+@pytest.mark.parametrize("lo,hi", [(0, 0), (-63, 63), (-63, 0), (0, 63)])
+def test_decode_scales_at_random(hq, hkv, d, lo, hi):
+    """Every block of V with a scale of its own; sequences of one split and of several."""
+    lengths, bt, k, ks, v, vs, q = decode_case(hq + 70, [1, 40, 1000, 2500], hq, hkv, d)
+    g = torch.Generator().manual_seed(d + hi)
+    if lo < hi:
+        vs = vs.sign() * 2.0 ** torch.randint(lo, hi + 1, vs.shape, generator=g).float()
+    q[:, :, 5] *= 2.0 ** 10
+    k[..., 5] = 0x08                 # 2^-6 times the scale
+    st, out = run_decode(lengths, bt, k, ks, v, vs, q)
+    assert st == 0
+    kd, vd = dense(k, ks)[1], dense(v, vs)[1]
+    for s, L in enumerate(lengths):
+        ids = torch.as_tensor(bt[s, :blocks(L)]).long()
+        for g in range(hkv):
+            kk, vv = (x[ids, g].reshape(-1, d)[:L] for x in (kd, vd))
+            sv = vs[1, ids, g].double().abs().repeat_interleave(BS)[:L]
+            h = slice(g * (hq // hkv), (g + 1) * (hq // hkv))
+            ref, lim = bound(q[s, h].double(), kk, vv, sv, chunk=False)
+            off = ((out[s, h].double() - ref).abs() / lim).max()
+            assert off <= 1, (s, g, float(off))
