@@ -839,16 +839,17 @@ __device__ __noinline__ void add_cleared(const ChunkArgs &a, int seq, int head, 
 // the weights, which are rounded to f16:
 //     w_x = 2^(l_x + e - M + kUp8),   O = sum_x w_x (v_x 2^-e),   z = sum over tiles of 2^-e sum_x w_x,
 // M the largest l_x + e so far (lazily, as above): weights within 2^-21 of it keep eleven bits, smaller ones are off by
-// 2^-32 of it, and with the maximum's growth of 2^8 the largest stay within f16.  That is for tiles whose blocks' scales
-// are no more than 2^kApart8 apart: f16 holds their values exactly, and M is at most that much above a row's largest
-// weight times its own block's scale, whose 2^-24 bounds the error.  Further apart, a block that a row does not see, or gives no
-// weight, would take the others' digits: then each block has an e of its own (logits_apart, out of line: the logits are
-// written anew, V's tile holds the codes themselves, and z is summed from weights without e).  So have the blocks of tiles
-// with an e below kLeast8, of zeros for one: with M from a tile at 2^57, the scaled weights of keys that count in z would
-// leave fp32's range (w is 2^(kUp8 - 24 + kLeast8 - 57) = 2^-114 at least for those within 2^-24 of the largest weight).  K's and V's loading warps tell
-// such tiles apart.  A row meets one where its largest logit seems to grow beyond all bounds (vtile), in the branch that it takes
-// then anyway: a check of its own in every tile took the mixed batch from 368 to 398 us, this takes it to 370, four tokens for
-// each of 128 sequences from 607 to 612, the prompt from 1620 to 1625.
+// 2^-32 of it, and with the maximum's growth of 2^8 the largest stay within f16.  That is for tiles whose blocks'
+// scales are no more than 2^kApart8 apart: f16 holds their values exactly, and M is at most that much above a row's largest
+// weight times its own block's scale, whose 2^-24 bounds the error.  Further apart, a block that a row does not see, or
+// gives no weight, would take the others' digits: then each block has an e of its own (logits_apart, out of line: the
+// logits are written anew, V's tile holds the codes themselves, and z is summed from weights without e).  So have the
+// blocks of tiles with an e below kLeast8, of zeros for one: with M from a tile at 2^57, the scaled weights of keys that
+// count in z would leave fp32's range (w is 2^(kUp8 - 24 + kLeast8 - 57) = 2^-114 at least for those within 2^-24 of the
+// largest weight).  K's and V's loading warps tell such tiles apart.  A row meets one where its largest logit seems to
+// grow beyond all bounds (vtile), in the branch that it takes then anyway: a check of its own in every tile took the mixed
+// batch from 368 to 398 us, this leaves it at 367, four tokens for each of 128 sequences at 610 (606), the prompt at
+// 1625 to 1635 (1620).
 // (As bf16, exact at any scale, two codes took four instructions instead of two, and weights kept eight bits: 64
 // sequences of 1 to 128 tokens 387 us and 379, four tokens for each of 128 sequences 611 and 604, one prompt alike.
 // With a scale for each block in the weights, and one instruction, the softmax took longer: 409 and 613.)
@@ -1133,25 +1134,36 @@ __device__ __forceinline__ void raise_reference(uint32_t to, float mt, float &m,
 
 // A row's logits in a key tile whose blocks of V are apart: log2 of a block's scale, and not of the tile's, goes into its
 // keys' logits (in TMEM; -infinity for those that the row does not see), and the weights without it into z.  Returns
-// the row's m and z.  (In the registers of the loop that calls it this made the ordinary tiles 10 % slower.)
+// the row's m and z.  (Inside the loop that calls it this made the ordinary tiles 10 % slower; with all 128 logits in
+// registers at once, 2 %.  If every tile is like that, four tokens for each of 128 sequences take 1130 us instead of 610, the
+// mixed batch 500 instead of 367, a prompt of 8192 tokens 2000 instead of 1625; 32 logits at a time, each with factors
+// of its own, 2870, 930 and 3410.)
 template <int D>
 __device__ __noinline__ float2 logits_apart(uint32_t ts, uint32_t to, const float *kscale, const float *vexp, float scale2,
                                             int lim, bool first, float2 mz)
 {
     float mt = -INFINITY;
 #pragma unroll 1
-    for (int c = 0; c < kTile; c += 32) {
-        uint32_t s[32];
-        tmem_ld32(ts + c, s, 0);
-        tmem_wait_ld32(s, 0);
+    for (int c0 = 0; c0 < kTile; c0 += 64) {
+        uint32_t s[64];
 #pragma unroll
-        for (int e = 0; e < 32; ++e) {
-            const float f = scale2 * kscale[(c + e) / kBlk];
-            const float l = c + e <= lim ? __uint_as_float(s[e]) + vexp[(c + e) / kBlk] / f : -INFINITY;
-            mt = fmaxf(mt, l * f);
-            s[e] = __float_as_uint(l);
+        for (int c = 0; c < 64; c += 32) tmem_ld32(ts + c0 + c, s, c);
+#pragma unroll
+        for (int c = 0; c < 64; c += 32) tmem_wait_ld32(s, c);
+#pragma unroll
+        for (int b = 0; b < 64 / kBlk; ++b) {
+            const float f = scale2 * kscale[c0 / kBlk + b], e = vexp[c0 / kBlk + b] / f;
+            float most = -INFINITY;
+#pragma unroll
+            for (int c = b * kBlk; c < b * kBlk + kBlk; ++c) {
+                const float l = c0 + c <= lim ? __uint_as_float(s[c]) + e : -INFINITY;
+                most = fmaxf(most, l);
+                s[c] = __float_as_uint(l);
+            }
+            mt = fmaxf(mt, most * f);
         }
-        tmem_st32(ts + c, s, 0);
+#pragma unroll
+        for (int c = 0; c < 64; c += 32) tmem_st32(ts + c0 + c, s, c);
     }
     tmem_wait_st();
     if (first)
@@ -1159,15 +1171,22 @@ __device__ __noinline__ float2 logits_apart(uint32_t ts, uint32_t to, const floa
     else if (__any_sync(0xffffffffu, mt > mz.x + kLazy))
         raise_reference<D, true>(to, mt, mz.x, mz.y);
     const float up = kUp8 - (mz.x == -INFINITY ? 0.f : mz.x);
+    float sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 1
-    for (int c = 0; c < kTile; c += 32) {
-        uint32_t s[32];
-        tmem_ld32(ts + c, s, 0);
-        tmem_wait_ld32(s, 0);
+    for (int c0 = 0; c0 < kTile; c0 += 64) {
+        uint32_t s[64];
 #pragma unroll
-        for (int e = 0; e < 32; ++e)
-            mz.y += ex2(fmaf(__uint_as_float(s[e]), scale2 * kscale[(c + e) / kBlk], up - vexp[(c + e) / kBlk]));
+        for (int c = 0; c < 64; c += 32) tmem_ld32(ts + c0 + c, s, c);
+#pragma unroll
+        for (int c = 0; c < 64; c += 32) tmem_wait_ld32(s, c);
+#pragma unroll
+        for (int b = 0; b < 64 / kBlk; ++b) {
+            const float f = scale2 * kscale[c0 / kBlk + b], e = up - vexp[c0 / kBlk + b];
+#pragma unroll
+            for (int c = b * kBlk; c < b * kBlk + kBlk; ++c) sum[c & 3] += ex2(fmaf(__uint_as_float(s[c]), f, e));
+        }
     }
+    mz.y += (sum[0] + sum[1]) + (sum[2] + sum[3]);
     return mz;
 }
 
