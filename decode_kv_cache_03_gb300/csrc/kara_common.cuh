@@ -85,48 +85,24 @@ __device__ __forceinline__ int64_t pool_off(const Geo &g, int l, int32_t blk, in
          + (int64_t)slot * g.D;
 }
 
-// Releases the old tail of sequence s, installs the fresh ids and sets the new length, unless an error was
-// recorded; `lanes` threads together.
-__device__ __forceinline__ void commit_sequence(const Geo &g, const SeqPlan &p, int32_t error, const int32_t *fresh,
-                                                int32_t *freed, int32_t *new_len, int32_t *bt, int s, int lane, int lanes)
-{
-    if (error != 0 || p.p0 < 0) {
-        if (lane == 0) new_len[s] = g.len[s];
-        return;
-    }
-    int32_t *row = bt + (int64_t)s * g.bt_stride + p.p0;
-    for (int t = lane; t < p.n_old; t += lanes) {
-        const int32_t old = row[t];
-        freed[p.off_old + t] = old;
-        row[t] = t < p.n_new ? fresh[p.off_new + t] : -1;
-    }
-    if (lane == 0) new_len[s] = p.Lnew;
-}
-
 __host__ __device__ __forceinline__ size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 
 // Host-side argument checks of the entry points; fills the geometry of a call.
 kara_status geo_from_args(const kara_cache *c, const kara_params *p, const kara_batch *b, Geo *g);
 
-// Launchers (each returns the launch error, if any; dependent: as a programmatic dependent of what
-// precedes it on the stream).
-cudaError_t launch_plan(const Geo &g, int64_t n_fresh, SeqPlan *plan, int32_t *err, cudaStream_t st,
-                        bool dependent = false);
+// Launchers (each returns the launch error, if any).
+cudaError_t launch_plan(const Geo &g, int64_t n_fresh, SeqPlan *plan, int32_t *err, cudaStream_t st);
 cudaError_t launch_compact(const Geo &g, const SeqPlan *plan, const int32_t *kept, const int32_t *fresh,
                            int64_t n_fresh, int32_t *err, cudaStream_t st);
 // The two halves of launch_compact: the fresh-id check of a whole batch, and the
 // kept-row check plus the copy of a batch or of a group of its sequences (plan
 // then points at the group's first entry; offsets into fresh stay the batch's).
 cudaError_t launch_fresh_check(const Geo &g, const SeqPlan *plan, const int32_t *fresh, int64_t n_fresh,
-                               int32_t *err, cudaStream_t st, bool dependent = false);
-cudaError_t launch_prepare(const Geo &g, const int32_t *kept, const int32_t *fresh, int64_t n_fresh, SeqPlan *plan,
-                           int32_t *done, int32_t *err, cudaStream_t st);
-cudaError_t launch_kept_check(const Geo &g, const int32_t *kept, int32_t *err, cudaStream_t st, bool dependent = false);
+                               int32_t *err, cudaStream_t st);
 cudaError_t launch_kept_copy(const Geo &g, const SeqPlan *plan, const int32_t *kept, const int32_t *fresh,
                              int64_t n_fresh, int32_t *err, cudaStream_t st);
 cudaError_t launch_commit(const Geo &g, const SeqPlan *plan, const int32_t *fresh, int32_t *freed,
-                          int32_t *new_len, int32_t *bt, const int32_t *err, cudaStream_t st,
-                          bool dependent = false);
+                          int32_t *new_len, int32_t *bt, const int32_t *err, cudaStream_t st);
 cudaError_t launch_select(int64_t nwin, int C, int K, int R, float lambda, int mode, int chunk, const float *scores,
                           int32_t *cand, int32_t *kept, cudaStream_t st);
 size_t score_scratch_bytes(const Geo &g);

@@ -6,7 +6,7 @@
 // memory.  The retained rows of each window are packed, in order, into fresh
 // blocks supplied by the caller; the old tail blocks are released only after
 // every copy is done and only if no error was recorded.
-#include "kara_tokens.cuh"
+#include "kara_plan.cuh"
 
 namespace kara {
 namespace {
@@ -304,6 +304,11 @@ cudaError_t launch_plan(const Geo &g, int64_t n_fresh, SeqPlan *plan, int32_t *e
     return launch<Geo, int64_t, SeqPlan *, int32_t *>(dependent, plan_kernel, 1, kPlanThreads, st, g, n_fresh, plan, err);
 }
 
+cudaError_t launch_plan(const Geo &g, int64_t n_fresh, SeqPlan *plan, int32_t *err, cudaStream_t st)
+{
+    return launch_plan(g, n_fresh, plan, err, st, false);
+}
+
 cudaError_t launch_prepare(const Geo &g, const int32_t *kept, const int32_t *fresh, int64_t n_fresh, SeqPlan *plan,
                            int32_t *done, int32_t *err, cudaStream_t st)
 {
@@ -323,6 +328,12 @@ cudaError_t launch_fresh_check(const Geo &g, const SeqPlan *plan, const int32_t 
         dependent, fresh_check_kernel, (unsigned)nb, kChkThreads, st, g, plan, fresh, n_fresh, err);
 }
 
+cudaError_t launch_fresh_check(const Geo &g, const SeqPlan *plan, const int32_t *fresh, int64_t n_fresh,
+                               int32_t *err, cudaStream_t st)
+{
+    return launch_fresh_check(g, plan, fresh, n_fresh, err, st, false);
+}
+
 cudaError_t launch_kept_check(const Geo &g, const int32_t *kept, int32_t *err, cudaStream_t st, bool dependent)
 {
     const int64_t nk = g.nwin * g.R;
@@ -337,7 +348,7 @@ cudaError_t launch_kept_copy(const Geo &g, const SeqPlan *plan, const int32_t *k
 {
     const int64_t blocks = g.nwin * 2;
     if (blocks == 0) return cudaSuccess;
-    const cudaError_t e = launch_kept_check(g, kept, err, st);
+    const cudaError_t e = launch_kept_check(g, kept, err, st, false);
     if (e != cudaSuccess) return e;
     if (g.D == 128)
         compact_kernel<128><<<(unsigned)blocks, 256, 0, st>>>(g, plan, kept, fresh, n_fresh, err);
@@ -360,6 +371,12 @@ cudaError_t launch_commit(const Geo &g, const SeqPlan *plan, const int32_t *fres
     if (g.n == 0) return cudaSuccess;
     return launch<Geo, const SeqPlan *, const int32_t *, int32_t *, int32_t *, int32_t *, const int32_t *>(
         dependent, commit_kernel, (unsigned)(g.n + 7) / 8, 256, st, g, plan, fresh, freed, new_len, bt, err);
+}
+
+cudaError_t launch_commit(const Geo &g, const SeqPlan *plan, const int32_t *fresh, int32_t *freed,
+                          int32_t *new_len, int32_t *bt, const int32_t *err, cudaStream_t st)
+{
+    return launch_commit(g, plan, fresh, freed, new_len, bt, err, st, false);
 }
 
 }  // namespace kara

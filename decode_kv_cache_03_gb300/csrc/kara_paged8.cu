@@ -15,7 +15,7 @@
 #include <cuda_fp16.h>
 
 #include "kara_cache8.cuh"
-#include "kara_tokens.cuh"
+#include "kara_plan.cuh"
 
 namespace kara {
 namespace {
