@@ -39,6 +39,22 @@ __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi)
     return r;
 }
 
+// (lo, hi) rounded to nearest-even f16, lo in the low half.
+__device__ __forceinline__ uint32_t f16x2(float lo, float hi)
+{
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+// (lo, hi) rounded to nearest-even bf16, lo in the low half.
+__device__ __forceinline__ uint32_t bf16x2(float lo, float hi)
+{
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
 // Two codes as f16 values (exact), the low byte's in the low half.
 __device__ __forceinline__ uint32_t f16_of_e4m3x2(uint32_t codes)
 {

@@ -462,22 +462,6 @@ __device__ __forceinline__ float ld_shared(uint32_t addr)
     return x;
 }
 
-// (lo, hi) rounded to nearest-even f16, lo in the low half.
-__device__ __forceinline__ uint32_t f16x2(float lo, float hi)
-{
-    uint32_t r;
-    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
-}
-
-// (lo, hi) rounded to nearest-even bf16, lo in the low half.
-__device__ __forceinline__ uint32_t bf16x2(float lo, float hi)
-{
-    uint32_t r;
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
-}
-
 // 32 bytes (32-byte aligned) from v[o..o+7].
 template <int N>
 __device__ __forceinline__ void st_global_32b(void *p, const uint32_t (&v)[N], const int o)

@@ -148,14 +148,6 @@ __device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// (lo, hi) rounded to nearest-even f16, lo in the low half.
-__device__ __forceinline__ uint32_t f16x2(float lo, float hi)
-{
-    uint32_t r;
-    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
-}
-
 // The power of two that brings a largest magnitude x into [2^14, 2^15), and its inverse
 // (both normal: an x below 2^-112 stays below).
 __device__ __forceinline__ void to_f16_range(float x, float &up, float &down)
@@ -196,14 +188,6 @@ __device__ __forceinline__ void weigh(float (&acc)[NC][4], uint32_t sb, uint32_t
                       f16_of_e4m3x2(v >> 16), b0, b1);
         }
     }
-}
-
-// (lo, hi) rounded to nearest-even bf16, lo in the low half.
-__device__ __forceinline__ uint32_t bf16x2(float lo, float hi)
-{
-    uint32_t r;
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
 }
 
 template <int D, int G>
@@ -567,7 +551,8 @@ constexpr int kLeast = 256, kMostSplits = 64;
 
 static int64_t splits_of(int32_t bt_stride, int split) { return ((int64_t)bt_stride * kBlk + split - 1) / split; }
 
-// CTAs that fill half of the places.
+// CTAs that fill half of the places on the GB300's 152 SMs (a constant: the workspace's size, which follows from it, is
+// asked for without a device too).
 static int64_t few_ctas(const kara_cache8 *c) { return 152 * (c->num_q_heads / c->num_kv_heads >= 6 ? 3 : 4) / 2; }
 
 static int split_of(const kara_cache8 *c, int32_t n, int32_t bt_stride)

@@ -45,13 +45,6 @@ struct Pool8 {
     }
 };
 
-__device__ __forceinline__ uint32_t bf16x2(float lo, float hi)
-{
-    uint32_t r;
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
-}
-
 struct ExpandArgs {
     Pool8 in;
     uint16_t *out[2];
