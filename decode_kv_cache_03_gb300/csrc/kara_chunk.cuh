@@ -1737,7 +1737,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tmem_st32(ts + 32, s, 32);
                     float s0, s1;
                     unpack2(add2(sum[0], sum[1]), s0, s1);
-                    z = E8 ? fmaf(s0 + s1, ld_shared(vt + 4), z) : z + s0 + s1;
+                    z = E8 ? fmaf(s0 + s1, ld_shared(vt + 4), z) : z + (s0 + s1);
                     tmem_wait_st();
                     tc_fence_before();
                 }
