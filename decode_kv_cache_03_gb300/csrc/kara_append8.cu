@@ -21,8 +21,9 @@
 // (Queries by the bf16 append's staged kernel, in a launch of their own: as fast at 76, and slower by that launch
 // in shorter calls, 512 sequences of a token 26.5 against 23.2, 512 tokens 11.2 against 7.4.  Four CTAs to an SM
 // instead of three, with spills: 57, but 512 tokens 7.1 for 6.5, 256 sequences of four 16.4 for 15.2; two heads to
-// a pair of warps: 58, but 8.0 and 16.0.)  128 sequences of a token take 7.2 us captured: the chain of slot, table
-// row, rows, largest value.
+// a pair of warps: 58, but 8.0 and 16.0.)  A token for each of up to 64 sequences takes 3.3 to 4.3 us captured, the chain
+// of slot, table row, rows, largest value; 128 take 7.3, 256 11.7: runs of one row have two warps each all the same, and
+// their CTAs come in rounds.
 #include "kara_cache8.cuh"
 #include "kara_rows.cuh"
 #include "kara_tokens.cuh"

@@ -67,8 +67,8 @@
 //
 // The 8-bit cache (E8; the comment ahead of load_queries has the arithmetic): tiles of K's codes are operands as
 // they lie, tiles of V's codes pass through four warps that write them as f16, so the ring of 5 tiles is
-// 2 (f16) + 3 + 2 (codes).  Four tokens x 128 sequences 605 us (bf16 745), 64 sequences of 1 to 128 tokens 368
-// (355), 8192 tokens over 8192 keys 1620 (1405).  No unit is full (tensor 41 and 52 %, issue slots 32 and 48 %, HBM 53 %
+// 2 (f16) + 3 + 2 (codes).  Four tokens x 128 sequences 610 us (bf16 745), 64 sequences of 1 to 128 tokens 367
+// (358), 8192 tokens over 8192 keys 1630 (1405).  No unit is full (tensor 41 and 52 %, issue slots 32 and 48 %, HBM 53 %
 // of the copy rate for few tokens): a step waits for logits, weights, and the conversion ahead of the weighted sum, whose
 // tiles leave room for two.  (Few rows: a softmax a quarter as long, by rows loaded four times, one more tile of
 // codes, or both kinds of codes a tile further ahead bring 0 to 1.5 %, and cost the others 1 to 5.)
